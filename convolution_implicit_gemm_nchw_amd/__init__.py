@@ -626,3 +626,368 @@ def convnd_bwd_filter(x, dy, filt, groups=1, pad_lo=None, pad_hi=None, stride=No
                                   st.cuda_stream), "convnd_bwd_filter")
     return dw
 
+
+
+# ---------------------------------------------------------------- state-space operators
+
+_LL = ctypes.c_longlong
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", _VP), ("stride_b", _LL), ("stride_d", _LL)]
+
+
+class _ScanIn(ctypes.Structure):
+    _fields_ = [("data", _VP), ("stride_b", _LL), ("stride_g", _LL), ("stride_n", _LL)]
+
+
+class _CausalConv(ctypes.Structure):
+    _fields_ = [("B", _I), ("D", _I), ("L", _I), ("K", _I), ("silu", _I), ("x", _Rows), ("w", _VP), ("bias", _VP),
+                ("initial_state", _VP), ("lengths", _VP), ("y", _Rows), ("final_state", _VP), ("dy", _Rows),
+                ("d_final_state", _VP), ("dx", _Rows), ("dw", _VP), ("dbias", _VP), ("d_initial_state", _VP)]
+
+
+class _Scan(ctypes.Structure):
+    _fields_ = [("B", _I), ("D", _I), ("L", _I), ("N", _I), ("G", _I), ("softplus", _I), ("x", _Rows),
+                ("delta", _Rows), ("z", _Rows), ("A", _VP), ("Bm", _ScanIn), ("Cm", _ScanIn), ("D_skip", _VP),
+                ("delta_bias", _VP), ("initial_state", _VP), ("lengths", _VP), ("y", _Rows), ("final_state", _VP),
+                ("states", _VP), ("dy", _Rows), ("d_final_state", _VP), ("dx", _Rows), ("ddelta", _Rows),
+                ("dz", _Rows), ("dA", _VP), ("dB", _VP), ("dC", _VP), ("dD", _VP), ("ddelta_bias", _VP),
+                ("d_initial_state", _VP)]
+
+
+_CP, _SP, _SZP = ctypes.POINTER(_CausalConv), ctypes.POINTER(_Scan), ctypes.POINTER(_SZ)
+for _name, _args in {
+        "causal_conv1d_fwd": [_CP, _I, _VP],
+        "causal_conv1d_bwd": [_CP, _I, _VP, _SZ, _VP],
+        "causal_conv1d_bwd_workspace_size": [_CP, _I, _SZ, _SZP],
+        "causal_conv1d_step": [_I, _I, _I, _I, _I, _Rows, _VP, _I, _VP, _VP, _VP, _VP, _Rows, _VP],
+        "selective_scan_fwd": [_SP, _I, _VP],
+        "selective_scan_bwd": [_SP, _I, _VP, _SZ, _VP],
+        "selective_scan_states_size": [_I, _I, _I, _I, _SZP],
+        "selective_scan_bwd_workspace_size": [_SP, _I, _SZP],
+        "selective_scan_step": [_SP, _I, _VP, _I, _VP, _VP, _VP],
+        "quantize_tokens": [_I, _I, _I, _I, _VP, _LL, _LL, _LL, _VP, _VP, _VP],
+        "matmul_i8": [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _SZ, _VP],
+        "matmul_i8_workspace_size": [_I, _I, _I, _I, _SZ, _SZP]}.items():
+    _fn = getattr(_lib, _name)
+    _fn.argtypes = _args
+    _fn.restype = _I
+
+
+def _device(name, t, shape, dtype, dev, packed=True):
+    """Raises unless t is a device tensor of this shape, type and device, contiguous when packed."""
+    if not torch.is_tensor(t) or not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
+    if packed and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _optional(name, t, shape, dtype, dev):
+    return None if t is None else _device(name, t, shape, dtype, dev)
+
+
+def _rows(name, t, shape, dtype, dev, out=False):
+    """The miconv_rows_t of a [B, D, L] (or [B, D]) tensor with contiguous time steps.  A fresh
+    output is packed; a given one may be a view, as inputs may."""
+    if t is None:
+        return _Rows(None, 0, 0)
+    _device(name, t, shape, dtype, dev, packed=False)
+    if len(shape) == 3 and shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
+    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _activation(name, t, ndim):
+    if not torch.is_tensor(t) or not t.is_cuda or t.dim() != ndim:
+        raise ValueError(f"{name} must be a {ndim}-dimensional device tensor")
+    return dtype_code(t)
+
+
+def _lm_stream(stream, dev):
+    """The stream the call runs on (the current one of the operands' device by default)."""
+    return stream if stream is not None else torch.cuda.current_stream(dev)
+
+
+def _scratch(need, workspace, stream):
+    """(pointer, bytes, owner): the caller's workspace tensor or one from `stream`'s pool."""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if need == 0:
+        return None, 0, None
+    with torch.cuda.stream(stream):
+        ws = torch.empty(need, dtype=torch.uint8, device=stream.device)
+    return ws.data_ptr(), need, ws
+
+
+def _fresh(t, shape, dtype, stream):
+    """t, or a new tensor from the pool of the stream that writes it."""
+    if t is not None:
+        return t
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=stream.device)
+
+
+def _conv_args(x, w, bias, silu, initial_state, lengths):
+    _activation("x", x, 3)
+    B, D, L = x.shape
+    if not torch.is_tensor(w) or w.dim() != 2:
+        raise ValueError("w must be [D, K]")
+    K, dev, dt = w.shape[1], x.device, x.dtype
+    c = _CausalConv(B=B, D=D, L=L, K=K, silu=int(bool(silu)))
+    c.x = _rows("x", x, (B, D, L), dt, dev)
+    c.w = _device("w", w, (D, K), dt, dev)
+    c.bias = _optional("bias", bias, (D,), torch.float32, dev)
+    c.initial_state = _optional("initial_state", initial_state, (B, D, K - 1), dt, dev)
+    c.lengths = _optional("lengths", lengths, (B,), torch.int32, dev)
+    return c, (B, D, L, K), dt, dev
+
+
+def causal_conv1d_fwd(x, w, bias=None, silu=False, initial_state=None, lengths=None, y=None, final_state=None,
+                      stream=None):
+    """y[b,d,t] = act(bias[d] + sum_k w[d,k] x~[b,d,t-K+1+k]) with act = SiLU when silu, x~ = initial_state
+    [B, D, K-1] before the first step (zeros without).  x [B, D, L] may be a view with contiguous
+    time steps; w [D, K], K <= 8, in x's dtype; bias fp32.  lengths (int32 [B]) are the valid steps of
+    right-padded sequences; y is 0 past them.  final_state [B, D, K-1], when given, is written."""
+    c, (B, D, L, K), dt, dev = _conv_args(x, w, bias, silu, initial_state, lengths)
+    st = _lm_stream(stream, dev)
+    y = _fresh(y, (B, D, L), dt, st)
+    c.y = _rows("y", y, (B, D, L), dt, dev)
+    c.final_state = _optional("final_state", final_state, (B, D, K - 1), dt, dev)
+    _check(_lib.causal_conv1d_fwd(ctypes.byref(c), dtype_code(x), st.cuda_stream), "causal_conv1d_fwd")
+    return y
+
+
+def causal_conv1d_bwd(x, w, dy, bias=None, silu=False, initial_state=None, lengths=None, d_final_state=None,
+                      dx=None, dw=None, dbias=None, d_initial_state=None, workspace=None, stream=None):
+    """(dx, dw, dbias) of causal_conv1d_fwd for the output gradient dy (and d_final_state): dx in x's
+    dtype, dw [D, K] and dbias [D] fp32 (None without a bias).  d_initial_state, when given, is written."""
+    c, (B, D, L, K), dt, dev = _conv_args(x, w, bias, silu, initial_state, lengths)
+    st = _lm_stream(stream, dev)
+    c.dy = _rows("dy", dy, (B, D, L), dt, dev)
+    c.d_final_state = _optional("d_final_state", d_final_state, (B, D, K - 1), dt, dev)
+    dx = _fresh(dx, (B, D, L), dt, st)
+    dw = _fresh(dw, (D, K), torch.float32, st)
+    if bias is not None:
+        dbias = _fresh(dbias, (D,), torch.float32, st)
+    c.dx = _rows("dx", dx, (B, D, L), dt, dev)
+    c.dw = _device("dw", dw, (D, K), torch.float32, dev)
+    c.dbias = _optional("dbias", dbias, (D,), torch.float32, dev)
+    c.d_initial_state = _optional("d_initial_state", d_initial_state, (B, D, K - 1), dt, dev)
+    need = _SZ(0)
+    code = dtype_code(x)
+    _check(_lib.causal_conv1d_bwd_workspace_size(ctypes.byref(c), code, MAX_WORKSPACE_BYTES, ctypes.byref(need)),
+           "causal_conv1d_bwd_workspace_size")
+    wp, wb, _keep = _scratch(need.value, workspace, st)
+    _check(_lib.causal_conv1d_bwd(ctypes.byref(c), code, wp, wb, st.cuda_stream), "causal_conv1d_bwd")
+    return dx, dw, dbias
+
+
+def _step_slots(state, state_out, slots, B, dev):
+    """(number of states, pointer to the slot of each sequence, where the states go)."""
+    if slots is None and state.shape[0] != B:
+        raise ValueError("without slots, state must hold one state for each sequence")
+    return state.shape[0], _optional("slots", slots, (B,), torch.int32, dev), state if state_out is None else state_out
+
+
+def causal_conv1d_step(x, state, w, bias=None, silu=False, state_out=None, slots=None, y=None, stream=None):
+    """One time step of causal_conv1d_fwd: x [B, D], state [B, D, K-1] (updated in place, or written to
+    state_out) -> y [B, D].  With slots (int32 [B]) state is a pool [S, D, K-1] and sequence b uses
+    state slots[b]; an index outside the pool marks an unused row (y = 0)."""
+    code = _activation("x", x, 2)
+    B, D = x.shape
+    if not torch.is_tensor(w) or w.dim() != 2 or not torch.is_tensor(state) or state.dim() != 3:
+        raise ValueError("w must be [D, K] and state [B, D, K-1]")
+    K, dev, dt = w.shape[1], x.device, x.dtype
+    S, sp, state_out = _step_slots(state, state_out, slots, B, dev)
+    st = _lm_stream(stream, dev)
+    y = _fresh(y, (B, D), dt, st)
+    _check(_lib.causal_conv1d_step(
+        B, D, K, int(bool(silu)), code, _rows("x", x, (B, D), dt, dev),
+        _device("state", state, (S, D, K - 1), dt, dev), S, sp, _device("w", w, (D, K), dt, dev),
+        _optional("bias", bias, (D,), torch.float32, dev), _device("state_out", state_out, (S, D, K - 1), dt, dev),
+        _rows("y", y, (B, D), dt, dev), st.cuda_stream), "causal_conv1d_step")
+    return y
+
+
+def _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias, softplus, lengths, step=False):
+    _activation("x", x, 2 if step else 3)
+    nb, nd = x.shape[:2]
+    L = 1 if step else x.shape[2]
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    if not torch.is_tensor(A) or A.dim() != 2 or not torch.is_tensor(Bm) or Bm.dim() != (3 if step else 4):
+        raise ValueError("A must be [D, N], B and C [B, G, N, L] ([B, G, N] for one step)")
+    N, G = A.shape[1], Bm.shape[1]
+    s = _Scan(B=nb, D=nd, L=L, N=N, G=G, softplus=int(bool(softplus)))
+    s.x = _rows("x", x, x.shape, dt, dev)
+    s.delta = _rows("delta", delta, x.shape, dt, dev)
+    s.z = _rows("z", z, x.shape, dt, dev)
+    s.A = _device("A", A, (nd, N), f32, dev)
+    for field, name, t in (("Bm", "B", Bm), ("Cm", "C", Cm)):
+        _device(name, t, (nb, G, N) + (() if step else (L,)), dt, dev, packed=False)
+        if not step and L > 1 and t.stride(3) != 1:
+            raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
+        setattr(s, field, _ScanIn(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+    s.D_skip = _optional("D", D, (nd,), f32, dev)
+    s.delta_bias = _optional("delta_bias", delta_bias, (nd,), f32, dev)
+    s.lengths = _optional("lengths", lengths, (nb,), torch.int32, dev)
+    return s, (nb, nd, L, N, G), dt, dev
+
+
+def selective_scan_states(x, A, stream=None):
+    """A buffer for the states that selective_scan_fwd saves for selective_scan_bwd."""
+    need = _SZ(0)
+    _check(_lib.selective_scan_states_size(x.shape[0], x.shape[1], x.shape[2], A.shape[1], ctypes.byref(need)),
+           "selective_scan_states_size")
+    return _fresh(None, (need.value // 4,), torch.float32, _lm_stream(stream, x.device))
+
+
+def _states_ptr(states, x, A):
+    if states is None:
+        return None
+    need = _SZ(0)
+    _check(_lib.selective_scan_states_size(x.shape[0], x.shape[1], x.shape[2], A.shape[1], ctypes.byref(need)),
+           "selective_scan_states_size")
+    return _device("states", states, (need.value // 4,), torch.float32, x.device)
+
+
+def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=False, initial_state=None,
+                       lengths=None, y=None, final_state=None, states=None, stream=None):
+    """Selective state space scan: with dt = softplus(delta + delta_bias),
+      h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t x_t B_t[n],  y_t = (sum_n C_t[n] h_t[n] + D x_t) * silu(z_t)
+    x, delta, z, y [B, D, L] (views with contiguous time steps), A [D, N] fp32, N <= 64, B, C [B, G, N, L]
+    (channel d reads group d // (D // G)), D and delta_bias fp32, initial_state [B, D, N] fp32.  lengths
+    as in causal_conv1d_fwd.  final_state [B, D, N] and states (selective_scan_states), when given, are
+    written."""
+    s, (nb, nd, L, N, G), dt, dev = _scan_args(x, delta, A, B, C, D, z, delta_bias, softplus, lengths)
+    st = _lm_stream(stream, dev)
+    y = _fresh(y, (nb, nd, L), dt, st)
+    s.y = _rows("y", y, (nb, nd, L), dt, dev)
+    s.initial_state = _optional("initial_state", initial_state, (nb, nd, N), torch.float32, dev)
+    s.final_state = _optional("final_state", final_state, (nb, nd, N), torch.float32, dev)
+    s.states = _states_ptr(states, x, A)
+    _check(_lib.selective_scan_fwd(ctypes.byref(s), dtype_code(x), st.cuda_stream), "selective_scan_fwd")
+    return y
+
+
+def selective_scan_bwd(x, delta, A, B, C, dy, states, D=None, z=None, delta_bias=None, softplus=False, lengths=None,
+                       d_final_state=None, d_initial_state=None, dx=None, ddelta=None, dz=None, workspace=None,
+                       stream=None):
+    """Gradients of selective_scan_fwd for the output gradient dy (and d_final_state); `states` is what
+    the forward pass saved for the same operands.  A dict of dx, ddelta, dz (x's dtype; dx, ddelta and dz
+    may be given, as views too) and dA, dB, dC, dD, ddelta_bias (fp32, B and C packed), None where the
+    operand is absent.  d_initial_state [B, D, N], when given, is written."""
+    s, (nb, nd, L, N, G), dt, dev = _scan_args(x, delta, A, B, C, D, z, delta_bias, softplus, lengths)
+    st, f32 = _lm_stream(stream, dev), torch.float32
+    s.dy = _rows("dy", dy, (nb, nd, L), dt, dev)
+    if states is None:
+        raise ValueError("states of the forward pass are needed")
+    s.states = _states_ptr(states, x, A)
+    s.d_final_state = _optional("d_final_state", d_final_state, (nb, nd, N), f32, dev)
+    s.d_initial_state = _optional("d_initial_state", d_initial_state, (nb, nd, N), f32, dev)
+    r = {"dx": _fresh(dx, (nb, nd, L), dt, st), "ddelta": _fresh(ddelta, (nb, nd, L), dt, st), "dz": None,
+         "dD": None, "ddelta_bias": None}
+    if z is not None:
+        r["dz"] = _fresh(dz, (nb, nd, L), dt, st)
+    for name, shape, wanted in (("dA", (nd, N), True), ("dB", (nb, G, N, L), True), ("dC", (nb, G, N, L), True),
+                                ("dD", (nd,), D is not None), ("ddelta_bias", (nd,), delta_bias is not None)):
+        if wanted:
+            r[name] = _fresh(None, shape, f32, st)
+            setattr(s, name, r[name].data_ptr())
+    for name in ("dx", "ddelta", "dz"):
+        setattr(s, name, _rows(name, r[name], (nb, nd, L), dt, dev))
+    need, code = _SZ(0), dtype_code(x)
+    _check(_lib.selective_scan_bwd_workspace_size(ctypes.byref(s), code, ctypes.byref(need)),
+           "selective_scan_bwd_workspace_size")
+    wp, wb, _keep = _scratch(need.value, workspace, st)
+    _check(_lib.selective_scan_bwd(ctypes.byref(s), code, wp, wb, st.cuda_stream), "selective_scan_bwd")
+    return r
+
+
+def selective_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=None, softplus=False, state_out=None,
+                        slots=None, y=None, stream=None):
+    """One time step of selective_scan_fwd: x, delta, z [B, D], B, C [B, G, N], state [B, D, N] fp32 (updated
+    in place, or written to state_out) -> y [B, D].  slots as in causal_conv1d_step."""
+    s, (nb, nd, _, N, G), dt, dev = _scan_args(x, delta, A, B, C, D, z, delta_bias, softplus, None, step=True)
+    if not torch.is_tensor(state) or state.dim() != 3:
+        raise ValueError("state must be [B, D, N]")
+    S, sp, state_out = _step_slots(state, state_out, slots, nb, dev)
+    st = _lm_stream(stream, dev)
+    y = _fresh(y, (nb, nd), dt, st)
+    s.y = _rows("y", y, (nb, nd), dt, dev)
+    _check(_lib.selective_scan_step(
+        ctypes.byref(s), dtype_code(x), _device("state", state, (S, nd, N), torch.float32, dev), S, sp,
+        _device("state_out", state_out, (S, nd, N), torch.float32, dev), st.cuda_stream), "selective_scan_step")
+    return y
+
+
+I8_PAD = 128
+
+
+def quantize_tokens(x, channel_major=False, q=None, scale=None, stream=None):
+    """Per-token quantisation to 8 bits: scale = max|x| / 127, q = round_half_even(127 x / max|x|).
+    x is [T, C] or [B, L, C] (tokens first) or, channel_major, [B, C, L] with contiguous time
+    steps.  Returns q [tokens, C_pad] int8 (C_pad = C rounded up to 128, zeros past C) and scale [tokens]
+    fp32; tokens run over [B, L] in that order.  A token with an infinity or NaN gets a NaN scale.  A
+    weight [O, C] is quantised by channel in the same way."""
+    if not torch.is_tensor(x) or not x.is_cuda or x.dim() not in (2, 3):
+        raise ValueError("x must be a device tensor of 2 or 3 dimensions")
+    code, dev = dtype_code(x), x.device
+    if channel_major:
+        if x.dim() != 3:
+            raise ValueError("channel-major x must be [B, C, L]")
+        nb, C, L = x.shape
+        sb, sc, sl = x.stride()
+        if L > 1 and sl != 1:
+            raise ValueError("x must have contiguous time steps (stride 1 along the last axis)")
+        sl = 1
+    else:
+        C = x.shape[-1]
+        if C > 1 and x.stride(-1) != 1:
+            raise ValueError("x must have contiguous channels (stride 1 along the last axis)")
+        if x.dim() == 3:
+            (nb, L), (sb, sl) = x.shape[:2], x.stride()[:2]
+        else:
+            nb, L, sb, sl = 1, x.shape[0], 0, x.stride(0)
+        sc = 1
+    pad = -(-C // I8_PAD) * I8_PAD
+    st = _lm_stream(stream, dev)
+    q = _fresh(q, (nb * L, pad), torch.int8, st)
+    scale = _fresh(scale, (nb * L,), torch.float32, st)
+    _check(_lib.quantize_tokens(nb, L, C, code, x.data_ptr(), sb, sl, sc,
+                                _device("q", q, (nb * L, pad), torch.int8, dev),
+                                _device("scale", scale, (nb * L,), torch.float32, dev), st.cuda_stream),
+           "quantize_tokens")
+    return q, scale
+
+
+def matmul_i8(q, scale, wq, wscale, bias=None, out_dtype=torch.float32, length=None, y=None, workspace=None,
+              stream=None):
+    """y[m, n] = scale[m] wscale[n] sum_k q[m, k] wq[n, k] (+ bias[n]), the sum exact in 32-bit integers.
+    q [T, C_pad] and wq [O, C_pad] int8 with scales as quantize_tokens gives them, bias fp32 [O].  y is
+    [T, O], or with `length` = L channel-major [T / L, O, L]; fp32 or bf16 (y's dtype, or out_dtype)."""
+    for name, t in (("q", q), ("wq", wq)):
+        if not torch.is_tensor(t) or not t.is_cuda or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-dimensional device tensor")
+    (T, pad), O, dev = q.shape, wq.shape[0], q.device
+    if length is not None and (length < 1 or T % length):
+        raise ValueError("length must divide the number of tokens")
+    nb, L = (1, T) if length is None else (T // length, length)
+    shape = (T, O) if length is None else (nb, O, L)
+    st = _lm_stream(stream, dev)
+    y = _fresh(y, shape, out_dtype, st)
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported dtype {y.dtype}; expected float32 or bfloat16")
+    args = (_device("q", q, (T, pad), torch.int8, dev), _device("scale", scale, (T,), torch.float32, dev),
+            _device("wq", wq, (O, pad), torch.int8, dev), _device("wscale", wscale, (O,), torch.float32, dev),
+            _optional("bias", bias, (O,), torch.float32, dev), int(length is not None), dtype_code(y),
+            _device("y", y, shape, y.dtype, dev))
+    need = _SZ(0)
+    _check(_lib.matmul_i8_workspace_size(nb, L, O, pad, MAX_WORKSPACE_BYTES, ctypes.byref(need)),
+           "matmul_i8_workspace_size")
+    wp, wb, _keep = _scratch(need.value, workspace, st)
+    _check(_lib.matmul_i8(nb, L, O, pad, *args, wp, wb, st.cuda_stream), "matmul_i8")
+    return y

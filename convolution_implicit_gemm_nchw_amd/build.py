@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmiconv.so")
 SOURCES = ["igemm.hip", "patch.hip", "bwdf16.hip", "pointwise.hip", "tinyc.hip", "noalloc.hip", "bwd_bias.hip",
-           "convnd.hip", "plan.cpp", "ndplan.cpp", "abi.cpp"]
+           "convnd.hip", "causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip",
+           "plan.cpp", "ndplan.cpp", "abi.cpp", "ssm_abi.cpp"]
 ARCH = "gfx950"
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 

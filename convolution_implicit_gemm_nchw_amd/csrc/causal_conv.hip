@@ -1,0 +1,314 @@
+// causal_conv.hip -- short causal depthwise convolution on [B][D][L] with bias
+// and SiLU: forward, backward and one-token step.
+//
+//   u[t] = bias + sum_k w[k] x~[t-K+1+k],  y = u * sigmoid(u)
+//
+// Memory bound: an element is read and written once (backward: x and dy read, dx
+// written) for 2K multiply-adds.  A thread takes eight consecutive time steps of
+// one row, so one 16-byte load (bf16) brings its own steps and a second, which
+// the neighbouring lane has loaded too, the K-1 before them; taps and bias stay
+// in registers.  K is a template argument: the tap loops unroll.
+#include "device.h"
+#include "ssm.h"
+#include "ssm_device.h"
+
+namespace miconv {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// The eight steps before t (x~ at t < 0 from the initial state).  t is a multiple of 8.
+template <int DT, int K>
+DEVI void load_before(const typename Elem<DT>::T *row, const typename Elem<DT>::T *init, int t, int end,
+                      float (&v)[8]) {
+    if (t > 0) {
+        load8<DT>(row, t - 8, end, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (init && i >= 9 - K) ? Elem<DT>::get(init[i - (9 - K)]) : 0.0f;
+    }
+}
+
+// x~ with the initial state in front: full[f], f = 0 .. n + K - 2.
+template <int DT, int K>
+DEVI float full_at(const typename Elem<DT>::T *row, const typename Elem<DT>::T *init, int f) {
+    if (f >= K - 1) return Elem<DT>::get(row[f - (K - 1)]);
+    return init ? Elem<DT>::get(init[f]) : 0.0f;
+}
+
+template <int DT, int K>
+__global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv_t c, int lg_tpr,
+                                                              long long row_blocks, long long work) {
+    typedef typename Elem<DT>::T T;
+    const int sub = threadIdx.x & ((1 << lg_tpr) - 1), rib = threadIdx.x >> lg_tpr;
+    const int rows_per_block = kThreads >> lg_tpr;
+    for (long long wk = blockIdx.x; wk < work; wk += gridDim.x) {
+        const long long tb = wk / row_blocks, rb = wk - tb * row_blocks;
+        const long long row = rb * rows_per_block + rib;
+        if (row >= (long long)c.B * c.D) continue;
+        const int b = (int)(row / c.D), d = (int)(row - (long long)b * c.D);
+        const long long t64 = ((tb << lg_tpr) + sub) * 8;
+        if (t64 >= c.L) continue;
+        const int t = (int)t64;
+        const int len = valid_steps(c.lengths, b, c.L);
+        const T *x = (const T *)c.x.data + b * c.x.stride_b + d * c.x.stride_d;
+        const T *init = c.initial_state ? (const T *)c.initial_state + row * (K - 1) : nullptr;
+        T *y = (T *)c.y.data + b * c.y.stride_b + d * c.y.stride_d;
+        float out[8] = {};
+        if (t < len) {
+            float v[16];
+            float (&before)[8] = *(float (*)[8])v, (&own)[8] = *(float (*)[8])(v + 8);
+            load8<DT>(x, t, len, own);
+            load_before<DT, K>(x, init, t, len, before);
+            float w[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k] = Elem<DT>::get(((const T *)c.w)[(long long)d * K + k]);
+            const float bias = c.bias ? c.bias[d] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float u = bias;
+#pragma unroll
+                for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[k], v[8 + i - (K - 1) + k], u);
+                out[i] = t + i < len ? (c.silu ? u * logistic(u) : u) : 0.0f;
+            }
+        }
+        store8<DT>(y, t, c.L, out);
+        if (t == 0 && c.final_state) {
+            T *fs = (T *)c.final_state + row * (K - 1);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) fs[j] = Elem<DT>::put(full_at<DT, K>(x, init, len + j));
+        }
+    }
+}
+
+// One work-group: channel d, items [split * per, ...) of the B * tiles eight-step
+// tiles.  A thread recomputes u of its own and the K-1 following steps (dx needs
+// their du), writes its dx and keeps its part of dw and dbias; the parts are
+// added in a fixed tree and written to part[split][d][K+1] (or dw, dbias).
+template <int DT, int K, int TH>
+__global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, int tiles, long long per, int splits,
+                                                        float *part) {
+    typedef typename Elem<DT>::T T;
+    __shared__ float red[TH / 64][K + 1];
+    const int d = blockIdx.x, split = blockIdx.y;
+    const long long items = (long long)c.B * tiles;
+    const long long first = split * per, last = first + per < items ? first + per : items;
+    float w[K], dw[K], db = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        w[k] = Elem<DT>::get(((const T *)c.w)[(long long)d * K + k]);
+        dw[k] = 0.0f;
+    }
+    const float bias = c.bias ? c.bias[d] : 0.0f;
+    for (long long it = first + threadIdx.x; it < last; it += TH) {
+        const int b = (int)(it / tiles), t = (int)(it - (long long)b * tiles) * 8;
+        const int len = valid_steps(c.lengths, b, c.L);
+        const long long row = (long long)b * c.D + d;
+        const T *x = (const T *)c.x.data + b * c.x.stride_b + d * c.x.stride_d;
+        const T *dy = (const T *)c.dy.data + b * c.dy.stride_b + d * c.dy.stride_d;
+        const T *init = c.initial_state ? (const T *)c.initial_state + row * (K - 1) : nullptr;
+        const T *dfs = c.d_final_state ? (const T *)c.d_final_state + row * (K - 1) : nullptr;
+        float v[24], g[16], out[8] = {};
+        if (t < len) {
+            load_before<DT, K>(x, init, t, len, *(float (*)[8])v);
+            load8<DT>(x, t, len, *(float (*)[8])(v + 8));
+            load8<DT>(x, t + 8, len, *(float (*)[8])(v + 16));
+            load8<DT>(dy, t, len, *(float (*)[8])g);
+            load8<DT>(dy, t + 8, len, *(float (*)[8])(g + 8));
+#pragma unroll
+            for (int i = 0; i < 8 + K - 1; ++i) {
+                if (!c.silu) continue;
+                float u = bias;
+#pragma unroll
+                for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[k], v[8 + i - (K - 1) + k], u);
+                const float sg = logistic(u);
+                // a step past the end has du = 0 whatever u is there
+                g[i] = t + i < len ? g[i] * (sg * __builtin_fmaf(u, 1.0f - sg, 1.0f)) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float s = 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    s = __builtin_fmaf(w[k], g[i + K - 1 - k], s);
+                    dw[k] = __builtin_fmaf(g[i], v[8 + i - (K - 1) + k], dw[k]);
+                }
+                db += g[i];
+                const int j = t + i - len + K - 1;   // final_state[j] is x[t + i]
+                if (dfs && j >= 0 && t + i < len) s += Elem<DT>::get(dfs[j]);
+                out[i] = t + i < len ? s : 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = 0.0f;
+        }
+        if (c.dx.data) store8<DT>((T *)c.dx.data + b * c.dx.stride_b + d * c.dx.stride_d, t, c.L, out);
+        if (t == 0 && c.d_initial_state) {
+            T *di = (T *)c.d_initial_state + row * (K - 1);
+#pragma unroll
+            for (int f = 0; f < K - 1; ++f) {
+                float s = 0.0f;
+#pragma unroll
+                for (int u = 0; u <= f; ++u) s = __builtin_fmaf(w[f - u], g[u], s);
+                if (dfs && f >= len) s += Elem<DT>::get(dfs[f - len]);
+                di[f] = Elem<DT>::put(s);
+            }
+        }
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int k = 0; k <= K; ++k) {
+        float s = k < K ? dw[k < K ? k : 0] : db;
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
+        if (lane == 0) red[wave][k] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x <= K) {
+        float s = 0.0f;
+        for (int i = 0; i < TH / 64; ++i) s += red[i][threadIdx.x];
+        if (splits > 1) {
+            part[((long long)split * c.D + d) * (K + 1) + threadIdx.x] = s;
+        } else if (threadIdx.x < K) {
+            if (c.dw) c.dw[(long long)d * K + threadIdx.x] = s;
+        } else if (c.dbias) {
+            c.dbias[d] = s;
+        }
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void causal_bwd_reduce(const float *part, float *dw, float *dbias, int D, int K,
+                                                              int splits) {
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, n = (long long)D * (K + 1);
+    if (i >= n) return;
+    float s = 0.0f;
+    for (int z = 0; z < splits; ++z) s += part[z * n + i];
+    const int d = (int)(i / (K + 1)), k = (int)(i - (long long)d * (K + 1));
+    if (k < K) {
+        if (dw) dw[(long long)d * K + k] = s;
+    } else if (dbias) {
+        dbias[d] = s;
+    }
+}
+
+// One thread per (sequence, channel): all reads of a state come before its writes,
+// so state_out may be state.
+template <int DT, int K>
+__global__ __launch_bounds__(kThreads) void causal_step_kernel(int B, int D, int silu, miconv_rows_t x,
+                                                               const typename Elem<DT>::T *state, int slots,
+                                                               const int *slot_of, const typename Elem<DT>::T *w,
+                                                               const float *bias, typename Elem<DT>::T *state_out,
+                                                               miconv_rows_t y) {
+    typedef typename Elem<DT>::T T;
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (long long)B * D) return;
+    const int b = (int)(i / D), d = (int)(i - (long long)b * D);
+    const int slot = slot_of ? slot_of[b] : b;
+    T *yo = (T *)y.data + b * y.stride_b + d * y.stride_d;
+    if (slot < 0 || slot >= slots) {
+        *yo = Elem<DT>::put(0.0f);
+        return;
+    }
+    const long long so = ((long long)slot * D + d) * (K - 1);
+    float v[K], u = bias ? bias[d] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) v[k] = Elem<DT>::get(state[so + k]);
+    v[K - 1] = Elem<DT>::get(((const T *)x.data)[b * x.stride_b + d * x.stride_d]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[(long long)d * K + k] , v[k], u);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) state_out[so + k] = Elem<DT>::put(v[k + 1]);
+    *yo = Elem<DT>::put(silu ? u * logistic(u) : u);
+}
+
+int lg2_up(long long v, int most) {
+    int l = 0;
+    while (l < most && (1ll << l) < v) ++l;
+    return l;
+}
+
+template <int DT, int K>
+int fwd_k(const miconv_causal_conv_t &c, hipStream_t st) {
+    const long long tiles = (c.L + 7) / 8;
+    const int lg = lg2_up(tiles, 8);
+    const long long rpb = kThreads >> lg, row_blocks = ((long long)c.B * c.D + rpb - 1) / rpb;
+    const long long work = row_blocks * ((tiles + (1ll << lg) - 1) >> lg);
+    const unsigned grid = (unsigned)(work < (1ll << 30) ? work : (1ll << 30));
+    hipLaunchKernelGGL((causal_fwd_kernel<DT, K>), dim3(grid), dim3(kThreads), 0, st, c, lg, row_blocks, work);
+    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+}
+
+template <int DT, int K>
+int bwd_k(const miconv_causal_conv_t &c, int splits, float *ws, hipStream_t st) {
+    const int tiles = (c.L + 7) / 8;
+    const long long items = (long long)c.B * tiles, per = (items + splits - 1) / splits;
+    if (per <= 64)
+        hipLaunchKernelGGL((causal_bwd_kernel<DT, K, 64>), dim3(c.D, splits), dim3(64), 0, st, c, tiles, per, splits,
+                           ws);
+    else
+        hipLaunchKernelGGL((causal_bwd_kernel<DT, K, kThreads>), dim3(c.D, splits), dim3(kThreads), 0, st, c, tiles,
+                           per, splits, ws);
+    if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    if (splits > 1 && (c.dw || c.dbias)) {
+        const long long n = (long long)c.D * (K + 1);
+        hipLaunchKernelGGL(causal_bwd_reduce, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                           ws, c.dw, c.dbias, c.D, K, splits);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    }
+    return MICONV_OK;
+}
+
+template <int DT, int K>
+int step_k(int B, int D, int silu, miconv_rows_t x, const void *state, int slots, const int *slot_of, const void *w,
+           const float *bias, void *state_out, miconv_rows_t y, hipStream_t st) {
+    typedef typename Elem<DT>::T T;
+    const long long n = (long long)B * D;
+    hipLaunchKernelGGL((causal_step_kernel<DT, K>), dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                       st, B, D, silu, x, (const T *)state, slots, slot_of, (const T *)w, bias, (T *)state_out, y);
+    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+}
+
+}  // namespace
+
+// Enough work-groups per channel to fill 256 CUs four deep, each with at least
+// 256 tiles of eight steps; fewer where the partial sums do not fit the budget.
+int causal_bwd_splits(const miconv_causal_conv_t &c, size_t budget) {
+    const long long items = (long long)c.B * ((c.L + 7) / 8), one = (long long)c.D * (c.K + 1) * 4;
+    long long s = 1024 / c.D;
+    if (s > items / 256) s = items / 256;
+    if (s > 64) s = 64;
+    if (s > (long long)budget / one) s = (long long)budget / one;
+    return s < 1 ? 1 : (int)s;
+}
+
+#define MICONV_BY_TAPS(F, ...)                                      \
+    switch (K) {                                                    \
+        case 1: return dtype ? F<1, 1>(__VA_ARGS__) : F<0, 1>(__VA_ARGS__); \
+        case 2: return dtype ? F<1, 2>(__VA_ARGS__) : F<0, 2>(__VA_ARGS__); \
+        case 3: return dtype ? F<1, 3>(__VA_ARGS__) : F<0, 3>(__VA_ARGS__); \
+        case 4: return dtype ? F<1, 4>(__VA_ARGS__) : F<0, 4>(__VA_ARGS__); \
+        case 5: return dtype ? F<1, 5>(__VA_ARGS__) : F<0, 5>(__VA_ARGS__); \
+        case 6: return dtype ? F<1, 6>(__VA_ARGS__) : F<0, 6>(__VA_ARGS__); \
+        case 7: return dtype ? F<1, 7>(__VA_ARGS__) : F<0, 7>(__VA_ARGS__); \
+        case 8: return dtype ? F<1, 8>(__VA_ARGS__) : F<0, 8>(__VA_ARGS__); \
+        default: return MICONV_ERR_BAD_DIM;                         \
+    }
+
+int launch_causal_fwd(const miconv_causal_conv_t &c, int dtype, hipStream_t st) {
+    const int K = c.K;
+    MICONV_BY_TAPS(fwd_k, c, st)
+}
+
+int launch_causal_bwd(const miconv_causal_conv_t &c, int dtype, int splits, float *ws, hipStream_t st) {
+    const int K = c.K;
+    MICONV_BY_TAPS(bwd_k, c, splits, ws, st)
+}
+
+int launch_causal_step(int B, int D, int K, int silu, int dtype, miconv_rows_t x, const void *state, int slots,
+                       const int *slot_of, const void *w, const float *bias, void *state_out, miconv_rows_t y,
+                       hipStream_t st) {
+    MICONV_BY_TAPS(step_k, B, D, silu, x, state, slots, slot_of, w, bias, state_out, y, st)
+}
+
+}  // namespace miconv

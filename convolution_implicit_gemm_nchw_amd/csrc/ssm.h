@@ -1,0 +1,46 @@
+// ssm.h -- host entries into the kernels of the state-space operators.  The
+// arguments are already validated; structures go to the kernels by value.
+#pragma once
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+
+#include "../../include/miconv.h"
+
+namespace miconv {
+
+// Time steps between two saved scan states.
+constexpr int kScanChunk = 512;
+
+inline int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
+
+// Channels one work-group of the scan's backward pass sums dB and dC over, and
+// the resulting number of partial sums per group of channels.
+struct ScanBwdPlan {
+    int R, parts;
+    size_t off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
+};
+ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s);
+
+// Work-groups per channel of the convolution's backward pass.
+int causal_bwd_splits(const miconv_causal_conv_t &c, size_t budget);
+
+int launch_causal_fwd(const miconv_causal_conv_t &c, int dtype, hipStream_t st);
+int launch_causal_bwd(const miconv_causal_conv_t &c, int dtype, int splits, float *ws, hipStream_t st);
+int launch_causal_step(int B, int D, int K, int silu, int dtype, miconv_rows_t x, const void *state, int slots,
+                       const int *slot_of, const void *w, const float *bias, void *state_out, miconv_rows_t y,
+                       hipStream_t st);
+
+int launch_scan_fwd(const miconv_scan_t &s, int dtype, hipStream_t st);
+int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st);
+int launch_scan_step(const miconv_scan_t &s, int dtype, const float *state, int slots, const int *slot_of,
+                     float *state_out, hipStream_t st);
+
+int launch_quantize(int B, int L, int C, int dtype, const void *x, long long sb, long long sl, long long sc,
+                    signed char *q, float *scale, hipStream_t st);
+// Splits of the summed axis matmul_i8 takes under `budget` bytes of workspace.
+int i8_splits(int T, int O, int K, size_t budget);
+int launch_matmul_i8(int B, int L, int O, int K, const signed char *q, const float *qs, const signed char *wq,
+                     const float *ws_, const float *bias, int channel_major, int out_dtype, void *y, int splits,
+                     int *part, hipStream_t st);
+
+}  // namespace miconv

@@ -1,0 +1,133 @@
+// ssm_device.h -- device helpers of the state-space operators: loads and stores
+// of eight consecutive time steps, exp / softplus / logistic in fp32.
+#pragma once
+#include "device.h"
+
+namespace miconv {
+
+// Rows start at any element, so vectors are aligned to the element only.
+typedef uint32_t u32x4_row __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<0> {
+    typedef float T;
+    static DEVI float get(float v) { return v; }
+    static DEVI float put(float v) { return v; }
+};
+template <>
+struct Elem<1> {
+    typedef __bf16 T;
+    static DEVI float get(__bf16 v) { return (float)v; }
+    static DEVI __bf16 put(float v) { return (__bf16)v; }   // to nearest, ties to even
+};
+
+// v[i] = row[t + i] for t + i < end, 0 from end on (not loaded).  t >= 0.
+template <int DT>
+DEVI void load8(const typename Elem<DT>::T *row, int t, int end, float (&v)[8]) {
+    if (t + 8 <= end) {
+        if constexpr (DT == 1) {
+            const u32x4 r = *(const u32x4_row *)(row + t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(r[i] << 16);
+                v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+            }
+        } else {
+            const u32x4 r0 = *(const u32x4_row *)(row + t), r1 = *(const u32x4_row *)(row + t + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = __uint_as_float(r0[i]);
+                v[4 + i] = __uint_as_float(r1[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = t + i < end ? Elem<DT>::get(row[t + i]) : 0.0f;
+    }
+}
+
+// row[t + i] = v[i] for t + i < end.
+template <int DT>
+DEVI void store8(typename Elem<DT>::T *row, int t, int end, const float (&v)[8]) {
+    if (t + 8 <= end) {
+        if constexpr (DT == 1) {
+            u32x4 r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                const bf16x2 p = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+                r[i] = __builtin_bit_cast(uint32_t, p);
+            }
+            *(u32x4_row *)(row + t) = r;
+        } else {
+            u32x4 r0, r1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r0[i] = __float_as_uint(v[i]);
+                r1[i] = __float_as_uint(v[4 + i]);
+            }
+            *(u32x4_row *)(row + t) = r0;
+            *(u32x4_row *)(row + t + 4) = r1;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (t + i < end) row[t + i] = Elem<DT>::put(v[i]);
+    }
+}
+
+DEVI float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
+DEVI float rcp_hw(float v) { return __builtin_amdgcn_rcpf(v); }
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = 1.92596299112661746887e-8f;   // log2(e) - kLog2e
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// exp(v) for v <= 0 with the rounding of v*log2(e) put right: the plain product
+// is off by |v| 2^-24 relative, which a step size of softplus(-7) would keep.
+DEVI float exp_neg(float v) {
+    const float t = v * kLog2e;
+    const float r = __builtin_fmaf(v, kLog2eLow, __builtin_fmaf(v, kLog2e, -t));
+    const float e = exp2_hw(t);
+    return v < -100.0f ? 0.0f : __builtin_fmaf(e, r * kLn2, e);
+}
+
+// 1 / (1 + exp(-v)), from exp(-|v|) so that neither end overflows.
+DEVI float logistic(float v) {
+    const float e = exp_neg(-__builtin_fabsf(v));
+    const float r = rcp_hw(1.0f + e);
+    return v < 0.0f ? e * r : r;
+}
+
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], with
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: the odd series, whose first term
+// left out is s^16/17 <= 2e-9 of the sum.  No cancellation at either end.
+DEVI float softplus(float v) {
+    const float e = exp_neg(-__builtin_fabsf(v));
+    const float s = e * rcp_hw(2.0f + e), q = s * s;
+    float p = 2.0f / 15.0f;
+    p = __builtin_fmaf(p, q, 2.0f / 13.0f);
+    p = __builtin_fmaf(p, q, 2.0f / 11.0f);
+    p = __builtin_fmaf(p, q, 2.0f / 9.0f);
+    p = __builtin_fmaf(p, q, 2.0f / 7.0f);
+    p = __builtin_fmaf(p, q, 2.0f / 5.0f);
+    p = __builtin_fmaf(p, q, 2.0f / 3.0f);
+    p = __builtin_fmaf(p, q, 2.0f);
+    return (v > 0.0f ? v : 0.0f) + s * p;
+}
+
+// Orders this wave's LDS accesses: what a lane wrote before is read by the others after.
+DEVI void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+DEVI int valid_steps(const int *lengths, int b, int L) {
+    if (!lengths) return L;
+    const int n = lengths[b];
+    return n < 0 ? 0 : (n > L ? L : n);
+}
+
+}  // namespace miconv

@@ -432,6 +432,165 @@ int convnd_workspace_size(int pass, const miconv_nd_desc_t *d, int dtype, size_t
 int convnd_describe(int pass, const miconv_nd_desc_t *d, int dtype, size_t workspace_bytes, char *buf,
                     size_t buflen);
 
+/*
+ * Operators of a state-space language-model layer.  Activations are
+ * [B][D][L] (batch, channel, time; time fastest): the layout of a 1-D
+ * convolution's tensors and of the 1x1 convolutions that project into and out
+ * of such a layer.  Conventions that differ from the convolutions above:
+ *
+ * Strides    an activation is a miconv_rows_t: element (b, d, t) is at
+ *            data + b*stride_b + d*stride_d + t (elements).  Inputs may have any
+ *            non-negative strides (halves of one projection, broadcast rows);
+ *            an output's rows must not overlap each other.
+ * Alignment  to the element only.  Tensors may be larger than 2 GiB; offsets
+ *            are 64-bit.  Every size is at most 2^30, and so is B*D.
+ * Types      dtype names the element type of every activation, of the
+ *            convolution's filter and of the activations' gradients.  Biases, A,
+ *            D, scan states and all gradients of parameters, B and C are fp32.
+ *            Sums, states and statistics are fp32 or wider; an activation is
+ *            rounded once, at its store.
+ * Lengths    lengths (int [B] in device memory, or NULL for L everywhere) gives
+ *            the valid time steps of each right-padded sequence, clamped to
+ *            0..L.  Steps past it are neither read into any result nor do they
+ *            change a state; outputs and gradients there are 0.
+ * Optional   a NULL pointer stands for an absent operand (bias, state, gate, ...).
+ * Errors     as above; MICONV_ERR_BAD_DIM covers sizes and strides out of range.
+ * Determinism results are bitwise reproducible for fixed arguments and
+ *            workspace_bytes (no atomics).
+ */
+#define MICONV_CAUSAL_MAX_TAPS 8
+#define MICONV_SCAN_MAX_STATES 64
+
+typedef struct miconv_rows {
+    void *data;
+    long long stride_b, stride_d;   /* elements */
+} miconv_rows_t;
+
+/*
+ * Short causal (depthwise) convolution.  w [D][K], K = 1..8, bias [D] fp32:
+ *   u[b,d,t] = bias[d] + sum_k w[d,k] * x~[b,d,t-K+1+k],   y = silu ? u*sigmoid(u) : u
+ * x~ at t < 0 is initial_state [B][D][K-1] (oldest first; NULL: zeros).
+ * final_state [B][D][K-1] gets the last K-1 values of (initial_state, valid x):
+ * the state from which causal_conv1d_step or the next chunk continues.
+ * The backward pass recomputes u.  dy (and d_final_state, the gradient of
+ * final_state) in; dx, dw [D][K] fp32, dbias [D] fp32, d_initial_state
+ * [B][D][K-1] out, each optional.
+ */
+typedef struct miconv_causal_conv {
+    int B, D, L, K, silu;
+    miconv_rows_t x;
+    const void *w;
+    const float *bias;
+    const void *initial_state;
+    const int *lengths;
+    miconv_rows_t y;              /* forward */
+    void *final_state;
+    miconv_rows_t dy;             /* backward */
+    const void *d_final_state;
+    miconv_rows_t dx;
+    float *dw, *dbias;
+    void *d_initial_state;
+} miconv_causal_conv_t;
+
+int causal_conv1d_fwd(const miconv_causal_conv_t *c, int dtype, void *stream);
+int causal_conv1d_bwd(const miconv_causal_conv_t *c, int dtype, void *workspace, size_t workspace_bytes,
+                      void *stream);
+/* Workspace the backward pass uses under workspace_limit (0 is always enough). */
+int causal_conv1d_bwd_workspace_size(const miconv_causal_conv_t *c, int dtype, size_t workspace_limit,
+                                     size_t *bytes_out);
+/*
+ * One time step for each of B sequences: x, y [B][D] (stride_b), state
+ * [slots][D][K-1].  With slot_of (int [B] in device memory) sequence b uses
+ * state slot_of[b]; an index outside 0..slots-1 marks an unused row: its y is 0
+ * and no state is touched (two rows of one call must not name one slot).
+ * Without, slots must be B.  state_out is state (updated in place) or a
+ * disjoint array of the same shape.
+ */
+int causal_conv1d_step(int B, int D, int K, int silu, int dtype, miconv_rows_t x, const void *state, int slots,
+                       const int *slot_of, const void *w, const float *bias, void *state_out, miconv_rows_t y,
+                       void *stream);
+
+/*
+ * Selective scan.  x, delta, z, y [B][D][L]; A [D][N] fp32, N = 1..64; Bm, Cm
+ * [B][G][N][L] (stride_b, stride_g, stride_n; time contiguous), channel d reading
+ * group d / (D/G); D_skip, delta_bias [D] fp32:
+ *   dt = softplus ? log(1 + exp(delta + delta_bias)) : delta + delta_bias
+ *   h_t[n] = exp(dt_t * A[n]) * h_{t-1}[n] + dt_t * x_t * Bm_t[n]
+ *   v_t    = sum_n Cm_t[n] * h_t[n] + D_skip * x_t,     y_t = z ? v_t * silu(z_t) : v_t
+ * h_{-1} is initial_state [B][D][N] fp32 (NULL: zeros); final_state gets the
+ * state after the last valid step.  A is meant to be negative; a decay that
+ * grows overflows as the recurrence does.
+ * `states` (selective_scan_states_size bytes; the forward pass writes it when it
+ * is not NULL) holds the states between chunks of time steps, from which the
+ * backward pass rebuilds the rest.
+ * Backward: dy and d_final_state in; dx, ddelta, dz, and in fp32 dA [D][N],
+ * dB, dC [B][G][N][L] packed, dD [D], ddelta_bias [D], d_initial_state [B][D][N]
+ * out.  dx, ddelta, dA, dB and dC are required; the others are optional, dz
+ * is given exactly when z is.
+ */
+typedef struct miconv_scan_in {
+    void *data;
+    long long stride_b, stride_g, stride_n;   /* elements */
+} miconv_scan_in_t;
+
+typedef struct miconv_scan {
+    int B, D, L, N, G, softplus;
+    miconv_rows_t x, delta, z;
+    const float *A;
+    miconv_scan_in_t Bm, Cm;
+    const float *D_skip, *delta_bias, *initial_state;
+    const int *lengths;
+    miconv_rows_t y;              /* forward */
+    float *final_state;
+    float *states;                /* written by the forward pass, read by the backward pass */
+    miconv_rows_t dy;             /* backward */
+    const float *d_final_state;
+    miconv_rows_t dx, ddelta, dz;
+    float *dA, *dB, *dC, *dD, *ddelta_bias, *d_initial_state;
+} miconv_scan_t;
+
+int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *stream);
+int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+int selective_scan_states_size(int B, int D, int L, int N, size_t *bytes_out);
+/* Workspace the backward pass needs (MICONV_ERR_WORKSPACE when given less). */
+int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out);
+/*
+ * One time step: x, delta, z, y [B][D], Bm, Cm [B][G][N] (L = 1 in the structure;
+ * lengths, initial_state, final_state and states unused), state [slots][D][N]
+ * fp32 with slot_of and state_out as in causal_conv1d_step.
+ */
+int selective_scan_step(const miconv_scan_t *s, int dtype, const float *state, int slots, const int *slot_of,
+                        float *state_out, void *stream);
+
+/*
+ * Products in 8-bit integers with a scale for each token and channel.
+ *
+ * quantize_tokens: token (b, l) of x has C values at data + b*stride_b +
+ * l*stride_l + c*stride_c, with stride_c == 1 (tokens first) or stride_l == 1
+ * (channel-major).  With m = max_c |x|:
+ *   scale[b*L + l] = m / 127,   q[b*L + l][c] = round_half_even(127 * x / m)  (0 for m == 0)
+ * A token that holds an infinity or a NaN gets the scale NaN and q = 0.  The
+ * rounding is that of the exact quotient.  q is [B*L][C_pad], C_pad = C rounded
+ * up to a multiple of 128, the padding 0.
+ */
+#define MICONV_I8_PAD 128
+
+int quantize_tokens(int B, int L, int C, int dtype, const void *x, long long stride_b, long long stride_l,
+                    long long stride_c, signed char *q, float *scale, void *stream);
+/*
+ * matmul_i8: for token m = b*L + l and channel n
+ *   y = qscale[m] * wscale[n] * sum_k q[m][k] * wq[n][k]  (+ bias[n])
+ * q [B*L][C_pad], wq [O][C_pad] int8, 16-byte aligned, C_pad a multiple of 128
+ * and at most 131072 (the integer sum then fits 32 bits).  y is [B*L][O]
+ * (channel_major 0) or [B][O][L] (1), packed, out_dtype fp32 or bf16.  The sum is
+ * exact; it is rounded to fp32 once, scaled by qscale, then wscale, then the bias
+ * is added.  Any workspace_bytes is valid; few tokens split the sum over it.
+ */
+int matmul_i8(int B, int L, int O, int C_pad, const signed char *q, const float *qscale, const signed char *wq,
+              const float *wscale, const float *bias, int channel_major, int out_dtype, void *y, void *workspace,
+              size_t workspace_bytes, void *stream);
+int matmul_i8_workspace_size(int B, int L, int O, int C_pad, size_t workspace_limit, size_t *bytes_out);
+
 /* Static text for a status code (never NULL). */
 const char *miconv_status_string(int status);
 

@@ -1,0 +1,255 @@
+"""State-space operators without a GPU: every refusal of the C ABI (fake device addresses that are never
+dereferenced), the binding's checks, workspace sizes, and the reference gradients against differences.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import convolution_implicit_gemm_nchw_amd as mc
+import ssm_reference as ref
+
+OK, E_NULL, E_DIM, E_OUT, E_DT, E_ALIAS, E_ALIGN, E_WS, E_HIP, E_PASS, E_BIG, E_INDEX = range(12)
+SLOT = 0x10000000          # spacing of the fake addresses
+
+
+def at(i):
+    return (i + 1) * SLOT
+
+
+def rows(i, D=6, L=40):
+    return mc._Rows(at(i), D * L, L)
+
+
+def conv_args(**kw):
+    c = mc._CausalConv(B=2, D=6, L=40, K=4, silu=1, x=rows(0), w=at(1), bias=at(2), initial_state=at(3),
+                       lengths=at(4), y=rows(5), final_state=at(6), dy=rows(7), d_final_state=at(8), dx=rows(9),
+                       dw=at(10), dbias=at(11), d_initial_state=at(12))
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def scan_in(i, N=5, L=40, G=2):
+    return mc._ScanIn(at(i), G * N * L, N * L, L)
+
+
+def scan_args(**kw):
+    s = mc._Scan(B=2, D=6, L=40, N=5, G=2, softplus=1, x=rows(0), delta=rows(1), z=rows(2), A=at(3), Bm=scan_in(4),
+                 Cm=scan_in(5), D_skip=at(6), delta_bias=at(7), initial_state=at(8), lengths=at(9), y=rows(10),
+                 final_state=at(11), states=at(12), dy=rows(13), d_final_state=at(14), dx=rows(15), ddelta=rows(16),
+                 dz=rows(17), dA=at(18), dB=at(19), dC=at(20), dD=at(21), ddelta_bias=at(22), d_initial_state=at(23))
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def cfwd(dtype=0, **kw):
+    return mc.lib().causal_conv1d_fwd(ctypes.byref(conv_args(**kw)), dtype, None)
+
+
+def cbwd(dtype=0, ws=None, wb=0, **kw):
+    return mc.lib().causal_conv1d_bwd(ctypes.byref(conv_args(**kw)), dtype, ws, wb, None)
+
+
+def sfwd(dtype=0, **kw):
+    return mc.lib().selective_scan_fwd(ctypes.byref(scan_args(**kw)), dtype, None)
+
+
+def sbwd(dtype=0, ws=at(30), wb=1 << 24, **kw):
+    return mc.lib().selective_scan_bwd(ctypes.byref(scan_args(**kw)), dtype, ws, wb, None)
+
+
+def test_convolution_refusals():
+    lib = mc.lib()
+    assert lib.causal_conv1d_fwd(None, 0, None) == E_NULL
+    for call in (cfwd, cbwd):
+        for bad in ({"B": 0}, {"D": -1}, {"L": 0}, {"K": 0}, {"K": 9}, {"B": (1 << 30) + 1},
+                    {"x": mc._Rows(at(0), -1, 40)}):
+            assert call(**bad) == E_DIM, bad
+        assert call(dtype=2) == E_DT
+        assert call(B=1 << 20, D=1 << 20) == E_BIG
+        assert call(x=mc._Rows(at(0), 1 << 50, 40)) == E_BIG
+        assert call(w=None) == E_NULL
+        assert call(x=mc._Rows(None, 240, 40)) == E_NULL
+        assert call(x=mc._Rows(at(0) + 2, 240, 40)) == E_ALIGN
+        assert call(dtype=1, x=mc._Rows(at(0) + 1, 240, 40)) == E_ALIGN
+        assert call(bias=at(2) + 2) == E_ALIGN
+    assert cfwd(y=mc._Rows(None, 0, 0)) == E_NULL
+    assert cfwd(y=rows(0)) == E_ALIAS                                 # in place
+    assert cfwd(y=mc._Rows(at(5), 240, 39)) == E_DIM                  # rows of y overlap
+    assert cfwd(y=mc._Rows(at(5), 0, 40)) == E_DIM
+    assert cfwd(final_state=at(0)) == E_ALIAS
+    assert cfwd(final_state=at(5) + 16) == E_ALIAS                    # two outputs
+    assert cbwd(dy=mc._Rows(None, 0, 0)) == E_NULL
+    assert cbwd(dx=rows(7)) == E_ALIAS
+    assert cbwd(dw=at(0)) == E_ALIAS
+    assert cbwd(ws=None, wb=64) == E_NULL
+    # a second half of the same buffer is no overlap for views of one batch stride, one step less is
+    x, half = mc._Rows(at(0), 480, 40), at(0) + 240 * 4
+    assert cfwd(x=x, y=mc._Rows(half - 4, 480, 40)) == E_ALIAS
+    assert cfwd(x=x, y=mc._Rows(half + 4, 480, 40)) == E_ALIAS
+    step = lib.causal_conv1d_step
+    r = mc._Rows(at(0), 6, 1)
+    args = [2, 6, 4, 1, 0, r, at(1), 2, None, at(2), at(3), at(4), mc._Rows(at(5), 6, 1), None]
+
+    def stepped(**kw):
+        a = list(args)
+        for k, v in kw.items():
+            a[int(k[1:])] = v
+        return step(*a)
+    assert stepped(_0=0) == E_DIM and stepped(_2=9) == E_DIM and stepped(_7=0) == E_DIM
+    assert stepped(_7=3) == E_DIM                                     # more states than sequences, no slots
+    assert stepped(_4=7) == E_DT
+    assert stepped(_6=None) == E_NULL and stepped(_9=None) == E_NULL and stepped(_11=None) == E_NULL
+    assert stepped(_11=at(1) + 4) == E_ALIAS                          # shifted on its own input
+    assert stepped(_12=mc._Rows(at(0), 6, 1)) == E_ALIAS
+
+
+def test_scan_refusals():
+    lib = mc.lib()
+    assert lib.selective_scan_fwd(None, 0, None) == E_NULL
+    for call in (sfwd, sbwd):
+        for bad in ({"B": 0}, {"D": 0}, {"L": 0}, {"N": 0}, {"N": 65}, {"G": 0}, {"G": 4},
+                    {"delta": mc._Rows(at(1), 240, -40)}, {"Bm": mc._ScanIn(at(4), 400, 200, -1)}):
+            assert call(**bad) == E_DIM, bad
+        assert call(dtype=5) == E_DT
+        assert call(B=1 << 20, D=3 << 20, G=1) == E_BIG
+        assert call(A=None) == E_NULL
+        assert call(Cm=mc._ScanIn(None, 400, 200, 40)) == E_NULL
+        assert call(delta=mc._Rows(None, 0, 0)) == E_NULL
+        assert call(A=at(3) + 1) == E_ALIGN
+        assert call(dtype=1, Bm=mc._ScanIn(at(4) + 1, 400, 200, 40)) == E_ALIGN
+    assert sfwd(y=mc._Rows(None, 0, 0)) == E_NULL
+    assert sfwd(y=rows(1)) == E_ALIAS
+    assert sfwd(final_state=at(8)) == E_ALIAS                         # states are not updated in place
+    assert sfwd(states=at(10)) == E_ALIAS
+    assert sbwd(ws=None, wb=0) == E_NULL
+    assert sbwd(wb=128) == E_WS
+    assert sbwd(states=None) == E_NULL
+    assert sbwd(dz=mc._Rows(None, 0, 0)) == E_NULL                    # a gate without its gradient
+    assert sbwd(z=mc._Rows(None, 0, 0)) == E_NULL                     # and the other way round
+    assert sbwd(dA=None) == E_NULL and sbwd(dB=None) == E_NULL
+    assert sbwd(dx=rows(13)) == E_ALIAS
+    assert sbwd(dC=at(30)) == E_ALIAS                                 # an output on the workspace
+    step = lambda slots=2, state=at(24), out=at(25), **kw: lib.selective_scan_step(  # noqa: E731
+        ctypes.byref(scan_args(L=kw.pop("L", 1), **kw)), 0, state, slots, None, out, None)
+    assert step(L=2) == E_DIM and step(slots=0) == E_DIM and step(slots=3) == E_DIM
+    assert step(state=None) == E_NULL and step(out=None) == E_NULL
+    assert step(out=at(24) + 4) == E_ALIAS
+
+
+def test_integer_product_refusals():
+    lib = mc.lib()
+    qt = lambda B=2, L=8, C=100, dt=0, x=at(0), s=(800, 100, 1), q=at(1), sc=at(2): lib.quantize_tokens(  # noqa: E731
+        B, L, C, dt, x, *s, q, sc, None)
+    assert qt(B=0) == E_DIM and qt(L=0) == E_DIM and qt(C=0) == E_DIM and qt(C=131073) == E_DIM
+    assert qt(s=(800, 100, 2)) == E_DIM and qt(s=(-1, 100, 1)) == E_DIM
+    assert qt(dt=9) == E_DT
+    assert qt(x=None) == E_NULL and qt(q=None) == E_NULL and qt(sc=None) == E_NULL
+    assert qt(x=at(0) + 2) == E_ALIGN and qt(q=at(1) + 8) == E_ALIGN
+    assert qt(q=at(0)) == E_ALIAS
+    assert qt(B=1 << 20, L=1 << 20) == E_BIG
+
+    def mm(B=2, L=8, O=16, K=128, q=at(0), qs=at(1), w=at(2), ws=at(3), bias=at(4), cm=0, dt=0, y=at(5), work=None,
+           wb=0):
+        return lib.matmul_i8(B, L, O, K, q, qs, w, ws, bias, cm, dt, y, work, wb, None)
+    assert mm(B=0) == E_DIM and mm(O=0) == E_DIM and mm(K=64) == E_DIM and mm(K=200) == E_DIM and mm(K=131200) == E_DIM
+    assert mm(dt=3) == E_DT
+    assert mm(q=None) == E_NULL and mm(w=None) == E_NULL and mm(y=None) == E_NULL and mm(wb=64) == E_NULL
+    assert mm(q=at(0) + 4) == E_ALIGN and mm(w=at(2) + 8) == E_ALIGN and mm(qs=at(1) + 1) == E_ALIGN
+    assert mm(y=at(2)) == E_ALIAS
+    assert mm(B=1 << 15, L=1 << 15, O=1 << 20) == E_BIG
+
+
+def test_workspace_sizes():
+    need = ctypes.c_size_t(0)
+    lib = mc.lib()
+    c = conv_args(B=64, L=8192)
+    assert lib.causal_conv1d_bwd_workspace_size(ctypes.byref(c), 0, 10 ** 9, ctypes.byref(need)) == OK
+    assert need.value > 0
+    for limit in (0, 100, 10 ** 4):
+        assert lib.causal_conv1d_bwd_workspace_size(ctypes.byref(c), 0, limit, ctypes.byref(need)) == OK
+        assert need.value <= limit
+    assert lib.selective_scan_states_size(3, 7, 1025, 5, ctypes.byref(need)) == OK
+    assert need.value % (4 * 3 * 7 * 5) == 0 and need.value > 0
+    assert lib.selective_scan_states_size(0, 7, 10, 5, ctypes.byref(need)) == E_DIM
+    assert lib.selective_scan_bwd_workspace_size(ctypes.byref(scan_args()), 0, ctypes.byref(need)) == OK
+    assert need.value > 0
+    for limit in (0, 1000, 10 ** 9):
+        assert lib.matmul_i8_workspace_size(1, 8, 512, 4096, limit, ctypes.byref(need)) == OK
+        assert need.value <= limit
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(2, 6, 40), torch.zeros(6, 4)
+    with pytest.raises(ValueError):
+        mc.causal_conv1d_fwd(x, w)
+    with pytest.raises(ValueError):
+        mc.selective_scan_step(x[:, :, 0], x[:, :, 0], w, x, x, torch.zeros(2, 6, 4))
+    with pytest.raises(ValueError):
+        mc.quantize_tokens(x)
+    with pytest.raises(ValueError):
+        mc.matmul_i8(w, w, w, w)
+
+
+# ------------------------------------------------------------------ the references' gradients
+
+def difference(f, v, i, h=1e-5):
+    a, b = v.copy(), v.copy()
+    a.flat[i] += h
+    b.flat[i] -= h
+    return (f(a) - f(b)) / (2 * h)
+
+
+@pytest.mark.parametrize("act", [False, True])
+def test_reference_convolution_gradients_against_differences(act):
+    rng = np.random.default_rng(3)
+    B, D, L, K = 3, 2, 7, 4
+    lengths = np.array([7, 0, 2])
+    v = {"x": rng.normal(size=(B, D, L)), "w": rng.normal(size=(D, K)), "bias": rng.normal(size=D),
+         "h0": rng.normal(size=(B, D, K - 1))}
+    dy, dfs = rng.normal(size=(B, D, L)), rng.normal(size=(B, D, K - 1))
+
+    def loss(name, val):
+        r = ref.conv(**{**v, name: val}, act=act, lengths=lengths)
+        return (r["y"][0] * dy).sum() + (r["fs"][0] * dfs).sum()
+    r = ref.conv(**v, act=act, lengths=lengths, dy=dy, dfs=dfs)
+    for name, out in (("x", "dx"), ("w", "dw"), ("bias", "db"), ("h0", "dh0")):
+        for i in range(v[name].size):
+            # second-order error of the difference h^2 = 1e-10 times third derivatives of order 10
+            assert abs(difference(lambda q: loss(name, q), v[name], i) - r[out][0].flat[i]) < 1e-7, (name, i)
+
+
+@pytest.mark.parametrize("gate,sp", [(True, True), (False, True), (True, False)])
+def test_reference_scan_gradients_against_differences(gate, sp):
+    rng = np.random.default_rng(4)
+    B, D, L, N, G = 3, 4, 5, 3, 2
+    lengths = np.array([5, 0, 2])
+    v = {"x": rng.normal(size=(B, D, L)), "delta": 0.3 * rng.normal(size=(B, D, L)) + (0 if sp else 0.5),
+         "A": -np.exp(0.3 * rng.normal(size=(D, N))), "Bm": rng.normal(size=(B, G, N, L)),
+         "Cm": rng.normal(size=(B, G, N, L)), "D": rng.normal(size=D), "bias": 0.3 * rng.normal(size=D),
+         "h0": rng.normal(size=(B, D, N))}
+    if gate:
+        v["z"] = rng.normal(size=(B, D, L))
+    dy, dfs = rng.normal(size=(B, D, L)), rng.normal(size=(B, D, N))
+
+    def loss(name, val):
+        r = ref.scan(**{**v, name: val}, sp=sp, lengths=lengths)
+        return (r["y"][0] * dy).sum() + (r["fs"][0] * dfs).sum()
+    r = ref.scan(**v, sp=sp, lengths=lengths, dy=dy, dfs=dfs)
+    names = {"x": "dx", "delta": "ddelta", "A": "dA", "Bm": "dB", "Cm": "dC", "D": "dD", "bias": "ddelta_bias",
+             "h0": "dh0"}
+    if gate:
+        names["z"] = "dz"
+    for name, out in names.items():
+        for i in range(v[name].size):
+            assert abs(difference(lambda q: loss(name, q), v[name], i) - r[out][0].flat[i]) < 1e-6, (name, i)
+
+
+def test_quantisation_reference_rounds_halves_to_even():
+    x = np.array([[254.0, 1.0, 3.0, 5.0, -1.0, -3.0], [0.0] * 6, [np.nan, 1, 2, 3, 4, 5], [np.inf, 1, 2, 3, 4, 5]])
+    q, s = ref.quantize(x)
+    assert q[0].tolist() == [127, 0, 2, 2, 0, -2] and not q[1:].any()
+    assert s[0] == np.float32(2) and s[1] == 0 and np.isnan(s[2]) and np.isnan(s[3])
