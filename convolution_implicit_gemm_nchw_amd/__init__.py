@@ -30,6 +30,7 @@ fallback path.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -627,8 +628,11 @@ def convnd_bwd_filter(x, dy, filt, groups=1, pad_lo=None, pad_hi=None, stride=No
     return dw
 
 
-
 # ---------------------------------------------------------------- state-space operators
+#
+# One token's calls are short, so the host side counts: the C structures are packed in one
+# struct.pack each (native alignment is the C layout), an operand is looked at once, and with no
+# stream given the current one is asked for its handle only.
 
 _LL = ctypes.c_longlong
 
@@ -642,12 +646,14 @@ class _ScanIn(ctypes.Structure):
 
 
 class _CausalConv(ctypes.Structure):
+    """miconv_causal_conv_t."""
     _fields_ = [("B", _I), ("D", _I), ("L", _I), ("K", _I), ("silu", _I), ("x", _Rows), ("w", _VP), ("bias", _VP),
                 ("initial_state", _VP), ("lengths", _VP), ("y", _Rows), ("final_state", _VP), ("dy", _Rows),
                 ("d_final_state", _VP), ("dx", _Rows), ("dw", _VP), ("dbias", _VP), ("d_initial_state", _VP)]
 
 
 class _Scan(ctypes.Structure):
+    """miconv_scan_t."""
     _fields_ = [("B", _I), ("D", _I), ("L", _I), ("N", _I), ("G", _I), ("softplus", _I), ("x", _Rows),
                 ("delta", _Rows), ("z", _Rows), ("A", _VP), ("Bm", _ScanIn), ("Cm", _ScanIn), ("D_skip", _VP),
                 ("delta_bias", _VP), ("initial_state", _VP), ("lengths", _VP), ("y", _Rows), ("final_state", _VP),
@@ -656,17 +662,22 @@ class _Scan(ctypes.Structure):
                 ("d_initial_state", _VP)]
 
 
-_CP, _SP, _SZP = ctypes.POINTER(_CausalConv), ctypes.POINTER(_Scan), ctypes.POINTER(_SZ)
+_CONV_PACK = struct.Struct("@5i Pqq4P Pqq P Pqq P Pqq 3P").pack
+_SCAN_PACK = struct.Struct("@6i PqqPqqPqq P PqqqPqqq 4P Pqq 2P Pqq P PqqPqqPqq 6P").pack
+assert struct.calcsize("@5i Pqq4P Pqq P Pqq P Pqq 3P") == ctypes.sizeof(_CausalConv)
+assert struct.calcsize("@6i PqqPqqPqq P PqqqPqqq 4P Pqq 2P Pqq P PqqPqqPqq 6P") == ctypes.sizeof(_Scan)
+
+_SZP = ctypes.POINTER(_SZ)
 for _name, _args in {
-        "causal_conv1d_fwd": [_CP, _I, _VP],
-        "causal_conv1d_bwd": [_CP, _I, _VP, _SZ, _VP],
-        "causal_conv1d_bwd_workspace_size": [_CP, _I, _SZ, _SZP],
+        "causal_conv1d_fwd": [_VP, _I, _VP],
+        "causal_conv1d_bwd": [_VP, _I, _VP, _SZ, _VP],
+        "causal_conv1d_bwd_workspace_size": [_VP, _I, _SZ, _SZP],
         "causal_conv1d_step": [_I, _I, _I, _I, _I, _Rows, _VP, _I, _VP, _VP, _VP, _VP, _Rows, _VP],
-        "selective_scan_fwd": [_SP, _I, _VP],
-        "selective_scan_bwd": [_SP, _I, _VP, _SZ, _VP],
+        "selective_scan_fwd": [_VP, _I, _VP],
+        "selective_scan_bwd": [_VP, _I, _VP, _SZ, _VP],
         "selective_scan_states_size": [_I, _I, _I, _I, _SZP],
-        "selective_scan_bwd_workspace_size": [_SP, _I, _SZP],
-        "selective_scan_step": [_SP, _I, _VP, _I, _VP, _VP, _VP],
+        "selective_scan_bwd_workspace_size": [_VP, _I, _SZP],
+        "selective_scan_step": [_VP, _I, _VP, _I, _VP, _VP, _VP],
         "quantize_tokens": [_I, _I, _I, _I, _VP, _LL, _LL, _LL, _VP, _VP, _VP],
         "matmul_i8": [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _SZ, _VP],
         "matmul_i8_workspace_size": [_I, _I, _I, _I, _SZ, _SZP]}.items():
@@ -674,76 +685,94 @@ for _name, _args in {
     _fn.argtypes = _args
     _fn.restype = _I
 
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
-def _device(name, t, shape, dtype, dev, packed=True):
-    """Raises unless t is a device tensor of this shape, type and device, contiguous when packed."""
-    if not torch.is_tensor(t) or not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
-    if packed and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+
+def _misfit(name, t, shape, dtype, dev):
+    if not torch.is_tensor(t):
+        raise ValueError(f"{name} must be a tensor")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {dev}, not "
+                     f"{t.dtype} of {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+def _packed(name, t, shape, dtype, dev):
+    """Address of a contiguous tensor of this shape, type and device; raises on any other."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _misfit(name, t, shape, dtype, dev)
     return t.data_ptr()
 
 
 def _optional(name, t, shape, dtype, dev):
-    return None if t is None else _device(name, t, shape, dtype, dev)
+    return 0 if t is None else _packed(name, t, shape, dtype, dev)
 
 
-def _rows(name, t, shape, dtype, dev, out=False):
-    """The miconv_rows_t of a [B, D, L] (or [B, D]) tensor with contiguous time steps.  A fresh
-    output is packed; a given one may be a view, as inputs may."""
+def _rows(name, t, shape, dtype, dev):
+    """(address, batch stride, channel stride) of a [B, D, L] or [B, D] tensor, a view with contiguous
+    time steps as it may be; zeros for None."""
     if t is None:
-        return _Rows(None, 0, 0)
-    _device(name, t, shape, dtype, dev, packed=False)
-    if len(shape) == 3 and shape[2] > 1 and t.stride(2) != 1:
+        return 0, 0, 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _misfit(name, t, shape, dtype, dev)
+    st = t.stride()
+    if len(st) == 3 and st[2] != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
-    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), st[0], st[1]
 
 
 def _activation(name, t, ndim):
-    if not torch.is_tensor(t) or not t.is_cuda or t.dim() != ndim:
+    """(dtype code, dtype, device index) of an operator's leading operand."""
+    if not isinstance(t, torch.Tensor) or t.dim() != ndim or not t.is_cuda:
         raise ValueError(f"{name} must be a {ndim}-dimensional device tensor")
-    return dtype_code(t)
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}; expected float32 or bfloat16")
+    return code, t.dtype, t.get_device()
 
 
-def _lm_stream(stream, dev):
-    """The stream the call runs on (the current one of the operands' device by default)."""
-    return stream if stream is not None else torch.cuda.current_stream(dev)
+def _handle(stream, dev):
+    """The hipStream_t of the call: the given stream's, or the current one's of the operands' device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _scratch(need, workspace, stream):
-    """(pointer, bytes, owner): the caller's workspace tensor or one from `stream`'s pool."""
+def _new(shape, dtype, like, stream):
+    """A tensor from the pool of the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scratch(need, workspace, like, stream):
+    """(pointer, bytes, owner): the caller's workspace tensor or one from the stream's pool."""
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if need == 0:
         return None, 0, None
-    with torch.cuda.stream(stream):
-        ws = torch.empty(need, dtype=torch.uint8, device=stream.device)
+    ws = _new((need,), torch.uint8, like, stream)
     return ws.data_ptr(), need, ws
 
 
-def _fresh(t, shape, dtype, stream):
-    """t, or a new tensor from the pool of the stream that writes it."""
-    if t is not None:
-        return t
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=stream.device)
+class _on:
+    """Makes the operands' device current for a call, when it is not."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        self.old = torch._C._cuda_getDevice()
+        if self.old != self.dev:
+            torch._C._cuda_setDevice(self.dev)
+
+    def __exit__(self, *_):
+        if self.old != self.dev:
+            torch._C._cuda_setDevice(self.old)
 
 
-def _conv_args(x, w, bias, silu, initial_state, lengths):
-    _activation("x", x, 3)
-    B, D, L = x.shape
-    if not torch.is_tensor(w) or w.dim() != 2:
+def _taps(w):
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be [D, K]")
-    K, dev, dt = w.shape[1], x.device, x.dtype
-    c = _CausalConv(B=B, D=D, L=L, K=K, silu=int(bool(silu)))
-    c.x = _rows("x", x, (B, D, L), dt, dev)
-    c.w = _device("w", w, (D, K), dt, dev)
-    c.bias = _optional("bias", bias, (D,), torch.float32, dev)
-    c.initial_state = _optional("initial_state", initial_state, (B, D, K - 1), dt, dev)
-    c.lengths = _optional("lengths", lengths, (B,), torch.int32, dev)
-    return c, (B, D, L, K), dt, dev
+    return w.shape[1]
 
 
 def causal_conv1d_fwd(x, w, bias=None, silu=False, initial_state=None, lengths=None, y=None, final_state=None,
@@ -752,12 +781,19 @@ def causal_conv1d_fwd(x, w, bias=None, silu=False, initial_state=None, lengths=N
     [B, D, K-1] before the first step (zeros without).  x [B, D, L] may be a view with contiguous
     time steps; w [D, K], K <= 8, in x's dtype; bias fp32.  lengths (int32 [B]) are the valid steps of
     right-padded sequences; y is 0 past them.  final_state [B, D, K-1], when given, is written."""
-    c, (B, D, L, K), dt, dev = _conv_args(x, w, bias, silu, initial_state, lengths)
-    st = _lm_stream(stream, dev)
-    y = _fresh(y, (B, D, L), dt, st)
-    c.y = _rows("y", y, (B, D, L), dt, dev)
-    c.final_state = _optional("final_state", final_state, (B, D, K - 1), dt, dev)
-    _check(_lib.causal_conv1d_fwd(ctypes.byref(c), dtype_code(x), st.cuda_stream), "causal_conv1d_fwd")
+    code, dt, dev = _activation("x", x, 3)
+    shape, K = x.shape, _taps(w)
+    B, D, L = shape
+    held = (B, D, K - 1)
+    if y is None:
+        y = _new(shape, dt, x, stream)
+    c = _CONV_PACK(B, D, L, K, bool(silu), *_rows("x", x, shape, dt, dev), _packed("w", w, (D, K), dt, dev),
+                   _optional("bias", bias, (D,), torch.float32, dev),
+                   _optional("initial_state", initial_state, held, dt, dev),
+                   _optional("lengths", lengths, (B,), torch.int32, dev), *_rows("y", y, shape, dt, dev),
+                   _optional("final_state", final_state, held, dt, dev), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    with _on(dev):
+        _check(_lib.causal_conv1d_fwd(c, code, _handle(stream, dev)), "causal_conv1d_fwd")
     return y
 
 
@@ -765,93 +801,101 @@ def causal_conv1d_bwd(x, w, dy, bias=None, silu=False, initial_state=None, lengt
                       dx=None, dw=None, dbias=None, d_initial_state=None, workspace=None, stream=None):
     """(dx, dw, dbias) of causal_conv1d_fwd for the output gradient dy (and d_final_state): dx in x's
     dtype, dw [D, K] and dbias [D] fp32 (None without a bias).  d_initial_state, when given, is written."""
-    c, (B, D, L, K), dt, dev = _conv_args(x, w, bias, silu, initial_state, lengths)
-    st = _lm_stream(stream, dev)
-    c.dy = _rows("dy", dy, (B, D, L), dt, dev)
-    c.d_final_state = _optional("d_final_state", d_final_state, (B, D, K - 1), dt, dev)
-    dx = _fresh(dx, (B, D, L), dt, st)
-    dw = _fresh(dw, (D, K), torch.float32, st)
-    if bias is not None:
-        dbias = _fresh(dbias, (D,), torch.float32, st)
-    c.dx = _rows("dx", dx, (B, D, L), dt, dev)
-    c.dw = _device("dw", dw, (D, K), torch.float32, dev)
-    c.dbias = _optional("dbias", dbias, (D,), torch.float32, dev)
-    c.d_initial_state = _optional("d_initial_state", d_initial_state, (B, D, K - 1), dt, dev)
+    code, dt, dev = _activation("x", x, 3)
+    shape, K, f32 = x.shape, _taps(w), torch.float32
+    B, D, L = shape
+    held = (B, D, K - 1)
+    if dx is None:
+        dx = _new(shape, dt, x, stream)
+    if dw is None:
+        dw = _new((D, K), f32, x, stream)
+    if bias is not None and dbias is None:
+        dbias = _new((D,), f32, x, stream)
+    c = _CONV_PACK(B, D, L, K, bool(silu), *_rows("x", x, shape, dt, dev), _packed("w", w, (D, K), dt, dev),
+                   _optional("bias", bias, (D,), f32, dev), _optional("initial_state", initial_state, held, dt, dev),
+                   _optional("lengths", lengths, (B,), torch.int32, dev), 0, 0, 0, 0, *_rows("dy", dy, shape, dt, dev),
+                   _optional("d_final_state", d_final_state, held, dt, dev), *_rows("dx", dx, shape, dt, dev),
+                   _packed("dw", dw, (D, K), f32, dev), _optional("dbias", dbias, (D,), f32, dev),
+                   _optional("d_initial_state", d_initial_state, held, dt, dev))
     need = _SZ(0)
-    code = dtype_code(x)
-    _check(_lib.causal_conv1d_bwd_workspace_size(ctypes.byref(c), code, MAX_WORKSPACE_BYTES, ctypes.byref(need)),
-           "causal_conv1d_bwd_workspace_size")
-    wp, wb, _keep = _scratch(need.value, workspace, st)
-    _check(_lib.causal_conv1d_bwd(ctypes.byref(c), code, wp, wb, st.cuda_stream), "causal_conv1d_bwd")
+    if workspace is None:
+        _check(_lib.causal_conv1d_bwd_workspace_size(c, code, MAX_WORKSPACE_BYTES, need),
+               "causal_conv1d_bwd_workspace_size")
+    wp, wb, _keep = _scratch(need.value, workspace, x, stream)
+    with _on(dev):
+        _check(_lib.causal_conv1d_bwd(c, code, wp, wb, _handle(stream, dev)), "causal_conv1d_bwd")
     return dx, dw, dbias
 
 
-def _step_slots(state, state_out, slots, B, dev):
-    """(number of states, pointer to the slot of each sequence, where the states go)."""
+def _slots(state, slots, B, dev):
+    """(number of states, address of the slot of each sequence)."""
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must have 3 dimensions")
     if slots is None and state.shape[0] != B:
         raise ValueError("without slots, state must hold one state for each sequence")
-    return state.shape[0], _optional("slots", slots, (B,), torch.int32, dev), state if state_out is None else state_out
+    return state.shape[0], None if slots is None else _packed("slots", slots, (B,), torch.int32, dev)
 
 
 def causal_conv1d_step(x, state, w, bias=None, silu=False, state_out=None, slots=None, y=None, stream=None):
     """One time step of causal_conv1d_fwd: x [B, D], state [B, D, K-1] (updated in place, or written to
     state_out) -> y [B, D].  With slots (int32 [B]) state is a pool [S, D, K-1] and sequence b uses
     state slots[b]; an index outside the pool marks an unused row (y = 0)."""
-    code = _activation("x", x, 2)
-    B, D = x.shape
-    if not torch.is_tensor(w) or w.dim() != 2 or not torch.is_tensor(state) or state.dim() != 3:
-        raise ValueError("w must be [D, K] and state [B, D, K-1]")
-    K, dev, dt = w.shape[1], x.device, x.dtype
-    S, sp, state_out = _step_slots(state, state_out, slots, B, dev)
-    st = _lm_stream(stream, dev)
-    y = _fresh(y, (B, D), dt, st)
-    _check(_lib.causal_conv1d_step(
-        B, D, K, int(bool(silu)), code, _rows("x", x, (B, D), dt, dev),
-        _device("state", state, (S, D, K - 1), dt, dev), S, sp, _device("w", w, (D, K), dt, dev),
-        _optional("bias", bias, (D,), torch.float32, dev), _device("state_out", state_out, (S, D, K - 1), dt, dev),
-        _rows("y", y, (B, D), dt, dev), st.cuda_stream), "causal_conv1d_step")
+    code, dt, dev = _activation("x", x, 2)
+    shape, K = x.shape, _taps(w)
+    B, D = shape
+    S, sp = _slots(state, slots, B, dev)
+    held = (S, D, K - 1)
+    if y is None:
+        y = _new(shape, dt, x, stream)
+    sin = _packed("state", state, held, dt, dev)
+    with _on(dev):
+        _check(_lib.causal_conv1d_step(
+            B, D, K, bool(silu), code, _Rows(*_rows("x", x, shape, dt, dev)), sin, S, sp,
+            _packed("w", w, (D, K), dt, dev), _optional("bias", bias, (D,), torch.float32, dev),
+            sin if state_out is None else _packed("state_out", state_out, held, dt, dev),
+            _Rows(*_rows("y", y, shape, dt, dev)), _handle(stream, dev)), "causal_conv1d_step")
     return y
 
 
-def _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias, softplus, lengths, step=False):
-    _activation("x", x, 2 if step else 3)
-    nb, nd = x.shape[:2]
-    L = 1 if step else x.shape[2]
-    dev, dt, f32 = x.device, x.dtype, torch.float32
-    if not torch.is_tensor(A) or A.dim() != 2 or not torch.is_tensor(Bm) or Bm.dim() != (3 if step else 4):
+def _scan_in(name, t, shape, dtype, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _misfit(name, t, shape, dtype, dev)
+    st = t.stride()
+    if len(st) == 4 and st[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
+    return t.data_ptr(), st[0], st[1], st[2]
+
+
+def _scan_common(x, delta, A, Bm, Cm, D, z, delta_bias, softplus, initial_state, lengths, step=False):
+    """(the leading fields of miconv_scan_t, [B, D, L, N, G], dtype code, dtype, device index)."""
+    code, dt, dev = _activation("x", x, 2 if step else 3)
+    shape, f32 = x.shape, torch.float32
+    nb, nd = shape[0], shape[1]
+    if (not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(Bm, torch.Tensor)
+            or Bm.dim() != (3 if step else 4)):
         raise ValueError("A must be [D, N], B and C [B, G, N, L] ([B, G, N] for one step)")
     N, G = A.shape[1], Bm.shape[1]
-    s = _Scan(B=nb, D=nd, L=L, N=N, G=G, softplus=int(bool(softplus)))
-    s.x = _rows("x", x, x.shape, dt, dev)
-    s.delta = _rows("delta", delta, x.shape, dt, dev)
-    s.z = _rows("z", z, x.shape, dt, dev)
-    s.A = _device("A", A, (nd, N), f32, dev)
-    for field, name, t in (("Bm", "B", Bm), ("Cm", "C", Cm)):
-        _device(name, t, (nb, G, N) + (() if step else (L,)), dt, dev, packed=False)
-        if not step and L > 1 and t.stride(3) != 1:
-            raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
-        setattr(s, field, _ScanIn(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
-    s.D_skip = _optional("D", D, (nd,), f32, dev)
-    s.delta_bias = _optional("delta_bias", delta_bias, (nd,), f32, dev)
-    s.lengths = _optional("lengths", lengths, (nb,), torch.int32, dev)
-    return s, (nb, nd, L, N, G), dt, dev
+    L = 1 if step else shape[2]
+    bc = (nb, G, N) if step else (nb, G, N, L)
+    f = (nb, nd, L, N, G, bool(softplus), *_rows("x", x, shape, dt, dev), *_rows("delta", delta, shape, dt, dev),
+         *_rows("z", z, shape, dt, dev), _packed("A", A, (nd, N), f32, dev), *_scan_in("B", Bm, bc, dt, dev),
+         *_scan_in("C", Cm, bc, dt, dev), _optional("D", D, (nd,), f32, dev),
+         _optional("delta_bias", delta_bias, (nd,), f32, dev),
+         _optional("initial_state", initial_state, (nb, nd, N), f32, dev),
+         _optional("lengths", lengths, (nb,), torch.int32, dev))
+    return f, (nb, nd, L, N, G), code, dt, dev
+
+
+def _states_count(x, A):
+    need = _SZ(0)
+    _check(_lib.selective_scan_states_size(x.shape[0], x.shape[1], x.shape[2], A.shape[1], need),
+           "selective_scan_states_size")
+    return need.value // 4
 
 
 def selective_scan_states(x, A, stream=None):
     """A buffer for the states that selective_scan_fwd saves for selective_scan_bwd."""
-    need = _SZ(0)
-    _check(_lib.selective_scan_states_size(x.shape[0], x.shape[1], x.shape[2], A.shape[1], ctypes.byref(need)),
-           "selective_scan_states_size")
-    return _fresh(None, (need.value // 4,), torch.float32, _lm_stream(stream, x.device))
-
-
-def _states_ptr(states, x, A):
-    if states is None:
-        return None
-    need = _SZ(0)
-    _check(_lib.selective_scan_states_size(x.shape[0], x.shape[1], x.shape[2], A.shape[1], ctypes.byref(need)),
-           "selective_scan_states_size")
-    return _device("states", states, (need.value // 4,), torch.float32, x.device)
+    return _new((_states_count(x, A),), torch.float32, x, stream)
 
 
 def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=False, initial_state=None,
@@ -862,14 +906,16 @@ def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softp
     (channel d reads group d // (D // G)), D and delta_bias fp32, initial_state [B, D, N] fp32.  lengths
     as in causal_conv1d_fwd.  final_state [B, D, N] and states (selective_scan_states), when given, are
     written."""
-    s, (nb, nd, L, N, G), dt, dev = _scan_args(x, delta, A, B, C, D, z, delta_bias, softplus, lengths)
-    st = _lm_stream(stream, dev)
-    y = _fresh(y, (nb, nd, L), dt, st)
-    s.y = _rows("y", y, (nb, nd, L), dt, dev)
-    s.initial_state = _optional("initial_state", initial_state, (nb, nd, N), torch.float32, dev)
-    s.final_state = _optional("final_state", final_state, (nb, nd, N), torch.float32, dev)
-    s.states = _states_ptr(states, x, A)
-    _check(_lib.selective_scan_fwd(ctypes.byref(s), dtype_code(x), st.cuda_stream), "selective_scan_fwd")
+    f, (nb, nd, L, N, G), code, dt, dev = _scan_common(x, delta, A, B, C, D, z, delta_bias, softplus, initial_state,
+                                                       lengths)
+    if y is None:
+        y = _new(x.shape, dt, x, stream)
+    s = _SCAN_PACK(*f, *_rows("y", y, x.shape, dt, dev),
+                   _optional("final_state", final_state, (nb, nd, N), torch.float32, dev),
+                   0 if states is None else _packed("states", states, (_states_count(x, A),), torch.float32, dev),
+                   0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    with _on(dev):
+        _check(_lib.selective_scan_fwd(s, code, _handle(stream, dev)), "selective_scan_fwd")
     return y
 
 
@@ -880,30 +926,28 @@ def selective_scan_bwd(x, delta, A, B, C, dy, states, D=None, z=None, delta_bias
     the forward pass saved for the same operands.  A dict of dx, ddelta, dz (x's dtype; dx, ddelta and dz
     may be given, as views too) and dA, dB, dC, dD, ddelta_bias (fp32, B and C packed), None where the
     operand is absent.  d_initial_state [B, D, N], when given, is written."""
-    s, (nb, nd, L, N, G), dt, dev = _scan_args(x, delta, A, B, C, D, z, delta_bias, softplus, lengths)
-    st, f32 = _lm_stream(stream, dev), torch.float32
-    s.dy = _rows("dy", dy, (nb, nd, L), dt, dev)
+    f, (nb, nd, L, N, G), code, dt, dev = _scan_common(x, delta, A, B, C, D, z, delta_bias, softplus, None, lengths)
+    shape, f32 = x.shape, torch.float32
     if states is None:
         raise ValueError("states of the forward pass are needed")
-    s.states = _states_ptr(states, x, A)
-    s.d_final_state = _optional("d_final_state", d_final_state, (nb, nd, N), f32, dev)
-    s.d_initial_state = _optional("d_initial_state", d_initial_state, (nb, nd, N), f32, dev)
-    r = {"dx": _fresh(dx, (nb, nd, L), dt, st), "ddelta": _fresh(ddelta, (nb, nd, L), dt, st), "dz": None,
-         "dD": None, "ddelta_bias": None}
-    if z is not None:
-        r["dz"] = _fresh(dz, (nb, nd, L), dt, st)
-    for name, shape, wanted in (("dA", (nd, N), True), ("dB", (nb, G, N, L), True), ("dC", (nb, G, N, L), True),
-                                ("dD", (nd,), D is not None), ("ddelta_bias", (nd,), delta_bias is not None)):
-        if wanted:
-            r[name] = _fresh(None, shape, f32, st)
-            setattr(s, name, r[name].data_ptr())
-    for name in ("dx", "ddelta", "dz"):
-        setattr(s, name, _rows(name, r[name], (nb, nd, L), dt, dev))
-    need, code = _SZ(0), dtype_code(x)
-    _check(_lib.selective_scan_bwd_workspace_size(ctypes.byref(s), code, ctypes.byref(need)),
-           "selective_scan_bwd_workspace_size")
-    wp, wb, _keep = _scratch(need.value, workspace, st)
-    _check(_lib.selective_scan_bwd(ctypes.byref(s), code, wp, wb, st.cuda_stream), "selective_scan_bwd")
+    r = {"dx": _new(shape, dt, x, stream) if dx is None else dx,
+         "ddelta": _new(shape, dt, x, stream) if ddelta is None else ddelta,
+         "dz": None if z is None else _new(shape, dt, x, stream) if dz is None else dz,
+         "dA": _new((nd, N), f32, x, stream), "dB": _new((nb, G, N, L), f32, x, stream),
+         "dC": _new((nb, G, N, L), f32, x, stream), "dD": None if D is None else _new((nd,), f32, x, stream),
+         "ddelta_bias": None if delta_bias is None else _new((nd,), f32, x, stream)}
+    s = _SCAN_PACK(*f, 0, 0, 0, 0, _packed("states", states, (_states_count(x, A),), f32, dev),
+                   *_rows("dy", dy, shape, dt, dev), _optional("d_final_state", d_final_state, (nb, nd, N), f32, dev),
+                   *_rows("dx", r["dx"], shape, dt, dev), *_rows("ddelta", r["ddelta"], shape, dt, dev),
+                   *_rows("dz", r["dz"], shape, dt, dev), r["dA"].data_ptr(), r["dB"].data_ptr(), r["dC"].data_ptr(),
+                   0 if D is None else r["dD"].data_ptr(), 0 if delta_bias is None else r["ddelta_bias"].data_ptr(),
+                   _optional("d_initial_state", d_initial_state, (nb, nd, N), f32, dev))
+    need = _SZ(0)
+    if workspace is None:
+        _check(_lib.selective_scan_bwd_workspace_size(s, code, need), "selective_scan_bwd_workspace_size")
+    wp, wb, _keep = _scratch(need.value, workspace, x, stream)
+    with _on(dev):
+        _check(_lib.selective_scan_bwd(s, code, wp, wb, _handle(stream, dev)), "selective_scan_bwd")
     return r
 
 
@@ -911,16 +955,18 @@ def selective_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=Non
                         slots=None, y=None, stream=None):
     """One time step of selective_scan_fwd: x, delta, z [B, D], B, C [B, G, N], state [B, D, N] fp32 (updated
     in place, or written to state_out) -> y [B, D].  slots as in causal_conv1d_step."""
-    s, (nb, nd, _, N, G), dt, dev = _scan_args(x, delta, A, B, C, D, z, delta_bias, softplus, None, step=True)
-    if not torch.is_tensor(state) or state.dim() != 3:
-        raise ValueError("state must be [B, D, N]")
-    S, sp, state_out = _step_slots(state, state_out, slots, nb, dev)
-    st = _lm_stream(stream, dev)
-    y = _fresh(y, (nb, nd), dt, st)
-    s.y = _rows("y", y, (nb, nd), dt, dev)
-    _check(_lib.selective_scan_step(
-        ctypes.byref(s), dtype_code(x), _device("state", state, (S, nd, N), torch.float32, dev), S, sp,
-        _device("state_out", state_out, (S, nd, N), torch.float32, dev), st.cuda_stream), "selective_scan_step")
+    f, (nb, nd, _, N, G), code, dt, dev = _scan_common(x, delta, A, B, C, D, z, delta_bias, softplus, None, None,
+                                                       step=True)
+    S, sp = _slots(state, slots, nb, dev)
+    if y is None:
+        y = _new(x.shape, dt, x, stream)
+    s = _SCAN_PACK(*f, *_rows("y", y, x.shape, dt, dev), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    sin = _packed("state", state, (S, nd, N), torch.float32, dev)
+    with _on(dev):
+        _check(_lib.selective_scan_step(
+            s, code, sin, S, sp,
+            sin if state_out is None else _packed("state_out", state_out, (S, nd, N), torch.float32, dev),
+            _handle(stream, dev)), "selective_scan_step")
     return y
 
 
@@ -933,34 +979,29 @@ def quantize_tokens(x, channel_major=False, q=None, scale=None, stream=None):
     steps.  Returns q [tokens, C_pad] int8 (C_pad = C rounded up to 128, zeros past C) and scale [tokens]
     fp32; tokens run over [B, L] in that order.  A token with an infinity or NaN gets a NaN scale.  A
     weight [O, C] is quantised by channel in the same way."""
-    if not torch.is_tensor(x) or not x.is_cuda or x.dim() not in (2, 3):
-        raise ValueError("x must be a device tensor of 2 or 3 dimensions")
-    code, dev = dtype_code(x), x.device
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3) or (channel_major and x.dim() != 3):
+        raise ValueError("x must be [T, C] or [B, L, C], or [B, C, L] when channel-major")
+    code, dt, dev = _activation("x", x, x.dim())
+    shape, st = x.shape, x.stride()
     if channel_major:
-        if x.dim() != 3:
-            raise ValueError("channel-major x must be [B, C, L]")
-        nb, C, L = x.shape
-        sb, sc, sl = x.stride()
+        (nb, C, L), (sb, sc, sl) = shape, st
         if L > 1 and sl != 1:
             raise ValueError("x must have contiguous time steps (stride 1 along the last axis)")
         sl = 1
     else:
-        C = x.shape[-1]
-        if C > 1 and x.stride(-1) != 1:
+        C, sc = shape[-1], 1
+        if C > 1 and st[-1] != 1:
             raise ValueError("x must have contiguous channels (stride 1 along the last axis)")
-        if x.dim() == 3:
-            (nb, L), (sb, sl) = x.shape[:2], x.stride()[:2]
-        else:
-            nb, L, sb, sl = 1, x.shape[0], 0, x.stride(0)
-        sc = 1
-    pad = -(-C // I8_PAD) * I8_PAD
-    st = _lm_stream(stream, dev)
-    q = _fresh(q, (nb * L, pad), torch.int8, st)
-    scale = _fresh(scale, (nb * L,), torch.float32, st)
-    _check(_lib.quantize_tokens(nb, L, C, code, x.data_ptr(), sb, sl, sc,
-                                _device("q", q, (nb * L, pad), torch.int8, dev),
-                                _device("scale", scale, (nb * L,), torch.float32, dev), st.cuda_stream),
-           "quantize_tokens")
+        nb, L, sb, sl = (shape[0], shape[1], st[0], st[1]) if len(shape) == 3 else (1, shape[0], 0, st[0])
+    held = (nb * L, -(-C // I8_PAD) * I8_PAD)
+    if q is None:
+        q = _new(held, torch.int8, x, stream)
+    if scale is None:
+        scale = _new((nb * L,), torch.float32, x, stream)
+    with _on(dev):
+        _check(_lib.quantize_tokens(nb, L, C, code, x.data_ptr(), sb, sl, sc, _packed("q", q, held, torch.int8, dev),
+                                    _packed("scale", scale, (nb * L,), torch.float32, dev), _handle(stream, dev)),
+               "quantize_tokens")
     return q, scale
 
 
@@ -970,24 +1011,26 @@ def matmul_i8(q, scale, wq, wscale, bias=None, out_dtype=torch.float32, length=N
     q [T, C_pad] and wq [O, C_pad] int8 with scales as quantize_tokens gives them, bias fp32 [O].  y is
     [T, O], or with `length` = L channel-major [T / L, O, L]; fp32 or bf16 (y's dtype, or out_dtype)."""
     for name, t in (("q", q), ("wq", wq)):
-        if not torch.is_tensor(t) or not t.is_cuda or t.dim() != 2:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
             raise ValueError(f"{name} must be a 2-dimensional device tensor")
-    (T, pad), O, dev = q.shape, wq.shape[0], q.device
+    (T, pad), O, dev, f32, i8 = q.shape, wq.shape[0], q.get_device(), torch.float32, torch.int8
     if length is not None and (length < 1 or T % length):
         raise ValueError("length must divide the number of tokens")
     nb, L = (1, T) if length is None else (T // length, length)
     shape = (T, O) if length is None else (nb, O, L)
-    st = _lm_stream(stream, dev)
-    y = _fresh(y, shape, out_dtype, st)
-    if y.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported dtype {y.dtype}; expected float32 or bfloat16")
-    args = (_device("q", q, (T, pad), torch.int8, dev), _device("scale", scale, (T,), torch.float32, dev),
-            _device("wq", wq, (O, pad), torch.int8, dev), _device("wscale", wscale, (O,), torch.float32, dev),
-            _optional("bias", bias, (O,), torch.float32, dev), int(length is not None), dtype_code(y),
-            _device("y", y, shape, y.dtype, dev))
+    code = _CODES.get(out_dtype if y is None else y.dtype)
+    if code is None:
+        raise ValueError("unsupported output dtype; expected float32 or bfloat16")
+    if y is None:
+        y = _new(shape, out_dtype, q, stream)
     need = _SZ(0)
-    _check(_lib.matmul_i8_workspace_size(nb, L, O, pad, MAX_WORKSPACE_BYTES, ctypes.byref(need)),
-           "matmul_i8_workspace_size")
-    wp, wb, _keep = _scratch(need.value, workspace, st)
-    _check(_lib.matmul_i8(nb, L, O, pad, *args, wp, wb, st.cuda_stream), "matmul_i8")
+    if workspace is None:
+        _check(_lib.matmul_i8_workspace_size(nb, L, O, pad, MAX_WORKSPACE_BYTES, need), "matmul_i8_workspace_size")
+    wp, wb, _keep = _scratch(need.value, workspace, q, stream)
+    with _on(dev):
+        _check(_lib.matmul_i8(nb, L, O, pad, _packed("q", q, (T, pad), i8, dev),
+                              _packed("scale", scale, (T,), f32, dev), _packed("wq", wq, (O, pad), i8, dev),
+                              _packed("wscale", wscale, (O,), f32, dev), _optional("bias", bias, (O,), f32, dev) or None,
+                              length is not None, code, _packed("y", y, shape, y.dtype, dev), wp, wb,
+                              _handle(stream, dev)), "matmul_i8")
     return y
