@@ -1,7 +1,10 @@
-// matmul_i8.hip -- y[m][n] = qs[m] ws[n] sum_k q[m][k] wq[n][k] (+ bias[n]).
+// matmul_i8.hip -- y[m][n] = qs[m] ws[n] sum_k q[m][k] wq[n][k] (+ bias[n]), the
+// sum exact in 32-bit integers on the integer MFMAs.
 //
-// A wave computes a 16 x 16 tile with 16x16x64 integer MFMAs: a lane holds 16
-// consecutive k of one row of each operand.
+// Both operands hold k contiguously, so either can be an MFMA's row operand.  The
+// one along whose axis y is contiguous (channels for token-major y, tokens for
+// channel-major y) takes the rows, called axis C below, because a lane's
+// accumulators run along the rows; the other is axis R.
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
@@ -10,61 +13,424 @@ namespace miconv {
 
 namespace {
 
-constexpr int kThreads = 256;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
 
-struct I8Out {
-    const float *qs, *ws, *bias;
+struct I8Args {
+    const signed char *c, *r;       // [NC][K], [NR][K]
+    const float *c_scale, *r_scale; // per row of c, of r
+    const float *c_bias, *r_bias;   // one of them, or none
+    int c_first;                    // order of the two scales: the tokens' first
     void *y;
-    int T, O, L, channel_major;
+    int NC, NR, K;
+    // y[r * row + c], or channel-major y[((c / len) * NR + r) * len + c % len]
+    long long row;
+    int len;                        // 0: the first form
+    FDiv fd_len;
+    int tiles_c, tiles_r;
+    int *part;                      // split sums [split][NR][NC], or null
+    int k_split;                    // bytes of k per split
 };
 
-template <int OD>
-DEVI void put_y(const I8Out &o, int m, int n, int sum) {
-    if (m >= o.T || n >= o.O) return;
-    float v = (float)sum * o.qs[m] * o.ws[n];
-    if (o.bias) v += o.bias[n];
-    long long at;
-    if (o.channel_major) {
-        const int b = m / o.L, l = m - b * o.L;
-        at = ((long long)b * o.O + n) * o.L + l;
-    } else {
-        at = (long long)m * o.O + n;
-    }
-    ((typename Elem<OD>::T *)o.y)[at] = Elem<OD>::put(v);
+DEVI float scaled(const I8Args &a, int sum, float cs, float rs) {
+    const float s = (float)sum;
+    return a.c_first ? s * cs * rs : s * rs * cs;
 }
 
+// Eight consecutive values of one row of y from c0 on.
 template <int OD>
-__global__ __launch_bounds__(kThreads) void matmul_i8_kernel(const signed char *q, const signed char *wq, int K,
-                                                             long long tiles_n, long long tiles, I8Out o) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const long long tile = (long long)blockIdx.x * (kThreads / 64) + wave;
-    if (tile >= tiles) return;
-    const int m0 = (int)(tile / tiles_n) * 16, n0 = (int)(tile % tiles_n) * 16;
-    const int r = lane & 15, kq = lane >> 4;
-    const int ma = m0 + r < o.T ? m0 + r : o.T - 1, nb = n0 + r < o.O ? n0 + r : o.O - 1;
-    const i32x4 *a = (const i32x4 *)(q + (long long)ma * K) + kq, *b = (const i32x4 *)(wq + (long long)nb * K) + kq;
-    i32x4 acc = {0, 0, 0, 0};
-    for (int k = 0; k < K / 16; k += 4) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[k], b[k], acc, 0, 0, 0);
+DEVI void put8(const I8Args &a, int r, int c0, const float (&v)[8]) {
+    typedef typename Elem<OD>::T T;
+    T *y = (T *)a.y;
+    if (a.len == 0) {
+        store8<OD>(y + (long long)r * a.row, c0, a.NC, v);
+        return;
+    }
+    const int b = (int)fdiv((uint32_t)c0, a.fd_len), l = c0 - b * a.len;
+    T *line = y + ((long long)b * a.NR + r) * a.len;
+    if (l + 8 <= a.len) {
+        store8<OD>(line, l, a.len, v);
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put_y<OD>(o, m0 + kq * 4 + i, n0 + r, acc[i]);
+    for (int i = 0; i < 8; ++i) {
+        const int c = c0 + i;
+        if (c >= a.NC) break;
+        const int bi = (int)fdiv((uint32_t)c, a.fd_len);
+        y[((long long)bi * a.NR + r) * a.len + (c - bi * a.len)] = Elem<OD>::put(v[i]);
+    }
+}
+
+// Scales and biases of eight columns.
+DEVI void columns(const I8Args &a, int c, float (&cs)[8], float (&cb)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int at = c + e < a.NC ? c + e : a.NC - 1;
+        cs[e] = a.c_scale[at];
+        cb[e] = a.c_bias ? a.c_bias[at] : 0.0f;
+    }
+}
+
+// The sums of eight columns of row r, stored as they are (split) or finished.
+template <int OD>
+DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8], const float (&cs)[8],
+                  const float (&cb)[8]) {
+    if (a.part && split >= 0) {
+        int *dst = a.part + ((long long)split * a.NR + r) * a.NC + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.NC) dst[e] = sum[e];
+        return;
+    }
+    const float rs = a.r_scale[r], rb = a.r_bias ? a.r_bias[r] : 0.0f;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = scaled(a, sum[e], cs[e], rs) + (cb[e] + rb);
+    put8<OD>(a, r, c, v);
+}
+
+// ------------------------------------------------------------------ tiles
+//
+// A work-group of WC x WR waves computes a (WC*FC*32) x (WR*FR*32) tile, a wave
+// FC x FR blocks of 32 x 32.  128 bytes of k of every row of the tile are brought
+// into LDS at a time, straight from memory (no registers in between), two stages
+// in turn: the next stage loads while this one is multiplied.  A row's eight
+// 16-byte pieces are stored at piece ^ (row & 7), so that the 32 rows that one
+// MFMA operand reads spread over all banks; since the load writes LDS in lane
+// order, the lanes fetch the pieces in that order instead.
+template <int WC, int WR, int FC, int FR>
+struct Tile {
+    static constexpr int kWaves = WC * WR, kThreads = 64 * kWaves;
+    static constexpr int C = WC * FC * 32, R = WR * FR * 32;
+    static constexpr int kBytes = (C + R) * 128;
+    static constexpr int kRowsPerLoad = kWaves * 8;
+
+    struct Src {
+        rsrc_t rc, rr;
+        uint32_t oc[C / kRowsPerLoad], orr[R / kRowsPerLoad];
+    };
+
+    static DEVI void source(const I8Args &a, int c0, int r0, Src &s) {
+        const int row = threadIdx.x >> 3, piece = (threadIdx.x & 7) ^ (row & 7);
+        s.rc = make_rsrc(a.c + (long long)c0 * a.K, 0x7fffffffu);
+        s.rr = make_rsrc(a.r + (long long)r0 * a.K, 0x7fffffffu);
+        // rows past the end read the last row; their results are not stored
+#pragma unroll
+        for (int i = 0; i < C / kRowsPerLoad; ++i) {
+            const int at = i * kRowsPerLoad + row;
+            s.oc[i] = (uint32_t)(c0 + at < a.NC ? at : a.NC - 1 - c0) * a.K + piece * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < R / kRowsPerLoad; ++i) {
+            const int at = i * kRowsPerLoad + row;
+            s.orr[i] = (uint32_t)(r0 + at < a.NR ? at : a.NR - 1 - r0) * a.K + piece * 16;
+        }
+    }
+
+    static DEVI void load(const Src &s, char *lds, int k) {
+        const int wave = uniform(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < C / kRowsPerLoad; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rc, (lds_void *)(lds + (i * kWaves + wave) * 1024), 16, s.oc[i],
+                                                     k, 0, 0);
+#pragma unroll
+        for (int i = 0; i < R / kRowsPerLoad; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rr, (lds_void *)(lds + C * 128 + (i * kWaves + wave) * 1024), 16,
+                                                     s.orr[i], k, 0, 0);
+    }
+
+    static DEVI void multiply(const char *lds, i32x16 (&acc)[FC][FR]) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int wc = wave % WC, wr = wave / WC, row = lane & 31, half = lane >> 5;
+        const char *pc = lds + (wc * FC * 32 + row) * 128, *pr = lds + C * 128 + (wr * FR * 32 + row) * 128;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int piece = ((kk * 2 + half) ^ (row & 7)) * 16;
+            i32x4 fc[FC], fr[FR];
+#pragma unroll
+            for (int i = 0; i < FC; ++i) fc[i] = *(const i32x4 *)(pc + i * 32 * 128 + piece);
+#pragma unroll
+            for (int j = 0; j < FR; ++j) fr[j] = *(const i32x4 *)(pr + j * 32 * 128 + piece);
+#pragma unroll
+            for (int i = 0; i < FC; ++i)
+#pragma unroll
+                for (int j = 0; j < FR; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fc[i], fr[j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
+template <int OD, int WC, int WR, int FC, int FR>
+__global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
+    typedef Tile<WC, WR, FC, FR> X;
+    __shared__ __attribute__((aligned(1024))) char stages[2 * X::kBytes];
+    // each XCD a contiguous range of tiles, in columns of eight C tiles: the tiles that
+    // run on it together share their operands in its L2
+    const int per_split = a.tiles_c * a.tiles_r, split = blockIdx.x / per_split;
+    const int t = xcd_remap(blockIdx.x - split * per_split, per_split);
+    const int band = t / (8 * a.tiles_r), in = t - band * 8 * a.tiles_r;
+    const int wide = a.tiles_c - band * 8 < 8 ? a.tiles_c - band * 8 : 8;
+    const int c0 = (band * 8 + in % wide) * X::C, r0 = (in / wide) * X::R;
+    typename X::Src src;
+    X::source(a, c0, r0, src);
+    i32x16 acc[FC][FR];
+#pragma unroll
+    for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int j = 0; j < FR; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    const int first = split * a.k_split, end = first + a.k_split < a.K ? first + a.k_split : a.K;
+    X::load(src, stages, first);
+    int now = 0;
+    for (int k = first; k < end; k += 128) {
+        __syncthreads();                       // this stage has arrived, the other has been read
+        if (k + 128 < end) X::load(src, stages + (X::kBytes - now), k + 128);
+        X::multiply(stages + now, acc);
+        now = X::kBytes - now;
+    }
+    __syncthreads();
+    // Through LDS, 32 rows of the wave's FC*32 columns at a time, so that y is written
+    // in 16-byte pieces of consecutive lanes; a row's pieces are permuted as above.
+    constexpr int kW = FC * 32, kMine = 32 * kW;
+    static_assert(X::kWaves * kMine * 4 <= 2 * X::kBytes, "the exchange fits the two stages");
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wc = wave % WC, wr = wave / WC;
+    int *mine = (int *)stages + wave * kMine;
+    constexpr int kLanes = kW / 8;             // lanes per row, eight columns each
+    const int col = (lane % kLanes) * 8, c = c0 + wc * kW + col;
+    float cs[8], cb[8];
+    columns(a, c, cs, cb);
+#pragma unroll
+    for (int j = 0; j < FR; ++j) {
+        const int rw = r0 + (wr * FR + j) * 32;
+#pragma unroll
+        for (int i = 0; i < FC; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                i32x4 four;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) four[e] = acc[i][j][g * 4 + e];
+                const int row = lane & 31, piece = (i * 8 + g * 2 + (lane >> 5)) ^ (row & 7);
+                *(i32x4 *)(mine + row * kW + piece * 4) = four;
+            }
+        wave_lds_sync();
+#pragma unroll 1
+        for (int p = 0; p < 32 * kLanes / 64; ++p) {
+            const int row = p * (64 / kLanes) + lane / kLanes, r = rw + row;
+            if (r >= a.NR || c >= a.NC) continue;
+            const i32x4 lo = *(const i32x4 *)(mine + row * kW + ((col >> 2) ^ (row & 7)) * 4);
+            const i32x4 hi = *(const i32x4 *)(mine + row * kW + (((col >> 2) + 1) ^ (row & 7)) * 4);
+            int sum[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[e] = lo[e];
+                sum[4 + e] = hi[e];
+            }
+            finish8<OD>(a, split, r, c, sum, cs, cb);
+        }
+        wave_lds_sync();
+    }
+}
+
+// Adds the splits' sums and finishes them.
+template <int OD>
+__global__ __launch_bounds__(256) void i8_join_kernel(I8Args a, int splits) {
+    const int per_row = (a.NC + 7) / 8;
+    const long long n = (long long)a.NR * per_row;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row) * 8;
+        int sum[8] = {};
+        for (int z = 0; z < splits; ++z) {
+            const int *p = a.part + ((long long)z * a.NR + r) * a.NC + c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < a.NC) sum[e] += p[e];
+        }
+        float cs[8], cb[8];
+        columns(a, c, cs, cb);
+        finish8<OD>(a, -1, r, c, sum, cs, cb);
+    }
+}
+
+// ------------------------------------------------------------------ few tokens
+//
+// With few tokens the weight's bytes count: each is read once, straight into
+// registers, as the row operand of 16x16x64 MFMAs.  A work-group takes 32 channels,
+// its eight waves an eighth of k each (pieces of 256 bytes in turn), and adds the
+// waves' sums in LDS.  FT blocks of 16 tokens.
+template <int OD, int FT>
+__global__ __launch_bounds__(512) void i8_few_kernel(const signed char *q, const signed char *wq, const float *qs,
+                                                     const float *ws, const float *bias, int T, int O, int K, int L,
+                                                     int channel_major, void *y) {
+    __shared__ int red[8][32][FT * 16 + 1];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane & 15, kq = (lane >> 4) * 16;
+    const int n0 = blockIdx.x * 32;
+    const signed char *pw[2], *pq[FT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int n = n0 + i * 16 + row;
+        pw[i] = wq + (long long)(n < O ? n : O - 1) * K + kq;
+    }
+#pragma unroll
+    for (int i = 0; i < FT; ++i) {
+        const int m = i * 16 + row;
+        pq[i] = q + (long long)(m < T ? m : T - 1) * K + kq;
+    }
+    i32x4 acc[2][FT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // the next 128 bytes of k load while these are multiplied
+    i32x4 a[2][2], b[2][FT];
+    auto fetch = [&](int k) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) a[s][i] = *(const i32x4 *)(pw[i] + k + s * 64);
+#pragma unroll
+            for (int j = 0; j < FT; ++j) b[s][j] = *(const i32x4 *)(pq[j] + k + s * 64);
+        }
+    };
+    if (wave * 128 < K) fetch(wave * 128);
+    for (int k = wave * 128; k < K; k += 8 * 128) {
+        i32x4 a0[2][2], b0[2][FT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) a0[s][i] = a[s][i];
+#pragma unroll
+            for (int j = 0; j < FT; ++j) b0[s][j] = b[s][j];
+        }
+        if (k + 8 * 128 < K) fetch(k + 8 * 128);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0[s][i], b0[s][j], acc[i][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[wave][i * 16 + (lane >> 4) * 4 + e][j * 16 + row] = acc[i][j][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * FT * 16; i += 512) {
+        // token-major: consecutive lanes on consecutive channels
+        const int n = channel_major ? i / (FT * 16) : i & 31, m = channel_major ? i % (FT * 16) : i >> 5;
+        if (n0 + n >= O || m >= T) continue;
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += red[w][n][m];
+        float v = (float)sum * qs[m] * ws[n0 + n];
+        if (bias) v += bias[n0 + n];
+        const int b = m / L;
+        const long long at = channel_major ? ((long long)b * O + n0 + n) * L + (m - b * L) : (long long)m * O + n0 + n;
+        ((typename Elem<OD>::T *)y)[at] = Elem<OD>::put(v);
+    }
+}
+
+template <int OD, int FT>
+void few(int T, int O, int K, int L, const signed char *q, const float *qs, const signed char *wq, const float *ws,
+         const float *bias, int channel_major, void *y, hipStream_t st) {
+    hipLaunchKernelGGL((i8_few_kernel<OD, FT>), dim3((unsigned)((O + 31) / 32)), dim3(512), 0, st, q, wq, qs, ws, bias,
+                       T, O, K, L, channel_major, y);
+}
+
+template <int OD, int WC, int WR, int FC, int FR>
+int tiled(I8Args a, int splits, hipStream_t st) {
+    typedef Tile<WC, WR, FC, FR> X;
+    a.tiles_c = (a.NC + X::C - 1) / X::C;
+    a.tiles_r = (a.NR + X::R - 1) / X::R;
+    if (splits == 1) a.part = nullptr;
+    a.k_split = ((a.K / 128 + splits - 1) / splits) * 128;
+    hipLaunchKernelGGL((i8_tile_kernel<OD, WC, WR, FC, FR>), dim3((unsigned)((long long)a.tiles_c * a.tiles_r * splits)),
+                       dim3(X::kThreads), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    if (splits > 1) {
+        long long blocks = ((long long)a.NR * ((a.NC + 7) / 8) + 255) / 256;
+        hipLaunchKernelGGL(i8_join_kernel<OD>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a,
+                           splits);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    }
+    return MICONV_OK;
+}
+
+constexpr int kFewTokens = 64;
+
+long long tile_count(long long T, long long O, int side) {
+    return ((T + side - 1) / side) * ((O + side - 1) / side);
+}
+
+// Side of the square tile: the largest that gives most of the 256 CUs a tile.
+int tile_side(int T, int O) {
+    if (tile_count(T, O, 256) >= 192) return 256;
+    if (tile_count(T, O, 128) >= 192) return 128;
+    return 64;
 }
 
 }  // namespace
 
-int i8_splits(int, int, int, size_t) { return 1; }
+// Splits of k where even the smallest tiles leave CUs idle, each at least 1024 long.
+int i8_splits(int T, int O, int K, size_t budget) {
+    if (T <= kFewTokens) return 1;
+    const long long tiles = tile_count(T, O, tile_side(T, O));
+    long long s = 256 / tiles;
+    if (s > K / 1024) s = K / 1024;
+    const size_t one = (size_t)T * O * 4;
+    if (s > (long long)(budget / one)) s = (long long)(budget / one);
+    if (s < 2) return 1;
+    const int steps = K / 128, per = (int)((steps + s - 1) / s);
+    return (steps + per - 1) / per;            // no empty split
+}
+
+template <int OD>
+static int i8_by_size(const I8Args &a, int T, int O, int splits, hipStream_t st) {
+    switch (tile_side(T, O)) {
+        case 256: return tiled<OD, 2, 4, 4, 2>(a, splits, st);
+        case 128: return tiled<OD, 2, 2, 2, 2>(a, splits, st);
+        default: return tiled<OD, 2, 2, 1, 1>(a, splits, st);
+    }
+}
 
 int launch_matmul_i8(int B, int L, int O, int K, const signed char *q, const float *qs, const signed char *wq,
-                     const float *ws, const float *bias, int channel_major, int out_dtype, void *y, int, int *,
-                     hipStream_t st) {
-    I8Out o = {qs, ws, bias, y, B * L, O, L, channel_major};
-    const long long tn = (O + 15) / 16, tiles = tn * ((o.T + 15) / 16);
-    const dim3 grid((unsigned)((tiles + 3) / 4));
-    if (out_dtype)
-        hipLaunchKernelGGL(matmul_i8_kernel<1>, grid, dim3(kThreads), 0, st, q, wq, K, tn, tiles, o);
-    else
-        hipLaunchKernelGGL(matmul_i8_kernel<0>, grid, dim3(kThreads), 0, st, q, wq, K, tn, tiles, o);
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+                     const float *ws, const float *bias, int channel_major, int out_dtype, void *y, int splits,
+                     int *part, hipStream_t st) {
+    const int T = B * L;
+    if (T <= kFewTokens) {
+        const int ft = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
+#define MICONV_FEW(FT)                                                                            \
+    (out_dtype ? few<1, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st)                \
+               : few<0, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st))
+        if (ft == 1)
+            MICONV_FEW(1);
+        else if (ft == 2)
+            MICONV_FEW(2);
+        else
+            MICONV_FEW(4);
+        return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+    }
+    I8Args a = {};
+    a.K = K;
+    a.y = y;
+    a.part = part;
+    if (channel_major) {
+        a.c = q; a.c_scale = qs; a.NC = T; a.c_first = 1;
+        a.r = wq; a.r_scale = ws; a.NR = O; a.r_bias = bias;
+        a.row = T;
+        a.len = B > 1 ? L : 0;
+        a.fd_len = make_fdiv((uint32_t)L);
+    } else {
+        a.c = wq; a.c_scale = ws; a.NC = O; a.c_bias = bias;
+        a.r = q; a.r_scale = qs; a.NR = T;
+        a.row = O;
+    }
+    return out_dtype ? i8_by_size<1>(a, T, O, splits, st) : i8_by_size<0>(a, T, O, splits, st);
 }
 
 }  // namespace miconv
