@@ -75,7 +75,7 @@ DEVI void columns(const I8Args &a, int c, float (&cs)[8], float (&cb)[8]) {
 // The sums of eight columns of row r, stored as they are (split) or finished.
 template <int OD>
 DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8], const float (&cs)[8],
-                  const float (&cb)[8]) {
+                  const float (&cb)[8], float rs, float rb) {
     if (a.part && split >= 0) {
         int *dst = a.part + ((long long)split * a.NR + r) * a.NC + c;
 #pragma unroll
@@ -83,7 +83,6 @@ DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8],
             if (c + e < a.NC) dst[e] = sum[e];
         return;
     }
-    const float rs = a.r_scale[r], rb = a.r_bias ? a.r_bias[r] : 0.0f;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = scaled(a, sum[e], cs[e], rs) + (cb[e] + rb);
@@ -184,9 +183,22 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
     const int first = split * a.k_split, end = first + a.k_split < a.K ? first + a.k_split : a.K;
     X::load(src, stages, first);
+    // what the epilogue needs from memory: a lane's columns' and one row's scale and bias
+    constexpr int kW = FC * 32, kMine = 32 * kW;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wc = wave % WC, wr = wave / WC;
+    constexpr int kLanes = kW / 8;             // lanes per row, eight columns each
+    const int col = (lane % kLanes) * 8, c = c0 + wc * kW + col;
+    float cs[8], cb[8];
+    columns(a, c, cs, cb);
+    static_assert(FR <= 2, "one row's scale per lane");
+    const int rl = r0 + wr * FR * 32 + lane, rc = rl < a.NR ? rl : a.NR - 1;
+    const float rs = a.r_scale[rc], rb = a.r_bias ? a.r_bias[rc] : 0.0f;
     int now = 0;
     for (int k = first; k < end; k += 128) {
-        __syncthreads();                       // this stage has arrived, the other has been read
+        // this stage has arrived (each wave waits for its own loads; the compiler does not
+        // always tie an LDS load to the reads behind the barrier), the other has been read
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
         if (k + 128 < end) X::load(src, stages + (X::kBytes - now), k + 128);
         X::multiply(stages + now, acc);
         now = X::kBytes - now;
@@ -194,14 +206,8 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
     __syncthreads();
     // Through LDS, 32 rows of the wave's FC*32 columns at a time, so that y is written
     // in 16-byte pieces of consecutive lanes; a row's pieces are permuted as above.
-    constexpr int kW = FC * 32, kMine = 32 * kW;
     static_assert(X::kWaves * kMine * 4 <= 2 * X::kBytes, "the exchange fits the two stages");
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wc = wave % WC, wr = wave / WC;
     int *mine = (int *)stages + wave * kMine;
-    constexpr int kLanes = kW / 8;             // lanes per row, eight columns each
-    const int col = (lane % kLanes) * 8, c = c0 + wc * kW + col;
-    float cs[8], cb[8];
-    columns(a, c, cs, cb);
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
         const int rw = r0 + (wr * FR + j) * 32;
@@ -216,9 +222,10 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
                 *(i32x4 *)(mine + row * kW + piece * 4) = four;
             }
         wave_lds_sync();
-#pragma unroll 1
+#pragma unroll 2
         for (int p = 0; p < 32 * kLanes / 64; ++p) {
             const int row = p * (64 / kLanes) + lane / kLanes, r = rw + row;
+            const float rsr = __shfl(rs, j * 32 + row), rbr = __shfl(rb, j * 32 + row);
             if (r >= a.NR || c >= a.NC) continue;
             const i32x4 lo = *(const i32x4 *)(mine + row * kW + ((col >> 2) ^ (row & 7)) * 4);
             const i32x4 hi = *(const i32x4 *)(mine + row * kW + (((col >> 2) + 1) ^ (row & 7)) * 4);
@@ -228,7 +235,7 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
                 sum[e] = lo[e];
                 sum[4 + e] = hi[e];
             }
-            finish8<OD>(a, split, r, c, sum, cs, cb);
+            finish8<OD>(a, split, r, c, sum, cs, cb, rsr, rbr);
         }
         wave_lds_sync();
     }
@@ -250,7 +257,7 @@ __global__ __launch_bounds__(256) void i8_join_kernel(I8Args a, int splits) {
         }
         float cs[8], cb[8];
         columns(a, c, cs, cb);
-        finish8<OD>(a, -1, r, c, sum, cs, cb);
+        finish8<OD>(a, -1, r, c, sum, cs, cb, a.r_scale[r], a.r_bias ? a.r_bias[r] : 0.0f);
     }
 }
 
