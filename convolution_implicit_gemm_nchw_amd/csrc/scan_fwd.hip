@@ -2,11 +2,18 @@
 //
 //   h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t x_t B_t[n],  v_t = sum_n C_t[n] h_t[n] + D x_t
 //
-// The map h -> a h + b composes: (a1, b1) then (a2, b2) is (a1 a2, a2 b1 + b2).  A
-// wave takes one row (sequence, channel) and 64 lanes x 8 time steps of it at a
-// time: each lane runs its eight steps from a zero state, the lanes' maps are
-// combined by a prefix scan over the wave, and each lane runs its steps again
-// from its true entry state.
+// The map h -> a h + b composes: (a1, b1) then (a2, b2) is (a1 a2, a2 b1 + b2).  A row
+// (sequence, channel) is taken by LANES lanes x ITEMS time steps at a time: each lane
+// runs its steps from a zero state, the lanes' maps are combined by a prefix scan, and
+// each lane runs its steps again from its true entry state.
+//
+// Bound by the vector ALUs, not by memory: a (step, state) pair costs seven slots of
+// four cycles -- argument, exponential (two), input, and a multiply-add each for the two
+// runs and for C h -- against 8 bytes per step for N = 16 pairs of them (bf16).  So
+//   - the lane crossings are DPP moves, and the decay over a range of lanes is the
+//     exponential of a sum of dt, which does not depend on n;
+//   - 16 steps per lane where the row is long enough: a scan costs about 36 slots;
+//   - B and C are widened to fp32 once per work-group, in LDS, for its channels.
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
@@ -17,14 +24,62 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <int DT>
-__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(miconv_scan_t s) {
+// Prefix sums of the lanes' dt: within rows of 16, halves of 32 and the whole wave.
+struct Sums {
+    float own, row, half, all;
+};
+
+DEVI Sums prefix_sums(float own) {
+    Sums s;
+    s.own = own;
+    float v = own;
+    v += cross<kRowShr + 1>(v);
+    v += cross<kRowShr + 2>(v);
+    v += cross<kRowShr + 4>(v);
+    v += cross<kRowShr + 8>(v);
+    s.row = v;
+    v += cross<kRowBcast15, 0xa>(v);
+    s.half = v;
+    v += cross<kRowBcast31, 0xc>(v);
+    s.all = v;
+    return s;
+}
+
+// The lanes' maps (product of decays, state from zero) combined along the wave: the
+// state after each lane's steps from a zero state before lane 0.  The product over a
+// range of steps is the exponential of the sum of dt, so only those that the first
+// steps need are multiplied up; a lane without a source reads 0, after which its
+// product no longer matters.
+DEVI float scan_rows(float h, float a2, const Sums &s) {
+    float p = exp2_hw(a2 * s.own);
+    h = __builtin_fmaf(p, cross<kRowShr + 1>(h), h);
+    p *= cross<kRowShr + 1>(p);
+    h = __builtin_fmaf(p, cross<kRowShr + 2>(h), h);
+    p *= cross<kRowShr + 2>(p);
+    h = __builtin_fmaf(p, cross<kRowShr + 4>(h), h);
+    p *= cross<kRowShr + 4>(p);
+    return __builtin_fmaf(p, cross<kRowShr + 8>(h), h);
+}
+
+// Work-groups of 8 waves; 64 lanes x 16 or 8 steps per row, or, for short rows, four rows
+// of 16 lanes x 8 steps per wave (then the row is a single chunk).
+constexpr int kScanWaves = 8;
+
+template <int DT, int LANES, int ITEMS>
+__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g) {
     typedef typename Elem<DT>::T T;
-    __shared__ float carry[kThreads / 64][MICONV_SCAN_MAX_STATES];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const long long row = (long long)blockIdx.x * (kThreads / 64) + wave;
-    if (row >= (long long)s.B * s.D) return;
-    const int b = (int)(row / s.D), d = (int)(row - (long long)b * s.D), g = d / (s.D / s.G);
+    constexpr int kT = LANES * ITEMS, kRows = 64 / LANES, kPairs = kT * 2 * 4;   // bytes of B and C per state
+    constexpr int kStage = 65536 / kPairs < 16 ? 65536 / kPairs : 16;            // states staged at a time
+    // [state][B, C][ITEMS / 4][LANES][4]: a lane reads four steps as 16 bytes next to its neighbours'
+    __shared__ __attribute__((aligned(16))) float bc[kStage * 2 * kT];
+    __shared__ float a_rows[LANES == 16 ? kScanWaves * kRows * MICONV_SCAN_MAX_STATES : 1];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), sub = lane % LANES;
+    const int per_group = s.D / s.G;
+    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g, g = bg % s.G, b = bg / s.G;
+    const int in_group = (blk * kScanWaves + wave) * kRows + lane / LANES;
+    const bool live = in_group < per_group;              // the last work-group's other rows only help to stage
+    const int d = g * per_group + (live ? in_group : 0);
+    const long long row = (long long)b * s.D + d;
     const int len = valid_steps(s.lengths, b, s.L);
     const T *x = (const T *)s.x.data + b * s.x.stride_b + d * s.x.stride_d;
     const T *dl = (const T *)s.delta.data + b * s.delta.stride_b + d * s.delta.stride_d;
@@ -32,67 +87,118 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(miconv_scan_t s) {
     T *y = (T *)s.y.data + b * s.y.stride_b + d * s.y.stride_d;
     const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
     const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
-    const float *A = s.A + (long long)d * s.N;
     const float skip = s.D_skip ? s.D_skip[d] : 0.0f, bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
-    float *carried = carry[wave];
-    const int chunks = (s.L + kScanChunk - 1) / kScanChunk;
-    if (lane < s.N) carried[lane] = s.initial_state ? s.initial_state[row * s.N + lane] : 0.0f;
-    for (int c = 0; c < chunks; ++c) {
+    const int saved = scan_chunks(s.L);
+    // 64 lanes per row: lane n holds the state n between chunks and A[n] log2(e).  16 lanes:
+    // one chunk, so states come from and go to memory; A in LDS.
+    float carried = 0.0f, a_lane = 0.0f, middle = 0.0f;
+    if constexpr (LANES == 64) {
+        if (lane < s.N) {
+            if (s.initial_state) carried = s.initial_state[row * s.N + lane];
+            a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
+        }
+    } else {
+        for (int n = sub; n < s.N; n += LANES) {
+            const float h0 = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
+            if (live && s.states) s.states[row * s.N + n] = h0;
+            a_rows[(wave * kRows + lane / LANES) * MICONV_SCAN_MAX_STATES + n] = s.A[(long long)d * s.N + n] * kLog2e;
+        }
         wave_lds_sync();
-        if (s.states && lane < s.N) s.states[(row * chunks + c) * s.N + lane] = carried[lane];
-        const int t = c * kScanChunk + lane * 8;
-        float xv[8], dt[8], v[8], sum = 0.0f;
-        load8<DT>(x, t, len, xv);
-        load8<DT>(dl, t, len, dt);
+    }
+    for (int t0 = 0; t0 < s.L; t0 += kT) {
+        const int c = t0 / kScanChunk, t = t0 + sub * ITEMS;
+        if (LANES == 64 && s.states && live && lane < s.N) s.states[(row * saved + c) * s.N + lane] = carried;
+        float xv[ITEMS], dt[ITEMS], v[ITEMS], sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int q = 0; q < ITEMS; q += 8) {
+            load8<DT>(x, t + q, len, *(float (*)[8])(xv + q));
+            load8<DT>(dl, t + q, len, *(float (*)[8])(dt + q));
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
             const float raw = dt[i] + bias;
             dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;   // no decay past the end
             sum += dt[i];
             v[i] = skip * xv[i];
             xv[i] *= dt[i];
         }
-        for (int n = 0; n < s.N; ++n) {
-            const float a2 = A[n] * kLog2e;
-            float bv[8], cv[8], a[8], h = 0.0f;
-            load8<DT>(Bm + n * s.Bm.stride_n, t, len, bv);
-            load8<DT>(Cm + n * s.Cm.stride_n, t, len, cv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] = exp2_hw(dt[i] * a2);
-                bv[i] *= xv[i];
-                h = __builtin_fmaf(a[i], h, bv[i]);
+        const Sums sums = prefix_sums(sum);
+        for (int n0 = 0; n0 < s.N; n0 += kStage) {
+            const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
+            __syncthreads();
+            for (int i = threadIdx.x; i < nn * 2 * (kT / 8); i += 64 * kScanWaves) {
+                const int at = i % (kT / 8) * 8, which = i / (kT / 8), n = n0 + (which >> 1);
+                float w[8];
+                load8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, t0 + at, len, w);
+                float *to = bc + which * kT + (at % ITEMS / 4) * LANES * 4 + at / ITEMS * 4;
+                *(f32x4 *)to = f32x4{w[0], w[1], w[2], w[3]};
+                *(f32x4 *)(to + LANES * 4) = f32x4{w[4], w[5], w[6], w[7]};
             }
-            float p = exp2_hw(sum * a2);
+            __syncthreads();
+            for (int k = 0; k < nn; ++k) {
+                const int n = n0 + k;
+                float a2, h0;
+                if constexpr (LANES == 64) {
+                    a2 = lane_of(a_lane, n);
+                    h0 = lane_of(carried, n);
+                } else {
+                    a2 = a_rows[(wave * kRows + lane / LANES) * MICONV_SCAN_MAX_STATES + n];
+                    h0 = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
+                }
+                const float *pb = bc + k * 2 * kT + sub * 4, *pc = pb + kT;
+                float a[ITEMS], bv[ITEMS], h = 0.0f;
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const float hp = __shfl_up(h, m), pp = __shfl_up(p, m);
-                if (lane >= m) {
-                    h = __builtin_fmaf(p, hp, h);
-                    p *= pp;
+                for (int i = 0; i < ITEMS; i += 4) {
+                    const f32x4 q = *(const f32x4 *)(pb + i * LANES);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        a[i + e] = exp2_hw(dt[i + e] * a2);
+                        bv[i + e] = q[e] * xv[i + e];
+                        h = __builtin_fmaf(a[i + e], h, bv[i + e]);
+                    }
+                }
+                h = scan_rows(h, a2, sums);
+                if constexpr (LANES == 64) {
+                    h = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(h), h);
+                    h = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(h), h);
+                    const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), h0, h);
+                    carried = lane == n ? lane_of(end, 63) : carried;
+                    if (kT > kScanChunk) middle = lane == n ? lane_of(end, 31) : middle;
+                    h = cross_or<kWaveShr1>(h0, end);
+                } else {
+                    const float end = __builtin_fmaf(exp2_hw(a2 * sums.row), h0, h);
+                    if (live && s.final_state && sub == LANES - 1) s.final_state[row * s.N + n] = end;
+                    h = cross_or<kRowShr + 1>(h0, end);
+                }
+#pragma unroll
+                for (int i = 0; i < ITEMS; i += 4) {
+                    const f32x4 q = *(const f32x4 *)(pc + i * LANES);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h = __builtin_fmaf(a[i + e], h, bv[i + e]);
+                        v[i + e] = __builtin_fmaf(q[e], h, v[i + e]);
+                    }
                 }
             }
-            const float h0 = carried[n];
-            const float end = __builtin_fmaf(p, h0, h);
-            h = __shfl_up(end, 1);
-            if (lane == 0) h = h0;
-            if (lane == 63) carried[n] = end;
+        }
+        if (kT > kScanChunk && s.states && live && lane < s.N && c + 1 < saved)
+            s.states[(row * saved + c + 1) * s.N + lane] = middle;
+        if (live) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h = __builtin_fmaf(a[i], h, bv[i]);
-                v[i] = __builtin_fmaf(cv[i], h, v[i]);
+            for (int q = 0; q < ITEMS; q += 8) {
+                float (&out)[8] = *(float (*)[8])(v + q);
+                if (t + q >= s.L) break;
+                if (z) {
+                    float zv[8];
+                    load8<DT>(z, t + q, len, zv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) out[i] *= zv[i] * logistic(zv[i]);
+                }
+                store8<DT>(y, t + q, s.L, out);
             }
         }
-        if (z) {
-            float zv[8];
-            load8<DT>(z, t, len, zv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= zv[i] * logistic(zv[i]);
-        }
-        if (t < s.L) store8<DT>(y, t, s.L, v);
     }
-    wave_lds_sync();
-    if (s.final_state && lane < s.N) s.final_state[row * s.N + lane] = carried[lane];
+    if (LANES == 64 && s.final_state && live && lane < s.N) s.final_state[row * s.N + lane] = carried;
 }
 
 // One thread per (sequence, channel); its N states are contiguous.
@@ -132,14 +238,18 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
 
 }  // namespace
 
-int launch_scan_fwd(const miconv_scan_t &s, int dtype, hipStream_t st) {
-    const long long rows = (long long)s.B * s.D, per = kThreads / 64;
-    const dim3 grid((unsigned)((rows + per - 1) / per));
-    if (dtype)
-        hipLaunchKernelGGL(scan_fwd_kernel<1>, grid, dim3(kThreads), 0, st, s);
-    else
-        hipLaunchKernelGGL(scan_fwd_kernel<0>, grid, dim3(kThreads), 0, st, s);
+template <int DT, int LANES, int ITEMS>
+static int scan_fwd(const miconv_scan_t &s, hipStream_t st) {
+    const int rows = kScanWaves * (64 / LANES), blocks_g = (s.D / s.G + rows - 1) / rows;
+    const dim3 grid((unsigned)((long long)s.B * s.G * blocks_g));
+    hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS>), grid, dim3(64 * kScanWaves), 0, st, s, blocks_g);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+}
+
+int launch_scan_fwd(const miconv_scan_t &s, int dtype, hipStream_t st) {
+    if (s.L <= 128) return dtype ? scan_fwd<1, 16, 8>(s, st) : scan_fwd<0, 16, 8>(s, st);
+    if (s.L <= 512) return dtype ? scan_fwd<1, 64, 8>(s, st) : scan_fwd<0, 64, 8>(s, st);
+    return dtype ? scan_fwd<1, 64, 16>(s, st) : scan_fwd<0, 64, 16>(s, st);
 }
 
 int launch_scan_step(const miconv_scan_t &s, int dtype, const float *state, int slots, const int *slot_of,

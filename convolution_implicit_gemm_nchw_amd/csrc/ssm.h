@@ -11,7 +11,7 @@ namespace miconv {
 // Time steps between two saved scan states.
 constexpr int kScanChunk = 512;
 
-inline int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
+constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
 // Channels one work-group of the scan's backward pass sums dB and dC over, and
 // the resulting number of partial sums per group of channels.

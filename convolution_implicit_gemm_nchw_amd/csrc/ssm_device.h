@@ -118,6 +118,25 @@ DEVI float softplus(float v) {
     return (v > 0.0f ? v : 0.0f) + s * p;
 }
 
+// Lane crossings of a wave of 64 in four rows of 16.
+constexpr int kRowShr = 0x110;      // + n: lane i reads lane i - n of its row
+constexpr int kRowShl = 0x100;      // + n: lane i reads lane i + n of its row
+constexpr int kWaveShl1 = 0x130, kWaveShr1 = 0x138;
+constexpr int kRowBcast15 = 0x142;  // rows 1..3 read the last lane of the row before
+constexpr int kRowBcast31 = 0x143;  // rows 2, 3 read lane 31
+
+// The crossing's source lane, or 0 where there is none.
+template <int CTRL, int ROWS = 0xf>
+DEVI float cross(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, ROWS == 0xf));
+}
+// The crossing's source lane, or `other` where there is none.
+template <int CTRL>
+DEVI float cross_or(float other, float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(other), __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+DEVI float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
+
 // Orders this wave's LDS accesses: what a lane wrote before is read by the others after.
 DEVI void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
