@@ -9,14 +9,22 @@
 //   dA[n] = sum_{b,t} dt_t g_t[n] a_t h_{t-1}[n]
 // h is rebuilt chunk by chunk from the states that the forward pass saved; G runs
 // through the chunks from the last to the first.  Both are scans of first-order
-// maps, over the lanes of a wave as in the forward pass.
+// maps, as in the forward pass.
 //
-// A work-group takes R channels of one sequence and group, a wave NS = 4 of the N
-// states for all of them, so that the sums over channels of dB and dC are kept in
-// its registers; the sums over states (d(dt), g B, v) meet in LDS.  The R-channel
-// sums go to the workspace and are added in order by a second kernel.  More than
-// 32 states are taken 32 at a time (a wave's sums would not fit its registers);
-// the sums over states of the earlier launches wait in the workspace.
+// Bound by the vector ALUs: a (step, state) pair costs 18 slots of four cycles and its
+// share of the two scans.  The split keeps everything else off that path:
+//   - a row of 16 lanes takes one channel, eight steps a lane, so the scans stay inside
+//     DPP rows (half the cost of a scan over the wave) and a wave holds four channels;
+//   - a work-group takes 16 channels (four such groups) of one sequence; its four waves
+//     have NS states each, for all 16 channels, so that the sums over channels of dB and
+//     dC are kept in registers and leave them once per chunk;
+//   - what belongs to a step (softplus, gate, their derivatives) is computed once, by
+//     the wave that owns the group, and shared through LDS;
+//   - the sums over states meet in LDS: in turn i wave w works on group (i + w) mod 4, so
+//     every group has one wave at a time adding to it, in a fixed order.
+// The 16-channel sums of dB and dC go to the workspace and are added in order by a
+// second kernel.  More than 16 states are taken 16 per launch; the sums over the states
+// of the earlier launches wait in the workspace.
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
@@ -25,242 +33,347 @@ namespace miconv {
 
 namespace {
 
-constexpr int NS = 4, kStates = 32;
-
-// Sum over the wave, in every lane.
-DEVI float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    return v;
-}
+constexpr int kStates = 16, kT = kScanChunk, kCh = kScanBwdChannels;
+static_assert(kT == 128 && kCh == 16, "16 lanes x 8 steps, 4 waves x 4 rows");
 
 struct BwdOut {
     float *dB, *dC;           // [parts][B][G][N][L]
     float *dA, *dD, *db;      // [B][D][N], [B][D], [B][D]
     float *sums;              // [3][B][D][L] sums over the states of earlier launches, or null
-    int R, parts;
+    int parts;
     int n_first, n_end, last; // states of this launch; whether it is the last one
 };
 
-template <int DT, int TH>
-__global__ __launch_bounds__(TH) void scan_bwd_kernel(miconv_scan_t s, BwdOut o) {
-    typedef typename Elem<DT>::T T;
-    extern __shared__ float lds[];
-    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int per_group = s.D / s.G;
-    const int part = blockIdx.x % o.parts, g = (blockIdx.x / o.parts) % s.G, b = blockIdx.x / (o.parts * s.G);
-    const int d0 = g * per_group + part * o.R;
-    const int R = per_group - part * o.R < o.R ? per_group - part * o.R : o.R;
-    const int n0 = o.n_first + wave * NS;
-    float *sums = lds;                                    // [waves][3][kScanChunk]
-    // [R][N] G of the step after the chunk; only this launch's states are used
-    float *carry = lds + waves * 3 * kScanChunk;
-    float *dA = carry + o.R * s.N;                        // [R][N]
-    float *dD = dA + o.R * s.N, *db = dD + o.R;           // [R]
-    const int len = valid_steps(s.lengths, b, s.L);
-    const int chunks = (s.L + kScanChunk - 1) / kScanChunk;
-    for (int i = threadIdx.x; i < R * s.N; i += blockDim.x) {
-        const long long at = ((long long)b * s.D + d0) * s.N + i;
-        carry[i] = s.d_final_state ? s.d_final_state[at] : 0.0f;
-        dA[i] = 0.0f;
-    }
-    for (int i = threadIdx.x; i < R; i += blockDim.x) dD[i] = db[i] = 0.0f;
-    __syncthreads();
-    const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
-    const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
-    for (int c = chunks - 1; c >= 0; --c) {
-        const int t = c * kScanChunk + lane * 8;
-        float dBv[NS][8], dCv[NS][8];
+// Per-step values of the 16 channels: [group][half][64 lanes][4 steps].
+struct Steps {
+    float v[4][2][64][4];
+};
+
+DEVI void put_steps(Steps &s, int group, int lane, const float (&v)[8]) {
+    *(f32x4 *)s.v[group][0][lane] = f32x4{v[0], v[1], v[2], v[3]};
+    *(f32x4 *)s.v[group][1][lane] = f32x4{v[4], v[5], v[6], v[7]};
+}
+DEVI void get_steps(const Steps &s, int group, int lane, float (&v)[8]) {
+    const f32x4 lo = *(const f32x4 *)s.v[group][0][lane], hi = *(const f32x4 *)s.v[group][1][lane];
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dBv[j][i] = dCv[j][i] = 0.0f;
-        for (int r = 0; r < R; ++r) {
-            const int d = d0 + r;
-            const long long row = (long long)b * s.D + d;
-            const T *x = (const T *)s.x.data + b * s.x.stride_b + d * s.x.stride_d;
-            const T *dl = (const T *)s.delta.data + b * s.delta.stride_b + d * s.delta.stride_d;
-            const T *dy = (const T *)s.dy.data + b * s.dy.stride_b + d * s.dy.stride_d;
-            const T *z = s.z.data ? (const T *)s.z.data + b * s.z.stride_b + d * s.z.stride_d : nullptr;
-            const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
-            float xv[8], dt[8], e[8], total = 0.0f, ddt[8], gB[8], v[8];
-            load8<DT>(x, t, len, xv);
-            load8<DT>(dl, t, len, dt);
-            load8<DT>(dy, t, len, e);
-            if (z) {
-                float zv[8];
-                load8<DT>(z, t, len, zv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] *= zv[i] * logistic(zv[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float raw = dt[i] + bias;
-                dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;
-                total += dt[i];
-                xv[i] *= dt[i];
-                ddt[i] = gB[i] = v[i] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const int n = n0 + j;
-                if (n >= o.n_end) break;
-                const float A = s.A[(long long)d * s.N + n], a2 = A * kLog2e;
-                float bv[8], cv[8], a[8], h = 0.0f, G = 0.0f;
-                load8<DT>(Bm + n * s.Bm.stride_n, t, len, bv);
-                load8<DT>(Cm + n * s.Cm.stride_n, t, len, cv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] = exp2_hw(dt[i] * a2);
-                    h = __builtin_fmaf(a[i], h, xv[i] * bv[i]);
-                }
-#pragma unroll
-                for (int i = 7; i >= 0; --i) G = a[i] * __builtin_fmaf(cv[i], e[i], G);
-                float p = exp2_hw(total * a2), q = p;
-#pragma unroll
-                for (int m = 1; m < 64; m <<= 1) {
-                    const float hp = __shfl_up(h, m), pp = __shfl_up(p, m);
-                    const float Gq = __shfl_down(G, m), qq = __shfl_down(q, m);
-                    if (lane >= m) {
-                        h = __builtin_fmaf(p, hp, h);
-                        p *= pp;
-                    }
-                    if (lane + m < 64) {
-                        G = __builtin_fmaf(q, Gq, G);
-                        q *= qq;
-                    }
-                }
-                const float h0 = s.states[(row * chunks + c) * s.N + n], G0 = carry[r * s.N + n];
-                h = __shfl_up(__builtin_fmaf(p, h0, h), 1);
-                if (lane == 0) h = h0;
-                const float Gend = __builtin_fmaf(q, G0, G);
-                G = __shfl_down(Gend, 1);
-                if (lane == 63) G = G0;
-                if (lane == 0) carry[r * s.N + n] = Gend;
-                float hh[8], ah[8], sA = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ah[i] = a[i] * h;
-                    h = __builtin_fmaf(xv[i], bv[i], ah[i]);
-                    hh[i] = h;
-                }
-#pragma unroll
-                for (int i = 7; i >= 0; --i) {
-                    const float gt = __builtin_fmaf(cv[i], e[i], G);
-                    G = a[i] * gt;
-                    const float w = gt * ah[i];
-                    ddt[i] = __builtin_fmaf(A, w, ddt[i]);
-                    sA = __builtin_fmaf(dt[i], w, sA);
-                    gB[i] = __builtin_fmaf(gt, bv[i], gB[i]);
-                    v[i] = __builtin_fmaf(cv[i], hh[i], v[i]);
-                    dBv[j][i] = __builtin_fmaf(gt, xv[i], dBv[j][i]);
-                    dCv[j][i] = __builtin_fmaf(e[i], hh[i], dCv[j][i]);
-                }
-                sA = wave_sum(sA);
-                if (lane == 0) dA[r * s.N + n] += sA;
-                // one state's loads at a time: the unrolled states' together do not fit the registers
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            float *mine = sums + wave * 3 * kScanChunk + lane * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                mine[i] = ddt[i];
-                mine[kScanChunk + i] = gB[i];
-                mine[2 * kScanChunk + i] = v[i];
-            }
-            __syncthreads();
-            const float skip = s.D_skip ? s.D_skip[d] : 0.0f;
-            float sD = 0.0f, sb = 0.0f;
-            T *dx = (T *)s.dx.data + b * s.dx.stride_b + d * s.dx.stride_d;
-            T *dd = (T *)s.ddelta.data + b * s.ddelta.stride_b + d * s.ddelta.stride_d;
-            T *dz = s.dz.data ? (T *)s.dz.data + b * s.dz.stride_b + d * s.dz.stride_d : nullptr;
-            for (int i = threadIdx.x; i < kScanChunk; i += blockDim.x) {
-                const int tt = c * kScanChunk + i;
-                if (tt >= s.L) break;
-                if (tt >= len) {
-                    dx[tt] = dd[tt] = Elem<DT>::put(0.0f);
-                    if (dz) dz[tt] = Elem<DT>::put(0.0f);
-                    continue;
-                }
-                float sdt = 0.0f, sgB = 0.0f, sv = 0.0f;
-                for (int w = 0; w < waves; ++w) {
-                    sdt += sums[w * 3 * kScanChunk + i];
-                    sgB += sums[w * 3 * kScanChunk + kScanChunk + i];
-                    sv += sums[w * 3 * kScanChunk + 2 * kScanChunk + i];
-                }
-                if (o.sums) {
-                    float *past = o.sums + row * s.L + tt;
-                    const long long one = (long long)s.B * s.D * s.L;
-                    if (o.n_first) {
-                        sdt += past[0];
-                        sgB += past[one];
-                        sv += past[2 * one];
-                    }
-                    if (!o.last) {
-                        past[0] = sdt;
-                        past[one] = sgB;
-                        past[2 * one] = sv;
-                        continue;
-                    }
-                }
-                const float xt = Elem<DT>::get(x[tt]), dyt = Elem<DT>::get(dy[tt]);
-                const float raw = Elem<DT>::get(dl[tt]) + bias;
-                float et = dyt;
-                if (z) {
-                    const float zt = Elem<DT>::get(z[tt]), sg = logistic(zt);
-                    et *= zt * sg;
-                    if (dz) dz[tt] = Elem<DT>::put(dyt * __builtin_fmaf(skip, xt, sv) * (sg * __builtin_fmaf(zt, 1.0f - sg, 1.0f)));
-                }
-                dx[tt] = Elem<DT>::put(__builtin_fmaf(s.softplus ? softplus(raw) : raw, sgB, skip * et));
-                sdt = __builtin_fmaf(xt, sgB, sdt);
-                if (s.softplus) sdt *= logistic(raw);
-                dd[tt] = Elem<DT>::put(sdt);
-                sD = __builtin_fmaf(et, xt, sD);
-                sb += sdt;
-            }
-            // the waves' parts of dD and dbias, in order
-            sD = wave_sum(sD);
-            sb = wave_sum(sb);
-            __syncthreads();
-            if (lane == 0) {
-                sums[2 * wave] = sD;
-                sums[2 * wave + 1] = sb;
-            }
-            __syncthreads();
-            if (threadIdx.x == 0)
-                for (int w = 0; w < waves; ++w) {
-                    dD[r] += sums[2 * w];
-                    db[r] += sums[2 * w + 1];
-                }
-            __syncthreads();
-        }
-        if (t < s.L) {
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const int n = n0 + j;
-                if (n >= o.n_end) break;
-                const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + n) * s.L;
-                store8<0>(o.dB + at, t, s.L, dBv[j]);
-                store8<0>(o.dC + at, t, s.L, dCv[j]);
-            }
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < R * s.N; i += blockDim.x) {
-        const int n = i % s.N;
-        if (n < o.n_first || n >= o.n_end) continue;
-        const long long at = ((long long)b * s.D + d0) * s.N + i;
-        o.dA[at] = dA[i];
-        if (s.d_initial_state) s.d_initial_state[at] = carry[i];
-    }
-    if (!o.last) return;
-    for (int i = threadIdx.x; i < R; i += blockDim.x) {
-        o.dD[(long long)b * s.D + d0 + i] = dD[i];
-        o.db[(long long)b * s.D + d0 + i] = db[i];
+    for (int i = 0; i < 4; ++i) {
+        v[i] = lo[i];
+        v[4 + i] = hi[i];
     }
 }
 
-// out[i] = sum over p of part[p][i], p in order, for up to three arrays.
+struct Lds {
+    Steps dt, dtx, e;                       // shared by the waves
+    Steps sdt, sgB, sv;                     // sums over states: A g a h, g B, C h
+    Steps zslope;                           // dy silu'(z)
+    float bc[kStates][2][2][16][4];         // B and C of the chunk: [state][B, C][half][lane of a row][4]
+    float a2[kCh][kStates];                 // A log2(e)
+    float carry[kCh][kStates];              // G of the step after the chunk
+    float dA[4][4][4][16];                  // [wave][turn][state][4 lanes of each row]
+};
+
+// Sums over the four rows of the wave: of u in rows 0, 1 and of v in rows 2, 3 (rows of a
+// pair hold what the next step adds).
+DEVI float join_halves(float u, float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(u), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+DEVI float join_rows(float u, float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(u), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+DEVI float row_sum(float v) {          // in the last lane of each row
+    v += cross<kRowShr + 1>(v);
+    v += cross<kRowShr + 2>(v);
+    v += cross<kRowShr + 4>(v);
+    return v + cross<kRowShr + 8>(v);
+}
+
+template <typename P>
+DEVI P *at_row(const miconv_rows_t &r, int b, int d) {
+    return (P *)r.data + b * r.stride_b + d * r.stride_d;
+}
+
+// v, of which the compiler does not know that it is: addresses made from it are made where
+// they are used rather than held in registers through the turns.
+DEVI int again(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+template <int DT, int NS>
+__global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOut o) {
+    typedef typename Elem<DT>::T T;
+    __shared__ __attribute__((aligned(16))) Lds m;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane >> 4, sub = lane & 15;
+    const int per_group = s.D / s.G;
+    const int part = blockIdx.x % o.parts, g = (blockIdx.x / o.parts) % s.G, b = blockIdx.x / (o.parts * s.G);
+    const int first = g * per_group + part * kCh;                        // the work-group's first channel
+    const int channels = per_group - part * kCh < kCh ? per_group - part * kCh : kCh;
+    const int nn = o.n_end - o.n_first, j0 = wave * NS;                  // states of the launch, of the wave
+    const int len = valid_steps(s.lengths, b, s.L);
+    const int chunks = (s.L + kT - 1) / kT;
+    // the channel that this lane owns between the turns
+    const int own = wave * 4 + row;
+    const bool live = own < channels;
+    const int d = first + (live ? own : 0);
+    const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
+    const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
+    const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f, skip = s.D_skip ? s.D_skip[d] : 0.0f;
+    for (int i = threadIdx.x; i < kCh * kStates; i += 256) {
+        const int c = i / kStates, j = i % kStates;
+        const bool used = c < channels && j < nn;
+        const long long at = ((long long)b * s.D + first + c) * s.N + o.n_first + j;
+        m.a2[c][j] = used ? s.A[(long long)(first + c) * s.N + o.n_first + j] * kLog2e : 0.0f;
+        m.carry[c][j] = used && s.d_final_state ? s.d_final_state[at] : 0.0f;
+    }
+    for (int i = threadIdx.x; i < 4 * 4 * 4 * 16; i += 256) (&m.dA[0][0][0][0])[i] = 0.0f;
+    float sD = 0.0f, sb = 0.0f;
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int t0 = c * kT, t = t0 + sub * 8;
+        float dB[NS][8], dC[NS][8];
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dB[j][i] = dC[j][i] = 0.0f;
+        if (t0 < len) {
+            // B and C of the chunk, and what belongs to the steps of the wave's own group
+            for (int i = threadIdx.x; i < nn * 32; i += 256) {
+                const int l = i & 15, which = i >> 4, n = o.n_first + (which >> 1);
+                float w[8];
+                load8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, t0 + l * 8, len, w);
+                *(f32x4 *)m.bc[which >> 1][which & 1][0][l] = f32x4{w[0], w[1], w[2], w[3]};
+                *(f32x4 *)m.bc[which >> 1][which & 1][1][l] = f32x4{w[4], w[5], w[6], w[7]};
+            }
+            {
+                float dt[8], e[8], dtx[8];
+                const int end = live ? len : 0, dv = again(d);
+                load8<DT>(at_row<const T>(s.x, b, dv), t, end, dtx);
+                load8<DT>(at_row<const T>(s.delta, b, dv), t, end, dt);
+                load8<DT>(at_row<const T>(s.dy, b, dv), t, end, e);
+                if (s.z.data) {
+                    float zv[8], zslope[8];
+                    load8<DT>(at_row<const T>(s.z, b, dv), t, end, zv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float sg = logistic(zv[i]);
+                        zslope[i] = e[i] * (sg * __builtin_fmaf(zv[i], 1.0f - sg, 1.0f));
+                        e[i] *= zv[i] * sg;
+                    }
+                    put_steps(m.zslope, wave, lane, zslope);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float raw = dt[i] + bias;
+                    dt[i] = t + i < end ? (s.softplus ? softplus(raw) : raw) : 0.0f;   // no decay past the end
+                    dtx[i] *= dt[i];
+                }
+                put_steps(m.dt, wave, lane, dt);
+                put_steps(m.dtx, wave, lane, dtx);
+                put_steps(m.e, wave, lane, e);
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int turn = 0; turn < 4; ++turn) {
+                const int group = (turn + wave) & 3, ch = group * 4 + row;
+                if (j0 < nn || turn == 0) {          // a wave without states adds zeros, as the first
+                    float dt[8], dtx[8], e[8], sdt[8], sgB[8], sv[8];
+                    get_steps(m.dt, group, lane, dt);
+                    get_steps(m.dtx, group, lane, dtx);
+                    get_steps(m.e, group, lane, e);
+                    if (turn == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sdt[i] = sgB[i] = sv[i] = 0.0f;
+                    } else {
+                        get_steps(m.sdt, group, lane, sdt);
+                        get_steps(m.sgB, group, lane, sgB);
+                        get_steps(m.sv, group, lane, sv);
+                    }
+                    float all = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) all += dt[i];
+                    float before = all, after = all;                      // inclusive sums along the row
+                    before += cross<kRowShr + 1>(before);
+                    before += cross<kRowShr + 2>(before);
+                    before += cross<kRowShr + 4>(before);
+                    before += cross<kRowShr + 8>(before);
+                    after += cross<kRowShl + 1>(after);
+                    after += cross<kRowShl + 2>(after);
+                    after += cross<kRowShl + 4>(after);
+                    after += cross<kRowShl + 8>(after);
+                    const bool there = ch < channels;
+                    const long long at = (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + o.n_first;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        const int n = j0 + j;
+                        if (n >= nn) break;
+                        const float a2 = m.a2[ch][n], G0 = m.carry[ch][n], h0 = there ? s.states[at + n] : 0.0f;
+                        float bv[8], cv[8], a[8], u[8], h = 0.0f, G = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const f32x4 fb = *(const f32x4 *)m.bc[n][0][q][sub], fc = *(const f32x4 *)m.bc[n][1][q][sub];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                bv[q * 4 + i] = fb[i];
+                                cv[q * 4 + i] = fc[i];
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            a[i] = exp2_hw(dt[i] * a2);
+                            u[i] = dtx[i] * bv[i];
+                            h = __builtin_fmaf(a[i], h, u[i]);
+                        }
+#pragma unroll
+                        for (int i = 7; i >= 0; --i) G = a[i] * __builtin_fmaf(cv[i], e[i], G);
+                        // both scans along the row; a lane without a source reads 0, after which
+                        // its product no longer matters
+                        float p = exp2_hw(all * a2), q = p;
+                        h = __builtin_fmaf(p, cross<kRowShr + 1>(h), h);
+                        G = __builtin_fmaf(q, cross<kRowShl + 1>(G), G);
+                        p *= cross<kRowShr + 1>(p);
+                        q *= cross<kRowShl + 1>(q);
+                        h = __builtin_fmaf(p, cross<kRowShr + 2>(h), h);
+                        G = __builtin_fmaf(q, cross<kRowShl + 2>(G), G);
+                        p *= cross<kRowShr + 2>(p);
+                        q *= cross<kRowShl + 2>(q);
+                        h = __builtin_fmaf(p, cross<kRowShr + 4>(h), h);
+                        G = __builtin_fmaf(q, cross<kRowShl + 4>(G), G);
+                        p *= cross<kRowShr + 4>(p);
+                        q *= cross<kRowShl + 4>(q);
+                        h = __builtin_fmaf(p, cross<kRowShr + 8>(h), h);
+                        G = __builtin_fmaf(q, cross<kRowShl + 8>(G), G);
+                        h = cross_or<kRowShr + 1>(h0, __builtin_fmaf(exp2_hw(before * a2), h0, h));
+                        const float Gend = __builtin_fmaf(exp2_hw(after * a2), G0, G);
+                        if (sub == 0) m.carry[ch][n] = Gend;
+                        G = cross_or<kRowShl + 1>(G0, Gend);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float ah = a[i] * h;
+                            h = ah + u[i];
+                            u[i] = ah;
+                            sv[i] = __builtin_fmaf(cv[i], h, sv[i]);
+                            dC[j][i] = __builtin_fmaf(e[i], h, dC[j][i]);
+                        }
+                        float sA = 0.0f;
+#pragma unroll
+                        for (int i = 7; i >= 0; --i) {
+                            const float gt = __builtin_fmaf(cv[i], e[i], G), w = gt * u[i];
+                            G = a[i] * gt;
+                            sdt[i] = __builtin_fmaf(a2, w, sdt[i]);
+                            sA = __builtin_fmaf(dt[i], w, sA);
+                            sgB[i] = __builtin_fmaf(gt, bv[i], sgB[i]);
+                            dB[j][i] = __builtin_fmaf(gt, dtx[i], dB[j][i]);
+                        }
+                        sA += cross<kRowShr + 8>(sA);
+                        sA += cross<kRowShr + 4>(sA);
+                        if (sub >= 12) m.dA[wave][turn][j][row * 4 + (sub & 3)] += sA;
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    put_steps(m.sdt, group, lane, sdt);
+                    put_steps(m.sgB, group, lane, sgB);
+                    put_steps(m.sv, group, lane, sv);
+                }
+                __syncthreads();
+            }
+            if (live && t < s.L) {
+                float sdt[8], sgB[8], sv[8], dt[8], e[8], xv[8];
+                const int dv = again(d);
+                get_steps(m.sdt, wave, lane, sdt);
+                get_steps(m.sgB, wave, lane, sgB);
+                get_steps(m.sv, wave, lane, sv);
+                if (o.sums) {
+                    float *past = o.sums + ((long long)b * s.D + dv) * s.L;
+                    const long long one = (long long)s.B * s.D * s.L;
+                    if (o.n_first) {
+                        float w[8];
+                        load8<0>(past, t, len, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sdt[i] += w[i];
+                        load8<0>(past + one, t, len, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sgB[i] += w[i];
+                        load8<0>(past + 2 * one, t, len, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sv[i] += w[i];
+                    }
+                    if (!o.last) {
+                        store8<0>(past, t, s.L, sdt);
+                        store8<0>(past + one, t, s.L, sgB);
+                        store8<0>(past + 2 * one, t, s.L, sv);
+                    }
+                }
+                if (o.last) {
+                    float slope[8];
+                    load8<DT>(at_row<const T>(s.delta, b, dv), t, len, slope);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) slope[i] = t + i >= len ? 0.0f : s.softplus ? logistic(slope[i] + bias) : 1.0f;
+                    get_steps(m.dt, wave, lane, dt);
+                    get_steps(m.e, wave, lane, e);
+                    load8<DT>(at_row<const T>(s.x, b, dv), t, len, xv);
+                    if (s.z.data) {
+                        float zslope[8];
+                        get_steps(m.zslope, wave, lane, zslope);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
+                        store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zslope);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // the states' sum was taken with A log2(e)
+                        sdt[i] = __builtin_fmaf(xv[i], sgB[i], sdt[i] * kLn2) * slope[i];
+                        sb += sdt[i];
+                        sD = __builtin_fmaf(e[i], xv[i], sD);
+                        sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
+                    }
+                    store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, sdt);
+                    store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, sgB);
+                }
+            }
+        } else if (live && t < s.L && o.last) {
+            const float zero[8] = {};
+            const int dv = again(d);
+            store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, zero);
+            store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, zero);
+            if (s.dz.data) store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zero);
+        }
+        // dB and dC summed over the wave's four rows: rows 0, 1 end up with dB, 2, 3 with dC, of
+        // the first and the second half of the wave's states
+        constexpr int NH = NS > 1 ? NS / 2 : 1;
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+            const int j2 = NS > 1 ? j + NH : j;
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = join_rows(join_halves(dB[j][i], dC[j][i]), join_halves(dB[j2][i], dC[j2][i]));
+            const int n = j0 + (row & 1 ? j2 : j);
+            if (n < nn && t < s.L && !(NS == 1 && (row & 1))) {
+                const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + o.n_first + n) * s.L;
+                store8<0>((row & 2 ? o.dC : o.dB) + at, t, s.L, w);
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kCh * kStates; i += 256) {
+        const int c = i / kStates, j = i % kStates;
+        if (c >= channels || j >= nn) continue;
+        const int w = j / NS, turn = (c / 4 - w) & 3;
+        const float *v = m.dA[w][turn][j % NS] + (c & 3) * 4;
+        const long long at = ((long long)b * s.D + first + c) * s.N + o.n_first + j;
+        o.dA[at] = (v[0] + v[1]) + (v[2] + v[3]);
+        if (s.d_initial_state) s.d_initial_state[at] = m.carry[c][j];
+    }
+    sD = row_sum(sD);
+    sb = row_sum(sb);
+    if (o.last && live && sub == 15) {
+        const long long at = (long long)b * s.D + again(d);
+        o.dD[at] = sD;
+        o.db[at] = sb;
+    }
+}
+
+// out[i] = sum over p of part[p][i], p in order.
 struct SumJob {
     const float *part;
     float *out;
@@ -287,9 +400,7 @@ __global__ __launch_bounds__(256) void scan_bwd_sum(SumJobs jobs) {
 
 ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     ScanBwdPlan p;
-    const int per_group = s.D / s.G;
-    p.R = per_group < 16 ? per_group : 16;
-    p.parts = (per_group + p.R - 1) / p.R;
+    p.parts = (s.D / s.G + kCh - 1) / kCh;
     const size_t bc = (size_t)p.parts * s.B * s.G * s.N * s.L, bd = (size_t)s.B * s.D;
     p.off_dB = 0;
     p.off_dC = bc;
@@ -310,26 +421,20 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     o.dD = ws + p.off_dD;
     o.db = ws + p.off_db;
     o.sums = s.N > kStates ? ws + p.off_sums : nullptr;
-    o.R = p.R;
     o.parts = p.parts;
     const dim3 grid((unsigned)((long long)s.B * s.G * p.parts));
     for (int n = 0; n < s.N; n += kStates) {
         o.n_first = n;
         o.n_end = s.N < n + kStates ? s.N : n + kStates;
         o.last = o.n_end == s.N;
-        const int waves = (o.n_end - n + NS - 1) / NS;
-        const size_t lds = ((size_t)waves * 3 * kScanChunk + 2 * (size_t)p.R * s.N + 2 * p.R) * 4;
-        const void *kern;
-        if (waves <= 4)
-            kern = dtype ? (const void *)scan_bwd_kernel<1, 256> : (const void *)scan_bwd_kernel<0, 256>;
-        else
-            kern = dtype ? (const void *)scan_bwd_kernel<1, 512> : (const void *)scan_bwd_kernel<0, 512>;
-        if (lds > 64 * 1024 &&
-            hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
-            return MICONV_ERR_HIP;
+        const int nn = o.n_end - n;
+        // as few states per wave as give each of the four waves some
+        const void *kern = nn <= 4   ? (dtype ? (const void *)scan_bwd_kernel<1, 1> : (const void *)scan_bwd_kernel<0, 1>)
+                           : nn <= 8 ? (dtype ? (const void *)scan_bwd_kernel<1, 2> : (const void *)scan_bwd_kernel<0, 2>)
+                                     : (dtype ? (const void *)scan_bwd_kernel<1, 4> : (const void *)scan_bwd_kernel<0, 4>);
         miconv_scan_t a = s;
         void *args[] = {(void *)&a, (void *)&o};
-        if (hipLaunchKernel(kern, grid, dim3(waves * 64), args, lds, st) != hipSuccess) return MICONV_ERR_HIP;
+        if (hipLaunchKernel(kern, grid, dim3(256), args, 0, st) != hipSuccess) return MICONV_ERR_HIP;
     }
     SumJobs jobs = {};
     const long long bc = (long long)s.B * s.G * s.N * s.L;

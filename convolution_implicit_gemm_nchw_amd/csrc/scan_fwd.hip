@@ -68,7 +68,7 @@ constexpr int kScanWaves = 8;
 template <int DT, int LANES, int ITEMS>
 __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g) {
     typedef typename Elem<DT>::T T;
-    constexpr int kT = LANES * ITEMS, kRows = 64 / LANES, kPairs = kT * 2 * 4;   // bytes of B and C per state
+    constexpr int kT = LANES * ITEMS, kRows = 64 / LANES, kEvery = kScanChunk / ITEMS, kPairs = kT * 2 * 4;   // bytes of B and C per state
     constexpr int kStage = 65536 / kPairs < 16 ? 65536 / kPairs : 16;            // states staged at a time
     // [state][B, C][ITEMS / 4][LANES][4]: a lane reads four steps as 16 bytes next to its neighbours'
     __shared__ __attribute__((aligned(16))) float bc[kStage * 2 * kT];
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     const int saved = scan_chunks(s.L);
     // 64 lanes per row: lane n holds the state n between chunks and A[n] log2(e).  16 lanes:
     // one chunk, so states come from and go to memory; A in LDS.
-    float carried = 0.0f, a_lane = 0.0f, middle = 0.0f;
+    float carried = 0.0f, a_lane = 0.0f;
     if constexpr (LANES == 64) {
         if (lane < s.N) {
             if (s.initial_state) carried = s.initial_state[row * s.N + lane];
@@ -107,7 +107,6 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     }
     for (int t0 = 0; t0 < s.L; t0 += kT) {
         const int c = t0 / kScanChunk, t = t0 + sub * ITEMS;
-        if (LANES == 64 && s.states && live && lane < s.N) s.states[(row * saved + c) * s.N + lane] = carried;
         float xv[ITEMS], dt[ITEMS], v[ITEMS], sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < ITEMS; q += 8) {
@@ -163,8 +162,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                     h = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(h), h);
                     const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), h0, h);
                     carried = lane == n ? lane_of(end, 63) : carried;
-                    if (kT > kScanChunk) middle = lane == n ? lane_of(end, 31) : middle;
                     h = cross_or<kWaveShr1>(h0, end);
+                    // lanes at the start of a saved chunk hold its entry state
+                    if (s.states && live && lane % kEvery == 0 && c + lane / kEvery < saved)
+                        s.states[(row * saved + c + lane / kEvery) * s.N + n] = h;
                 } else {
                     const float end = __builtin_fmaf(exp2_hw(a2 * sums.row), h0, h);
                     if (live && s.final_state && sub == LANES - 1) s.final_state[row * s.N + n] = end;
@@ -181,8 +182,6 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                 }
             }
         }
-        if (kT > kScanChunk && s.states && live && lane < s.N && c + 1 < saved)
-            s.states[(row * saved + c + 1) * s.N + lane] = middle;
         if (live) {
 #pragma unroll
             for (int q = 0; q < ITEMS; q += 8) {

@@ -9,14 +9,15 @@
 namespace miconv {
 
 // Time steps between two saved scan states.
-constexpr int kScanChunk = 512;
+constexpr int kScanChunk = 128;
+// Channels that one work-group of the scan's backward pass sums dB and dC over.
+constexpr int kScanBwdChannels = 16;
 
 constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
-// Channels one work-group of the scan's backward pass sums dB and dC over, and
-// the resulting number of partial sums per group of channels.
+// Workspace of the scan's backward pass: partial sums per group of channels, and offsets.
 struct ScanBwdPlan {
-    int R, parts;
+    int parts;
     size_t off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
 };
 ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s);
