@@ -373,7 +373,9 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     }
 }
 
-// out[i] = sum over p of part[p][i], p in order.
+// out[i] = sum over p of part[p][i] for several arrays: a work-group takes 256 consecutive i,
+// a wave a quarter of the parts (four i per lane, so every load is 16 bytes next to its
+// neighbours'); the quarters are added in order.
 struct SumJob {
     const float *part;
     float *out;
@@ -382,17 +384,40 @@ struct SumJob {
 };
 struct SumJobs {
     SumJob j[5];
+    long long first[6];       // first work-group of each array
     int count;
 };
 
 __global__ __launch_bounds__(256) void scan_bwd_sum(SumJobs jobs) {
-    for (int k = 0; k < jobs.count; ++k) {
-        const SumJob j = jobs.j[k];
-        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < j.n; i += (long long)gridDim.x * 256) {
-            float a = 0.0f;
-            for (int p = 0; p < j.parts; ++p) a += j.part[p * j.n + i];
-            j.out[i] = a;
+    __shared__ f32x4 quarter[4][64];
+    int k = 0;
+    while (k + 1 < jobs.count && (long long)blockIdx.x >= jobs.first[k + 1]) ++k;
+    const SumJob j = jobs.j[k];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long i = ((long long)blockIdx.x - jobs.first[k]) * 256 + lane * 4;
+    const int per = (j.parts + 3) / 4, p0 = wave * per, p1 = p0 + per < j.parts ? p0 + per : j.parts;
+    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i + 4 <= j.n) {
+        const float *src = j.part + i;
+#pragma unroll 8
+        for (int p = p0; p < p1; ++p) {
+            const u32x4 v = *(const u32x4_row *)(src + p * j.n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] += __uint_as_float(v[e]);
         }
+    } else {
+        for (int p = p0; p < p1; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < j.n) a[e] += j.part[p * j.n + i + e];
+    }
+    quarter[wave][lane] = a;
+    __syncthreads();
+    if (wave == 0) {
+        a = (quarter[0][lane] + quarter[1][lane]) + (quarter[2][lane] + quarter[3][lane]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i + e < j.n) j.out[i + e] = a[e];
     }
 }
 
@@ -443,9 +468,8 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     jobs.j[jobs.count++] = {o.dA, s.dA, (long long)s.D * s.N, s.B};
     if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B};
     if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B};
-    long long blocks = (bc + 255) / 256;
-    if (blocks > 4096) blocks = 4096;
-    hipLaunchKernelGGL(scan_bwd_sum, dim3((unsigned)blocks), dim3(256), 0, st, jobs);
+    for (int k = 0; k < jobs.count; ++k) jobs.first[k + 1] = jobs.first[k] + (jobs.j[k].n + 255) / 256;
+    hipLaunchKernelGGL(scan_bwd_sum, dim3((unsigned)jobs.first[jobs.count]), dim3(256), 0, st, jobs);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 

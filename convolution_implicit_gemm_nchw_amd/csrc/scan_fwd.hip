@@ -200,39 +200,73 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     if (LANES == 64 && s.final_state && live && lane < s.N) s.final_state[row * s.N + lane] = carried;
 }
 
-// One thread per (sequence, channel); its N states are contiguous.
-template <int DT>
+// One time step.  Memory bound: 8 bytes per state, read and written once.  PER lanes per
+// (sequence, channel), four states each, so that consecutive lanes read consecutive 16
+// bytes of the states; their products with C are added across the lanes.  VEC: N is a
+// multiple of 4 and the states are 16-byte aligned.  All reads of a state come before its
+// writes, so state_out may be state.
+template <int DT, int PER, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, const float *state, int slots,
                                                              const int *slot_of, float *state_out) {
     typedef typename Elem<DT>::T T;
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int sub = threadIdx.x % PER, n0 = sub * 4;
+    const long long i = (long long)blockIdx.x * (kThreads / PER) + threadIdx.x / PER;
     if (i >= (long long)s.B * s.D) return;
     const int b = (int)(i / s.D), d = (int)(i - (long long)b * s.D), g = d / (s.D / s.G);
     const int slot = slot_of ? slot_of[b] : b;
     T *yo = (T *)s.y.data + b * s.y.stride_b + d * s.y.stride_d;
     if (slot < 0 || slot >= slots) {
-        *yo = Elem<DT>::put(0.0f);
+        if (sub == 0) *yo = Elem<DT>::put(0.0f);
         return;
+    }
+    const long long so = ((long long)slot * s.D + d) * s.N + n0;
+    const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
+    const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
+    const float *A = s.A + (long long)d * s.N + n0;
+    float h[4], a[4], bv[4], cv[4];
+    if (VEC && n0 < s.N) {
+        const f32x4 hv = *(const f32x4 *)(state + so);
+        const u32x4 av = *(const u32x4_row *)A;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[e] = hv[e];
+            a[e] = __uint_as_float(av[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool in = n0 + e < s.N;
+        if (!VEC || n0 >= s.N) {
+            h[e] = in ? state[so + e] : 0.0f;
+            a[e] = in ? A[e] : 0.0f;
+        }
+        bv[e] = in ? Elem<DT>::get(Bm[(n0 + e) * s.Bm.stride_n]) : 0.0f;
+        cv[e] = in ? Elem<DT>::get(Cm[(n0 + e) * s.Cm.stride_n]) : 0.0f;
     }
     const float x = Elem<DT>::get(((const T *)s.x.data)[b * s.x.stride_b + d * s.x.stride_d]);
     const float raw = Elem<DT>::get(((const T *)s.delta.data)[b * s.delta.stride_b + d * s.delta.stride_d]) +
                       (s.delta_bias ? s.delta_bias[d] : 0.0f);
+    const float z = s.z.data ? Elem<DT>::get(((const T *)s.z.data)[b * s.z.stride_b + d * s.z.stride_d]) : 0.0f;
     const float dt = s.softplus ? softplus(raw) : raw, dtx = dt * x;
-    const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
-    const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
-    const long long so = ((long long)slot * s.D + d) * s.N;
-    float v = s.D_skip ? s.D_skip[d] * x : 0.0f;
-    for (int n = 0; n < s.N; ++n) {
-        const float a = exp2_hw(dt * (s.A[(long long)d * s.N + n] * kLog2e));
-        const float h = __builtin_fmaf(a, state[so + n], dtx * Elem<DT>::get(Bm[n * s.Bm.stride_n]));
-        state_out[so + n] = h;
-        v = __builtin_fmaf(Elem<DT>::get(Cm[n * s.Cm.stride_n]), h, v);
+    float v = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = __builtin_fmaf(exp2_hw(dt * (a[e] * kLog2e)), h[e], dtx * bv[e]);
+        v = __builtin_fmaf(cv[e], h[e], v);
     }
-    if (s.z.data) {
-        const float z = Elem<DT>::get(((const T *)s.z.data)[b * s.z.stride_b + d * s.z.stride_d]);
-        v *= z * logistic(z);
+    if (VEC && n0 < s.N) {
+        *(f32x4 *)(state_out + so) = f32x4{h[0], h[1], h[2], h[3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + e < s.N) state_out[so + e] = h[e];
     }
-    *yo = Elem<DT>::put(v);
+#pragma unroll
+    for (int m = 1; m < PER; m <<= 1) v += __shfl_xor(v, m);
+    if (sub == 0) {
+        v = s.D_skip ? __builtin_fmaf(s.D_skip[d], x, v) : v;
+        *yo = Elem<DT>::put(s.z.data ? v * (z * logistic(z)) : v);
+    }
 }
 
 }  // namespace
@@ -251,15 +285,31 @@ int launch_scan_fwd(const miconv_scan_t &s, int dtype, hipStream_t st) {
     return dtype ? scan_fwd<1, 64, 16>(s, st) : scan_fwd<0, 64, 16>(s, st);
 }
 
+template <int DT, int PER>
+static int scan_step(const miconv_scan_t &s, const float *state, int slots, const int *slot_of, float *state_out,
+                     hipStream_t st) {
+    const long long rows = (long long)s.B * s.D;
+    const dim3 grid((unsigned)((rows + kThreads / PER - 1) / (kThreads / PER)));
+    if (s.N % 4 == 0 && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0)
+        hipLaunchKernelGGL((scan_step_kernel<DT, PER, true>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
+                           state_out);
+    else
+        hipLaunchKernelGGL((scan_step_kernel<DT, PER, false>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
+                           state_out);
+    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+}
+
 int launch_scan_step(const miconv_scan_t &s, int dtype, const float *state, int slots, const int *slot_of,
                      float *state_out, hipStream_t st) {
-    const long long rows = (long long)s.B * s.D;
-    const dim3 grid((unsigned)((rows + kThreads - 1) / kThreads));
-    if (dtype)
-        hipLaunchKernelGGL(scan_step_kernel<1>, grid, dim3(kThreads), 0, st, s, state, slots, slot_of, state_out);
-    else
-        hipLaunchKernelGGL(scan_step_kernel<0>, grid, dim3(kThreads), 0, st, s, state, slots, slot_of, state_out);
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+#define MICONV_STEP(PER)                                                        \
+    return dtype ? scan_step<1, PER>(s, state, slots, slot_of, state_out, st)   \
+                 : scan_step<0, PER>(s, state, slots, slot_of, state_out, st)
+    if (s.N <= 4) MICONV_STEP(1);
+    if (s.N <= 8) MICONV_STEP(2);
+    if (s.N <= 16) MICONV_STEP(4);
+    if (s.N <= 32) MICONV_STEP(8);
+    MICONV_STEP(16);
+#undef MICONV_STEP
 }
 
 }  // namespace miconv
