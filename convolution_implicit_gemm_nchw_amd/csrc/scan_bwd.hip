@@ -130,31 +130,63 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     }
     for (int i = threadIdx.x; i < 4 * 4 * 4 * 16; i += 256) (&m.dA[0][0][0][0])[i] = 0.0f;
     float sD = 0.0f, sb = 0.0f;
-    for (int c = chunks - 1; c >= 0; --c) {
+    const int end = live ? len : 0;
+    // Chunks past the sequence's end: zeros.
+    int c = chunks - 1;
+    for (; c >= 0 && c * kT >= len; --c) {
+        const int t = c * kT + sub * 8, dv = again(d);
+        const float zero[8] = {};
+        if (live && t < s.L && o.last) {
+            store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, zero);
+            store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, zero);
+            if (s.dz.data) store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zero);
+        }
+        for (int i = wave * 4 + row; i < 2 * nn && t < s.L; i += 16) {
+            const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + o.n_first + (i >> 1)) * s.L;
+            store8<0>((i & 1 ? o.dC : o.dB) + at, t, s.L, zero);
+        }
+    }
+    // What a chunk reads of its rows, fetched while the chunk before is finished.
+    Raw8<DT> rx, rd, ry, rz, rbc[2];
+    auto fetch = [&](int c) {
+        const int t = c * kT + sub * 8, dv = again(d);
+        rx = fetch8<DT>(at_row<const T>(s.x, b, dv), t, end);
+        rd = fetch8<DT>(at_row<const T>(s.delta, b, dv), t, end);
+        ry = fetch8<DT>(at_row<const T>(s.dy, b, dv), t, end);
+        rz = fetch8<DT>(at_row<const T>(s.z.data ? s.z : s.x, b, dv), t, end);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = threadIdx.x + k * 256, which = (i < nn * 32 ? i : 0) >> 4, n = o.n_first + (which >> 1);
+            rbc[k] = fetch8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, c * kT + sub * 8, len);
+        }
+    };
+    if (c >= 0) fetch(c);
+    for (; c >= 0; --c) {
         const int t0 = c * kT, t = t0 + sub * 8;
         float dB[NS][8], dC[NS][8];
 #pragma unroll
         for (int j = 0; j < NS; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) dB[j][i] = dC[j][i] = 0.0f;
-        if (t0 < len) {
+        {
             // B and C of the chunk, and what belongs to the steps of the wave's own group
-            for (int i = threadIdx.x; i < nn * 32; i += 256) {
-                const int l = i & 15, which = i >> 4, n = o.n_first + (which >> 1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = threadIdx.x + k * 256, which = i >> 4;
+                if (i >= nn * 32) break;
                 float w[8];
-                load8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, t0 + l * 8, len, w);
-                *(f32x4 *)m.bc[which >> 1][which & 1][0][l] = f32x4{w[0], w[1], w[2], w[3]};
-                *(f32x4 *)m.bc[which >> 1][which & 1][1][l] = f32x4{w[4], w[5], w[6], w[7]};
+                widen8<DT>(rbc[k], w);
+                *(f32x4 *)m.bc[which >> 1][which & 1][0][sub] = f32x4{w[0], w[1], w[2], w[3]};
+                *(f32x4 *)m.bc[which >> 1][which & 1][1][sub] = f32x4{w[4], w[5], w[6], w[7]};
             }
             {
                 float dt[8], e[8], dtx[8];
-                const int end = live ? len : 0, dv = again(d);
-                load8<DT>(at_row<const T>(s.x, b, dv), t, end, dtx);
-                load8<DT>(at_row<const T>(s.delta, b, dv), t, end, dt);
-                load8<DT>(at_row<const T>(s.dy, b, dv), t, end, e);
+                widen8<DT>(rx, dtx);
+                widen8<DT>(rd, dt);
+                widen8<DT>(ry, e);
                 if (s.z.data) {
                     float zv[8], zslope[8];
-                    load8<DT>(at_row<const T>(s.z, b, dv), t, end, zv);
+                    widen8<DT>(rz, zv);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float sg = logistic(zv[i]);
@@ -190,6 +222,11 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                         get_steps(m.sgB, group, lane, sgB);
                         get_steps(m.sv, group, lane, sv);
                     }
+                    float h0s[NS];
+                    const bool there = ch < channels;
+                    const float *entry = s.states + (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + o.n_first;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) h0s[j] = there && j0 + j < nn ? entry[j0 + j] : 0.0f;
                     float all = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) all += dt[i];
@@ -202,13 +239,11 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     after += cross<kRowShl + 2>(after);
                     after += cross<kRowShl + 4>(after);
                     after += cross<kRowShl + 8>(after);
-                    const bool there = ch < channels;
-                    const long long at = (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + o.n_first;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) {
                         const int n = j0 + j;
                         if (n >= nn) break;
-                        const float a2 = m.a2[ch][n], G0 = m.carry[ch][n], h0 = there ? s.states[at + n] : 0.0f;
+                        const float a2 = m.a2[ch][n], G0 = m.carry[ch][n], h0 = h0s[j];
                         float bv[8], cv[8], a[8], u[8], h = 0.0f, G = 0.0f;
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
@@ -277,67 +312,16 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                 }
                 __syncthreads();
             }
-            if (live && t < s.L) {
-                float sdt[8], sgB[8], sv[8], dt[8], e[8], xv[8];
-                const int dv = again(d);
-                get_steps(m.sdt, wave, lane, sdt);
-                get_steps(m.sgB, wave, lane, sgB);
-                get_steps(m.sv, wave, lane, sv);
-                if (o.sums) {
-                    float *past = o.sums + ((long long)b * s.D + dv) * s.L;
-                    const long long one = (long long)s.B * s.D * s.L;
-                    if (o.n_first) {
-                        float w[8];
-                        load8<0>(past, t, len, w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sdt[i] += w[i];
-                        load8<0>(past + one, t, len, w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sgB[i] += w[i];
-                        load8<0>(past + 2 * one, t, len, w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sv[i] += w[i];
-                    }
-                    if (!o.last) {
-                        store8<0>(past, t, s.L, sdt);
-                        store8<0>(past + one, t, s.L, sgB);
-                        store8<0>(past + 2 * one, t, s.L, sv);
-                    }
-                }
-                if (o.last) {
-                    float slope[8];
-                    load8<DT>(at_row<const T>(s.delta, b, dv), t, len, slope);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) slope[i] = t + i >= len ? 0.0f : s.softplus ? logistic(slope[i] + bias) : 1.0f;
-                    get_steps(m.dt, wave, lane, dt);
-                    get_steps(m.e, wave, lane, e);
-                    load8<DT>(at_row<const T>(s.x, b, dv), t, len, xv);
-                    if (s.z.data) {
-                        float zslope[8];
-                        get_steps(m.zslope, wave, lane, zslope);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
-                        store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zslope);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // the states' sum was taken with A log2(e)
-                        sdt[i] = __builtin_fmaf(xv[i], sgB[i], sdt[i] * kLn2) * slope[i];
-                        sb += sdt[i];
-                        sD = __builtin_fmaf(e[i], xv[i], sD);
-                        sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
-                    }
-                    store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, sdt);
-                    store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, sgB);
-                }
-            }
-        } else if (live && t < s.L && o.last) {
-            const float zero[8] = {};
-            const int dv = again(d);
-            store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, zero);
-            store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, zero);
-            if (s.dz.data) store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zero);
         }
+        // this chunk's x and delta once more, and the next chunk's rows, while dB and dC leave
+        Raw8<DT> ox, od;
+        {
+            const int dv = again(d);
+            ox = fetch8<DT>(at_row<const T>(s.x, b, dv), t, end);
+            od = fetch8<DT>(at_row<const T>(s.delta, b, dv), t, end);
+        }
+        fetch(c > 0 ? c - 1 : 0);              // (without a condition: else the old values stay live)
+        __builtin_amdgcn_sched_barrier(0);
         // dB and dC summed over the wave's four rows: rows 0, 1 end up with dB, 2, 3 with dC, of
         // the first and the second half of the wave's states
         constexpr int NH = NS > 1 ? NS / 2 : 1;
@@ -351,6 +335,61 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             if (n < nn && t < s.L && !(NS == 1 && (row & 1))) {
                 const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + o.n_first + n) * s.L;
                 store8<0>((row & 2 ? o.dC : o.dB) + at, t, s.L, w);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (live) {
+            const int dv = again(d);
+            float sdt[8], sgB[8], sv[8], dt[8], e[8], xv[8];
+            get_steps(m.sdt, wave, lane, sdt);
+            get_steps(m.sgB, wave, lane, sgB);
+            get_steps(m.sv, wave, lane, sv);
+            if (o.sums) {
+                float *past = o.sums + ((long long)b * s.D + dv) * s.L;
+                const long long one = (long long)s.B * s.D * s.L;
+                if (o.n_first) {
+                    float w[8];
+                    load8<0>(past, t, len, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sdt[i] += w[i];
+                    load8<0>(past + one, t, len, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sgB[i] += w[i];
+                    load8<0>(past + 2 * one, t, len, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sv[i] += w[i];
+                }
+                if (!o.last) {
+                    store8<0>(past, t, s.L, sdt);
+                    store8<0>(past + one, t, s.L, sgB);
+                    store8<0>(past + 2 * one, t, s.L, sv);
+                }
+            }
+            if (o.last) {
+                float slope[8];
+                widen8<DT>(od, slope);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) slope[i] = t + i >= len ? 0.0f : s.softplus ? logistic(slope[i] + bias) : 1.0f;
+                get_steps(m.dt, wave, lane, dt);
+                get_steps(m.e, wave, lane, e);
+                widen8<DT>(ox, xv);
+                if (s.z.data) {
+                    float zslope[8];
+                    get_steps(m.zslope, wave, lane, zslope);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
+                    store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zslope);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    // the states' sum was taken with A log2(e)
+                    sdt[i] = __builtin_fmaf(xv[i], sgB[i], sdt[i] * kLn2) * slope[i];
+                    sb += sdt[i];
+                    sD = __builtin_fmaf(e[i], xv[i], sD);
+                    sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
+                }
+                store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, sdt);
+                store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, sgB);
             }
         }
     }

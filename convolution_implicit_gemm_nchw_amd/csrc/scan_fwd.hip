@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
 // One time step.  Memory bound: 8 bytes per state, read and written once.  PER lanes per
 // (sequence, channel), four states each, so that consecutive lanes read consecutive 16
 // bytes of the states; their products with C are added across the lanes.  VEC: N is a
-// multiple of 4 and the states are 16-byte aligned.  All reads of a state come before its
+// multiple of 4, the states are 16-byte aligned, B and C have their states next to each other.  All reads of a state come before its
 // writes, so state_out may be state.
 template <int DT, int PER, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, const float *state, int slots,
@@ -232,6 +232,8 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
             h[e] = hv[e];
             a[e] = __uint_as_float(av[e]);
         }
+        load4<DT>(Bm + n0, bv);
+        load4<DT>(Cm + n0, cv);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -239,9 +241,9 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
         if (!VEC || n0 >= s.N) {
             h[e] = in ? state[so + e] : 0.0f;
             a[e] = in ? A[e] : 0.0f;
+            bv[e] = in ? Elem<DT>::get(Bm[(n0 + e) * s.Bm.stride_n]) : 0.0f;
+            cv[e] = in ? Elem<DT>::get(Cm[(n0 + e) * s.Cm.stride_n]) : 0.0f;
         }
-        bv[e] = in ? Elem<DT>::get(Bm[(n0 + e) * s.Bm.stride_n]) : 0.0f;
-        cv[e] = in ? Elem<DT>::get(Cm[(n0 + e) * s.Cm.stride_n]) : 0.0f;
     }
     const float x = Elem<DT>::get(((const T *)s.x.data)[b * s.x.stride_b + d * s.x.stride_d]);
     const float raw = Elem<DT>::get(((const T *)s.delta.data)[b * s.delta.stride_b + d * s.delta.stride_d]) +
@@ -290,7 +292,8 @@ static int scan_step(const miconv_scan_t &s, const float *state, int slots, cons
                      hipStream_t st) {
     const long long rows = (long long)s.B * s.D;
     const dim3 grid((unsigned)((rows + kThreads / PER - 1) / (kThreads / PER)));
-    if (s.N % 4 == 0 && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0)
+    const bool together = s.N == 1 || (s.Bm.stride_n == 1 && s.Cm.stride_n == 1);
+    if (s.N % 4 == 0 && together && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0)
         hipLaunchKernelGGL((scan_step_kernel<DT, PER, true>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
                            state_out);
     else

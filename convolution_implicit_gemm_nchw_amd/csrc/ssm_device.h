@@ -48,6 +48,75 @@ DEVI void load8(const typename Elem<DT>::T *row, int t, int end, float (&v)[8]) 
     }
 }
 
+typedef uint32_t u32x2_row __attribute__((ext_vector_type(2), aligned(2)));
+
+template <int DT>
+DEVI void load4(const typename Elem<DT>::T *p, float (&v)[4]) {
+    if constexpr (DT == 1) {
+        const u32x2 r = *(const u32x2_row *)p;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = __uint_as_float(r[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+    } else {
+        const u32x4 r = *(const u32x4_row *)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+    }
+}
+
+// The same as load8 in two steps: fetch8 issues the loads, widen8 takes their values later.
+template <int DT>
+struct Raw8 {
+    u32x4 r[DT == 1 ? 1 : 2];
+};
+
+template <int DT>
+DEVI Raw8<DT> fetch8(const typename Elem<DT>::T *row, int t, int end) {
+    Raw8<DT> o;
+    if (t + 8 <= end) {
+        o.r[0] = *(const u32x4_row *)(row + t);
+        if constexpr (DT == 0) o.r[1] = *(const u32x4_row *)(row + t + 4);
+    } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0;
+            if (t + i < end) {
+                if constexpr (DT == 1)
+                    v[i] = ((const uint16_t *)row)[t + i];
+                else
+                    v[i] = ((const uint32_t *)row)[t + i];
+            }
+        }
+        if constexpr (DT == 1) {
+            o.r[0] = pack<2>(v);
+        } else {
+            o.r[0] = pack<4>(v);
+            o.r[1] = pack<4>(v + 4);
+        }
+    }
+    return o;
+}
+
+template <int DT>
+DEVI void widen8(const Raw8<DT> &o, float (&v)[8]) {
+    if constexpr (DT == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(o.r[0][i] << 16);
+            v[2 * i + 1] = __uint_as_float(o.r[0][i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(o.r[0][i]);
+            v[4 + i] = __uint_as_float(o.r[DT == 0][i]);
+        }
+    }
+}
+
 // row[t + i] = v[i] for t + i < end.
 template <int DT>
 DEVI void store8(typename Elem<DT>::T *row, int t, int end, const float (&v)[8]) {
