@@ -38,7 +38,9 @@ static_assert(kT == 128 && kCh == 16, "16 lanes x 8 steps, 4 waves x 4 rows");
 
 struct BwdOut {
     float *dB, *dC;           // [parts][B][G][N][L]
-    float *dA, *dD, *db;      // [B][D][N], [B][D], [B][D]
+    float *dA, *dD, *db;      // [segs][B][D][N], [segs][B][D], [segs][B][D]
+    const float *G;           // [B][D][chunks][N] G of the step after each chunk, or null: one segment
+    int segs, seg_chunks;     // time segments (a work-group each), chunks of one
     float *sums;              // [3][B][D][L] sums over the states of earlier launches, or null
     int parts;
     int n_first, n_end, last; // states of this launch; whether it is the last one
@@ -108,12 +110,14 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     __shared__ __attribute__((aligned(16))) Lds m;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane >> 4, sub = lane & 15;
     const int per_group = s.D / s.G;
-    const int part = blockIdx.x % o.parts, g = (blockIdx.x / o.parts) % s.G, b = blockIdx.x / (o.parts * s.G);
+    const int part = blockIdx.x % o.parts, bg = blockIdx.x / o.parts % (s.B * s.G), seg = blockIdx.x / (o.parts * s.B * s.G);
+    const int g = bg % s.G, b = bg / s.G;
     const int first = g * per_group + part * kCh;                        // the work-group's first channel
     const int channels = per_group - part * kCh < kCh ? per_group - part * kCh : kCh;
     const int nn = o.n_end - o.n_first, j0 = wave * NS;                  // states of the launch, of the wave
     const int len = valid_steps(s.lengths, b, s.L);
     const int chunks = (s.L + kT - 1) / kT;
+    const int c_first = seg * o.seg_chunks, c_end = c_first + o.seg_chunks < chunks ? c_first + o.seg_chunks : chunks;
     // the channel that this lane owns between the turns
     const int own = wave * 4 + row;
     const bool live = own < channels;
@@ -126,14 +130,16 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         const bool used = c < channels && j < nn;
         const long long at = ((long long)b * s.D + first + c) * s.N + o.n_first + j;
         m.a2[c][j] = used ? s.A[(long long)(first + c) * s.N + o.n_first + j] * kLog2e : 0.0f;
-        m.carry[c][j] = used && s.d_final_state ? s.d_final_state[at] : 0.0f;
+        const float *G = c_end < chunks ? o.G + (((long long)b * s.D + first + c) * chunks + c_end - 1) * s.N + o.n_first + j
+                                        : (s.d_final_state ? s.d_final_state + at : nullptr);
+        m.carry[c][j] = used && G ? *G : 0.0f;
     }
     for (int i = threadIdx.x; i < 4 * 4 * 4 * 16; i += 256) (&m.dA[0][0][0][0])[i] = 0.0f;
     float sD = 0.0f, sb = 0.0f;
     const int end = live ? len : 0;
     // Chunks past the sequence's end: zeros.
-    int c = chunks - 1;
-    for (; c >= 0 && c * kT >= len; --c) {
+    int c = c_end - 1;
+    for (; c >= c_first && c * kT >= len; --c) {
         const int t = c * kT + sub * 8, dv = again(d);
         const float zero[8] = {};
         if (live && t < s.L && o.last) {
@@ -160,8 +166,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             rbc[k] = fetch8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, c * kT + sub * 8, len);
         }
     };
-    if (c >= 0) fetch(c);
-    for (; c >= 0; --c) {
+    if (c >= c_first) fetch(c);
+    for (; c >= c_first; --c) {
         const int t0 = c * kT, t = t0 + sub * 8;
         float dB[NS][8], dC[NS][8];
 #pragma unroll
@@ -320,7 +326,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             ox = fetch8<DT>(at_row<const T>(s.x, b, dv), t, end);
             od = fetch8<DT>(at_row<const T>(s.delta, b, dv), t, end);
         }
-        fetch(c > 0 ? c - 1 : 0);              // (without a condition: else the old values stay live)
+        fetch(c > c_first ? c - 1 : c);              // (without a condition: else the old values stay live)
         __builtin_amdgcn_sched_barrier(0);
         // dB and dC summed over the wave's four rows: rows 0, 1 end up with dB, 2, 3 with dC, of
         // the first and the second half of the wave's states
@@ -400,15 +406,99 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         const int w = j / NS, turn = (c / 4 - w) & 3;
         const float *v = m.dA[w][turn][j % NS] + (c & 3) * 4;
         const long long at = ((long long)b * s.D + first + c) * s.N + o.n_first + j;
-        o.dA[at] = (v[0] + v[1]) + (v[2] + v[3]);
-        if (s.d_initial_state) s.d_initial_state[at] = m.carry[c][j];
+        o.dA[(long long)seg * s.B * s.D * s.N + at] = (v[0] + v[1]) + (v[2] + v[3]);
+        if (s.d_initial_state && seg == 0) s.d_initial_state[at] = m.carry[c][j];
     }
     sD = row_sum(sD);
     sb = row_sum(sb);
     if (o.last && live && sub == 15) {
-        const long long at = (long long)b * s.D + again(d);
+        const long long at = ((long long)seg * s.B + b) * s.D + again(d);
         o.dD[at] = sD;
         o.db[at] = sb;
+    }
+}
+
+// G at the end of every chunk, for a backward pass whose time segments run side by side:
+// the forward kernel's scan with the lanes in reversed order of time, and no outputs but
+// the values between chunks.  A wave per row, 64 lanes x 16 steps, the work-group's rows
+// sharing C in LDS.
+constexpr int kCarryWaves = 8, kCarryItems = 16, kCarryT = 64 * kCarryItems;
+
+template <int DT>
+__global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(miconv_scan_t s, float *out, int blocks_g) {
+    typedef typename Elem<DT>::T T;
+    constexpr int kStage = 16, kEvery = kT / kCarryItems;
+    __shared__ __attribute__((aligned(16))) float cs[kStage][kCarryT];     // [ITEMS / 4][lane][4]
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int per_group = s.D / s.G;
+    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g, g = bg % s.G, b = bg / s.G;
+    const int in_group = blk * kCarryWaves + wave;
+    const bool live = in_group < per_group;
+    const int d = g * per_group + (live ? in_group : 0);
+    const long long row = (long long)b * s.D + d;
+    const int len = valid_steps(s.lengths, b, s.L), chunks = (s.L + kT - 1) / kT;
+    const T *dl = at_row<const T>(s.delta, b, d), *dy = at_row<const T>(s.dy, b, d);
+    const T *z = s.z.data ? at_row<const T>(s.z, b, d) : nullptr;
+    const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
+    const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
+    float carried = 0.0f, a_lane = 0.0f;               // lane n: state n
+    if (lane < s.N) {
+        if (s.d_final_state) carried = s.d_final_state[row * s.N + lane];
+        a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
+    }
+    for (int t0 = (s.L - 1) / kCarryT * kCarryT; t0 >= 0; t0 -= kCarryT) {
+        const int t = t0 + (63 - lane) * kCarryItems;
+        float dt[kCarryItems], e[kCarryItems], sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kCarryItems; q += 8) {
+            load8<DT>(dl, t + q, len, *(float (*)[8])(dt + q));
+            load8<DT>(dy, t + q, len, *(float (*)[8])(e + q));
+            if (z) {
+                float zv[8];
+                load8<DT>(z, t + q, len, zv);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[q + i] *= zv[i] * logistic(zv[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kCarryItems; ++i) {
+            const float raw = dt[i] + bias;
+            dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;
+            sum += dt[i];
+        }
+        const Sums sums = prefix_sums(sum);
+        for (int n0 = 0; n0 < s.N; n0 += kStage) {
+            const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
+            __syncthreads();
+            for (int i = threadIdx.x; i < nn * (kCarryT / 8); i += 64 * kCarryWaves) {
+                const int at = i % (kCarryT / 8) * 8, k = i / (kCarryT / 8);
+                float w[8];
+                load8<DT>(Cm + (n0 + k) * s.Cm.stride_n, t0 + at, len, w);
+                float *to = cs[k] + (at % kCarryItems / 4) * 256 + (63 - at / kCarryItems) * 4;
+                *(f32x4 *)to = f32x4{w[0], w[1], w[2], w[3]};
+                *(f32x4 *)(to + 256) = f32x4{w[4], w[5], w[6], w[7]};
+            }
+            __syncthreads();
+            for (int k = 0; k < nn; ++k) {
+                const int n = n0 + k;
+                const float a2 = lane_of(a_lane, n), G0 = lane_of(carried, n);
+                float G = 0.0f;
+#pragma unroll
+                for (int i = kCarryItems - 4; i >= 0; i -= 4) {
+                    const f32x4 c = *(const f32x4 *)(cs[k] + i * 64 + lane * 4);
+#pragma unroll
+                    for (int j = 3; j >= 0; --j) G = exp2_hw(dt[i + j] * a2) * __builtin_fmaf(c[j], e[i + j], G);
+                }
+                G = scan_rows(G, a2, sums);
+                G = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(G), G);
+                G = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(G), G);
+                const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), G0, G);
+                carried = lane == n ? lane_of(end, 63) : carried;
+                G = cross_or<kWaveShr1>(G0, end);
+                const int c = t0 / kT + (64 - lane) / kEvery - 1;      // the chunk that ends where this lane begins
+                if (live && lane % kEvery == 0 && c < chunks) out[(row * chunks + c) * s.N + n] = G;
+            }
+        }
     }
 }
 
@@ -462,16 +552,26 @@ __global__ __launch_bounds__(256) void scan_bwd_sum(SumJobs jobs) {
 
 }  // namespace
 
+// Where the groups of 16 channels alone give the 256 CUs (two work-groups each) less than
+// half of what they hold, the time axis is split too, at the price of a pass that finds G
+// between the segments.
 ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     ScanBwdPlan p;
     p.parts = (s.D / s.G + kCh - 1) / kCh;
+    const long long groups = (long long)s.B * s.G * p.parts;
+    const int chunks = scan_chunks(s.L);
+    long long segs = groups * 2 <= 512 && chunks >= 4 ? 512 / groups : 1;
+    if (segs > chunks) segs = chunks;
+    p.seg_chunks = (int)((chunks + segs - 1) / segs);
+    p.segs = (chunks + p.seg_chunks - 1) / p.seg_chunks;
     const size_t bc = (size_t)p.parts * s.B * s.G * s.N * s.L, bd = (size_t)s.B * s.D;
     p.off_dB = 0;
     p.off_dC = bc;
     p.off_dA = 2 * bc;
-    p.off_dD = p.off_dA + bd * s.N;
-    p.off_db = p.off_dD + bd;
-    p.off_sums = p.off_db + bd;
+    p.off_dD = p.off_dA + bd * s.N * p.segs;
+    p.off_db = p.off_dD + bd * p.segs;
+    p.off_G = p.off_db + bd * p.segs;
+    p.off_sums = p.off_G + (p.segs > 1 ? bd * chunks * s.N : 0);
     p.bytes = (p.off_sums + (s.N > kStates ? 3 * bd * s.L : 0)) * 4;
     return p;
 }
@@ -484,9 +584,21 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     o.dA = ws + p.off_dA;
     o.dD = ws + p.off_dD;
     o.db = ws + p.off_db;
+    o.G = p.segs > 1 ? ws + p.off_G : nullptr;
     o.sums = s.N > kStates ? ws + p.off_sums : nullptr;
     o.parts = p.parts;
-    const dim3 grid((unsigned)((long long)s.B * s.G * p.parts));
+    o.segs = p.segs;
+    o.seg_chunks = p.seg_chunks;
+    if (p.segs > 1) {
+        const int blocks_g = (s.D / s.G + kCarryWaves - 1) / kCarryWaves;
+        const dim3 cgrid((unsigned)((long long)s.B * s.G * blocks_g)), cblock(64 * kCarryWaves);
+        if (dtype)
+            hipLaunchKernelGGL(scan_bwd_carry_kernel<1>, cgrid, cblock, 0, st, s, ws + p.off_G, blocks_g);
+        else
+            hipLaunchKernelGGL(scan_bwd_carry_kernel<0>, cgrid, cblock, 0, st, s, ws + p.off_G, blocks_g);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    }
+    const dim3 grid((unsigned)((long long)s.B * s.G * p.parts * p.segs));
     for (int n = 0; n < s.N; n += kStates) {
         o.n_first = n;
         o.n_end = s.N < n + kStates ? s.N : n + kStates;
@@ -504,9 +616,9 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     const long long bc = (long long)s.B * s.G * s.N * s.L;
     jobs.j[jobs.count++] = {o.dB, s.dB, bc, p.parts};
     jobs.j[jobs.count++] = {o.dC, s.dC, bc, p.parts};
-    jobs.j[jobs.count++] = {o.dA, s.dA, (long long)s.D * s.N, s.B};
-    if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B};
-    if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B};
+    jobs.j[jobs.count++] = {o.dA, s.dA, (long long)s.D * s.N, s.B * p.segs};
+    if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B * p.segs};
+    if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B * p.segs};
     for (int k = 0; k < jobs.count; ++k) jobs.first[k + 1] = jobs.first[k] + (jobs.j[k].n + 255) / 256;
     hipLaunchKernelGGL(scan_bwd_sum, dim3((unsigned)jobs.first[jobs.count]), dim3(256), 0, st, jobs);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;

@@ -24,43 +24,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Prefix sums of the lanes' dt: within rows of 16, halves of 32 and the whole wave.
-struct Sums {
-    float own, row, half, all;
-};
-
-DEVI Sums prefix_sums(float own) {
-    Sums s;
-    s.own = own;
-    float v = own;
-    v += cross<kRowShr + 1>(v);
-    v += cross<kRowShr + 2>(v);
-    v += cross<kRowShr + 4>(v);
-    v += cross<kRowShr + 8>(v);
-    s.row = v;
-    v += cross<kRowBcast15, 0xa>(v);
-    s.half = v;
-    v += cross<kRowBcast31, 0xc>(v);
-    s.all = v;
-    return s;
-}
-
-// The lanes' maps (product of decays, state from zero) combined along the wave: the
-// state after each lane's steps from a zero state before lane 0.  The product over a
-// range of steps is the exponential of the sum of dt, so only those that the first
-// steps need are multiplied up; a lane without a source reads 0, after which its
-// product no longer matters.
-DEVI float scan_rows(float h, float a2, const Sums &s) {
-    float p = exp2_hw(a2 * s.own);
-    h = __builtin_fmaf(p, cross<kRowShr + 1>(h), h);
-    p *= cross<kRowShr + 1>(p);
-    h = __builtin_fmaf(p, cross<kRowShr + 2>(h), h);
-    p *= cross<kRowShr + 2>(p);
-    h = __builtin_fmaf(p, cross<kRowShr + 4>(h), h);
-    p *= cross<kRowShr + 4>(p);
-    return __builtin_fmaf(p, cross<kRowShr + 8>(h), h);
-}
-
 // Work-groups of 8 waves; 64 lanes x 16 or 8 steps per row, or, for short rows, four rows
 // of 16 lanes x 8 steps per wave (then the row is a single chunk).
 constexpr int kScanWaves = 8;

@@ -15,10 +15,11 @@ constexpr int kScanBwdChannels = 16;
 
 constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
-// Workspace of the scan's backward pass: partial sums per group of channels, and offsets.
+// Workspace of the scan's backward pass: partial sums per group of channels, time segments
+// that run side by side, and offsets.
 struct ScanBwdPlan {
-    int parts;
-    size_t off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
+    int parts, segs, seg_chunks;
+    size_t off_G, off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
 };
 ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s);
 
