@@ -37,45 +37,44 @@ DEVI float full_at(const typename Elem<DT>::T *row, const typename Elem<DT>::T *
     return init ? Elem<DT>::get(init[f]) : 0.0f;
 }
 
-template <int DT, int K>
-__global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv_t c, int lg_tpr,
-                                                              long long row_blocks, long long work) {
+// 2^lg_tpr threads per row.  WAVE: a row takes whole waves, so that what belongs to it
+// (addresses, taps, bias) is scalar.
+template <int DT, int K, bool WAVE>
+__global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv_t c, int lg_tpr, FDiv fd_D) {
     typedef typename Elem<DT>::T T;
-    const int sub = threadIdx.x & ((1 << lg_tpr) - 1), rib = threadIdx.x >> lg_tpr;
-    const int rows_per_block = kThreads >> lg_tpr;
-    for (long long wk = blockIdx.x; wk < work; wk += gridDim.x) {
-        const long long tb = wk / row_blocks, rb = wk - tb * row_blocks;
-        const long long row = rb * rows_per_block + rib;
-        if (row >= (long long)c.B * c.D) continue;
-        const int b = (int)(row / c.D), d = (int)(row - (long long)b * c.D);
-        const long long t64 = ((tb << lg_tpr) + sub) * 8;
-        if (t64 >= c.L) continue;
+    const int sub = threadIdx.x & ((1 << lg_tpr) - 1);
+    const int rib = WAVE ? uniform(threadIdx.x >> lg_tpr) : threadIdx.x >> lg_tpr;
+    const long long row64 = (long long)blockIdx.x * (kThreads >> lg_tpr) + rib;
+    if (row64 >= (long long)c.B * c.D) return;
+    const int row = (int)row64, b = WAVE ? uniform((int)fdiv(row, fd_D)) : (int)fdiv(row, fd_D), d = row - b * c.D;
+    const int len = valid_steps(c.lengths, b, c.L);
+    const T *x = (const T *)c.x.data + b * c.x.stride_b + d * c.x.stride_d;
+    const T *init = c.initial_state ? (const T *)c.initial_state + (long long)row * (K - 1) : nullptr;
+    T *y = (T *)c.y.data + b * c.y.stride_b + d * c.y.stride_d;
+    float w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = Elem<DT>::get(((const T *)c.w)[(long long)d * K + k]);
+    const float bias = c.bias ? c.bias[d] : 0.0f;
+    for (long long t64 = (((long long)blockIdx.y << lg_tpr) + sub) * 8; t64 < c.L;
+         t64 += ((long long)gridDim.y << lg_tpr) * 8) {
         const int t = (int)t64;
-        const int len = valid_steps(c.lengths, b, c.L);
-        const T *x = (const T *)c.x.data + b * c.x.stride_b + d * c.x.stride_d;
-        const T *init = c.initial_state ? (const T *)c.initial_state + row * (K - 1) : nullptr;
-        T *y = (T *)c.y.data + b * c.y.stride_b + d * c.y.stride_d;
         float out[8] = {};
         if (t < len) {
             float v[16];
             float (&before)[8] = *(float (*)[8])v, (&own)[8] = *(float (*)[8])(v + 8);
             load8<DT>(x, t, len, own);
             load_before<DT, K>(x, init, t, len, before);
-            float w[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) w[k] = Elem<DT>::get(((const T *)c.w)[(long long)d * K + k]);
-            const float bias = c.bias ? c.bias[d] : 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float u = bias;
 #pragma unroll
                 for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[k], v[8 + i - (K - 1) + k], u);
-                out[i] = t + i < len ? (c.silu ? u * logistic(u) : u) : 0.0f;
+                out[i] = t + i < len ? (c.silu ? u * logistic_for<DT>(u) : u) : 0.0f;
             }
         }
         store8<DT>(y, t, c.L, out);
         if (t == 0 && c.final_state) {
-            T *fs = (T *)c.final_state + row * (K - 1);
+            T *fs = (T *)c.final_state + (long long)row * (K - 1);
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) fs[j] = Elem<DT>::put(full_at<DT, K>(x, init, len + j));
         }
@@ -101,8 +100,10 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
         dw[k] = 0.0f;
     }
     const float bias = c.bias ? c.bias[d] : 0.0f;
+    int b = (int)((first + threadIdx.x) / tiles), tile = (int)(first + threadIdx.x - (long long)b * tiles);
+    const int step_b = TH / tiles, step_t = TH - step_b * tiles;
     for (long long it = first + threadIdx.x; it < last; it += TH) {
-        const int b = (int)(it / tiles), t = (int)(it - (long long)b * tiles) * 8;
+        const int t = tile * 8;
         const int len = valid_steps(c.lengths, b, c.L);
         const long long row = (long long)b * c.D + d;
         const T *x = (const T *)c.x.data + b * c.x.stride_b + d * c.x.stride_d;
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
                 float u = bias;
 #pragma unroll
                 for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[k], v[8 + i - (K - 1) + k], u);
-                const float sg = logistic(u);
+                const float sg = logistic_for<DT>(u);
                 // a step past the end has du = 0 whatever u is there
                 g[i] = t + i < len ? g[i] * (sg * __builtin_fmaf(u, 1.0f - sg, 1.0f)) : 0.0f;
             }
@@ -154,6 +155,12 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
                 if (dfs && f >= len) s += Elem<DT>::get(dfs[f - len]);
                 di[f] = Elem<DT>::put(s);
             }
+        }
+        b += step_b;
+        tile += step_t;
+        if (tile >= tiles) {
+            tile -= tiles;
+            ++b;
         }
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -219,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void causal_step_kernel(int B, int D, int
     for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[(long long)d * K + k] , v[k], u);
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) state_out[so + k] = Elem<DT>::put(v[k + 1]);
-    *yo = Elem<DT>::put(silu ? u * logistic(u) : u);
+    *yo = Elem<DT>::put(silu ? u * logistic_for<DT>(u) : u);
 }
 
 int lg2_up(long long v, int most) {
@@ -233,9 +240,13 @@ int fwd_k(const miconv_causal_conv_t &c, hipStream_t st) {
     const long long tiles = (c.L + 7) / 8;
     const int lg = lg2_up(tiles, 8);
     const long long rpb = kThreads >> lg, row_blocks = ((long long)c.B * c.D + rpb - 1) / rpb;
-    const long long work = row_blocks * ((tiles + (1ll << lg) - 1) >> lg);
-    const unsigned grid = (unsigned)(work < (1ll << 30) ? work : (1ll << 30));
-    hipLaunchKernelGGL((causal_fwd_kernel<DT, K>), dim3(grid), dim3(kThreads), 0, st, c, lg, row_blocks, work);
+    const long long along = (tiles + (1ll << lg) - 1) >> lg;
+    const dim3 grid((unsigned)row_blocks, (unsigned)(along < 65535 ? along : 65535));
+    const FDiv fd = make_fdiv((uint32_t)c.D);
+    if (lg >= 6)
+        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true>), grid, dim3(kThreads), 0, st, c, lg, fd);
+    else
+        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                     float zv[8];
                     load8<DT>(z, t + q, len, zv);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) out[i] *= zv[i] * logistic(zv[i]);
+                    for (int i = 0; i < 8; ++i) out[i] *= zv[i] * logistic_for<DT>(zv[i]);
                 }
                 store8<DT>(y, t + q, s.L, out);
             }
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
     for (int m = 1; m < PER; m <<= 1) v += __shfl_xor(v, m);
     if (sub == 0) {
         v = s.D_skip ? __builtin_fmaf(s.D_skip[d], x, v) : v;
-        *yo = Elem<DT>::put(s.z.data ? v * (z * logistic(z)) : v);
+        *yo = Elem<DT>::put(s.z.data ? v * (z * logistic_for<DT>(z)) : v);
     }
 }
 
