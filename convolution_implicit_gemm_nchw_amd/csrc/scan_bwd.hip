@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     widen8<DT>(rz, zv);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float sg = logistic(zv[i]);
+                        const float sg = logistic_for<DT>(zv[i]);
                         zslope[i] = e[i] * (sg * __builtin_fmaf(zv[i], 1.0f - sg, 1.0f));
                         e[i] *= zv[i] * sg;
                     }
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                 float slope[8];
                 widen8<DT>(od, slope);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) slope[i] = t + i >= len ? 0.0f : s.softplus ? logistic(slope[i] + bias) : 1.0f;
+                for (int i = 0; i < 8; ++i) slope[i] = t + i >= len ? 0.0f : s.softplus ? logistic_for<DT>(slope[i] + bias) : 1.0f;
                 get_steps(m.dt, wave, lane, dt);
                 get_steps(m.e, wave, lane, e);
                 widen8<DT>(ox, xv);

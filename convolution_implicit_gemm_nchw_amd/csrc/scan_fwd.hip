@@ -68,7 +68,8 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
         }
         wave_lds_sync();
     }
-    for (int t0 = 0; t0 < s.L; t0 += kT) {
+    int t0 = 0;
+    for (; t0 < len; t0 += kT) {
         const int c = t0 / kScanChunk, t = t0 + sub * ITEMS;
         float xv[ITEMS], dt[ITEMS], v[ITEMS], sum = 0.0f;
 #pragma unroll
@@ -160,7 +161,18 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
             }
         }
     }
-    if (LANES == 64 && s.final_state && live && lane < s.N) s.final_state[row * s.N + lane] = carried;
+    if (!live) return;
+    if (LANES == 64 && s.final_state && lane < s.N) s.final_state[row * s.N + lane] = carried;
+    if (LANES == 16 && s.final_state && len == 0)
+        for (int n = sub; n < s.N; n += LANES)
+            s.final_state[row * s.N + n] = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
+    // chunks past the end: zeros, and the states stay
+    for (int t = t0 + sub * 8; t < s.L; t += LANES * 8) {
+        const float zero[8] = {};
+        store8<DT>(y, t, s.L, zero);
+    }
+    if (LANES == 64 && s.states && lane < s.N)
+        for (int c = t0 / kScanChunk; c < saved; ++c) s.states[(row * saved + c) * s.N + lane] = carried;
 }
 
 // One time step.  Memory bound: 8 bytes per state, read and written once.  PER lanes per

@@ -170,9 +170,11 @@ DEVI float logistic(float v) {
     return v < 0.0f ? e * r : r;
 }
 
-// The logistic function on the way to a value stored in DT's type.  For bf16 the plain
-// exponential serves: its relative error |v| 2^-23 (2^-16 at |v| = 100) stays far below
-// half a step of the store, 2^-9, at half the instructions.  exp(-v) = inf gives 0.
+// The logistic function of gates and slopes, for operands of DT's type.  With bf16 operands
+// the plain exponential serves, at a third of the instructions: its relative error |v| 2^-23
+// stays far below the operands' own half step, 2^-9 (and that of a bf16 result).  In the
+// step size it would not do: there an error is multiplied by the length of the memory.
+// exp(-v) = inf gives 0.
 template <int DT>
 DEVI float logistic_for(float v) {
     if constexpr (DT == 1)
