@@ -30,7 +30,6 @@ fallback path.
 """
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -630,18 +629,19 @@ def convnd_bwd_filter(x, dy, filt, groups=1, pad_lo=None, pad_hi=None, stride=No
 
 # ---------------------------------------------------------------- state-space operators
 #
-# One token's calls are short, so the host side counts: the C structures are packed in one
-# struct.pack each (native alignment is the C layout), an operand is looked at once, and with no
-# stream given the current one is asked for its handle only (a convolution step: 23 -> 9 us).
+# One token's calls take a few microseconds on the device, so their operands are checked and
+# marshalled in C++ (csrc/bind.cpp): a scan step costs 5 us of host time instead of 14 us in Python.
 
 _LL = ctypes.c_longlong
 
 
 class _Rows(ctypes.Structure):
+    """miconv_rows_t."""
     _fields_ = [("data", _VP), ("stride_b", _LL), ("stride_d", _LL)]
 
 
 class _ScanIn(ctypes.Structure):
+    """miconv_scan_in_t."""
     _fields_ = [("data", _VP), ("stride_b", _LL), ("stride_g", _LL), ("stride_n", _LL)]
 
 
@@ -662,11 +662,6 @@ class _Scan(ctypes.Structure):
                 ("d_initial_state", _VP)]
 
 
-_CONV_PACK = struct.Struct("@5i Pqq4P Pqq P Pqq P Pqq 3P").pack
-_SCAN_PACK = struct.Struct("@6i PqqPqqPqq P PqqqPqqq 4P Pqq 2P Pqq P PqqPqqPqq 6P").pack
-assert struct.calcsize("@5i Pqq4P Pqq P Pqq P Pqq 3P") == ctypes.sizeof(_CausalConv)
-assert struct.calcsize("@6i PqqPqqPqq P PqqqPqqq 4P Pqq 2P Pqq P PqqPqqPqq 6P") == ctypes.sizeof(_Scan)
-
 _SZP = ctypes.POINTER(_SZ)
 for _name, _args in {
         "causal_conv1d_fwd": [_VP, _I, _VP],
@@ -685,91 +680,20 @@ for _name, _args in {
     _fn.argtypes = _args
     _fn.restype = _I
 
-_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_bind_path = os.path.join(_HERE, "_miconv_bind.so")
+if not os.path.exists(_bind_path):
+    raise ImportError(f"{_bind_path} is not built; run `python convolution_implicit_gemm_nchw_amd/build.py`.")
+from . import _miconv_bind as _bind  # noqa: E402
+
+_bind.errors(_check, torch.OutOfMemoryError)
 
 
-def _misfit(name, t, shape, dtype, dev):
-    if not torch.is_tensor(t):
-        raise ValueError(f"{name} must be a tensor")
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {dev}, not "
-                     f"{t.dtype} of {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
-
-
-def _packed(name, t, shape, dtype, dev):
-    """Address of a contiguous tensor of this shape, type and device; raises on any other."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
-            or not t.is_contiguous()):
-        _misfit(name, t, shape, dtype, dev)
-    return t.data_ptr()
-
-
-def _optional(name, t, shape, dtype, dev):
-    return 0 if t is None else _packed(name, t, shape, dtype, dev)
-
-
-def _rows(name, t, shape, dtype, dev):
-    """(address, batch stride, channel stride) of a [B, D, L] or [B, D] tensor, a view with contiguous
-    time steps as it may be; zeros for None."""
-    if t is None:
-        return 0, 0, 0
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _misfit(name, t, shape, dtype, dev)
-    st = t.stride()
-    if len(st) == 3 and st[2] != 1 and shape[2] > 1:
-        raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
-    return t.data_ptr(), st[0], st[1]
-
-
-def _activation(name, t, ndim):
-    """(dtype code, dtype, device index) of an operator's leading operand."""
-    if not isinstance(t, torch.Tensor) or t.dim() != ndim or not t.is_cuda:
-        raise ValueError(f"{name} must be a {ndim}-dimensional device tensor")
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {t.dtype}; expected float32 or bfloat16")
-    return code, t.dtype, t.get_device()
-
-
-# the current stream's hipStream_t of a device
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _new(shape, dtype, like, stream):
-    """A tensor from the pool of the stream that writes it."""
+def _call(fn, stream, *args):
+    """fn(*args) with `stream` current: kernels run, and new tensors are allocated, on it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return fn(*args)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
-
-
-def _scratch(need, workspace, like, stream):
-    """(pointer, bytes, owner): the caller's workspace tensor or one from the stream's pool."""
-    if workspace is not None:
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    if need == 0:
-        return None, 0, None
-    ws = _new((need,), torch.uint8, like, stream)
-    return ws.data_ptr(), need, ws
-
-
-_current_device = torch._C._cuda_getDevice
-
-
-def _run(name, dev, stream, fn, *args):
-    """fn(*args, stream handle) with the operands' device current."""
-    if _current_device() == dev:
-        status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if status:
-        _check(status, name)
-
-
-def _taps(w):
-    if not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError("w must be [D, K]")
-    return w.shape[1]
+        return fn(*args)
 
 
 def causal_conv1d_fwd(x, w, bias=None, silu=False, initial_state=None, lengths=None, y=None, final_state=None,
@@ -778,118 +702,27 @@ def causal_conv1d_fwd(x, w, bias=None, silu=False, initial_state=None, lengths=N
     [B, D, K-1] before the first step (zeros without).  x [B, D, L] may be a view with contiguous
     time steps; w [D, K], K <= 8, in x's dtype; bias fp32.  lengths (int32 [B]) are the valid steps of
     right-padded sequences; y is 0 past them.  final_state [B, D, K-1], when given, is written."""
-    code, dt, dev = _activation("x", x, 3)
-    shape, K = x.shape, _taps(w)
-    B, D, L = shape
-    held = (B, D, K - 1)
-    if y is None:
-        y = _new(shape, dt, x, stream)
-    c = _CONV_PACK(B, D, L, K, bool(silu), *_rows("x", x, shape, dt, dev), _packed("w", w, (D, K), dt, dev),
-                   _optional("bias", bias, (D,), torch.float32, dev),
-                   _optional("initial_state", initial_state, held, dt, dev),
-                   _optional("lengths", lengths, (B,), torch.int32, dev), *_rows("y", y, shape, dt, dev),
-                   _optional("final_state", final_state, held, dt, dev), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _run("causal_conv1d_fwd", dev, stream, _lib.causal_conv1d_fwd, c, code)
-    return y
+    return _call(_bind.causal_conv1d_fwd, stream, x, w, bias, silu, initial_state, lengths, y, final_state)
 
 
 def causal_conv1d_bwd(x, w, dy, bias=None, silu=False, initial_state=None, lengths=None, d_final_state=None,
                       dx=None, dw=None, dbias=None, d_initial_state=None, workspace=None, stream=None):
     """(dx, dw, dbias) of causal_conv1d_fwd for the output gradient dy (and d_final_state): dx in x's
     dtype, dw [D, K] and dbias [D] fp32 (None without a bias).  d_initial_state, when given, is written."""
-    code, dt, dev = _activation("x", x, 3)
-    shape, K, f32 = x.shape, _taps(w), torch.float32
-    B, D, L = shape
-    held = (B, D, K - 1)
-    if dx is None:
-        dx = _new(shape, dt, x, stream)
-    if dw is None:
-        dw = _new((D, K), f32, x, stream)
-    if bias is not None and dbias is None:
-        dbias = _new((D,), f32, x, stream)
-    c = _CONV_PACK(B, D, L, K, bool(silu), *_rows("x", x, shape, dt, dev), _packed("w", w, (D, K), dt, dev),
-                   _optional("bias", bias, (D,), f32, dev), _optional("initial_state", initial_state, held, dt, dev),
-                   _optional("lengths", lengths, (B,), torch.int32, dev), 0, 0, 0, 0, *_rows("dy", dy, shape, dt, dev),
-                   _optional("d_final_state", d_final_state, held, dt, dev), *_rows("dx", dx, shape, dt, dev),
-                   _packed("dw", dw, (D, K), f32, dev), _optional("dbias", dbias, (D,), f32, dev),
-                   _optional("d_initial_state", d_initial_state, held, dt, dev))
-    need = _SZ(0)
-    if workspace is None:
-        _check(_lib.causal_conv1d_bwd_workspace_size(c, code, MAX_WORKSPACE_BYTES, need),
-               "causal_conv1d_bwd_workspace_size")
-    wp, wb, _keep = _scratch(need.value, workspace, x, stream)
-    _run("causal_conv1d_bwd", dev, stream, _lib.causal_conv1d_bwd, c, code, wp, wb)
-    return dx, dw, dbias
-
-
-def _slots(state, slots, B, dev):
-    """(number of states, address of the slot of each sequence)."""
-    if not isinstance(state, torch.Tensor) or state.dim() != 3:
-        raise ValueError("state must have 3 dimensions")
-    if slots is None and state.shape[0] != B:
-        raise ValueError("without slots, state must hold one state for each sequence")
-    return state.shape[0], None if slots is None else _packed("slots", slots, (B,), torch.int32, dev)
+    return _call(_bind.causal_conv1d_bwd, stream, x, w, bias, silu, initial_state, lengths, dy, d_final_state, dx, dw,
+                 dbias, d_initial_state, workspace)
 
 
 def causal_conv1d_step(x, state, w, bias=None, silu=False, state_out=None, slots=None, y=None, stream=None):
     """One time step of causal_conv1d_fwd: x [B, D], state [B, D, K-1] (updated in place, or written to
     state_out) -> y [B, D].  With slots (int32 [B]) state is a pool [S, D, K-1] and sequence b uses
     state slots[b]; an index outside the pool marks an unused row (y = 0)."""
-    code, dt, dev = _activation("x", x, 2)
-    shape, K = x.shape, _taps(w)
-    B, D = shape
-    S, sp = _slots(state, slots, B, dev)
-    held = (S, D, K - 1)
-    if y is None:
-        y = _new(shape, dt, x, stream)
-    sin = _packed("state", state, held, dt, dev)
-    _run("causal_conv1d_step", dev, stream, _lib.causal_conv1d_step, B, D, K, bool(silu), code,
-         _Rows(*_rows("x", x, shape, dt, dev)), sin, S, sp, _packed("w", w, (D, K), dt, dev),
-         _optional("bias", bias, (D,), torch.float32, dev),
-         sin if state_out is None else _packed("state_out", state_out, held, dt, dev),
-         _Rows(*_rows("y", y, shape, dt, dev)))
-    return y
-
-
-def _scan_in(name, t, shape, dtype, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _misfit(name, t, shape, dtype, dev)
-    st = t.stride()
-    if len(st) == 4 and st[3] != 1 and shape[3] > 1:
-        raise ValueError(f"{name} must have contiguous time steps (stride 1 along the last axis)")
-    return t.data_ptr(), st[0], st[1], st[2]
-
-
-def _scan_common(x, delta, A, Bm, Cm, D, z, delta_bias, softplus, initial_state, lengths, step=False):
-    """(the leading fields of miconv_scan_t, [B, D, L, N, G], dtype code, dtype, device index)."""
-    code, dt, dev = _activation("x", x, 2 if step else 3)
-    shape, f32 = x.shape, torch.float32
-    nb, nd = shape[0], shape[1]
-    if (not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(Bm, torch.Tensor)
-            or Bm.dim() != (3 if step else 4)):
-        raise ValueError("A must be [D, N], B and C [B, G, N, L] ([B, G, N] for one step)")
-    N, G = A.shape[1], Bm.shape[1]
-    L = 1 if step else shape[2]
-    bc = (nb, G, N) if step else (nb, G, N, L)
-    f = (nb, nd, L, N, G, bool(softplus), *_rows("x", x, shape, dt, dev), *_rows("delta", delta, shape, dt, dev),
-         *_rows("z", z, shape, dt, dev), _packed("A", A, (nd, N), f32, dev), *_scan_in("B", Bm, bc, dt, dev),
-         *_scan_in("C", Cm, bc, dt, dev), _optional("D", D, (nd,), f32, dev),
-         _optional("delta_bias", delta_bias, (nd,), f32, dev),
-         _optional("initial_state", initial_state, (nb, nd, N), f32, dev),
-         _optional("lengths", lengths, (nb,), torch.int32, dev))
-    return f, (nb, nd, L, N, G), code, dt, dev
-
-
-def _states_count(x, A):
-    need = _SZ(0)
-    _check(_lib.selective_scan_states_size(x.shape[0], x.shape[1], x.shape[2], A.shape[1], need),
-           "selective_scan_states_size")
-    return need.value // 4
+    return _call(_bind.causal_conv1d_step, stream, x, state, w, bias, silu, state_out, slots, y)
 
 
 def selective_scan_states(x, A, stream=None):
     """A buffer for the states that selective_scan_fwd saves for selective_scan_bwd."""
-    return _new((_states_count(x, A),), torch.float32, x, stream)
+    return _call(_bind.selective_scan_states, stream, x, A)
 
 
 def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=False, initial_state=None,
@@ -900,16 +733,8 @@ def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softp
     (channel d reads group d // (D // G)), D and delta_bias fp32, initial_state [B, D, N] fp32.  lengths
     as in causal_conv1d_fwd.  final_state [B, D, N] and states (selective_scan_states), when given, are
     written."""
-    f, (nb, nd, L, N, G), code, dt, dev = _scan_common(x, delta, A, B, C, D, z, delta_bias, softplus, initial_state,
-                                                       lengths)
-    if y is None:
-        y = _new(x.shape, dt, x, stream)
-    s = _SCAN_PACK(*f, *_rows("y", y, x.shape, dt, dev),
-                   _optional("final_state", final_state, (nb, nd, N), torch.float32, dev),
-                   0 if states is None else _packed("states", states, (_states_count(x, A),), torch.float32, dev),
-                   0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _run("selective_scan_fwd", dev, stream, _lib.selective_scan_fwd, s, code)
-    return y
+    return _call(_bind.selective_scan_fwd, stream, x, delta, A, B, C, D, z, delta_bias, softplus, lengths,
+                 initial_state, y, final_state, states)
 
 
 def selective_scan_bwd(x, delta, A, B, C, dy, states, D=None, z=None, delta_bias=None, softplus=False, lengths=None,
@@ -919,44 +744,17 @@ def selective_scan_bwd(x, delta, A, B, C, dy, states, D=None, z=None, delta_bias
     the forward pass saved for the same operands.  A dict of dx, ddelta, dz (x's dtype; dx, ddelta and dz
     may be given, as views too) and dA, dB, dC, dD, ddelta_bias (fp32, B and C packed), None where the
     operand is absent.  d_initial_state [B, D, N], when given, is written."""
-    f, (nb, nd, L, N, G), code, dt, dev = _scan_common(x, delta, A, B, C, D, z, delta_bias, softplus, None, lengths)
-    shape, f32 = x.shape, torch.float32
-    if states is None:
-        raise ValueError("states of the forward pass are needed")
-    r = {"dx": _new(shape, dt, x, stream) if dx is None else dx,
-         "ddelta": _new(shape, dt, x, stream) if ddelta is None else ddelta,
-         "dz": None if z is None else _new(shape, dt, x, stream) if dz is None else dz,
-         "dA": _new((nd, N), f32, x, stream), "dB": _new((nb, G, N, L), f32, x, stream),
-         "dC": _new((nb, G, N, L), f32, x, stream), "dD": None if D is None else _new((nd,), f32, x, stream),
-         "ddelta_bias": None if delta_bias is None else _new((nd,), f32, x, stream)}
-    s = _SCAN_PACK(*f, 0, 0, 0, 0, _packed("states", states, (_states_count(x, A),), f32, dev),
-                   *_rows("dy", dy, shape, dt, dev), _optional("d_final_state", d_final_state, (nb, nd, N), f32, dev),
-                   *_rows("dx", r["dx"], shape, dt, dev), *_rows("ddelta", r["ddelta"], shape, dt, dev),
-                   *_rows("dz", r["dz"], shape, dt, dev), r["dA"].data_ptr(), r["dB"].data_ptr(), r["dC"].data_ptr(),
-                   0 if D is None else r["dD"].data_ptr(), 0 if delta_bias is None else r["ddelta_bias"].data_ptr(),
-                   _optional("d_initial_state", d_initial_state, (nb, nd, N), f32, dev))
-    need = _SZ(0)
-    if workspace is None:
-        _check(_lib.selective_scan_bwd_workspace_size(s, code, need), "selective_scan_bwd_workspace_size")
-    wp, wb, _keep = _scratch(need.value, workspace, x, stream)
-    _run("selective_scan_bwd", dev, stream, _lib.selective_scan_bwd, s, code, wp, wb)
-    return r
+    return dict(zip(("dx", "ddelta", "dz", "dA", "dB", "dC", "dD", "ddelta_bias"),
+                    _call(_bind.selective_scan_bwd, stream, x, delta, A, B, C, D, z, delta_bias, softplus, lengths, dy,
+                          states, d_final_state, d_initial_state, dx, ddelta, dz, workspace)))
 
 
 def selective_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=None, softplus=False, state_out=None,
                         slots=None, y=None, stream=None):
     """One time step of selective_scan_fwd: x, delta, z [B, D], B, C [B, G, N], state [B, D, N] fp32 (updated
     in place, or written to state_out) -> y [B, D].  slots as in causal_conv1d_step."""
-    f, (nb, nd, _, N, G), code, dt, dev = _scan_common(x, delta, A, B, C, D, z, delta_bias, softplus, None, None,
-                                                       step=True)
-    S, sp = _slots(state, slots, nb, dev)
-    if y is None:
-        y = _new(x.shape, dt, x, stream)
-    s = _SCAN_PACK(*f, *_rows("y", y, x.shape, dt, dev), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    sin = _packed("state", state, (S, nd, N), torch.float32, dev)
-    _run("selective_scan_step", dev, stream, _lib.selective_scan_step, s, code, sin, S, sp,
-         sin if state_out is None else _packed("state_out", state_out, (S, nd, N), torch.float32, dev))
-    return y
+    return _call(_bind.selective_scan_step, stream, x, delta, A, B, C, D, z, delta_bias, softplus, None, state,
+                 state_out, slots, y)
 
 
 I8_PAD = 128
@@ -968,28 +766,7 @@ def quantize_tokens(x, channel_major=False, q=None, scale=None, stream=None):
     steps.  Returns q [tokens, C_pad] int8 (C_pad = C rounded up to 128, zeros past C) and scale [tokens]
     fp32; tokens run over [B, L] in that order.  A token with an infinity or NaN gets a NaN scale.  A
     weight [O, C] is quantised by channel in the same way."""
-    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3) or (channel_major and x.dim() != 3):
-        raise ValueError("x must be [T, C] or [B, L, C], or [B, C, L] when channel-major")
-    code, dt, dev = _activation("x", x, x.dim())
-    shape, st = x.shape, x.stride()
-    if channel_major:
-        (nb, C, L), (sb, sc, sl) = shape, st
-        if L > 1 and sl != 1:
-            raise ValueError("x must have contiguous time steps (stride 1 along the last axis)")
-        sl = 1
-    else:
-        C, sc = shape[-1], 1
-        if C > 1 and st[-1] != 1:
-            raise ValueError("x must have contiguous channels (stride 1 along the last axis)")
-        nb, L, sb, sl = (shape[0], shape[1], st[0], st[1]) if len(shape) == 3 else (1, shape[0], 0, st[0])
-    held = (nb * L, -(-C // I8_PAD) * I8_PAD)
-    if q is None:
-        q = _new(held, torch.int8, x, stream)
-    if scale is None:
-        scale = _new((nb * L,), torch.float32, x, stream)
-    _run("quantize_tokens", dev, stream, _lib.quantize_tokens, nb, L, C, code, x.data_ptr(), sb, sl, sc,
-         _packed("q", q, held, torch.int8, dev), _packed("scale", scale, (nb * L,), torch.float32, dev))
-    return q, scale
+    return _call(_bind.quantize_tokens, stream, x, channel_major, q, scale)
 
 
 def matmul_i8(q, scale, wq, wscale, bias=None, out_dtype=torch.float32, length=None, y=None, workspace=None,
@@ -997,25 +774,6 @@ def matmul_i8(q, scale, wq, wscale, bias=None, out_dtype=torch.float32, length=N
     """y[m, n] = scale[m] wscale[n] sum_k q[m, k] wq[n, k] (+ bias[n]), the sum exact in 32-bit integers.
     q [T, C_pad] and wq [O, C_pad] int8 with scales as quantize_tokens gives them, bias fp32 [O].  y is
     [T, O], or with `length` = L channel-major [T / L, O, L]; fp32 or bf16 (y's dtype, or out_dtype)."""
-    for name, t in (("q", q), ("wq", wq)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
-            raise ValueError(f"{name} must be a 2-dimensional device tensor")
-    (T, pad), O, dev, f32, i8 = q.shape, wq.shape[0], q.get_device(), torch.float32, torch.int8
-    if length is not None and (length < 1 or T % length):
-        raise ValueError("length must divide the number of tokens")
-    nb, L = (1, T) if length is None else (T // length, length)
-    shape = (T, O) if length is None else (nb, O, L)
-    code = _CODES.get(out_dtype if y is None else y.dtype)
-    if code is None:
-        raise ValueError("unsupported output dtype; expected float32 or bfloat16")
-    if y is None:
-        y = _new(shape, out_dtype, q, stream)
-    need = _SZ(0)
-    if workspace is None:
-        _check(_lib.matmul_i8_workspace_size(nb, L, O, pad, MAX_WORKSPACE_BYTES, need), "matmul_i8_workspace_size")
-    wp, wb, _keep = _scratch(need.value, workspace, q, stream)
-    _run("matmul_i8", dev, stream, _lib.matmul_i8, nb, L, O, pad, _packed("q", q, (T, pad), i8, dev),
-         _packed("scale", scale, (T,), f32, dev), _packed("wq", wq, (O, pad), i8, dev),
-         _packed("wscale", wscale, (O,), f32, dev), _optional("bias", bias, (O,), f32, dev), length is not None, code,
-         _packed("y", y, shape, y.dtype, dev), wp, wb)
-    return y
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported dtype {out_dtype}; expected float32 or bfloat16")
+    return _call(_bind.matmul_i8, stream, q, scale, wq, wscale, bias, out_dtype is torch.bfloat16, length, y, workspace)

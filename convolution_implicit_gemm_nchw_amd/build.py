@@ -1,4 +1,5 @@
-"""Build the HIP library ``libmiconv.so`` in-tree with hipcc for gfx950.
+"""Build the HIP library ``libmiconv.so`` in-tree with hipcc for gfx950, and the binding module of
+its state-space operators, ``_miconv_bind.so``, against torch's headers.
 
 Always recompiles.  Objects are compiled in parallel, then linked into one
 shared library next to this file.  Packed-fp32 VALU instructions are disabled
@@ -16,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmiconv.so")
+BIND = os.path.join(HERE, "_miconv_bind.so")
 SOURCES = ["igemm.hip", "patch.hip", "bwdf16.hip", "pointwise.hip", "tinyc.hip", "noalloc.hip", "bwd_bias.hip",
            "convnd.hip", "causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip",
            "plan.cpp", "ndplan.cpp", "abi.cpp", "ssm_abi.cpp"]
@@ -34,6 +36,20 @@ def compile_flags():
     return ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
+
+
+def bind_command(out):
+    """The host compiler's line for the binding module (it links the library next to it)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    includes = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                os.path.join(ROCM, "include"), sysconfig.get_paths()["include"]]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + i for i in includes] +
+            [os.path.join(CSRC, "bind.cpp"), "-o", out, "-L" + HERE, "-l:libmiconv.so", "-L" + os.path.join(base, "lib"),
+             "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 
 _REMARK = re.compile(r"remark: .*?(Function Name|ScratchSize \[bytes/lane\]): (\S+)")
@@ -93,6 +109,12 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp_lib, LIB)
+    tmp_bind = BIND + ".tmp"
+    cmd = bind_command(tmp_bind)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp_bind, BIND)
     return LIB
 
 
