@@ -93,17 +93,17 @@ DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8],
 //
 // A work-group of WC x WR waves computes a (WC*FC*32) x (WR*FR*32) tile, a wave
 // FC x FR blocks of 32 x 32.  128 bytes of k of every row of the tile are brought
-// into LDS at a time, straight from memory (no registers in between), two stages
-// in turn: the next stage loads while this one is multiplied.  A row's eight
+// into LDS at a time, straight from memory (no registers in between), ST stages in
+// turn: the next ones load while this one is multiplied.  A row's eight
 // 16-byte pieces are stored at piece ^ (row & 7), so that the 32 rows that one
 // MFMA operand reads spread over all banks; since the load writes LDS in lane
 // order, the lanes fetch the pieces in that order instead.
-template <int WC, int WR, int FC, int FR>
+template <int WC, int WR, int FC, int FR, int ST>
 struct Tile {
     static constexpr int kWaves = WC * WR, kThreads = 64 * kWaves;
     static constexpr int C = WC * FC * 32, R = WR * FR * 32;
     static constexpr int kBytes = (C + R) * 128;
-    static constexpr int kRowsPerLoad = kWaves * 8;
+    static constexpr int kRowsPerLoad = kWaves * 8, kLoads = (C + R) / kRowsPerLoad;   // per wave and stage
 
     struct Src {
         rsrc_t rc, rr;
@@ -156,15 +156,14 @@ struct Tile {
 #pragma unroll
                 for (int j = 0; j < FR; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fc[i], fr[j], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
 };
 
-template <int OD, int WC, int WR, int FC, int FR>
+template <int OD, int WC, int WR, int FC, int FR, int ST>
 __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
-    typedef Tile<WC, WR, FC, FR> X;
-    __shared__ __attribute__((aligned(1024))) char stages[2 * X::kBytes];
+    typedef Tile<WC, WR, FC, FR, ST> X;
+    __shared__ __attribute__((aligned(1024))) char stages[ST * X::kBytes];
     // each XCD a contiguous range of tiles, in columns of eight C tiles: the tiles that
     // run on it together share their operands in its L2
     const int per_split = a.tiles_c * a.tiles_r, split = blockIdx.x / per_split;
@@ -182,7 +181,9 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
     const int first = split * a.k_split, end = first + a.k_split < a.K ? first + a.k_split : a.K;
-    X::load(src, stages, first);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+        if (first + i * 128 < end) X::load(src, stages + i * X::kBytes, first + i * 128);
     // what the epilogue needs from memory: a lane's columns' and one row's scale and bias
     constexpr int kW = FC * 32, kMine = 32 * kW;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wc = wave % WC, wr = wave / WC;
@@ -193,20 +194,25 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
     static_assert(FR <= 2, "one row's scale per lane");
     const int rl = r0 + wr * FR * 32 + lane, rc = rl < a.NR ? rl : a.NR - 1;
     const float rs = a.r_scale[rc], rb = a.r_bias ? a.r_bias[rc] : 0.0f;
-    int now = 0;
+    int now = 0, next = ST - 1;
     for (int k = first; k < end; k += 128) {
-        // this stage has arrived (each wave waits for its own loads; the compiler does not
-        // always tie an LDS load to the reads behind the barrier), the other has been read
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // this stage has arrived (each wave waits for its own loads, of which those of the
+        // ST - 2 stages after it may be in flight; the compiler does not always tie an LDS load
+        // to the reads behind the barrier), and the stage before has been read
+        if (ST > 2 && k + (ST - 2) * 128 < end)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((ST - 2) * X::kLoads) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (k + 128 < end) X::load(src, stages + (X::kBytes - now), k + 128);
-        X::multiply(stages + now, acc);
-        now = X::kBytes - now;
+        if (k + (ST - 1) * 128 < end) X::load(src, stages + next * X::kBytes, k + (ST - 1) * 128);
+        X::multiply(stages + now * X::kBytes, acc);
+        now = now + 1 < ST ? now + 1 : 0;
+        next = next + 1 < ST ? next + 1 : 0;
     }
     __syncthreads();
     // Through LDS, 32 rows of the wave's FC*32 columns at a time, so that y is written
     // in 16-byte pieces of consecutive lanes; a row's pieces are permuted as above.
-    static_assert(X::kWaves * kMine * 4 <= 2 * X::kBytes, "the exchange fits the two stages");
+    static_assert(X::kWaves * kMine * 4 <= ST * X::kBytes, "the exchange fits the stages");
     int *mine = (int *)stages + wave * kMine;
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
@@ -349,14 +355,14 @@ void few(int T, int O, int K, int L, const signed char *q, const float *qs, cons
                        T, O, K, L, channel_major, y);
 }
 
-template <int OD, int WC, int WR, int FC, int FR>
+template <int OD, int WC, int WR, int FC, int FR, int ST>
 int tiled(I8Args a, int splits, hipStream_t st) {
-    typedef Tile<WC, WR, FC, FR> X;
+    typedef Tile<WC, WR, FC, FR, ST> X;
     a.tiles_c = (a.NC + X::C - 1) / X::C;
     a.tiles_r = (a.NR + X::R - 1) / X::R;
     if (splits == 1) a.part = nullptr;
     a.k_split = ((a.K / 128 + splits - 1) / splits) * 128;
-    hipLaunchKernelGGL((i8_tile_kernel<OD, WC, WR, FC, FR>), dim3((unsigned)((long long)a.tiles_c * a.tiles_r * splits)),
+    hipLaunchKernelGGL((i8_tile_kernel<OD, WC, WR, FC, FR, ST>), dim3((unsigned)((long long)a.tiles_c * a.tiles_r * splits)),
                        dim3(X::kThreads), 0, st, a);
     if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
     if (splits > 1) {
@@ -399,9 +405,11 @@ int i8_splits(int T, int O, int K, size_t budget) {
 template <int OD>
 static int i8_by_size(const I8Args &a, int T, int O, int splits, hipStream_t st) {
     switch (tile_side(T, O)) {
-        case 256: return tiled<OD, 2, 4, 4, 2>(a, splits, st);
-        case 128: return tiled<OD, 2, 2, 2, 2>(a, splits, st);
-        default: return tiled<OD, 2, 2, 1, 1>(a, splits, st);
+        // small tiles leave LDS room for four stages, which tall and narrow products (few tiles,
+        // long k) need: 65 tokens, 4096 -> 8192: 17.4 us with two, 12.8 with four
+        case 256: return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
+        case 128: return tiled<OD, 2, 2, 2, 2, 2>(a, splits, st);
+        default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);
     }
 }
 
