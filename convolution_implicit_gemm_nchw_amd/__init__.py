@@ -23,8 +23,12 @@ and the current stream.  The functions carry the C ABI's names
   convnd_fwd / convnd_bwd_data / convnd_bwd_filter  (1-3 spatial dims, groups, dilation,
                                                 asymmetric or "same"/"valid" padding)
   plan_candidates / plan_select / plan_cache_clear / plan_cache_entries   (the plan cache)
+  causal_conv1d_fwd / causal_conv1d_bwd / causal_conv1d_step   short causal depthwise convolution, [B, D, L]
+  selective_scan_fwd / selective_scan_bwd / selective_scan_step (selective_scan_states)   state-space scan
+  quantize_tokens / matmul_i8                   8-bit products with a scale for each token and channel
 
-Inputs must all be float32 or all bfloat16, contiguous, on the current device.
+Inputs must all be float32 or all bfloat16, contiguous, on the current device (the state-space
+operators also take strided rows and say what else differs).
 If the shared library is missing this module raises on import: there is no
 fallback path.
 """
