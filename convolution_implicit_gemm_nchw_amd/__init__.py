@@ -634,7 +634,7 @@ def convnd_bwd_filter(x, dy, filt, groups=1, pad_lo=None, pad_hi=None, stride=No
 # ---------------------------------------------------------------- state-space operators
 #
 # One token's calls take a few microseconds on the device, so their operands are checked and
-# marshalled in C++ (csrc/bind.cpp): a scan step costs 5 us of host time instead of 14 us in Python.
+# marshalled in C++ (csrc_lm/bind.cpp): a scan step costs 5 us of host time instead of 14 us in Python.
 
 _LL = ctypes.c_longlong
 

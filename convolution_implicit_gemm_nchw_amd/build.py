@@ -18,9 +18,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmiconv.so")
 BIND = os.path.join(HERE, "_miconv_bind.so")
+CSRC_LM = os.path.join(HERE, "csrc_lm")   # the state-space operators
 SOURCES = ["igemm.hip", "patch.hip", "bwdf16.hip", "pointwise.hip", "tinyc.hip", "noalloc.hip", "bwd_bias.hip",
-           "convnd.hip", "causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip",
-           "plan.cpp", "ndplan.cpp", "abi.cpp", "ssm_abi.cpp"]
+           "convnd.hip", "plan.cpp", "ndplan.cpp", "abi.cpp"]
+SOURCES_LM = ["causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip", "ssm_abi.cpp"]
 ARCH = "gfx950"
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
@@ -38,6 +39,11 @@ def compile_flags():
             "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 
 
+def sources():
+    """(name, path) of every source of the library."""
+    return [(s, os.path.join(CSRC, s)) for s in SOURCES] + [(s, os.path.join(CSRC_LM, s)) for s in SOURCES_LM]
+
+
 def bind_command(out):
     """The host compiler's line for the binding module (it links the library next to it)."""
     import sysconfig
@@ -48,7 +54,7 @@ def bind_command(out):
                 os.path.join(ROCM, "include"), sysconfig.get_paths()["include"]]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
              "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + i for i in includes] +
-            [os.path.join(CSRC, "bind.cpp"), "-o", out, "-L" + HERE, "-l:libmiconv.so", "-L" + os.path.join(base, "lib"),
+            [os.path.join(CSRC_LM, "bind.cpp"), "-o", out, "-L" + HERE, "-l:libmiconv.so", "-L" + os.path.join(base, "lib"),
              "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 
@@ -74,7 +80,7 @@ def build(verbose: bool = False) -> str:
     hipcc = _hipcc()
     with tempfile.TemporaryDirectory(prefix="miconv_build_") as tmp:
         procs, objs = [], []
-        for src in SOURCES:
+        for src, path in sources():
             obj = os.path.join(tmp, src + ".o")
             if src.endswith(".hip"):
                 cmd = [hipcc] + compile_flags() + ["-Rpass-analysis=kernel-resource-usage", "-x", "hip"]
@@ -82,7 +88,7 @@ def build(verbose: bool = False) -> str:
                 cmd = [hipcc, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__",
                        "-I" + os.path.join(ROCM, "include"), "-I" + os.path.join(ROOT, "include"),
                        "-I" + CSRC]
-            cmd = cmd + ["-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = cmd + ["-c", path, "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
