@@ -672,7 +672,8 @@ for _name, _args in {
         "causal_conv1d_bwd": [_VP, _I, _VP, _SZ, _VP],
         "causal_conv1d_bwd_workspace_size": [_VP, _I, _SZ, _SZP],
         "causal_conv1d_step": [_I, _I, _I, _I, _I, _Rows, _VP, _I, _VP, _VP, _VP, _VP, _Rows, _VP],
-        "selective_scan_fwd": [_VP, _I, _VP],
+        "selective_scan_fwd": [_VP, _I, _VP, _SZ, _VP],
+        "selective_scan_fwd_workspace_size": [_VP, _I, _SZ, _SZP],
         "selective_scan_bwd": [_VP, _I, _VP, _SZ, _VP],
         "selective_scan_states_size": [_I, _I, _I, _I, _SZP],
         "selective_scan_bwd_workspace_size": [_VP, _I, _SZP],
@@ -730,7 +731,7 @@ def selective_scan_states(x, A, stream=None):
 
 
 def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=False, initial_state=None,
-                       lengths=None, y=None, final_state=None, states=None, stream=None):
+                       lengths=None, y=None, final_state=None, states=None, workspace=None, stream=None):
     """Selective state space scan: with dt = softplus(delta + delta_bias),
       h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t x_t B_t[n],  y_t = (sum_n C_t[n] h_t[n] + D x_t) * silu(z_t)
     x, delta, z, y [B, D, L] (views with contiguous time steps), A [D, N] fp32, N <= 64, B, C [B, G, N, L]
@@ -738,7 +739,7 @@ def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, softp
     as in causal_conv1d_fwd.  final_state [B, D, N] and states (selective_scan_states), when given, are
     written."""
     return _call(_bind.selective_scan_fwd, stream, x, delta, A, B, C, D, z, delta_bias, softplus, lengths,
-                 initial_state, y, final_state, states)
+                 initial_state, y, final_state, states, workspace)
 
 
 def selective_scan_bwd(x, delta, A, B, C, dy, states, D=None, z=None, delta_bias=None, softplus=False, lengths=None,

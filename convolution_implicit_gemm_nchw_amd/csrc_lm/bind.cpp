@@ -313,7 +313,7 @@ PyObject *scan_states(Args a) {
     return THPVariable_Wrap(at::empty({n}, x.t.options().dtype(at::kFloat)));
 }
 
-// (..., initial_state, y, final_state, states) -> y
+// (..., initial_state, y, final_state, states, workspace) -> y
 PyObject *scan_fwd(Args a) {
     const Lead x("x", a[0], 3);
     miconv_scan_t s = scan_common(x, a, false);
@@ -323,7 +323,12 @@ PyObject *scan_fwd(Args a) {
     s.final_state = (float *)optional("final_state", a[12], {s.B, s.D, s.N}, at::kFloat, x.dev);
     if (a[13] != Py_None)
         s.states = (float *)packed("states", a[13], {states_count(s.B, s.D, s.L, s.N)}, at::kFloat, x.dev);
-    run("selective_scan_fwd", x.dev, [&](void *st) { return selective_scan_fwd(&s, x.code, st); });
+    size_t need = 0;
+    if (a[14] == Py_None)
+        check(selective_scan_fwd_workspace_size(&s, x.code, MICONV_MAX_WORKSPACE_BYTES, &need),
+              "selective_scan_fwd_workspace_size");
+    const Scratch ws(a[14], need, x);
+    run("selective_scan_fwd", x.dev, [&](void *st) { return selective_scan_fwd(&s, x.code, ws.p, ws.n, st); });
     return y.wrap();
 }
 
@@ -498,7 +503,7 @@ PyMethodDef methods[] = {ENTRY("causal_conv1d_fwd", conv_fwd, 8),
                          ENTRY("causal_conv1d_bwd", conv_bwd, 13),
                          ENTRY("causal_conv1d_step", conv_step, 8),
                          ENTRY("selective_scan_states", scan_states, 2),
-                         ENTRY("selective_scan_fwd", scan_fwd, 14),
+                         ENTRY("selective_scan_fwd", scan_fwd, 15),
                          ENTRY("selective_scan_bwd", scan_bwd, 18),
                          ENTRY("selective_scan_step", scan_step, 14),
                          ENTRY("quantize_tokens", quantize, 4),

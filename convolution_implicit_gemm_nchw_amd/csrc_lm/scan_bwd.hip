@@ -421,17 +421,27 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
 // G at the end of every chunk, for a backward pass whose time segments run side by side:
 // the forward kernel's scan with the lanes in reversed order of time, and no outputs but
 // the values between chunks.  A wave per row, 64 lanes x 16 steps, the work-group's rows
-// sharing C in LDS.
+// sharing C in LDS.  Few rows split this pass too: a wave per row and segment then starts
+// from zero, notes the G that leaves its segment and the sums of dt, and a second kernel
+// adds what comes from the segments after it.
+struct Carry {
+    float *G;                 // [B][D][chunks][N]
+    float *ends, *after;      // [B][D][segs][N + 1] G and sum of dt; [B][D][chunks] dt up to the segment's end
+    int segs, steps;
+};
+
 constexpr int kCarryWaves = 8, kCarryItems = 16, kCarryT = 64 * kCarryItems;
 
 template <int DT>
-__global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(miconv_scan_t s, float *out, int blocks_g) {
+__global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(miconv_scan_t s, Carry out, int blocks_g) {
     typedef typename Elem<DT>::T T;
     constexpr int kStage = 16, kEvery = kT / kCarryItems;
     __shared__ __attribute__((aligned(16))) float cs[kStage][kCarryT];     // [ITEMS / 4][lane][4]
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int per_group = s.D / s.G;
-    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g, g = bg % s.G, b = bg / s.G;
+    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g % (s.B * s.G), g = bg % s.G, b = bg / s.G;
+    const int seg = blockIdx.x / (blocks_g * s.B * s.G), start = seg * out.steps;
+    const int stop = out.segs == 1 || s.L - start < out.steps ? s.L : start + out.steps;
     const int in_group = blk * kCarryWaves + wave;
     const bool live = in_group < per_group;
     const int d = g * per_group + (live ? in_group : 0);
@@ -443,10 +453,11 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
     const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
     float carried = 0.0f, a_lane = 0.0f;               // lane n: state n
     if (lane < s.N) {
-        if (s.d_final_state) carried = s.d_final_state[row * s.N + lane];
+        if (s.d_final_state && out.segs == 1) carried = s.d_final_state[row * s.N + lane];
         a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
     }
-    for (int t0 = (s.L - 1) / kCarryT * kCarryT; t0 >= 0; t0 -= kCarryT) {
+    float later = 0.0f;                                // dt from the chunk's end to the segment's
+    for (int t0 = start + (stop - 1 - start) / kCarryT * kCarryT; t0 >= start; t0 -= kCarryT) {
         const int t = t0 + (63 - lane) * kCarryItems;
         float dt[kCarryItems], e[kCarryItems], sum = 0.0f;
 #pragma unroll
@@ -467,6 +478,10 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
             sum += dt[i];
         }
         const Sums sums = prefix_sums(sum);
+        const int ends_here = t0 / kT + (64 - lane) / kEvery - 1;      // the chunk that ends where this lane begins
+        const bool saves = live && lane % kEvery == 0 && ends_here * kT < stop;
+        if (out.segs > 1 && saves) out.after[row * chunks + ends_here] = later + (sums.all - sum);
+        later += lane_of(sums.all, 63);
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
             const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
             __syncthreads();
@@ -493,14 +508,39 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
                 G = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(G), G);
                 G = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(G), G);
                 const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), G0, G);
-                carried = lane == n ? lane_of(end, 63) : carried;
+                carried = keep(carried, end, n);
                 G = cross_or<kWaveShr1>(G0, end);
-                const int c = t0 / kT + (64 - lane) / kEvery - 1;      // the chunk that ends where this lane begins
-                if (live && lane % kEvery == 0 && c < chunks) out[(row * chunks + c) * s.N + n] = G;
+                if (saves) out.G[(row * chunks + ends_here) * s.N + n] = G;
             }
         }
     }
+    if (out.segs > 1 && live) {
+        float *to = out.ends + (row * out.segs + seg) * (s.N + 1);
+        if (lane < s.N) to[lane] = carried;
+        if (lane == 0) to[s.N] = later;
+    }
 }
+
+// G at every chunk's end: what the segment found plus what enters it from the right.  A
+// thread per row and state, from the last segment to the first.
+__global__ __launch_bounds__(256) void scan_bwd_chain_kernel(miconv_scan_t s, Carry out) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (long long)s.B * s.D * s.N) return;
+    const long long row = i / s.N;
+    const int n = (int)(i - row * s.N), d = (int)(row % s.D), chunks = (s.L + kT - 1) / kT, per = out.steps / kT;
+    const float a2 = s.A[(long long)d * s.N + n] * kLog2e;
+    float G = s.d_final_state ? s.d_final_state[i] : 0.0f;
+    for (int seg = out.segs - 1; seg >= 0; --seg) {
+        const int last = (seg + 1) * per < chunks ? (seg + 1) * per : chunks;
+        for (int c = seg * per; c < last; ++c) {
+            float *at = out.G + (row * chunks + c) * s.N + n;
+            *at = __builtin_fmaf(exp2_hw(a2 * out.after[row * chunks + c]), G, *at);
+        }
+        const float *end = out.ends + (row * out.segs + seg) * (s.N + 1);
+        G = __builtin_fmaf(exp2_hw(a2 * end[s.N]), G, end[n]);
+    }
+}
+
 
 // out[i] = sum over p of part[p][i] for several arrays: a work-group takes 256 consecutive i,
 // a wave a quarter of the parts (four i per lane, so every load is 16 bytes next to its
@@ -570,8 +610,21 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     p.off_dA = 2 * bc;
     p.off_dD = p.off_dA + bd * s.N * p.segs;
     p.off_db = p.off_dD + bd * p.segs;
+    // the pass between the segments is split as the forward scan is
+    const long long rows_groups = (long long)s.B * s.G * ((s.D / s.G + kCarryWaves - 1) / kCarryWaves);
+    const int long_chunks = (s.L + kCarryT - 1) / kCarryT;
+    p.carry_segs = 1;
+    p.carry_steps = 0;
+    if (p.segs > 1 && rows_groups <= 128 && long_chunks >= 3) {
+        const long long n = 512 / rows_groups < long_chunks ? 512 / rows_groups : long_chunks;
+        const int per = (int)((long_chunks + n - 1) / n);
+        p.carry_segs = (long_chunks + per - 1) / per;
+        p.carry_steps = per * kCarryT;
+    }
     p.off_G = p.off_db + bd * p.segs;
-    p.off_sums = p.off_G + (p.segs > 1 ? bd * chunks * s.N : 0);
+    p.off_ends = p.off_G + (p.segs > 1 ? bd * chunks * s.N : 0);
+    p.off_after = p.off_ends + (p.carry_segs > 1 ? bd * p.carry_segs * (s.N + 1) : 0);
+    p.off_sums = p.off_after + (p.carry_segs > 1 ? bd * chunks : 0);
     p.bytes = (p.off_sums + (s.N > kStates ? 3 * bd * s.L : 0)) * 4;
     return p;
 }
@@ -591,11 +644,15 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     o.seg_chunks = p.seg_chunks;
     if (p.segs > 1) {
         const int blocks_g = (s.D / s.G + kCarryWaves - 1) / kCarryWaves;
-        const dim3 cgrid((unsigned)((long long)s.B * s.G * blocks_g)), cblock(64 * kCarryWaves);
+        const Carry out = {ws + p.off_G, ws + p.off_ends, ws + p.off_after, p.carry_segs, p.carry_steps};
+        const dim3 cgrid((unsigned)((long long)s.B * s.G * blocks_g * p.carry_segs)), cblock(64 * kCarryWaves);
         if (dtype)
-            hipLaunchKernelGGL(scan_bwd_carry_kernel<1>, cgrid, cblock, 0, st, s, ws + p.off_G, blocks_g);
+            hipLaunchKernelGGL(scan_bwd_carry_kernel<1>, cgrid, cblock, 0, st, s, out, blocks_g);
         else
-            hipLaunchKernelGGL(scan_bwd_carry_kernel<0>, cgrid, cblock, 0, st, s, ws + p.off_G, blocks_g);
+            hipLaunchKernelGGL(scan_bwd_carry_kernel<0>, cgrid, cblock, 0, st, s, out, blocks_g);
+        if (p.carry_segs > 1)
+            hipLaunchKernelGGL(scan_bwd_chain_kernel, dim3((unsigned)(((long long)s.B * s.D * s.N + 255) / 256)), dim3(256),
+                               0, st, s, out);
         if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
     }
     const dim3 grid((unsigned)((long long)s.B * s.G * p.parts * p.segs));

@@ -24,21 +24,25 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Work-groups of 8 waves; 64 lanes x 16 or 8 steps per row, or, for short rows, four rows
-// of 16 lanes x 8 steps per wave (then the row is a single chunk).
+// Work-groups of 8 waves; 64 lanes x 16 or 8 steps per row, or four rows of 16 lanes x 8 or
+// 16 steps per wave.
 constexpr int kScanWaves = 8;
 
 template <int DT, int LANES, int ITEMS>
-__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g) {
+__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g, ScanSplit split) {
     typedef typename Elem<DT>::T T;
     constexpr int kT = LANES * ITEMS, kRows = 64 / LANES, kEvery = kScanChunk / ITEMS, kPairs = kT * 2 * 4;   // bytes of B and C per state
     constexpr int kStage = 65536 / kPairs < 16 ? 65536 / kPairs : 16;            // states staged at a time
     // [state][B, C][ITEMS / 4][LANES][4]: a lane reads four steps as 16 bytes next to its neighbours'
     __shared__ __attribute__((aligned(16))) float bc[kStage * 2 * kT];
-    __shared__ float a_rows[LANES == 16 ? kScanWaves * kRows * MICONV_SCAN_MAX_STATES : 1];
+    // 16 lanes per row: A[n] log2(e) and the state n between chunks, of each row
+    __shared__ float a_rows[LANES == 16 ? kScanWaves * kRows : 1][MICONV_SCAN_MAX_STATES];
+    __shared__ float h_rows[LANES == 16 ? kScanWaves * kRows : 1][MICONV_SCAN_MAX_STATES];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), sub = lane % LANES;
     const int per_group = s.D / s.G;
-    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g, g = bg % s.G, b = bg / s.G;
+    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g % (s.B * s.G), g = bg % s.G, b = bg / s.G;
+    const int seg = blockIdx.x / (blocks_g * s.B * s.G), start = seg * split.steps;
+    const int stop = split.segs == 1 || s.L - start < split.steps ? s.L : start + split.steps;
     const int in_group = (blk * kScanWaves + wave) * kRows + lane / LANES;
     const bool live = in_group < per_group;              // the last work-group's other rows only help to stage
     const int d = g * per_group + (live ? in_group : 0);
@@ -52,24 +56,26 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
     const float skip = s.D_skip ? s.D_skip[d] : 0.0f, bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
     const int saved = scan_chunks(s.L);
-    // 64 lanes per row: lane n holds the state n between chunks and A[n] log2(e).  16 lanes:
-    // one chunk, so states come from and go to memory; A in LDS.
+    // 64 lanes per row: lane n holds them for state n
+    const int my = LANES == 16 ? wave * kRows + lane / LANES : 0;
     float carried = 0.0f, a_lane = 0.0f;
     if constexpr (LANES == 64) {
         if (lane < s.N) {
-            if (s.initial_state) carried = s.initial_state[row * s.N + lane];
+            if (split.segs > 1)
+                carried = split.entry[(row * split.segs + seg) * s.N + lane];
+            else if (s.initial_state)
+                carried = s.initial_state[row * s.N + lane];
             a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
         }
     } else {
         for (int n = sub; n < s.N; n += LANES) {
-            const float h0 = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
-            if (live && s.states) s.states[row * s.N + n] = h0;
-            a_rows[(wave * kRows + lane / LANES) * MICONV_SCAN_MAX_STATES + n] = s.A[(long long)d * s.N + n] * kLog2e;
+            h_rows[my][n] = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
+            a_rows[my][n] = s.A[(long long)d * s.N + n] * kLog2e;
         }
         wave_lds_sync();
     }
-    int t0 = 0;
-    for (; t0 < len; t0 += kT) {
+    int t0 = start;
+    for (; t0 < len && t0 < stop; t0 += kT) {
         const int c = t0 / kScanChunk, t = t0 + sub * ITEMS;
         float xv[ITEMS], dt[ITEMS], v[ITEMS], sum = 0.0f;
 #pragma unroll
@@ -105,8 +111,8 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                     a2 = lane_of(a_lane, n);
                     h0 = lane_of(carried, n);
                 } else {
-                    a2 = a_rows[(wave * kRows + lane / LANES) * MICONV_SCAN_MAX_STATES + n];
-                    h0 = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
+                    a2 = a_rows[my][n];
+                    h0 = h_rows[my][n];
                 }
                 const float *pb = bc + k * 2 * kT + sub * 4, *pc = pb + kT;
                 float a[ITEMS], bv[ITEMS], h = 0.0f;
@@ -125,16 +131,16 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                     h = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(h), h);
                     h = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(h), h);
                     const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), h0, h);
-                    carried = lane == n ? lane_of(end, 63) : carried;
+                    carried = keep(carried, end, n);
                     h = cross_or<kWaveShr1>(h0, end);
-                    // lanes at the start of a saved chunk hold its entry state
-                    if (s.states && live && lane % kEvery == 0 && c + lane / kEvery < saved)
-                        s.states[(row * saved + c + lane / kEvery) * s.N + n] = h;
                 } else {
                     const float end = __builtin_fmaf(exp2_hw(a2 * sums.row), h0, h);
-                    if (live && s.final_state && sub == LANES - 1) s.final_state[row * s.N + n] = end;
+                    if (sub == LANES - 1) h_rows[my][n] = end;
                     h = cross_or<kRowShr + 1>(h0, end);
                 }
+                // lanes at the start of a saved chunk hold its entry state
+                if (s.states && live && sub % kEvery == 0 && c + sub / kEvery < saved)
+                    s.states[(row * saved + c + sub / kEvery) * s.N + n] = h;
 #pragma unroll
                 for (int i = 0; i < ITEMS; i += 4) {
                     const f32x4 q = *(const f32x4 *)(pc + i * LANES);
@@ -162,17 +168,109 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
         }
     }
     if (!live) return;
-    if (LANES == 64 && s.final_state && lane < s.N) s.final_state[row * s.N + lane] = carried;
-    if (LANES == 16 && s.final_state && len == 0)
-        for (int n = sub; n < s.N; n += LANES)
-            s.final_state[row * s.N + n] = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
-    // chunks past the end: zeros, and the states stay
-    for (int t = t0 + sub * 8; t < s.L; t += LANES * 8) {
+    if constexpr (LANES == 16) wave_lds_sync();
+    for (int n = sub; n < s.N; n += LANES) {
+        const float h = LANES == 64 ? carried : h_rows[my][n];
+        if (s.final_state && stop == s.L) s.final_state[row * s.N + n] = h;
+        // chunks past the end: the state stays
+        if (s.states)
+            for (int c = t0 / kScanChunk; c * kScanChunk < stop; ++c) s.states[(row * saved + c) * s.N + n] = h;
+    }
+    for (int t = t0 + sub * 8; t < stop; t += LANES * 8) {
         const float zero[8] = {};
         store8<DT>(y, t, s.L, zero);
     }
-    if (LANES == 64 && s.states && lane < s.N)
-        for (int c = t0 / kScanChunk; c < saved; ++c) s.states[(row * saved + c) * s.N + lane] = carried;
+}
+
+// Few rows and a long time axis: the state that each segment would end with from zero, and
+// its sum of dt.  A wave per row and segment of split.steps (a multiple of 1024).
+template <int DT>
+__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_local_kernel(miconv_scan_t s, int blocks_g, ScanSplit split) {
+    typedef typename Elem<DT>::T T;
+    constexpr int ITEMS = 16, kT = 64 * ITEMS, kStage = 16;
+    __shared__ __attribute__((aligned(16))) float bs[kStage][kT];       // [ITEMS / 4][lane][4]
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int per_group = s.D / s.G;
+    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g % (s.B * s.G), g = bg % s.G, b = bg / s.G;
+    const int seg = blockIdx.x / (blocks_g * s.B * s.G), start = seg * split.steps;
+    const int stop = s.L - start < split.steps ? s.L : start + split.steps;
+    const int in_group = blk * kScanWaves + wave;
+    const bool live = in_group < per_group;
+    const int d = g * per_group + (live ? in_group : 0);
+    const long long row = (long long)b * s.D + d;
+    const int len = valid_steps(s.lengths, b, s.L);
+    const T *x = (const T *)s.x.data + b * s.x.stride_b + d * s.x.stride_d;
+    const T *dl = (const T *)s.delta.data + b * s.delta.stride_b + d * s.delta.stride_d;
+    const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
+    const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
+    const float a_lane = lane < s.N ? s.A[(long long)d * s.N + lane] * kLog2e : 0.0f;
+    float carried = 0.0f, total = 0.0f;
+    for (int t0 = start; t0 < len && t0 < stop; t0 += kT) {
+        const int t = t0 + lane * ITEMS;
+        float xv[ITEMS], dt[ITEMS], sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < ITEMS; q += 8) {
+            load8<DT>(x, t + q, len, *(float (*)[8])(xv + q));
+            load8<DT>(dl, t + q, len, *(float (*)[8])(dt + q));
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const float raw = dt[i] + bias;
+            dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;
+            sum += dt[i];
+            xv[i] *= dt[i];
+        }
+        const Sums sums = prefix_sums(sum);
+        total += lane_of(sums.all, 63);
+        for (int n0 = 0; n0 < s.N; n0 += kStage) {
+            const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
+            __syncthreads();
+            for (int i = threadIdx.x; i < nn * (kT / 8); i += 64 * kScanWaves) {
+                const int at = i % (kT / 8) * 8, k = i / (kT / 8);
+                float w[8];
+                load8<DT>(Bm + (n0 + k) * s.Bm.stride_n, t0 + at, len, w);
+                float *to = bs[k] + (at % ITEMS / 4) * 256 + at / ITEMS * 4;
+                *(f32x4 *)to = f32x4{w[0], w[1], w[2], w[3]};
+                *(f32x4 *)(to + 256) = f32x4{w[4], w[5], w[6], w[7]};
+            }
+            __syncthreads();
+            for (int k = 0; k < nn; ++k) {
+                const int n = n0 + k;
+                const float a2 = lane_of(a_lane, n);
+                float h = 0.0f;
+#pragma unroll
+                for (int i = 0; i < ITEMS; i += 4) {
+                    const f32x4 q = *(const f32x4 *)(bs[k] + i * 64 + lane * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h = __builtin_fmaf(exp2_hw(dt[i + e] * a2), h, q[e] * xv[i + e]);
+                }
+                h = scan_rows(h, a2, sums);
+                h = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(h), h);
+                h = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(h), h);
+                h = __builtin_fmaf(exp2_hw(a2 * sums.all), lane_of(carried, n), h);
+                carried = keep(carried, h, n);
+            }
+        }
+    }
+    if (!live) return;
+    if (lane < s.N) split.entry[(row * split.segs + seg) * s.N + lane] = carried;
+    if (lane == 0) split.sums[row * split.segs + seg] = total;
+}
+
+// The state before each segment, in place of its local end.  A thread per row and state.
+__global__ __launch_bounds__(kThreads) void scan_chain_kernel(miconv_scan_t s, ScanSplit split) {
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (long long)s.B * s.D * s.N) return;
+    const long long row = i / s.N;
+    const int n = (int)(i - row * s.N), d = (int)(row % s.D);
+    const float a2 = s.A[(long long)d * s.N + n] * kLog2e;
+    float h = s.initial_state ? s.initial_state[i] : 0.0f;
+    for (int seg = 0; seg < split.segs; ++seg) {
+        float *at = split.entry + (row * split.segs + seg) * s.N + n;
+        const float local = *at;
+        *at = h;
+        h = __builtin_fmaf(exp2_hw(a2 * split.sums[row * split.segs + seg]), h, local);
+    }
 }
 
 // One time step.  Memory bound: 8 bytes per state, read and written once.  PER lanes per
@@ -249,17 +347,77 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
 }  // namespace
 
 template <int DT, int LANES, int ITEMS>
-static int scan_fwd(const miconv_scan_t &s, hipStream_t st) {
+static int scan_fwd(const miconv_scan_t &s, const ScanSplit &split, hipStream_t st) {
     const int rows = kScanWaves * (64 / LANES), blocks_g = (s.D / s.G + rows - 1) / rows;
-    const dim3 grid((unsigned)((long long)s.B * s.G * blocks_g));
-    hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS>), grid, dim3(64 * kScanWaves), 0, st, s, blocks_g);
+    const dim3 grid((unsigned)((long long)s.B * s.G * blocks_g * split.segs));
+    hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS>), grid, dim3(64 * kScanWaves), 0, st, s, blocks_g, split);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 
-int launch_scan_fwd(const miconv_scan_t &s, int dtype, hipStream_t st) {
-    if (s.L <= 128) return dtype ? scan_fwd<1, 16, 8>(s, st) : scan_fwd<0, 16, 8>(s, st);
-    if (s.L <= 512) return dtype ? scan_fwd<1, 64, 8>(s, st) : scan_fwd<0, 64, 8>(s, st);
-    return dtype ? scan_fwd<1, 64, 16>(s, st) : scan_fwd<0, 64, 16>(s, st);
+namespace {
+
+// Which form of the kernel takes a problem: the one with the least work on the longest CU.
+// A work-group's time per chunk, N = 16 bf16, alone on its CU and where two share it, in us:
+// 64 lanes x 16 steps 14.5 and 24, 64 x 8 8.7 and 14.8, four rows of 16 x 8 6.7 and 11.4.
+// So many long rows take 64 x 16 (2 x 4096 rows of 2048: 99 against 119 and 121 us), a
+// length just past a chunk or many short rows take 16 x 8 (2 x 4096 rows of 129: 17 against
+// 54 and 33; of 1200: 77 against 103 and 90), few rows of a few hundred 64 x 8 (2048 rows of
+// 300: 14 against 23 and 24).
+enum ScanForm { kLong, kMiddle, kRows };
+
+double form_cost(const miconv_scan_t &s, int rows, int steps, double alone, double shared) {
+    const double groups = (double)s.B * s.G * ((s.D / s.G + rows - 1) / rows), chunks = (s.L + steps - 1) / steps;
+    return chunks * (groups <= 256 ? alone : shared * (groups < 512 ? 1.0 : groups / 512));
+}
+
+ScanForm scan_form(const miconv_scan_t &s) {
+    const double a = form_cost(s, kScanWaves, 1024, 14.5, 24.0), b = form_cost(s, kScanWaves, 512, 8.7, 14.8),
+                 c = form_cost(s, 4 * kScanWaves, 128, 6.7, 11.4);
+    return a <= b && a <= c ? kLong : (b <= c ? kMiddle : kRows);
+}
+
+}  // namespace
+
+// The time axis is split where the rows alone leave half of the CUs without work and a row
+// has at least three chunks of 1024: each segment costs its local state's pass (two thirds of
+// the scan) besides, but runs beside the others.
+ScanSplit plan_scan_fwd(const miconv_scan_t &s, size_t budget) {
+    ScanSplit p = {1, 0, nullptr, nullptr, 0};
+    const long long groups = (long long)s.B * s.G * ((s.D / s.G + kScanWaves - 1) / kScanWaves);
+    const int chunks = (s.L + 1023) / 1024;
+    if (groups > 128 || chunks < 3) return p;
+    long long segs = 512 / groups < chunks ? 512 / groups : chunks;
+    const int per = (int)((chunks + segs - 1) / segs);
+    segs = (chunks + per - 1) / per;
+    const size_t rows = (size_t)s.B * s.D, bytes = rows * segs * (s.N + 1) * 4;
+    if (bytes > budget) return p;
+    p.segs = (int)segs;
+    p.steps = per * 1024;
+    p.bytes = bytes;
+    return p;
+}
+
+int launch_scan_fwd(const miconv_scan_t &s, int dtype, ScanSplit split, float *ws, hipStream_t st) {
+    if (split.segs > 1) {
+        const long long rows = (long long)s.B * s.D;
+        split.entry = ws;
+        split.sums = ws + rows * split.segs * s.N;
+        const int blocks_g = (s.D / s.G + kScanWaves - 1) / kScanWaves;
+        const dim3 grid((unsigned)((long long)s.B * s.G * blocks_g * split.segs)), block(64 * kScanWaves);
+        if (dtype)
+            hipLaunchKernelGGL(scan_local_kernel<1>, grid, block, 0, st, s, blocks_g, split);
+        else
+            hipLaunchKernelGGL(scan_local_kernel<0>, grid, block, 0, st, s, blocks_g, split);
+        hipLaunchKernelGGL(scan_chain_kernel, dim3((unsigned)((rows * s.N + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                           st, s, split);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+        return dtype ? scan_fwd<1, 64, 16>(s, split, st) : scan_fwd<0, 64, 16>(s, split, st);
+    }
+    switch (scan_form(s)) {
+        case kLong: return dtype ? scan_fwd<1, 64, 16>(s, split, st) : scan_fwd<0, 64, 16>(s, split, st);
+        case kMiddle: return dtype ? scan_fwd<1, 64, 8>(s, split, st) : scan_fwd<0, 64, 8>(s, split, st);
+        default: return dtype ? scan_fwd<1, 16, 8>(s, split, st) : scan_fwd<0, 16, 8>(s, split, st);
+    }
 }
 
 template <int DT, int PER>

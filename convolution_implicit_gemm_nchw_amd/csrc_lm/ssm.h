@@ -15,11 +15,21 @@ constexpr int kScanBwdChannels = 16;
 
 constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
+// Time segments of the scan's forward pass that run side by side (1: none), their length,
+// and in the workspace the state before each segment [B][D][segs][N] and its sum of dt.
+struct ScanSplit {
+    int segs, steps;
+    float *entry, *sums;
+    size_t bytes;
+};
+ScanSplit plan_scan_fwd(const miconv_scan_t &s, size_t budget);
+
 // Workspace of the scan's backward pass: partial sums per group of channels, time segments
 // that run side by side, and offsets.
 struct ScanBwdPlan {
     int parts, segs, seg_chunks;
-    size_t off_G, off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
+    int carry_segs, carry_steps;        // time segments of the pass that finds G between them
+    size_t off_G, off_ends, off_after, off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
 };
 ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s);
 
@@ -32,7 +42,7 @@ int launch_causal_step(int B, int D, int K, int silu, int dtype, miconv_rows_t x
                        const int *slot_of, const void *w, const float *bias, void *state_out, miconv_rows_t y,
                        hipStream_t st);
 
-int launch_scan_fwd(const miconv_scan_t &s, int dtype, hipStream_t st);
+int launch_scan_fwd(const miconv_scan_t &s, int dtype, ScanSplit split, float *ws, hipStream_t st);
 int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st);
 int launch_scan_step(const miconv_scan_t &s, int dtype, const float *state, int slots, const int *slot_of,
                      float *state_out, hipStream_t st);

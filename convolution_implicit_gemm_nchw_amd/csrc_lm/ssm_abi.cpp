@@ -224,10 +224,20 @@ int selective_scan_states_size(int B, int D, int L, int N, size_t *bytes_out) {
     return MICONV_OK;
 }
 
-int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *stream) {
+int selective_scan_fwd_workspace_size(const miconv_scan_t *s, int dtype, size_t workspace_limit, size_t *bytes_out) {
+    if (!s || !bytes_out) return MICONV_ERR_NULL;
+    const int st = check_scan_sizes(*s, dtype);
+    if (st != MICONV_OK) return st;
+    *bytes_out = plan_scan_fwd(*s, workspace_limit).bytes;
+    return MICONV_OK;
+}
+
+int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
     if (!s) return MICONV_ERR_NULL;
     const int st = check_scan_sizes(*s, dtype);
     if (st != MICONV_OK) return st;
+    if (!workspace && workspace_bytes) return MICONV_ERR_NULL;
+    const ScanSplit split = plan_scan_fwd(*s, workspace ? workspace_bytes : 0);
     const size_t es = elem_size(dtype), ns = state_count(*s);
     Checker k;
     scan_inputs(*s, es, &k);
@@ -236,8 +246,9 @@ int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *stream) {
     k.output(rows_span(s->y, s->B, s->D, s->L, es), true);
     k.output(flat(s->final_state, ns, 4), false);
     k.output(flat(s->states, ns * scan_chunks(s->L), 4), false);
+    if (split.bytes) k.output(flat(workspace, split.bytes / 4, 4), true);
     const int bad = k.done();
-    return bad != MICONV_OK ? bad : launch_scan_fwd(*s, dtype, (hipStream_t)stream);
+    return bad != MICONV_OK ? bad : launch_scan_fwd(*s, dtype, split, (float *)workspace, (hipStream_t)stream);
 }
 
 int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out) {

@@ -256,6 +256,13 @@ DEVI float scan_rows(float h, float a2, const Sums &s) {
     return __builtin_fmaf(p, cross<kRowShr + 8>(h), h);
 }
 
+// `held` with lane n's value replaced by lane 63's of v.  (The lane is read ahead of the choice:
+// inside it only lane n would run, and v need not be computed in lane 63.)
+DEVI float keep(float held, float v, int n) {
+    const float last = lane_of(v, 63);
+    return (int)(threadIdx.x & 63) == n ? last : held;
+}
+
 // Orders this wave's LDS accesses: what a lane wrote before is read by the others after.
 DEVI void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -549,7 +549,10 @@ typedef struct miconv_scan {
     float *dA, *dB, *dC, *dD, *ddelta_bias, *d_initial_state;
 } miconv_scan_t;
 
-int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *stream);
+int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+/* Workspace the forward pass uses under workspace_limit (0 is always enough; few long rows
+ * split the time axis over it). */
+int selective_scan_fwd_workspace_size(const miconv_scan_t *s, int dtype, size_t workspace_limit, size_t *bytes_out);
 int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 int selective_scan_states_size(int B, int D, int L, int N, size_t *bytes_out);
 /* Workspace the backward pass needs (MICONV_ERR_WORKSPACE when given less). */

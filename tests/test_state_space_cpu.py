@@ -53,8 +53,8 @@ def cbwd(dtype=0, ws=None, wb=0, **kw):
     return mc.lib().causal_conv1d_bwd(ctypes.byref(conv_args(**kw)), dtype, ws, wb, None)
 
 
-def sfwd(dtype=0, **kw):
-    return mc.lib().selective_scan_fwd(ctypes.byref(scan_args(**kw)), dtype, None)
+def sfwd(dtype=0, ws=None, wb=0, **kw):
+    return mc.lib().selective_scan_fwd(ctypes.byref(scan_args(**kw)), dtype, ws, wb, None)
 
 
 def sbwd(dtype=0, ws=at(30), wb=1 << 24, **kw):
@@ -109,7 +109,8 @@ def test_convolution_refusals():
 
 def test_scan_refusals():
     lib = mc.lib()
-    assert lib.selective_scan_fwd(None, 0, None) == E_NULL
+    assert lib.selective_scan_fwd(None, 0, None, 0, None) == E_NULL
+    assert sfwd(ws=None, wb=64) == E_NULL
     for call in (sfwd, sbwd):
         for bad in ({"B": 0}, {"D": 0}, {"L": 0}, {"N": 0}, {"N": 65}, {"G": 0}, {"G": 4},
                     {"delta": mc._Rows(at(1), 240, -40)}, {"Bm": mc._ScanIn(at(4), 400, 200, -1)}):
@@ -175,6 +176,11 @@ def test_workspace_sizes():
     assert lib.selective_scan_states_size(3, 7, 1025, 5, ctypes.byref(need)) == OK
     assert need.value % (4 * 3 * 7 * 5) == 0 and need.value > 0
     assert lib.selective_scan_states_size(0, 7, 10, 5, ctypes.byref(need)) == E_DIM
+    few = scan_args(L=8192, B=1)
+    for limit in (0, 1000, 10 ** 6, 10 ** 9):
+        assert lib.selective_scan_fwd_workspace_size(ctypes.byref(few), 0, limit, ctypes.byref(need)) == OK
+        assert need.value <= limit
+    assert need.value > 0
     assert lib.selective_scan_bwd_workspace_size(ctypes.byref(scan_args()), 0, ctypes.byref(need)) == OK
     assert need.value > 0
     for limit in (0, 1000, 10 ** 9):

@@ -168,7 +168,9 @@ SCAN = [(1, 1, 1, 1, 1, False, False, False, False, False),
         (2, 2, 1100, 17, 1, True, True, False, True, True),
         (6, 2, 1030, 33, 2, True, True, True, True, True),
         (1, 33, 70, 64, 1, False, True, False, True, True),
-        (1, 2, 2600, 3, 1, True, True, False, True, True)]
+        (1, 2, 2600, 3, 1, True, True, False, True, True),
+        (2, 3, 4400, 5, 1, True, True, True, True, True),          # few rows: the time axis split
+        (3, 17, 3200, 16, 1, False, True, True, True, True)]
 
 
 def scan_data(case, dt):
@@ -225,6 +227,14 @@ def test_scan(mc, case, dt):
     agree("y", y, want["y"], dt, case)
     agree("fs", fs, want["fs"], "f32", case)
     rest()
+    # without a workspace the time axis stays whole
+    none = torch.empty(1, dtype=torch.uint8, device=DEV)
+    states2, fs2 = torch.full_like(states, float("nan")), torch.full_like(fs, float("nan"))
+    y2 = mc.selective_scan_fwd(v["x"], v["delta"], d["A"], Bm, Cm, initial_state=d.get("h0"), final_state=fs2,
+                               states=states2, workspace=none, **common)
+    agree("y whole", y2, want["y"], dt, case)
+    agree("fs whole", fs2, want["fs"], "f32", case)
+    assert bool(states.isfinite().all()) and bool(states2.isfinite().all())
     dh0 = torch.full((B, D, N), float("nan"), device=DEV)
     outs = {k: out_view((B, D, L), dt) for k in ("dx", "ddelta") + (("dz",) if gate else ())}
     args = (v["x"], v["delta"], d["A"], Bm, Cm, v["dy"], states)
