@@ -81,16 +81,19 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv
     }
 }
 
-// One work-group: channel d, items [split * per, ...) of the B * tiles eight-step
-// tiles.  A thread recomputes u of its own and the K-1 following steps (dx needs
-// their du), writes its dx and keeps its part of dw and dbias; the parts are
-// added in a fixed tree and written to part[split][d][K+1] (or dw, dbias).
-template <int DT, int K, int TH>
-__global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, int tiles, long long per, int splits,
+// One work-group: channel d, items [split * per, ...) of the B * tiles eight-step tiles.
+// dx needs du of the K-1 steps after its own, which the next lane has: a wave takes 63
+// consecutive tiles, and its last lane only computes du for the one before.  (Computing
+// those steps again instead takes two more loads and (K-1)/8 more gates per step: 16 x 2048
+// x 1024, K 4, bf16: 60 us.)  A thread keeps its part of dw and dbias; the parts are added
+// in a fixed tree and written to part[split][d][K+1] (or dw, dbias).
+template <int DT, int K>
+__global__ __launch_bounds__(kThreads) void causal_bwd_kernel(miconv_causal_conv_t c, int tiles, long long per, int splits,
                                                         float *part) {
     typedef typename Elem<DT>::T T;
-    __shared__ float red[TH / 64][K + 1];
-    const int d = blockIdx.x, split = blockIdx.y;
+    __shared__ float red[kThreads / 64][K + 1];
+    const int waves = blockDim.x >> 6, step = waves * 63, d = blockIdx.x, split = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const long long items = (long long)c.B * tiles;
     const long long first = split * per, last = first + per < items ? first + per : items;
     float w[K], dw[K], db = 0.0f;
@@ -100,25 +103,25 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
         dw[k] = 0.0f;
     }
     const float bias = c.bias ? c.bias[d] : 0.0f;
-    int b = (int)((first + threadIdx.x) / tiles), tile = (int)(first + threadIdx.x - (long long)b * tiles);
-    const int step_b = TH / tiles, step_t = TH - step_b * tiles;
-    for (long long it = first + threadIdx.x; it < last; it += TH) {
-        const int t = tile * 8;
-        const int len = valid_steps(c.lengths, b, c.L);
-        const long long row = (long long)b * c.D + d;
-        const T *x = (const T *)c.x.data + b * c.x.stride_b + d * c.x.stride_d;
-        const T *dy = (const T *)c.dy.data + b * c.dy.stride_b + d * c.dy.stride_d;
+    const long long mine = first + wave * 63 + lane;
+    int b = (int)(mine / tiles), tile = (int)(mine - (long long)b * tiles);
+    const int step_b = step / tiles, step_t = step - step_b * tiles;
+    for (long long base = first + wave * 63; base < last; base += step) {
+        const long long it = base + lane;
+        const bool there = it < items, counts = lane < 63 && it < last;
+        const int t = tile * 8, bb = there ? b : 0;
+        const int len = there ? valid_steps(c.lengths, bb, c.L) : 0;
+        const long long row = (long long)bb * c.D + d;
         const T *init = c.initial_state ? (const T *)c.initial_state + row * (K - 1) : nullptr;
-        const T *dfs = c.d_final_state ? (const T *)c.d_final_state + row * (K - 1) : nullptr;
-        float v[24], g[16], out[8] = {};
+        float v[16], g[8 + K];                 // x~ of the eight steps before and of these; du
         if (t < len) {
+            const T *x = (const T *)c.x.data + bb * c.x.stride_b + d * c.x.stride_d;
+            const T *dy = (const T *)c.dy.data + bb * c.dy.stride_b + d * c.dy.stride_d;
             load_before<DT, K>(x, init, t, len, *(float (*)[8])v);
             load8<DT>(x, t, len, *(float (*)[8])(v + 8));
-            load8<DT>(x, t + 8, len, *(float (*)[8])(v + 16));
             load8<DT>(dy, t, len, *(float (*)[8])g);
-            load8<DT>(dy, t + 8, len, *(float (*)[8])(g + 8));
 #pragma unroll
-            for (int i = 0; i < 8 + K - 1; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 if (!c.silu) continue;
                 float u = bias;
 #pragma unroll
@@ -127,6 +130,18 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
                 // a step past the end has du = 0 whatever u is there
                 g[i] = t + i < len ? g[i] * (sg * __builtin_fmaf(u, 1.0f - sg, 1.0f)) : 0.0f;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = v[i] = v[8 + i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) {
+            const float next = cross<kWaveShl1>(g[i]);
+            g[8 + i] = tile + 1 < tiles ? next : 0.0f;
+        }
+        if (counts) {
+            const T *dfs = c.d_final_state ? (const T *)c.d_final_state + row * (K - 1) : nullptr;
+            float out[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float s = 0.0f;
@@ -140,20 +155,17 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
                 if (dfs && j >= 0 && t + i < len) s += Elem<DT>::get(dfs[j]);
                 out[i] = t + i < len ? s : 0.0f;
             }
-        } else {
+            if (c.dx.data) store8<DT>((T *)c.dx.data + bb * c.dx.stride_b + d * c.dx.stride_d, t, c.L, out);
+            if (t == 0 && c.d_initial_state) {
+                T *di = (T *)c.d_initial_state + row * (K - 1);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = 0.0f;
-        }
-        if (c.dx.data) store8<DT>((T *)c.dx.data + b * c.dx.stride_b + d * c.dx.stride_d, t, c.L, out);
-        if (t == 0 && c.d_initial_state) {
-            T *di = (T *)c.d_initial_state + row * (K - 1);
+                for (int f = 0; f < K - 1; ++f) {
+                    float s = 0.0f;
 #pragma unroll
-            for (int f = 0; f < K - 1; ++f) {
-                float s = 0.0f;
-#pragma unroll
-                for (int u = 0; u <= f; ++u) s = __builtin_fmaf(w[f - u], g[u], s);
-                if (dfs && f >= len) s += Elem<DT>::get(dfs[f - len]);
-                di[f] = Elem<DT>::put(s);
+                    for (int u = 0; u <= f; ++u) s = __builtin_fmaf(w[f - u], g[u], s);
+                    if (dfs && f >= len) s += Elem<DT>::get(dfs[f - len]);
+                    di[f] = Elem<DT>::put(s);
+                }
             }
         }
         b += step_b;
@@ -163,7 +175,6 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
             ++b;
         }
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int k = 0; k <= K; ++k) {
         float s = k < K ? dw[k < K ? k : 0] : db;
@@ -174,7 +185,7 @@ __global__ __launch_bounds__(TH) void causal_bwd_kernel(miconv_causal_conv_t c, 
     __syncthreads();
     if (threadIdx.x <= K) {
         float s = 0.0f;
-        for (int i = 0; i < TH / 64; ++i) s += red[i][threadIdx.x];
+        for (int i = 0; i < waves; ++i) s += red[i][threadIdx.x];
         if (splits > 1) {
             part[((long long)split * c.D + d) * (K + 1) + threadIdx.x] = s;
         } else if (threadIdx.x < K) {
@@ -254,12 +265,9 @@ template <int DT, int K>
 int bwd_k(const miconv_causal_conv_t &c, int splits, float *ws, hipStream_t st) {
     const int tiles = (c.L + 7) / 8;
     const long long items = (long long)c.B * tiles, per = (items + splits - 1) / splits;
-    if (per <= 64)
-        hipLaunchKernelGGL((causal_bwd_kernel<DT, K, 64>), dim3(c.D, splits), dim3(64), 0, st, c, tiles, per, splits,
-                           ws);
-    else
-        hipLaunchKernelGGL((causal_bwd_kernel<DT, K, kThreads>), dim3(c.D, splits), dim3(kThreads), 0, st, c, tiles,
-                           per, splits, ws);
+    // up to four waves; fewer only where they hold all of a channel's tiles at once
+    const int waves = per >= 4 * 63 ? 4 : (int)((per + 62) / 63);
+    hipLaunchKernelGGL((causal_bwd_kernel<DT, K>), dim3(c.D, splits), dim3(waves * 64), 0, st, c, tiles, per, splits, ws);
     if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
     if (splits > 1 && (c.dw || c.dbias)) {
         const long long n = (long long)c.D * (K + 1);
