@@ -217,11 +217,11 @@ __global__ __launch_bounds__(kThreads) void causal_step_kernel(int B, int D, int
                                                                const typename Elem<DT>::T *state, int slots,
                                                                const int *slot_of, const typename Elem<DT>::T *w,
                                                                const float *bias, typename Elem<DT>::T *state_out,
-                                                               miconv_rows_t y) {
+                                                               miconv_rows_t y, FDiv fd_D) {
     typedef typename Elem<DT>::T T;
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (long long)B * D) return;
-    const int b = (int)(i / D), d = (int)(i - (long long)b * D);
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;                   // rows are at most 2^30
+    if (i >= (uint32_t)B * (uint32_t)D) return;
+    const int b = (int)fdiv(i, fd_D), d = (int)i - b * D;
     const int slot = slot_of ? slot_of[b] : b;
     T *yo = (T *)y.data + b * y.stride_b + d * y.stride_d;
     if (slot < 0 || slot >= slots) {
@@ -284,7 +284,8 @@ int step_k(int B, int D, int silu, miconv_rows_t x, const void *state, int slots
     typedef typename Elem<DT>::T T;
     const long long n = (long long)B * D;
     hipLaunchKernelGGL((causal_step_kernel<DT, K>), dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                       st, B, D, silu, x, (const T *)state, slots, slot_of, (const T *)w, bias, (T *)state_out, y);
+                       st, B, D, silu, x, (const T *)state, slots, slot_of, (const T *)w, bias, (T *)state_out, y,
+                       make_fdiv((uint32_t)D));
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 

@@ -280,12 +280,13 @@ __global__ __launch_bounds__(kThreads) void scan_chain_kernel(miconv_scan_t s, S
 // writes, so state_out may be state.
 template <int DT, int PER, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, const float *state, int slots,
-                                                             const int *slot_of, float *state_out) {
+                                                             const int *slot_of, float *state_out, FDiv fd_D,
+                                                             FDiv fd_group) {
     typedef typename Elem<DT>::T T;
     const int sub = threadIdx.x % PER, n0 = sub * 4;
-    const long long i = (long long)blockIdx.x * (kThreads / PER) + threadIdx.x / PER;
-    if (i >= (long long)s.B * s.D) return;
-    const int b = (int)(i / s.D), d = (int)(i - (long long)b * s.D), g = d / (s.D / s.G);
+    const uint32_t i = blockIdx.x * (kThreads / PER) + threadIdx.x / PER;     // rows are at most 2^30
+    if (i >= (uint32_t)s.B * (uint32_t)s.D) return;
+    const int b = (int)fdiv(i, fd_D), d = (int)i - b * s.D, g = (int)fdiv(d, fd_group);
     const int slot = slot_of ? slot_of[b] : b;
     T *yo = (T *)s.y.data + b * s.y.stride_b + d * s.y.stride_d;
     if (slot < 0 || slot >= slots) {
@@ -425,13 +426,14 @@ static int scan_step(const miconv_scan_t &s, const float *state, int slots, cons
                      hipStream_t st) {
     const long long rows = (long long)s.B * s.D;
     const dim3 grid((unsigned)((rows + kThreads / PER - 1) / (kThreads / PER)));
+    const FDiv fd_D = make_fdiv((uint32_t)s.D), fd_group = make_fdiv((uint32_t)(s.D / s.G));
     const bool together = s.N == 1 || (s.Bm.stride_n == 1 && s.Cm.stride_n == 1);
     if (s.N % 4 == 0 && together && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0)
         hipLaunchKernelGGL((scan_step_kernel<DT, PER, true>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
-                           state_out);
+                           state_out, fd_D, fd_group);
     else
         hipLaunchKernelGGL((scan_step_kernel<DT, PER, false>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
-                           state_out);
+                           state_out, fd_D, fd_group);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 
