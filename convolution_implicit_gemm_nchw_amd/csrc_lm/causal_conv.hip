@@ -39,7 +39,7 @@ DEVI float full_at(const typename Elem<DT>::T *row, const typename Elem<DT>::T *
 
 // 2^lg_tpr threads per row.  WAVE: a row takes whole waves, so that what belongs to it
 // (addresses, taps, bias) is scalar.
-template <int DT, int K, bool WAVE>
+template <int DT, int K, bool WAVE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv_t c, int lg_tpr, FDiv fd_D) {
     typedef typename Elem<DT>::T T;
     const int sub = threadIdx.x & ((1 << lg_tpr) - 1);
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv
                 out[i] = t + i < len ? (c.silu ? u * logistic_for<DT>(u) : u) : 0.0f;
             }
         }
-        store8<DT>(y, t, c.L, out);
+        store8<DT, STREAM>(y, t, c.L, out);
         if (t == 0 && c.final_state) {
             T *fs = (T *)c.final_state + (long long)row * (K - 1);
 #pragma unroll
@@ -254,10 +254,12 @@ int fwd_k(const miconv_causal_conv_t &c, hipStream_t st) {
     const long long along = (tiles + (1ll << lg) - 1) >> lg;
     const dim3 grid((unsigned)row_blocks, (unsigned)(along < 65535 ? along : 65535));
     const FDiv fd = make_fdiv((uint32_t)c.D);
-    if (lg >= 6)
-        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true>), grid, dim3(kThreads), 0, st, c, lg, fd);
+    if (lg < 6)
+        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, false, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
+    else if (streams((size_t)c.B * c.D * c.L * sizeof(typename Elem<DT>::T)))
+        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, true>), grid, dim3(kThreads), 0, st, c, lg, fd);
     else
-        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
+        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 

@@ -39,18 +39,18 @@ DEVI float scaled(const I8Args &a, int sum, float cs, float rs) {
 }
 
 // Eight consecutive values of one row of y from c0 on.
-template <int OD>
+template <int OD, bool STREAM>
 DEVI void put8(const I8Args &a, int r, int c0, const float (&v)[8]) {
     typedef typename Elem<OD>::T T;
     T *y = (T *)a.y;
     if (a.len == 0) {
-        store8<OD>(y + (long long)r * a.row, c0, a.NC, v);
+        store8<OD, STREAM>(y + (long long)r * a.row, c0, a.NC, v);
         return;
     }
     const int b = (int)fdiv((uint32_t)c0, a.fd_len), l = c0 - b * a.len;
     T *line = y + ((long long)b * a.NR + r) * a.len;
     if (l + 8 <= a.len) {
-        store8<OD>(line, l, a.len, v);
+        store8<OD, STREAM>(line, l, a.len, v);
         return;
     }
 #pragma unroll
@@ -73,7 +73,7 @@ DEVI void columns(const I8Args &a, int c, float (&cs)[8], float (&cb)[8]) {
 }
 
 // The sums of eight columns of row r, stored as they are (split) or finished.
-template <int OD>
+template <int OD, bool STREAM = false>
 DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8], const float (&cs)[8],
                   const float (&cb)[8], float rs, float rb) {
     if (a.part && split >= 0) {
@@ -86,7 +86,7 @@ DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8],
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = scaled(a, sum[e], cs[e], rs) + (cb[e] + rb);
-    put8<OD>(a, r, c, v);
+    put8<OD, STREAM>(a, r, c, v);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -160,7 +160,7 @@ struct Tile {
     }
 };
 
-template <int OD, int WC, int WR, int FC, int FR, int ST>
+template <int OD, int WC, int WR, int FC, int FR, int ST, bool STREAM>
 __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
     typedef Tile<WC, WR, FC, FR, ST> X;
     __shared__ __attribute__((aligned(1024))) char stages[ST * X::kBytes];
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
                 sum[e] = lo[e];
                 sum[4 + e] = hi[e];
             }
-            finish8<OD>(a, split, r, c, sum, cs, cb, rsr, rbr);
+            finish8<OD, STREAM>(a, split, r, c, sum, cs, cb, rsr, rbr);
         }
         wave_lds_sync();
     }
@@ -355,14 +355,14 @@ void few(int T, int O, int K, int L, const signed char *q, const float *qs, cons
                        T, O, K, L, channel_major, y);
 }
 
-template <int OD, int WC, int WR, int FC, int FR, int ST>
+template <int OD, int WC, int WR, int FC, int FR, int ST, bool STREAM = false>
 int tiled(I8Args a, int splits, hipStream_t st) {
     typedef Tile<WC, WR, FC, FR, ST> X;
     a.tiles_c = (a.NC + X::C - 1) / X::C;
     a.tiles_r = (a.NR + X::R - 1) / X::R;
     if (splits == 1) a.part = nullptr;
     a.k_split = ((a.K / 128 + splits - 1) / splits) * 128;
-    hipLaunchKernelGGL((i8_tile_kernel<OD, WC, WR, FC, FR, ST>), dim3((unsigned)((long long)a.tiles_c * a.tiles_r * splits)),
+    hipLaunchKernelGGL((i8_tile_kernel<OD, WC, WR, FC, FR, ST, STREAM>), dim3((unsigned)((long long)a.tiles_c * a.tiles_r * splits)),
                        dim3(X::kThreads), 0, st, a);
     if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
     if (splits > 1) {
@@ -407,7 +407,9 @@ static int i8_by_size(const I8Args &a, int T, int O, int splits, hipStream_t st)
     switch (tile_side(T, O)) {
         // small tiles leave LDS room for four stages, which tall and narrow products (few tiles,
         // long k) need: 65 tokens, 4096 -> 8192: 17.4 us with two, 12.8 with four
-        case 256: return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
+        case 256:
+            if (streams((size_t)T * O * sizeof(typename Elem<OD>::T))) return tiled<OD, 2, 4, 4, 2, 2, true>(a, splits, st);
+            return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
         case 128: return tiled<OD, 2, 2, 2, 2, 2>(a, splits, st);
         default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);
     }

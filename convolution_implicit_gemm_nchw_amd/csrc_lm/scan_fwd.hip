@@ -277,8 +277,10 @@ __global__ __launch_bounds__(kThreads) void scan_chain_kernel(miconv_scan_t s, S
 // (sequence, channel), four states each, so that consecutive lanes read consecutive 16
 // bytes of the states; their products with C are added across the lanes.  VEC: N is a
 // multiple of 4, the states are 16-byte aligned, B and C have their states next to each other.  All reads of a state come before its
-// writes, so state_out may be state.
-template <int DT, int PER, bool VEC>
+// writes, so state_out may be state.  STREAM: states of 16 MB or more pass by the caches, as
+// those of a model's layers together do not fit them from one token to the next (256
+// sequences of 4096 channels: 35.7 -> 31.7 us).
+template <int DT, int PER, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, const float *state, int slots,
                                                              const int *slot_of, float *state_out, FDiv fd_D,
                                                              FDiv fd_group) {
@@ -299,7 +301,11 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
     const float *A = s.A + (long long)d * s.N + n0;
     float h[4], a[4], bv[4], cv[4];
     if (VEC && n0 < s.N) {
-        const f32x4 hv = *(const f32x4 *)(state + so);
+        f32x4 hv;
+        if constexpr (STREAM)
+            hv = __builtin_nontemporal_load((const f32x4 *)(state + so));
+        else
+            hv = *(const f32x4 *)(state + so);
         const u32x4 av = *(const u32x4_row *)A;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -331,7 +337,11 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
         v = __builtin_fmaf(cv[e], h[e], v);
     }
     if (VEC && n0 < s.N) {
-        *(f32x4 *)(state_out + so) = f32x4{h[0], h[1], h[2], h[3]};
+        const f32x4 hv = {h[0], h[1], h[2], h[3]};
+        if constexpr (STREAM)
+            __builtin_nontemporal_store(hv, (f32x4 *)(state_out + so));
+        else
+            *(f32x4 *)(state_out + so) = hv;
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -428,12 +438,11 @@ static int scan_step(const miconv_scan_t &s, const float *state, int slots, cons
     const dim3 grid((unsigned)((rows + kThreads / PER - 1) / (kThreads / PER)));
     const FDiv fd_D = make_fdiv((uint32_t)s.D), fd_group = make_fdiv((uint32_t)(s.D / s.G));
     const bool together = s.N == 1 || (s.Bm.stride_n == 1 && s.Cm.stride_n == 1);
-    if (s.N % 4 == 0 && together && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0)
-        hipLaunchKernelGGL((scan_step_kernel<DT, PER, true>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
-                           state_out, fd_D, fd_group);
-    else
-        hipLaunchKernelGGL((scan_step_kernel<DT, PER, false>), grid, dim3(kThreads), 0, st, s, state, slots, slot_of,
-                           state_out, fd_D, fd_group);
+    const bool vec = s.N % 4 == 0 && together && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0;
+    const auto kern = !vec ? scan_step_kernel<DT, PER, false, false>
+                           : ((size_t)rows * s.N * 4 >= (16u << 20) ? scan_step_kernel<DT, PER, true, true>
+                                                                    : scan_step_kernel<DT, PER, true, false>);
+    hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, st, s, state, slots, slot_of, state_out, fd_D, fd_group);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 

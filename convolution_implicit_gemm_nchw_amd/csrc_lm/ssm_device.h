@@ -117,8 +117,16 @@ DEVI void widen8(const Raw8<DT> &o, float (&v)[8]) {
     }
 }
 
-// row[t + i] = v[i] for t + i < end.
-template <int DT>
+template <bool STREAM>
+DEVI void put_vec(u32x4 v, u32x4_row *to) {
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(v, to);
+    else
+        *to = v;
+}
+
+// row[t + i] = v[i] for t + i < end.  STREAM: past the caches, see streams().
+template <int DT, bool STREAM = false>
 DEVI void store8(typename Elem<DT>::T *row, int t, int end, const float (&v)[8]) {
     if (t + 8 <= end) {
         if constexpr (DT == 1) {
@@ -129,7 +137,7 @@ DEVI void store8(typename Elem<DT>::T *row, int t, int end, const float (&v)[8])
                 const bf16x2 p = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
                 r[i] = __builtin_bit_cast(uint32_t, p);
             }
-            *(u32x4_row *)(row + t) = r;
+            put_vec<STREAM>(r, (u32x4_row *)(row + t));
         } else {
             u32x4 r0, r1;
 #pragma unroll
@@ -137,8 +145,8 @@ DEVI void store8(typename Elem<DT>::T *row, int t, int end, const float (&v)[8])
                 r0[i] = __float_as_uint(v[i]);
                 r1[i] = __float_as_uint(v[4 + i]);
             }
-            *(u32x4_row *)(row + t) = r0;
-            *(u32x4_row *)(row + t + 4) = r1;
+            put_vec<STREAM>(r0, (u32x4_row *)(row + t));
+            put_vec<STREAM>(r1, (u32x4_row *)(row + t + 4));
         }
     } else {
 #pragma unroll

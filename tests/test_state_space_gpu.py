@@ -440,6 +440,33 @@ def test_other_stream_and_graph_replays(mc):
         eager = [t.clone() for t in layer()]
 
 
+def test_large_outputs(mc):
+    """Outputs large enough to be written past the caches: bit for bit those of two halves that are not."""
+    f = Data(9, "bf16")
+    x = torch.randn(2, 1024, 32769, device=DEV).bfloat16()            # 128 MB and odd rows
+    w, bias = f.make(1024, 4)[1], f.make(1024, dtype=torch.float32)[1]
+    y = mc.causal_conv1d_fwd(x, w, bias=bias, silu=True)
+    for i in range(2):
+        assert torch.equal(y[i:i + 1], mc.causal_conv1d_fwd(x[i:i + 1], w, bias=bias, silu=True))
+    B, D, N = 66, 4096, 16                                             # 17 MB of states
+    x, dl, z = (torch.randn(B, D, device=DEV).bfloat16() for _ in range(3))
+    Bm, Cm = (torch.randn(B, 1, N, device=DEV).bfloat16() for _ in range(2))
+    A, state = -torch.rand(D, N, device=DEV), torch.randn(B, D, N, device=DEV)
+    out = torch.empty_like(state)
+    y = mc.selective_scan_step(x, dl, A, Bm, Cm, state, z=z, softplus=True, state_out=out)
+    for i in (slice(0, 33), slice(33, 66)):
+        part = state[i].clone()
+        assert torch.equal(y[i], mc.selective_scan_step(x[i], dl[i], A, Bm[i], Cm[i], part, z=z[i], softplus=True))
+        assert torch.equal(part, out[i])
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.randint(-127, 128, (8195, 128), generator=gen, device=DEV, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (8203, 128), generator=gen, device=DEV, dtype=torch.int8)
+    s, ws = torch.rand(8195, device=DEV), torch.rand(8203, device=DEV)
+    y = mc.matmul_i8(q, s, wq, ws, out_dtype=torch.bfloat16)          # 134 MB
+    for i in (slice(0, 4000), slice(4000, 8195)):
+        assert torch.equal(y[i], mc.matmul_i8(q[i], s[i], wq, ws, out_dtype=torch.bfloat16))
+
+
 def test_offsets_past_32_bits(mc):
     """Rows of one buffer more than 2^31 elements apart."""
     D, L, N = 3, 20, 4
