@@ -97,13 +97,6 @@ DEVI P *at_row(const miconv_rows_t &r, int b, int d) {
     return (P *)r.data + b * r.stride_b + d * r.stride_d;
 }
 
-// v, of which the compiler does not know that it is: addresses made from it are made where
-// they are used rather than held in registers through the turns.
-DEVI int again(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-
 template <int DT, int NS>
 __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOut o) {
     typedef typename Elem<DT>::T T;

@@ -95,13 +95,15 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
             const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
             __syncthreads();
-            for (int i = threadIdx.x; i < nn * 2 * (kT / 8); i += 64 * kScanWaves) {
-                const int at = i % (kT / 8) * 8, which = i / (kT / 8), n = n0 + (which >> 1);
+            // where this thread's eight steps of a staged row are, and go to
+            const int tid = again(threadIdx.x), at = tid % (kT / 8) * 8;
+            float *const to = bc + (at % ITEMS / 4) * LANES * 4 + at / ITEMS * 4;
+            for (int which = tid / (kT / 8); which < 2 * nn; which += 64 * kScanWaves / (kT / 8)) {
+                const int n = n0 + (which >> 1);
                 float w[8];
                 load8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, t0 + at, len, w);
-                float *to = bc + which * kT + (at % ITEMS / 4) * LANES * 4 + at / ITEMS * 4;
-                *(f32x4 *)to = f32x4{w[0], w[1], w[2], w[3]};
-                *(f32x4 *)(to + LANES * 4) = f32x4{w[4], w[5], w[6], w[7]};
+                *(f32x4 *)(to + which * kT) = f32x4{w[0], w[1], w[2], w[3]};
+                *(f32x4 *)(to + which * kT + LANES * 4) = f32x4{w[4], w[5], w[6], w[7]};
             }
             __syncthreads();
             for (int k = 0; k < nn; ++k) {

@@ -271,6 +271,13 @@ DEVI float keep(float held, float v, int n) {
     return (int)(threadIdx.x & 63) == n ? last : held;
 }
 
+// v, of which the compiler does not know that it is: addresses made from it are made where
+// they are used rather than held in registers through the turns.
+DEVI int again(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // Orders this wave's LDS accesses: what a lane wrote before is read by the others after.
 DEVI void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
