@@ -194,12 +194,9 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     }
                     put_steps(m.zslope, wave, lane, zslope);
                 }
+                step_sizes(dt, bias, s.softplus, t, live ? t0 + kT : len + 1, end);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float raw = dt[i] + bias;
-                    dt[i] = t + i < end ? (s.softplus ? softplus(raw) : raw) : 0.0f;   // no decay past the end
-                    dtx[i] *= dt[i];
-                }
+                for (int i = 0; i < 8; ++i) dtx[i] *= dt[i];
                 put_steps(m.dt, wave, lane, dt);
                 put_steps(m.dtx, wave, lane, dtx);
                 put_steps(m.e, wave, lane, e);
@@ -464,12 +461,9 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
                 for (int i = 0; i < 8; ++i) e[q + i] *= zv[i] * logistic(zv[i]);
             }
         }
+        step_sizes(dt, bias, s.softplus, t, t0 + kCarryT, len);
 #pragma unroll
-        for (int i = 0; i < kCarryItems; ++i) {
-            const float raw = dt[i] + bias;
-            dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;
-            sum += dt[i];
-        }
+        for (int i = 0; i < kCarryItems; ++i) sum += dt[i];
         const Sums sums = prefix_sums(sum);
         const int ends_here = t0 / kT + (64 - lane) / kEvery - 1;      // the chunk that ends where this lane begins
         const bool saves = live && lane % kEvery == 0 && ends_here * kT < stop;

@@ -83,10 +83,9 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
             load8<DT>(x, t + q, len, *(float (*)[8])(xv + q));
             load8<DT>(dl, t + q, len, *(float (*)[8])(dt + q));
         }
+        step_sizes(dt, bias, s.softplus, t, t0 + kT, len);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const float raw = dt[i] + bias;
-            dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;   // no decay past the end
             sum += dt[i];
             v[i] = skip * xv[i];
             xv[i] *= dt[i];
@@ -215,10 +214,9 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_local_kernel(miconv_s
             load8<DT>(x, t + q, len, *(float (*)[8])(xv + q));
             load8<DT>(dl, t + q, len, *(float (*)[8])(dt + q));
         }
+        step_sizes(dt, bias, s.softplus, t, t0 + kT, len);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const float raw = dt[i] + bias;
-            dt[i] = t + i < len ? (s.softplus ? softplus(raw) : raw) : 0.0f;
             sum += dt[i];
             xv[i] *= dt[i];
         }

@@ -284,6 +284,21 @@ DEVI void wave_lds_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// dt of n consecutive steps from t on, in place of delta; 0 (no decay) from `end` on, which only a
+// chunk that reaches past it has to look at.
+template <int N>
+DEVI void step_sizes(float (&dt)[N], float bias, int use_softplus, int t, int chunk_end, int end) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        dt[i] += bias;
+        if (use_softplus) dt[i] = softplus(dt[i]);
+    }
+    if (chunk_end > end) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dt[i] = t + i < end ? dt[i] : 0.0f;
+    }
+}
+
 DEVI int valid_steps(const int *lengths, int b, int L) {
     if (!lengths) return L;
     const int n = lengths[b];
