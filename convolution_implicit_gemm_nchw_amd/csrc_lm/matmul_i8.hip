@@ -5,6 +5,10 @@
 // one along whose axis y is contiguous (channels for token-major y, tokens for
 // channel-major y) takes the rows, called axis C below, because a lane's
 // accumulators run along the rows; the other is axis R.
+//
+// Many tokens are bound by the MFMAs under the power limit (8192 tokens, 4096 -> 8192: 250 us,
+// 2.2 POP/s with the output; on zeros a fifth less), few by the weight's bytes (8 tokens: 7.3 us,
+// 4.6 TB/s).
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
@@ -374,27 +378,34 @@ int tiled(I8Args a, int splits, hipStream_t st) {
     return MICONV_OK;
 }
 
+// Up to here one 16-token block after the other costs less than a 64-row tile (4096 -> 8192:
+// 16 tokens 8.0 against 14.3 us, 64 tokens 14.0 against 16.6).
 constexpr int kFewTokens = 64;
 
 long long tile_count(long long T, long long O, int side) {
     return ((T + side - 1) / side) * ((O + side - 1) / side);
 }
 
-// Side of the square tile: the largest that gives most of the 256 CUs a tile.
+// Side of the square tile: the largest that gives most of the 256 CUs a tile.  4096 deep, in us:
+// 128 tiles of 256 57.7 against 39.7 with side 128, 176 tiles 57.7 against 58.7, 208 58.9
+// against 67.4; 1024 deep: 126 tiles of 128 10.3 against 7.4 with side 64, 169 10.5 against 10.9.
 int tile_side(int T, int O) {
-    if (tile_count(T, O, 256) >= 192) return 256;
-    if (tile_count(T, O, 128) >= 192) return 128;
+    if (tile_count(T, O, 256) >= 176) return 256;
+    if (tile_count(T, O, 128) >= 160) return 128;
     return 64;
 }
 
 }  // namespace
 
-// Splits of k where even the smallest tiles leave CUs idle, each at least 1024 long.
+// Splits of k: a step of 128 bytes takes 0.3 us, joining the sums 4 to 5 us, so only products
+// 8192 deep or more with few tiles gain (100 tokens, 8192 -> 512: 21.0 us whole, 16.3 in four;
+// 128 tokens, 4096 -> 2048: 12.1 whole, 14.8 in two), each split at least 2048 deep.
 int i8_splits(int T, int O, int K, size_t budget) {
-    if (T <= kFewTokens) return 1;
+    if (T <= kFewTokens || K < 8192) return 1;
     const long long tiles = tile_count(T, O, tile_side(T, O));
-    long long s = 256 / tiles;
-    if (s > K / 1024) s = K / 1024;
+    long long s = 160 / tiles;
+    if (s > K / 2048) s = K / 2048;
+    if (s > 16) s = 16;
     const size_t one = (size_t)T * O * 4;
     if (s > (long long)(budget / one)) s = (long long)(budget / one);
     if (s < 2) return 1;

@@ -308,7 +308,7 @@ def test_scan_values_at_the_ends(mc):
 # ------------------------------------------------------------------ 8-bit products
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("C", [1, 3, 127, 128, 129, 1000, 4096])
+@pytest.mark.parametrize("C", [1, 3, 127, 128, 129, 1000, 2000, 4096, 5000, 9000])
 def test_quantisation(mc, dt, C):
     f = Data(C, dt)
     T = 37
@@ -349,7 +349,7 @@ def test_quantisation(mc, dt, C):
 #       B  L    O     K(padded)
 I8 = [(1, 1, 1, 128), (1, 3, 17, 128), (2, 1, 64, 256), (1, 16, 128, 1024), (3, 5, 257, 640), (1, 33, 1000, 384),
       (2, 65, 130, 256), (1, 256, 512, 512), (3, 100, 300, 128), (1, 530, 515, 896), (7, 1, 4096, 4096),
-      (1, 24, 40, 131072), (1, 130, 8200, 128), (1, 2050, 33, 256)]
+      (1, 24, 40, 131072), (1, 130, 8200, 128), (1, 2050, 33, 256), (2, 50, 70, 8192), (1, 66, 200, 16512)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
