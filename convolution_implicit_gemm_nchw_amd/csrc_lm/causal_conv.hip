@@ -295,7 +295,8 @@ int step_k(int B, int D, int silu, miconv_rows_t x, const void *state, int slots
 }  // namespace
 
 // Enough work-groups per channel to fill 256 CUs four deep, each with at least
-// 256 tiles of eight steps; fewer where the partial sums do not fit the budget.
+// 256 tiles of eight steps; fewer where the partial sums do not fit the budget.  (16 x 64 rows of
+// 8192, bf16: 23 us split 16 ways, 122 whole; 8 x 512 of 2048: 20.6 in two, 23.4 whole.)
 int causal_bwd_splits(const miconv_causal_conv_t &c, size_t budget) {
     const long long items = (long long)c.B * ((c.L + 7) / 8), one = (long long)c.D * (c.K + 1) * 4;
     long long s = 1024 / c.D;

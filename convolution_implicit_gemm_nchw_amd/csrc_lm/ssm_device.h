@@ -26,7 +26,7 @@ struct Elem<1> {
 // v[i] = row[t + i] for t + i < end, 0 from end on (not loaded).  t >= 0.
 template <int DT>
 DEVI void load8(const typename Elem<DT>::T *row, int t, int end, float (&v)[8]) {
-    if (t + 8 <= end) {
+    if (__builtin_expect(t + 8 <= end, 1)) {
         if constexpr (DT == 1) {
             const u32x4 r = *(const u32x4_row *)(row + t);
 #pragma unroll
@@ -75,7 +75,7 @@ struct Raw8 {
 template <int DT>
 DEVI Raw8<DT> fetch8(const typename Elem<DT>::T *row, int t, int end) {
     Raw8<DT> o;
-    if (t + 8 <= end) {
+    if (__builtin_expect(t + 8 <= end, 1)) {
         o.r[0] = *(const u32x4_row *)(row + t);
         if constexpr (DT == 0) o.r[1] = *(const u32x4_row *)(row + t + 4);
     } else {
@@ -128,7 +128,7 @@ DEVI void put_vec(u32x4 v, u32x4_row *to) {
 // row[t + i] = v[i] for t + i < end.  STREAM: past the caches, see streams().
 template <int DT, bool STREAM = false>
 DEVI void store8(typename Elem<DT>::T *row, int t, int end, const float (&v)[8]) {
-    if (t + 8 <= end) {
+    if (__builtin_expect(t + 8 <= end, 1)) {
         if constexpr (DT == 1) {
             u32x4 r;
 #pragma unroll
