@@ -170,7 +170,9 @@ SCAN = [(1, 1, 1, 1, 1, False, False, False, False, False),
         (1, 33, 70, 64, 1, False, True, False, True, True),
         (1, 2, 2600, 3, 1, True, True, False, True, True),
         (2, 3, 4400, 5, 1, True, True, True, True, True),          # few rows: the time axis split
-        (3, 17, 3200, 16, 1, False, True, True, True, True)]
+        (3, 17, 3200, 16, 1, False, True, True, True, True),
+        (2, 2110, 129, 5, 1, True, True, False, True, True),       # many rows: four per wave, several chunks
+        (3, 1500, 260, 3, 2, True, True, True, True, True)]
 
 
 def scan_data(case, dt):
