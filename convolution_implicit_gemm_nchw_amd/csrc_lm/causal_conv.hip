@@ -257,8 +257,8 @@ int fwd_k(const miconv_causal_conv_t &c, hipStream_t st) {
     const FDiv fd = make_fdiv((uint32_t)c.D);
     if (lg < 6)
         hipLaunchKernelGGL((causal_fwd_kernel<DT, K, false, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
-    else if (streams((size_t)c.B * c.D * c.L * sizeof(typename Elem<DT>::T)))
-        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, true>), grid, dim3(kThreads), 0, st, c, lg, fd);
+    else if (streams(DT, (size_t)c.B * c.D * c.L))
+        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, DT == 1>), grid, dim3(kThreads), 0, st, c, lg, fd);
     else
         hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;

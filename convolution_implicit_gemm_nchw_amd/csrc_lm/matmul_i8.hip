@@ -99,8 +99,9 @@ DEVI void finish8(const I8Args &a, int split, int r, int c, const int (&sum)[8],
 // FC x FR blocks of 32 x 32.  128 bytes of k of every row of the tile are brought
 // into LDS at a time, straight from memory (no registers in between), ST stages in
 // turn: the next ones load while this one is multiplied.  A row's eight
-// 16-byte pieces are stored at piece ^ (row & 7), so that the 32 rows that one
-// MFMA operand reads spread over all banks; since the load writes LDS in lane
+// 16-byte pieces are stored at piece ^ (row / 2 & 7): two rows span the 64 banks, so the
+// 16 rows that a part of an MFMA operand's read covers take 16 different places (with row & 7
+// a fifth of the time went to bank conflicts); since the load writes LDS in lane
 // order, the lanes fetch the pieces in that order instead.
 template <int WC, int WR, int FC, int FR, int ST>
 struct Tile {
@@ -115,7 +116,7 @@ struct Tile {
     };
 
     static DEVI void source(const I8Args &a, int c0, int r0, Src &s) {
-        const int row = threadIdx.x >> 3, piece = (threadIdx.x & 7) ^ (row & 7);
+        const int row = threadIdx.x >> 3, piece = (threadIdx.x & 7) ^ (row >> 1 & 7);
         s.rc = make_rsrc(a.c + (long long)c0 * a.K, 0x7fffffffu);
         s.rr = make_rsrc(a.r + (long long)r0 * a.K, 0x7fffffffu);
         // rows past the end read the last row; their results are not stored
@@ -149,7 +150,7 @@ struct Tile {
         const char *pc = lds + (wc * FC * 32 + row) * 128, *pr = lds + C * 128 + (wr * FR * 32 + row) * 128;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            const int piece = ((kk * 2 + half) ^ (row & 7)) * 16;
+            const int piece = ((kk * 2 + half) ^ (row >> 1 & 7)) * 16;
             i32x4 fc[FC], fr[FR];
 #pragma unroll
             for (int i = 0; i < FC; ++i) fc[i] = *(const i32x4 *)(pc + i * 32 * 128 + piece);
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
     for (int i = 0; i < ST - 1; ++i)
         if (first + i * 128 < end) X::load(src, stages + i * X::kBytes, first + i * 128);
     // what the epilogue needs from memory: a lane's columns' and one row's scale and bias
-    constexpr int kW = FC * 32, kMine = 32 * kW;
+    constexpr int kW = FC * 32, kMine = 32 * kW, kMix = kW >= 64 ? 15 : 7;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wc = wave % WC, wr = wave / WC;
     constexpr int kLanes = kW / 8;             // lanes per row, eight columns each
     const int col = (lane % kLanes) * 8, c = c0 + wc * kW + col;
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
                 i32x4 four;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) four[e] = acc[i][j][g * 4 + e];
-                const int row = lane & 31, piece = (i * 8 + g * 2 + (lane >> 5)) ^ (row & 7);
+                const int row = lane & 31, piece = (i * 8 + g * 2 + (lane >> 5)) ^ (row & kMix);
                 *(i32x4 *)(mine + row * kW + piece * 4) = four;
             }
         wave_lds_sync();
@@ -237,8 +238,8 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
             const int row = p * (64 / kLanes) + lane / kLanes, r = rw + row;
             const float rsr = __shfl(rs, j * 32 + row), rbr = __shfl(rb, j * 32 + row);
             if (r >= a.NR || c >= a.NC) continue;
-            const i32x4 lo = *(const i32x4 *)(mine + row * kW + ((col >> 2) ^ (row & 7)) * 4);
-            const i32x4 hi = *(const i32x4 *)(mine + row * kW + (((col >> 2) + 1) ^ (row & 7)) * 4);
+            const i32x4 lo = *(const i32x4 *)(mine + row * kW + ((col >> 2) ^ (row & kMix)) * 4);
+            const i32x4 hi = *(const i32x4 *)(mine + row * kW + (((col >> 2) + 1) ^ (row & kMix)) * 4);
             int sum[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -419,7 +420,7 @@ static int i8_by_size(const I8Args &a, int T, int O, int splits, hipStream_t st)
         // small tiles leave LDS room for four stages, which tall and narrow products (few tiles,
         // long k) need: 65 tokens, 4096 -> 8192: 17.4 us with two, 12.8 with four
         case 256:
-            if (streams((size_t)T * O * sizeof(typename Elem<OD>::T))) return tiled<OD, 2, 4, 4, 2, 2, true>(a, splits, st);
+            if (streams(OD, (size_t)T * O)) return tiled<OD, 2, 4, 4, 2, 2, OD == 1>(a, splits, st);
             return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
         case 128: return tiled<OD, 2, 2, 2, 2, 2>(a, splits, st);
         default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);

@@ -15,10 +15,12 @@ constexpr int kScanBwdChannels = 16;
 
 constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
-// Whether an output is written past the caches: from half of the 256 MB last-level cache on,
-// where the next reader would not find it there.  (Causal forward, bf16, followed by a read of
+// Whether an output is written past the caches: in bf16 from half of the 256 MB last-level cache
+// on, where the next reader would not find it there.  (Causal forward followed by a read of
 // its output: 128 MB 121 -> 106 us; 64 MB 50 -> 55 us, though the call alone falls from 31 to 25.)
-constexpr bool streams(size_t bytes) { return bytes >= (128u << 20); }
+// Not in fp32, where a lane's eight values are two stores that the caches have to join
+// (8192 x 8192 from 8-bit products 128 deep: 74 -> 101 us).
+constexpr bool streams(int dtype, size_t count) { return dtype == MICONV_BF16 && count * 2 >= (128u << 20); }
 
 // Time segments of the scan's forward pass that run side by side (1: none), their length,
 // and in the workspace the state before each segment [B][D][segs][N] and its sum of dt.
