@@ -6,9 +6,9 @@
 // channel-major y) takes the rows, called axis C below, because a lane's
 // accumulators run along the rows; the other is axis R.
 //
-// Many tokens are bound by the MFMAs under the power limit (8192 tokens, 4096 -> 8192: 250 us,
-// 2.2 POP/s with the output; on zeros a fifth less), few by the weight's bytes (8 tokens: 7.3 us,
-// 4.6 TB/s).
+// Many tokens are bound by the MFMAs under the power limit (8192 tokens, 4096 -> 8192: 233 us,
+// 2.36 POP/s with the output; on zeros 172 us, 3.2 POP/s), few by the weight's bytes (8 tokens:
+// 7.3 us, 4.6 TB/s).
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
@@ -108,6 +108,10 @@ struct Tile {
     static constexpr int kWaves = WC * WR, kThreads = 64 * kWaves;
     static constexpr int C = WC * FC * 32, R = WR * FR * 32;
     static constexpr int kBytes = (C + R) * 128;
+    // Waves of eight blocks read LDS as long as they multiply, and gain from reading ahead
+    // (8192 tokens, 8192 -> 8192: 456 -> 431 us); smaller ones lose (2048 tokens, 4096 -> 2048,
+    // in tiles of 128: 26.3 -> 27.2).
+    static constexpr bool kAhead = FC * FR >= 8;
     static constexpr int kRowsPerLoad = kWaves * 8, kLoads = (C + R) / kRowsPerLoad;   // per wave and stage
 
     struct Src {
@@ -132,36 +136,61 @@ struct Tile {
         }
     }
 
-    static DEVI void load(const Src &s, char *lds, int k) {
+    // Part 0 of a stage's loads is axis C's, part 1 axis R's.
+    static DEVI void load_axis(const Src &s, char *lds, int k, int part) {
         const int wave = uniform(threadIdx.x >> 6);
+        if (part == 0) {
 #pragma unroll
-        for (int i = 0; i < C / kRowsPerLoad; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rc, (lds_void *)(lds + (i * kWaves + wave) * 1024), 16, s.oc[i],
-                                                     k, 0, 0);
+            for (int i = 0; i < C / kRowsPerLoad; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rc, (lds_void *)(lds + (i * kWaves + wave) * 1024), 16,
+                                                         s.oc[i], k, 0, 0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < R / kRowsPerLoad; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rr, (lds_void *)(lds + C * 128 + (i * kWaves + wave) * 1024), 16,
-                                                     s.orr[i], k, 0, 0);
+            for (int i = 0; i < R / kRowsPerLoad; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rr, (lds_void *)(lds + C * 128 + (i * kWaves + wave) * 1024),
+                                                         16, s.orr[i], k, 0, 0);
+        }
     }
 
-    static DEVI void multiply(const char *lds, i32x16 (&acc)[FC][FR]) {
+    static DEVI void load(const Src &s, char *lds, int k) {
+        load_axis(s, lds, k, 0);
+        load_axis(s, lds, k, 1);
+    }
+
+    // The operands of 32 steps of k: a lane's 16 bytes of each block.
+    struct Frag {
+        i32x4 c[FC], r[FR];
+    };
+
+    static DEVI void fetch(const char *lds, int kk, Frag &f) {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         const int wc = wave % WC, wr = wave / WC, row = lane & 31, half = lane >> 5;
         const char *pc = lds + (wc * FC * 32 + row) * 128, *pr = lds + C * 128 + (wr * FR * 32 + row) * 128;
+        const int piece = ((kk * 2 + half) ^ (row >> 1 & 7)) * 16;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int piece = ((kk * 2 + half) ^ (row >> 1 & 7)) * 16;
-            i32x4 fc[FC], fr[FR];
+        for (int j = 0; j < FR; ++j) f.r[j] = *(const i32x4 *)(pr + j * 32 * 128 + piece);
 #pragma unroll
-            for (int i = 0; i < FC; ++i) fc[i] = *(const i32x4 *)(pc + i * 32 * 128 + piece);
+        for (int i = 0; i < FC; ++i) f.c[i] = *(const i32x4 *)(pc + i * 32 * 128 + piece);
+    }
+
+    static DEVI void multiply(const Frag &f, i32x16 (&acc)[FC][FR]) {
 #pragma unroll
-            for (int j = 0; j < FR; ++j) fr[j] = *(const i32x4 *)(pr + j * 32 * 128 + piece);
+        for (int i = 0; i < FC; ++i)
 #pragma unroll
-            for (int i = 0; i < FC; ++i)
+            for (int j = 0; j < FR; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.c[i], f.r[j], acc[i][j], 0, 0, 0);
+    }
+
+    // A read of LDS after each product, of those since the last call; by itself the compiler
+    // puts the reads first.
+    static DEVI void interleave() {
 #pragma unroll
-                for (int j = 0; j < FR; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fc[i], fr[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < FC + FR; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, FC * FR, 0);
+        __builtin_amdgcn_sched_barrier(0);
     }
 };
 
@@ -199,20 +228,68 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
     static_assert(FR <= 2, "one row's scale per lane");
     const int rl = r0 + wr * FR * 32 + lane, rc = rl < a.NR ? rl : a.NR - 1;
     const float rs = a.r_scale[rc], rb = a.r_bias ? a.r_bias[rc] : 0.0f;
-    int now = 0, next = ST - 1;
-    for (int k = first; k < end; k += 128) {
-        // this stage has arrived (each wave waits for its own loads, of which those of the
-        // ST - 2 stages after it may be in flight; the compiler does not always tie an LDS load
-        // to the reads behind the barrier), and the stage before has been read
-        if (ST > 2 && k + (ST - 2) * 128 < end)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((ST - 2) * X::kLoads) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (k + (ST - 1) * 128 < end) X::load(src, stages + next * X::kBytes, k + (ST - 1) * 128);
-        X::multiply(stages + now * X::kBytes, acc);
-        now = now + 1 < ST ? now + 1 : 0;
-        next = next + 1 < ST ? next + 1 : 0;
+    typename X::Frag f0, f1;
+    if constexpr (X::kAhead) {
+        // Operands are read one fragment ahead of the products, over the end of the stage: after
+        // its third fragment's products the next stage must have arrived and every wave have
+        // read this one, whose place the stage after next takes.  One half of its loads is
+        // issued there, the other a fragment later.
+        char *in = stages, *to = stages + X::kBytes;
+        const auto arrived = [] {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __syncthreads();
+        };
+        if (first + 128 < end) X::load_axis(src, to, first + 128, 0);
+        arrived();
+        X::fetch(in, 0, f0);
+        for (int k = first + 128; k < end; k += 128) {
+            X::load_axis(src, to, k, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            X::fetch(in, 1, f1);
+            X::multiply(f0, acc);
+            X::interleave();
+            X::fetch(in, 2, f0);
+            X::multiply(f1, acc);
+            X::interleave();
+            X::fetch(in, 3, f1);
+            X::multiply(f0, acc);
+            X::interleave();
+            arrived();
+            if (k + 128 < end) X::load_axis(src, in, k + 128, 0);
+            X::fetch(to, 0, f0);
+            X::multiply(f1, acc);
+            X::interleave();
+            char *const was = in;
+            in = to;
+            to = was;
+        }
+        X::fetch(in, 1, f1);
+        X::multiply(f0, acc);
+        X::fetch(in, 2, f0);
+        X::multiply(f1, acc);
+        X::fetch(in, 3, f1);
+        X::multiply(f0, acc);
+        X::multiply(f1, acc);
+    } else {
+        int now = 0, next = ST - 1;
+        for (int k = first; k < end; k += 128) {
+            // this stage has arrived (each wave waits for its own loads, of which those of the
+            // ST - 2 stages after it may be in flight; the compiler does not always tie an LDS
+            // load to the reads behind the barrier), and the stage before has been read
+            if (ST > 2 && k + (ST - 2) * 128 < end)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((ST - 2) * X::kLoads) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (k + (ST - 1) * 128 < end) X::load(src, stages + next * X::kBytes, k + (ST - 1) * 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                X::fetch(stages + now * X::kBytes, kk, f0);
+                X::multiply(f0, acc);
+            }
+            now = now + 1 < ST ? now + 1 : 0;
+            next = next + 1 < ST ? next + 1 : 0;
+        }
     }
     __syncthreads();
     // Through LDS, 32 rows of the wave's FC*32 columns at a time, so that y is written
