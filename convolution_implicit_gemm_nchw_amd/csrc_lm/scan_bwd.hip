@@ -67,6 +67,11 @@ DEVI void get_steps(const Steps &s, int group, int lane, float (&v)[8]) {
     }
 }
 
+// Where the rows of a work-group's channels and states start, kept in LDS: made from bases and
+// strides in every chunk they cost a tenth of the kernel's instructions, and held in registers
+// they spill.
+enum { kX, kDelta, kDy, kZ, kDx, kDdelta, kDz, kB, kC, kDB, kDC, kTable };
+
 struct Lds {
     Steps dt, dtx, e;                       // shared by the waves
     Steps sdt, sgB, sv;                     // sums over states: A g a h, g B, C h
@@ -74,7 +79,9 @@ struct Lds {
     float bc[kStates][2][2][16][4];         // B and C of the chunk: [state][B, C][half][lane of a row][4]
     float a2[kCh][kStates];                 // A log2(e)
     float carry[kCh][kStates];              // G of the step after the chunk
+    float none[kStates];                    // zeros: what the other lanes read in its place
     float dA[4][4][4][16];                  // [wave][turn][state][4 lanes of each row]
+    unsigned long long rows[kTable][16];    // addresses, see below
 };
 
 // Sums over the four rows of the wave: of u in rows 0, 1 and of v in rows 2, 3 (rows of a
@@ -100,6 +107,12 @@ DEVI P *at_row(const miconv_rows_t &r, int b, int d) {
     return (P *)r.data + b * r.stride_b + d * r.stride_d;
 }
 
+// An address of the table, which is known to be one of global memory.
+template <typename P>
+DEVI P *row_at(const Lds &m, int what, int i) {
+    return (P *)(__attribute__((address_space(1))) P *)m.rows[what][i];
+}
+
 template <int DT, int NS>
 __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOut o) {
     typedef typename Elem<DT>::T T;
@@ -118,9 +131,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     const int own = wave * 4 + row;
     const bool live = own < channels;
     const int d = first + (live ? own : 0);
-    const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
-    const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
     const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f, skip = s.D_skip ? s.D_skip[d] : 0.0f;
+    const bool gated = s.z.data != nullptr;
     for (int i = threadIdx.x; i < kCh * kStates; i += 256) {
         const int c = i / kStates, j = i % kStates;
         const bool used = c < channels && j < nn;
@@ -131,39 +143,63 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         m.carry[c][j] = used && G ? *G : 0.0f;
     }
     for (int i = threadIdx.x; i < 4 * 4 * 4 * 16; i += 256) (&m.dA[0][0][0][0])[i] = 0.0f;
+    if (threadIdx.x < kStates) m.none[threadIdx.x] = 0.0f;
+    if (threadIdx.x < 16) {
+        const int k = threadIdx.x, dk = first + (k < channels ? k : 0), n = o.n_first + (k < nn ? k : 0);
+        m.rows[kX][k] = (unsigned long long)at_row<const T>(s.x, b, dk);
+        m.rows[kDelta][k] = (unsigned long long)at_row<const T>(s.delta, b, dk);
+        m.rows[kDy][k] = (unsigned long long)at_row<const T>(s.dy, b, dk);
+        m.rows[kZ][k] = (unsigned long long)at_row<const T>(s.z.data ? s.z : s.x, b, dk);
+        m.rows[kDx][k] = (unsigned long long)at_row<T>(s.dx, b, dk);
+        m.rows[kDdelta][k] = (unsigned long long)at_row<T>(s.ddelta, b, dk);
+        m.rows[kDz][k] = s.z.data ? (unsigned long long)at_row<T>(s.dz, b, dk) : 0;
+        m.rows[kB][k] = (unsigned long long)((const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g + n * s.Bm.stride_n);
+        m.rows[kC][k] = (unsigned long long)((const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g + n * s.Cm.stride_n);
+        const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + n) * s.L;
+        m.rows[kDB][k] = (unsigned long long)(o.dB + at);
+        m.rows[kDC][k] = (unsigned long long)(o.dC + at);
+    }
+    __syncthreads();
     float sD = 0.0f, sb = 0.0f;
     const int end = live ? len : 0;
     // Chunks past the sequence's end: zeros.
     int c = c_end - 1;
     for (; c >= c_first && c * kT >= len; --c) {
-        const int t = c * kT + sub * 8, dv = again(d);
+        const int t = c * kT + sub * 8;
         const float zero[8] = {};
         if (live && t < s.L && o.last) {
-            store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, zero);
-            store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, zero);
-            if (s.dz.data) store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zero);
+            store8<DT>(row_at<T>(m, kDx, own), t, s.L, zero);
+            store8<DT>(row_at<T>(m, kDdelta, own), t, s.L, zero);
+            if (gated) store8<DT>(row_at<T>(m, kDz, own), t, s.L, zero);
         }
-        for (int i = wave * 4 + row; i < 2 * nn && t < s.L; i += 16) {
-            const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + o.n_first + (i >> 1)) * s.L;
-            store8<0>((i & 1 ? o.dC : o.dB) + at, t, s.L, zero);
-        }
+        for (int i = wave * 4 + row; i < 2 * nn && t < s.L; i += 16)
+            store8<0>(row_at<float>(m, i & 1 ? kDC : kDB, i >> 1), t, s.L, zero);
     }
     // What a chunk reads of its rows, fetched while the chunk before is finished.
     Raw8<DT> rx, rd, ry, rz, rbc[2];
     auto fetch = [&](int c) {
-        const int t = c * kT + sub * 8, dv = again(d);
-        rx = fetch8<DT>(at_row<const T>(s.x, b, dv), t, end);
-        rd = fetch8<DT>(at_row<const T>(s.delta, b, dv), t, end);
-        ry = fetch8<DT>(at_row<const T>(s.dy, b, dv), t, end);
-        rz = fetch8<DT>(at_row<const T>(s.z.data ? s.z : s.x, b, dv), t, end);
+        const int t = c * kT + sub * 8;
+        rx = fetch8<DT>(row_at<const T>(m, kX, own), t, end);
+        rd = fetch8<DT>(row_at<const T>(m, kDelta, own), t, end);
+        ry = fetch8<DT>(row_at<const T>(m, kDy, own), t, end);
+        rz = fetch8<DT>(row_at<const T>(m, kZ, own), t, end);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int i = threadIdx.x + k * 256, which = (i < nn * 32 ? i : 0) >> 4, n = o.n_first + (which >> 1);
-            rbc[k] = fetch8<DT>(which & 1 ? Cm + n * s.Cm.stride_n : Bm + n * s.Bm.stride_n, c * kT + sub * 8, len);
+            const int i = threadIdx.x + k * 256, which = (i < nn * 32 ? i : 0) >> 4;
+            rbc[k] = fetch8<DT>(row_at<const T>(m, which & 1 ? kC : kB, which >> 1), t, len);
         }
     };
     if (c >= c_first) fetch(c);
+    // Of the two work-groups that share a CU's ALUs the older one would be served first and leave
+    // the other to end alone, at half the ALUs' rate.  The one with more work left goes first, to
+    // a chunk's precision at the end (L 2048: 291 -> 263 us).
+    __builtin_amdgcn_s_setprio(3);
+    const int todo = c - c_first + 1;
     for (; c >= c_first; --c) {
+        const int left = c - c_first;
+        if (left == 0) __builtin_amdgcn_s_setprio(0);
+        else if (left * 8 <= todo) __builtin_amdgcn_s_setprio(1);
+        else if (left * 8 <= todo * 3) __builtin_amdgcn_s_setprio(2);
         const int t0 = c * kT, t = t0 + sub * 8;
         float dB[NS][8], dC[NS][8];
 #pragma unroll
@@ -186,7 +222,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                 widen8<DT>(rx, dtx);
                 widen8<DT>(rd, dt);
                 widen8<DT>(ry, e);
-                if (s.z.data) {
+                if (gated) {
                     float zv[8], zslope[8];
                     widen8<DT>(rz, zv);
 #pragma unroll
@@ -222,28 +258,20 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                         get_steps(m.sv, group, lane, sv);
                     }
                     float h0s[NS];
-                    const bool there = ch < channels;
+                    const bool there = ch < channels && sub == 0;
                     const float *entry = s.states + (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + o.n_first;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) h0s[j] = there && j0 + j < nn ? entry[j0 + j] : 0.0f;
                     float all = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) all += dt[i];
-                    float before = all, after = all;                      // inclusive sums along the row
-                    before += cross<kRowShr + 1>(before);
-                    before += cross<kRowShr + 2>(before);
-                    before += cross<kRowShr + 4>(before);
-                    before += cross<kRowShr + 8>(before);
-                    after += cross<kRowShl + 1>(after);
-                    after += cross<kRowShl + 2>(after);
-                    after += cross<kRowShl + 4>(after);
-                    after += cross<kRowShl + 8>(after);
+                    const float *const entry_G = sub == 15 ? &m.carry[ch][j0] : m.none;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) {
                         const int n = j0 + j;
                         if (n >= nn) break;
-                        const float a2 = m.a2[ch][n], G0 = m.carry[ch][n], h0 = h0s[j];
-                        float bv[8], cv[8], a[8], u[8], h = 0.0f, G = 0.0f;
+                        const float a2 = m.a2[ch][n], G0 = entry_G[j], h0 = h0s[j];       // of the row's end, else 0
+                        float bv[8], cv[8], a[8], u[8], h = h0, G = G0;
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const f32x4 fb = *(const f32x4 *)m.bc[n][0][q][sub], fc = *(const f32x4 *)m.bc[n][1][q][sub];
@@ -261,27 +289,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                         }
 #pragma unroll
                         for (int i = 7; i >= 0; --i) G = a[i] * __builtin_fmaf(cv[i], e[i], G);
-                        // both scans along the row; a lane without a source reads 0, after which
-                        // its product no longer matters
-                        float p = exp2_hw(all * a2), q = p;
-                        h = __builtin_fmaf(p, cross<kRowShr + 1>(h), h);
-                        G = __builtin_fmaf(q, cross<kRowShl + 1>(G), G);
-                        p *= cross<kRowShr + 1>(p);
-                        q *= cross<kRowShl + 1>(q);
-                        h = __builtin_fmaf(p, cross<kRowShr + 2>(h), h);
-                        G = __builtin_fmaf(q, cross<kRowShl + 2>(G), G);
-                        p *= cross<kRowShr + 2>(p);
-                        q *= cross<kRowShl + 2>(q);
-                        h = __builtin_fmaf(p, cross<kRowShr + 4>(h), h);
-                        G = __builtin_fmaf(q, cross<kRowShl + 4>(G), G);
-                        p *= cross<kRowShr + 4>(p);
-                        q *= cross<kRowShl + 4>(q);
-                        h = __builtin_fmaf(p, cross<kRowShr + 8>(h), h);
-                        G = __builtin_fmaf(q, cross<kRowShl + 8>(G), G);
-                        h = cross_or<kRowShr + 1>(h0, __builtin_fmaf(exp2_hw(before * a2), h0, h));
-                        const float Gend = __builtin_fmaf(exp2_hw(after * a2), G0, G);
-                        if (sub == 0) m.carry[ch][n] = Gend;
-                        G = cross_or<kRowShl + 1>(G0, Gend);
+                        scan_rows(h, G, exp2_hw(all * a2));
+                        if (sub == 0) m.carry[ch][n] = G;
+                        h = cross_or<kRowShr + 1>(h0, h);
+                        G = cross_or<kRowShl + 1>(G0, G);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float ah = a[i] * h;
@@ -302,7 +313,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                         }
                         sA += cross<kRowShr + 8>(sA);
                         sA += cross<kRowShr + 4>(sA);
-                        if (sub >= 12) m.dA[wave][turn][j][row * 4 + (sub & 3)] += sA;
+                        // (one lane adds to each place: the order is the program's)
+                        if (sub >= 12)
+                            __hip_atomic_fetch_add(&m.dA[wave][turn][j][row * 4 + (sub & 3)], sA, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_WORKGROUP);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     put_steps(m.sdt, group, lane, sdt);
@@ -315,9 +329,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         // this chunk's x and delta once more, and the next chunk's rows, while dB and dC leave
         Raw8<DT> ox, od;
         {
-            const int dv = again(d);
-            ox = fetch8<DT>(at_row<const T>(s.x, b, dv), t, end);
-            od = fetch8<DT>(at_row<const T>(s.delta, b, dv), t, end);
+            ox = fetch8<DT>(row_at<const T>(m, kX, own), t, end);
+            od = fetch8<DT>(row_at<const T>(m, kDelta, own), t, end);
         }
         fetch(c > c_first ? c - 1 : c);              // (without a condition: else the old values stay live)
         __builtin_amdgcn_sched_barrier(0);
@@ -331,20 +344,17 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = join_rows(join_halves(dB[j][i], dC[j][i]), join_halves(dB[j2][i], dC[j2][i]));
             const int n = j0 + (row & 1 ? j2 : j);
-            if (n < nn && t < s.L && !(NS == 1 && (row & 1))) {
-                const long long at = ((((long long)part * s.B + b) * s.G + g) * s.N + o.n_first + n) * s.L;
-                store8<0>((row & 2 ? o.dC : o.dB) + at, t, s.L, w);
-            }
+            if (n < nn && t < s.L && !(NS == 1 && (row & 1)))
+                store8<0>(row_at<float>(m, row & 2 ? kDC : kDB, n), t, s.L, w);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (live) {
-            const int dv = again(d);
             float sdt[8], sgB[8], sv[8], dt[8], e[8], xv[8];
             get_steps(m.sdt, wave, lane, sdt);
             get_steps(m.sgB, wave, lane, sgB);
             get_steps(m.sv, wave, lane, sv);
             if (o.sums) {
-                float *past = o.sums + ((long long)b * s.D + dv) * s.L;
+                float *past = o.sums + ((long long)b * s.D + d) * s.L;
                 const long long one = (long long)s.B * s.D * s.L;
                 if (o.n_first) {
                     float w[8];
@@ -367,17 +377,26 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             if (o.last) {
                 float slope[8];
                 widen8<DT>(od, slope);
+                if (s.softplus) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) slope[i] = t + i >= len ? 0.0f : s.softplus ? logistic_for<DT>(slope[i] + bias) : 1.0f;
+                    for (int i = 0; i < 8; ++i) slope[i] = logistic_for<DT>(slope[i] + bias);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) slope[i] = 1.0f;
+                }
+                if (t0 + kT > len) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) slope[i] = t + i < len ? slope[i] : 0.0f;
+                }
                 get_steps(m.dt, wave, lane, dt);
                 get_steps(m.e, wave, lane, e);
                 widen8<DT>(ox, xv);
-                if (s.z.data) {
+                if (gated) {
                     float zslope[8];
                     get_steps(m.zslope, wave, lane, zslope);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
-                    store8<DT>(at_row<T>(s.dz, b, dv), t, s.L, zslope);
+                    store8<DT>(row_at<T>(m, kDz, own), t, s.L, zslope);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -387,8 +406,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     sD = __builtin_fmaf(e[i], xv[i], sD);
                     sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
                 }
-                store8<DT>(at_row<T>(s.ddelta, b, dv), t, s.L, sdt);
-                store8<DT>(at_row<T>(s.dx, b, dv), t, s.L, sgB);
+                store8<DT>(row_at<T>(m, kDdelta, own), t, s.L, sdt);
+                store8<DT>(row_at<T>(m, kDx, own), t, s.L, sgB);
             }
         }
     }
@@ -405,7 +424,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     sD = row_sum(sD);
     sb = row_sum(sb);
     if (o.last && live && sub == 15) {
-        const long long at = ((long long)seg * s.B + b) * s.D + again(d);
+        const long long at = ((long long)seg * s.B + b) * s.D + d;
         o.dD[at] = sD;
         o.db[at] = sb;
     }
@@ -467,11 +486,11 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
         step_sizes(dt, bias, s.softplus, t, t0 + kCarryT, len);
 #pragma unroll
         for (int i = 0; i < kCarryItems; ++i) sum += dt[i];
-        const Sums sums = prefix_sums(sum);
         const int ends_here = t0 / kT + (64 - lane) / kEvery - 1;      // the chunk that ends where this lane begins
         const bool saves = live && lane % kEvery == 0 && ends_here * kT < stop;
-        if (out.segs > 1 && saves) out.after[row * chunks + ends_here] = later + (sums.all - sum);
-        later += lane_of(sums.all, 63);
+        const float sums = prefix_sum(sum);
+        if (out.segs > 1 && saves) out.after[row * chunks + ends_here] = later + (sums - sum);
+        later += lane_of(sums, 63);
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
             const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
             __syncthreads();
@@ -487,19 +506,16 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
             for (int k = 0; k < nn; ++k) {
                 const int n = n0 + k;
                 const float a2 = lane_of(a_lane, n), G0 = lane_of(carried, n);
-                float G = 0.0f;
+                float G = lane == 0 ? G0 : 0.0f;
 #pragma unroll
                 for (int i = kCarryItems - 4; i >= 0; i -= 4) {
                     const f32x4 c = *(const f32x4 *)(cs[k] + i * 64 + lane * 4);
 #pragma unroll
                     for (int j = 3; j >= 0; --j) G = exp2_hw(dt[i + j] * a2) * __builtin_fmaf(c[j], e[i + j], G);
                 }
-                G = scan_rows(G, a2, sums);
-                G = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(G), G);
-                G = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(G), G);
-                const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), G0, G);
-                carried = keep(carried, end, n);
-                G = cross_or<kWaveShr1>(G0, end);
+                G = scan_lanes<64>(G, exp2_hw(a2 * sum));
+                carried = keep(carried, G, n);
+                G = cross_or<kWaveShr1>(G0, G);
                 if (saves) out.G[(row * chunks + ends_here) * s.N + n] = G;
             }
         }

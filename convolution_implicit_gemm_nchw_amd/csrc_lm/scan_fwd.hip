@@ -92,7 +92,6 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
             v[i] = skip * xv[i];
             xv[i] *= dt[i];
         }
-        const Sums sums = prefix_sums(sum);
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
             const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
             __syncthreads();
@@ -118,7 +117,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                     h0 = h_rows[my][n];
                 }
                 const float *pb = bc + k * 2 * kT + sub * 4, *pc = pb + kT;
-                float a[ITEMS], bv[ITEMS], h = 0.0f;
+                float a[ITEMS], bv[ITEMS], h = sub == 0 ? h0 : 0.0f;
 #pragma unroll
                 for (int i = 0; i < ITEMS; i += 4) {
                     const f32x4 q = *(const f32x4 *)(pb + i * LANES);
@@ -129,17 +128,13 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                         h = __builtin_fmaf(a[i + e], h, bv[i + e]);
                     }
                 }
-                h = scan_rows(h, a2, sums);
+                h = scan_lanes<LANES>(h, exp2_hw(a2 * sum));
                 if constexpr (LANES == 64) {
-                    h = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(h), h);
-                    h = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(h), h);
-                    const float end = __builtin_fmaf(exp2_hw(a2 * sums.all), h0, h);
-                    carried = keep(carried, end, n);
-                    h = cross_or<kWaveShr1>(h0, end);
+                    carried = keep(carried, h, n);
+                    h = cross_or<kWaveShr1>(h0, h);
                 } else {
-                    const float end = __builtin_fmaf(exp2_hw(a2 * sums.row), h0, h);
-                    if (sub == LANES - 1) h_rows[my][n] = end;
-                    h = cross_or<kRowShr + 1>(h0, end);
+                    if (sub == LANES - 1) h_rows[my][n] = h;
+                    h = cross_or<kRowShr + 1>(h0, h);
                 }
                 // lanes at the start of a saved chunk hold its entry state
                 if (s.states && live && sub % kEvery == 0 && c + sub / kEvery < saved)
@@ -222,8 +217,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_local_kernel(miconv_s
             sum += dt[i];
             xv[i] *= dt[i];
         }
-        const Sums sums = prefix_sums(sum);
-        total += lane_of(sums.all, 63);
+        total += lane_of(prefix_sum(sum), 63);
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
             const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
             __syncthreads();
@@ -239,17 +233,15 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_local_kernel(miconv_s
             for (int k = 0; k < nn; ++k) {
                 const int n = n0 + k;
                 const float a2 = lane_of(a_lane, n);
-                float h = 0.0f;
+                const float h0 = lane_of(carried, n);
+                float h = lane == 0 ? h0 : 0.0f;
 #pragma unroll
                 for (int i = 0; i < ITEMS; i += 4) {
                     const f32x4 q = *(const f32x4 *)(bs[k] + i * 64 + lane * 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) h = __builtin_fmaf(exp2_hw(dt[i + e] * a2), h, q[e] * xv[i + e]);
                 }
-                h = scan_rows(h, a2, sums);
-                h = __builtin_fmaf(exp2_hw(a2 * sums.row), cross<kRowBcast15, 0xa>(h), h);
-                h = __builtin_fmaf(exp2_hw(a2 * sums.half), cross<kRowBcast31, 0xc>(h), h);
-                h = __builtin_fmaf(exp2_hw(a2 * sums.all), lane_of(carried, n), h);
+                h = scan_lanes<64>(h, exp2_hw(a2 * sum));
                 carried = keep(carried, h, n);
             }
         }

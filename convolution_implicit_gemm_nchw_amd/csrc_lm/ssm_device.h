@@ -163,7 +163,7 @@ constexpr float kLog2eLow = 1.92596299112661746887e-8f;   // log2(e) - kLog2e
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // exp(v) for v <= 0 with the rounding of v*log2(e) put right: the plain product
-// is off by |v| 2^-24 relative, which a step size of softplus(-7) would keep.
+// is off by |v| 2^-24 relative.
 DEVI float exp_neg(float v) {
     const float t = v * kLog2e;
     const float r = __builtin_fmaf(v, kLog2eLow, __builtin_fmaf(v, kLog2e, -t));
@@ -180,9 +180,8 @@ DEVI float logistic(float v) {
 
 // The logistic function of gates and slopes, for operands of DT's type.  With bf16 operands
 // the plain exponential serves, at a third of the instructions: its relative error |v| 2^-23
-// stays far below the operands' own half step, 2^-9 (and that of a bf16 result).  In the
-// step size it would not do: there an error is multiplied by the length of the memory.
-// exp(-v) = inf gives 0.
+// stays far below the operands' own half step, 2^-9 (and that of a bf16 result).  exp(-v) = inf
+// gives 0.
 template <int DT>
 DEVI float logistic_for(float v) {
     if constexpr (DT == 1)
@@ -192,20 +191,20 @@ DEVI float logistic_for(float v) {
 }
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], with
-// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: the odd series, whose first term
-// left out is s^16/17 <= 2e-9 of the sum.  No cancellation at either end.
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: s times a polynomial in s^2 whose relative
+// error's extremes are equal, 2^-27 (the series itself would need three terms more).  No
+// cancellation at either end.  The rounding of |v| log2(e) stays in: it is worth |v| 2^-24 of e,
+// as much as half a step of v itself.  Found to be within 4 + |v| half steps of the result.
 DEVI float softplus(float v) {
-    const float e = exp_neg(-__builtin_fabsf(v));
+    const float e = exp2_hw(__builtin_fabsf(v) * -kLog2e);
     const float s = e * rcp_hw(2.0f + e), q = s * s;
-    float p = 2.0f / 15.0f;
-    p = __builtin_fmaf(p, q, 2.0f / 13.0f);
-    p = __builtin_fmaf(p, q, 2.0f / 11.0f);
-    p = __builtin_fmaf(p, q, 2.0f / 9.0f);
-    p = __builtin_fmaf(p, q, 2.0f / 7.0f);
-    p = __builtin_fmaf(p, q, 2.0f / 5.0f);
-    p = __builtin_fmaf(p, q, 2.0f / 3.0f);
+    float p = 0.28178334f;
+    p = __builtin_fmaf(p, q, 0.27960601f);
+    p = __builtin_fmaf(p, q, 0.40024909f);
+    p = __builtin_fmaf(p, q, 0.66666317f);
     p = __builtin_fmaf(p, q, 2.0f);
-    return (v > 0.0f ? v : 0.0f) + s * p;
+    const int bits = __float_as_int(v);        // its maximum with 0 is max(v, 0), in one instruction
+    return __builtin_fmaf(s, p, __int_as_float(bits > 0 ? bits : 0));
 }
 
 // Lane crossings of a wave of 64 in four rows of 16.
@@ -227,41 +226,72 @@ DEVI float cross_or(float other, float v) {
 }
 DEVI float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
 
-// Prefix sums of the lanes' dt: within rows of 16, halves of 32 and the whole wave.
-struct Sums {
-    float own, row, half, all;
-};
-
-DEVI Sums prefix_sums(float own) {
-    Sums s;
-    s.own = own;
-    float v = own;
+// Sums of v over the lanes up to each one.
+DEVI float prefix_sum(float v) {
     v += cross<kRowShr + 1>(v);
     v += cross<kRowShr + 2>(v);
     v += cross<kRowShr + 4>(v);
     v += cross<kRowShr + 8>(v);
-    s.row = v;
     v += cross<kRowBcast15, 0xa>(v);
-    s.half = v;
-    v += cross<kRowBcast31, 0xc>(v);
-    s.all = v;
-    return s;
+    return v + cross<kRowBcast31, 0xc>(v);
 }
 
-// The lanes' maps (product of decays, state from zero) combined along the wave: the
-// state after each lane's steps from a zero state before lane 0.  The product over a
-// range of steps is the exponential of the sum of dt, so only those that the first
-// steps need are multiplied up; a lane without a source reads 0, after which its
-// product no longer matters.
-DEVI float scan_rows(float h, float a2, const Sums &s) {
-    float p = exp2_hw(a2 * s.own);
-    h = __builtin_fmaf(p, cross<kRowShr + 1>(h), h);
-    p *= cross<kRowShr + 1>(p);
-    h = __builtin_fmaf(p, cross<kRowShr + 2>(h), h);
-    p *= cross<kRowShr + 2>(p);
-    h = __builtin_fmaf(p, cross<kRowShr + 4>(h), h);
-    p *= cross<kRowShr + 4>(p);
-    return __builtin_fmaf(p, cross<kRowShr + 8>(h), h);
+// Scans of the lanes' maps v -> p v + h (the product of a lane's decays, its state from zero):
+// h becomes the state after the lane's steps, from the first lane's h on, which includes
+// what entered it.  A step adds p times the source lane's h and multiplies p by its p; a lane
+// without a source stays as it is.  Written as instructions, because the compiler takes two
+// for the crossing and the fma where one does both.  A crossing may read a
+// register that a vector instruction wrote only after two wait states, which the compiler does not
+// count in here: between dependent instructions stand two others or an s_nop.
+//
+// Along each row of 16, h upwards and g downwards, both by p:
+DEVI void scan_rows(float &h, float &g, float p) {
+    float q = p;
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %0, %2 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %1, %3 row_shl:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %2, %2 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %3, %3 row_shl:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %0, %2 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %1, %3 row_shl:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %2, %2 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %3, %3 row_shl:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %0, %2 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %1, %3 row_shl:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %2, %2 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %3, %3 row_shl:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %0, %2 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %1, %3 row_shl:8 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1"
+        : "+v"(h), "+v"(g), "+v"(p), "+v"(q));
+}
+
+// Upwards, along each row of 16 or the whole wave:
+template <int LANES>
+DEVI float scan_lanes(float h, float p) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %0, %1 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %1, %1 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 0\n\t"
+        "v_fmac_f32_dpp %0, %0, %1 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %1, %1 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 0\n\t"
+        "v_fmac_f32_dpp %0, %0, %1 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %1, %1 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 0\n\t"
+        "v_fmac_f32_dpp %0, %0, %1 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %1, %1 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 0"
+        : "+v"(h), "+v"(p));
+    if constexpr (LANES == 64)
+        asm("s_nop 0\n\t"
+            "v_fmac_f32_dpp %0, %0, %1 row_bcast:15 row_mask:0xa bank_mask:0xf\n\t"
+            "v_mul_f32_dpp %1, %1, %1 row_bcast:15 row_mask:0xa bank_mask:0xf\n\t"
+            "s_nop 0\n\t"
+            "v_fmac_f32_dpp %0, %0, %1 row_bcast:31 row_mask:0xc bank_mask:0xf\n\t"
+            "s_nop 1"
+            : "+v"(h), "+v"(p));
+    return h;
 }
 
 // `held` with lane n's value replaced by lane 63's of v.  (The lane is read ahead of the choice:
@@ -289,9 +319,10 @@ DEVI void wave_lds_sync() {
 template <int N>
 DEVI void step_sizes(float (&dt)[N], float bias, int use_softplus, int t, int chunk_end, int end) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        dt[i] += bias;
-        if (use_softplus) dt[i] = softplus(dt[i]);
+    for (int i = 0; i < N; ++i) dt[i] += bias;
+    if (use_softplus) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dt[i] = softplus(dt[i]);
     }
     if (chunk_end > end) {
 #pragma unroll
