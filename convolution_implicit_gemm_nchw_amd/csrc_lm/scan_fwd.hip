@@ -76,6 +76,13 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
         }
         wave_lds_sync();
     }
+    // Work-groups that share a CU: the older one would be served first and the last one end alone,
+    // at a part of the ALUs' rate.  The one with more stages left goes first (2 x 4096 rows of 2048:
+    // 98 -> 90 us, of 4096: 178 -> 163; 3 x 1536 of 1000, fp32, whose last work-groups start as the first
+    // end: 43 -> 45).
+    __builtin_amdgcn_s_setprio(3);
+    const int stages = ((len < stop ? len : stop) - start + kT - 1) / kT * ((s.N + kStage - 1) / kStage);
+    int left = stages;
     int t0 = start;
     for (; t0 < len && t0 < stop; t0 += kT) {
         const int c = t0 / kScanChunk, t = t0 + sub * ITEMS;
@@ -94,6 +101,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
         }
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
             const int nn = s.N - n0 < kStage ? s.N - n0 : kStage;
+            --left;
+            if (left == 0) __builtin_amdgcn_s_setprio(0);
+            else if (left * 4 <= stages) __builtin_amdgcn_s_setprio(1);
+            else if (left * 2 <= stages) __builtin_amdgcn_s_setprio(2);
             __syncthreads();
             // where this thread's eight steps of a staged row are, and go to
             const int tid = again(threadIdx.x), at = tid % (kT / 8) * 8;
