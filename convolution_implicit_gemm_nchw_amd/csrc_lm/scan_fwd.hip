@@ -10,12 +10,12 @@
 // Bound by the vector ALUs, not by memory: a (step, state) pair costs seven slots of
 // four cycles -- argument, exponential (two), input, and a multiply-add each for the two
 // runs and for C h -- against 8 bytes per step for N = 16 pairs of them (bf16).  So
-//   - the lane crossings are DPP moves, and the decay over a range of lanes is the
-//     exponential of a sum of dt, which does not depend on n;
-//   - 16 steps per lane where the row is long enough: a scan costs about 36 slots;
+//   - a lane crossing of the scan is part of its fma (DPP), and what enters the chunk is
+//     the first lane's start: the scan costs 26 slots;
+//   - 16 steps per lane where the row is long enough to share it;
 //   - B and C are widened to fp32 once per work-group, in LDS, for its channels.
-// 1 x 4096 rows of 4096, N 16, bf16: 107 us, 2.5 T pairs/s; 12 instructions per pair with the
-// per-step work (softplus, gate, conversions, staging), the ALUs busy 86 % of the time.
+// 1 x 4096 rows of 4096, N 16, bf16: 90 us, 3.0 T pairs/s; 10.5 instructions per pair with the
+// per-step work (softplus, gate, conversions, staging), the ALUs busy 87 % of the time.
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
@@ -374,11 +374,11 @@ namespace {
 
 // Which form of the kernel takes a problem: the one with the least work on the longest CU.
 // A work-group's time per chunk, N = 16 bf16, alone on its CU and where two share it, in us:
-// 64 lanes x 16 steps 14.5 and 24, 64 x 8 8.7 and 14.8, four rows of 16 x 8 6.7 and 11.4.
-// So many long rows take 64 x 16 (2 x 4096 rows of 2048: 99 against 119 and 121 us), a
-// length just past a chunk or many short rows take 16 x 8 (2 x 4096 rows of 129: 17 against
-// 54 and 33; of 1200: 77 against 103 and 90), few rows of a few hundred 64 x 8 (2048 rows of
-// 300: 14 against 23 and 24).
+// 64 lanes x 16 steps 14 and 20.3, 64 x 8 8.4 and 11.7, four rows of 16 x 8 7.2 and 9.9.
+// So many long rows take 64 x 16 (2 x 4096 rows of 2048: 81 against 91 and 117 us), lengths
+// just past its chunk 64 x 8 (of 1536: 71 against 81 and 89), a length just past a chunk or
+// many short rows 16 x 8 (of 129: 16 against 46 and 29; of 300: 24 against 48 and 31), few rows of
+// a few hundred 64 x 8 (2048 rows of 300: 12 against 20 and 23).
 enum ScanForm { kLong, kMiddle, kRows };
 
 double form_cost(const miconv_scan_t &s, int rows, int steps, double alone, double shared) {
@@ -387,8 +387,8 @@ double form_cost(const miconv_scan_t &s, int rows, int steps, double alone, doub
 }
 
 ScanForm scan_form(const miconv_scan_t &s) {
-    const double a = form_cost(s, kScanWaves, 1024, 14.5, 24.0), b = form_cost(s, kScanWaves, 512, 8.7, 14.8),
-                 c = form_cost(s, 4 * kScanWaves, 128, 6.7, 11.4);
+    const double a = form_cost(s, kScanWaves, 1024, 14.0, 20.3), b = form_cost(s, kScanWaves, 512, 8.4, 11.7),
+                 c = form_cost(s, 4 * kScanWaves, 128, 7.2, 9.9);
     return a <= b && a <= c ? kLong : (b <= c ? kMiddle : kRows);
 }
 
