@@ -464,12 +464,13 @@ long long tile_count(long long T, long long O, int side) {
     return ((T + side - 1) / side) * ((O + side - 1) / side);
 }
 
-// Side of the square tile: the largest that gives most of the 256 CUs a tile.  4096 deep, in us:
-// 128 tiles of 256 57.7 against 39.7 with side 128, 176 tiles 57.7 against 58.7, 208 58.9
-// against 67.4; 1024 deep: 126 tiles of 128 10.3 against 7.4 with side 64, 169 10.5 against 10.9.
+// Side of the square tile: the largest that gives most of the 256 CUs a tile.  In us: 128 tiles of
+// 256, 4096 deep, 52.6 against 41.7 with side 128; 144 tiles 52.6 against 58.9 (1024 deep 23.4 against
+// 22.1); 128 tiles of 128, 4096 deep, 23.2 against 17.1 with side 64; 144 tiles, 2048 deep, 12.7
+// against 15.9.
 int tile_side(int T, int O) {
-    if (tile_count(T, O, 256) >= 176) return 256;
-    if (tile_count(T, O, 128) >= 160) return 128;
+    if (tile_count(T, O, 256) >= 140) return 256;
+    if (tile_count(T, O, 128) >= 140) return 128;
     return 64;
 }
 
@@ -499,7 +500,12 @@ static int i8_by_size(const I8Args &a, int T, int O, int splits, hipStream_t st)
         case 256:
             if (streams(OD, (size_t)T * O)) return tiled<OD, 2, 4, 4, 2, 2, OD == 1>(a, splits, st);
             return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
-        case 128: return tiled<OD, 2, 2, 2, 2, 2>(a, splits, st);
+        // eight waves of a block pair each rather than four of four (1300 tokens, 2048 -> 2048: 15.0 ->
+        // 12.8 us).  Two stages let two work-groups share a CU; where each has its own and k is
+        // long, four hide more (2048 tokens, 4096 -> 2048: 27.0 -> 25.1 us; 2048 deep 14.6 -> 15.1)
+        case 128:
+            if (tile_count(T, O, 128) * splits <= 256 && a.K >= 4096) return tiled<OD, 4, 2, 1, 2, 4>(a, splits, st);
+            return tiled<OD, 4, 2, 1, 2, 2>(a, splits, st);
         default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);
     }
 }
