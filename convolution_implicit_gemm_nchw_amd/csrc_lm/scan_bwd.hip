@@ -23,8 +23,9 @@
 //   - the sums over states meet in LDS: in turn i wave w works on group (i + w) mod 4, so
 //     every group has one wave at a time adding to it, in a fixed order.
 // The 16-channel sums of dB and dC go to the workspace and are added in order by a
-// second kernel.  More than 16 states are taken 16 per launch; the sums over the states
-// of the earlier launches wait in the workspace.
+// second kernel.  More than 16 states are taken 16 per launch, the sums over the states
+// of the earlier launches waiting in the workspace, or, where a launch leaves CUs without a
+// work-group, by work-groups side by side, whose sums another kernel adds and finishes.
 //
 // 2 x 4096 rows of 2048, N 16, bf16: 238 us and 23 us for the second kernel; 27 instructions per
 // pair (17 in the states' loop), the ALUs busy 82 % of the time.
@@ -44,9 +45,10 @@ struct BwdOut {
     float *dA, *dD, *db;      // [segs][B][D][N], [segs][B][D], [segs][B][D]
     const float *G;           // [B][D][chunks][N] G of the step after each chunk, or null: one segment
     int segs, seg_chunks;     // time segments (a work-group each), chunks of one
-    float *sums;              // [3][B][D][L] sums over the states of earlier launches, or null
+    float *sums;              // [3][B][D][L] sums over the states of earlier launches, or null; side by side
+                              // [blocks of 16 states] of them
     int parts;
-    int n_first, n_end, last; // states of this launch; whether it is the last one
+    int n_first, n_end, last; // states of this launch (side by side: 16 per blockIdx.y); whether it finishes
 };
 
 // Per-step values of the 16 channels: [group][half][64 lanes][4 steps].
@@ -102,6 +104,46 @@ DEVI float row_sum(float v) {          // in the last lane of each row
     return v + cross<kRowShr + 8>(v);
 }
 
+// e = dy silu(z) in place of dy, and dy silu'(z).
+template <int DT>
+DEVI void gate(float (&e)[8], const float (&z)[8], float (&zslope)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float sg = logistic_for<DT>(z[i]);
+        zslope[i] = e[i] * (sg * __builtin_fmaf(z[i], 1.0f - sg, 1.0f));
+        e[i] *= z[i] * sg;
+    }
+}
+
+// The derivative of the step size in place of delta, 0 past the end.
+template <int DT>
+DEVI void slopes(float (&v)[8], float bias, int use_softplus, int t, int chunk_end, int len) {
+    if (use_softplus) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = logistic_for<DT>(v[i] + bias);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+    }
+    if (chunk_end > len) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = t + i < len ? v[i] : 0.0f;
+    }
+}
+
+// From the sums over the states (that of A g a h was taken with A log2(e)) to d(delta) and
+// dx, and the sums over time of the bias's and D's gradients.
+DEVI void finish_steps(const float (&x)[8], const float (&slope)[8], const float (&dt)[8], const float (&e)[8], float skip,
+                       float (&sdt)[8], float (&sgB)[8], float &sb, float &sD) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        sdt[i] = __builtin_fmaf(x[i], sgB[i], sdt[i] * kLn2) * slope[i];
+        sb += sdt[i];
+        sD = __builtin_fmaf(e[i], x[i], sD);
+        sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
+    }
+}
+
 template <typename P>
 DEVI P *at_row(const miconv_rows_t &r, int b, int d) {
     return (P *)r.data + b * r.stride_b + d * r.stride_d;
@@ -123,7 +165,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     const int g = bg % s.G, b = bg / s.G;
     const int first = g * per_group + part * kCh;                        // the work-group's first channel
     const int channels = per_group - part * kCh < kCh ? per_group - part * kCh : kCh;
-    const int nn = o.n_end - o.n_first, j0 = wave * NS;                  // states of the launch, of the wave
+    const int n_first = o.n_first + blockIdx.y * kStates;                // states of the work-group, of the wave
+    const int nn = o.n_end - n_first < kStates ? o.n_end - n_first : kStates, j0 = wave * NS;
     const int len = valid_steps(s.lengths, b, s.L);
     const int chunks = (s.L + kT - 1) / kT;
     const int c_first = seg * o.seg_chunks, c_end = c_first + o.seg_chunks < chunks ? c_first + o.seg_chunks : chunks;
@@ -136,16 +179,16 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     for (int i = threadIdx.x; i < kCh * kStates; i += 256) {
         const int c = i / kStates, j = i % kStates;
         const bool used = c < channels && j < nn;
-        const long long at = ((long long)b * s.D + first + c) * s.N + o.n_first + j;
-        m.a2[c][j] = used ? s.A[(long long)(first + c) * s.N + o.n_first + j] * kLog2e : 0.0f;
-        const float *G = c_end < chunks ? o.G + (((long long)b * s.D + first + c) * chunks + c_end - 1) * s.N + o.n_first + j
+        const long long at = ((long long)b * s.D + first + c) * s.N + n_first + j;
+        m.a2[c][j] = used ? s.A[(long long)(first + c) * s.N + n_first + j] * kLog2e : 0.0f;
+        const float *G = c_end < chunks ? o.G + (((long long)b * s.D + first + c) * chunks + c_end - 1) * s.N + n_first + j
                                         : (s.d_final_state ? s.d_final_state + at : nullptr);
         m.carry[c][j] = used && G ? *G : 0.0f;
     }
     for (int i = threadIdx.x; i < 4 * 4 * 4 * 16; i += 256) (&m.dA[0][0][0][0])[i] = 0.0f;
     if (threadIdx.x < kStates) m.none[threadIdx.x] = 0.0f;
     if (threadIdx.x < 16) {
-        const int k = threadIdx.x, dk = first + (k < channels ? k : 0), n = o.n_first + (k < nn ? k : 0);
+        const int k = threadIdx.x, dk = first + (k < channels ? k : 0), n = n_first + (k < nn ? k : 0);
         m.rows[kX][k] = (unsigned long long)at_row<const T>(s.x, b, dk);
         m.rows[kDelta][k] = (unsigned long long)at_row<const T>(s.delta, b, dk);
         m.rows[kDy][k] = (unsigned long long)at_row<const T>(s.dy, b, dk);
@@ -225,12 +268,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                 if (gated) {
                     float zv[8], zslope[8];
                     widen8<DT>(rz, zv);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float sg = logistic_for<DT>(zv[i]);
-                        zslope[i] = e[i] * (sg * __builtin_fmaf(zv[i], 1.0f - sg, 1.0f));
-                        e[i] *= zv[i] * sg;
-                    }
+                    gate<DT>(e, zv, zslope);
                     put_steps(m.zslope, wave, lane, zslope);
                 }
                 step_sizes(dt, bias, s.softplus, t, live ? t0 + kT : len + 1, end);
@@ -259,7 +297,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     }
                     float h0s[NS];
                     const bool there = ch < channels && sub == 0;
-                    const float *entry = s.states + (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + o.n_first;
+                    const float *entry = s.states + (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + n_first;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) h0s[j] = there && j0 + j < nn ? entry[j0 + j] : 0.0f;
                     float all = 0.0f;
@@ -354,8 +392,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             get_steps(m.sgB, wave, lane, sgB);
             get_steps(m.sv, wave, lane, sv);
             if (o.sums) {
-                float *past = o.sums + ((long long)b * s.D + d) * s.L;
                 const long long one = (long long)s.B * s.D * s.L;
+                float *past = o.sums + 3 * one * blockIdx.y + ((long long)b * s.D + again(d)) * s.L;
                 if (o.n_first) {
                     float w[8];
                     load8<0>(past, t, len, w);
@@ -377,17 +415,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             if (o.last) {
                 float slope[8];
                 widen8<DT>(od, slope);
-                if (s.softplus) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) slope[i] = logistic_for<DT>(slope[i] + bias);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) slope[i] = 1.0f;
-                }
-                if (t0 + kT > len) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) slope[i] = t + i < len ? slope[i] : 0.0f;
-                }
+                slopes<DT>(slope, bias, s.softplus, t, t0 + kT, len);
                 get_steps(m.dt, wave, lane, dt);
                 get_steps(m.e, wave, lane, e);
                 widen8<DT>(ox, xv);
@@ -398,14 +426,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
                     store8<DT>(row_at<T>(m, kDz, own), t, s.L, zslope);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // the states' sum was taken with A log2(e)
-                    sdt[i] = __builtin_fmaf(xv[i], sgB[i], sdt[i] * kLn2) * slope[i];
-                    sb += sdt[i];
-                    sD = __builtin_fmaf(e[i], xv[i], sD);
-                    sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
-                }
+                finish_steps(xv, slope, dt, e, skip, sdt, sgB, sb, sD);
                 store8<DT>(row_at<T>(m, kDdelta, own), t, s.L, sdt);
                 store8<DT>(row_at<T>(m, kDx, own), t, s.L, sgB);
             }
@@ -417,7 +438,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         if (c >= channels || j >= nn) continue;
         const int w = j / NS, turn = (c / 4 - w) & 3;
         const float *v = m.dA[w][turn][j % NS] + (c & 3) * 4;
-        const long long at = ((long long)b * s.D + first + c) * s.N + o.n_first + j;
+        const long long at = ((long long)b * s.D + first + c) * s.N + n_first + j;
         o.dA[(long long)seg * s.B * s.D * s.N + at] = (v[0] + v[1]) + (v[2] + v[3]);
         if (s.d_initial_state && seg == 0) s.d_initial_state[at] = m.carry[c][j];
     }
@@ -427,6 +448,54 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         const long long at = ((long long)seg * s.B + b) * s.D + d;
         o.dD[at] = sD;
         o.db[at] = sb;
+    }
+}
+
+// Side by side: the blocks' sums added in order, then what the last of successive launches does.
+// A wave per row, eight steps a lane.
+template <int DT>
+__global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, BwdOut o, int blocks) {
+    typedef typename Elem<DT>::T T;
+    const int lane = threadIdx.x & 63;
+    const long long row = (long long)blockIdx.x * 4 + uniform(threadIdx.x >> 6), rows = (long long)s.B * s.D;
+    if (row >= rows) return;
+    const int b = (int)(row / s.D), d = (int)(row - (long long)b * s.D), len = valid_steps(s.lengths, b, s.L);
+    const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f, skip = s.D_skip ? s.D_skip[d] : 0.0f;
+    float sD = 0.0f, sb = 0.0f;
+    for (int t = lane * 8; t < s.L; t += 512) {
+        float sum[3][8] = {}, x[8], dt[8], e[8], slope[8];
+        for (int k = 0; k < blocks; ++k)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                float w[8];
+                load8<0>(o.sums + ((k * 3 + j) * rows + row) * s.L, t, len, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[j][i] += w[i];
+            }
+        load8<DT>(at_row<const T>(s.x, b, d), t, len, x);
+        load8<DT>(at_row<const T>(s.delta, b, d), t, len, dt);
+        load8<DT>(at_row<const T>(s.dy, b, d), t, len, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) slope[i] = dt[i];
+        slopes<DT>(slope, bias, s.softplus, t, t + 8, len);
+        step_sizes(dt, bias, s.softplus, t, t + 8, len);
+        if (s.z.data) {
+            float z[8], zslope[8];
+            load8<DT>(at_row<const T>(s.z, b, d), t, len, z);
+            gate<DT>(e, z, zslope);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, x[i], sum[2][i]);
+            store8<DT>(at_row<T>(s.dz, b, d), t, s.L, zslope);
+        }
+        finish_steps(x, slope, dt, e, skip, sum[0], sum[1], sb, sD);
+        store8<DT>(at_row<T>(s.ddelta, b, d), t, s.L, sum[0]);
+        store8<DT>(at_row<T>(s.dx, b, d), t, s.L, sum[1]);
+    }
+    sD = prefix_sum(sD);
+    sb = prefix_sum(sb);
+    if (lane == 63) {
+        o.dD[row] = sD;
+        o.db[row] = sb;
     }
 }
 
@@ -610,6 +679,10 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     if (segs > chunks) segs = chunks;
     p.seg_chunks = (int)((chunks + segs - 1) / segs);
     p.segs = (chunks + p.seg_chunks - 1) / p.seg_chunks;
+    // blocks of 16 states side by side where one of them leaves CUs without a second work-group (64
+    // states, bf16: 1024 rows of 300 170 -> 64 us, 4096 of 128 81 -> 62, 4 x 100 of 2, with the
+    // forward pass, 106 -> 58; a block of one state costs: 17 states, 4096 rows of 100 45 -> 48)
+    p.beside = s.N > kStates && groups * p.segs <= 256 ? (s.N + kStates - 1) / kStates : 1;
     const size_t bc = (size_t)p.parts * s.B * s.G * s.N * s.L, bd = (size_t)s.B * s.D;
     p.off_dB = 0;
     p.off_dC = bc;
@@ -631,7 +704,7 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     p.off_ends = p.off_G + (p.segs > 1 ? bd * chunks * s.N : 0);
     p.off_after = p.off_ends + (p.carry_segs > 1 ? bd * p.carry_segs * (s.N + 1) : 0);
     p.off_sums = p.off_after + (p.carry_segs > 1 ? bd * chunks : 0);
-    p.bytes = (p.off_sums + (s.N > kStates ? 3 * bd * s.L : 0)) * 4;
+    p.bytes = (p.off_sums + (s.N > kStates ? 3 * bd * s.L * p.beside : 0)) * 4;
     return p;
 }
 
@@ -661,11 +734,12 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
                                0, st, s, out);
         if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
     }
-    const dim3 grid((unsigned)((long long)s.B * s.G * p.parts * p.segs));
-    for (int n = 0; n < s.N; n += kStates) {
+    const dim3 grid((unsigned)((long long)s.B * s.G * p.parts * p.segs), (unsigned)p.beside);
+    const int per_launch = kStates * p.beside;
+    for (int n = 0; n < s.N; n += per_launch) {
         o.n_first = n;
-        o.n_end = s.N < n + kStates ? s.N : n + kStates;
-        o.last = o.n_end == s.N;
+        o.n_end = s.N < n + per_launch ? s.N : n + per_launch;
+        o.last = p.beside == 1 && o.n_end == s.N;
         const int nn = o.n_end - n;
         // as few states per wave as give each of the four waves some
         const void *kern = nn <= 4   ? (dtype ? (const void *)scan_bwd_kernel<1, 1> : (const void *)scan_bwd_kernel<0, 1>)
@@ -675,13 +749,22 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
         void *args[] = {(void *)&a, (void *)&o};
         if (hipLaunchKernel(kern, grid, dim3(256), args, 0, st) != hipSuccess) return MICONV_ERR_HIP;
     }
+    const int time_parts = p.beside > 1 ? 1 : p.segs;     // of dD and the bias's gradient
+    if (p.beside > 1) {
+        const dim3 rows((unsigned)(((long long)s.B * s.D + 3) / 4));
+        if (dtype)
+            hipLaunchKernelGGL(scan_bwd_finish_kernel<1>, rows, dim3(256), 0, st, s, o, p.beside);
+        else
+            hipLaunchKernelGGL(scan_bwd_finish_kernel<0>, rows, dim3(256), 0, st, s, o, p.beside);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    }
     SumJobs jobs = {};
     const long long bc = (long long)s.B * s.G * s.N * s.L;
     jobs.j[jobs.count++] = {o.dB, s.dB, bc, p.parts};
     jobs.j[jobs.count++] = {o.dC, s.dC, bc, p.parts};
     jobs.j[jobs.count++] = {o.dA, s.dA, (long long)s.D * s.N, s.B * p.segs};
-    if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B * p.segs};
-    if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B * p.segs};
+    if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B * time_parts};
+    if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B * time_parts};
     for (int k = 0; k < jobs.count; ++k) jobs.first[k + 1] = jobs.first[k] + (jobs.j[k].n + 255) / 256;
     hipLaunchKernelGGL(scan_bwd_sum, dim3((unsigned)jobs.first[jobs.count]), dim3(256), 0, st, jobs);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;

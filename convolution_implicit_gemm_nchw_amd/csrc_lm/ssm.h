@@ -35,6 +35,7 @@ ScanSplit plan_scan_fwd(const miconv_scan_t &s, size_t budget);
 // that run side by side, and offsets.
 struct ScanBwdPlan {
     int parts, segs, seg_chunks;
+    int beside;                         // blocks of 16 states in one launch (1: one after the other)
     int carry_segs, carry_steps;        // time segments of the pass that finds G between them
     size_t off_G, off_ends, off_after, off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
 };

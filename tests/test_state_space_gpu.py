@@ -255,6 +255,20 @@ def test_scan(mc, case, dt):
         assert t is None or torch.equal(t, again[name]), name      # bitwise repeatable
 
 
+# more than 16 states where the channels alone fill the card: one block of 16 after the other
+# (few channels, in SCAN, take them side by side)
+BLOCKS = [(5, 848, 9, 33, 1, True, True, True, True, True),
+          (3, 1400, 131, 17, 1, False, True, True, False, True),
+          (9, 470, 2, 64, 1, True, False, False, True, False),
+          (1, 40, 1, 50, 2, True, True, False, True, True)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", BLOCKS, ids=lambda c: "-".join(map(str, c)))
+def test_scan_of_many_states(mc, case, dt):
+    test_scan(mc, case, dt)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("N,G", [(1, 1), (5, 2), (16, 1), (64, 2)])
 def test_scan_step_continues_the_prompt(mc, dt, N, G):
