@@ -672,18 +672,39 @@ __global__ __launch_bounds__(64 * kSumWaves) void scan_bwd_sum(SumJobs jobs) {
 
 }  // namespace
 
-// Where the groups of 16 channels alone give the 256 CUs (two work-groups each) less than
-// half of what they hold, the time axis is split too, at the price of a pass that finds G
-// between the segments.
+// Where the groups of 16 channels give the 256 CUs (two work-groups each) half of what they hold or less,
+// the time axis can be split too, at the price of a pass that finds G between the segments.
+// It is where the estimate for N = 16, bf16 gains: a chunk takes 11 us of a work-group alone on its CU and 14 of
+// two, 1024 steps of the pass between 12 and 20 (4096 rows of 512: 60 us whole, 68 in two; of 1024: 105 and
+// 95; 1024 rows of 256: 32 and 35; of 512: 54 and 37).
 ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     ScanBwdPlan p;
     p.parts = (s.D / s.G + kCh - 1) / kCh;
     const long long groups = (long long)s.B * s.G * p.parts;
     const int chunks = scan_chunks(s.L);
-    long long segs = groups * 2 <= 512 && chunks >= 4 ? 512 / groups : 1;
-    if (segs > chunks) segs = chunks;
-    p.seg_chunks = (int)((chunks + segs - 1) / segs);
-    p.segs = (chunks + p.seg_chunks - 1) / p.seg_chunks;
+    p.segs = 1;
+    p.seg_chunks = chunks;
+    p.carry_segs = 1;
+    p.carry_steps = 0;
+    if (groups * 2 <= 512 && chunks > 1) {
+        const long long segs = 512 / groups < chunks ? 512 / groups : chunks;
+        const int seg_chunks = (int)((chunks + segs - 1) / segs);
+        // the pass between the segments is split as the forward scan is
+        const long long rows_groups = (long long)s.B * s.G * ((s.D / s.G + kCarryWaves - 1) / kCarryWaves);
+        const int long_chunks = (s.L + kCarryT - 1) / kCarryT;
+        int per = long_chunks;
+        if (rows_groups <= 128 && long_chunks >= 3) {
+            const long long n = 512 / rows_groups < long_chunks ? 512 / rows_groups : long_chunks;
+            per = (int)((long_chunks + n - 1) / n);
+        }
+        const double between = 3 + per * (rows_groups <= 256 ? 12.0 : rows_groups <= 512 ? 20.0 : 20.0 * rows_groups / 512);
+        if (seg_chunks * (groups * segs <= 256 ? 11.0 : 14.0) + between < chunks * 11.0) {
+            p.seg_chunks = seg_chunks;
+            p.segs = (chunks + seg_chunks - 1) / seg_chunks;
+            p.carry_segs = (long_chunks + per - 1) / per;
+            p.carry_steps = per < long_chunks ? per * kCarryT : 0;
+        }
+    }
     // blocks of 16 states side by side where one of them leaves CUs without a second work-group (64
     // states, bf16: 1024 rows of 300 170 -> 64 us, 4096 of 128 81 -> 62, 4 x 100 of 2, with the
     // forward pass, 106 -> 58; a block of one state costs: 17 states, 4096 rows of 100 45 -> 48)
@@ -694,17 +715,6 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     p.off_dA = 2 * bc;
     p.off_dD = p.off_dA + bd * s.N * p.segs;
     p.off_db = p.off_dD + bd * p.segs;
-    // the pass between the segments is split as the forward scan is
-    const long long rows_groups = (long long)s.B * s.G * ((s.D / s.G + kCarryWaves - 1) / kCarryWaves);
-    const int long_chunks = (s.L + kCarryT - 1) / kCarryT;
-    p.carry_segs = 1;
-    p.carry_steps = 0;
-    if (p.segs > 1 && rows_groups <= 128 && long_chunks >= 3) {
-        const long long n = 512 / rows_groups < long_chunks ? 512 / rows_groups : long_chunks;
-        const int per = (int)((long_chunks + n - 1) / n);
-        p.carry_segs = (long_chunks + per - 1) / per;
-        p.carry_steps = per * kCarryT;
-    }
     p.off_G = p.off_db + bd * p.segs;
     p.off_ends = p.off_G + (p.segs > 1 ? bd * chunks * s.N : 0);
     p.off_after = p.off_ends + (p.carry_segs > 1 ? bd * p.carry_segs * (s.N + 1) : 0);
