@@ -26,26 +26,29 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Work-groups of 8 waves; 64 lanes x 16 or 8 steps per row, or four rows of 16 lanes x 8 or
-// 16 steps per wave.
+// Work-groups of 8 waves; 64 lanes x 16 or 8 steps per row, or four rows of 16 lanes x 8 steps per
+// wave.  SHARE: the waves take the same four rows and an eighth of the states each, their parts of
+// v meeting in LDS: few short rows then wait for N / 8 states rather than N.
 constexpr int kScanWaves = 8;
 
-template <int DT, int LANES, int ITEMS>
+template <int DT, int LANES, int ITEMS, bool SHARE = false>
 __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g, ScanSplit split) {
     typedef typename Elem<DT>::T T;
     constexpr int kT = LANES * ITEMS, kRows = 64 / LANES, kEvery = kScanChunk / ITEMS, kPairs = kT * 2 * 4;   // bytes of B and C per state
-    constexpr int kStage = 65536 / kPairs < 16 ? 65536 / kPairs : 16;            // states staged at a time
+    constexpr int kStage = SHARE ? 32 : 65536 / kPairs < 16 ? 65536 / kPairs : 16;            // states staged at a time
     // [state][B, C][ITEMS / 4][LANES][4]: a lane reads four steps as 16 bytes next to its neighbours'
     __shared__ __attribute__((aligned(16))) float bc[kStage * 2 * kT];
     // 16 lanes per row: A[n] log2(e) and the state n between chunks, of each row
-    __shared__ float a_rows[LANES == 16 ? kScanWaves * kRows : 1][MICONV_SCAN_MAX_STATES];
-    __shared__ float h_rows[LANES == 16 ? kScanWaves * kRows : 1][MICONV_SCAN_MAX_STATES];
+    constexpr int kHeld = LANES == 64 ? 1 : SHARE ? kRows : kScanWaves * kRows;
+    __shared__ float a_rows[kHeld][MICONV_SCAN_MAX_STATES], h_rows[kHeld][MICONV_SCAN_MAX_STATES];
+    // SHARE: the waves' parts of v, [wave][row][step]
+    __shared__ __attribute__((aligned(16))) float parts[SHARE ? kScanWaves * kRows * kT : 1];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), sub = lane % LANES;
     const int per_group = s.D / s.G;
     const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g % (s.B * s.G), g = bg % s.G, b = bg / s.G;
     const int seg = blockIdx.x / (blocks_g * s.B * s.G), start = seg * split.steps;
     const int stop = split.segs == 1 || s.L - start < split.steps ? s.L : start + split.steps;
-    const int in_group = (blk * kScanWaves + wave) * kRows + lane / LANES;
+    const int in_group = (SHARE ? blk : blk * kScanWaves + wave) * kRows + lane / LANES;
     const bool live = in_group < per_group;              // the last work-group's other rows only help to stage
     const int d = g * per_group + (live ? in_group : 0);
     const long long row = (long long)b * s.D + d;
@@ -59,7 +62,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     const float skip = s.D_skip ? s.D_skip[d] : 0.0f, bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
     const int saved = scan_chunks(s.L);
     // 64 lanes per row: lane n holds them for state n
-    const int my = LANES == 16 ? wave * kRows + lane / LANES : 0;
+    const int my = LANES == 64 ? 0 : (SHARE ? 0 : wave * kRows) + lane / LANES;
+    // SHARE: wave w has the states w, w + 8, ...
+    constexpr int kStride = SHARE ? kScanWaves : 1;
+    const int n_mine = SHARE ? wave : 0;
     float carried = 0.0f, a_lane = 0.0f;
     if constexpr (LANES == 64) {
         if (lane < s.N) {
@@ -70,7 +76,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
             a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
         }
     } else {
-        for (int n = sub; n < s.N; n += LANES) {
+        for (int n = n_mine + sub * kStride; n < s.N; n += LANES * kStride) {
             h_rows[my][n] = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
             a_rows[my][n] = s.A[(long long)d * s.N + n] * kLog2e;
         }
@@ -96,7 +102,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             sum += dt[i];
-            v[i] = skip * xv[i];
+            v[i] = !SHARE || wave == 0 ? skip * xv[i] : 0.0f;
             xv[i] *= dt[i];
         }
         for (int n0 = 0; n0 < s.N; n0 += kStage) {
@@ -117,7 +123,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                 *(f32x4 *)(to + which * kT + LANES * 4) = f32x4{w[4], w[5], w[6], w[7]};
             }
             __syncthreads();
-            for (int k = 0; k < nn; ++k) {
+            for (int k = n_mine; k < nn; k += kStride) {
                 const int n = n0 + k;
                 float a2, h0;
                 if constexpr (LANES == 64) {
@@ -161,7 +167,25 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                 }
             }
         }
-        if (live) {
+        if constexpr (SHARE) {
+            float *const to = parts + (wave * kRows + lane / LANES) * kT + sub * ITEMS;
+#pragma unroll
+            for (int i = 0; i < ITEMS; i += 4) *(f32x4 *)(to + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+            __syncthreads();
+            static_assert(kRows * kT == 64 * kScanWaves, "a step of a row per thread");
+            const int r = threadIdx.x / kT, step = threadIdx.x % kT, at = t0 + step, dr = blk * kRows + r;
+            if (dr < per_group && at < s.L) {
+                const int dd = g * per_group + dr;
+                float out = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kScanWaves; ++w) out += parts[(w * kRows + r) * kT + step];
+                if (s.z.data && at < len) {
+                    const float zv = Elem<DT>::get(((const T *)s.z.data + b * s.z.stride_b + dd * s.z.stride_d)[at]);
+                    out *= zv * logistic_for<DT>(zv);
+                }
+                ((T *)s.y.data + b * s.y.stride_b + dd * s.y.stride_d)[at] = Elem<DT>::put(at < len ? out : 0.0f);
+            }
+        } else if (live) {
 #pragma unroll
             for (int q = 0; q < ITEMS; q += 8) {
                 float (&out)[8] = *(float (*)[8])(v + q);
@@ -178,13 +202,14 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     }
     if (!live) return;
     if constexpr (LANES == 16) wave_lds_sync();
-    for (int n = sub; n < s.N; n += LANES) {
+    for (int n = n_mine + sub * kStride; n < s.N; n += LANES * kStride) {
         const float h = LANES == 64 ? carried : h_rows[my][n];
         if (s.final_state && stop == s.L) s.final_state[row * s.N + n] = h;
         // chunks past the end: the state stays
         if (s.states)
             for (int c = t0 / kScanChunk; c * kScanChunk < stop; ++c) s.states[(row * saved + c) * s.N + n] = h;
     }
+    if (SHARE && wave) return;
     for (int t = t0 + sub * 8; t < stop; t += LANES * 8) {
         const float zero[8] = {};
         store8<DT>(y, t, s.L, zero);
@@ -362,11 +387,11 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
 
 }  // namespace
 
-template <int DT, int LANES, int ITEMS>
+template <int DT, int LANES, int ITEMS, bool SHARE = false>
 static int scan_fwd(const miconv_scan_t &s, const ScanSplit &split, hipStream_t st) {
-    const int rows = kScanWaves * (64 / LANES), blocks_g = (s.D / s.G + rows - 1) / rows;
+    const int rows = (SHARE ? 1 : kScanWaves) * (64 / LANES), blocks_g = (s.D / s.G + rows - 1) / rows;
     const dim3 grid((unsigned)((long long)s.B * s.G * blocks_g * split.segs));
-    hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS>), grid, dim3(64 * kScanWaves), 0, st, s, blocks_g, split);
+    hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS, SHARE>), grid, dim3(64 * kScanWaves), 0, st, s, blocks_g, split);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 
@@ -374,12 +399,15 @@ namespace {
 
 // Which form of the kernel takes a problem: the one with the least work on the longest CU.
 // A work-group's time per chunk, N = 16 bf16, alone on its CU and where two share it, in us:
-// 64 lanes x 16 steps 14 and 20.3, 64 x 8 8.4 and 11.7, four rows of 16 x 8 7.2 and 9.9.
+// 64 lanes x 16 steps 14 and 20.3, 64 x 8 8.4 and 11.7, four rows of 16 x 8 7.2 and 9.9, the same with
+// the eight waves sharing four rows' states 2.5 and 3.5 (5 where more than two wait for a CU).
 // So many long rows take 64 x 16 (2 x 4096 rows of 2048: 81 against 91 and 117 us), lengths
 // just past its chunk 64 x 8 (of 1536: 71 against 81 and 89), a length just past a chunk or
 // many short rows 16 x 8 (of 129: 16 against 46 and 29; of 300: 24 against 48 and 31), few rows of
-// a few hundred 64 x 8 (2048 rows of 300: 12 against 20 and 23).
-enum ScanForm { kLong, kMiddle, kRows };
+// a few hundred 64 x 8 (1024 rows of 500: 12.6 against 19.7, 30 and 13.5), few short rows the
+// shared form (1024 rows of 2: 5.7 against 10, of 256: 7.9 against 11.3; 64 states, of 128: 8.2
+// against 25, of 1000: 47 against 52).
+enum ScanForm { kLong, kMiddle, kRows, kShared };
 
 double form_cost(const miconv_scan_t &s, int rows, int steps, double alone, double shared) {
     const double groups = (double)s.B * s.G * ((s.D / s.G + rows - 1) / rows), chunks = (s.L + steps - 1) / steps;
@@ -387,8 +415,13 @@ double form_cost(const miconv_scan_t &s, int rows, int steps, double alone, doub
 }
 
 ScanForm scan_form(const miconv_scan_t &s) {
-    const double a = form_cost(s, kScanWaves, 1024, 14.0, 20.3), b = form_cost(s, kScanWaves, 512, 8.4, 11.7),
-                 c = form_cost(s, 4 * kScanWaves, 128, 7.2, 9.9);
+    const double per_state = 0.2 + 0.05 * s.N;                       // of the times at N = 16
+    const double a = per_state * form_cost(s, kScanWaves, 1024, 14.0, 20.3),
+                 b = per_state * form_cost(s, kScanWaves, 512, 8.4, 11.7),
+                 c = per_state * form_cost(s, 4 * kScanWaves, 128, 7.2, 9.9);
+    const double groups = (double)s.B * s.G * ((s.D / s.G + 3) / 4), chunks = (s.L + 127) / 128;
+    const double d = (0.64 + 0.0225 * s.N) * chunks * (groups <= 256 ? 2.5 : groups <= 512 ? 3.5 : groups / 512 * 5.0);
+    if (d < a && d < b && d < c) return kShared;
     return a <= b && a <= c ? kLong : (b <= c ? kMiddle : kRows);
 }
 
@@ -432,6 +465,7 @@ int launch_scan_fwd(const miconv_scan_t &s, int dtype, ScanSplit split, float *w
     switch (scan_form(s)) {
         case kLong: return dtype ? scan_fwd<1, 64, 16>(s, split, st) : scan_fwd<0, 64, 16>(s, split, st);
         case kMiddle: return dtype ? scan_fwd<1, 64, 8>(s, split, st) : scan_fwd<0, 64, 8>(s, split, st);
+        case kShared: return dtype ? scan_fwd<1, 16, 8, true>(s, split, st) : scan_fwd<0, 16, 8, true>(s, split, st);
         default: return dtype ? scan_fwd<1, 16, 8>(s, split, st) : scan_fwd<0, 16, 8>(s, split, st);
     }
 }
