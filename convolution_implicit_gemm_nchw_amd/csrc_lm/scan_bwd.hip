@@ -27,8 +27,8 @@
 // of the earlier launches waiting in the workspace, or, where a launch leaves CUs without a
 // work-group, by work-groups side by side, whose sums another kernel adds and finishes.
 //
-// 2 x 4096 rows of 2048, N 16, bf16: 238 us and 23 us for the second kernel; 27 instructions per
-// pair (17 in the states' loop), the ALUs busy 82 % of the time.
+// 2 x 4096 rows of 2048, N 16, bf16: 260 us, 22 of them the second kernel's; 27 instructions per
+// pair (17 in the states' loop), the ALUs busy 81 % of the time.
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
