@@ -677,10 +677,13 @@ for _name, _args in {
         "selective_scan_bwd": [_VP, _I, _VP, _SZ, _VP],
         "selective_scan_states_size": [_I, _I, _I, _I, _SZP],
         "selective_scan_bwd_workspace_size": [_VP, _I, _SZP],
+        "selective_scan_fwd_describe": [_VP, _I, _SZ, ctypes.c_char_p, _SZ],
+        "selective_scan_bwd_describe": [_VP, _I, ctypes.c_char_p, _SZ],
         "selective_scan_step": [_VP, _I, _VP, _I, _VP, _VP, _VP],
         "quantize_tokens": [_I, _I, _I, _I, _VP, _LL, _LL, _LL, _VP, _VP, _VP],
         "matmul_i8": [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _SZ, _VP],
-        "matmul_i8_workspace_size": [_I, _I, _I, _I, _SZ, _SZP]}.items():
+        "matmul_i8_workspace_size": [_I, _I, _I, _I, _SZ, _SZP],
+        "matmul_i8_describe": [_I, _I, _I, _I, _SZ, ctypes.c_char_p, _SZ]}.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _I
@@ -762,6 +765,22 @@ def selective_scan_step(x, delta, A, B, C, state, D=None, z=None, delta_bias=Non
                  state_out, slots, y)
 
 
+def selective_scan_fwd_describe(B, D, L, N, G=1, dtype=F32, workspace_bytes=MAX_WORKSPACE_BYTES):
+    """The form of the kernel and the time segments that selective_scan_fwd takes for these sizes."""
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.selective_scan_fwd_describe(ctypes.byref(_Scan(B=B, D=D, L=L, N=N, G=G)), dtype, workspace_bytes, buf, 256),
+           "selective_scan_fwd_describe")
+    return buf.value.decode()
+
+
+def selective_scan_bwd_describe(B, D, L, N, G=1, dtype=F32):
+    """The time segments and blocks of states that selective_scan_bwd takes for these sizes."""
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.selective_scan_bwd_describe(ctypes.byref(_Scan(B=B, D=D, L=L, N=N, G=G)), dtype, buf, 256),
+           "selective_scan_bwd_describe")
+    return buf.value.decode()
+
+
 I8_PAD = 128
 
 
@@ -782,3 +801,10 @@ def matmul_i8(q, scale, wq, wscale, bias=None, out_dtype=torch.float32, length=N
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"unsupported dtype {out_dtype}; expected float32 or bfloat16")
     return _call(_bind.matmul_i8, stream, q, scale, wq, wscale, bias, out_dtype is torch.bfloat16, length, y, workspace)
+
+
+def matmul_i8_describe(tokens, O, C_pad, workspace_bytes=MAX_WORKSPACE_BYTES):
+    """The kernel that matmul_i8 takes for these sizes: few tokens, or tile, stages and splits."""
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.matmul_i8_describe(1, tokens, O, C_pad, workspace_bytes, buf, 256), "matmul_i8_describe")
+    return buf.value.decode()

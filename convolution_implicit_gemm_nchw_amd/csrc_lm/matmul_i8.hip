@@ -492,19 +492,27 @@ int i8_splits(int T, int O, int K, size_t budget) {
     return (steps + per - 1) / per;            // no empty split
 }
 
+I8Form i8_form(int T, int O, int K, int splits) {
+    if (T <= kFewTokens) return {T <= 16 ? 1 : (T <= 32 ? 2 : 4), 0, 0};
+    const int side = tile_side(T, O);
+    // small tiles leave LDS room for four stages, which tall and narrow products (few tiles,
+    // long k) need: 65 tokens, 4096 -> 8192: 17.4 us with two, 12.8 with four.  Of the 128-tiles two
+    // stages let two work-groups share a CU; where each has its own and k is long, four hide
+    // more (2048 tokens, 4096 -> 2048: 27.0 -> 25.1 us; 2048 deep 14.6 -> 15.1)
+    const bool four = side == 64 || (side == 128 && tile_count(T, O, 128) * splits <= 256 && K >= 4096);
+    return {0, side, four ? 4 : 2};
+}
+
 template <int OD>
-static int i8_by_size(const I8Args &a, int T, int O, int splits, hipStream_t st) {
-    switch (tile_side(T, O)) {
-        // small tiles leave LDS room for four stages, which tall and narrow products (few tiles,
-        // long k) need: 65 tokens, 4096 -> 8192: 17.4 us with two, 12.8 with four
+static int i8_by_form(const I8Args &a, const I8Form &f, bool stream, int splits, hipStream_t st) {
+    switch (f.side) {
         case 256:
-            if (streams(OD, (size_t)T * O)) return tiled<OD, 2, 4, 4, 2, 2, OD == 1>(a, splits, st);
+            if (stream) return tiled<OD, 2, 4, 4, 2, 2, OD == 1>(a, splits, st);
             return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
         // eight waves of a block pair each rather than four of four (1300 tokens, 2048 -> 2048: 15.0 ->
-        // 12.8 us).  Two stages let two work-groups share a CU; where each has its own and k is
-        // long, four hide more (2048 tokens, 4096 -> 2048: 27.0 -> 25.1 us; 2048 deep 14.6 -> 15.1)
+        // 12.8 us)
         case 128:
-            if (tile_count(T, O, 128) * splits <= 256 && a.K >= 4096) return tiled<OD, 4, 2, 1, 2, 4>(a, splits, st);
+            if (f.stages == 4) return tiled<OD, 4, 2, 1, 2, 4>(a, splits, st);
             return tiled<OD, 4, 2, 1, 2, 2>(a, splits, st);
         default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);
     }
@@ -514,14 +522,14 @@ int launch_matmul_i8(int B, int L, int O, int K, const signed char *q, const flo
                      const float *ws, const float *bias, int channel_major, int out_dtype, void *y, int splits,
                      int *part, hipStream_t st) {
     const int T = B * L;
-    if (T <= kFewTokens) {
-        const int ft = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
+    const I8Form f = i8_form(T, O, K, splits);
+    if (f.few) {
 #define MICONV_FEW(FT)                                                                            \
     (out_dtype ? few<1, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st)                \
                : few<0, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st))
-        if (ft == 1)
+        if (f.few == 1)
             MICONV_FEW(1);
-        else if (ft == 2)
+        else if (f.few == 2)
             MICONV_FEW(2);
         else
             MICONV_FEW(4);
@@ -542,7 +550,8 @@ int launch_matmul_i8(int B, int L, int O, int K, const signed char *q, const flo
         a.r = q; a.r_scale = qs; a.NR = T;
         a.row = O;
     }
-    return out_dtype ? i8_by_size<1>(a, T, O, splits, st) : i8_by_size<0>(a, T, O, splits, st);
+    const bool stream = streams(out_dtype, (size_t)T * O);
+    return out_dtype ? i8_by_form<1>(a, f, stream, splits, st) : i8_by_form<0>(a, f, stream, splits, st);
 }
 
 }  // namespace miconv

@@ -407,14 +407,12 @@ namespace {
 // a few hundred 64 x 8 (1024 rows of 500: 12.6 against 19.7, 30 and 13.5), few short rows the
 // shared form (1024 rows of 2: 5.7 against 10, of 256: 7.9 against 11.3; 64 states, of 128: 8.2
 // against 25, of 1000: 47 against 52).
-enum ScanForm { kLong, kMiddle, kRows, kShared };
-
 double form_cost(const miconv_scan_t &s, int rows, int steps, double alone, double shared) {
     const double groups = (double)s.B * s.G * ((s.D / s.G + rows - 1) / rows), chunks = (s.L + steps - 1) / steps;
     return chunks * (groups <= 256 ? alone : shared * (groups < 512 ? 1.0 : groups / 512));
 }
 
-ScanForm scan_form(const miconv_scan_t &s) {
+ScanForm cheapest_form(const miconv_scan_t &s) {
     const double per_state = 0.2 + 0.05 * s.N;                       // of the times at N = 16
     const double a = per_state * form_cost(s, kScanWaves, 1024, 14.0, 20.3),
                  b = per_state * form_cost(s, kScanWaves, 512, 8.4, 11.7),
@@ -426,6 +424,9 @@ ScanForm scan_form(const miconv_scan_t &s) {
 }
 
 }  // namespace
+
+// (time segments are whole chunks of 64 x 16)
+ScanForm scan_form(const miconv_scan_t &s, const ScanSplit &split) { return split.segs > 1 ? kLong : cheapest_form(s); }
 
 // The time axis is split where the rows alone leave half of the CUs without work and a row
 // has at least three chunks of 1024: each segment costs its local state's pass (two thirds of
@@ -460,9 +461,8 @@ int launch_scan_fwd(const miconv_scan_t &s, int dtype, ScanSplit split, float *w
         hipLaunchKernelGGL(scan_chain_kernel, dim3((unsigned)((rows * s.N + kThreads - 1) / kThreads)), dim3(kThreads), 0,
                            st, s, split);
         if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
-        return dtype ? scan_fwd<1, 64, 16>(s, split, st) : scan_fwd<0, 64, 16>(s, split, st);
     }
-    switch (scan_form(s)) {
+    switch (scan_form(s, split)) {
         case kLong: return dtype ? scan_fwd<1, 64, 16>(s, split, st) : scan_fwd<0, 64, 16>(s, split, st);
         case kMiddle: return dtype ? scan_fwd<1, 64, 8>(s, split, st) : scan_fwd<0, 64, 8>(s, split, st);
         case kShared: return dtype ? scan_fwd<1, 16, 8, true>(s, split, st) : scan_fwd<0, 16, 8, true>(s, split, st);

@@ -30,6 +30,9 @@ struct ScanSplit {
     size_t bytes;
 };
 ScanSplit plan_scan_fwd(const miconv_scan_t &s, size_t budget);
+// The forms of the scan's forward kernel: lanes x steps per row; shared: a row's states over the waves.
+enum ScanForm { kLong, kMiddle, kRows, kShared };
+ScanForm scan_form(const miconv_scan_t &s, const ScanSplit &split);
 
 // Workspace of the scan's backward pass: partial sums per group of channels, time segments
 // that run side by side, and offsets.
@@ -59,6 +62,11 @@ int launch_quantize(int B, int L, int C, int dtype, const void *x, long long sb,
                     signed char *q, float *scale, hipStream_t st);
 // Splits of the summed axis matmul_i8 takes under `budget` bytes of workspace.
 int i8_splits(int T, int O, int K, size_t budget);
+// The kernel it takes: blocks of 16 tokens for few (0: tiles), else the tile's side and LDS stages.
+struct I8Form {
+    int few, side, stages;
+};
+I8Form i8_form(int T, int O, int K, int splits);
 int launch_matmul_i8(int B, int L, int O, int K, const signed char *q, const float *qs, const signed char *wq,
                      const float *ws_, const float *bias, int channel_major, int out_dtype, void *y, int splits,
                      int *part, hipStream_t st);

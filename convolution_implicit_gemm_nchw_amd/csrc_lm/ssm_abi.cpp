@@ -2,6 +2,7 @@
 // validation (before anything is enqueued), workspace sizing, launch.
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
+#include <stdio.h>
 
 #include "../../include/miconv.h"
 #include "ssm.h"
@@ -251,6 +252,18 @@ int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *workspace, size_
     return bad != MICONV_OK ? bad : launch_scan_fwd(*s, dtype, split, (float *)workspace, (hipStream_t)stream);
 }
 
+int selective_scan_fwd_describe(const miconv_scan_t *s, int dtype, size_t workspace_bytes, char *buf, size_t buflen) {
+    if (!buf || buflen == 0) return MICONV_ERR_NULL;
+    buf[0] = 0;
+    if (!s) return MICONV_ERR_NULL;
+    const int st = check_scan_sizes(*s, dtype);
+    if (st != MICONV_OK) return st;
+    const ScanSplit p = plan_scan_fwd(*s, workspace_bytes);
+    static const char *const names[] = {"64x16", "64x8", "16x8", "16x8shared"};
+    snprintf(buf, buflen, "algo=scan_fwd form=%s segments=%d ws=%zu", names[scan_form(*s, p)], p.segs, p.bytes);
+    return MICONV_OK;
+}
+
 int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out) {
     if (!s || !bytes_out) return MICONV_ERR_NULL;
     const int st = check_scan_sizes(*s, dtype);
@@ -286,6 +299,18 @@ int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_
     k.output(flat(workspace, p.bytes / 4, 4), true);
     const int bad = k.done();
     return bad != MICONV_OK ? bad : launch_scan_bwd(*s, dtype, (float *)workspace, (hipStream_t)stream);
+}
+
+int selective_scan_bwd_describe(const miconv_scan_t *s, int dtype, char *buf, size_t buflen) {
+    if (!buf || buflen == 0) return MICONV_ERR_NULL;
+    buf[0] = 0;
+    if (!s) return MICONV_ERR_NULL;
+    const int st = check_scan_sizes(*s, dtype);
+    if (st != MICONV_OK) return st;
+    const ScanBwdPlan p = plan_scan_bwd(*s);
+    snprintf(buf, buflen, "algo=scan_bwd segments=%d carry_segments=%d beside=%d ws=%zu", p.segs, p.carry_segs, p.beside,
+             p.bytes);
+    return MICONV_OK;
 }
 
 int selective_scan_step(const miconv_scan_t *s, int dtype, const float *state, int slots, const int *slot_of,
@@ -343,6 +368,20 @@ int matmul_i8_workspace_size(int B, int L, int O, int C_pad, size_t workspace_li
     if (st != MICONV_OK) return st;
     const int s = i8_splits(B * L, O, C_pad, workspace_limit);
     *bytes_out = s > 1 ? (size_t)s * B * L * O * 4 : 0;
+    return MICONV_OK;
+}
+
+int matmul_i8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, char *buf, size_t buflen) {
+    if (!buf || buflen == 0) return MICONV_ERR_NULL;
+    buf[0] = 0;
+    const int st = check_i8_sizes(B, L, O, C_pad);
+    if (st != MICONV_OK) return st;
+    const int splits = i8_splits(B * L, O, C_pad, workspace_bytes);
+    const I8Form f = i8_form(B * L, O, C_pad, splits);
+    if (f.few)
+        snprintf(buf, buflen, "algo=i8_few tokens=%d", f.few * 16);
+    else
+        snprintf(buf, buflen, "algo=i8_tile tile=%d stages=%d splits=%d", f.side, f.stages, splits);
     return MICONV_OK;
 }
 

@@ -553,10 +553,15 @@ int selective_scan_fwd(const miconv_scan_t *s, int dtype, void *workspace, size_
 /* Workspace the forward pass uses under workspace_limit (0 is always enough; few long rows
  * split the time axis over it). */
 int selective_scan_fwd_workspace_size(const miconv_scan_t *s, int dtype, size_t workspace_limit, size_t *bytes_out);
+/* One-line description of what a call with these sizes and this workspace runs (form of the kernel,
+ * time segments), as miconv_plan_describe writes it; only the sizes of the structure are read.  Pure
+ * host computation. */
+int selective_scan_fwd_describe(const miconv_scan_t *s, int dtype, size_t workspace_bytes, char *buf, size_t buflen);
 int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 int selective_scan_states_size(int B, int D, int L, int N, size_t *bytes_out);
 /* Workspace the backward pass needs (MICONV_ERR_WORKSPACE when given less). */
 int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out);
+int selective_scan_bwd_describe(const miconv_scan_t *s, int dtype, char *buf, size_t buflen);
 /*
  * One time step: x, delta, z, y [B][D], Bm, Cm [B][G][N] (L = 1 in the structure;
  * lengths, initial_state, final_state and states unused), state [slots][D][N]
@@ -593,6 +598,8 @@ int matmul_i8(int B, int L, int O, int C_pad, const signed char *q, const float 
               const float *wscale, const float *bias, int channel_major, int out_dtype, void *y, void *workspace,
               size_t workspace_bytes, void *stream);
 int matmul_i8_workspace_size(int B, int L, int O, int C_pad, size_t workspace_limit, size_t *bytes_out);
+/* One-line description of the kernel a call runs (few tokens, or tile, stages and splits). */
+int matmul_i8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, char *buf, size_t buflen);
 
 /* Static text for a status code (never NULL). */
 const char *miconv_status_string(int status);
