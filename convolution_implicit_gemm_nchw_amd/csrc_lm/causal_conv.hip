@@ -41,11 +41,11 @@ DEVI float full_at(const typename Elem<DT>::T *row, const typename Elem<DT>::T *
 // 2^lg_tpr threads per row.  WAVE: a row takes whole waves, so that what belongs to it
 // (addresses, taps, bias) is scalar.
 template <int DT, int K, bool WAVE, bool STREAM>
-__global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv_t c, int lg_tpr, FDiv fd_D) {
+__global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv_t c, int lg_tpr, FDiv fd_D, uint32_t first) {
     typedef typename Elem<DT>::T T;
     const int sub = threadIdx.x & ((1 << lg_tpr) - 1);
     const int rib = WAVE ? uniform(threadIdx.x >> lg_tpr) : threadIdx.x >> lg_tpr;
-    const long long row64 = (long long)blockIdx.x * (kThreads >> lg_tpr) + rib;
+    const long long row64 = (long long)(first + blockIdx.x) * (kThreads >> lg_tpr) + rib;
     if (row64 >= (long long)c.B * c.D) return;
     const int row = (int)row64, b = WAVE ? uniform((int)fdiv(row, fd_D)) : (int)fdiv(row, fd_D), d = row - b * c.D;
     const int len = valid_steps(c.lengths, b, c.L);
@@ -90,10 +90,10 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv
 // in a fixed tree and written to part[split][d][K+1] (or dw, dbias).
 template <int DT, int K>
 __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(miconv_causal_conv_t c, int tiles, long long per, int splits,
-                                                        float *part) {
+                                                        float *part, uint32_t first_channel) {
     typedef typename Elem<DT>::T T;
     __shared__ float red[kThreads / 64][K + 1];
-    const int waves = blockDim.x >> 6, step = waves * 63, d = blockIdx.x, split = blockIdx.y;
+    const int waves = blockDim.x >> 6, step = waves * 63, d = first_channel + blockIdx.x, split = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const long long items = (long long)c.B * tiles;
     const long long first = split * per, last = first + per < items ? first + per : items;
@@ -253,15 +253,13 @@ int fwd_k(const miconv_causal_conv_t &c, hipStream_t st) {
     const int lg = lg2_up(tiles, 8);
     const long long rpb = kThreads >> lg, row_blocks = ((long long)c.B * c.D + rpb - 1) / rpb;
     const long long along = (tiles + (1ll << lg) - 1) >> lg;
-    const dim3 grid((unsigned)row_blocks, (unsigned)(along < 65535 ? along : 65535));
     const FDiv fd = make_fdiv((uint32_t)c.D);
-    if (lg < 6)
-        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, false, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
-    else if (streams(DT, (size_t)c.B * c.D * c.L))
-        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, DT == 1>), grid, dim3(kThreads), 0, st, c, lg, fd);
-    else
-        hipLaunchKernelGGL((causal_fwd_kernel<DT, K, true, false>), grid, dim3(kThreads), 0, st, c, lg, fd);
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+    const auto kern = lg < 6 ? causal_fwd_kernel<DT, K, false, false>
+                             : (streams(DT, (size_t)c.B * c.D * c.L) ? causal_fwd_kernel<DT, K, true, DT == 1>
+                                                                     : causal_fwd_kernel<DT, K, true, false>);
+    return launch_groups(row_blocks, kThreads, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL(kern, dim3(n, (unsigned)(along < 65535 ? along : 65535)), dim3(kThreads), 0, st, c, lg, fd, first);
+    });
 }
 
 template <int DT, int K>
@@ -270,8 +268,11 @@ int bwd_k(const miconv_causal_conv_t &c, int splits, float *ws, hipStream_t st) 
     const long long items = (long long)c.B * tiles, per = (items + splits - 1) / splits;
     // up to four waves; fewer only where they hold all of a channel's tiles at once
     const int waves = per >= 4 * 63 ? 4 : (int)((per + 62) / 63);
-    hipLaunchKernelGGL((causal_bwd_kernel<DT, K>), dim3(c.D, splits), dim3(waves * 64), 0, st, c, tiles, per, splits, ws);
-    if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    const int bad = launch_groups(c.D, waves * 64, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL((causal_bwd_kernel<DT, K>), dim3(n, splits), dim3(waves * 64), 0, st, c, tiles, per, splits, ws,
+                           first);
+    });
+    if (bad != MICONV_OK) return bad;
     if (splits > 1 && (c.dw || c.dbias)) {
         const long long n = (long long)c.D * (K + 1);
         hipLaunchKernelGGL(causal_bwd_reduce, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,

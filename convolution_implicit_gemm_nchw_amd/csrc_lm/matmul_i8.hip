@@ -358,10 +358,10 @@ __global__ __launch_bounds__(256) void i8_join_kernel(I8Args a, int splits) {
 template <int OD, int FT>
 __global__ __launch_bounds__(512) void i8_few_kernel(const signed char *q, const signed char *wq, const float *qs,
                                                      const float *ws, const float *bias, int T, int O, int K, int L,
-                                                     int channel_major, void *y) {
+                                                     int channel_major, void *y, uint32_t first) {
     __shared__ int red[8][32][FT * 16 + 1];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane & 15, kq = (lane >> 4) * 16;
-    const int n0 = blockIdx.x * 32;
+    const int n0 = (int)(first + blockIdx.x) * 32;
     const signed char *pw[2], *pq[FT];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -431,10 +431,12 @@ __global__ __launch_bounds__(512) void i8_few_kernel(const signed char *q, const
 }
 
 template <int OD, int FT>
-void few(int T, int O, int K, int L, const signed char *q, const float *qs, const signed char *wq, const float *ws,
+int few(int T, int O, int K, int L, const signed char *q, const float *qs, const signed char *wq, const float *ws,
          const float *bias, int channel_major, void *y, hipStream_t st) {
-    hipLaunchKernelGGL((i8_few_kernel<OD, FT>), dim3((unsigned)((O + 31) / 32)), dim3(512), 0, st, q, wq, qs, ws, bias,
-                       T, O, K, L, channel_major, y);
+    return launch_groups(((long long)O + 31) / 32, 512, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL((i8_few_kernel<OD, FT>), dim3(n), dim3(512), 0, st, q, wq, qs, ws, bias, T, O, K, L, channel_major,
+                           y, first);
+    });
 }
 
 template <int OD, int WC, int WR, int FC, int FR, int ST, bool STREAM = false>
@@ -527,13 +529,7 @@ int launch_matmul_i8(int B, int L, int O, int K, const signed char *q, const flo
 #define MICONV_FEW(FT)                                                                            \
     (out_dtype ? few<1, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st)                \
                : few<0, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st))
-        if (f.few == 1)
-            MICONV_FEW(1);
-        else if (f.few == 2)
-            MICONV_FEW(2);
-        else
-            MICONV_FEW(4);
-        return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+        return f.few == 1 ? MICONV_FEW(1) : (f.few == 2 ? MICONV_FEW(2) : MICONV_FEW(4));
     }
     I8Args a = {};
     a.K = K;

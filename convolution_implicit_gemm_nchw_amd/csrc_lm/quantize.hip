@@ -66,10 +66,10 @@ DEVI uint32_t max8(const float (&v)[8], uint32_t m) {
 template <int DT, int TPT, int NV>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(int L, int C, int C_pad, long long tokens,
                                                             const typename Elem<DT>::T *x, long long sb, long long sl,
-                                                            signed char *q, float *scale) {
+                                                            signed char *q, float *scale, uint32_t first) {
     __shared__ uint32_t red[kThreads / 64];
     const int sub = threadIdx.x % TPT;
-    const long long tok = (long long)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+    const long long tok = (long long)(first + blockIdx.x) * (kThreads / TPT) + threadIdx.x / TPT;
     if (TPT == 64 && tok >= tokens) return;     // one wave: no barrier ahead
     const int b = (int)(tok / L), l = (int)(tok - (long long)b * L);
     const typename Elem<DT>::T *row = x + b * sb + l * sl;
@@ -113,10 +113,11 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(int L, int C, int C_
 template <int DT>
 __global__ __launch_bounds__(kThreads) void quantize_cm_kernel(int L, int C, int C_pad, int tiles,
                                                                const typename Elem<DT>::T *x, long long sb, long long sc,
-                                                               signed char *q, float *scale) {
+                                                               signed char *q, float *scale, uint32_t first) {
     __shared__ uint32_t red[64][33];
     __shared__ __attribute__((aligned(16))) signed char turn[32][72];
-    const int b = blockIdx.x / tiles, l0 = (blockIdx.x - b * tiles) * 32;
+    const uint32_t tile = first + blockIdx.x;
+    const int b = tile / tiles, l0 = (tile - b * tiles) * 32;
     const int part = threadIdx.x & 3, ch = threadIdx.x >> 2, l = l0 + part * 8;
     const typename Elem<DT>::T *base = x + b * sb;
     uint32_t m[8] = {};
@@ -161,26 +162,20 @@ int quantize(int B, int L, int C, const void *xp, long long sb, long long sl, lo
     const long long tokens = (long long)B * L;
     if (sc != 1 && C > 1) {
         const int tiles = (L + 31) / 32;
-        hipLaunchKernelGGL(quantize_cm_kernel<DT>, dim3((unsigned)((long long)B * tiles)), dim3(kThreads), 0, st, L, C,
-                           C_pad, tiles, x, sb, sc, q, scale);
-    } else if (C <= 2048) {
-        // a wave per token: no barrier (8192 tokens of 1000: 7.9 us against 13.8 with a work-group
-        // per token, of 2048 13.4 against 15.2, of 4096 26.2 against 19.7)
-        const dim3 grid((unsigned)((tokens + 3) / 4));
-        if (C <= 1024)
-            hipLaunchKernelGGL((quantize_kernel<DT, 64, 2>), grid, dim3(kThreads), 0, st, L, C, C_pad, tokens, x, sb, sl, q,
-                               scale);
-        else
-            hipLaunchKernelGGL((quantize_kernel<DT, 64, 4>), grid, dim3(kThreads), 0, st, L, C, C_pad, tokens, x, sb, sl, q,
-                               scale);
-    } else if (C <= 4096) {
-        hipLaunchKernelGGL((quantize_kernel<DT, 256, 2>), dim3((unsigned)tokens), dim3(kThreads), 0, st, L, C, C_pad,
-                           tokens, x, sb, sl, q, scale);
-    } else {
-        hipLaunchKernelGGL((quantize_kernel<DT, 256, 4>), dim3((unsigned)tokens), dim3(kThreads), 0, st, L, C, C_pad,
-                           tokens, x, sb, sl, q, scale);
+        return launch_groups((long long)B * tiles, kThreads, [&](unsigned n, unsigned first) {
+            hipLaunchKernelGGL(quantize_cm_kernel<DT>, dim3(n), dim3(kThreads), 0, st, L, C, C_pad, tiles, x, sb, sc, q, scale,
+                               first);
+        });
     }
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+    // up to 2048 channels a wave per token: no barrier (8192 tokens of 1000: 7.9 us against 13.8 with a
+    // work-group per token, of 2048 13.4 against 15.2, of 4096 26.2 against 19.7)
+    const auto kern = C <= 1024   ? quantize_kernel<DT, 64, 2>
+                      : C <= 2048 ? quantize_kernel<DT, 64, 4>
+                      : C <= 4096 ? quantize_kernel<DT, 256, 2>
+                                  : quantize_kernel<DT, 256, 4>;
+    return launch_groups(C <= 2048 ? (tokens + 3) / 4 : tokens, kThreads, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL(kern, dim3(n), dim3(kThreads), 0, st, L, C, C_pad, tokens, x, sb, sl, q, scale, first);
+    });
 }
 
 }  // namespace

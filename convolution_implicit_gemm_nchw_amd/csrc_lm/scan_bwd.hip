@@ -156,12 +156,13 @@ DEVI P *row_at(const Lds &m, int what, int i) {
 }
 
 template <int DT, int NS>
-__global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOut o) {
+__global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOut o, uint32_t first_group) {
     typedef typename Elem<DT>::T T;
     __shared__ __attribute__((aligned(16))) Lds m;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane >> 4, sub = lane & 15;
     const int per_group = s.D / s.G;
-    const int part = blockIdx.x % o.parts, bg = blockIdx.x / o.parts % (s.B * s.G), seg = blockIdx.x / (o.parts * s.B * s.G);
+    const uint32_t id = first_group + blockIdx.x;
+    const int part = id % o.parts, bg = id / o.parts % (s.B * s.G), seg = id / (o.parts * s.B * s.G);
     const int g = bg % s.G, b = bg / s.G;
     const int first = g * per_group + part * kCh;                        // the work-group's first channel
     const int channels = per_group - part * kCh < kCh ? per_group - part * kCh : kCh;
@@ -635,13 +636,14 @@ struct SumJobs {
     int count;
 };
 
-__global__ __launch_bounds__(64 * kSumWaves) void scan_bwd_sum(SumJobs jobs) {
+__global__ __launch_bounds__(64 * kSumWaves) void scan_bwd_sum(SumJobs jobs, uint32_t first_group) {
     __shared__ f32x4 share[kSumWaves][64];
     int k = 0;
-    while (k + 1 < jobs.count && (long long)blockIdx.x >= jobs.first[k + 1]) ++k;
+    const long long group = (long long)first_group + blockIdx.x;
+    while (k + 1 < jobs.count && group >= jobs.first[k + 1]) ++k;
     const SumJob j = jobs.j[k];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const long long i = ((long long)blockIdx.x - jobs.first[k]) * 256 + lane * 4;
+    const long long i = (group - jobs.first[k]) * 256 + lane * 4;
     const int per = (j.parts + kSumWaves - 1) / kSumWaves, p0 = wave * per, p1 = p0 + per < j.parts ? p0 + per : j.parts;
     f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
     if (i + 4 <= j.n) {
@@ -749,7 +751,6 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
                                0, st, s, out);
         if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
     }
-    const dim3 grid((unsigned)((long long)s.B * s.G * p.parts * p.segs), (unsigned)p.beside);
     const int per_launch = kStates * p.beside;
     for (int n = 0; n < s.N; n += per_launch) {
         o.n_first = n;
@@ -760,9 +761,12 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
         const void *kern = nn <= 4   ? (dtype ? (const void *)scan_bwd_kernel<1, 1> : (const void *)scan_bwd_kernel<0, 1>)
                            : nn <= 8 ? (dtype ? (const void *)scan_bwd_kernel<1, 2> : (const void *)scan_bwd_kernel<0, 2>)
                                      : (dtype ? (const void *)scan_bwd_kernel<1, 4> : (const void *)scan_bwd_kernel<0, 4>);
-        miconv_scan_t a = s;
-        void *args[] = {(void *)&a, (void *)&o};
-        if (hipLaunchKernel(kern, grid, dim3(256), args, 0, st) != hipSuccess) return MICONV_ERR_HIP;
+        const int bad = launch_groups((long long)s.B * s.G * p.parts * p.segs, 256, [&](unsigned groups, unsigned first) {
+            miconv_scan_t a = s;
+            void *args[] = {(void *)&a, (void *)&o, (void *)&first};
+            (void)hipLaunchKernel(kern, dim3(groups, (unsigned)p.beside), dim3(256), args, 0, st);
+        });
+        if (bad != MICONV_OK) return bad;
     }
     const int time_parts = p.beside > 1 ? 1 : p.segs;     // of dD and the bias's gradient
     if (p.beside > 1) {
@@ -781,8 +785,9 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B * time_parts};
     if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B * time_parts};
     for (int k = 0; k < jobs.count; ++k) jobs.first[k + 1] = jobs.first[k] + (jobs.j[k].n + 255) / 256;
-    hipLaunchKernelGGL(scan_bwd_sum, dim3((unsigned)jobs.first[jobs.count]), dim3(64 * kSumWaves), 0, st, jobs);
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+    return launch_groups(jobs.first[jobs.count], 64 * kSumWaves, [&](unsigned groups, unsigned first) {
+        hipLaunchKernelGGL(scan_bwd_sum, dim3(groups), dim3(64 * kSumWaves), 0, st, jobs, first);
+    });
 }
 
 }  // namespace miconv

@@ -32,7 +32,8 @@ constexpr int kThreads = 256;
 constexpr int kScanWaves = 8;
 
 template <int DT, int LANES, int ITEMS, bool SHARE = false>
-__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g, ScanSplit split) {
+__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_scan_t s, int blocks_g, ScanSplit split,
+                                                                        uint32_t first_group) {
     typedef typename Elem<DT>::T T;
     constexpr int kT = LANES * ITEMS, kRows = 64 / LANES, kEvery = kScanChunk / ITEMS, kPairs = kT * 2 * 4;   // bytes of B and C per state
     constexpr int kStage = SHARE ? 32 : 65536 / kPairs < 16 ? 65536 / kPairs : 16;            // states staged at a time
@@ -45,8 +46,9 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
     __shared__ __attribute__((aligned(16))) float parts[SHARE ? kScanWaves * kRows * kT : 1];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), sub = lane % LANES;
     const int per_group = s.D / s.G;
-    const int blk = blockIdx.x % blocks_g, bg = blockIdx.x / blocks_g % (s.B * s.G), g = bg % s.G, b = bg / s.G;
-    const int seg = blockIdx.x / (blocks_g * s.B * s.G), start = seg * split.steps;
+    const uint32_t group = first_group + blockIdx.x;
+    const int blk = group % blocks_g, bg = group / blocks_g % (s.B * s.G), g = bg % s.G, b = bg / s.G;
+    const int seg = group / (blocks_g * s.B * s.G), start = seg * split.steps;
     const int stop = split.segs == 1 || s.L - start < split.steps ? s.L : start + split.steps;
     const int in_group = (SHARE ? blk : blk * kScanWaves + wave) * kRows + lane / LANES;
     const bool live = in_group < per_group;              // the last work-group's other rows only help to stage
@@ -313,10 +315,10 @@ __global__ __launch_bounds__(kThreads) void scan_chain_kernel(miconv_scan_t s, S
 template <int DT, int PER, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, const float *state, int slots,
                                                              const int *slot_of, float *state_out, FDiv fd_D,
-                                                             FDiv fd_group) {
+                                                             FDiv fd_group, uint32_t first_group) {
     typedef typename Elem<DT>::T T;
     const int sub = threadIdx.x % PER, n0 = sub * 4;
-    const uint32_t i = blockIdx.x * (kThreads / PER) + threadIdx.x / PER;     // rows are at most 2^30
+    const uint32_t i = (first_group + blockIdx.x) * (kThreads / PER) + threadIdx.x / PER;     // rows are at most 2^30
     if (i >= (uint32_t)s.B * (uint32_t)s.D) return;
     const int b = (int)fdiv(i, fd_D), d = (int)i - b * s.D, g = (int)fdiv(d, fd_group);
     const int slot = slot_of ? slot_of[b] : b;
@@ -390,9 +392,10 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
 template <int DT, int LANES, int ITEMS, bool SHARE = false>
 static int scan_fwd(const miconv_scan_t &s, const ScanSplit &split, hipStream_t st) {
     const int rows = (SHARE ? 1 : kScanWaves) * (64 / LANES), blocks_g = (s.D / s.G + rows - 1) / rows;
-    const dim3 grid((unsigned)((long long)s.B * s.G * blocks_g * split.segs));
-    hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS, SHARE>), grid, dim3(64 * kScanWaves), 0, st, s, blocks_g, split);
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+    return launch_groups((long long)s.B * s.G * blocks_g * split.segs, 64 * kScanWaves, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL((scan_fwd_kernel<DT, LANES, ITEMS, SHARE>), dim3(n), dim3(64 * kScanWaves), 0, st, s, blocks_g,
+                           split, first);
+    });
 }
 
 namespace {
@@ -474,15 +477,15 @@ template <int DT, int PER>
 static int scan_step(const miconv_scan_t &s, const float *state, int slots, const int *slot_of, float *state_out,
                      hipStream_t st) {
     const long long rows = (long long)s.B * s.D;
-    const dim3 grid((unsigned)((rows + kThreads / PER - 1) / (kThreads / PER)));
     const FDiv fd_D = make_fdiv((uint32_t)s.D), fd_group = make_fdiv((uint32_t)(s.D / s.G));
     const bool together = s.N == 1 || (s.Bm.stride_n == 1 && s.Cm.stride_n == 1);
     const bool vec = s.N % 4 == 0 && together && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0;
     const auto kern = !vec ? scan_step_kernel<DT, PER, false, false>
                            : ((size_t)rows * s.N * 4 >= (16u << 20) ? scan_step_kernel<DT, PER, true, true>
                                                                     : scan_step_kernel<DT, PER, true, false>);
-    hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, st, s, state, slots, slot_of, state_out, fd_D, fd_group);
-    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+    return launch_groups((rows + kThreads / PER - 1) / (kThreads / PER), kThreads, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL(kern, dim3(n), dim3(kThreads), 0, st, s, state, slots, slot_of, state_out, fd_D, fd_group, first);
+    });
 }
 
 int launch_scan_step(const miconv_scan_t &s, int dtype, const float *state, int slots, const int *slot_of,

@@ -15,6 +15,20 @@ constexpr int kScanBwdChannels = 16;
 
 constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
+// A launch counts its work-items along an axis in 32 bits and drops, without an error, what lies past
+// them: more work-groups than that go in several launches.  launch(n, first) launches n of them
+// from the first on.
+template <typename F>
+int launch_groups(long long groups, int threads, F launch) {
+    const long long most = 0xffffffffll / threads;
+    for (long long first = 0; first < groups; first += most) {
+        const long long n = groups - first < most ? groups - first : most;
+        launch((unsigned)n, (unsigned)first);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    }
+    return MICONV_OK;
+}
+
 // Whether an output is written past the caches: in bf16 from half of the 256 MB last-level cache
 // on, where the next reader would not find it there.  (Causal forward followed by a read of
 // its output: 128 MB 121 -> 106 us; 64 MB 50 -> 55 us, though the call alone falls from 31 to 25.)
