@@ -303,7 +303,7 @@ int causal_bwd_splits(const miconv_causal_conv_t &c, size_t budget) {
     long long s = 1024 / c.D;
     if (s > items / 256) s = items / 256;
     if (s > 64) s = 64;
-    if (s > (long long)budget / one) s = (long long)budget / one;
+    if (s > (long long)(budget / (size_t)one)) s = (long long)(budget / (size_t)one);
     return s < 1 ? 1 : (int)s;
 }
 

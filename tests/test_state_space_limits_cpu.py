@@ -1,0 +1,32 @@
+"""State-space operators without a GPU: workspace sizes under any limit."""
+import ctypes
+
+import pytest
+
+import convolution_implicit_gemm_nchw_amd as mc
+import test_state_space_cpu as base
+
+OK = base.OK
+SIZE_MAX = (1 << 64) - 1
+
+
+def sizes(call, limits):
+    need, out = ctypes.c_size_t(0), []
+    for limit in limits:
+        assert call(limit, ctypes.byref(need)) == OK
+        assert need.value <= limit
+        out.append(need.value)
+    return out
+
+
+@pytest.mark.parametrize("name", ["convolution", "scan", "product"])
+def test_workspace_size_under_any_limit(name):
+    """Problems that split their sums: no limit gives what a large one gives, a small one less."""
+    lib = mc.lib()
+    conv, scan = base.conv_args(B=64, L=8192), base.scan_args(B=1, L=8192)
+    call = {"convolution": lambda n, p: lib.causal_conv1d_bwd_workspace_size(ctypes.byref(conv), 0, n, p),
+            "scan": lambda n, p: lib.selective_scan_fwd_workspace_size(ctypes.byref(scan), 0, n, p),
+            "product": lambda n, p: lib.matmul_i8_workspace_size(1, 100, 70, 8192, n, p)}[name]
+    none, some, large, huge, top = sizes(call, (0, 1000, 10 ** 9, 1 << 63, SIZE_MAX))
+    assert none == 0 and some < large
+    assert large == huge == top and large > 0
