@@ -115,9 +115,9 @@ DEVI void gate(float (&e)[8], const float (&z)[8], float (&zslope)[8]) {
     }
 }
 
-// The derivative of the step size in place of delta, 0 past the end.
+// The derivative of the step size in place of delta.
 template <int DT>
-DEVI void slopes(float (&v)[8], float bias, int use_softplus, int t, int chunk_end, int len) {
+DEVI void slopes(float (&v)[8], float bias, int use_softplus) {
     if (use_softplus) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = logistic_for<DT>(v[i] + bias);
@@ -125,23 +125,22 @@ DEVI void slopes(float (&v)[8], float bias, int use_softplus, int t, int chunk_e
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 1.0f;
     }
-    if (chunk_end > len) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = t + i < len ? v[i] : 0.0f;
-    }
 }
 
 // From the sums over the states (that of A g a h was taken with A log2(e)) to d(delta) and
 // dx, and the sums over time of the bias's and D's gradients.
 DEVI void finish_steps(const float (&x)[8], const float (&slope)[8], const float (&dt)[8], const float (&e)[8], float skip,
-                       float (&sdt)[8], float (&sgB)[8], float &sb, float &sD) {
+                       int t, int chunk_end, int len, float (&sdt)[8], float (&sgB)[8], float &sb, float &sD) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         sdt[i] = __builtin_fmaf(x[i], sgB[i], sdt[i] * kLn2) * slope[i];
-        sb += sdt[i];
         sD = __builtin_fmaf(e[i], x[i], sD);
         sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
     }
+    zero_past(sdt, t, chunk_end, len);
+    zero_past(sgB, t, chunk_end, len);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sb += sdt[i];
 }
 
 template <typename P>
@@ -382,6 +381,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             float w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = join_rows(join_halves(dB[j][i], dC[j][i]), join_halves(dB[j2][i], dC[j2][i]));
+            zero_past(w, t, t0 + kT, len);
             const int n = j0 + (row & 1 ? j2 : j);
             if (n < nn && t < s.L && !(NS == 1 && (row & 1)))
                 store8<0>(row_at<float>(m, row & 2 ? kDC : kDB, n), t, s.L, w);
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             if (o.last) {
                 float slope[8];
                 widen8<DT>(od, slope);
-                slopes<DT>(slope, bias, s.softplus, t, t0 + kT, len);
+                slopes<DT>(slope, bias, s.softplus);
                 get_steps(m.dt, wave, lane, dt);
                 get_steps(m.e, wave, lane, e);
                 widen8<DT>(ox, xv);
@@ -425,9 +425,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     get_steps(m.zslope, wave, lane, zslope);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
+                    zero_past(zslope, t, t0 + kT, len);
                     store8<DT>(row_at<T>(m, kDz, own), t, s.L, zslope);
                 }
-                finish_steps(xv, slope, dt, e, skip, sdt, sgB, sb, sD);
+                finish_steps(xv, slope, dt, e, skip, t, t0 + kT, len, sdt, sgB, sb, sD);
                 store8<DT>(row_at<T>(m, kDdelta, own), t, s.L, sdt);
                 store8<DT>(row_at<T>(m, kDx, own), t, s.L, sgB);
             }
@@ -478,7 +479,7 @@ __global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, B
         load8<DT>(at_row<const T>(s.dy, b, d), t, len, e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) slope[i] = dt[i];
-        slopes<DT>(slope, bias, s.softplus, t, t + 8, len);
+        slopes<DT>(slope, bias, s.softplus);
         step_sizes(dt, bias, s.softplus, t, t + 8, len);
         if (s.z.data) {
             float z[8], zslope[8];
@@ -486,9 +487,10 @@ __global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, B
             gate<DT>(e, z, zslope);
 #pragma unroll
             for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, x[i], sum[2][i]);
+            zero_past(zslope, t, t + 8, len);
             store8<DT>(at_row<T>(s.dz, b, d), t, s.L, zslope);
         }
-        finish_steps(x, slope, dt, e, skip, sum[0], sum[1], sb, sD);
+        finish_steps(x, slope, dt, e, skip, t, t + 8, len, sum[0], sum[1], sb, sD);
         store8<DT>(at_row<T>(s.ddelta, b, d), t, s.L, sum[0]);
         store8<DT>(at_row<T>(s.dx, b, d), t, s.L, sum[1]);
     }

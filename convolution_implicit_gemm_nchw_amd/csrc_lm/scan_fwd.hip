@@ -198,6 +198,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
 #pragma unroll
                     for (int i = 0; i < 8; ++i) out[i] *= zv[i] * logistic_for<DT>(zv[i]);
                 }
+                zero_past(out, t + q, t0 + kT, len);
                 store8<DT>(y, t + q, s.L, out);
             }
         }

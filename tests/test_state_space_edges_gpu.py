@@ -1,0 +1,68 @@
+"""State-space operators where a multiplication by zero does not clear what it meets: states, parameters and
+steps that hold infinities or NaN next to the padding of a ragged batch.
+"""
+import pytest
+import torch
+
+import test_state_space_gpu as base
+
+pytestmark = pytest.mark.gpu
+mc = base.mc
+DEV, TDT = base.DEV, base.TDT
+INF = float("inf")
+
+#         B  D     L     N  the forward pass takes        lengths
+SHAPES = [(2, 3, 900, 5, "64x16 segments=1", [897, 450]),
+          (2, 300, 500, 4, "64x8 segments=1", [1, 403]),
+          (2, 4100, 129, 3, "16x8 segments=1", [128, 30]),
+          (2, 3, 300, 17, "16x8shared segments=1", [3, 290]),
+          (1, 64, 3100, 2, "64x16 segments=4", [1029])]
+
+
+def inputs(B, D, L, N, dt, seed=0):
+    f = base.Data(seed, dt)
+    d = {k: f.make(B, D, L)[1] for k in ("x", "delta", "z", "dy")}
+    d["B"], d["C"] = f.make(B, 1, N, L)[1], f.make(B, 1, N, L)[1]
+    d["A"] = torch.full((D, N), -0.01, device=DEV)
+    d["D"] = f.make(D, dtype=torch.float32)[1]
+    d["h0"] = f.make(B, D, N, dtype=torch.float32)[1]
+    d["dfs"] = f.make(B, D, N, dtype=torch.float32)[1]
+    return d
+
+
+def forward_backward(mc, d, n, gate):
+    B, D, L = d["x"].shape
+    common = dict(D=d["D"], z=d["z"] if gate else None, softplus=True, lengths=n)
+    r = {"fs": torch.full_like(d["h0"], 7.0), "dh0": torch.full_like(d["h0"], 7.0)}
+    states = mc.selective_scan_states(d["x"], d["A"])
+    r["y"] = mc.selective_scan_fwd(d["x"], d["delta"], d["A"], d["B"], d["C"], initial_state=d["h0"],
+                                   final_state=r["fs"], states=states, **common)
+    r.update(mc.selective_scan_bwd(d["x"], d["delta"], d["A"], d["B"], d["C"], d["dy"], states,
+                                   d_final_state=d["dfs"], d_initial_state=r["dh0"], **common))
+    return r
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("B,D,L,N,form,lengths", SHAPES)
+def test_padding_is_zero_whatever_a_row_holds(mc, B, D, L, N, form, lengths, gate, dt):
+    """A state of infinity, an infinite gradient of the final state and a NaN parameter stay in their rows
+    and out of the padding."""
+    assert form in mc.selective_scan_fwd_describe(B, D, L, N)
+    d = inputs(B, D, L, N, dt)
+    n = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    clean = forward_backward(mc, d, n, gate)
+    d["h0"][0, 1] = INF
+    d["dfs"][B - 1, 0] = -INF
+    d["D"][2] = float("nan")
+    r = forward_backward(mc, d, n, gate)
+    assert bool((r["fs"][0, 1] == INF).all())
+    others = [c for c in range(D) if c not in (0, 1, 2)]
+    for name in ("y", "dx", "ddelta") + (("dz",) if gate else ()):
+        for b, m in enumerate(lengths):
+            assert not r[name][b, :, m:].any() and bool(r[name][b, :, m:].isfinite().all()), (name, b)
+        assert torch.equal(r[name][:, others], clean[name][:, others]), name
+    for name in ("dB", "dC"):
+        for b, m in enumerate(lengths):
+            assert not r[name][b, :, :, m:].any() and bool(r[name][b, :, :, m:].isfinite().all()), (name, b)
+    assert torch.equal(r["dA"][others], clean["dA"][others])
