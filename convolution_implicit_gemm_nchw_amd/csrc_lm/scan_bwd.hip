@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
         const int c = i / kStates, j = i % kStates;
         const bool used = c < channels && j < nn;
         const long long at = ((long long)b * s.D + first + c) * s.N + n_first + j;
-        m.a2[c][j] = used ? s.A[(long long)(first + c) * s.N + n_first + j] * kLog2e : 0.0f;
+        m.a2[c][j] = used ? log2_decay(s.A[(long long)(first + c) * s.N + n_first + j]) : 0.0f;
         const float *G = c_end < chunks ? o.G + (((long long)b * s.D + first + c) * chunks + c_end - 1) * s.N + n_first + j
                                         : (s.d_final_state ? s.d_final_state + at : nullptr);
         m.carry[c][j] = used && G ? *G : 0.0f;
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
     float carried = 0.0f, a_lane = 0.0f;               // lane n: state n
     if (lane < s.N) {
         if (s.d_final_state && out.segs == 1) carried = s.d_final_state[row * s.N + lane];
-        a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
+        a_lane = log2_decay(s.A[(long long)d * s.N + lane]);
     }
     float later = 0.0f;                                // dt from the chunk's end to the segment's
     for (int t0 = start + (stop - 1 - start) / kCarryT * kCarryT; t0 >= start; t0 -= kCarryT) {
@@ -606,7 +606,7 @@ __global__ __launch_bounds__(256) void scan_bwd_chain_kernel(miconv_scan_t s, Ca
     if (i >= (long long)s.B * s.D * s.N) return;
     const long long row = i / s.N;
     const int n = (int)(i - row * s.N), d = (int)(row % s.D), chunks = (s.L + kT - 1) / kT, per = out.steps / kT;
-    const float a2 = s.A[(long long)d * s.N + n] * kLog2e;
+    const float a2 = log2_decay(s.A[(long long)d * s.N + n]);
     float G = s.d_final_state ? s.d_final_state[i] : 0.0f;
     for (int seg = out.segs - 1; seg >= 0; --seg) {
         const int last = (seg + 1) * per < chunks ? (seg + 1) * per : chunks;

@@ -75,12 +75,12 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
                 carried = split.entry[(row * split.segs + seg) * s.N + lane];
             else if (s.initial_state)
                 carried = s.initial_state[row * s.N + lane];
-            a_lane = s.A[(long long)d * s.N + lane] * kLog2e;
+            a_lane = log2_decay(s.A[(long long)d * s.N + lane]);
         }
     } else {
         for (int n = n_mine + sub * kStride; n < s.N; n += LANES * kStride) {
             h_rows[my][n] = s.initial_state ? s.initial_state[row * s.N + n] : 0.0f;
-            a_rows[my][n] = s.A[(long long)d * s.N + n] * kLog2e;
+            a_rows[my][n] = log2_decay(s.A[(long long)d * s.N + n]);
         }
         wave_lds_sync();
     }
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_local_kernel(miconv_s
     const T *dl = (const T *)s.delta.data + b * s.delta.stride_b + d * s.delta.stride_d;
     const T *Bm = (const T *)s.Bm.data + b * s.Bm.stride_b + g * s.Bm.stride_g;
     const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f;
-    const float a_lane = lane < s.N ? s.A[(long long)d * s.N + lane] * kLog2e : 0.0f;
+    const float a_lane = lane < s.N ? log2_decay(s.A[(long long)d * s.N + lane]) : 0.0f;
     float carried = 0.0f, total = 0.0f;
     for (int t0 = start; t0 < len && t0 < stop; t0 += kT) {
         const int t = t0 + lane * ITEMS;
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void scan_chain_kernel(miconv_scan_t s, S
     if (i >= (long long)s.B * s.D * s.N) return;
     const long long row = i / s.N;
     const int n = (int)(i - row * s.N), d = (int)(row % s.D);
-    const float a2 = s.A[(long long)d * s.N + n] * kLog2e;
+    const float a2 = log2_decay(s.A[(long long)d * s.N + n]);
     float h = s.initial_state ? s.initial_state[i] : 0.0f;
     for (int seg = 0; seg < split.segs; ++seg) {
         float *at = split.entry + (row * split.segs + seg) * s.N + n;
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
     float v = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        h[e] = __builtin_fmaf(exp2_hw(dt * (a[e] * kLog2e)), h[e], dtx * bv[e]);
+        h[e] = __builtin_fmaf(exp2_hw(dt * log2_decay(a[e])), h[e], dtx * bv[e]);
         v = __builtin_fmaf(cv[e], h[e], v);
     }
     if (VEC && n0 < s.N) {

@@ -207,6 +207,13 @@ DEVI float softplus(float v) {
     return __builtin_fmaf(s, p, __int_as_float(bits > 0 ? bits : 0));
 }
 
+// A log2(e), held to what fp32 has: a step of size 0 then decays by exp2(0 * that) = 1 rather
+// than by exp2(0 * -inf), as the definition does for every finite A.
+DEVI float log2_decay(float A) {
+    const float a = A * kLog2e;
+    return a < -__FLT_MAX__ ? -__FLT_MAX__ : a;
+}
+
 // Lane crossings of a wave of 64 in four rows of 16.
 constexpr int kRowShr = 0x110;      // + n: lane i reads lane i - n of its row
 constexpr int kRowShl = 0x100;      // + n: lane i reads lane i + n of its row

@@ -1,5 +1,5 @@
 """State-space operators where a multiplication by zero does not clear what it meets: states, parameters and
-steps that hold infinities or NaN next to the padding of a ragged batch.
+steps that hold infinities or NaN next to the padding of a ragged batch, and decays that leave fp32.
 """
 import pytest
 import torch
@@ -66,3 +66,31 @@ def test_padding_is_zero_whatever_a_row_holds(mc, B, D, L, N, form, lengths, gat
         for b, m in enumerate(lengths):
             assert not r[name][b, :, :, m:].any() and bool(r[name][b, :, :, m:].isfinite().all()), (name, b)
     assert torch.equal(r["dA"][others], clean["dA"][others])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("B,D,L,N,form,lengths", SHAPES)
+def test_decay_past_fp32(mc, B, D, L, N, form, lengths, dt):
+    """A so negative that A log2(e) is no fp32 number: every decay is 0, as for -1e30, and a step past the
+    end leaves the state as it is."""
+    d = inputs(B, D, L, N, dt, seed=1)
+    n = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    d["A"].fill_(-1e30)
+    want = forward_backward(mc, d, n, True)
+    assert bool(want["fs"].isfinite().all())
+    for a in (-3e38, -INF):
+        d["A"].fill_(a)
+        got = forward_backward(mc, d, n, True)
+        for k in want:
+            assert want[k] is None or torch.equal(got[k], want[k]), (a, k)
+
+
+@pytest.mark.parametrize("N", [3, 16])
+def test_step_of_size_zero(mc, N):
+    """softplus(-200) is 0 in fp32: the state stays, whatever finite decay it has."""
+    f = base.Data(2, "f32")
+    x, Bm, state = f.make(2, 5)[1], f.make(2, 1, N)[1], f.make(2, 5, N)[1]
+    delta, out = torch.full_like(x, -200.0), torch.empty(2, 5, N, device=DEV)
+    for a in (-1.0, -1e30, -3e38):
+        mc.selective_scan_step(x, delta, torch.full((5, N), a, device=DEV), Bm, Bm, state, softplus=True, state_out=out)
+        assert torch.equal(out, state), a
