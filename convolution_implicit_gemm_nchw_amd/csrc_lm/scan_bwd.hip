@@ -115,9 +115,9 @@ DEVI void gate(float (&e)[8], const float (&z)[8], float (&zslope)[8]) {
     }
 }
 
-// The derivative of the step size in place of delta.
+// The derivative of the step size in place of delta, 0 past the end.
 template <int DT>
-DEVI void slopes(float (&v)[8], float bias, int use_softplus) {
+DEVI void slopes(float (&v)[8], float bias, int use_softplus, int t, int chunk_end, int len) {
     if (use_softplus) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = logistic_for<DT>(v[i] + bias);
@@ -125,22 +125,30 @@ DEVI void slopes(float (&v)[8], float bias, int use_softplus) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 1.0f;
     }
+    if (chunk_end > len) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = t + i < len ? v[i] : 0.0f;
+    }
 }
 
 // From the sums over the states (that of A g a h was taken with A log2(e)) to d(delta) and
 // dx, and the sums over time of the bias's and D's gradients.
 DEVI void finish_steps(const float (&x)[8], const float (&slope)[8], const float (&dt)[8], const float (&e)[8], float skip,
-                       int t, int chunk_end, int len, float (&sdt)[8], float (&sgB)[8], float &sb, float &sD) {
+                       float (&sdt)[8], float (&sgB)[8], float &sb, float &sD) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         sdt[i] = __builtin_fmaf(x[i], sgB[i], sdt[i] * kLn2) * slope[i];
+        sb += sdt[i];
         sD = __builtin_fmaf(e[i], x[i], sD);
         sgB[i] = __builtin_fmaf(dt[i], sgB[i], skip * e[i]);
     }
-    zero_past(sdt, t, chunk_end, len);
-    zero_past(sgB, t, chunk_end, len);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sb += sdt[i];
+}
+
+// Zeros from max(t, end) to t + 8, as far as the row goes.
+template <int DT>
+DEVI void zero_past(typename Elem<DT>::T *row, int t, int end, int L) {
+    const float zero[8] = {};
+    store8<DT>(row, t < end ? end : t, t + 8 < L ? t + 8 : L, zero);
 }
 
 template <typename P>
@@ -205,18 +213,20 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     __syncthreads();
     float sD = 0.0f, sb = 0.0f;
     const int end = live ? len : 0;
-    // Chunks past the sequence's end: zeros.
+    // What lies past the sequence's end is zeros, and not computed: states and parameters that are
+    // not finite would make padding NaN.
     int c = c_end - 1;
-    for (; c >= c_first && c * kT >= len; --c) {
+    for (; c >= c_first; --c) {
         const int t = c * kT + sub * 8;
-        const float zero[8] = {};
-        if (live && t < s.L && o.last) {
-            store8<DT>(row_at<T>(m, kDx, own), t, s.L, zero);
-            store8<DT>(row_at<T>(m, kDdelta, own), t, s.L, zero);
-            if (gated) store8<DT>(row_at<T>(m, kDz, own), t, s.L, zero);
+        if (len >= s.L || len >= (c + 1) * kT) break;
+        if (live && o.last) {
+            zero_past<DT>(row_at<T>(m, kDx, own), t, len, s.L);
+            zero_past<DT>(row_at<T>(m, kDdelta, own), t, len, s.L);
+            if (gated) zero_past<DT>(row_at<T>(m, kDz, own), t, len, s.L);
         }
-        for (int i = wave * 4 + row; i < 2 * nn && t < s.L; i += 16)
-            store8<0>(row_at<float>(m, i & 1 ? kDC : kDB, i >> 1), t, s.L, zero);
+        for (int i = wave * 4 + row; i < 2 * nn; i += 16)
+            zero_past<0>(row_at<float>(m, i & 1 ? kDC : kDB, i >> 1), t, len, s.L);
+        if (c * kT < len) break;
     }
     // What a chunk reads of its rows, fetched while the chunk before is finished.
     Raw8<DT> rx, rd, ry, rz, rbc[2];
@@ -381,10 +391,9 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             float w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = join_rows(join_halves(dB[j][i], dC[j][i]), join_halves(dB[j2][i], dC[j2][i]));
-            zero_past(w, t, t0 + kT, len);
             const int n = j0 + (row & 1 ? j2 : j);
-            if (n < nn && t < s.L && !(NS == 1 && (row & 1)))
-                store8<0>(row_at<float>(m, row & 2 ? kDC : kDB, n), t, s.L, w);
+            if (n < nn && t < len && !(NS == 1 && (row & 1)))
+                store8<0>(row_at<float>(m, row & 2 ? kDC : kDB, n), t, len, w);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (live) {
@@ -416,7 +425,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
             if (o.last) {
                 float slope[8];
                 widen8<DT>(od, slope);
-                slopes<DT>(slope, bias, s.softplus);
+                slopes<DT>(slope, bias, s.softplus, t, t0 + kT, len);
                 get_steps(m.dt, wave, lane, dt);
                 get_steps(m.e, wave, lane, e);
                 widen8<DT>(ox, xv);
@@ -425,12 +434,11 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     get_steps(m.zslope, wave, lane, zslope);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, xv[i], sv[i]);
-                    zero_past(zslope, t, t0 + kT, len);
-                    store8<DT>(row_at<T>(m, kDz, own), t, s.L, zslope);
+                    store8<DT>(row_at<T>(m, kDz, own), t, len, zslope);
                 }
-                finish_steps(xv, slope, dt, e, skip, t, t0 + kT, len, sdt, sgB, sb, sD);
-                store8<DT>(row_at<T>(m, kDdelta, own), t, s.L, sdt);
-                store8<DT>(row_at<T>(m, kDx, own), t, s.L, sgB);
+                finish_steps(xv, slope, dt, e, skip, sdt, sgB, sb, sD);
+                store8<DT>(row_at<T>(m, kDdelta, own), t, len, sdt);
+                store8<DT>(row_at<T>(m, kDx, own), t, len, sgB);
             }
         }
     }
@@ -479,7 +487,7 @@ __global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, B
         load8<DT>(at_row<const T>(s.dy, b, d), t, len, e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) slope[i] = dt[i];
-        slopes<DT>(slope, bias, s.softplus);
+        slopes<DT>(slope, bias, s.softplus, t, t + 8, len);
         step_sizes(dt, bias, s.softplus, t, t + 8, len);
         if (s.z.data) {
             float z[8], zslope[8];
@@ -487,12 +495,16 @@ __global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, B
             gate<DT>(e, z, zslope);
 #pragma unroll
             for (int i = 0; i < 8; ++i) zslope[i] *= __builtin_fmaf(skip, x[i], sum[2][i]);
-            zero_past(zslope, t, t + 8, len);
-            store8<DT>(at_row<T>(s.dz, b, d), t, s.L, zslope);
+            store8<DT>(at_row<T>(s.dz, b, d), t, len, zslope);
+            if (len < s.L && t + 8 > len) zero_past<DT>(at_row<T>(s.dz, b, d), t, len, s.L);
         }
-        finish_steps(x, slope, dt, e, skip, t, t + 8, len, sum[0], sum[1], sb, sD);
-        store8<DT>(at_row<T>(s.ddelta, b, d), t, s.L, sum[0]);
-        store8<DT>(at_row<T>(s.dx, b, d), t, s.L, sum[1]);
+        finish_steps(x, slope, dt, e, skip, sum[0], sum[1], sb, sD);
+        store8<DT>(at_row<T>(s.ddelta, b, d), t, len, sum[0]);
+        store8<DT>(at_row<T>(s.dx, b, d), t, len, sum[1]);
+        if (len < s.L && t + 8 > len) {
+            zero_past<DT>(at_row<T>(s.ddelta, b, d), t, len, s.L);
+            zero_past<DT>(at_row<T>(s.dx, b, d), t, len, s.L);
+        }
     }
     sD = prefix_sum(sD);
     sb = prefix_sum(sb);

@@ -191,15 +191,14 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
 #pragma unroll
             for (int q = 0; q < ITEMS; q += 8) {
                 float (&out)[8] = *(float (*)[8])(v + q);
-                if (t + q >= s.L) break;
+                if (t + q >= len) break;
                 if (z) {
                     float zv[8];
                     load8<DT>(z, t + q, len, zv);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) out[i] *= zv[i] * logistic_for<DT>(zv[i]);
                 }
-                zero_past(out, t + q, t0 + kT, len);
-                store8<DT>(y, t + q, s.L, out);
+                store8<DT>(y, t + q, len, out);
             }
         }
     }
@@ -213,9 +212,11 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(miconv_sca
             for (int c = t0 / kScanChunk; c * kScanChunk < stop; ++c) s.states[(row * saved + c) * s.N + n] = h;
     }
     if (SHARE && wave) return;
-    for (int t = t0 + sub * 8; t < stop; t += LANES * 8) {
+    // what lies past the end is not computed (an infinite state would make padding NaN)
+    const int past = SHARE ? t0 : (len < start ? start : len);
+    for (int t = past + sub * 8; t < stop; t += LANES * 8) {
         const float zero[8] = {};
-        store8<DT>(y, t, s.L, zero);
+        store8<DT>(y, t, stop, zero);
     }
 }
 

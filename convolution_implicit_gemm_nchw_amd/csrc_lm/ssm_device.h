@@ -337,15 +337,6 @@ DEVI void step_sizes(float (&dt)[N], float bias, int use_softplus, int t, int ch
     }
 }
 
-// Outputs past the sequence's end in place of v, which there is what the row's state and parameters
-// made of zeros: NaN, where they hold an infinity.  Only a chunk that reaches past it looks.
-DEVI void zero_past(float (&v)[8], int t, int chunk_end, int end) {
-    if (chunk_end > end) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = t + i < end ? v[i] : 0.0f;
-    }
-}
-
 DEVI int valid_steps(const int *lengths, int b, int L) {
     if (!lengths) return L;
     const int n = lengths[b];
