@@ -88,7 +88,10 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(miconv_causal_conv
 // those steps again instead takes two more loads and (K-1)/8 more gates per step: 16 x 2048
 // x 1024, K 4, bf16: 60 us.)  A thread keeps its part of dw and dbias; the parts are added
 // in a fixed tree and written to part[split][d][K+1] (or dw, dbias).
-template <int DT, int K>
+// A step past the end (du = 0) stands before values of its window that belong to the sequence: without
+// SILU it is left out of dw, so that an infinity among them stays in its own tap.  With SILU such a
+// value has made du of its last step NaN, and with it all taps (selects there cost 8 %: 3 x 1001 x 1533).
+template <int DT, int K, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(miconv_causal_conv_t c, int tiles, long long per, int splits,
                                                         float *part, uint32_t first_channel) {
     typedef typename Elem<DT>::T T;
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(miconv_causal_conv
             load8<DT>(dy, t, len, *(float (*)[8])g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (!c.silu) continue;
+                if (!SILU) continue;
                 float u = bias;
 #pragma unroll
                 for (int k = 0; k < K; ++k) u = __builtin_fmaf(w[k], v[8 + i - (K - 1) + k], u);
@@ -149,12 +152,27 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(miconv_causal_conv
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     s = __builtin_fmaf(w[k], g[i + K - 1 - k], s);
-                    dw[k] = __builtin_fmaf(g[i], v[8 + i - (K - 1) + k], dw[k]);
+                    if (SILU) dw[k] = __builtin_fmaf(g[i], v[8 + i - (K - 1) + k], dw[k]);
                 }
                 db += g[i];
                 const int j = t + i - len + K - 1;   // final_state[j] is x[t + i]
                 if (dfs && j >= 0 && t + i < len) s += Elem<DT>::get(dfs[j]);
                 out[i] = t + i < len ? s : 0.0f;
+            }
+            if constexpr (!SILU) {
+                const int own = len - t;
+                if (own >= 8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k] = __builtin_fmaf(g[i], v[8 + i - (K - 1) + k], dw[k]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            dw[k] = i < own ? __builtin_fmaf(g[i], v[8 + i - (K - 1) + k], dw[k]) : dw[k];
+                }
             }
             if (c.dx.data) store8<DT>((T *)c.dx.data + bb * c.dx.stride_b + d * c.dx.stride_d, t, c.L, out);
             if (t == 0 && c.d_initial_state) {
@@ -268,8 +286,9 @@ int bwd_k(const miconv_causal_conv_t &c, int splits, float *ws, hipStream_t st) 
     const long long items = (long long)c.B * tiles, per = (items + splits - 1) / splits;
     // up to four waves; fewer only where they hold all of a channel's tiles at once
     const int waves = per >= 4 * 63 ? 4 : (int)((per + 62) / 63);
+    const auto kern = c.silu ? causal_bwd_kernel<DT, K, true> : causal_bwd_kernel<DT, K, false>;
     const int bad = launch_groups(c.D, waves * 64, [&](unsigned n, unsigned first) {
-        hipLaunchKernelGGL((causal_bwd_kernel<DT, K>), dim3(n, splits), dim3(waves * 64), 0, st, c, tiles, per, splits, ws,
+        hipLaunchKernelGGL(kern, dim3(n, splits), dim3(waves * 64), 0, st, c, tiles, per, splits, ws,
                            first);
     });
     if (bad != MICONV_OK) return bad;

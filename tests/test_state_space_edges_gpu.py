@@ -94,3 +94,30 @@ def test_step_of_size_zero(mc, N):
     for a in (-1.0, -1e30, -3e38):
         mc.selective_scan_step(x, delta, torch.full((5, N), a, device=DEV), Bm, Bm, state, softplus=True, state_out=out)
         assert torch.equal(out, state), a
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_convolution_gradients_keep_an_infinity_in_its_tap(mc, dt):
+    """Without an activation dw[k] = sum_t dy[t] x[t-K+1+k]: an infinity at the last step reaches the last
+    tap alone, whatever the length leaves of an eight-step tile."""
+    K, D = 4, 3
+    for L, n in ((13, None), (16, None), (24, 13), (700, 509)):
+        f = base.Data(L, dt)
+        x, dy, w = f.make(2, D, L)[1], f.make(2, D, L)[1], f.make(D, K)[1]
+        h0 = f.make(2, D, K - 1)[1]
+        lengths = None if n is None else torch.tensor([n, n], dtype=torch.int32, device=DEV)
+        call = dict(lengths=lengths, initial_state=h0, bias=torch.zeros(D, device=DEV))
+        clean = mc.causal_conv1d_bwd(x, w, dy, **call)
+        x[1, 1, (n or L) - 1] = INF
+        dy[1, 1, (n or L) - 1] = 1.0
+        dx, dw, db = mc.causal_conv1d_bwd(x, w, dy, **call)
+        assert float(dw[1, K - 1]) == INF and bool(dw[1, :K - 1].isfinite().all()), (L, n, dw[1])
+        assert bool(dx.isfinite().all()) and bool(db.isfinite().all())
+        assert torch.equal(dw[[0, 2]], clean[1][[0, 2]])
+    # one valid step: of the state before it only the taps that reach it
+    x, dy, w, h0 = (base.Data(9, dt).make(*s)[1] for s in ((1, D, 20), (1, D, 20), (D, K), (1, D, K - 1)))
+    h0[0, 1, K - 2] = INF
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    _, dw, _ = mc.causal_conv1d_bwd(x, w, dy, lengths=one, initial_state=h0)
+    finite = dw[1].isfinite().tolist()
+    assert finite == [True, True, False, True], dw[1]
