@@ -688,12 +688,24 @@ for _name, _args in {
     _fn.argtypes = _args
     _fn.restype = _I
 
-_bind_path = os.path.join(_HERE, "_miconv_bind.so")
-if not os.path.exists(_bind_path):
-    raise ImportError(f"{_bind_path} is not built; run `python convolution_implicit_gemm_nchw_amd/build.py`.")
-from . import _miconv_bind as _bind  # noqa: E402
+BIND_PATH = os.path.join(_HERE, "_miconv_bind.so")
 
-_bind.errors(_check, torch.OutOfMemoryError)
+
+class _Unloaded:
+    """Stands for the binding module until one of its functions is asked for: the convolutions, which do
+    without it, can then be used where it is not built."""
+
+    def __getattr__(self, name):
+        global _bind
+        if not os.path.exists(BIND_PATH):
+            raise ImportError(f"{BIND_PATH} is not built; run `python convolution_implicit_gemm_nchw_amd/build.py`.")
+        from . import _miconv_bind
+        _miconv_bind.errors(_check, torch.OutOfMemoryError)
+        _bind = _miconv_bind
+        return getattr(_bind, name)
+
+
+_bind = _Unloaded()
 
 
 def _call(fn, stream, *args):

@@ -30,3 +30,32 @@ def test_workspace_size_under_any_limit(name):
     none, some, large, huge, top = sizes(call, (0, 1000, 10 ** 9, 1 << 63, SIZE_MAX))
     assert none == 0 and some < large
     assert large == huge == top and large > 0
+
+
+def test_the_convolutions_need_no_binding_module(tmp_path):
+    """A package without _miconv_bind.so imports and serves the convolutions; the operators that need it say so."""
+    import os
+    import subprocess
+    import sys
+    package = tmp_path / "convolution_implicit_gemm_nchw_amd"
+    package.mkdir()
+    here = os.path.dirname(mc.__file__)
+    for name in ("__init__.py", "libmiconv.so"):
+        os.symlink(os.path.join(here, name), package / name)
+    code = """
+import torch
+import convolution_implicit_gemm_nchw_amd as mc
+assert mc.__file__.startswith({0!r})
+assert mc.workspace_size(mc.FWD, mc.F32, [2, 8, 16, 16, 8, 3, 3, 1, 1, 1, 1, 16, 16]) >= 0
+assert mc.selective_scan_fwd_describe(1, 16, 40, 4)
+for _ in range(2):
+    try:
+        mc.quantize_tokens(torch.zeros(2, 3))
+    except ImportError as e:
+        assert "_miconv_bind.so" in str(e) and "build.py" in str(e)
+    else:
+        raise AssertionError("no ImportError")
+""".format(str(package))
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert r.returncode == 0, r.stderr
