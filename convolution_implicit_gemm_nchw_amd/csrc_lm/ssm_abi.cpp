@@ -42,17 +42,25 @@ int check_out_rows(const Span &s) {
     return b_outer || d_outer ? MICONV_OK : MICONV_ERR_BAD_DIM;
 }
 
-// Whether two tensors share memory.  Ranges that interleave are told apart when
-// both have the same batch stride, as two halves of one projection have.
+// The bytes that a tensor's rows cover modulo `period`, from its first on: an axis whose stride
+// is a multiple of it adds none.
+long long window(const Span &s, long long period) {
+    const long long es = (long long)s.es, b = (s.nb - 1) * s.sb * es, d = (s.nd - 1) * s.sd * es;
+    return s.L * es + (s.sb * es % period ? b : 0) + (s.sd * es % period ? d : 0);
+}
+
+// Whether two tensors share memory.  Ranges that interleave are told apart where one of their strides
+// repeats both, each in a part of its own: halves of one projection, or slices along time of one buffer.
 bool share(const Span &a, const Span &b) {
     if (!a.at || !b.at) return false;
     const size_t an = a.bytes(), bn = b.bytes();
     if (a.at + an <= b.at || b.at + bn <= a.at) return false;
-    if (a.sb == b.sb && a.sb > 0 && a.es == b.es && a.nb > 1 && b.nb > 1) {
-        const long long ra = (a.nd - 1) * a.sd + a.L, rb = (b.nd - 1) * b.sd + b.L;
-        long long off = ((long long)(b.at - a.at)) % (long long)(a.sb * a.es);
-        if (off < 0) off += a.sb * (long long)a.es;
-        if (off >= ra * (long long)a.es && off + rb * (long long)a.es <= a.sb * (long long)a.es) return false;
+    const long long es_a = (long long)a.es, es_b = (long long)b.es;
+    for (const long long period : {a.sb * es_a, a.sd * es_a, b.sb * es_b, b.sd * es_b}) {
+        if (period <= 0) continue;
+        long long off = (long long)(b.at - a.at) % period;
+        if (off < 0) off += period;
+        if (off >= window(a, period) && off + window(b, period) <= period) return false;
     }
     return true;
 }

@@ -121,3 +121,39 @@ def test_convolution_gradients_keep_an_infinity_in_its_tap(mc, dt):
     _, dw, _ = mc.causal_conv1d_bwd(x, w, dy, lengths=one, initial_state=h0)
     finite = dw[1].isfinite().tolist()
     assert finite == [True, True, False, True], dw[1]
+
+
+def test_slices_of_one_buffer(mc):
+    """Operands and outputs that lie in one buffer without sharing an element: slices along time, every
+    other channel, batches inside channels.  One element more is refused."""
+    B, D, L, N = 2, 5, 24, 3
+    f = base.Data(4, "f32")
+    x, dl, w = f.make(B, D, L)[1], f.make(B, D, L)[1], f.make(D, 4)[1]
+    want = mc.causal_conv1d_fwd(x, w, silu=True)
+    time = torch.zeros(B, D, 2 * L, device=DEV)
+    inner = torch.zeros(D, 2, B, L, device=DEV).permute(2, 1, 0, 3)
+    for xs, ys in ((time[:, :, :L], time[:, :, L:]), (time[:, :, L:], time[:, :, :L]),
+                   (torch.zeros(B, 2 * D, L, device=DEV)[:, i::2] for i in (0, 1)), (inner[:, 0], inner[:, 1])):
+        xs.copy_(x)
+        mc.causal_conv1d_fwd(xs, w, silu=True, y=ys)
+        assert torch.equal(ys, want) and torch.equal(xs, x)
+    with pytest.raises(ValueError):
+        mc.causal_conv1d_fwd(time[:, :, :L], w, y=time[:, :, L - 1:2 * L - 1])
+    with pytest.raises(ValueError):
+        mc.causal_conv1d_fwd(inner[:, 0], w, y=inner[:, 0])
+    # the three gradients of a scan next to each other, row by row
+    A, Bm, Cm = -torch.rand(D, N, device=DEV), f.make(B, 1, N, L)[1], f.make(B, 1, N, L)[1]
+    states = mc.selective_scan_states(x, A)
+    mc.selective_scan_fwd(x, dl, A, Bm, Cm, z=x, softplus=True, states=states)
+    r = mc.selective_scan_bwd(x, dl, A, Bm, Cm, x, states, z=x, softplus=True)
+    out = torch.zeros(B, D, 3, L, device=DEV)
+    mc.selective_scan_bwd(x, dl, A, Bm, Cm, x, states, z=x, softplus=True, dx=out[:, :, 0], ddelta=out[:, :, 1],
+                          dz=out[:, :, 2])
+    for i, k in enumerate(("dx", "ddelta", "dz")):
+        assert torch.equal(out[:, :, i], r[k]), k
+    # one step: every other value of a buffer
+    pairs, state = torch.zeros(B, 2 * D, device=DEV), f.make(B, D, 3)[1]
+    y = mc.causal_conv1d_step(x[..., 0], state.clone(), w)
+    pairs[:, ::2] = x[..., 0]
+    mc.causal_conv1d_step(pairs[:, ::2], state, w, y=pairs[:, 1::2])
+    assert torch.equal(pairs[:, 1::2], y)
