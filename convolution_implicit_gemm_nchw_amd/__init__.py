@@ -678,7 +678,8 @@ for _name, _args in {
         "selective_scan_states_size": [_I, _I, _I, _I, _SZP],
         "selective_scan_bwd_workspace_size": [_VP, _I, _SZP],
         "selective_scan_fwd_describe": [_VP, _I, _SZ, ctypes.c_char_p, _SZ],
-        "selective_scan_bwd_describe": [_VP, _I, ctypes.c_char_p, _SZ],
+        "selective_scan_bwd_workspace_size_ex": [_VP, _I, _SZ, _SZP],
+        "selective_scan_bwd_describe": [_VP, _I, _SZ, ctypes.c_char_p, _SZ],
         "selective_scan_step": [_VP, _I, _VP, _I, _VP, _VP, _VP],
         "quantize_tokens": [_I, _I, _I, _I, _VP, _LL, _LL, _LL, _VP, _VP, _VP],
         "matmul_i8": [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _SZ, _VP],
@@ -785,10 +786,19 @@ def selective_scan_fwd_describe(B, D, L, N, G=1, dtype=F32, workspace_bytes=MAX_
     return buf.value.decode()
 
 
-def selective_scan_bwd_describe(B, D, L, N, G=1, dtype=F32):
-    """The time segments and blocks of states that selective_scan_bwd takes for these sizes."""
+def selective_scan_bwd_workspace(B, D, L, N, G=1, dtype=F32, limit=MAX_WORKSPACE_BYTES):
+    """The workspace that selective_scan_bwd uses under `limit`, or the least it needs if that is more."""
+    out = _SZ(0)
+    _check(_lib.selective_scan_bwd_workspace_size_ex(ctypes.byref(_Scan(B=B, D=D, L=L, N=N, G=G)), dtype, limit,
+                                                     ctypes.byref(out)), "selective_scan_bwd_workspace_size_ex")
+    return out.value
+
+
+def selective_scan_bwd_describe(B, D, L, N, G=1, dtype=F32, workspace_bytes=MAX_WORKSPACE_BYTES):
+    """The time segments, blocks of states and slices (sequences x groups x channels x steps) that selective_scan_bwd
+    takes for these sizes."""
     buf = ctypes.create_string_buffer(256)
-    _check(_lib.selective_scan_bwd_describe(ctypes.byref(_Scan(B=B, D=D, L=L, N=N, G=G)), dtype, buf, 256),
+    _check(_lib.selective_scan_bwd_describe(ctypes.byref(_Scan(B=B, D=D, L=L, N=N, G=G)), dtype, workspace_bytes, buf, 256),
            "selective_scan_bwd_describe")
     return buf.value.decode()
 

@@ -49,6 +49,7 @@ struct BwdOut {
                               // [blocks of 16 states] of them
     int parts;
     int n_first, n_end, last; // states of this launch (side by side: 16 per blockIdx.y); whether it finishes
+    int t_first, chunks;      // a slice of the time steps: its first one; saved states per row
 };
 
 // Per-step values of the 16 channels: [group][half][64 lanes][4 steps].
@@ -175,7 +176,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
     const int channels = per_group - part * kCh < kCh ? per_group - part * kCh : kCh;
     const int n_first = o.n_first + blockIdx.y * kStates;                // states of the work-group, of the wave
     const int nn = o.n_end - n_first < kStates ? o.n_end - n_first : kStates, j0 = wave * NS;
-    const int len = valid_steps(s.lengths, b, s.L);
+    const int len = valid_steps(s.lengths, b, s.L, o.t_first);
     const int chunks = (s.L + kT - 1) / kT;
     const int c_first = seg * o.seg_chunks, c_end = c_first + o.seg_chunks < chunks ? c_first + o.seg_chunks : chunks;
     // the channel that this lane owns between the turns
@@ -307,7 +308,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(miconv_scan_t s, BwdOu
                     }
                     float h0s[NS];
                     const bool there = ch < channels && sub == 0;
-                    const float *entry = s.states + (((long long)b * s.D + first + (there ? ch : 0)) * chunks + c) * s.N + n_first;
+                    const float *entry = s.states + (((long long)b * s.D + first + (there ? ch : 0)) * o.chunks + c) * s.N + n_first;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) h0s[j] = there && j0 + j < nn ? entry[j0 + j] : 0.0f;
                     float all = 0.0f;
@@ -469,7 +470,8 @@ __global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, B
     const int lane = threadIdx.x & 63;
     const long long row = (long long)blockIdx.x * 4 + uniform(threadIdx.x >> 6), rows = (long long)s.B * s.D;
     if (row >= rows) return;
-    const int b = (int)(row / s.D), d = (int)(row - (long long)b * s.D), len = valid_steps(s.lengths, b, s.L);
+    const int b = (int)(row / s.D), d = (int)(row - (long long)b * s.D);
+    const int len = valid_steps(s.lengths, b, s.L, o.t_first);
     const float bias = s.delta_bias ? s.delta_bias[d] : 0.0f, skip = s.D_skip ? s.D_skip[d] : 0.0f;
     float sD = 0.0f, sb = 0.0f;
     for (int t = lane * 8; t < s.L; t += 512) {
@@ -523,7 +525,7 @@ __global__ __launch_bounds__(256) void scan_bwd_finish_kernel(miconv_scan_t s, B
 struct Carry {
     float *G;                 // [B][D][chunks][N]
     float *ends, *after;      // [B][D][segs][N + 1] G and sum of dt; [B][D][chunks] dt up to the segment's end
-    int segs, steps;
+    int segs, steps, t_first;
 };
 
 constexpr int kCarryWaves = 8, kCarryItems = 16, kCarryT = 64 * kCarryItems;
@@ -542,7 +544,7 @@ __global__ __launch_bounds__(64 * kCarryWaves, 4) void scan_bwd_carry_kernel(mic
     const bool live = in_group < per_group;
     const int d = g * per_group + (live ? in_group : 0);
     const long long row = (long long)b * s.D + d;
-    const int len = valid_steps(s.lengths, b, s.L), chunks = (s.L + kT - 1) / kT;
+    const int len = valid_steps(s.lengths, b, s.L, out.t_first), chunks = (s.L + kT - 1) / kT;
     const T *dl = at_row<const T>(s.delta, b, d), *dy = at_row<const T>(s.dy, b, d);
     const T *z = s.z.data ? at_row<const T>(s.z, b, d) : nullptr;
     const T *Cm = (const T *)s.Cm.data + b * s.Cm.stride_b + g * s.Cm.stride_g;
@@ -642,7 +644,8 @@ struct SumJob {
     const float *part;
     float *out;
     long long n;
-    int parts;
+    int parts, add;           // add: to what out holds
+    int row, row_out;         // out's rows of `row` are row_out apart, where that is more
 };
 struct SumJobs {
     SumJob j[5];
@@ -682,7 +685,11 @@ __global__ __launch_bounds__(64 * kSumWaves) void scan_bwd_sum(SumJobs jobs, uin
         for (int w = 1; w < kSumWaves; ++w) a += share[w][lane];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (i + e < j.n) j.out[i + e] = a[e];
+            if (i + e < j.n) {
+                long long at = i + e;
+                if (j.row < j.row_out) at += at / j.row * (j.row_out - j.row);
+                j.out[at] = j.add ? j.out[at] + a[e] : a[e];
+            }
     }
 }
 
@@ -692,8 +699,9 @@ __global__ __launch_bounds__(64 * kSumWaves) void scan_bwd_sum(SumJobs jobs, uin
 // the time axis can be split too, at the price of a pass that finds G between the segments.
 // It is where the estimate for N = 16, bf16 gains: a chunk takes 11 us of a work-group alone on its CU and 14 of
 // two, 1024 steps of the pass between 12 and 20 (4096 rows of 512: 60 us whole, 68 in two; of 1024: 105 and
-// 95; 1024 rows of 256: 32 and 35; of 512: 54 and 37).
-ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
+// 95; 1024 rows of 256: 32 and 35; of 512: 54 and 37).  `whole` takes neither segments nor blocks of states
+// side by side: the least workspace.
+static ScanBwdPlan plan_rows(const miconv_scan_t &s, bool whole) {
     ScanBwdPlan p;
     p.parts = (s.D / s.G + kCh - 1) / kCh;
     const long long groups = (long long)s.B * s.G * p.parts;
@@ -702,7 +710,7 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     p.seg_chunks = chunks;
     p.carry_segs = 1;
     p.carry_steps = 0;
-    if (groups * 2 <= 512 && chunks > 1) {
+    if (groups * 2 <= 512 && chunks > 1 && !whole) {
         const long long segs = 512 / groups < chunks ? 512 / groups : chunks;
         const int seg_chunks = (int)((chunks + segs - 1) / segs);
         // the pass between the segments is split as the forward scan is
@@ -724,7 +732,7 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     // blocks of 16 states side by side where one of them leaves CUs without a second work-group (64
     // states, bf16: 1024 rows of 300 170 -> 64 us, 4096 of 128 81 -> 62, 4 x 100 of 2, with the
     // forward pass, 106 -> 58; a block of one state costs: 17 states, 4096 rows of 100 45 -> 48)
-    p.beside = s.N > kStates && groups * p.segs <= 256 ? (s.N + kStates - 1) / kStates : 1;
+    p.beside = s.N > kStates && groups * p.segs <= 256 && !whole ? (s.N + kStates - 1) / kStates : 1;
     const size_t bc = (size_t)p.parts * s.B * s.G * s.N * s.L, bd = (size_t)s.B * s.D;
     p.off_dB = 0;
     p.off_dC = bc;
@@ -739,8 +747,106 @@ ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s) {
     return p;
 }
 
-int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st) {
-    const ScanBwdPlan p = plan_scan_bwd(s);
+ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s, size_t budget) {
+    const ScanBwdPlan p = plan_rows(s, false);
+    return p.bytes <= budget ? p : plan_rows(s, true);
+}
+
+// Of `sequences` sequences from b on, the channels from `first` on in groups from g on, and the steps from t on.
+// More than one sequence goes with all groups and channels, more than one group with all channels.
+static miconv_scan_t slice_of(const miconv_scan_t &s, size_t es, int b, int sequences, int g, int groups, size_t first,
+                              int channels, int t, int steps) {
+    miconv_scan_t r = s;
+    const size_t row = (size_t)b * s.D + first;
+    r.B = sequences;
+    r.G = groups;
+    r.D = groups * channels;
+    r.L = steps;
+    for (miconv_rows_t *v : {&r.x, &r.delta, &r.z, &r.dy, &r.dx, &r.ddelta, &r.dz})
+        if (v->data) v->data = (char *)v->data + ((size_t)b * v->stride_b + first * v->stride_d + t) * es;
+    for (miconv_scan_in_t *v : {&r.Bm, &r.Cm}) v->data = (char *)v->data + ((size_t)b * v->stride_b + (size_t)g * v->stride_g + t) * es;
+    if (s.lengths) r.lengths = s.lengths + b;
+    r.A = s.A + first * s.N;
+    if (s.D_skip) r.D_skip = s.D_skip + first;
+    if (s.delta_bias) r.delta_bias = s.delta_bias + first;
+    r.states = s.states + (row * scan_chunks(s.L) + t / kScanChunk) * s.N;
+    if (s.d_final_state) r.d_final_state = s.d_final_state + row * s.N;
+    if (s.d_initial_state) r.d_initial_state = s.d_initial_state + row * s.N;
+    r.dA = s.dA + first * s.N;
+    if (s.dD) r.dD = s.dD + first;
+    if (s.ddelta_bias) r.ddelta_bias = s.ddelta_bias + first;
+    const size_t bc = ((size_t)b * s.G + g) * s.N * s.L + t;
+    r.dB = s.dB + bc;
+    r.dC = s.dC + bc;
+    return r;
+}
+
+// The most of `n`, in equal shares of whole `unit`s, whose bytes(share) fit the budget; one unit if none do.
+template <typename F>
+static int share_within(int n, int unit, size_t budget, F bytes) {
+    if (n <= unit || bytes(n) <= budget) return n;
+    int fits = 1, over = (n + unit - 1) / unit;                   // units
+    while (over - fits > 1) {
+        const int mid = fits + (over - fits) / 2;
+        (bytes(mid * unit) <= budget ? fits : over) = mid;
+    }
+    const int most = fits * unit, shares = (n + most - 1) / most, even = (n + shares - 1) / shares;
+    return (even + unit - 1) / unit * unit;
+}
+
+// Slices cost least where each still gives the CUs their two work-groups each (512): so sequences are
+// sliced down to that, then the time axis, which only adds launches, then the rows left.
+// (In 10^9 bytes and in what they take whole, bf16: 8 x 8192 rows of 8192, N 16: 8.4 ms in 8 slices, 7.9 whole in
+// 4.3 GB; 1 x 8192 of 65536: 8.3 in 5, 8.1 in 4.3 GB; 2 x 8192 of 8192, N 64: 9.2 in 8, 8.7 in 5.9 GB.)
+ScanBwdSlice slice_scan_bwd(const miconv_scan_t &s, size_t budget) {
+    const int per_group = s.D / s.G, chunks = scan_chunks(s.L);
+    ScanBwdSlice r = {s.B, s.G, per_group, s.L, 0, 0};
+    const auto size = [&](bool whole) {
+        miconv_scan_t one = s;
+        one.B = r.sequences;
+        one.G = r.groups;
+        one.D = r.groups * r.channels;
+        one.L = r.steps;
+        r.carry = r.steps < s.L ? 2 * (size_t)one.B * one.D * s.N : 0;
+        r.bytes = r.carry * 4 + plan_rows(one, whole).bytes;
+        return r.bytes;
+    };
+    if (size(false) <= budget) return r;
+    const long long per_sequence = (long long)s.G * ((per_group + kCh - 1) / kCh);
+    const int filling = (int)(per_sequence >= 512 ? 1 : (512 + per_sequence - 1) / per_sequence);
+    if (s.B > filling) {
+        r.sequences = share_within(s.B, 1, budget, [&](int n) { r.sequences = n; return size(false); });
+        if (r.sequences < filling) r.sequences = filling;
+    }
+    const auto sliced = [&](int n) {
+        r.steps = n < chunks ? n * kT : s.L;
+        return size(false);
+    };
+    if (size(false) > budget) sliced(share_within(chunks, 1, budget, sliced));
+    if (r.bytes > budget && r.sequences > 1) {
+        r.sequences = share_within(r.sequences, 1, budget, [&](int n) { r.sequences = n; return size(false); });
+        size(false);
+    }
+    if (r.bytes > budget && r.groups > 1) {
+        r.groups = share_within(s.G, 1, budget, [&](int n) { r.groups = n; return size(false); });
+        size(false);
+    }
+    if (r.bytes > budget) {
+        r.channels = share_within(per_group, kCh, budget, [&](int n) { r.channels = n; return size(false); });
+        size(false);
+    }
+    if (r.bytes > budget) size(true);
+    return r;
+}
+
+// What one slice does about the others.
+struct BwdPlace {
+    int add_bc, add_rest;     // dB and dC, the other sums over sequences hold those of earlier slices
+    int t, L;                 // its first step, all steps
+};
+
+static int launch_slice(const miconv_scan_t &s, int dtype, size_t budget, const BwdPlace &place, float *ws, hipStream_t st) {
+    const ScanBwdPlan p = plan_scan_bwd(s, budget);
     BwdOut o;
     o.dB = ws + p.off_dB;
     o.dC = ws + p.off_dC;
@@ -752,9 +858,11 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     o.parts = p.parts;
     o.segs = p.segs;
     o.seg_chunks = p.seg_chunks;
+    o.t_first = place.t;
+    o.chunks = scan_chunks(place.L);
     if (p.segs > 1) {
         const int blocks_g = (s.D / s.G + kCarryWaves - 1) / kCarryWaves;
-        const Carry out = {ws + p.off_G, ws + p.off_ends, ws + p.off_after, p.carry_segs, p.carry_steps};
+        const Carry out = {ws + p.off_G, ws + p.off_ends, ws + p.off_after, p.carry_segs, p.carry_steps, place.t};
         const dim3 cgrid((unsigned)((long long)s.B * s.G * blocks_g * p.carry_segs)), cblock(64 * kCarryWaves);
         if (dtype)
             hipLaunchKernelGGL(scan_bwd_carry_kernel<1>, cgrid, cblock, 0, st, s, out, blocks_g);
@@ -793,15 +901,36 @@ int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st
     }
     SumJobs jobs = {};
     const long long bc = (long long)s.B * s.G * s.N * s.L;
-    jobs.j[jobs.count++] = {o.dB, s.dB, bc, p.parts};
-    jobs.j[jobs.count++] = {o.dC, s.dC, bc, p.parts};
-    jobs.j[jobs.count++] = {o.dA, s.dA, (long long)s.D * s.N, s.B * p.segs};
-    if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B * time_parts};
-    if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B * time_parts};
+    jobs.j[jobs.count++] = {o.dB, s.dB, bc, p.parts, place.add_bc, s.L, place.L};
+    jobs.j[jobs.count++] = {o.dC, s.dC, bc, p.parts, place.add_bc, s.L, place.L};
+    jobs.j[jobs.count++] = {o.dA, s.dA, (long long)s.D * s.N, s.B * p.segs, place.add_rest, 0, 0};
+    if (s.dD) jobs.j[jobs.count++] = {o.dD, s.dD, s.D, s.B * time_parts, place.add_rest, 0, 0};
+    if (s.ddelta_bias) jobs.j[jobs.count++] = {o.db, s.ddelta_bias, s.D, s.B * time_parts, place.add_rest, 0, 0};
     for (int k = 0; k < jobs.count; ++k) jobs.first[k + 1] = jobs.first[k] + (jobs.j[k].n + 255) / 256;
     return launch_groups(jobs.first[jobs.count], 64 * kSumWaves, [&](unsigned groups, unsigned first) {
         hipLaunchKernelGGL(scan_bwd_sum, dim3(groups), dim3(64 * kSumWaves), 0, st, jobs, first);
     });
+}
+
+int launch_scan_bwd(const miconv_scan_t &s, int dtype, const ScanBwdSlice &slice, float *ws, hipStream_t st) {
+    const int per_group = s.D / s.G, last = (s.L - 1) / slice.steps;
+    const size_t budget = slice.bytes - slice.carry * 4;
+    float *const carry[2] = {ws, ws + slice.carry / 2};
+    const auto left = [](long long n, int most) { return (int)(n < most ? n : most); };
+    for (long long b = 0; b < s.B; b += slice.sequences)
+        for (long long g = 0; g < s.G; g += slice.groups)
+            for (long long d = 0; d < per_group; d += slice.channels)
+                for (int k = last; k >= 0; --k) {
+                    const BwdPlace place = {d > 0, b > 0 || k < last, k * slice.steps, s.L};
+                    miconv_scan_t part = slice_of(s, dtype ? 2 : 4, (int)b, left(s.B - b, slice.sequences), (int)g,
+                                                  left(s.G - g, slice.groups), (size_t)g * per_group + d,
+                                                  left(per_group - d, slice.channels), place.t, left(s.L - place.t, slice.steps));
+                    if (k < last) part.d_final_state = carry[(k + 1) & 1];
+                    if (k > 0) part.d_initial_state = carry[k & 1];
+                    const int bad = launch_slice(part, dtype, budget, place, ws + slice.carry, st);
+                    if (bad != MICONV_OK) return bad;
+                }
+    return MICONV_OK;
 }
 
 }  // namespace miconv

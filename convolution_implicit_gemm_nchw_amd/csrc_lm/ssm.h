@@ -56,7 +56,18 @@ struct ScanBwdPlan {
     int carry_segs, carry_steps;        // time segments of the pass that finds G between them
     size_t off_G, off_ends, off_after, off_dB, off_dC, off_dA, off_dD, off_db, off_sums, bytes;   // floats, except bytes
 };
-ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s);
+// The fastest plan within the budget, or the smallest one where none is.
+ScanBwdPlan plan_scan_bwd(const miconv_scan_t &s, size_t budget);
+
+// The backward pass goes through its problem slice by slice where the workspace asks for it: sequences,
+// groups of one sequence, channels of one group (a multiple of kScanBwdChannels), and of each the time
+// steps (a multiple of kScanChunk) from the last on.
+struct ScanBwdSlice {
+    int sequences, groups, channels, steps;
+    size_t carry, bytes;                // floats that pass from one time slice to the next; workspace of the largest
+};
+// The largest slice within the budget, or the smallest there is.
+ScanBwdSlice slice_scan_bwd(const miconv_scan_t &s, size_t budget);
 
 // Work-groups per channel of the convolution's backward pass.
 int causal_bwd_splits(const miconv_causal_conv_t &c, size_t budget);
@@ -68,7 +79,7 @@ int launch_causal_step(int B, int D, int K, int silu, int dtype, miconv_rows_t x
                        hipStream_t st);
 
 int launch_scan_fwd(const miconv_scan_t &s, int dtype, ScanSplit split, float *ws, hipStream_t st);
-int launch_scan_bwd(const miconv_scan_t &s, int dtype, float *ws, hipStream_t st);
+int launch_scan_bwd(const miconv_scan_t &s, int dtype, const ScanBwdSlice &slice, float *ws, hipStream_t st);
 int launch_scan_step(const miconv_scan_t &s, int dtype, const float *state, int slots, const int *slot_of,
                      float *state_out, hipStream_t st);
 

@@ -272,12 +272,23 @@ int selective_scan_fwd_describe(const miconv_scan_t *s, int dtype, size_t worksp
     return MICONV_OK;
 }
 
-int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out) {
+// The slices of a backward pass with this workspace, of which it uses the cap at most.
+static ScanBwdSlice bwd_slice(const miconv_scan_t &s, size_t workspace_bytes) {
+    const size_t cap = MICONV_MAX_WORKSPACE_BYTES;
+    return slice_scan_bwd(s, workspace_bytes < cap ? workspace_bytes : cap);
+}
+
+int selective_scan_bwd_workspace_size_ex(const miconv_scan_t *s, int dtype, size_t workspace_limit,
+                                         size_t *bytes_out) {
     if (!s || !bytes_out) return MICONV_ERR_NULL;
     const int st = check_scan_sizes(*s, dtype);
     if (st != MICONV_OK) return st;
-    *bytes_out = plan_scan_bwd(*s).bytes;
+    *bytes_out = bwd_slice(*s, workspace_limit).bytes;
     return MICONV_OK;
+}
+
+int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out) {
+    return selective_scan_bwd_workspace_size_ex(s, dtype, MICONV_MAX_WORKSPACE_BYTES, bytes_out);
 }
 
 int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
@@ -285,7 +296,7 @@ int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_
     const int st = check_scan_sizes(*s, dtype);
     if (st != MICONV_OK) return st;
     if (!workspace) return MICONV_ERR_NULL;
-    const ScanBwdPlan p = plan_scan_bwd(*s);
+    const ScanBwdSlice p = bwd_slice(*s, workspace_bytes);
     const size_t es = elem_size(dtype), ns = state_count(*s), nbc = (size_t)s->B * s->G * s->N * s->L;
     if (workspace_bytes < p.bytes) return MICONV_ERR_WORKSPACE;
     if ((s->z.data != nullptr) != (s->dz.data != nullptr)) return MICONV_ERR_NULL;
@@ -306,18 +317,25 @@ int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_
     k.output(flat(s->d_initial_state, ns, 4), false);
     k.output(flat(workspace, p.bytes / 4, 4), true);
     const int bad = k.done();
-    return bad != MICONV_OK ? bad : launch_scan_bwd(*s, dtype, (float *)workspace, (hipStream_t)stream);
+    return bad != MICONV_OK ? bad : launch_scan_bwd(*s, dtype, p, (float *)workspace, (hipStream_t)stream);
 }
 
-int selective_scan_bwd_describe(const miconv_scan_t *s, int dtype, char *buf, size_t buflen) {
+int selective_scan_bwd_describe(const miconv_scan_t *s, int dtype, size_t workspace_bytes, char *buf, size_t buflen) {
     if (!buf || buflen == 0) return MICONV_ERR_NULL;
     buf[0] = 0;
     if (!s) return MICONV_ERR_NULL;
     const int st = check_scan_sizes(*s, dtype);
     if (st != MICONV_OK) return st;
-    const ScanBwdPlan p = plan_scan_bwd(*s);
-    snprintf(buf, buflen, "algo=scan_bwd segments=%d carry_segments=%d beside=%d ws=%zu", p.segs, p.carry_segs, p.beside,
-             p.bytes);
+    const ScanBwdSlice r = bwd_slice(*s, workspace_bytes);
+    if (workspace_bytes < r.bytes) return MICONV_ERR_WORKSPACE;
+    miconv_scan_t one = *s;
+    one.B = r.sequences;
+    one.G = r.groups;
+    one.D = r.groups * r.channels;
+    one.L = r.steps;
+    const ScanBwdPlan p = plan_scan_bwd(one, r.bytes - r.carry * 4);
+    snprintf(buf, buflen, "algo=scan_bwd segments=%d carry_segments=%d beside=%d slice=%dx%dx%dx%d ws=%zu", p.segs,
+             p.carry_segs, p.beside, r.sequences, r.groups, r.channels, r.steps, r.bytes);
     return MICONV_OK;
 }
 

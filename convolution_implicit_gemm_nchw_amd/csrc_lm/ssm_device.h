@@ -337,9 +337,10 @@ DEVI void step_sizes(float (&dt)[N], float bias, int use_softplus, int t, int ch
     }
 }
 
-DEVI int valid_steps(const int *lengths, int b, int L) {
+// Valid steps of sequence b among L from `first` on.
+DEVI int valid_steps(const int *lengths, int b, int L, int first = 0) {
     if (!lengths) return L;
-    const int n = lengths[b];
+    const int n = (lengths[b] < 0 ? 0 : lengths[b]) - first;
     return n < 0 ? 0 : (n > L ? L : n);
 }
 

@@ -559,9 +559,14 @@ int selective_scan_fwd_workspace_size(const miconv_scan_t *s, int dtype, size_t 
 int selective_scan_fwd_describe(const miconv_scan_t *s, int dtype, size_t workspace_bytes, char *buf, size_t buflen);
 int selective_scan_bwd(const miconv_scan_t *s, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 int selective_scan_states_size(int B, int D, int L, int N, size_t *bytes_out);
-/* Workspace the backward pass needs (MICONV_ERR_WORKSPACE when given less). */
+/* Workspace the backward pass uses under workspace_limit (in the first form under
+ * MICONV_MAX_WORKSPACE_BYTES, which it uses at most of whatever it is given).  With less
+ * than the whole problem asks for it goes through it in slices of its rows and time steps; if the
+ * smallest slice (128 steps of 16 channels) asks for more than the limit, that is the
+ * result, and selective_scan_bwd returns MICONV_ERR_WORKSPACE for less. */
 int selective_scan_bwd_workspace_size(const miconv_scan_t *s, int dtype, size_t *bytes_out);
-int selective_scan_bwd_describe(const miconv_scan_t *s, int dtype, char *buf, size_t buflen);
+int selective_scan_bwd_workspace_size_ex(const miconv_scan_t *s, int dtype, size_t workspace_limit, size_t *bytes_out);
+int selective_scan_bwd_describe(const miconv_scan_t *s, int dtype, size_t workspace_bytes, char *buf, size_t buflen);
 /*
  * One time step: x, delta, z, y [B][D], Bm, Cm [B][G][N] (L = 1 in the structure;
  * lengths, initial_state, final_state and states unused), state [slots][D][N]

@@ -74,3 +74,49 @@ def test_product_streams_its_output(mc):
         # sums below 2^24 are exact in fp32, in any order
         want = (q[i:i + 1639].float() @ w.float().t() * s[i:i + 1639, None] * ws).bfloat16()
         assert torch.equal(y[i:i + 1639], want) and torch.equal(ycm[i // 1639], want.t()), i
+
+
+#           B  D   L     N   G  gate  softplus ragged state skip        limits, slice (sequences x groups x channels x steps)
+SLICES = [((3, 40, 300, 5, 2, True, True, True, True, True),
+           [(0, "1x1x16x128"), (20000, "1x1x20x128"), (50000, "2x2x20x128"), (100000, "3x2x20x128"), (10 ** 9, "3x2x20x300")]),
+          ((2, 50, 700, 40, 1, True, True, True, True, True),
+           [(0, "beside=1 slice=1x1x16x128"), (300000, "beside=3 slice=1x1x32x128"), (1000000, "beside=3 slice=2x1x50x128")]),
+          ((1, 20, 5000, 3, 1, False, True, True, False, True),
+           [(30000, "segments=4 carry_segments=1 beside=1 slice=1x1x20x512"),
+            (200000, "segments=20 carry_segments=3 beside=1 slice=1x1x20x2560")]),
+          ((2, 8, 6000, 20, 1, True, False, True, True, False),
+           [(200000, "beside=2 slice=2x1x8x256"), (800000, "segments=8 carry_segments=1 beside=2 slice=2x1x8x1024")])]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case,limits", SLICES, ids=lambda c: "-".join(map(str, c)) if isinstance(c, tuple) else "")
+def test_backward_scan_in_slices(mc, case, limits, dt):
+    """The same gradients from whatever workspace the caller has, none of it past the workspace's end."""
+    import torch
+    B, D, L, N, G, gate, sp, ragged, state, skip = case
+    h, d, nh, n = base.scan_data(case, dt)
+    want = base.scan_reference(h, nh, sp)
+    v = {k: base.view(base.poison(d[k], nh))[0] for k in ("x", "delta", "dy", "z") if k in d}
+    Bm, Cm = (base.poison(d[k], nh) for k in ("Bm", "Cm"))
+    common = dict(D=d.get("D"), z=v.get("z"), delta_bias=d.get("bias"), softplus=sp, lengths=n)
+    states = mc.selective_scan_states(v["x"], d["A"])
+    mc.selective_scan_fwd(v["x"], v["delta"], d["A"], Bm, Cm, initial_state=d.get("h0"), states=states, **common)
+    code = 1 if dt == "bf16" else 0
+    for limit, text in limits:
+        size = mc.selective_scan_bwd_workspace(*case[:5], dtype=code, limit=limit)
+        assert text in mc.selective_scan_bwd_describe(*case[:5], dtype=code, workspace_bytes=size)
+        buf = torch.full((size + 4096,), 0xa5, dtype=torch.uint8, device=base.DEV)
+        outs = {k: base.out_view((B, D, L), dt) for k in ("dx", "ddelta") + (("dz",) if gate else ())}
+        for repeat in range(2):                                 # what a call leaves in the workspace does not matter
+            dh0 = torch.full((B, D, N), float("nan"), device=base.DEV)
+            r = mc.selective_scan_bwd(v["x"], v["delta"], d["A"], Bm, Cm, v["dy"], states, d_final_state=d.get("dfs"),
+                                      d_initial_state=dh0, workspace=buf[:size], **{k: o[0] for k, o in outs.items()}, **common)
+            for name in ("dx", "ddelta", "dz", "dA", "dB", "dC", "dD", "ddelta_bias"):
+                if r[name] is not None:
+                    base.agree(name, r[name], want[name], dt if name in outs else "f32", (case, limit))
+            base.agree("dh0", dh0, want["dh0"], "f32", (case, limit))
+            for _, check in outs.values():
+                check()
+        assert bool((buf[size:] == 0xa5).all())
+    with pytest.raises(ValueError):
+        mc.selective_scan_bwd(v["x"], v["delta"], d["A"], Bm, Cm, v["dy"], states, workspace=buf[:1000], **common)

@@ -59,3 +59,37 @@ for _ in range(2):
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
                        env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert r.returncode == 0, r.stderr
+
+
+LARGE = [(8, 4096, 4096, 16), (8, 8192, 8192, 16), (8, 8192, 8192, 64), (1, 8192, 1 << 20, 64), (1 << 20, 16, 3, 64),
+         (1, 1 << 30, 1, 64), (4096, 8192, 1, 64), (1, 16, 1 << 22, 64), (16, 1024, 16384, 64, 8)]
+
+
+@pytest.mark.parametrize("size", LARGE, ids=lambda s: "-".join(map(str, s)))
+def test_backward_scan_keeps_to_the_workspace_cap(size):
+    need = ctypes.c_size_t(0)
+    B, D, L, N, G = (size + (1,))[:5]
+    s = mc._Scan(B=B, D=D, L=L, N=N, G=G)
+    assert mc.lib().selective_scan_bwd_workspace_size(ctypes.byref(s), 0, ctypes.byref(need)) == OK
+    assert 0 < need.value <= mc.MAX_WORKSPACE_BYTES
+    assert mc.selective_scan_bwd_workspace(*size, limit=SIZE_MAX) == need.value
+
+
+@pytest.mark.parametrize("size", LARGE + [(3, 40, 300, 5, 2), (2, 50, 700, 40), (1, 20, 5000, 3), (2, 8, 6000, 20)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_backward_scan_under_any_limit(size):
+    """The size under a limit is within it, or the least there is; a call given that much uses that much."""
+    least = mc.selective_scan_bwd_workspace(*size, limit=0)
+    assert least <= 2 * 8 * 128 * 64 * 4                      # a slice of 128 steps of 16 channels at most
+    before = 0
+    for limit in [0, least - 1, least] + [10 ** k for k in range(4, 10)] + [SIZE_MAX]:
+        w = mc.selective_scan_bwd_workspace(*size, limit=limit)
+        assert w == least or least < w <= limit
+        assert before <= w
+        before = w
+        assert mc.selective_scan_bwd_workspace(*size, limit=w) == w
+        assert mc.selective_scan_bwd_describe(*size, workspace_bytes=w).endswith(f" ws={w}")
+    with pytest.raises(ValueError):
+        mc.selective_scan_bwd_describe(*size, workspace_bytes=least - 1)
+    B, D, L, N, G = (size + (1,))[:5]
+    assert base.sbwd(B=B, D=D, L=L, N=N, G=G, ws=base.at(30), wb=least - 1) == base.E_WS
