@@ -136,7 +136,8 @@ void check(int status, const char *where) {
     throw Raised();
 }
 
-// Calls fn(..., stream) with the operands' device current, on its current stream.
+// Calls fn(..., stream) with the operands' device current, on its current stream.  fn throws nothing:
+// the device that was current before would not be set again.
 template <typename F>
 void run(const char *where, int dev, F fn) {
     const int now = c10::hip::current_device();
@@ -256,9 +257,9 @@ PyObject *conv_step(Args a) {
     const float *bias = (const float *)optional("bias", a[3], {D}, at::kFloat, x.dev);
     const int silu = truth(a[4]);
     const Out y("y", a[7], x.t.sizes(), x.dt, x, true);
+    const miconv_rows_t xr = rows_of("x", x.t), yr = rows_of("y", y.t);
     run("causal_conv1d_step", x.dev, [&](void *st) {
-        return causal_conv1d_step(B, D, K, silu, x.code, rows_of("x", x.t), in, s.slots, s.slot_of, w, bias, out,
-                                  rows_of("y", y.t), st);
+        return causal_conv1d_step(B, D, K, silu, x.code, xr, in, s.slots, s.slot_of, w, bias, out, yr, st);
     });
     return y.wrap();
 }
@@ -398,9 +399,11 @@ PyObject *quantize(Args a) {
         if (C > 1 && x.t.stride(dims - 1) != 1) refuse("x must have contiguous channels (stride 1 along the last axis)");
     }
     const int64_t pad = (C + MICONV_I8_PAD - 1) / MICONV_I8_PAD * MICONV_I8_PAD;
+    const int B = dim(nb), tokens = dim(L), channels = dim(C);
     const Out q("q", a[2], {nb * L, pad}, at::kChar, x), scale("scale", a[3], {nb * L}, at::kFloat, x);
+    const void *data = x.t.data_ptr();
     run("quantize_tokens", x.dev, [&](void *st) {
-        return quantize_tokens(dim(nb), dim(L), dim(C), x.code, x.t.data_ptr(), sb, sl, sc, (signed char *)q.data(),
+        return quantize_tokens(B, tokens, channels, x.code, data, sb, sl, sc, (signed char *)q.data(),
                                (float *)scale.data(), st);
     });
     return tuple({&q, &scale});
@@ -450,9 +453,10 @@ PyObject *matmul(Args a) {
         held = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
     }
     if (held.defined()) work = held.data_ptr();
+    const int code = code_of(y.scalar_type());
+    void *out = y.data_ptr();
     run("matmul_i8", dev, [&](void *st) {
-        return matmul_i8(B, L, O, K, qp, qs, wp, ws, bias, cm, code_of(y.scalar_type()), y.data_ptr(), work,
-                         work ? need : 0, st);
+        return matmul_i8(B, L, O, K, qp, qs, wp, ws, bias, cm, code, out, work, work ? need : 0, st);
     });
     return THPVariable_Wrap(y);
 }
