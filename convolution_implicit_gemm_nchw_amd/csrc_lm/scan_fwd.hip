@@ -311,10 +311,11 @@ __global__ __launch_bounds__(kThreads) void scan_chain_kernel(miconv_scan_t s, S
 // (sequence, channel), four states each, so that consecutive lanes read consecutive 16
 // bytes of the states; their products with C are added across the lanes.  VEC: N is a
 // multiple of 4, the states are 16-byte aligned, B and C have their states next to each other.  All reads of a state come before its
-// writes, so state_out may be state.  STREAM: states of 16 MB or more pass by the caches, as
-// those of a model's layers together do not fit them from one token to the next (256
-// sequences of 4096 channels: 35.7 -> 31.7 us).
-template <int DT, int PER, bool VEC, bool STREAM>
+// writes, so state_out may be state.  Such states pass by the caches: those of a model's layers
+// together do not fit them from one token to the next (32 layers in turn, bf16, N 16, a step of 2.1 MB of states
+// 3.98 -> 3.59 us, of 16.8 MB 11.4 -> 9.8, of 67 MB 33.3 -> 31.5; one layer's alone, read again at once, 3.3 us
+// either way, 9.4 -> 9.1 and 28.3 -> 31.2).
+template <int DT, int PER, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, const float *state, int slots,
                                                              const int *slot_of, float *state_out, FDiv fd_D,
                                                              FDiv fd_group, uint32_t first_group) {
@@ -335,11 +336,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
     const float *A = s.A + (long long)d * s.N + n0;
     float h[4], a[4], bv[4], cv[4];
     if (VEC && n0 < s.N) {
-        f32x4 hv;
-        if constexpr (STREAM)
-            hv = __builtin_nontemporal_load((const f32x4 *)(state + so));
-        else
-            hv = *(const f32x4 *)(state + so);
+        const f32x4 hv = __builtin_nontemporal_load((const f32x4 *)(state + so));
         const u32x4 av = *(const u32x4_row *)A;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -372,10 +369,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(miconv_scan_t s, co
     }
     if (VEC && n0 < s.N) {
         const f32x4 hv = {h[0], h[1], h[2], h[3]};
-        if constexpr (STREAM)
-            __builtin_nontemporal_store(hv, (f32x4 *)(state_out + so));
-        else
-            *(f32x4 *)(state_out + so) = hv;
+        __builtin_nontemporal_store(hv, (f32x4 *)(state_out + so));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -482,9 +476,7 @@ static int scan_step(const miconv_scan_t &s, const float *state, int slots, cons
     const FDiv fd_D = make_fdiv((uint32_t)s.D), fd_group = make_fdiv((uint32_t)(s.D / s.G));
     const bool together = s.N == 1 || (s.Bm.stride_n == 1 && s.Cm.stride_n == 1);
     const bool vec = s.N % 4 == 0 && together && ((uintptr_t)state | (uintptr_t)state_out) % 16 == 0;
-    const auto kern = !vec ? scan_step_kernel<DT, PER, false, false>
-                           : ((size_t)rows * s.N * 4 >= (16u << 20) ? scan_step_kernel<DT, PER, true, true>
-                                                                    : scan_step_kernel<DT, PER, true, false>);
+    const auto kern = vec ? scan_step_kernel<DT, PER, true> : scan_step_kernel<DT, PER, false>;
     return launch_groups((rows + kThreads / PER - 1) / (kThreads / PER), kThreads, [&](unsigned n, unsigned first) {
         hipLaunchKernelGGL(kern, dim3(n), dim3(kThreads), 0, st, s, state, slots, slot_of, state_out, fd_D, fd_group, first);
     });
