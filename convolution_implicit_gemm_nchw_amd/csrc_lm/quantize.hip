@@ -4,9 +4,11 @@
 //
 // The rounding is that of the exact quotient.  t = x * (127 / m) in fp32 is off by
 // less than 1.6e-5 (|t| <= 127, two roundings), so it decides unless it lies within
-// 1e-4 of a half; those few go to 64 bits, where x and m have at most 24 significant
-// bits, 127 x / m is a half exactly or at least 2^-25 away from one, and a half is
-// held without error.
+// 1e-4 of a half; those few go to 64 bits.  With x = X 2^a, m = M 2^b (X, M of 24 bits) the quotient
+// differs from a half (2k+1)/2 by (254 X 2^(a-b) - (2k+1) M) / 2M: it is one, which a double holds
+// and the division gives without error, or at least 2^(a-b) / 2^25 away.  A quotient next to a half
+// is about 1/2 or more, so x / m is at least about 1/254 and a - b >= -8: 2^-33, far more than the
+// double's error of 2^-46.
 //
 // Memory bound (8192 x 4096 bf16: 19.7 us, 5.1 TB/s).  Tokens first: a token's values stay in registers between the
 // maximum and the rounding, so x is read once.  Channel-major: a tile of 32 tokens

@@ -96,10 +96,10 @@ extern "C" {
 #define MICONV_ERR_DTYPE 4       /* dtype is neither MICONV_F32 nor MICONV_BF16 */
 #define MICONV_ERR_ALIAS 5       /* the output overlaps an input or the workspace */
 #define MICONV_ERR_ALIGN 6       /* a base pointer is not 16-byte aligned */
-#define MICONV_ERR_WORKSPACE 7   /* reserved: no budget is ever rejected (plans adapt) */
+#define MICONV_ERR_WORKSPACE 7   /* selective_scan_bwd alone: less than its smallest slice (all other plans adapt to any budget) */
 #define MICONV_ERR_HIP 8         /* a HIP call or kernel launch failed */
 #define MICONV_ERR_PASS 9        /* unknown pass id */
-#define MICONV_ERR_TOO_LARGE 10  /* a tensor is 2 GiB or larger */
+#define MICONV_ERR_TOO_LARGE 10  /* a tensor is 2 GiB or larger (state-space operators: a size past its bound) */
 #define MICONV_ERR_INDEX 11      /* plan candidate index out of range */
 
 /* The workspace cap of SystemDS MAX_WORKSPACE_LIMIT_BYTES (1e9 bytes). */
@@ -443,7 +443,8 @@ int convnd_describe(int pass, const miconv_nd_desc_t *d, int dtype, size_t works
  *            non-negative strides (halves of one projection, broadcast rows);
  *            an output's rows must not overlap each other.
  * Alignment  to the element only.  Tensors may be larger than 2 GiB; offsets
- *            are 64-bit.  Every size is at most 2^30, and so is B*D.
+ *            are 64-bit.  Every size is at most 2^30, and so are B*D, B*G*N and B*L of
+ *            the tokens; a launch that this would make too large is made in parts.
  * Types      dtype names the element type of every activation, of the
  *            convolution's filter and of the activations' gradients.  Biases, A,
  *            D, scan states and all gradients of parameters, B and C are fp32.
@@ -453,10 +454,16 @@ int convnd_describe(int pass, const miconv_nd_desc_t *d, int dtype, size_t works
  *            the valid time steps of each right-padded sequence, clamped to
  *            0..L.  Steps past it are neither read into any result nor do they
  *            change a state; outputs and gradients there are 0.
+ *            That holds whatever a state or a parameter is: an infinity or a NaN
+ *            stays in the valid steps of the rows that it reaches.
+ * Overlap    an output may lie between the rows of another operand (slices of one
+ *            buffer along any axis), but share no element with it.
  * Optional   a NULL pointer stands for an absent operand (bias, state, gate, ...).
+ * Workspace  as above, at most min(workspace_bytes, 1e9) bytes; only selective_scan_bwd
+ *            has a least size.
  * Errors     as above; MICONV_ERR_BAD_DIM covers sizes and strides out of range.
  * Determinism results are bitwise reproducible for fixed arguments and
- *            workspace_bytes (no atomics).
+ *            workspace_bytes: every sum has a fixed order.
  */
 #define MICONV_CAUSAL_MAX_TAPS 8
 #define MICONV_SCAN_MAX_STATES 64
@@ -597,7 +604,8 @@ int quantize_tokens(int B, int L, int C, int dtype, const void *x, long long str
  * and at most 131072 (the integer sum then fits 32 bits).  y is [B*L][O]
  * (channel_major 0) or [B][O][L] (1), packed, out_dtype fp32 or bf16.  The sum is
  * exact; it is rounded to fp32 once, scaled by qscale, then wscale, then the bias
- * is added.  Any workspace_bytes is valid; few tokens split the sum over it.
+ * is added.  Any workspace_bytes is valid: deep products of few tiles (more than 64 tokens,
+ * C_pad from 8192 on) split the sum over it.  The 16 x 16 blocks of the output are at most 2^30.
  */
 int matmul_i8(int B, int L, int O, int C_pad, const signed char *q, const float *qscale, const signed char *wq,
               const float *wscale, const float *bias, int channel_major, int out_dtype, void *y, void *workspace,
