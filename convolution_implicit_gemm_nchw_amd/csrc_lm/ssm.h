@@ -15,9 +15,8 @@ constexpr int kScanBwdChannels = 16;
 
 constexpr int scan_chunks(int L) { return (L + kScanChunk - 1) / kScanChunk; }
 
-// A launch counts its work-items along an axis in 32 bits and drops, without an error, what lies past
-// them: more work-groups than that go in several launches.  launch(n, first) launches n of them
-// from the first on.
+// A launch counts its work-items along an axis modulo 2^32, without an error: more work-groups than
+// that go in several launches.  launch(n, first) launches n of them from the first on.
 template <typename F>
 int launch_groups(long long groups, int threads, F launch) {
     const long long most = 0xffffffffll / threads;
