@@ -666,6 +666,15 @@ class _Scan(ctypes.Structure):
                 ("d_initial_state", _VP)]
 
 
+class _GatedDelta(ctypes.Structure):
+    """miconv_gated_delta_t."""
+    _fields_ = [("B", _I), ("Hk", _I), ("Hv", _I), ("P", _I), ("V", _I), ("L", _I), ("l2norm", _I),
+                ("scale", ctypes.c_float), ("q", _Rows), ("k", _Rows), ("v", _Rows), ("g", _Rows), ("beta", _Rows),
+                ("initial_state", _VP), ("lengths", _VP), ("y", _Rows), ("final_state", _VP), ("states", _VP),
+                ("dy", _Rows), ("d_final_state", _VP), ("dq", _Rows), ("dk", _Rows), ("dv", _Rows), ("dg", _VP),
+                ("dbeta", _VP), ("d_initial_state", _VP)]
+
+
 _SZP = ctypes.POINTER(_SZ)
 for _name, _args in {
         "causal_conv1d_fwd": [_VP, _I, _VP],
@@ -684,7 +693,13 @@ for _name, _args in {
         "quantize_tokens": [_I, _I, _I, _I, _VP, _LL, _LL, _LL, _VP, _VP, _VP],
         "matmul_i8": [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _SZ, _VP],
         "matmul_i8_workspace_size": [_I, _I, _I, _I, _SZ, _SZP],
-        "matmul_i8_describe": [_I, _I, _I, _I, _SZ, ctypes.c_char_p, _SZ]}.items():
+        "matmul_i8_describe": [_I, _I, _I, _I, _SZ, ctypes.c_char_p, _SZ],
+        "gated_delta_fwd": [_VP, _I, _VP, _SZ, _VP],
+        "gated_delta_bwd": [_VP, _I, _VP, _SZ, _VP],
+        "gated_delta_step": [_VP, _I, _VP, _I, _VP, _VP, _VP],
+        "gated_delta_states_size": [_I, _I, _I, _I, _I, _SZP],
+        "gated_delta_workspace_size": [_VP, _I, _I, _SZ, _SZP],
+        "gated_delta_describe": [_VP, _I, _I, _SZ, ctypes.c_char_p, _SZ]}.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _I
@@ -800,6 +815,64 @@ def selective_scan_bwd_describe(B, D, L, N, G=1, dtype=F32, workspace_bytes=MAX_
     buf = ctypes.create_string_buffer(256)
     _check(_lib.selective_scan_bwd_describe(ctypes.byref(_Scan(B=B, D=D, L=L, N=N, G=G)), dtype, workspace_bytes, buf, 256),
            "selective_scan_bwd_describe")
+    return buf.value.decode()
+
+
+# ---------------------------------------------------------------- gated delta rule
+
+def gated_delta_states(q, v, g, key_heads=None, stream=None):
+    """A buffer for what gated_delta_fwd saves for gated_delta_bwd: 64 steps' states at a time, fp32."""
+    return _call(_bind.gated_delta_states, stream, q, v, g, key_heads)
+
+
+def gated_delta_fwd(q, k, v, g, beta, key_heads=None, scale=None, l2norm=False, initial_state=None, lengths=None, y=None,
+                    final_state=None, states=None, workspace=None, stream=None):
+    """Gated delta rule: a state S [P, V] per head that forgets by exp(g) and corrects what it holds for a key,
+      z_t = v_t - exp(g_t) S^T k_t,   S <- exp(g_t) S + k_t (beta_t z_t)^T,   y_t = S^T q_t
+    q, k [B, Hk * P, L] and v, y [B, Hv * V, L] (views with contiguous time steps), g and beta fp32 [B, Hv, L],
+    Hk = key_heads (default Hv); value head h reads query and key of head h // (Hv // Hk).  q is multiplied by
+    scale (default P ** -0.5); with l2norm each query and key is divided by sqrt(its sum of squares + 1e-6) first.
+    P <= 256, V <= 512.  initial_state [B, Hv, P, V] fp32; lengths as in causal_conv1d_fwd.  final_state and states
+    (gated_delta_states), when given, are written."""
+    return _call(_bind.gated_delta_fwd, stream, q, k, v, g, beta, key_heads, scale, l2norm, lengths, initial_state, y,
+                 final_state, states, workspace)
+
+
+def gated_delta_bwd(q, k, v, g, beta, dy, states, key_heads=None, scale=None, l2norm=False, lengths=None,
+                    d_final_state=None, d_initial_state=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of gated_delta_fwd for the output gradient dy (and d_final_state); `states` is what the forward
+    pass saved for the same operands.  A dict of dq, dk, dv (q's dtype; they may be given, as views too), dg and dbeta
+    (fp32 [B, Hv, L]).  d_initial_state [B, Hv, P, V], when given, is written."""
+    return dict(zip(("dq", "dk", "dv", "dg", "dbeta"),
+                    _call(_bind.gated_delta_bwd, stream, q, k, v, g, beta, key_heads, scale, l2norm, lengths, dy, states,
+                          d_final_state, d_initial_state, dq, dk, dv, workspace)))
+
+
+def gated_delta_step(q, k, v, g, beta, state, key_heads=None, scale=None, l2norm=False, state_out=None, slots=None,
+                     y=None, stream=None):
+    """One time step of gated_delta_fwd: q, k [B, Hk * P], v [B, Hv * V], g and beta [B, Hv], state [B, Hv, P, V]
+    fp32 (updated in place, or written to state_out) -> y [B, Hv * V].  slots as in causal_conv1d_step."""
+    return _call(_bind.gated_delta_step, stream, q, k, v, g, beta, key_heads, scale, l2norm, None, state, state_out,
+                 slots, y)
+
+
+def _delta_sizes(B, Hk, Hv, P, V, L):
+    return ctypes.byref(_GatedDelta(B=B, Hk=Hk, Hv=Hv, P=P, V=V, L=L))
+
+
+def gated_delta_workspace(B, Hk, Hv, P, V, L, dtype=F32, backward=False, limit=MAX_WORKSPACE_BYTES):
+    """The workspace that a pass uses under `limit`, or the least it needs if that is more."""
+    out = _SZ(0)
+    _check(_lib.gated_delta_workspace_size(_delta_sizes(B, Hk, Hv, P, V, L), dtype, int(backward), limit,
+                                           ctypes.byref(out)), "gated_delta_workspace_size")
+    return out.value
+
+
+def gated_delta_describe(B, Hk, Hv, P, V, L, dtype=F32, backward=False, workspace_bytes=MAX_WORKSPACE_BYTES):
+    """The slices (sequences x chunks of 64 steps) in which a pass takes these sizes."""
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.gated_delta_describe(_delta_sizes(B, Hk, Hv, P, V, L), dtype, int(backward), workspace_bytes, buf, 256),
+           "gated_delta_describe")
     return buf.value.decode()
 
 

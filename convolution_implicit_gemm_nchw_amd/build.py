@@ -18,10 +18,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmiconv.so")
 BIND = os.path.join(HERE, "_miconv_bind.so")
-CSRC_LM = os.path.join(HERE, "csrc_lm")   # the state-space operators
+CSRC_LM = os.path.join(HERE, "csrc_lm")   # the language-model operators
 SOURCES = ["igemm.hip", "patch.hip", "bwdf16.hip", "pointwise.hip", "tinyc.hip", "noalloc.hip", "bwd_bias.hip",
            "convnd.hip", "plan.cpp", "ndplan.cpp", "abi.cpp"]
-SOURCES_LM = ["causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip", "ssm_abi.cpp"]
+SOURCES_LM = ["causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip", "ssm_abi.cpp",
+              "delta_prepare.hip", "delta_fwd.hip", "delta_bwd.hip", "delta_abi.cpp"]
 ARCH = "gfx950"
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 

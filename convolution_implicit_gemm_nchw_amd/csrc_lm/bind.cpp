@@ -12,6 +12,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -461,6 +462,129 @@ PyObject *matmul(Args a) {
     return THPVariable_Wrap(y);
 }
 
+// ------------------------------------------------------------------ gated delta rule
+
+// q, k, v, g, beta, key_heads, scale, l2norm, lengths: the first nine arguments of all.
+miconv_gated_delta_t delta_common(const Lead &q, Args a, bool step) {
+    miconv_gated_delta_t d = {};
+    const int64_t dims = step ? 2 : 3;
+    const at::Tensor &v = tensor("v", a[2]), &g = tensor("g", a[3]);
+    if (v.dim() != dims || g.dim() != dims) refuse(step ? "v must be [B, Hv * V] and g [B, Hv]" : "v must be [B, Hv * V, L] and g [B, Hv, L]");
+    d.B = dim(q.t.size(0));
+    d.L = step ? 1 : dim(q.t.size(2));
+    d.Hv = dim(g.size(1));
+    d.Hk = d.Hv;
+    if (a[5] != Py_None) {
+        const long n = PyLong_AsLong(a[5]);
+        if (n == -1 && PyErr_Occurred()) throw Raised();
+        if (n < 1 || n > 0x7fffffff) refuse("key_heads must be positive");
+        d.Hk = (int)n;
+    }
+    if (d.Hk < 1 || d.Hv < 1 || q.t.size(1) % d.Hk || v.size(1) % d.Hv)
+        refuse("the channels of q must divide by key_heads and those of v by the heads of g");
+    d.P = dim(q.t.size(1) / d.Hk);
+    d.V = dim(v.size(1) / d.Hv);
+    const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)(d.P > 0 ? d.P : 1)) : PyFloat_AsDouble(a[6]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised();
+    d.scale = (float)scale;
+    d.l2norm = truth(a[7]);
+    const int64_t values[3] = {d.B, (int64_t)d.Hv * d.V, d.L}, heads[3] = {d.B, d.Hv, d.L};
+    d.q = rows_of("q", q.t);
+    d.k = rows_of("k", fits("k", a[1], q.t.sizes(), q.dt, q.dev));
+    d.v = rows_of("v", fits("v", a[2], at::IntArrayRef(values, dims), q.dt, q.dev));
+    d.g = rows_of("g", fits("g", a[3], at::IntArrayRef(heads, dims), at::kFloat, q.dev));
+    d.beta = rows_of("beta", fits("beta", a[4], at::IntArrayRef(heads, dims), at::kFloat, q.dev));
+    d.lengths = (const int *)optional("lengths", a[8], {d.B}, at::kInt, q.dev);
+    return d;
+}
+
+int64_t delta_states_count(const miconv_gated_delta_t &d) {
+    size_t bytes = 0;
+    check(gated_delta_states_size(d.B, d.Hv, d.P, d.V, d.L, &bytes), "gated_delta_states_size");
+    return (int64_t)(bytes / 4);
+}
+
+// (q, v, g, key_heads) -> states
+PyObject *delta_states(Args a) {
+    const Lead q("q", a[0], 3);
+    const at::Tensor &v = tensor("v", a[1]), &g = tensor("g", a[2]);
+    if (v.dim() != 3 || g.dim() != 3 || g.size(1) < 1 || v.size(1) % g.size(1)) refuse("v must be [B, Hv * V, L] and g [B, Hv, L]");
+    miconv_gated_delta_t d = {};
+    d.B = dim(q.t.size(0));
+    d.L = dim(q.t.size(2));
+    d.Hv = dim(g.size(1));
+    d.V = dim(v.size(1) / d.Hv);
+    long hk = d.Hv;
+    if (a[3] != Py_None) hk = PyLong_AsLong(a[3]);
+    if (hk == -1 && PyErr_Occurred()) throw Raised();
+    if (hk < 1 || q.t.size(1) % hk) refuse("the channels of q must divide by key_heads");
+    d.P = dim(q.t.size(1) / hk);
+    return THPVariable_Wrap(at::empty({delta_states_count(d)}, q.t.options().dtype(at::kFloat)));
+}
+
+size_t delta_workspace(const miconv_gated_delta_t &d, int code, int backward, PyObject *given) {
+    size_t need = 0;
+    if (given == Py_None)
+        check(gated_delta_workspace_size(&d, code, backward, MICONV_MAX_WORKSPACE_BYTES, &need), "gated_delta_workspace_size");
+    return need;
+}
+
+// (..., initial_state, y, final_state, states, workspace) -> y
+PyObject *delta_fwd(Args a) {
+    const Lead q("q", a[0], 3);
+    miconv_gated_delta_t d = delta_common(q, a, false);
+    d.initial_state = (const float *)optional("initial_state", a[9], {d.B, d.Hv, d.P, d.V}, at::kFloat, q.dev);
+    const Out y("y", a[10], tensor("v", a[2]).sizes(), q.dt, q, true);
+    d.y = rows_of("y", y.t);
+    d.final_state = (float *)optional("final_state", a[11], {d.B, d.Hv, d.P, d.V}, at::kFloat, q.dev);
+    if (a[12] != Py_None) d.states = (float *)packed("states", a[12], {delta_states_count(d)}, at::kFloat, q.dev);
+    const Scratch ws(a[13], delta_workspace(d, q.code, 0, a[13]), q);
+    run("gated_delta_fwd", q.dev, [&](void *st) { return gated_delta_fwd(&d, q.code, ws.p, ws.n, st); });
+    return y.wrap();
+}
+
+// (..., dy, states, d_final_state, d_initial_state, dq, dk, dv, workspace) -> (dq, dk, dv, dg, dbeta)
+PyObject *delta_bwd(Args a) {
+    const Lead q("q", a[0], 3);
+    miconv_gated_delta_t d = delta_common(q, a, false);
+    const at::Tensor &v = tensor("v", a[2]);
+    if (a[9] == Py_None) refuse("dy must be a tensor");
+    if (a[10] == Py_None) refuse("states of the forward pass are needed");
+    d.dy = rows_of("dy", fits("dy", a[9], v.sizes(), q.dt, q.dev));
+    d.states = (float *)packed("states", a[10], {delta_states_count(d)}, at::kFloat, q.dev);
+    d.d_final_state = (const float *)optional("d_final_state", a[11], {d.B, d.Hv, d.P, d.V}, at::kFloat, q.dev);
+    d.d_initial_state = (float *)optional("d_initial_state", a[12], {d.B, d.Hv, d.P, d.V}, at::kFloat, q.dev);
+    const Out dq("dq", a[13], q.t.sizes(), q.dt, q, true), dk("dk", a[14], q.t.sizes(), q.dt, q, true),
+        dv("dv", a[15], v.sizes(), q.dt, q, true);
+    const Out dg("dg", Py_None, {d.B, d.Hv, d.L}, at::kFloat, q), db("dbeta", Py_None, {d.B, d.Hv, d.L}, at::kFloat, q);
+    d.dq = rows_of("dq", dq.t);
+    d.dk = rows_of("dk", dk.t);
+    d.dv = rows_of("dv", dv.t);
+    d.dg = (float *)dg.data();
+    d.dbeta = (float *)db.data();
+    const Scratch ws(a[16], delta_workspace(d, q.code, 1, a[16]), q);
+    run("gated_delta_bwd", q.dev, [&](void *st) { return gated_delta_bwd(&d, q.code, ws.p, ws.n, st); });
+    return tuple({&dq, &dk, &dv, &dg, &db});
+}
+
+// (..., state, state_out, slots, y) -> y
+PyObject *delta_step(Args a) {
+    const Lead q("q", a[0], 2);
+    miconv_gated_delta_t d = delta_common(q, a, true);
+    const at::Tensor &t = tensor("state", a[9]);
+    if (t.dim() != 4) refuse("state must have 4 dimensions");
+    const int slots = dim(t.size(0));
+    if (a[11] == Py_None && slots != d.B) refuse("without slots, state must hold one state for each sequence");
+    const int *slot_of = (const int *)optional("slots", a[11], {d.B}, at::kInt, q.dev);
+    const float *in = (const float *)packed("state", a[9], {slots, d.Hv, d.P, d.V}, at::kFloat, q.dev);
+    float *out = a[10] == Py_None ? (float *)in
+                                  : (float *)packed("state_out", a[10], {slots, d.Hv, d.P, d.V}, at::kFloat, q.dev);
+    const Out y("y", a[12], tensor("v", a[2]).sizes(), q.dt, q, true);
+    d.y = rows_of("y", y.t);
+    run("gated_delta_step", q.dev, [&](void *st) { return gated_delta_step(&d, q.code, in, slots, slot_of, out, st); });
+    return y.wrap();
+}
+
 // ------------------------------------------------------------------ module
 
 // fn with N arguments; no C++ exception leaves it.
@@ -512,6 +636,10 @@ PyMethodDef methods[] = {ENTRY("causal_conv1d_fwd", conv_fwd, 8),
                          ENTRY("selective_scan_step", scan_step, 14),
                          ENTRY("quantize_tokens", quantize, 4),
                          ENTRY("matmul_i8", matmul, 9),
+                         ENTRY("gated_delta_states", delta_states, 4),
+                         ENTRY("gated_delta_fwd", delta_fwd, 14),
+                         ENTRY("gated_delta_bwd", delta_bwd, 17),
+                         ENTRY("gated_delta_step", delta_step, 13),
                          {"errors", (PyCFunction)(void *)errors, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_miconv_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,687 @@
+// delta_bwd.hip -- gradients of the gated delta rule.
+//
+// With dS the gradient of the state after a chunk and T = inv(I + diag(beta) (D * k k^T)_{i>j}):
+//   du = (D * q k^T)^T dy + f (k dS),   F = T^T du,   dv = beta F,
+//   dS <- e_last dS + (e q)^T dy - (e k)^T (beta F)
+// goes from the last chunk to the first (delta_bwd_kernel).  The rest of a chunk needs nothing but what stands
+// on its two ends, and runs for all chunks side by side (delta_grads_kernel): with Z and the state S before the
+// chunk, which the forward pass saved,
+//   dP_ij = beta_j D_ij dy_i.Z_j (i >= j),   dA_ij = -beta_i beta_j D_ij F_i.Z_j (i > j),   dbeta_i = F_i.Z_i
+//   dq = e (S dy) + dP k,   read = dA k - e beta (S F),   write = f beta (dS Z) + dP^T q + dA^T k,   dk = read + write
+// A key reads with the decays up to its step and writes against them, so the gradient of the sum G_i is
+// q_i.dq_i + k_i.read_i - k_i.write_i, and that of g_t the sum of those from t on, with what the chunk's end adds:
+// e_last <S, dS> + sum_j k_j.(f beta dS Z)_j.
+#include "delta_device.h"
+
+namespace miconv {
+
+namespace {
+
+// Laid out and split as the forward scan; the state here is dS.
+template <int DT, int DK, int NT>
+__global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
+    constexpr int TI = in_planes(DT), kKS = DK / 32, kMT = DK / 64, kN = NT * 16;
+    constexpr int kPitchS = DK + 8, kPitchT = kDeltaChunk + 8, kPlaneS = kN * kPitchS, kPlaneT = kN * kPitchT;
+    typedef typename Elem<DT>::T T;
+    __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * kPlaneS], Up[3 * kPlaneT], Wp[3 * kPlaneT];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
+    const int row4 = grp * 4, mine = wave * 16 + row4;
+    const int total = a.s.nb * a.d.Hv * a.slices;
+    const int id = xcd_remap(blockIdx.x, total);
+    const int slice = id % a.slices, bh = id / a.slices, h = bh % a.d.Hv, b = bh / a.d.Hv, B = a.s.b0 + b;
+    const int hk = h / a.rep, v0 = slice * kN;
+    const int valid = valid_steps(a.d.lengths, B, a.d.L);
+    const int steps_first = a.s.c0 * kDeltaChunk;
+    int chunks = (valid - steps_first + kDeltaChunk - 1) / kDeltaChunk;
+    chunks = chunks < 0 ? 0 : (chunks > a.s.nc ? a.s.nc : chunks);
+
+    f32x4 S[kMT][NT];
+    {
+        const int P = a.last ? a.d.P : DK, V = a.last ? a.d.V : a.Vp;
+        const float *in = a.last ? a.d.d_final_state : state_in;
+        const long long at = a.last ? (long long)B * a.d.Hv + h : bh;
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
+                    S[i][n][r] = in && p < P && v < V ? in[(at * P + p) * V + v] : 0.0f;
+                }
+    }
+    const auto put_state = [&] {
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float v[4] = {S[i][n][0], S[i][n][1], S[i][n][2], S[i][n][3]};
+                put_planes<3>(Sp + (n * 16 + col) * kPitchS + (wave * kMT + i) * 16 + row4, kPlaneS, v);
+            }
+    };
+    put_state();
+
+    const size_t of_k = ((size_t)b * a.s.nc * a.d.Hk + hk) * TI * 64 * DK * 2, step_k = (size_t)a.d.Hk * TI * 64 * DK * 2;
+    const size_t of_v = (size_t)b * a.s.nc * a.d.Hv + h;
+    constexpr int kPlaneK = 64 * DK * 2;
+    // three planes of 256 key channels are more than the registers hold ahead of their use
+    constexpr bool kLate = TI == 3 && DK == 256;
+    u32x4 fk[kKS][TI], ft[kMT][2][TI], fq[kMT][2][TI], fi[2][3], fa[2][3];
+    u32x4 raw[NT][2][TI];                      // dy as column operand: 8 steps from ks * 32 + grp * 8 on
+    float scaled[NT][2][8];                    // and times e q's factor
+    f32x4 vek, vfk, vbeta;
+    float last = 0.0f;
+    const T *grow[NT];
+    T *out[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int v = v0 + n * 16 + col, at = h * a.d.V + (v < a.d.V ? v : 0);
+        grow[n] = row_of<DT>(a.d.dy, B, at);
+        out[n] = row_of<DT>(a.d.dv, B, at);
+    }
+    const auto load_k = [&](int c) {
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+            fragment<TI>(a.ws + a.w.k + of_k + c * step_k, wave * kKS + ks, kPlaneK, fk[ks]);
+    };
+    const auto load_turned = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                fragment<TI>(a.ws + a.w.q + of_k + c * step_k, (wave * kMT + i) * 2 + ks, kPlaneK, fq[i][ks]);
+                fragment<TI>(a.ws + a.w.kt + of_k + c * step_k, (wave * kMT + i) * 2 + ks, kPlaneK, ft[i][ks]);
+            }
+    };
+    // both are upper triangular: the first 32 columns of rows from 32 on are zero and not stored
+    const auto load_solve = [&](int c) {
+        const char *i = a.ws + a.w.inv + (of_v + (size_t)c * a.d.Hv) * 3 * 8192;
+        const char *at = a.ws + a.w.attn + (of_v + (size_t)c * a.d.Hv) * 3 * 8192;
+        if (wave < 2) {
+            fragment<3>(i, wave * 2, 8192, fi[0]);
+            fragment<3>(at, wave * 2, 8192, fa[0]);
+        }
+        fragment<3>(i, wave * 2 + 1, 8192, fi[1]);
+        fragment<3>(at, wave * 2 + 1, 8192, fa[1]);
+    };
+    const auto load_steps = [&](int c) {
+        const DeltaSteps *s = (const DeltaSteps *)(a.ws + a.w.steps + (of_v + (size_t)c * a.d.Hv) * sizeof(DeltaSteps));
+        vek = *(const f32x4 *)(s->ek + mine);
+        vfk = *(const f32x4 *)(s->fk + mine);
+        vbeta = *(const f32x4 *)(s->beta + mine);
+        last = s->last;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const f32x4 lo = *(const f32x4 *)(s->eq + ks * 32 + grp * 8), hi = *(const f32x4 *)(s->eq + ks * 32 + grp * 8 + 4);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float g[8];
+                load8<DT>(grow[n], steps_first + c * kDeltaChunk + ks * 32 + grp * 8,
+                          v0 + n * 16 + col < a.d.V ? valid : 0, g);
+                split8<TI>(g, raw[n][ks]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    scaled[n][ks][e] = g[e] * lo[e];
+                    scaled[n][ks][4 + e] = g[4 + e] * hi[e];
+                }
+            }
+        }
+    };
+    if (chunks) {
+        load_k(chunks - 1);
+        load_solve(chunks - 1);
+        load_steps(chunks - 1);
+        if constexpr (!kLate) load_turned(chunks - 1);
+    }
+    // chunks past the sequence's end
+    for (int c = chunks; c < a.s.nc; ++c) {
+        const float zeros[4] = {};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (v0 + n * 16 + col < a.d.V)
+                store4_until<DT>(out[n], steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+    }
+    for (int c = chunks - 1; c >= 0; --c) {
+        const size_t at = of_v + (size_t)c * a.d.Hv;
+        float *after = (float *)(a.ws + a.w.after) + at * DK * a.Vp, *Fout = (float *)(a.ws + a.w.F) + at * a.Vp * kDeltaChunk;
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    after[(size_t)((wave * kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 kd = {0, 0, 0, 0}, back = {0, 0, 0, 0};
+            if (wave < 2) multiply<3, TI, 2>(fa[0], raw[n][0], back);
+            multiply<3, TI, 2>(fa[1], raw[n][1], back);
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks) {
+                u32x4 s[3];
+                get_planes<3>(Sp + (n * 16 + col) * kPitchS + ks * 32 + grp * 8, kPlaneS, s);
+                multiply<TI, 3, 2>(fk[ks], s, kd);
+            }
+            float du[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], kd[r], back[r]);
+            put_planes<3>(Up + (n * 16 + col) * kPitchT + mine, kPlaneT, du);
+        }
+        if (c) load_k(c - 1);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 F = {0, 0, 0, 0};
+            u32x4 u[3];
+            const uint16_t *from = Up + (n * 16 + col) * kPitchT + grp * 8;
+            if (wave < 2) {
+                get_planes<3>(from, kPlaneT, u);
+                multiply<3, 3, 2>(fi[0], u, F);
+            }
+            get_planes<3>(from + 32, kPlaneT, u);
+            multiply<3, 3, 2>(fi[1], u, F);
+            *(f32x4 *)(Fout + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = F;
+            float w[4], dv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                dv[r] = vbeta[r] * F[r];
+                w[r] = -(vek[r] * dv[r]);
+            }
+            put_planes<3>(Wp + (n * 16 + col) * kPitchT + mine, kPlaneT, w);
+            if (v0 + n * 16 + col < a.d.V) {
+                const int t = steps_first + c * kDeltaChunk + mine;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dv[r] = t + r < valid ? dv[r] : 0.0f;
+                store4_until<DT>(out[n], t, a.d.L, dv);
+            }
+        }
+        if (c) load_solve(c - 1);
+        if constexpr (kLate) load_turned(c);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) S[i][n] *= last;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4 g[3];
+                split8<3>(scaled[n][ks], g);
+#pragma unroll
+                for (int i = 0; i < kMT; ++i) multiply<TI, 3, 2>(fq[i][ks], g, S[i][n]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4 w[3];
+                get_planes<3>(Wp + (n * 16 + col) * kPitchT + ks * 32 + grp * 8, kPlaneT, w);
+#pragma unroll
+                for (int i = 0; i < kMT; ++i) multiply<TI, 3, 2>(ft[i][ks], w, S[i][n]);
+            }
+        if (c) {
+            if constexpr (!kLate) load_turned(c - 1);
+            load_steps(c - 1);
+        }
+        put_state();
+    }
+    {
+        float *to = a.first ? a.d.d_initial_state : state_out;
+        const int P = a.first ? a.d.P : DK, V = a.first ? a.d.V : a.Vp;
+        const long long at = a.first ? (long long)B * a.d.Hv + h : bh;
+        if (to) {
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
+                        if (p < P && v < V) to[(at * P + p) * V + v] = S[i][n][r];
+                    }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the rest of each chunk
+//
+// A work-group takes one chunk of one key head, its value heads in turn, whose gradients of q and k add up in
+// registers.  A wave owns NC tiles of 16 key channels for all 64 steps; the state and dS are its column operands,
+// read from memory once and split in registers.  Z, F and dy stand in LDS as planes [step][value channel],
+// 64 channels at a time; after them, in the same place, dP and dA in both orders.
+template <int DT, int DK>
+struct Grads {
+    static constexpr int kWaves = DK == 64 ? 4 : 8, kThreads = kWaves * 64, kNC = DK / 16 / kWaves;
+    static constexpr int kTiles = 16 / kWaves;             // column tiles of the 64 x 64 products per wave
+    static constexpr int kPitch = 72, kPlane = 64 * kPitch;   // bf16 elements
+    static constexpr int TI = in_planes(DT);
+    static constexpr bool kKeep = DK < 256;
+    static constexpr int kValues = 6 + TI, kPlanes = kValues > 12 ? kValues : 12;
+};
+
+// Sums over the 16 lanes of a row.
+DEVI float sum16(float v) {
+    v += cross<0xB1>(v);                       // quad_perm 1,0,3,2
+    v += cross<0x4E>(v);                       // quad_perm 2,3,0,1
+    v += cross<0x141>(v);                      // row_half_mirror
+    v += cross<0x140>(v);                      // row_mirror
+    return v;
+}
+
+template <int DT, int DK>
+__global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(DeltaArgs a) {
+    typedef Grads<DT, DK> X;
+    constexpr int TI = X::TI, NC = X::kNC, W = X::kWaves, TILES = X::kTiles;
+    typedef typename Elem<DT>::T T;
+    __shared__ __attribute__((aligned(16))) uint16_t shared[X::kPlanes * X::kPlane];
+    __shared__ float rows[W][4][64];           // a wave's part of q.dq, k.(read - write), and q.dq, k.dk in full
+    __shared__ float part[W];                  // of what the chunk's end adds
+    __shared__ float norm_q[64], norm_k[64];   // q.dq and k.dk of all heads, for the normalisation
+    __shared__ float diag[64], diag_p[64], e[64], f[64];
+    __shared__ __attribute__((aligned(16))) DeltaSteps steps;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6);
+    const int id = a.more + blockIdx.x;
+    const int hk = id % a.d.Hk, bc = id / a.d.Hk, c = bc % a.s.nc, b = bc / a.s.nc, B = a.s.b0 + b;
+    const int t0 = (a.s.c0 + c) * kDeltaChunk, valid = valid_steps(a.d.lengths, B, a.d.L), end = valid - t0;
+    const int stop = a.d.L - t0 < kDeltaChunk ? a.d.L - t0 : kDeltaChunk;     // steps of this chunk in the tensors
+    if (end <= 0) {                            // a chunk past the sequence's end
+        for (int i = tid; i < a.d.P * kDeltaChunk; i += X::kThreads) {
+            const int d = i / kDeltaChunk, t = i % kDeltaChunk;
+            if (t >= stop) continue;
+            row_of<DT>(a.d.dq, B, hk * a.d.P + d)[t0 + t] = Elem<DT>::put(0.0f);
+            row_of<DT>(a.d.dk, B, hk * a.d.P + d)[t0 + t] = Elem<DT>::put(0.0f);
+        }
+        for (int i = tid; i < a.rep * kDeltaChunk; i += X::kThreads) {
+            const int h = hk * a.rep + i / kDeltaChunk, t = i % kDeltaChunk;
+            if (t >= stop) continue;
+            const size_t at = ((size_t)B * a.d.Hv + h) * a.d.L + t0 + t;
+            a.d.dg[at] = a.d.dbeta[at] = 0.0f;
+        }
+        return;
+    }
+    // The sums over heads stay in registers where these hold them, else in the workspace, each lane's own.
+    f32x4 dq[X::kKeep ? 4 : 1][NC], dk[X::kKeep ? 4 : 1][NC];
+    if constexpr (X::kKeep) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) dq[m][n] = dk[m][n] = f32x4{0, 0, 0, 0};
+    }
+    if (tid < 64) norm_q[tid] = norm_k[tid] = 0.0f;
+
+    for (int hr = 0; hr < a.rep; ++hr) {
+        const int h = hk * a.rep + hr;
+        // a lane's place, of which the compiler does not know that it is the same for all heads: what is made from
+        // it is then not held in registers from one to the next
+        const int lane = again(tid & 63), col = lane & 15, grp = lane >> 4, row4 = grp * 4;
+        const int d0 = wave * NC * 16 + col;   // key channels d0 + 16 n
+        const size_t of_v = (size_t)bc * a.d.Hv + h;
+        const float *S0 = (const float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0 + c) * delta_saved(a.d.P, a.d.V);
+        const float *Zs = S0 + (size_t)DK * a.Vp;
+        const float *S1 = (const float *)(a.ws + a.w.after) + of_v * DK * a.Vp;
+        const float *Fs = (const float *)(a.ws + a.w.F) + of_v * a.Vp * kDeltaChunk;
+        __syncthreads();                       // the head before has read steps, shared and rows
+        if (tid < (int)(sizeof(DeltaSteps) / 16))
+            ((u32x4 *)&steps)[tid] = ((const u32x4 *)(a.ws + a.w.steps + of_v * sizeof(DeltaSteps)))[tid];
+        f32x4 q_[4][NC], read[4][NC], write[4][NC], FZ[TILES], OZ[TILES];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) q_[m][n] = read[m][n] = write[m][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) FZ[j] = OZ[j] = f32x4{0, 0, 0, 0};
+        float ends = 0.0f;
+        const int mi = wave * 4 / W, j0 = wave % (W / 4);         // the wave's tiles: row mi, columns j0 + j W / 4
+
+        for (int v0 = 0; v0 < a.Vp; v0 += 64) {
+            if (v0) __syncthreads();           // the channels before are used up
+            // blocks of 4 steps x 8 channels: Z, F, dy
+            for (int i = again(tid); i < 3 * 128; i += X::kThreads) {
+                const int which = i >> 7, t = (i & 15) * 4, v = v0 + (i >> 4 & 7) * 8;
+                float x[8][4];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (which == 2) {
+                        if (v + k < a.d.V) {
+                            load4_until<DT>(row_of<DT>(a.d.dy, B, h * a.d.V + v + k) + t0, t, end, x[k]);
+                            continue;
+                        }
+                    } else if (v + k < a.Vp) {
+                        const f32x4 s = *(const f32x4 *)((which ? Fs : Zs) + (size_t)(v + k) * kDeltaChunk + t);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[k][r] = s[r];
+                        continue;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[k][r] = 0.0f;
+                }
+                uint16_t *to = shared + which * 3 * X::kPlane + t * X::kPitch + (v - v0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float eight[8] = {x[0][r], x[1][r], x[2][r], x[3][r], x[4][r], x[5][r], x[6][r], x[7][r]};
+                    u32x4 s[3];
+                    split8<3>(eight, s);
+                    *(u32x4 *)(to + r * X::kPitch) = s[0];
+                    if (which < 2 || TI == 3) {
+                        *(u32x4 *)(to + r * X::kPitch + X::kPlane) = s[1];
+                        *(u32x4 *)(to + r * X::kPitch + 2 * X::kPlane) = s[2];
+                    }
+                }
+            }
+            __syncthreads();
+            const uint16_t *Zp = shared, *Fp = shared + 3 * X::kPlane, *Op = shared + 6 * X::kPlane;
+#pragma unroll 1
+            for (int ks = 0; ks < 2; ++ks) {
+                if (v0 + ks * 32 >= a.Vp) break;
+                const int at = again(ks * 32 + grp * 8);
+                // F Z^T and dy Z^T up to the diagonal
+                {
+                    u32x4 fr[3], og[TI];
+                    get_planes<3>(Fp + (mi * 16 + col) * X::kPitch + at, X::kPlane, fr);
+                    get_planes<TI>(Op + (mi * 16 + col) * X::kPitch + at, X::kPlane, og);
+#pragma unroll
+                    for (int j = 0; j < TILES; ++j) {
+                        const int jt = j0 + j * (W / 4);
+                        if (jt > mi) break;
+                        u32x4 z[3];
+                        get_planes<3>(Zp + (jt * 16 + col) * X::kPitch + at, X::kPlane, z);
+                        multiply<3, 3, 2>(fr, z, FZ[j]);
+                        multiply<TI, 3, 2>(og, z, OZ[j]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    u32x4 s0[3], s1[3];
+                    {
+                        const unsigned from = again(d0 + n * 16) * a.Vp + v0 + at;
+                        float x[8], y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 4) {
+                            const f32x4 lo = *(const f32x4 *)(S0 + from + k), hi = *(const f32x4 *)(S1 + from + k);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                x[k + r] = lo[r];
+                                y[k + r] = hi[r];
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) ends = __builtin_fmaf(x[k], y[k], ends);
+                        split8<3>(x, s0);
+                        split8<3>(y, s1);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        u32x4 og[TI], r3[3];
+                        get_planes<TI>(Op + (m * 16 + col) * X::kPitch + at, X::kPlane, og);
+                        multiply<TI, 3, 2>(og, s0, q_[m][n]);
+                        get_planes<3>(Fp + (m * 16 + col) * X::kPitch + at, X::kPlane, r3);
+                        multiply<3, 3, 2>(r3, s0, read[m][n]);
+                        get_planes<3>(Zp + (m * 16 + col) * X::kPitch + at, X::kPlane, r3);
+                        multiply<3, 3, 2>(r3, s1, write[m][n]);
+                        __builtin_amdgcn_sched_barrier(0);   // loads further ahead would not fit the registers
+                    }
+                }
+            }
+        }
+        if (tid < 64) {
+            e[tid] = exp_any((float)steps.G[tid]);
+            f[tid] = exp_any((float)(steps.G[63] - steps.G[tid]));
+        }
+        __syncthreads();                       // and the products have left the planes
+        ends *= steps.last;
+        // the rows' factors; the chunk's end reaches its decays through the last of them
+        // four steps of a channel of key or query
+        const auto four = [&](const miconv_rows_t &rows, int d, int t, float (&v)[4]) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = 0.0f;
+            const int at = again(d);
+            if (at < a.d.P) load4_until<DT>(row_of<DT>(rows, B, hk * a.d.P + at) + t0, t, end, v);
+        };
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int t = again(m * 16 + row4);
+                float k[4];
+                four(a.d.k, d0 + n * 16, t, k);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float beta = steps.beta[t + r];
+                    q_[m][n][r] *= e[t + r];
+                    read[m][n][r] *= -(e[t + r] * beta);
+                    write[m][n][r] *= f[t + r] * beta;
+                    ends = __builtin_fmaf(k[r] * steps.rk[t + r], write[m][n][r], ends);
+                }
+                // here, not where the sum is used, with all its terms in registers till then
+                asm volatile("" : "+v"(ends), "+v"(q_[m][n]), "+v"(read[m][n]), "+v"(write[m][n]));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        // dP and dA as row operands: [i][j] times the key's factor of j, for q and read, and [j][i] times the query's
+        // or key's factor of i, for write
+        uint16_t *Mq = shared, *Mr = shared + 3 * X::kPlane, *Mp = shared + 6 * X::kPlane, *Ma = shared + 9 * X::kPlane;
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+            const int jt = j0 + j * (W / 4);
+            if (jt > (mi | 1)) break;          // a block of 32 columns past the diagonal is never read
+            const int cj = again(jt * 16 + col);
+            const double Gj = steps.G[cj];
+            const float bj = steps.beta[cj], rkj = steps.rk[cj];
+            float pq[4], ar[4], pw[4], aw[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = mi * 16 + row4 + r;
+                const float D = i >= cj ? exp_any((float)(steps.G[i] - Gj)) * bj : 0.0f;
+                const float dP = i > cj ? D * OZ[j][r] : 0.0f, dA = i > cj ? -(D * steps.beta[i]) * FZ[j][r] : 0.0f;
+                pq[r] = dP * rkj;
+                ar[r] = dA * rkj;
+                pw[r] = dP * (steps.rq[i] * a.d.scale);
+                aw[r] = dA * steps.rk[i];
+                if (i == cj) {
+                    diag[i] = FZ[j][r];
+                    diag_p[i] = D * OZ[j][r];
+                }
+            }
+            u32x2 s[3];
+            const auto across = [&](uint16_t *to) {
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        to[p * X::kPlane + (mi * 16 + row4 + r) * X::kPitch + cj] =
+                            (uint16_t)(r & 1 ? s[p][r >> 1] >> 16 : s[p][r >> 1]);
+            };
+            split4<3>(pq, s);
+            across(Mq);
+            split4<3>(ar, s);
+            across(Mr);
+            put_planes<3>(Mp + cj * X::kPitch + mi * 16 + row4, X::kPlane, pw);
+            put_planes<3>(Ma + cj * X::kPitch + mi * 16 + row4, X::kPlane, aw);
+        }
+        __syncthreads();
+        const size_t of_k = ((size_t)bc * a.d.Hk + hk) * TI * 64 * DK * 2;
+        constexpr int kPlaneK = 64 * DK * 2;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4 fk[TI], fq[TI];
+                fragment<TI>(a.ws + a.w.kt + of_k, (wave * NC + n) * 2 + ks, kPlaneK, fk);
+                fragment<TI>(a.ws + a.w.q + of_k, (wave * NC + n) * 2 + ks, kPlaneK, fq);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int at = again((m * 16 + col) * X::kPitch + ks * 32 + grp * 8);
+                    u32x4 s[3];
+                    if (m >= 2 * ks) {         // columns up to the diagonal
+                        get_planes<3>(Mq + at, X::kPlane, s);
+                        multiply<3, TI, 2>(s, fk, q_[m][n]);
+                        get_planes<3>(Mr + at, X::kPlane, s);
+                        multiply<3, TI, 2>(s, fk, read[m][n]);
+                    }
+                    if (m < 2 * ks + 2) {      // columns from the diagonal on
+                        get_planes<3>(Mp + at, X::kPlane, s);
+                        multiply<3, TI, 2>(s, fq, write[m][n]);
+                        get_planes<3>(Ma + at, X::kPlane, s);
+                        multiply<3, TI, 2>(s, fk, write[m][n]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        // The rows' products with normalised query and key.  A step's own dP_ii k_i and dP_ii q_i add the same to
+        // q_i.dq_i and k_i.write_i, so they enter after the decays' part: its terms then cancel no further than its
+        // definition's do, and the first step from a zero state gets a zero.
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            float x[4] = {}, y[4] = {}, z[4] = {}, w[4] = {};
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                float k[4], q[4];
+                four(a.d.k, d0 + n * 16, m * 16 + row4, k);
+                four(a.d.q, d0 + n * 16, m * 16 + row4, q);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = m * 16 + row4 + r;
+                    x[r] = __builtin_fmaf(q[r], q_[m][n][r], x[r]);
+                    y[r] = __builtin_fmaf(k[r], read[m][n][r] - write[m][n][r], y[r]);
+                    q_[m][n][r] = __builtin_fmaf(diag_p[t] * steps.rk[t], k[r], q_[m][n][r]);
+                    write[m][n][r] = __builtin_fmaf(diag_p[t] * (steps.rq[t] * a.d.scale), q[r], write[m][n][r]);
+                    z[r] = __builtin_fmaf(q[r], q_[m][n][r], z[r]);
+                    w[r] = __builtin_fmaf(k[r], read[m][n][r] + write[m][n][r], w[r]);
+                    if constexpr (X::kKeep) {
+                        dq[m][n][r] += q_[m][n][r];
+                        dk[m][n][r] += read[m][n][r] + write[m][n][r];
+                    }
+                }
+                if constexpr (!X::kKeep) {
+                    f32x4 *const sums = (f32x4 *)(a.ws + a.w.sums) + (((size_t)bc * a.d.Hk + hk) * 2 * 4 * NC + (m * NC + n) * 2) * X::kThreads + again(tid);
+                    read[m][n] += write[m][n];
+                    if (hr) {
+                        q_[m][n] += sums[0];
+                        read[m][n] += sums[X::kThreads];
+                    }
+                    if (hr + 1 < a.rep) {
+                        sums[0] = q_[m][n];
+                        sums[X::kThreads] = read[m][n];
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = m * 16 + row4 + r;
+                x[r] = sum16(x[r]);
+                y[r] = sum16(y[r]);
+                z[r] = sum16(z[r]);
+                w[r] = sum16(w[r]);
+                if (col == 0) {
+                    rows[wave][0][t] = x[r] * steps.rq[t];
+                    rows[wave][1][t] = y[r] * steps.rk[t];
+                    rows[wave][2][t] = z[r] * steps.rq[t];
+                    rows[wave][3][t] = w[r] * steps.rk[t];
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int o = 32; o; o /= 2) ends += __shfl_xor(ends, o);
+        if (lane == 0) part[wave] = ends;
+        __syncthreads();
+        if (wave == 0) {
+            float x = 0.0f, y = 0.0f, z = 0.0f, u = 0.0f, w = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                x += rows[i][0][lane];
+                y += rows[i][1][lane];
+                z += rows[i][2][lane];
+                u += rows[i][3][lane];
+                w += part[i];
+            }
+            norm_q[lane] += z;
+            norm_k[lane] += u;
+            // sums of the decays' gradients from each step on, in 64 bits like the decays' own
+            double s = (double)x * a.d.scale + y;
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) {
+                const double other = __shfl_down(s, o);
+                if (lane + o < 64) s += other;
+            }
+            if (lane < stop) {
+                const size_t at = ((size_t)B * a.d.Hv + h) * a.d.L + t0 + lane;
+                a.d.dg[at] = lane < end ? (float)(s + w) : 0.0f;
+                a.d.dbeta[at] = lane < end ? diag[lane] : 0.0f;
+            }
+        }
+        if (hr + 1 < a.rep) continue;
+        __syncthreads();
+        // through the normalisation n = r x: dx = r (dn - n (n . dn))
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int d = again(d0 + n * 16);
+            if (d >= a.d.P) continue;
+            T *const qrow = row_of<DT>(a.d.dq, B, hk * a.d.P + d) + t0, *const krow = row_of<DT>(a.d.dk, B, hk * a.d.P + d) + t0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int t = m * 16 + row4;
+                float k[4], q[4], x[4], y[4];
+                four(a.d.k, d, t, k);
+                four(a.d.q, d, t, q);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float rq = steps.rq[t + r], rk = steps.rk[t + r];
+                    float g, u;
+                    if constexpr (X::kKeep) {
+                        g = dq[m][n][r], u = dk[m][n][r];
+                    } else {
+                        g = q_[m][n][r], u = read[m][n][r];
+                    }
+                    if (a.d.l2norm) {
+                        g -= q[r] * rq * norm_q[t + r];
+                        u -= k[r] * rk * norm_k[t + r];
+                    }
+                    x[r] = t + r < end ? g * (rq * a.d.scale) : 0.0f;
+                    y[r] = t + r < end ? u * rk : 0.0f;
+                }
+                store4_until<DT>(qrow, t, stop, x);
+                store4_until<DT>(krow, t, stop, y);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+}
+
+template <int DT, int DK>
+int backward(DeltaArgs a, hipStream_t st) {
+    float *carry = (float *)(a.ws + a.w.state);
+    a.slices = a.Vp / 16;
+    hipLaunchKernelGGL((delta_bwd_kernel<DT, DK, 1>), dim3((unsigned)(a.s.nb * a.d.Hv * a.slices)), dim3(256), 0, st, a,
+                       carry, carry);
+    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+}
+
+template <int DT, int DK>
+int gradients(DeltaArgs a, hipStream_t st) {
+    return launch_groups((long long)a.s.nb * a.s.nc * a.d.Hk, Grads<DT, DK>::kThreads, [&](unsigned n, unsigned first) {
+        a.more = (int)first;
+        hipLaunchKernelGGL((delta_grads_kernel<DT, DK>), dim3(n), dim3(Grads<DT, DK>::kThreads), 0, st, a);
+    });
+}
+
+}  // namespace
+
+int launch_delta_bwd(const DeltaArgs &a, int dtype, hipStream_t st) {
+    switch (delta_key_pad(a.d.P)) {
+        case 64: return dtype == MICONV_BF16 ? backward<1, 64>(a, st) : backward<0, 64>(a, st);
+        case 128: return dtype == MICONV_BF16 ? backward<1, 128>(a, st) : backward<0, 128>(a, st);
+        default: return dtype == MICONV_BF16 ? backward<1, 256>(a, st) : backward<0, 256>(a, st);
+    }
+}
+
+int launch_delta_grads(const DeltaArgs &a, int dtype, hipStream_t st) {
+    switch (delta_key_pad(a.d.P)) {
+        case 64: return dtype == MICONV_BF16 ? gradients<1, 64>(a, st) : gradients<0, 64>(a, st);
+        case 128: return dtype == MICONV_BF16 ? gradients<1, 128>(a, st) : gradients<0, 128>(a, st);
+        default: return dtype == MICONV_BF16 ? gradients<1, 256>(a, st) : gradients<0, 256>(a, st);
+    }
+}
+
+}  // namespace miconv

@@ -1,0 +1,457 @@
+// delta_fwd.hip -- the gated delta rule from chunk to chunk, forward, and its single-token step.
+#include "delta_device.h"
+
+namespace miconv {
+
+namespace {
+
+// One work-group of four waves carries a value slice of NT * 16 channels of one head through time; the
+// state [DK][NT * 16] stays in accumulators.  A wave owns 16 of a chunk's 64 steps in the products with the state
+// and with the inverse, and DK / 4 key channels of the state.  Row operands come from memory in operand
+// order, the next chunk's as soon as this one's are used; what waves exchange (the state's planes, X, u) are column
+// operands in LDS, [channel][step or key channel], rows padded by 8 against bank conflicts.
+template <int DK, int NT>
+struct Scan {
+    static constexpr int kKS = DK / 32, kMT = DK / 64, kN = NT * 16;
+    static constexpr int kPitchS = DK + 8, kPitchT = kDeltaChunk + 8;   // bf16 elements
+    static constexpr int kPlaneS = kN * kPitchS, kPlaneT = kN * kPitchT;
+};
+
+template <int DT, int DK, int NT, bool SAVE>
+__global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
+    constexpr int TI = in_planes(DT), OO = out_order(DT), OP = OO + 1;
+    typedef Scan<DK, NT> X;
+    typedef typename Elem<DT>::T T;
+    __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * X::kPlaneS], Xp[3 * X::kPlaneT], Up[OP * X::kPlaneT],
+        Uf[3 * X::kPlaneT];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
+    const int row4 = grp * 4, mine = wave * 16 + row4;             // a lane's four steps
+    // the slices of a head side by side on one XCD: they share its operands in the L2
+    const int total = a.s.nb * a.d.Hv * a.slices;
+    const int id = xcd_remap(blockIdx.x, total);
+    const int slice = id % a.slices, bh = id / a.slices, h = bh % a.d.Hv, b = bh / a.d.Hv, B = a.s.b0 + b;
+    const int hk = h / a.rep, v0 = slice * X::kN;
+    const int valid = valid_steps(a.d.lengths, B, a.d.L);
+    const int steps_first = a.s.c0 * kDeltaChunk;
+    int chunks = (valid - steps_first + kDeltaChunk - 1) / kDeltaChunk;
+    chunks = chunks < 0 ? 0 : (chunks > a.s.nc ? a.s.nc : chunks);
+
+    // the state: from the caller, from the slice of time before, or zeros
+    f32x4 S[X::kMT][NT];
+    {
+        const int P = a.first ? a.d.P : DK, V = a.first ? a.d.V : a.Vp;
+        const float *in = a.first ? a.d.initial_state : state_in;
+        const long long at = a.first ? (long long)B * a.d.Hv + h : bh;
+#pragma unroll
+        for (int i = 0; i < X::kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
+                    S[i][n][r] = in && p < P && v < V ? in[(at * P + p) * V + v] : 0.0f;
+                }
+    }
+    const auto put_state = [&] {
+#pragma unroll
+        for (int i = 0; i < X::kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float v[4] = {S[i][n][0], S[i][n][1], S[i][n][2], S[i][n][3]};
+                put_planes<3>(Sp + (n * 16 + col) * X::kPitchS + (wave * X::kMT + i) * 16 + row4, X::kPlaneS, v);
+            }
+    };
+    put_state();
+
+    const size_t of_k = ((size_t)b * a.s.nc * a.d.Hk + hk) * TI * 64 * DK * 2, step_k = (size_t)a.d.Hk * TI * 64 * DK * 2;
+    const size_t of_v = (size_t)b * a.s.nc * a.d.Hv + h;
+    constexpr int kPlaneK = 64 * DK * 2;
+    u32x4 fk[X::kKS][TI], fq[X::kKS][TI], ft[X::kMT][2][TI], fi[2][3], fa[2][OP];
+    float vin[NT][4];
+    f32x4 vek, veq, vfk, vbeta;
+    float last = 0.0f;
+    const char *pk = a.ws + a.w.k + of_k, *pq = a.ws + a.w.q + of_k, *pt = a.ws + a.w.kt + of_k;
+    const char *pi = a.ws + a.w.inv + of_v * 3 * 8192, *pa = a.ws + a.w.attn + of_v * OP * 8192;
+    const char *ps = a.ws + a.w.steps + of_v * sizeof(DeltaSteps);
+    const T *vrow[NT];
+    T *yrow[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int v = v0 + n * 16 + col, at = h * a.d.V + (v < a.d.V ? v : 0);
+        vrow[n] = row_of<DT>(a.d.v, B, at);
+        yrow[n] = row_of<DT>(a.d.y, B, at);
+    }
+    const auto load_kq = [&](int c) {
+#pragma unroll
+        for (int ks = 0; ks < X::kKS; ++ks) {
+            fragment<TI>(pk + c * step_k, wave * X::kKS + ks, kPlaneK, fk[ks]);
+            fragment<TI>(pq + c * step_k, wave * X::kKS + ks, kPlaneK, fq[ks]);
+        }
+    };
+    const auto load_steps = [&](int c) {
+        const DeltaSteps *s = (const DeltaSteps *)(ps + (size_t)c * a.d.Hv * sizeof(DeltaSteps));
+        vek = *(const f32x4 *)(s->ek + mine);
+        veq = *(const f32x4 *)(s->eq + mine);
+        vfk = *(const f32x4 *)(s->fk + mine);
+        vbeta = *(const f32x4 *)(s->beta + mine);
+        last = s->last;
+    };
+    const auto load_v = [&](int c) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            load4_until<DT>(vrow[n], steps_first + c * kDeltaChunk + mine, v0 + n * 16 + col < a.d.V ? valid : 0, vin[n]);
+    };
+    const auto load_inverse = [&](int c) {
+        const char *i = pi + (size_t)c * a.d.Hv * 3 * 8192;
+        fragment<3>(i, wave * 2, 8192, fi[0]);
+        if (wave >= 2) fragment<3>(i, wave * 2 + 1, 8192, fi[1]);
+    };
+    const auto load_attn = [&](int c) {
+        const char *at = pa + (size_t)c * a.d.Hv * OP * 8192;
+        fragment<OP>(at, wave * 2, 8192, fa[0]);
+        if (wave >= 2) fragment<OP>(at, wave * 2 + 1, 8192, fa[1]);
+    };
+    const auto load_kt = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < X::kMT; ++i)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                fragment<TI>(pt + c * step_k, (wave * X::kMT + i) * 2 + ks, kPlaneK, ft[i][ks]);
+    };
+    if (chunks) {
+        load_kq(0);
+        load_v(0);
+        load_steps(0);
+        load_inverse(0);
+        load_kt(0);
+        load_attn(0);
+    }
+    float *saved = SAVE ? (float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0) * delta_saved(a.d.P, a.d.V) : nullptr;
+
+    for (int c = 0; c < chunks; ++c) {
+        const bool more = c + 1 < chunks;
+        if constexpr (SAVE) {
+#pragma unroll
+            for (int i = 0; i < X::kMT; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        saved[(size_t)((wave * X::kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
+        }
+        __syncthreads();
+        f32x4 ks_[NT], qs[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) ks_[n] = qs[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < X::kKS; ++ks)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                u32x4 s[3];
+                get_planes<3>(Sp + (n * 16 + col) * X::kPitchS + ks * 32 + grp * 8, X::kPlaneS, s);
+                multiply<TI, 3, 2>(fk[ks], s, ks_[n]);
+                multiply<TI, 3, OO>(fq[ks], s, qs[n]);
+            }
+        if (more) load_kq(c + 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], ks_[n][r], vin[n][r]);
+            put_planes<3>(Xp + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, x);
+        }
+        if (more) load_v(c + 1);
+        __syncthreads();
+        f32x4 z[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            z[n] = f32x4{0, 0, 0, 0};
+            u32x4 x[3];
+            const uint16_t *from = Xp + (n * 16 + col) * X::kPitchT + grp * 8;
+            get_planes<3>(from, X::kPlaneT, x);
+            multiply<3, 3, 2>(fi[0], x, z[n]);
+            if (wave >= 2) {
+                get_planes<3>(from + 32, X::kPlaneT, x);
+                multiply<3, 3, 2>(fi[1], x, z[n]);
+            }
+        }
+        if (more) load_inverse(c + 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float u[4], uf[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                u[r] = vbeta[r] * z[n][r];
+                uf[r] = u[r] * vfk[r];
+            }
+            put_planes<3>(Uf + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, uf);
+            put_planes<OP>(Up + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, u);
+            if constexpr (SAVE)
+                *(f32x4 *)(saved + (size_t)DK * a.Vp + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = z[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < X::kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[i][n] *= last;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                u32x4 u[3];
+                get_planes<3>(Uf + (n * 16 + col) * X::kPitchT + ks * 32 + grp * 8, X::kPlaneT, u);
+#pragma unroll
+                for (int i = 0; i < X::kMT; ++i) multiply<TI, 3, 2>(ft[i][ks], u, S[i][n]);
+            }
+        if (more) load_kt(c + 1);
+        put_state();
+        // y
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 o = {0, 0, 0, 0};
+            u32x4 u[OP];
+            const uint16_t *from = Up + (n * 16 + col) * X::kPitchT + grp * 8;
+            get_planes<OP>(from, X::kPlaneT, u);
+            multiply<OP, OP, OO>(fa[0], u, o);
+            if (wave >= 2) {
+                get_planes<OP>(from + 32, X::kPlaneT, u);
+                multiply<OP, OP, OO>(fa[1], u, o);
+            }
+            float y[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(veq[r], qs[n][r], o[r]);
+            if (v0 + n * 16 + col < a.d.V) {
+                const int t = steps_first + c * kDeltaChunk + mine;
+                // past the sequence's end: zeros, up to the end of the rows
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
+                store4_until<DT>(yrow[n], t, a.d.L, y);
+            }
+        }
+        if (more) {
+            load_attn(c + 1);
+            load_steps(c + 1);
+        }
+        if constexpr (SAVE) saved += delta_saved(a.d.P, a.d.V);
+    }
+    // chunks past the sequence's end
+    for (int c = chunks; c < a.s.nc; ++c) {
+        const float zeros[4] = {};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (v0 + n * 16 + col < a.d.V)
+                store4_until<DT>(yrow[n], steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+    }
+    {
+        float *out = a.last ? a.d.final_state : state_out;
+        const int P = a.last ? a.d.P : DK, V = a.last ? a.d.V : a.Vp;
+        const long long at = a.last ? (long long)B * a.d.Hv + h : bh;
+        if (out) {
+#pragma unroll
+            for (int i = 0; i < X::kMT; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
+                        if (p < P && v < V) out[(at * P + p) * V + v] = S[i][n][r];
+                    }
+        }
+    }
+}
+
+template <int DT, int DK, int NT>
+int forward(const DeltaArgs &a, hipStream_t st) {
+    float *carry = (float *)(a.ws + a.w.state);
+    const unsigned groups = (unsigned)(a.s.nb * a.d.Hv * a.slices);
+    if (a.d.states)
+        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, true>), dim3(groups), dim3(256), 0, st, a, carry, carry);
+    else
+        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, false>), dim3(groups), dim3(256), 0, st, a, carry, carry);
+    return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
+}
+
+template <int DT, int DK>
+int forward_by_slices(DeltaArgs a, hipStream_t st) {
+    a.slices = a.Vp / 16;
+    return forward<DT, DK, 1>(a, st);
+}
+
+template <int DT>
+int forward_by_width(const DeltaArgs &a, hipStream_t st) {
+    switch (delta_key_pad(a.d.P)) {
+        case 64: return forward_by_slices<DT, 64>(a, st);
+        case 128: return forward_by_slices<DT, 128>(a, st);
+        default: return forward_by_slices<DT, 256>(a, st);
+    }
+}
+
+// ------------------------------------------------------------------ one token
+//
+// The state's bytes: read once, held in registers between the two products with it, written once.  A work-group
+// takes 64 value channels of one head; a thread four neighbouring channels of every 16th key channel.
+constexpr int kStepValues = 64;
+
+template <int DT, int DK>
+__global__ __launch_bounds__(256) void delta_step_kernel(miconv_gated_delta_t d, const float *state, int slots,
+                                                         const int *slot_of, float *state_out, int tiles, int first) {
+    constexpr int kRows = DK / 16;
+    typedef typename Elem<DT>::T T;
+    __shared__ float ks[DK], qs[DK], sums[4][2];
+    __shared__ __attribute__((aligned(16))) float red[4][kStepValues];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int id = first + blockIdx.x, tile = id % tiles, bh = id / tiles, h = bh % d.Hv, b = bh / d.Hv;
+    const int hk = h / (d.Hv / d.Hk), v = tile * kStepValues + (tid & 15) * 4, p0 = tid >> 4;
+    const int slot = slot_of ? slot_of[b] : b;
+    const bool unused = slot < 0 || slot >= slots;
+    T *const y = row_of<DT>(d.y, b, 0) + ((long long)h * d.V) * d.y.stride_d;
+    if (unused) {
+        if (tid < 16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (v + e < d.V) y[(long long)(v + e) * d.y.stride_d] = Elem<DT>::put(0.0f);
+        }
+        return;
+    }
+    const long long head = ((long long)slot * d.Hv + h) * d.P * d.V;
+    float S[kRows][4];
+    const bool whole = v + 4 <= d.V && d.V % 4 == 0 && (uintptr_t)state % 16 == 0 && (uintptr_t)state_out % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int p = i * 16 + p0;
+        const float *from = state + head + (long long)p * d.V + v;
+        if (p < d.P && whole) {
+            const f32x4 s = __builtin_nontemporal_load((const f32x4 *)from);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] = s[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] = p < d.P && v + e < d.V ? from[e] : 0.0f;
+        }
+    }
+    {
+        float k = 0.0f, q = 0.0f;
+        if (tid < d.P) {
+            k = Elem<DT>::get(*row_of<DT>(d.k, b, hk * d.P + tid));
+            q = Elem<DT>::get(*row_of<DT>(d.q, b, hk * d.P + tid));
+        }
+        if (d.l2norm) {
+            float kk = k * k, qq = q * q;
+#pragma unroll
+            for (int o = 32; o; o /= 2) {
+                kk += __shfl_xor(kk, o);
+                qq += __shfl_xor(qq, o);
+            }
+            if (lane == 0) {
+                sums[wave][0] = kk;
+                sums[wave][1] = qq;
+            }
+            __syncthreads();
+            kk = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
+            qq = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
+            k *= 1.0f / __builtin_sqrtf(kk + MICONV_DELTA_NORM_EPS);
+            q *= 1.0f / __builtin_sqrtf(qq + MICONV_DELTA_NORM_EPS);
+        }
+        if (tid < DK) {
+            ks[tid] = k;
+            qs[tid] = q * d.scale;
+        }
+    }
+    const float g = ((const float *)d.g.data)[(long long)b * d.g.stride_b + (long long)h * d.g.stride_d];
+    const float beta = ((const float *)d.beta.data)[(long long)b * d.beta.stride_b + (long long)h * d.beta.stride_d];
+    const float decay = exp_any(g);
+    float vin[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        vin[e] = v + e < d.V ? Elem<DT>::get(*row_of<DT>(d.v, b, h * d.V + v + e)) : 0.0f;
+    __syncthreads();
+    // a sum over the key channels: over the thread's rows, its wave's four row groups, the waves
+    const auto total = [&](float (&s)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] += __shfl_xor(s[e], 16);
+            s[e] += __shfl_xor(s[e], 32);
+        }
+        if (lane < 16) *(f32x4 *)&red[wave][lane * 4] = f32x4{s[0], s[1], s[2], s[3]};
+        __syncthreads();
+        f32x4 r = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) r += *(const f32x4 *)&red[w][(tid & 15) * 4];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = r[e];
+    };
+    float u[4] = {};
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const float k = ks[i * 16 + p0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            S[i][e] *= decay;
+            u[e] = __builtin_fmaf(k, S[i][e], u[e]);
+        }
+    }
+    total(u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = beta * (vin[e] - u[e]);
+    float o[4] = {};
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int p = i * 16 + p0;
+        const float k = ks[p], q = qs[p];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            S[i][e] = __builtin_fmaf(k, u[e], S[i][e]);
+            o[e] = __builtin_fmaf(q, S[i][e], o[e]);
+        }
+        float *to = state_out + head + (long long)p * d.V + v;
+        if (p < d.P && whole) {
+            __builtin_nontemporal_store(f32x4{S[i][0], S[i][1], S[i][2], S[i][3]}, (f32x4 *)to);
+        } else if (p < d.P) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (v + e < d.V) to[e] = S[i][e];
+        }
+    }
+    total(o);
+    if (tid < 16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (v + e < d.V) y[(long long)(v + e) * d.y.stride_d] = Elem<DT>::put(o[e]);
+    }
+}
+
+template <int DT>
+int step(const miconv_gated_delta_t &d, const float *state, int slots, const int *slot_of, float *state_out,
+         hipStream_t st) {
+    const int tiles = (d.V + kStepValues - 1) / kStepValues;
+    return launch_groups((long long)d.B * d.Hv * tiles, 256, [&](unsigned n, unsigned first) {
+        switch (delta_key_pad(d.P)) {
+            case 64:
+                hipLaunchKernelGGL((delta_step_kernel<DT, 64>), dim3(n), dim3(256), 0, st, d, state, slots, slot_of,
+                                   state_out, tiles, (int)first);
+                break;
+            case 128:
+                hipLaunchKernelGGL((delta_step_kernel<DT, 128>), dim3(n), dim3(256), 0, st, d, state, slots, slot_of,
+                                   state_out, tiles, (int)first);
+                break;
+            default:
+                hipLaunchKernelGGL((delta_step_kernel<DT, 256>), dim3(n), dim3(256), 0, st, d, state, slots, slot_of,
+                                   state_out, tiles, (int)first);
+        }
+    });
+}
+
+}  // namespace
+
+int launch_delta_fwd(const DeltaArgs &a, int dtype, hipStream_t st) {
+    return dtype == MICONV_BF16 ? forward_by_width<1>(a, st) : forward_by_width<0>(a, st);
+}
+
+int launch_delta_step(const miconv_gated_delta_t &d, int dtype, const float *state, int slots, const int *slot_of,
+                      float *state_out, hipStream_t st) {
+    return dtype == MICONV_BF16 ? step<1>(d, state, slots, slot_of, state_out, st)
+                                : step<0>(d, state, slots, slot_of, state_out, st);
+}
+
+}  // namespace miconv

@@ -96,7 +96,7 @@ extern "C" {
 #define MICONV_ERR_DTYPE 4       /* dtype is neither MICONV_F32 nor MICONV_BF16 */
 #define MICONV_ERR_ALIAS 5       /* the output overlaps an input or the workspace */
 #define MICONV_ERR_ALIGN 6       /* a base pointer is not 16-byte aligned */
-#define MICONV_ERR_WORKSPACE 7   /* selective_scan_bwd alone: less than its smallest slice (all other plans adapt to any budget) */
+#define MICONV_ERR_WORKSPACE 7   /* selective_scan_bwd, gated_delta_*: less than the smallest slice (all other plans adapt to any budget) */
 #define MICONV_ERR_HIP 8         /* a HIP call or kernel launch failed */
 #define MICONV_ERR_PASS 9        /* unknown pass id */
 #define MICONV_ERR_TOO_LARGE 10  /* a tensor is 2 GiB or larger (state-space operators: a size past its bound) */
@@ -613,6 +613,63 @@ int matmul_i8(int B, int L, int O, int C_pad, const signed char *q, const float 
 int matmul_i8_workspace_size(int B, int L, int O, int C_pad, size_t workspace_limit, size_t *bytes_out);
 /* One-line description of the kernel a call runs (few tokens, or tile, stages and splits). */
 int matmul_i8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, char *buf, size_t buflen);
+
+/*
+ * Gated delta rule: a linear attention whose state [P][V] per head forgets by a
+ * gate and corrects what it holds for a key.  q, k [B][Hk*P][L] (head hk's
+ * channels hk*P ..), v, y [B][Hv*V][L], value head h reading query and key of
+ * head h / (Hv/Hk); g (log decays, meant to be <= 0; below -200 counts as -200) and
+ * beta [B][Hv][L] fp32:
+ *   q^ = scale * q / |q|,  k^ = k / |k|  if l2norm (|.| = sqrt(sum of squares + 1e-6) over the head),
+ *   q^ = scale * q,        k^ = k        otherwise
+ *   z_t = v_t - exp(g_t) S_{t-1}^T k^_t,   S_t = exp(g_t) S_{t-1} + k^_t (beta_t z_t)^T,   y_t = S_t^T q^_t
+ * S_{-1} is initial_state [B][Hv][P][V] fp32 (NULL: zeros); final_state gets the
+ * state after the last valid step.  P = 1..256, V = 1..512, Hv a multiple of Hk
+ * and at most 65536.
+ * Steps are taken in chunks of 64: a value that is not finite may reach all steps of its chunk,
+ * and the steps after, of the value channels (v, state) or heads (q, k, g, beta) that it belongs to.
+ * `states` (gated_delta_states_size bytes; the forward pass writes it when it is not
+ * NULL) holds what the backward pass takes up at each chunk.
+ * Backward: dy and d_final_state in; dq, dk, dv and in fp32, packed, dg, dbeta
+ * [B][Hv][L] and d_initial_state out; d_final_state and d_initial_state are optional.
+ * Heads that share a key head add up in dq and dk.
+ * Workspace: the fastest plan within it; gated_delta_workspace_size is what a
+ * pass uses under workspace_limit, or the least it needs if that is more (a chunk of one
+ * sequence), below which it returns MICONV_ERR_WORKSPACE.
+ */
+#define MICONV_DELTA_MAX_KEY 256
+#define MICONV_DELTA_MAX_VALUE 512
+#define MICONV_DELTA_NORM_EPS 1e-6f
+
+typedef struct miconv_gated_delta {
+    int B, Hk, Hv, P, V, L, l2norm;
+    float scale;
+    miconv_rows_t q, k, v, g, beta;
+    const float *initial_state;
+    const int *lengths;
+    miconv_rows_t y;              /* forward */
+    float *final_state;
+    float *states;                /* written by the forward pass, read by the backward pass */
+    miconv_rows_t dy;             /* backward */
+    const float *d_final_state;
+    miconv_rows_t dq, dk, dv;
+    float *dg, *dbeta, *d_initial_state;
+} miconv_gated_delta_t;
+
+int gated_delta_fwd(const miconv_gated_delta_t *d, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+int gated_delta_bwd(const miconv_gated_delta_t *d, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+int gated_delta_states_size(int B, int Hv, int P, int V, int L, size_t *bytes_out);
+int gated_delta_workspace_size(const miconv_gated_delta_t *d, int dtype, int backward, size_t workspace_limit,
+                               size_t *bytes_out);
+/* The slices (sequences x chunks) and value tiles a call with these sizes and workspace takes. */
+int gated_delta_describe(const miconv_gated_delta_t *d, int dtype, int backward, size_t workspace_bytes, char *buf,
+                         size_t buflen);
+/*
+ * One time step for each of B sequences (L = 1): q, k, v, y [B][...] (stride_b, stride_d),
+ * state [slots][Hv][P][V]; slots, slot_of and state_out as for causal_conv1d_step.
+ */
+int gated_delta_step(const miconv_gated_delta_t *d, int dtype, const float *state, int slots, const int *slot_of,
+                     float *state_out, void *stream);
 
 /* Static text for a status code (never NULL). */
 const char *miconv_status_string(int status);
