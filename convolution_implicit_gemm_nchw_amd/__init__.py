@@ -666,6 +666,18 @@ class _Scan(ctypes.Structure):
                 ("d_initial_state", _VP)]
 
 
+class _Tokens(ctypes.Structure):
+    """miconv_tokens_t."""
+    _fields_ = [("data", _VP), ("stride_b", _LL), ("stride_l", _LL), ("stride_c", _LL)]
+
+
+class _LayerNorm(ctypes.Structure):
+    """miconv_layer_norm_t."""
+    _fields_ = [("B", _I), ("L", _I), ("C", _I), ("eps", ctypes.c_float), ("x", _Tokens), ("weight", _VP), ("bias", _VP),
+                ("lengths", _VP), ("y", _Tokens), ("stats", _VP), ("dy", _Tokens), ("dx", _Tokens), ("dw", _VP),
+                ("db", _VP)]
+
+
 class _GatedDelta(ctypes.Structure):
     """miconv_gated_delta_t."""
     _fields_ = [("B", _I), ("Hk", _I), ("Hv", _I), ("P", _I), ("V", _I), ("L", _I), ("l2norm", _I),
@@ -699,7 +711,10 @@ for _name, _args in {
         "gated_delta_step": [_VP, _I, _VP, _I, _VP, _VP, _VP],
         "gated_delta_states_size": [_I, _I, _I, _I, _I, _SZP],
         "gated_delta_workspace_size": [_VP, _I, _I, _SZ, _SZP],
-        "gated_delta_describe": [_VP, _I, _I, _SZ, ctypes.c_char_p, _SZ]}.items():
+        "gated_delta_describe": [_VP, _I, _I, _SZ, ctypes.c_char_p, _SZ],
+        "layer_norm_fwd": [_VP, _I, _VP],
+        "layer_norm_bwd": [_VP, _I, _VP, _SZ, _VP],
+        "layer_norm_bwd_workspace_size": [_VP, _I, _SZ, _SZP]}.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _I
@@ -874,6 +889,29 @@ def gated_delta_describe(B, Hk, Hv, P, V, L, dtype=F32, backward=False, workspac
     _check(_lib.gated_delta_describe(_delta_sizes(B, Hk, Hv, P, V, L), dtype, int(backward), workspace_bytes, buf, 256),
            "gated_delta_describe")
     return buf.value.decode()
+
+
+# ---------------------------------------------------------------- layer norm
+
+def layer_norm_stats(x, channel_major=False, stream=None):
+    """A buffer [2, tokens] for the mean and 1 / standard deviation that layer_norm_fwd saves for layer_norm_bwd."""
+    return _call(_bind.layer_norm_stats, stream, x, channel_major)
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, channel_major=False, lengths=None, y=None, stats=None, stream=None):
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the channels of each token.  x is [T, C] or [B, L, C]
+    (tokens first) or, channel_major, [C, T] or [B, C, L], a view with a contiguous last axis; weight and bias fp32 [C].
+    lengths (int32 [B]) are the valid tokens of right-padded sequences; y is 0 past them.  stats (layer_norm_stats),
+    when given, is written."""
+    return _call(_bind.layer_norm_fwd, stream, x, weight, bias, eps, channel_major, lengths, y, stats)
+
+
+def layer_norm_bwd(x, dy, stats, weight=None, bias=None, channel_major=False, lengths=None, dx=None, dw=None, db=None,
+                   workspace=None, stream=None):
+    """(dx, dw, db) of layer_norm_fwd for the output gradient dy: dx in x's dtype, dw and db fp32 [C] (None without
+    a weight, a bias).  `stats` is what the forward pass saved for the same x; dx 0 past the lengths, whose padding is
+    no part of dw and db."""
+    return _call(_bind.layer_norm_bwd, stream, x, dy, stats, weight, bias, channel_major, lengths, dx, dw, db, workspace)
 
 
 I8_PAD = 128

@@ -585,6 +585,84 @@ PyObject *delta_step(Args a) {
     return y.wrap();
 }
 
+// ------------------------------------------------------------------ layer norm
+
+// A [.., L, C] operand, or channel-major [.., C, L], of 2 or 3 dimensions.
+miconv_tokens_t tokens_of(const char *name, const at::Tensor &t, bool cm) {
+    const int64_t d = t.dim(), last = t.size(d - 1);
+    if (last > 1 && t.stride(d - 1) != 1)
+        refuse(std::string(name) + " must be contiguous along its last axis");
+    const int64_t inner = last > 1 ? 1 : t.stride(d - 1), sb = d == 3 ? t.stride(0) : 0, mid = t.stride(d - 2);
+    // an axis of one element counts as contiguous
+    if (cm) return {t.data_ptr(), sb, inner, t.size(d - 2) > 1 ? mid : 1};
+    return {t.data_ptr(), sb, mid, last > 1 ? inner : 1};
+}
+
+// The sizes of x, tokens first or channel-major.
+miconv_layer_norm_t norm_common(const Lead &x, bool cm) {
+    miconv_layer_norm_t n = {};
+    const int64_t d = x.t.dim();
+    n.B = d == 3 ? dim(x.t.size(0)) : 1;
+    n.L = dim(x.t.size(cm ? d - 1 : d - 2));
+    n.C = dim(x.t.size(cm ? d - 2 : d - 1));
+    n.x = tokens_of("x", x.t, cm);
+    return n;
+}
+
+Lead norm_lead(PyObject *o) {
+    const int64_t d = THPVariable_Check(o) ? THPVariable_Unpack(o).dim() : 3;
+    return Lead("x", o, d == 2 ? 2 : 3);
+}
+
+// (x, channel_major) -> stats
+PyObject *norm_stats(Args a) {
+    const Lead x = norm_lead(a[0]);
+    const miconv_layer_norm_t n = norm_common(x, truth(a[1]));
+    return THPVariable_Wrap(at::empty({2, (int64_t)n.B * n.L}, x.t.options().dtype(at::kFloat)));
+}
+
+// (x, weight, bias, eps, channel_major, lengths, y, stats) -> y
+PyObject *norm_fwd(Args a) {
+    const Lead x = norm_lead(a[0]);
+    const bool cm = truth(a[4]);
+    miconv_layer_norm_t n = norm_common(x, cm);
+    n.weight = (const float *)optional("weight", a[1], {n.C}, at::kFloat, x.dev);
+    n.bias = (const float *)optional("bias", a[2], {n.C}, at::kFloat, x.dev);
+    const double eps = PyFloat_AsDouble(a[3]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+    n.eps = (float)eps;
+    n.lengths = (const int *)optional("lengths", a[5], {n.B}, at::kInt, x.dev);
+    const Out y("y", a[6], x.t.sizes(), x.dt, x, true);
+    n.y = tokens_of("y", y.t, cm);
+    n.stats = (float *)optional("stats", a[7], {2, (int64_t)n.B * n.L}, at::kFloat, x.dev);
+    run("layer_norm_fwd", x.dev, [&](void *st) { return layer_norm_fwd(&n, x.code, st); });
+    return y.wrap();
+}
+
+// (x, dy, stats, weight, bias, channel_major, lengths, dx, dw, db, workspace) -> (dx, dw, db)
+PyObject *norm_bwd(Args a) {
+    const Lead x = norm_lead(a[0]);
+    const bool cm = truth(a[5]);
+    miconv_layer_norm_t n = norm_common(x, cm);
+    n.dy = tokens_of("dy", fits("dy", a[1], x.t.sizes(), x.dt, x.dev), cm);
+    n.stats = (float *)packed("stats", a[2], {2, (int64_t)n.B * n.L}, at::kFloat, x.dev);
+    n.weight = (const float *)optional("weight", a[3], {n.C}, at::kFloat, x.dev);
+    optional("bias", a[4], {n.C}, at::kFloat, x.dev);
+    n.lengths = (const int *)optional("lengths", a[6], {n.B}, at::kInt, x.dev);
+    const Out dx("dx", a[7], x.t.sizes(), x.dt, x, true);
+    const Out dw = a[3] == Py_None && a[8] == Py_None ? Out() : Out("dw", a[8], {n.C}, at::kFloat, x);
+    const Out db = a[4] == Py_None && a[9] == Py_None ? Out() : Out("db", a[9], {n.C}, at::kFloat, x);
+    n.dx = tokens_of("dx", dx.t, cm);
+    n.dw = (float *)dw.data();
+    n.db = (float *)db.data();
+    size_t need = 0;
+    if (a[10] == Py_None)
+        check(layer_norm_bwd_workspace_size(&n, x.code, MICONV_MAX_WORKSPACE_BYTES, &need), "layer_norm_bwd_workspace_size");
+    const Scratch ws(a[10], need, x);
+    run("layer_norm_bwd", x.dev, [&](void *st) { return layer_norm_bwd(&n, x.code, ws.p, ws.n, st); });
+    return tuple({&dx, &dw, &db});
+}
+
 // ------------------------------------------------------------------ module
 
 // fn with N arguments; no C++ exception leaves it.
@@ -640,6 +718,9 @@ PyMethodDef methods[] = {ENTRY("causal_conv1d_fwd", conv_fwd, 8),
                          ENTRY("gated_delta_fwd", delta_fwd, 14),
                          ENTRY("gated_delta_bwd", delta_bwd, 17),
                          ENTRY("gated_delta_step", delta_step, 13),
+                         ENTRY("layer_norm_stats", norm_stats, 2),
+                         ENTRY("layer_norm_fwd", norm_fwd, 8),
+                         ENTRY("layer_norm_bwd", norm_bwd, 11),
                          {"errors", (PyCFunction)(void *)errors, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_miconv_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

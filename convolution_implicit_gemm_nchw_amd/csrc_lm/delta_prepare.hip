@@ -251,8 +251,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     // columns 0..31 of rows 32.. (backward).
     char *const inv = a.ws + a.w.inv + of_v * 3 * 8192, *const attn = a.ws + a.w.attn + of_v * X::kOut * 8192;
 #pragma unroll
-    for (int f = wave; f < 8; f += 4) {
-        const int tile = f >> 1, ks = f & 1;
+    for (int half = 0; half < 2; ++half) {
+        const int f = half * 4 + wave, tile = f >> 1, ks = f & 1;
         if (BWD ? (tile >= 2 && ks == 0) : (tile < 2 && ks == 1)) continue;
         const int at = (tile * 16 + col) * kRow + ks * 32 + (lane >> 4) * 8;
         float v[8], m[8];

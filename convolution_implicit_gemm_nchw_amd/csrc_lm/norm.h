@@ -1,0 +1,19 @@
+// norm.h -- host entries into layer norm's kernels; arguments are already validated.
+#pragma once
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+
+#include "../../include/miconv.h"
+#include "ssm.h"
+
+namespace miconv {
+
+// Whether channels are contiguous in every operand (tokens first), else time steps are.
+bool norm_tokens_first(const miconv_layer_norm_t &n, bool backward);
+// Work-groups of the backward pass, each with a row of partial sums of dw and db in the workspace; 1 needs none.
+int norm_parts(const miconv_layer_norm_t &n, int dtype, size_t budget);
+
+int launch_norm_fwd(const miconv_layer_norm_t &n, int dtype, hipStream_t st);
+int launch_norm_bwd(const miconv_layer_norm_t &n, int dtype, int parts, float *ws, hipStream_t st);
+
+}  // namespace miconv

@@ -96,7 +96,7 @@ extern "C" {
 #define MICONV_ERR_DTYPE 4       /* dtype is neither MICONV_F32 nor MICONV_BF16 */
 #define MICONV_ERR_ALIAS 5       /* the output overlaps an input or the workspace */
 #define MICONV_ERR_ALIGN 6       /* a base pointer is not 16-byte aligned */
-#define MICONV_ERR_WORKSPACE 7   /* selective_scan_bwd, gated_delta_*: less than the smallest slice (all other plans adapt to any budget) */
+#define MICONV_ERR_WORKSPACE 7   /* selective_scan_bwd, gated_delta_*, layer_norm_bwd: less than the least they need (all other plans adapt to any budget) */
 #define MICONV_ERR_HIP 8         /* a HIP call or kernel launch failed */
 #define MICONV_ERR_PASS 9        /* unknown pass id */
 #define MICONV_ERR_TOO_LARGE 10  /* a tensor is 2 GiB or larger (state-space operators: a size past its bound) */
@@ -670,6 +670,43 @@ int gated_delta_describe(const miconv_gated_delta_t *d, int dtype, int backward,
  */
 int gated_delta_step(const miconv_gated_delta_t *d, int dtype, const float *state, int slots, const int *slot_of,
                      float *state_out, void *stream);
+
+/*
+ * Layer normalisation over the channels of each token (b, l):
+ *   y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(mean of (x - mean)^2 + eps)
+ * A miconv_tokens_t holds element (b, l, c) at data + b*stride_b + l*stride_l +
+ * c*stride_c; either stride_c is 1 in every operand (tokens first) or stride_l
+ * is (channel-major), an axis of one element having any stride.  weight, bias [C] fp32 (NULL: ones, zeros).  stats [2][B*L] fp32
+ * (mean, then rstd; tokens run over [B, L] in that order), when given, is written by the forward pass and read
+ * by the backward pass.  lengths as above: padding is 0 in y and dx, and no part of dw or db.
+ * Backward: dy and stats in; dx, and in fp32 dw = sum over tokens of dy * (x - mean) * rstd and
+ * db = sum over tokens of dy out, dw and db optional.  C is at most 2^20, B*L at most 2^30.
+ * Workspace: partial sums of dw and db; the fastest split that fits, 8*C bytes at least
+ * (else MICONV_ERR_WORKSPACE).
+ */
+#define MICONV_NORM_MAX_CHANNELS (1 << 20)
+
+typedef struct miconv_tokens {
+    void *data;
+    long long stride_b, stride_l, stride_c;   /* elements */
+} miconv_tokens_t;
+
+typedef struct miconv_layer_norm {
+    int B, L, C;
+    float eps;
+    miconv_tokens_t x;
+    const float *weight, *bias;
+    const int *lengths;
+    miconv_tokens_t y;            /* forward */
+    float *stats;                 /* written by the forward pass, read by the backward pass */
+    miconv_tokens_t dy;           /* backward */
+    miconv_tokens_t dx;
+    float *dw, *db;
+} miconv_layer_norm_t;
+
+int layer_norm_fwd(const miconv_layer_norm_t *n, int dtype, void *stream);
+int layer_norm_bwd(const miconv_layer_norm_t *n, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+int layer_norm_bwd_workspace_size(const miconv_layer_norm_t *n, int dtype, size_t workspace_limit, size_t *bytes_out);
 
 /* Static text for a status code (never NULL). */
 const char *miconv_status_string(int status);
