@@ -712,6 +712,10 @@ for _name, _args in {
         "gated_delta_states_size": [_I, _I, _I, _I, _I, _SZP],
         "gated_delta_workspace_size": [_VP, _I, _I, _SZ, _SZP],
         "gated_delta_describe": [_VP, _I, _I, _SZ, ctypes.c_char_p, _SZ],
+        "quantize_f8": [_I, _I, _I, _I, _VP, _LL, _LL, _LL, _VP, _VP, _VP],
+        "matmul_f8": [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _SZ, _VP],
+        "matmul_f8_workspace_size": [_I, _I, _I, _I, _SZ, _SZP],
+        "matmul_f8_describe": [_I, _I, _I, _I, _SZ, ctypes.c_char_p, _SZ],
         "layer_norm_fwd": [_VP, _I, _VP],
         "layer_norm_bwd": [_VP, _I, _VP, _SZ, _VP],
         "layer_norm_bwd_workspace_size": [_VP, _I, _SZ, _SZP]}.items():
@@ -940,4 +944,31 @@ def matmul_i8_describe(tokens, O, C_pad, workspace_bytes=MAX_WORKSPACE_BYTES):
     """The kernel that matmul_i8 takes for these sizes: few tokens, or tile, stages and splits."""
     buf = ctypes.create_string_buffer(256)
     _check(_lib.matmul_i8_describe(1, tokens, O, C_pad, workspace_bytes, buf, 256), "matmul_i8_describe")
+    return buf.value.decode()
+
+
+def quantize_f8(x, channel_major=False, q=None, scale=None, stream=None):
+    """Quantisation to 8-bit floating point with a power of two for each token and block of 128 channels: the least
+    2^e, e >= -127, with max|x| <= 448 * 2^e, and q = x / 2^e rounded to nearest, ties to even.  x as for
+    quantize_tokens.  Returns q [tokens, C_pad] float8_e4m3fn (C_pad = C rounded up to 128, zeros past C) and scale
+    [C_pad / 128, tokens] float8_e8m0fnu.  A block with an infinity or a NaN becomes NaN.  A weight [O, C] is
+    quantised in the same way; w.t()[None] or dy.t()[None] is channel_major, with blocks along the other axis,
+    as the products of a backward pass take them."""
+    return _call(_bind.quantize_f8, stream, x, channel_major, q, scale)
+
+
+def matmul_f8(q, scale, wq, wscale, bias=None, out_dtype=torch.float32, length=None, y=None, workspace=None,
+              stream=None):
+    """y[m, n] = sum over blocks j of 128 of scale[j, m] wscale[j, n] sum_k q[m, k] wq[n, k] (+ bias[n]), summed in
+    fp32.  q [T, C_pad] and wq [O, C_pad] float8_e4m3fn with scales as quantize_f8 gives them, bias fp32 [O].  y is
+    [T, O], or with `length` = L channel-major [T / L, O, L]; fp32 or bf16 (y's dtype, or out_dtype)."""
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported dtype {out_dtype}; expected float32 or bfloat16")
+    return _call(_bind.matmul_f8, stream, q, scale, wq, wscale, bias, out_dtype is torch.bfloat16, length, y, workspace)
+
+
+def matmul_f8_describe(tokens, O, C_pad, workspace_bytes=MAX_WORKSPACE_BYTES):
+    """The kernel that matmul_f8 takes for these sizes: few tokens, or tile, stages and splits."""
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.matmul_f8_describe(1, tokens, O, C_pad, workspace_bytes, buf, 256), "matmul_f8_describe")
     return buf.value.decode()

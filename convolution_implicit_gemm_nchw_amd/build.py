@@ -22,7 +22,8 @@ CSRC_LM = os.path.join(HERE, "csrc_lm")   # the language-model operators
 SOURCES = ["igemm.hip", "patch.hip", "bwdf16.hip", "pointwise.hip", "tinyc.hip", "noalloc.hip", "bwd_bias.hip",
            "convnd.hip", "plan.cpp", "ndplan.cpp", "abi.cpp"]
 SOURCES_LM = ["causal_conv.hip", "scan_fwd.hip", "scan_bwd.hip", "quantize.hip", "matmul_i8.hip", "ssm_abi.cpp",
-              "delta_prepare.hip", "delta_fwd.hip", "delta_bwd.hip", "delta_abi.cpp", "layer_norm.hip", "norm_abi.cpp"]
+              "delta_prepare.hip", "delta_fwd.hip", "delta_bwd.hip", "delta_abi.cpp", "layer_norm.hip", "norm_abi.cpp",
+              "quantize_f8.hip", "matmul_f8.hip", "f8_abi.cpp"]
 ARCH = "gfx950"
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 

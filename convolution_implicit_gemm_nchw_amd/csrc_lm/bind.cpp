@@ -384,33 +384,91 @@ PyObject *scan_step(Args a) {
 
 // ------------------------------------------------------------------ 8-bit products
 
+// Tokens [T, C] or [B, L, C], or channel-major [B, C, L], by their strides.
+struct TokenView {
+    int B, L, C;
+    int64_t sb = 0, sl, sc = 1;
+    TokenView(const Lead &x, bool cm) {
+        const int64_t dims = x.t.dim();
+        int64_t nb = 1, l, c;
+        if (cm) {
+            nb = x.t.size(0), c = x.t.size(1), l = x.t.size(2);
+            sb = x.t.stride(0), sc = x.t.stride(1), sl = 1;
+            if (l > 1 && x.t.stride(2) != 1) refuse("x must have contiguous time steps (stride 1 along the last axis)");
+        } else {
+            if (dims == 3) nb = x.t.size(0), sb = x.t.stride(0);
+            l = x.t.size(dims - 2), sl = x.t.stride(dims - 2), c = x.t.size(dims - 1);
+            if (c > 1 && x.t.stride(dims - 1) != 1) refuse("x must have contiguous channels (stride 1 along the last axis)");
+        }
+        B = dim(nb), L = dim(l), C = dim(c);
+    }
+};
+
+Lead token_lead(PyObject *o, bool cm) {
+    return Lead("x", o, THPVariable_Check(o) && !cm && THPVariable_Unpack(o).dim() == 2 ? 2 : 3);
+}
+
 // (x, channel_major, q, scale) -> (q, scale)
 PyObject *quantize(Args a) {
     const bool cm = truth(a[1]);
-    const int64_t dims = THPVariable_Check(a[0]) && !cm && THPVariable_Unpack(a[0]).dim() == 2 ? 2 : 3;
-    const Lead x("x", a[0], dims);
-    int64_t nb = 1, L, C, sb = 0, sl, sc = 1;
-    if (cm) {
-        nb = x.t.size(0), C = x.t.size(1), L = x.t.size(2);
-        sb = x.t.stride(0), sc = x.t.stride(1), sl = 1;
-        if (L > 1 && x.t.stride(2) != 1) refuse("x must have contiguous time steps (stride 1 along the last axis)");
-    } else {
-        if (dims == 3) nb = x.t.size(0), sb = x.t.stride(0);
-        L = x.t.size(dims - 2), sl = x.t.stride(dims - 2), C = x.t.size(dims - 1);
-        if (C > 1 && x.t.stride(dims - 1) != 1) refuse("x must have contiguous channels (stride 1 along the last axis)");
-    }
-    const int64_t pad = (C + MICONV_I8_PAD - 1) / MICONV_I8_PAD * MICONV_I8_PAD;
-    const int B = dim(nb), tokens = dim(L), channels = dim(C);
-    const Out q("q", a[2], {nb * L, pad}, at::kChar, x), scale("scale", a[3], {nb * L}, at::kFloat, x);
+    const Lead x = token_lead(a[0], cm);
+    const TokenView v(x, cm);
+    const int64_t pad = ((int64_t)v.C + MICONV_I8_PAD - 1) / MICONV_I8_PAD * MICONV_I8_PAD, tokens = (int64_t)v.B * v.L;
+    const Out q("q", a[2], {tokens, pad}, at::kChar, x), scale("scale", a[3], {tokens}, at::kFloat, x);
     const void *data = x.t.data_ptr();
     run("quantize_tokens", x.dev, [&](void *st) {
-        return quantize_tokens(B, tokens, channels, x.code, data, sb, sl, sc, (signed char *)q.data(),
+        return quantize_tokens(v.B, v.L, v.C, x.code, data, v.sb, v.sl, v.sc, (signed char *)q.data(),
                                (float *)scale.data(), st);
     });
     return tuple({&q, &scale});
 }
 
+// (x, channel_major, q, scale) -> (q, scale)
+PyObject *quantize_blocks(Args a) {
+    const bool cm = truth(a[1]);
+    const Lead x = token_lead(a[0], cm);
+    const TokenView v(x, cm);
+    const int64_t blocks = ((int64_t)v.C + MICONV_I8_PAD - 1) / MICONV_I8_PAD, tokens = (int64_t)v.B * v.L;
+    const Out q("q", a[2], {tokens, blocks * MICONV_I8_PAD}, at::kFloat8_e4m3fn, x),
+        scale("scale", a[3], {blocks, tokens}, at::kFloat8_e8m0fnu, x);
+    const void *data = x.t.data_ptr();
+    run("quantize_f8", x.dev, [&](void *st) {
+        return quantize_f8(v.B, v.L, v.C, x.code, data, v.sb, v.sl, v.sc, (unsigned char *)q.data(),
+                           (unsigned char *)scale.data(), st);
+    });
+    return tuple({&q, &scale});
+}
+
+// The two products' types and entry points.
+struct Int8 {
+    typedef signed char Q;
+    typedef float S;
+    static constexpr at::ScalarType kQ = at::kChar, kS = at::kFloat;
+    static constexpr bool kBlocks = false;
+    static constexpr const char *kName = "matmul_i8";
+    static constexpr auto size = matmul_i8_workspace_size;
+    static constexpr auto call = matmul_i8;
+};
+struct Float8 {
+    typedef unsigned char Q, S;
+    static constexpr at::ScalarType kQ = at::kFloat8_e4m3fn, kS = at::kFloat8_e8m0fnu;
+    static constexpr bool kBlocks = true;
+    static constexpr const char *kName = "matmul_f8";
+    static constexpr auto size = matmul_f8_workspace_size;
+    static constexpr auto call = matmul_f8;
+};
+
+// The scales of n rows of K: one each, or one for each block of 128.
+template <typename X>
+const typename X::S *scales(const char *name, PyObject *o, int n, int K, int dev) {
+    const int64_t blocks[2] = {K / MICONV_I8_PAD, n}, each[1] = {n};
+    const at::Tensor &t = fits(name, o, X::kBlocks ? at::IntArrayRef(blocks, 2) : at::IntArrayRef(each, 1), X::kS, dev);
+    if (!t.is_contiguous()) refuse(std::string(name) + " must be contiguous");
+    return (const typename X::S *)t.data_ptr();
+}
+
 // (q, scale, wq, wscale, bias, bf16, length, y, workspace) -> y
+template <typename X>
 PyObject *matmul(Args a) {
     const at::Tensor &q = tensor("q", a[0]), &w = tensor("wq", a[2]);
     if (!q.is_cuda() || q.dim() != 2 || w.dim() != 2) refuse("q and wq must be 2-dimensional device tensors");
@@ -425,10 +483,10 @@ PyObject *matmul(Args a) {
         L = dim(length);
         B = T / L;
     }
-    const signed char *qp = (const signed char *)packed("q", a[0], {T, K}, at::kChar, dev);
-    const float *qs = (const float *)packed("scale", a[1], {T}, at::kFloat, dev);
-    const signed char *wp = (const signed char *)packed("wq", a[2], {O, K}, at::kChar, dev);
-    const float *ws = (const float *)packed("wscale", a[3], {O}, at::kFloat, dev);
+    const auto *qp = (const typename X::Q *)packed("q", a[0], {T, K}, X::kQ, dev);
+    const auto *qs = scales<X>("scale", a[1], T, K, dev);
+    const auto *wp = (const typename X::Q *)packed("wq", a[2], {O, K}, X::kQ, dev);
+    const auto *ws = scales<X>("wscale", a[3], O, K, dev);
     const float *bias = (const float *)optional("bias", a[4], {O}, at::kFloat, dev);
     at::Tensor y;
     if (a[7] == Py_None) {
@@ -442,7 +500,7 @@ PyObject *matmul(Args a) {
     }
     size_t need = 0;
     if (a[8] == Py_None)
-        check(matmul_i8_workspace_size(B, L, O, K, MICONV_MAX_WORKSPACE_BYTES, &need), "matmul_i8_workspace_size");
+        check(X::size(B, L, O, K, MICONV_MAX_WORKSPACE_BYTES, &need), (std::string(X::kName) + "_workspace_size").c_str());
     at::Tensor held;
     void *work = nullptr;
     if (a[8] != Py_None) {
@@ -456,8 +514,8 @@ PyObject *matmul(Args a) {
     if (held.defined()) work = held.data_ptr();
     const int code = code_of(y.scalar_type());
     void *out = y.data_ptr();
-    run("matmul_i8", dev, [&](void *st) {
-        return matmul_i8(B, L, O, K, qp, qs, wp, ws, bias, cm, code, out, work, work ? need : 0, st);
+    run(X::kName, dev, [&](void *st) {
+        return X::call(B, L, O, K, qp, qs, wp, ws, bias, cm, code, out, work, work ? need : 0, st);
     });
     return THPVariable_Wrap(y);
 }
@@ -713,7 +771,9 @@ PyMethodDef methods[] = {ENTRY("causal_conv1d_fwd", conv_fwd, 8),
                          ENTRY("selective_scan_bwd", scan_bwd, 18),
                          ENTRY("selective_scan_step", scan_step, 14),
                          ENTRY("quantize_tokens", quantize, 4),
-                         ENTRY("matmul_i8", matmul, 9),
+                         ENTRY("matmul_i8", matmul<Int8>, 9),
+                         ENTRY("quantize_f8", quantize_blocks, 4),
+                         ENTRY("matmul_f8", matmul<Float8>, 9),
                          ENTRY("gated_delta_states", delta_states, 4),
                          ENTRY("gated_delta_fwd", delta_fwd, 14),
                          ENTRY("gated_delta_bwd", delta_bwd, 17),

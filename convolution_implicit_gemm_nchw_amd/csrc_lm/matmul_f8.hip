@@ -1,0 +1,588 @@
+// matmul_f8.hip -- y[m][n] = sum over blocks of 128 of 2^(qs[m] + ws[n]) sum_k q[m][k] wq[n][k] (+ bias[n]), in 8-bit
+// floating point (e4m3) with a power of two for each row and block of either operand.
+//
+// The scaled MFMAs multiply 64 steps of k (128 for 16 x 16 blocks) and apply each row's power of two, so the blocks'
+// sums meet in one fp32 accumulator.  Inside, such an MFMA brings its products to the largest one's exponent and drops
+// bits: found to be 1.5e-5 of the result (2-norm), far below the half step of a bf16 y, 2^-8.  For fp32 y the operands are widened, with their
+// scales, to bf16, which holds both exactly, and multiplied by the bf16 MFMAs at half the rate: 1e-7.  Both operands hold k contiguously, so either can be an MFMA's row operand: the one along
+// whose axis y is contiguous (channels for token-major y, tokens for channel-major y), axis C below, because a
+// lane's accumulators run along the rows; the other is axis R.  Tiles arrive in LDS and leave it as in the 8-bit
+// integer product (matmul_i8.hip).
+#include "device.h"
+#include "f8.h"
+#include "ssm_device.h"
+#include "tile_store.h"
+
+namespace miconv {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+struct F8Args {
+    const unsigned char *c, *r;              // [NC][K], [NR][K]
+    const unsigned char *c_scale, *r_scale;  // [K / 128][NC], [K / 128][NR]
+    const float *c_bias, *r_bias;            // one of them, or none
+    void *y;
+    int NC, NR, K;
+    long long row;                           // as in store_row8
+    int len;
+    FDiv fd_len;
+    int tiles_c, tiles_r;
+    float *part;                             // split sums [split][NR][NC], or null
+    int k_split;                             // steps of k per split
+};
+
+DEVI i32x8 join(i32x4 lo, i32x4 hi) { return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}; }
+
+// A lane's 32 steps of k are two pieces of 16; which ones is free, as long as both operands take the same.
+DEVI f32x16 product(i32x8 a, i32x8 b, f32x16 acc, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, sa, 0, sb);
+}
+
+// 32 steps of k as bf16 with their scale (a float of which the exponent counts), for four MFMAs of 16.
+struct Wide {
+    bf16x8 v[4];
+};
+DEVI Wide widen(i32x8 q, int scale) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const float s = __uint_as_float((uint32_t)scale << 23);
+    Wide w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * i + e], s, false);
+            const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * i + e], s, true);
+            w.v[i][4 * e] = lo[0];
+            w.v[i][4 * e + 1] = lo[1];
+            w.v[i][4 * e + 2] = hi[0];
+            w.v[i][4 * e + 3] = hi[1];
+        }
+    return w;
+}
+
+DEVI f32x16 product(const Wide &a, const Wide &b, f32x16 acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], acc, 0, 0, 0);
+    return acc;
+}
+
+DEVI f32x4 product16(const Wide &a, const Wide &b, f32x4 acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], acc, 0, 0, 0);
+    return acc;
+}
+
+DEVI void biases(const F8Args &a, int c, float (&cb)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cb[e] = a.c_bias ? a.c_bias[c + e < a.NC ? c + e : a.NC - 1] : 0.0f;
+}
+
+// The sums of eight columns of row r, stored as they are (split) or finished.
+template <int OD, bool STREAM = false>
+DEVI void finish8(const F8Args &a, int split, int r, int c, const float (&sum)[8], const float (&cb)[8], float rb) {
+    if (a.part && split >= 0) {
+        float *dst = a.part + ((long long)split * a.NR + r) * a.NC + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.NC) dst[e] = sum[e];
+        return;
+    }
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = sum[e] + (cb[e] + rb);
+    store_row8<OD, STREAM>(a.y, a.row, a.len, a.fd_len, a.NC, a.NR, r, c, v);
+}
+
+// ------------------------------------------------------------------ tiles
+//
+// A work-group of WC x WR waves computes a (WC*FC*32) x (WR*FR*32) tile, a wave FC x FR blocks of 32 x 32; 128 steps
+// of k of every row, one block of the scales, are a stage in LDS.  A row's eight 16-byte pieces are stored at piece ^ (row / 2 & 7).
+template <int WC, int WR, int FC, int FR, int ST>
+struct Tile {
+    static constexpr int kWaves = WC * WR, kThreads = 64 * kWaves;
+    static constexpr int C = WC * FC * 32, R = WR * FR * 32;
+    static constexpr int kBytes = (C + R) * 128;
+    static constexpr bool kAhead = FC * FR >= 8;
+    static constexpr int kRowsPerLoad = kWaves * 8, kLoads = (C + R) / kRowsPerLoad;   // per wave and stage
+
+    struct Src {
+        rsrc_t rc, rr;
+        uint32_t oc[C / kRowsPerLoad], orr[R / kRowsPerLoad];
+    };
+
+    static DEVI void source(const F8Args &a, int c0, int r0, Src &s) {
+        const int row = threadIdx.x >> 3, piece = (threadIdx.x & 7) ^ (row >> 1 & 7);
+        s.rc = make_rsrc(a.c + (long long)c0 * a.K, 0x7fffffffu);
+        s.rr = make_rsrc(a.r + (long long)r0 * a.K, 0x7fffffffu);
+        // rows past the end read the last row; their results are not stored
+#pragma unroll
+        for (int i = 0; i < C / kRowsPerLoad; ++i) {
+            const int at = i * kRowsPerLoad + row;
+            s.oc[i] = (uint32_t)(c0 + at < a.NC ? at : a.NC - 1 - c0) * a.K + piece * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < R / kRowsPerLoad; ++i) {
+            const int at = i * kRowsPerLoad + row;
+            s.orr[i] = (uint32_t)(r0 + at < a.NR ? at : a.NR - 1 - r0) * a.K + piece * 16;
+        }
+    }
+
+    // Part 0 of a stage's loads is axis C's, part 1 axis R's.
+    static DEVI void load_axis(const Src &s, char *lds, int k, int part) {
+        const int wave = uniform(threadIdx.x >> 6);
+        if (part == 0) {
+#pragma unroll
+            for (int i = 0; i < C / kRowsPerLoad; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rc, (lds_void *)(lds + (i * kWaves + wave) * 1024), 16,
+                                                         s.oc[i], k, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R / kRowsPerLoad; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rr, (lds_void *)(lds + C * 128 + (i * kWaves + wave) * 1024),
+                                                         16, s.orr[i], k, 0, 0);
+        }
+    }
+
+    // A lane's scales of the block from k on: of its row in each of the wave's blocks.
+    struct Scales {
+        int c[FC], r[FR];
+    };
+
+    static DEVI void scales(const F8Args &a, int c0, int r0, int k, Scales &s) {
+        const int wave = uniform(threadIdx.x >> 6), wc = wave % WC, wr = wave / WC, row = again(threadIdx.x & 31);
+        const unsigned char *pc = a.c_scale + (long long)(k >> 7) * a.NC, *pr = a.r_scale + (long long)(k >> 7) * a.NR;
+#pragma unroll
+        for (int i = 0; i < FC; ++i) {
+            const int at = c0 + (wc * FC + i) * 32 + row;
+            s.c[i] = pc[(uint32_t)(at < a.NC ? at : a.NC - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < FR; ++j) {
+            const int at = r0 + (wr * FR + j) * 32 + row;
+            s.r[j] = pr[(uint32_t)(at < a.NR ? at : a.NR - 1)];
+        }
+    }
+
+    // A lane's operand of half h of the stage's 128 steps: block i of axis C, block j of axis R.
+    static DEVI i32x8 take(const char *row, int h) {
+        const int lane = threadIdx.x & 63, p = h * 4 + (lane >> 5) * 2, mix = lane >> 1 & 7;
+        return join(*(const i32x4 *)(row + ((p ^ mix) * 16)), *(const i32x4 *)(row + (((p + 1) ^ mix) * 16)));
+    }
+    static DEVI i32x8 take_c(const char *lds, int h, int i) {
+        const int wave = threadIdx.x >> 6, wc = wave % WC;
+        return take(lds + ((wc * FC + i) * 32 + (threadIdx.x & 31)) * 128, h);
+    }
+    static DEVI i32x8 take_r(const char *lds, int h, int j) {
+        const int wave = threadIdx.x >> 6, wr = wave / WC;
+        return take(lds + C * 128 + ((wr * FR + j) * 32 + (threadIdx.x & 31)) * 128, h);
+    }
+};
+
+template <int OD, int WC, int WR, int FC, int FR, int ST, bool STREAM>
+__global__ __launch_bounds__(64 * WC * WR) void f8_tile_kernel(F8Args a) {
+    typedef Tile<WC, WR, FC, FR, ST> X;
+    __shared__ __attribute__((aligned(1024))) char stages[ST * X::kBytes];
+    // each XCD a contiguous range of tiles, in columns of eight C tiles
+    const int per_split = a.tiles_c * a.tiles_r, split = blockIdx.x / per_split;
+    const int t = xcd_remap(blockIdx.x - split * per_split, per_split);
+    const int band = t / (8 * a.tiles_r), in_band = t - band * 8 * a.tiles_r;
+    const int wide = a.tiles_c - band * 8 < 8 ? a.tiles_c - band * 8 : 8;
+    const int c0 = (band * 8 + in_band % wide) * X::C, r0 = (in_band / wide) * X::R;
+    typename X::Src src;
+    X::source(a, c0, r0, src);
+    f32x16 acc[FC][FR];
+#pragma unroll
+    for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int j = 0; j < FR; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    const int first = split * a.k_split, end = first + a.k_split < a.K ? first + a.k_split : a.K;
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+        if (first + i * 128 < end) {
+            X::load_axis(src, stages + i * X::kBytes, first + i * 128, 0);
+            X::load_axis(src, stages + i * X::kBytes, first + i * 128, 1);
+        }
+    static_assert(!X::kAhead || FC % 2 == 0, "a stage ends on the second of two operands");
+    typename X::Scales now;
+    X::scales(a, c0, r0, first, now);
+    if constexpr (X::kAhead && OD == 1) {
+        // Operands are read one block of axis C ahead of the products, over the end of the stage: before its last
+        // block's products the next stage must have arrived and every wave have read this one, whose place the stage
+        // after next takes.  One half of its loads is issued there, the other with the next stage's first block.
+        char *in = stages, *to = stages + X::kBytes;
+        const auto arrived = [] {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __syncthreads();
+        };
+        typename X::Scales next = now;
+        i32x8 r[2][FR], x[2];
+        if (first + 128 < end) X::load_axis(src, to, first + 128, 0);
+        arrived();
+#pragma unroll
+        for (int j = 0; j < FR; ++j) r[0][j] = X::take_r(in, 0, j);
+        x[0] = X::take_c(in, 0, 0);
+        const auto step = [&](int h, int i) {
+#pragma unroll
+            for (int j = 0; j < FR; ++j) acc[i][j] = product(x[(h * FC + i) & 1], r[h][j], acc[i][j], now.c[i], now.r[j]);
+        };
+        // the stage's blocks but the last, each after the next one's read
+        const auto stage = [&] {
+#pragma unroll
+            for (int s = 0; s < 2 * FC - 1; ++s) {
+                if (s == FC - 2) {
+#pragma unroll
+                    for (int j = 0; j < FR; ++j) r[1][j] = X::take_r(in, 1, j);
+                }
+                x[(s + 1) & 1] = X::take_c(in, (s + 1) / FC, (s + 1) % FC);
+                step(s / FC, s % FC);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        for (int k = first + 128; k < end; k += 128) {
+            X::load_axis(src, to, k, 1);
+            X::scales(a, c0, r0, k, next);
+            __builtin_amdgcn_sched_barrier(0);
+            stage();
+            arrived();
+            if (k + 128 < end) X::load_axis(src, in, k + 128, 0);
+#pragma unroll
+            for (int j = 0; j < FR; ++j) r[0][j] = X::take_r(to, 0, j);
+            x[0] = X::take_c(to, 0, 0);
+            step(1, FC - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            now = next;
+            char *const was = in;
+            in = to;
+            to = was;
+        }
+        stage();
+        step(1, FC - 1);
+    } else {
+        int at = 0, fill = ST - 1;
+        for (int k = first; k < end; k += 128) {
+            // this stage has arrived (each wave waits for its own loads, of which those of the ST - 2 stages after it
+            // may be in flight), and the stage before has been read
+            if (ST > 2 && k + (ST - 2) * 128 < end)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((ST - 2) * X::kLoads) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            typename X::Scales next = now;
+            if (k + 128 < end) X::scales(a, c0, r0, k + 128, next);
+            // after the scales: what a wait counts as the youngest are then tiles
+            if (k + (ST - 1) * 128 < end) {
+                X::load_axis(src, stages + fill * X::kBytes, k + (ST - 1) * 128, 0);
+                X::load_axis(src, stages + fill * X::kBytes, k + (ST - 1) * 128, 1);
+            }
+            const char *in = stages + at * X::kBytes;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (OD == 1) {
+                    i32x8 r[FR];
+#pragma unroll
+                    for (int j = 0; j < FR; ++j) r[j] = X::take_r(in, h, j);
+#pragma unroll
+                    for (int i = 0; i < FC; ++i) {
+                        const i32x8 x = X::take_c(in, h, i);
+#pragma unroll
+                        for (int j = 0; j < FR; ++j) acc[i][j] = product(x, r[j], acc[i][j], now.c[i], now.r[j]);
+                    }
+                } else {
+                    Wide r[FR];
+#pragma unroll
+                    for (int j = 0; j < FR; ++j) r[j] = widen(X::take_r(in, h, j), now.r[j]);
+#pragma unroll
+                    for (int i = 0; i < FC; ++i) {
+                        const Wide x = widen(X::take_c(in, h, i), now.c[i]);
+#pragma unroll
+                        for (int j = 0; j < FR; ++j) acc[i][j] = product(x, r[j], acc[i][j]);
+                    }
+                }
+            }
+            now = next;
+            at = at + 1 < ST ? at + 1 : 0;
+            fill = fill + 1 < ST ? fill + 1 : 0;
+        }
+    }
+    constexpr int kW = FC * 32, kMine = 32 * kW, kMix = kW >= 64 ? 15 : 7;
+    constexpr int kLanes = kW / 8;             // lanes per row of the output, eight columns each
+    const int thread = again(threadIdx.x);     // nothing made from it takes registers during the products
+    const int lane = thread & 63, wave = thread >> 6, wc = wave % WC, wr = wave / WC;
+    const int col = (lane % kLanes) * 8, c = c0 + wc * kW + col;
+    static_assert(FR <= 2, "one row's bias per lane");
+    float cb[8];
+    biases(a, c, cb);
+    const int rl = r0 + wr * FR * 32 + lane, rc = rl < a.NR ? rl : a.NR - 1;
+    const float rb = a.r_bias ? a.r_bias[rc] : 0.0f;
+    __syncthreads();
+    // Through LDS, 32 rows of the wave's FC*32 columns at a time, so that y is written in 16-byte pieces of
+    // consecutive lanes; a row's pieces are permuted as above.
+    static_assert(X::kWaves * kMine * 4 <= ST * X::kBytes, "the exchange fits the stages");
+    float *mine = (float *)stages + wave * kMine;
+#pragma unroll
+    for (int j = 0; j < FR; ++j) {
+        const int rw = r0 + (wr * FR + j) * 32;
+#pragma unroll
+        for (int i = 0; i < FC; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 four;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) four[e] = acc[i][j][g * 4 + e];
+                const int row = lane & 31, piece = (i * 8 + g * 2 + (lane >> 5)) ^ (row & kMix);
+                *(f32x4 *)(mine + row * kW + piece * 4) = four;
+            }
+        wave_lds_sync();
+#pragma unroll 2
+        for (int p = 0; p < 32 * kLanes / 64; ++p) {
+            const int row = p * (64 / kLanes) + lane / kLanes, r = rw + row;
+            const float rbr = __shfl(rb, j * 32 + row);
+            if (r >= a.NR || c >= a.NC) continue;
+            const f32x4 lo = *(const f32x4 *)(mine + row * kW + ((col >> 2) ^ (row & kMix)) * 4);
+            const f32x4 hi = *(const f32x4 *)(mine + row * kW + (((col >> 2) + 1) ^ (row & kMix)) * 4);
+            float sum[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[e] = lo[e];
+                sum[4 + e] = hi[e];
+            }
+            finish8<OD, STREAM>(a, split, r, c, sum, cb, rbr);
+        }
+        wave_lds_sync();
+    }
+}
+
+// Adds the splits' sums in their order and finishes them.
+template <int OD>
+__global__ __launch_bounds__(256) void f8_join_kernel(F8Args a, int splits) {
+    const int per_row = (a.NC + 7) / 8;
+    const long long n = (long long)a.NR * per_row;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row) * 8;
+        float sum[8] = {};
+        for (int z = 0; z < splits; ++z) {
+            const float *p = a.part + ((long long)z * a.NR + r) * a.NC + c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < a.NC) sum[e] += p[e];
+        }
+        float cb[8];
+        biases(a, c, cb);
+        finish8<OD>(a, -1, r, c, sum, cb, a.r_bias ? a.r_bias[r] : 0.0f);
+    }
+}
+
+// ------------------------------------------------------------------ few tokens
+//
+// With few tokens the weight's bytes count: each is read once, straight into registers, as the row operand of
+// 16x16x128 MFMAs, a block of the scales each.  A work-group takes 32 channels, its eight waves an eighth of the blocks each,
+// in turn, and adds the waves' sums in LDS.  FT blocks of 16 tokens.
+template <int OD, int FT>
+__global__ __launch_bounds__(512) void f8_few_kernel(const unsigned char *q, const unsigned char *wq, const unsigned char *qs,
+                                                     const unsigned char *ws, const float *bias, int T, int O, int K, int L,
+                                                     int channel_major, void *y, uint32_t first) {
+    __shared__ float red[8][32][FT * 16 + 1];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane & 15, kq = (lane >> 4) * 16;
+    const int n0 = (int)(first + blockIdx.x) * 32, blocks = K >> 7;
+    const unsigned char *pw[2], *pq[FT], *sw[2], *sq[FT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int n = n0 + i * 16 + row < O ? n0 + i * 16 + row : O - 1;
+        pw[i] = wq + (long long)n * K + kq;
+        sw[i] = ws + n;
+    }
+#pragma unroll
+    for (int i = 0; i < FT; ++i) {
+        const int m = i * 16 + row < T ? i * 16 + row : T - 1;
+        pq[i] = q + (long long)m * K + kq;
+        sq[i] = qs + m;
+    }
+    f32x4 acc[2][FT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    // the next block loads while this one is multiplied
+    i32x4 a[2][2], b[FT][2];
+    int as[2], bs[FT];
+    auto fetch = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a[i][0] = *(const i32x4 *)(pw[i] + k * 128);
+            a[i][1] = *(const i32x4 *)(pw[i] + k * 128 + 64);
+            as[i] = sw[i][(long long)k * O];
+        }
+#pragma unroll
+        for (int j = 0; j < FT; ++j) {
+            b[j][0] = *(const i32x4 *)(pq[j] + k * 128);
+            b[j][1] = *(const i32x4 *)(pq[j] + k * 128 + 64);
+            bs[j] = sq[j][(long long)k * T];
+        }
+    };
+    if (wave < blocks) fetch(wave);
+    for (int k = wave; k < blocks; k += 8) {
+        i32x8 a0[2], b0[FT];
+        int as0[2], bs0[FT];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a0[i] = join(a[i][0], a[i][1]);
+            as0[i] = as[i];
+        }
+#pragma unroll
+        for (int j = 0; j < FT; ++j) {
+            b0[j] = join(b[j][0], b[j][1]);
+            bs0[j] = bs[j];
+        }
+        if (k + 8 < blocks) fetch(k + 8);
+        if constexpr (OD == 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0[i], b0[j], acc[i][j], 0, 0, 0, as0[i], 0,
+                                                                                 bs0[j]);
+        } else {
+            const Wide w[2] = {widen(a0[0], as0[0]), widen(a0[1], as0[1])};
+#pragma unroll
+            for (int j = 0; j < FT; ++j) {
+                const Wide x = widen(b0[j], bs0[j]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[i][j] = product16(w[i], x, acc[i][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[wave][i * 16 + (lane >> 4) * 4 + e][j * 16 + row] = acc[i][j][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * FT * 16; i += 512) {
+        // token-major: consecutive lanes on consecutive channels
+        const int n = channel_major ? i / (FT * 16) : i & 31, m = channel_major ? i % (FT * 16) : i >> 5;
+        if (n0 + n >= O || m >= T) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += red[w][n][m];
+        if (bias) v += bias[n0 + n];
+        const int at_b = m / L;
+        const long long at = channel_major ? ((long long)at_b * O + n0 + n) * L + (m - at_b * L) : (long long)m * O + n0 + n;
+        ((typename Elem<OD>::T *)y)[at] = Elem<OD>::put(v);
+    }
+}
+
+template <int OD, int FT>
+int few(int T, int O, int K, int L, const unsigned char *q, const unsigned char *qs, const unsigned char *wq,
+        const unsigned char *ws, const float *bias, int channel_major, void *y, hipStream_t st) {
+    return launch_groups(((long long)O + 31) / 32, 512, [&](unsigned n, unsigned first) {
+        hipLaunchKernelGGL((f8_few_kernel<OD, FT>), dim3(n), dim3(512), 0, st, q, wq, qs, ws, bias, T, O, K, L, channel_major,
+                           y, first);
+    });
+}
+
+template <int OD, int WC, int WR, int FC, int FR, int ST, bool STREAM = false>
+int tiled(F8Args a, int splits, hipStream_t st) {
+    typedef Tile<WC, WR, FC, FR, ST> X;
+    a.tiles_c = (a.NC + X::C - 1) / X::C;
+    a.tiles_r = (a.NR + X::R - 1) / X::R;
+    if (splits == 1) a.part = nullptr;
+    a.k_split = ((a.K / 128 + splits - 1) / splits) * 128;
+    hipLaunchKernelGGL((f8_tile_kernel<OD, WC, WR, FC, FR, ST, STREAM>),
+                       dim3((unsigned)((long long)a.tiles_c * a.tiles_r * splits)), dim3(X::kThreads), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    if (splits > 1) {
+        const long long blocks = ((long long)a.NR * ((a.NC + 7) / 8) + 255) / 256;
+        hipLaunchKernelGGL(f8_join_kernel<OD>, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, a, splits);
+        if (hipGetLastError() != hipSuccess) return MICONV_ERR_HIP;
+    }
+    return MICONV_OK;
+}
+
+constexpr int kFewTokens = 64;
+
+long long tile_count(long long T, long long O, int side) {
+    return ((T + side - 1) / side) * ((O + side - 1) / side);
+}
+
+// Side of the square tile: the largest that gives most of the 256 CUs a tile.
+int tile_side(int T, int O) {
+    if (tile_count(T, O, 256) >= 140) return 256;
+    if (tile_count(T, O, 128) >= 140) return 128;
+    return 64;
+}
+
+}  // namespace
+
+// Splits of k, for deep products of few tiles, each at least 2048 deep.
+int f8_splits(int T, int O, int K, size_t budget) {
+    if (T <= kFewTokens || K < 8192) return 1;
+    const long long tiles = tile_count(T, O, tile_side(T, O));
+    long long s = 160 / tiles;
+    if (s > K / 2048) s = K / 2048;
+    if (s > 16) s = 16;
+    const size_t one = (size_t)T * O * 4;
+    if (s > (long long)(budget / one)) s = (long long)(budget / one);
+    if (s < 2) return 1;
+    const int steps = K / 128, per = (int)((steps + s - 1) / s);
+    return (steps + per - 1) / per;            // no empty split
+}
+
+F8Form f8_form(int T, int O, int K, int splits) {
+    if (T <= kFewTokens) return {T <= 16 ? 1 : (T <= 32 ? 2 : 4), 0, 0};
+    const int side = tile_side(T, O);
+    const bool four = side == 64 || (side == 128 && tile_count(T, O, 128) * splits <= 256 && K >= 4096);
+    return {0, side, four ? 4 : 2};
+}
+
+template <int OD>
+static int f8_by_form(const F8Args &a, const F8Form &f, bool stream, int splits, hipStream_t st) {
+    switch (f.side) {
+        case 256:
+            if (stream) return tiled<OD, 2, 4, 4, 2, 2, OD == 1>(a, splits, st);
+            return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
+        case 128:
+            if (f.stages == 4) return tiled<OD, 4, 2, 1, 2, 4>(a, splits, st);
+            return tiled<OD, 4, 2, 1, 2, 2>(a, splits, st);
+        default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);
+    }
+}
+
+int launch_matmul_f8(int B, int L, int O, int K, const unsigned char *q, const unsigned char *qs, const unsigned char *wq,
+                     const unsigned char *ws, const float *bias, int channel_major, int out_dtype, void *y, int splits,
+                     float *part, hipStream_t st) {
+    const int T = B * L;
+    const F8Form f = f8_form(T, O, K, splits);
+    if (f.few) {
+#define MICONV_FEW(FT)                                                                            \
+    (out_dtype ? few<1, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st)                \
+               : few<0, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st))
+        return f.few == 1 ? MICONV_FEW(1) : (f.few == 2 ? MICONV_FEW(2) : MICONV_FEW(4));
+#undef MICONV_FEW
+    }
+    F8Args a = {};
+    a.K = K;
+    a.y = y;
+    a.part = part;
+    if (channel_major) {
+        a.c = q; a.c_scale = qs; a.NC = T;
+        a.r = wq; a.r_scale = ws; a.NR = O; a.r_bias = bias;
+        a.row = T;
+        a.len = B > 1 ? L : 0;
+        a.fd_len = make_fdiv((uint32_t)L);
+    } else {
+        a.c = wq; a.c_scale = ws; a.NC = O; a.c_bias = bias;
+        a.r = q; a.r_scale = qs; a.NR = T;
+        a.row = O;
+    }
+    const bool stream = streams(out_dtype, (size_t)T * O);
+    return out_dtype ? f8_by_form<1>(a, f, stream, splits, st) : f8_by_form<0>(a, f, stream, splits, st);
+}
+
+}  // namespace miconv

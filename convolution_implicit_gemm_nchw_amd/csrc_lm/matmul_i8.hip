@@ -12,6 +12,7 @@
 #include "device.h"
 #include "ssm.h"
 #include "ssm_device.h"
+#include "tile_store.h"
 
 namespace miconv {
 
@@ -45,25 +46,7 @@ DEVI float scaled(const I8Args &a, int sum, float cs, float rs) {
 // Eight consecutive values of one row of y from c0 on.
 template <int OD, bool STREAM>
 DEVI void put8(const I8Args &a, int r, int c0, const float (&v)[8]) {
-    typedef typename Elem<OD>::T T;
-    T *y = (T *)a.y;
-    if (a.len == 0) {
-        store8<OD, STREAM>(y + (long long)r * a.row, c0, a.NC, v);
-        return;
-    }
-    const int b = (int)fdiv((uint32_t)c0, a.fd_len), l = c0 - b * a.len;
-    T *line = y + ((long long)b * a.NR + r) * a.len;
-    if (l + 8 <= a.len) {
-        store8<OD, STREAM>(line, l, a.len, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = c0 + i;
-        if (c >= a.NC) break;
-        const int bi = (int)fdiv((uint32_t)c, a.fd_len);
-        y[((long long)bi * a.NR + r) * a.len + (c - bi * a.len)] = Elem<OD>::put(v[i]);
-    }
+    store_row8<OD, STREAM>(a.y, a.row, a.len, a.fd_len, a.NC, a.NR, r, c0, v);
 }
 
 // Scales and biases of eight columns.

@@ -615,6 +615,32 @@ int matmul_i8_workspace_size(int B, int L, int O, int C_pad, size_t workspace_li
 int matmul_i8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, char *buf, size_t buflen);
 
 /*
+ * Products in 8-bit floating point (e4m3) with a power of two for each token, or channel, and block of 128.
+ *
+ * quantize_f8: x as for quantize_tokens.  For each token and block of 128 channels, with m = max |x| over it:
+ *   scale = the least 2^e, e >= -127, with m <= 448 * 2^e,   q = x / scale rounded to nearest, ties to even
+ * q is [B*L][C_pad] (e4m3 bits), C_pad = C rounded up to a multiple of 128, the padding 0;
+ * scale is [C_pad / 128][B*L], e + 127 (e8m0 bits).  A block that holds an infinity or a NaN gets the scale's NaN,
+ * 255, and NaN for each q.  A weight [O][C] is quantised in the same way; its transpose or a
+ * gradient's, for the products of a backward pass, through the strides.
+ */
+int quantize_f8(int B, int L, int C, int dtype, const void *x, long long stride_b, long long stride_l,
+                long long stride_c, unsigned char *q, unsigned char *scale, void *stream);
+/*
+ * matmul_f8: for token m = b*L + l and channel n
+ *   y = sum over blocks j of 2^(qscale[j][m] - 127 + wscale[j][n] - 127) sum_{k in j} q[m][k] * wq[n][k]  (+ bias[n])
+ * q [B*L][C_pad], wq [O][C_pad], 16-byte aligned, C_pad a multiple of 128 and at most 131072; qscale
+ * [C_pad / 128][B*L], wscale [C_pad / 128][O]; a scale of 255 makes the token's, or channel's, y NaN.
+ * y, out_dtype and the workspace as for matmul_i8.  Sums are fp32; y is rounded once.
+ */
+int matmul_f8(int B, int L, int O, int C_pad, const unsigned char *q, const unsigned char *qscale,
+              const unsigned char *wq, const unsigned char *wscale, const float *bias, int channel_major, int out_dtype,
+              void *y, void *workspace, size_t workspace_bytes, void *stream);
+int matmul_f8_workspace_size(int B, int L, int O, int C_pad, size_t workspace_limit, size_t *bytes_out);
+/* One-line description of the kernel a call runs (few tokens, or tile, stages and splits). */
+int matmul_f8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, char *buf, size_t buflen);
+
+/*
  * Gated delta rule: a linear attention whose state [P][V] per head forgets by a
  * gate and corrects what it holds for a key.  q, k [B][Hk*P][L] (head hk's
  * channels hk*P ..), v, y [B][Hv*V][L], value head h reading query and key of
