@@ -42,10 +42,10 @@ struct DeltaSlice {
 };
 
 // Places in the workspace, in bytes.  Matrices are stored in the order in which a wave's lanes take
-// the row operand of 16x16x32 MFMAs: [row tile of 16][32 columns][lane][8], a plane of bf16 after the other.
+// the row operand of 16x16x32 MFMAs: [row tile of 16][32 columns][lane][8].
 struct DeltaWork {
-    size_t k, q, kt;                       // k [t][p], q [t][p] (forward) or q^T (backward), k^T [p][t]
-    size_t inv, attn;                      // the inverse and (D * q k^T), transposed in the backward pass
+    size_t k, q;                           // k and (forward) q, [t][p], a plane of bf16 after the other
+    size_t inv, attn;                      // the inverse and (D * q k^T), fp32, transposed in the backward pass
     size_t steps;                          // DeltaSteps
     size_t state;                          // [nb][Hv][Pp][Vp] fp32: carried between slices of time
     size_t F, after;                       // backward: [chunk][Vp][64], [chunk][Pp][Vp] fp32

@@ -17,12 +17,11 @@ DeltaWork delta_work(const miconv_gated_delta_t &d, int dtype, const DeltaSlice 
     };
     const size_t chunks = (size_t)s.nb * s.nc, heads = chunks * d.Hv, DK = delta_key_pad(d.P), Vp = delta_value_pad(d.V);
     const size_t operand = chunks * d.Hk * (dtype == MICONV_BF16 ? 1 : 3) * kDeltaChunk * DK * 2;
-    const size_t square = kDeltaChunk * kDeltaChunk * 2;
+    const size_t square = kDeltaChunk * kDeltaChunk * 4;
     take(&w.k, operand);
-    take(&w.q, operand);
-    take(&w.kt, operand);
-    take(&w.inv, heads * 3 * square);
-    take(&w.attn, heads * (!backward && dtype == MICONV_BF16 ? 2 : 3) * square);
+    if (!backward) take(&w.q, operand);
+    take(&w.inv, heads * square);
+    take(&w.attn, heads * square);
     take(&w.steps, heads * sizeof(DeltaSteps));
     if (backward) {
         take(&w.F, heads * Vp * kDeltaChunk * 4);

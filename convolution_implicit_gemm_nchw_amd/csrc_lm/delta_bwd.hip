@@ -66,9 +66,9 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
     constexpr int kPlaneK = 64 * DK * 2;
     // three planes of 256 key channels are more than the registers hold ahead of their use
     constexpr bool kLate = TI == 3 && DK == 256;
-    u32x4 fk[kKS][TI], ft[kMT][2][TI], fq[kMT][2][TI], fi[2][3], fa[2][3];
-    u32x4 raw[NT][2][TI];                      // dy as column operand: 8 steps from ks * 32 + grp * 8 on
-    float scaled[NT][2][8];                    // and times e q's factor
+    u32x4 fk[kKS][TI];
+    Raw8<DT> ft[kMT][2], fq[kMT][2], fg[NT][2];   // k^T, q^T and, as column operand, dy
+    Eight fi[2], fa[2], feq[2];                // feq: the queries' factors of the steps that fg holds
     f32x4 vek, vfk, vbeta;
     float last = 0.0f;
     const T *grow[NT];
@@ -84,25 +84,44 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
         for (int ks = 0; ks < kKS; ++ks)
             fragment<TI>(a.ws + a.w.k + of_k + c * step_k, wave * kKS + ks, kPlaneK, fk[ks]);
     };
-    const auto load_turned = [&](int c) {
+    const T *krow[kMT], *qrow[kMT];
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) {
+        const int p = (wave * kMT + i) * 16 + col, at = hk * a.d.P + (p < a.d.P ? p : 0);
+        krow[i] = row_of<DT>(a.d.k, B, at);
+        qrow[i] = row_of<DT>(a.d.q, B, at);
+    }
+    const auto turned = [&](const T *row, int c, int ks, bool whole) {
+        return steps8<DT>(row, whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+    };
+    const auto load_turned = [&](int c, bool whole) {
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                fragment<TI>(a.ws + a.w.q + of_k + c * step_k, (wave * kMT + i) * 2 + ks, kPlaneK, fq[i][ks]);
-                fragment<TI>(a.ws + a.w.kt + of_k + c * step_k, (wave * kMT + i) * 2 + ks, kPlaneK, ft[i][ks]);
+                ft[i][ks] = turned(krow[i], c, ks, whole);
+                fq[i][ks] = turned(qrow[i], c, ks, whole);
             }
     };
     // both are upper triangular: the first 32 columns of rows from 32 on are zero and not stored
-    const auto load_solve = [&](int c) {
-        const char *i = a.ws + a.w.inv + (of_v + (size_t)c * a.d.Hv) * 3 * 8192;
-        const char *at = a.ws + a.w.attn + (of_v + (size_t)c * a.d.Hv) * 3 * 8192;
-        if (wave < 2) {
-            fragment<3>(i, wave * 2, 8192, fi[0]);
-            fragment<3>(at, wave * 2, 8192, fa[0]);
-        }
-        fragment<3>(i, wave * 2 + 1, 8192, fi[1]);
-        fragment<3>(at, wave * 2 + 1, 8192, fa[1]);
+    const Eight nothing = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    fi[0] = fa[0] = nothing;
+    const auto load_inverse = [&](int c) {
+        const char *i = a.ws + a.w.inv + (of_v + (size_t)c * a.d.Hv) * 16384;
+        if (wave < 2) fi[0] = fragment32(i, wave * 2);
+        fi[1] = fragment32(i, wave * 2 + 1);
+    };
+    const auto load_attn = [&](int c) {
+        const char *at = a.ws + a.w.attn + (of_v + (size_t)c * a.d.Hv) * 16384;
+        if (wave < 2) fa[0] = fragment32(at, wave * 2);
+        fa[1] = fragment32(at, wave * 2 + 1);
+    };
+    const auto load_dy = [&](int c, bool whole) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                fg[n][ks] = steps8<DT>(grow[n], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
     };
     const auto load_steps = [&](int c) {
         const DeltaSteps *s = (const DeltaSteps *)(a.ws + a.w.steps + (of_v + (size_t)c * a.d.Hv) * sizeof(DeltaSteps));
@@ -112,26 +131,19 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
         last = s->last;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            const f32x4 lo = *(const f32x4 *)(s->eq + ks * 32 + grp * 8), hi = *(const f32x4 *)(s->eq + ks * 32 + grp * 8 + 4);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float g[8];
-                load8<DT>(grow[n], steps_first + c * kDeltaChunk + ks * 32 + grp * 8,
-                          v0 + n * 16 + col < a.d.V ? valid : 0, g);
-                split8<TI>(g, raw[n][ks]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    scaled[n][ks][e] = g[e] * lo[e];
-                    scaled[n][ks][4 + e] = g[4 + e] * hi[e];
-                }
-            }
+            const f32x4 *eq = (const f32x4 *)(s->eq + ks * 32 + grp * 8);
+            feq[ks] = {eq[0], eq[1]};
         }
     };
+    // as in the forward scan; here the chunk that ends inside comes first
+    int full = (valid - steps_first) / kDeltaChunk;
+    full = valid <= steps_first ? 0 : (full < chunks ? full : chunks);
     if (chunks) {
         load_k(chunks - 1);
-        load_solve(chunks - 1);
-        load_steps(chunks - 1);
-        if constexpr (!kLate) load_turned(chunks - 1);
+        load_attn(chunks - 1);
+        load_inverse(chunks - 1);
+        load_dy(chunks - 1, full == chunks);
+        if constexpr (!kLate) load_turned(chunks - 1, full == chunks);
     }
     // chunks past the sequence's end
     for (int c = chunks; c < a.s.nc; ++c) {
@@ -139,11 +151,16 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             if (v0 + n * 16 + col < a.d.V)
-                store4_until<DT>(out[n], steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+                store4_until<DT>(out[n], steps_first + (c + 1) * kDeltaChunk <= a.d.L, steps_first + c * kDeltaChunk + mine,
+                                 a.d.L, zeros);
     }
-    for (int c = chunks - 1; c >= 0; --c) {
+    const auto chunk = [&](const int c, auto is_full) {
+        constexpr bool FULL = decltype(is_full)::value;
+        const int next = c ? c - 1 : 0;
+        const bool whole = FULL || c;          // of the next chunk's loads, or again the same
         const size_t at = of_v + (size_t)c * a.d.Hv;
         float *after = (float *)(a.ws + a.w.after) + at * DK * a.Vp, *Fout = (float *)(a.ws + a.w.F) + at * a.Vp * kDeltaChunk;
+        load_steps(c);                         // ahead of the stores: loads come back in their order, stores among them
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -151,65 +168,101 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     after[(size_t)((wave * kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
+        f32x4 back[NT];
+        {
+            u32x4 a0[3], a1[3];
+            planes_of<3>(fa[0], a0);
+            planes_of<3>(fa[1], a1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                Sums<2> sum;
+                u32x4 g[TI];
+                planes_of<DT>(only<DT>(fg[n][0], v0 + n * 16 + col < a.d.V), g);
+                sum.add(a0, g);
+                planes_of<DT>(only<DT>(fg[n][1], v0 + n * 16 + col < a.d.V), g);
+                sum.add(a1, g);
+                back[n] = sum.total();
+            }
+        }
+        load_attn(next);
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            f32x4 kd = {0, 0, 0, 0}, back = {0, 0, 0, 0};
-            if (wave < 2) multiply<3, TI, 2>(fa[0], raw[n][0], back);
-            multiply<3, TI, 2>(fa[1], raw[n][1], back);
+            Sums<2> kd;
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks) {
                 u32x4 s[3];
                 get_planes<3>(Sp + (n * 16 + col) * kPitchS + ks * 32 + grp * 8, kPlaneS, s);
-                multiply<TI, 3, 2>(fk[ks], s, kd);
+                kd.add(fk[ks], s);
             }
+            const f32x4 k = kd.total();
             float du[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], kd[r], back[r]);
+            for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], k[r], back[n][r]);
             put_planes<3>(Up + (n * 16 + col) * kPitchT + mine, kPlaneT, du);
         }
-        if (c) load_k(c - 1);
+        load_k(next);
         __syncthreads();
+        {
+            u32x4 i0[3], i1[3];
+            planes_of<3>(fi[0], i0);
+            planes_of<3>(fi[1], i1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            f32x4 F = {0, 0, 0, 0};
-            u32x4 u[3];
-            const uint16_t *from = Up + (n * 16 + col) * kPitchT + grp * 8;
-            if (wave < 2) {
+            for (int n = 0; n < NT; ++n) {
+                Sums<2> sum;
+                u32x4 u[3];
+                const uint16_t *from = Up + (n * 16 + col) * kPitchT + grp * 8;
                 get_planes<3>(from, kPlaneT, u);
-                multiply<3, 3, 2>(fi[0], u, F);
-            }
-            get_planes<3>(from + 32, kPlaneT, u);
-            multiply<3, 3, 2>(fi[1], u, F);
-            *(f32x4 *)(Fout + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = F;
-            float w[4], dv[4];
+                sum.add(i0, u);
+                get_planes<3>(from + 32, kPlaneT, u);
+                sum.add(i1, u);
+                const f32x4 F = sum.total();
+                *(f32x4 *)(Fout + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = F;
+                float w[4], dv[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                dv[r] = vbeta[r] * F[r];
-                w[r] = -(vek[r] * dv[r]);
-            }
-            put_planes<3>(Wp + (n * 16 + col) * kPitchT + mine, kPlaneT, w);
-            if (v0 + n * 16 + col < a.d.V) {
-                const int t = steps_first + c * kDeltaChunk + mine;
+                for (int r = 0; r < 4; ++r) {
+                    dv[r] = vbeta[r] * F[r];
+                    w[r] = -(vek[r] * dv[r]);
+                }
+                put_planes<3>(Wp + (n * 16 + col) * kPitchT + mine, kPlaneT, w);
+                if (v0 + n * 16 + col < a.d.V) {
+                    const int t = steps_first + c * kDeltaChunk + mine;
+                    if constexpr (!FULL) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dv[r] = t + r < valid ? dv[r] : 0.0f;
-                store4_until<DT>(out[n], t, a.d.L, dv);
+                        for (int r = 0; r < 4; ++r) dv[r] = t + r < valid ? dv[r] : 0.0f;
+                    }
+                    store4_until<DT>(out[n], FULL, t, a.d.L, dv);
+                }
             }
         }
-        if (c) load_solve(c - 1);
-        if constexpr (kLate) load_turned(c);
+        load_inverse(next);
+        // dS: what the queries give needs none of the above
+        u32x4 g[NT][2][3];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < kMT; ++i) S[i][n] *= last;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                u32x4 g[3];
-                split8<3>(scaled[n][ks], g);
+                float x[8];
+                widen8<DT>(only<DT>(fg[n][ks], v0 + n * 16 + col < a.d.V), x);
 #pragma unroll
-                for (int i = 0; i < kMT; ++i) multiply<TI, 3, 2>(fq[i][ks], g, S[i][n]);
+                for (int e = 0; e < 4; ++e) {
+                    x[e] *= feq[ks].lo[e];
+                    x[4 + e] *= feq[ks].hi[e];
+                }
+                split8<3>(x, g[n][ks]);
             }
-        }
+        load_dy(next, FULL || whole);
+        Sums<2> sum[kMT][NT];
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                if constexpr (kLate) fq[i][ks] = turned(qrow[i], c, ks, FULL);
+                u32x4 q[TI];
+                planes_of<DT>(only<DT>(fq[i][ks], (wave * kMT + i) * 16 + col < a.d.P), q);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) sum[i][n].add(q, g[n][ks]);
+            }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -218,14 +271,22 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
                 u32x4 w[3];
                 get_planes<3>(Wp + (n * 16 + col) * kPitchT + ks * 32 + grp * 8, kPlaneT, w);
 #pragma unroll
-                for (int i = 0; i < kMT; ++i) multiply<TI, 3, 2>(ft[i][ks], w, S[i][n]);
+                for (int i = 0; i < kMT; ++i) {
+                    if constexpr (kLate) ft[i][ks] = turned(krow[i], c, ks, FULL);
+                    u32x4 k[TI];
+                    planes_of<DT>(only<DT>(ft[i][ks], (wave * kMT + i) * 16 + col < a.d.P), k);
+                    sum[i][n].add(k, w);
+                }
             }
-        if (c) {
-            if constexpr (!kLate) load_turned(c - 1);
-            load_steps(c - 1);
-        }
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * last + sum[i][n].total();
+        if constexpr (!kLate) load_turned(next, FULL || whole);
         put_state();
-    }
+    };
+    if (full < chunks) chunk(full, Whole<false>());
+    for (int c = full - 1; c >= 0; --c) chunk(c, Whole<true>());
     {
         float *to = a.first ? a.d.d_initial_state : state_out;
         const int P = a.first ? a.d.P : DK, V = a.first ? a.d.V : a.Vp;
@@ -284,6 +345,7 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
     const int id = a.more + blockIdx.x;
     const int hk = id % a.d.Hk, bc = id / a.d.Hk, c = bc % a.s.nc, b = bc / a.s.nc, B = a.s.b0 + b;
     const int t0 = (a.s.c0 + c) * kDeltaChunk, valid = valid_steps(a.d.lengths, B, a.d.L), end = valid - t0;
+    const bool whole = end >= kDeltaChunk;
     const int stop = a.d.L - t0 < kDeltaChunk ? a.d.L - t0 : kDeltaChunk;     // steps of this chunk in the tensors
     if (end <= 0) {                            // a chunk past the sequence's end
         for (int i = tid; i < a.d.P * kDeltaChunk; i += X::kThreads) {
@@ -338,23 +400,19 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
             if (v0) __syncthreads();           // the channels before are used up
             // blocks of 4 steps x 8 channels: Z, F, dy
             for (int i = again(tid); i < 3 * 128; i += X::kThreads) {
-                const int which = i >> 7, t = (i & 15) * 4, v = v0 + (i >> 4 & 7) * 8;
+                const int which = uniform(i >> 7), t = (i & 15) * 4, v = v0 + (i >> 4 & 7) * 8;
                 float x[8][4];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
+                    const bool in = v + k < (which == 2 ? a.d.V : a.Vp);
                     if (which == 2) {
-                        if (v + k < a.d.V) {
-                            load4_until<DT>(row_of<DT>(a.d.dy, B, h * a.d.V + v + k) + t0, t, end, x[k]);
-                            continue;
-                        }
-                    } else if (v + k < a.Vp) {
-                        const f32x4 s = *(const f32x4 *)((which ? Fs : Zs) + (size_t)(v + k) * kDeltaChunk + t);
+                        const T *row = row_of<DT>(a.d.dy, B, h * a.d.V + (in ? v + k : 0)) + t0;
+                        widen4<DT>(steps4<DT>(row, whole, t, end), in, x[k]);
+                    } else {
+                        const f32x4 s = *(const f32x4 *)((which ? Fs : Zs) + (size_t)(in ? v + k : 0) * kDeltaChunk + t);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[k][r] = s[r];
-                        continue;
+                        for (int r = 0; r < 4; ++r) x[k][r] = in ? s[r] : 0.0f;
                     }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) x[k][r] = 0.0f;
                 }
                 uint16_t *to = shared + which * 3 * X::kPlane + t * X::kPitch + (v - v0);
 #pragma unroll
@@ -429,14 +487,13 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
             f[tid] = exp_any((float)(steps.G[63] - steps.G[tid]));
         }
         __syncthreads();                       // and the products have left the planes
+        settle();
         ends *= steps.last;
         // the rows' factors; the chunk's end reaches its decays through the last of them
         // four steps of a channel of key or query
         const auto four = [&](const miconv_rows_t &rows, int d, int t, float (&v)[4]) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = 0.0f;
             const int at = again(d);
-            if (at < a.d.P) load4_until<DT>(row_of<DT>(rows, B, hk * a.d.P + at) + t0, t, end, v);
+            widen4<DT>(steps4<DT>(row_of<DT>(rows, B, hk * a.d.P + (at < a.d.P ? at : 0)) + t0, whole, t, end), at < a.d.P, v);
         };
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -499,15 +556,15 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
             put_planes<3>(Ma + cj * X::kPitch + mi * 16 + row4, X::kPlane, aw);
         }
         __syncthreads();
-        const size_t of_k = ((size_t)bc * a.d.Hk + hk) * TI * 64 * DK * 2;
-        constexpr int kPlaneK = 64 * DK * 2;
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
+            const int d = again(d0 + n * 16), row = hk * a.d.P + (d < a.d.P ? d : 0);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
+                const int t = ks * 32 + grp * 8;
                 u32x4 fk[TI], fq[TI];
-                fragment<TI>(a.ws + a.w.kt + of_k, (wave * NC + n) * 2 + ks, kPlaneK, fk);
-                fragment<TI>(a.ws + a.w.q + of_k, (wave * NC + n) * 2 + ks, kPlaneK, fq);
+                planes_of<DT>(only<DT>(steps8<DT>(row_of<DT>(a.d.k, B, row) + t0, whole, t, end), d < a.d.P), fk);
+                planes_of<DT>(only<DT>(steps8<DT>(row_of<DT>(a.d.q, B, row) + t0, whole, t, end), d < a.d.P), fq);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int at = again((m * 16 + col) * X::kPitch + ks * 32 + grp * 8);
@@ -528,6 +585,7 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
                 }
             }
         }
+        settle();
         // The rows' products with normalised query and key.  A step's own dP_ii k_i and dP_ii q_i add the same to
         // q_i.dq_i and k_i.write_i, so they enter after the decays' part: its terms then cancel no further than its
         // definition's do, and the first step from a zero state gets a zero.
@@ -641,8 +699,8 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
                     x[r] = t + r < end ? g * (rq * a.d.scale) : 0.0f;
                     y[r] = t + r < end ? u * rk : 0.0f;
                 }
-                store4_until<DT>(qrow, t, stop, x);
-                store4_until<DT>(krow, t, stop, y);
+                store4_until<DT>(qrow, stop == kDeltaChunk, t, stop, x);
+                store4_until<DT>(krow, stop == kDeltaChunk, t, stop, y);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }

@@ -80,6 +80,133 @@ DEVI void multiply(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4 &acc) {
                                                               __builtin_bit_cast(bf16x8, b[j]), acc, 0, 0, 0);
 }
 
+// The same with a sum for each order, for a few products that the next step waits for: an MFMA's sum is ready only
+// several issues later, and the orders' chains run side by side.
+template <int ORDER>
+struct Sums {
+    f32x4 s[ORDER + 1];
+    DEVI Sums() {
+#pragma unroll
+        for (int i = 0; i <= ORDER; ++i) s[i] = f32x4{0, 0, 0, 0};
+    }
+    template <int NA, int NB>
+    DEVI void add(const u32x4 (&a)[NA], const u32x4 (&b)[NB]) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                if (i + j <= ORDER)
+                    s[i + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
+                                                                       __builtin_bit_cast(bf16x8, b[j]), s[i + j], 0, 0, 0);
+    }
+    // After settle().  Read here, not where the total is used.
+    DEVI f32x4 total() const {
+        f32x4 t = s[ORDER];
+#pragma unroll
+        for (int i = ORDER - 1; i >= 0; --i) t += s[i];
+        asm volatile("" : "+v"(t));
+        return t;
+    }
+};
+
+// Eight fp32 values of a fragment stored as [lane][8] fp32.
+struct Eight {
+    f32x4 lo, hi;
+};
+DEVI Eight fragment32(const char *at, int frag) {
+    const f32x4 *p = (const f32x4 *)(at + frag * 2048 + (threadIdx.x & 63) * 32);
+    return {p[0], p[1]};
+}
+template <int N>
+DEVI void planes_of(const Eight &e, u32x4 (&v)[N]) {
+    const float f[8] = {e.lo[0], e.lo[1], e.lo[2], e.lo[3], e.hi[0], e.hi[1], e.hi[2], e.hi[3]};
+    split8<N>(f, v);
+}
+
+template <bool W>
+struct Whole {
+    static constexpr bool value = W;
+};
+
+// Consecutive steps of one row as they stand, zeros from `end` on.  `whole` says for the whole wave that none lies
+// there: a branch per lane would wait for its load before the other side could run.
+template <int DT>
+DEVI Raw8<DT> steps8(const typename Elem<DT>::T *row, bool whole, int t, int end) {
+    if (!whole) return fetch8<DT>(row, t, end);
+    Raw8<DT> o;
+    o.r[0] = *(const u32x4_row *)(row + t);
+    if constexpr (DT == 0) o.r[1] = *(const u32x4_row *)(row + t + 4);
+    return o;
+}
+
+template <int DT>
+struct Raw4 {
+    uint32_t r[DT == 1 ? 2 : 4];
+};
+template <int DT>
+DEVI Raw4<DT> steps4(const typename Elem<DT>::T *row, bool whole, int t, int end) {
+    Raw4<DT> o;
+    if (whole) {
+        if constexpr (DT == 1) {
+            const u32x2 v = *(const u32x2_row *)(row + t);
+            o.r[0] = v[0];
+            o.r[1] = v[1];
+        } else {
+            const u32x4 v = *(const u32x4_row *)(row + t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o.r[i] = v[i];
+        }
+        return o;
+    }
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = 0;
+        if (t + i < end) {
+            if constexpr (DT == 1)
+                v[i] = ((const uint16_t *)row)[t + i];
+            else
+                v[i] = ((const uint32_t *)row)[t + i];
+        }
+    }
+    if constexpr (DT == 1) {
+        o.r[0] = v[0] | v[1] << 16;
+        o.r[1] = v[2] | v[3] << 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.r[i] = v[i];
+    }
+    return o;
+}
+// Their values, or zeros where `in` is false: of a row that stands for one past the tensor's.
+template <int DT>
+DEVI void widen4(const Raw4<DT> &o, bool in, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = DT == 0 ? o.r[i & (DT == 0 ? 3 : 1)] : (i & 1 ? o.r[i >> 1] & 0xffff0000u : o.r[i >> 1] << 16);
+        v[i] = in ? __uint_as_float(u) : 0.0f;
+    }
+}
+template <int DT>
+DEVI Raw8<DT> only(const Raw8<DT> &o, bool in) {
+    Raw8<DT> r;
+#pragma unroll
+    for (int h = 0; h < (DT == 1 ? 1 : 2); ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.r[h][i] = in ? o.r[h][i] : 0u;
+    return r;
+}
+template <int DT>
+DEVI void planes_of(const Raw8<DT> &r, u32x4 (&v)[in_planes(DT)]) {
+    if constexpr (DT == 1) {
+        v[0] = r.r[0];
+    } else {
+        float f[8];
+        widen8<DT>(r, f);
+        split8<3>(f, v);
+    }
+}
+
 // A lane's 16 bytes of every plane of fragment `frag`; planes are `plane` bytes apart.
 template <int N>
 DEVI void fragment(const char *at, int frag, int plane, u32x4 (&v)[N]) {
@@ -87,21 +214,10 @@ DEVI void fragment(const char *at, int frag, int plane, u32x4 (&v)[N]) {
     for (int p = 0; p < N; ++p) v[p] = *(const u32x4 *)(at + p * plane + frag * 1024 + (threadIdx.x & 63) * 16);
 }
 
-// Four consecutive elements of a row, zeros from `end` on (not loaded).
+// row[t + i] = v[i] for t + i < end; `whole` as for steps8.
 template <int DT>
-DEVI void load4_until(const typename Elem<DT>::T *row, int t, int end, float (&v)[4]) {
-    if (__builtin_expect(t + 4 <= end, 1)) {
-        load4<DT>(row + t, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = t + i < end ? Elem<DT>::get(row[t + i]) : 0.0f;
-    }
-}
-
-// row[t + i] = v[i] for t + i < end.
-template <int DT>
-DEVI void store4_until(typename Elem<DT>::T *row, int t, int end, const float (&v)[4]) {
-    if (__builtin_expect(t + 4 <= end, 1)) {
+DEVI void store4_until(typename Elem<DT>::T *row, bool whole, int t, int end, const float (&v)[4]) {
+    if (whole) {
         if constexpr (DT == 1) {
             u32x2 r;
 #pragma unroll

@@ -66,12 +66,16 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
     const size_t of_k = ((size_t)b * a.s.nc * a.d.Hk + hk) * TI * 64 * DK * 2, step_k = (size_t)a.d.Hk * TI * 64 * DK * 2;
     const size_t of_v = (size_t)b * a.s.nc * a.d.Hv + h;
     constexpr int kPlaneK = 64 * DK * 2;
-    u32x4 fk[X::kKS][TI], fq[X::kKS][TI], ft[X::kMT][2][TI], fi[2][3], fa[2][OP];
-    float vin[NT][4];
-    f32x4 vek, veq, vfk, vbeta;
-    float last = 0.0f;
-    const char *pk = a.ws + a.w.k + of_k, *pq = a.ws + a.w.q + of_k, *pt = a.ws + a.w.kt + of_k;
-    const char *pi = a.ws + a.w.inv + of_v * 3 * 8192, *pa = a.ws + a.w.attn + of_v * OP * 8192;
+    // three planes of 256 key channels are more than the registers hold ahead of their use
+    constexpr bool kLate = TI == 3 && DK == 256;
+    u32x4 fk[X::kKS][TI], fq[X::kKS][TI];
+    Raw8<DT> ft[X::kMT][2];
+    Eight fi[2], fa[2];
+    Raw4<DT> vin[NT];
+    f32x4 vek, veq, vfk, vbeta, nek, neq, nfk, nbeta;              // of this chunk, and of the next
+    float last = 0.0f, nlast = 0.0f;
+    const char *pk = a.ws + a.w.k + of_k, *pq = a.ws + a.w.q + of_k;
+    const char *pi = a.ws + a.w.inv + of_v * 16384, *pa = a.ws + a.w.attn + of_v * 16384;
     const char *ps = a.ws + a.w.steps + of_v * sizeof(DeltaSteps);
     const T *vrow[NT];
     T *yrow[NT];
@@ -85,51 +89,76 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int ks = 0; ks < X::kKS; ++ks) {
             fragment<TI>(pk + c * step_k, wave * X::kKS + ks, kPlaneK, fk[ks]);
-            fragment<TI>(pq + c * step_k, wave * X::kKS + ks, kPlaneK, fq[ks]);
+            if constexpr (!kLate) fragment<TI>(pq + c * step_k, wave * X::kKS + ks, kPlaneK, fq[ks]);
         }
     };
     const auto load_steps = [&](int c) {
         const DeltaSteps *s = (const DeltaSteps *)(ps + (size_t)c * a.d.Hv * sizeof(DeltaSteps));
-        vek = *(const f32x4 *)(s->ek + mine);
-        veq = *(const f32x4 *)(s->eq + mine);
-        vfk = *(const f32x4 *)(s->fk + mine);
-        vbeta = *(const f32x4 *)(s->beta + mine);
-        last = s->last;
+        nek = *(const f32x4 *)(s->ek + mine);
+        neq = *(const f32x4 *)(s->eq + mine);
+        nfk = *(const f32x4 *)(s->fk + mine);
+        nbeta = *(const f32x4 *)(s->beta + mine);
+        nlast = s->last;
     };
-    const auto load_v = [&](int c) {
+    const auto load_v = [&](int c, bool whole) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            load4_until<DT>(vrow[n], steps_first + c * kDeltaChunk + mine, v0 + n * 16 + col < a.d.V ? valid : 0, vin[n]);
+        for (int n = 0; n < NT; ++n) vin[n] = steps4<DT>(vrow[n], whole, steps_first + c * kDeltaChunk + mine, valid);
     };
+    // the second 32 columns of rows 0..31 are zero and not stored
+    const Eight nothing = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    fi[1] = fa[1] = nothing;
     const auto load_inverse = [&](int c) {
-        const char *i = pi + (size_t)c * a.d.Hv * 3 * 8192;
-        fragment<3>(i, wave * 2, 8192, fi[0]);
-        if (wave >= 2) fragment<3>(i, wave * 2 + 1, 8192, fi[1]);
+        const char *i = pi + (size_t)c * a.d.Hv * 16384;
+        fi[0] = fragment32(i, wave * 2);
+        if (wave >= 2) fi[1] = fragment32(i, wave * 2 + 1);
     };
     const auto load_attn = [&](int c) {
-        const char *at = pa + (size_t)c * a.d.Hv * OP * 8192;
-        fragment<OP>(at, wave * 2, 8192, fa[0]);
-        if (wave >= 2) fragment<OP>(at, wave * 2 + 1, 8192, fa[1]);
+        const char *at = pa + (size_t)c * a.d.Hv * 16384;
+        fa[0] = fragment32(at, wave * 2);
+        if (wave >= 2) fa[1] = fragment32(at, wave * 2 + 1);
     };
-    const auto load_kt = [&](int c) {
+    const T *krow[X::kMT];
+#pragma unroll
+    for (int i = 0; i < X::kMT; ++i) {
+        const int p = (wave * X::kMT + i) * 16 + col;
+        krow[i] = row_of<DT>(a.d.k, B, hk * a.d.P + (p < a.d.P ? p : 0));
+    }
+    const auto load_kt = [&](int c, bool whole) {
 #pragma unroll
         for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
-                fragment<TI>(pt + c * step_k, (wave * X::kMT + i) * 2 + ks, kPlaneK, ft[i][ks]);
+                ft[i][ks] = steps8<DT>(krow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
     };
-    if (chunks) {
-        load_kq(0);
-        load_v(0);
-        load_steps(0);
-        load_inverse(0);
-        load_kt(0);
-        load_attn(0);
-    }
     float *saved = SAVE ? (float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0) * delta_saved(a.d.P, a.d.V) : nullptr;
 
-    for (int c = 0; c < chunks; ++c) {
-        const bool more = c + 1 < chunks;
+    // Chunks of 64 valid steps, and the one that ends inside, if any, whose loads look at each step.  A chunk's loads
+    // for the next one stand without a branch (after the last they load it again), so that a chunk is one block
+    // of code: no wait is counted along a way that was not taken.
+    int full = (valid - steps_first) / kDeltaChunk;
+    full = valid <= steps_first ? 0 : (full < chunks ? full : chunks);
+    if (chunks) {
+        load_steps(0);
+        load_kq(0);
+        load_inverse(0);
+        load_attn(0);
+        if (full) {
+            load_v(0, true);
+            if constexpr (!kLate) load_kt(0, true);
+        }
+    }
+    const auto chunk = [&](const int c, auto is_full) {
+        constexpr bool FULL = decltype(is_full)::value;
+        const int next = c + 1 < chunks ? c + 1 : c, next_full = c + 1 < full ? c + 1 : c;
+        vek = nek;
+        veq = neq;
+        vfk = nfk;
+        vbeta = nbeta;
+        last = nlast;
+        if constexpr (!FULL) {
+            load_v(c, false);
+            if constexpr (!kLate) load_kt(c, false);
+        }
         if constexpr (SAVE) {
 #pragma unroll
             for (int i = 0; i < X::kMT; ++i)
@@ -140,42 +169,56 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
                         saved[(size_t)((wave * X::kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
         }
         __syncthreads();
-        f32x4 ks_[NT], qs[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) ks_[n] = qs[n] = f32x4{0, 0, 0, 0};
+        Sums<2> ks_[NT];
+        Sums<OO> qs[NT];
 #pragma unroll
         for (int ks = 0; ks < X::kKS; ++ks)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 u32x4 s[3];
                 get_planes<3>(Sp + (n * 16 + col) * X::kPitchS + ks * 32 + grp * 8, X::kPlaneS, s);
-                multiply<TI, 3, 2>(fk[ks], s, ks_[n]);
-                multiply<TI, 3, OO>(fq[ks], s, qs[n]);
+                if constexpr (kLate) fragment<TI>(pq + c * step_k, wave * X::kKS + ks, kPlaneK, fq[ks]);
+                ks_[n].add(fk[ks], s);
+                qs[n].add(fq[ks], s);
             }
-        if (more) load_kq(c + 1);
+        f32x4 kS[NT], qS[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            kS[n] = ks_[n].total();
+            qS[n] = qs[n].total();
+        }
+        // loads come back in their order, stores among them: the next chunk's factors, first of all needed, go first
+        load_steps(next);
+        load_kq(next);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float x[4];
+            widen4<DT>(vin[n], v0 + n * 16 + col < a.d.V, x);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], ks_[n][r], vin[n][r]);
+            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], kS[n][r], x[r]);
             put_planes<3>(Xp + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, x);
         }
-        if (more) load_v(c + 1);
+        if constexpr (FULL) load_v(next_full, true);
         __syncthreads();
         f32x4 z[NT];
+        {
+            u32x4 i0[3], i1[3];
+            planes_of<3>(fi[0], i0);
+            planes_of<3>(fi[1], i1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            z[n] = f32x4{0, 0, 0, 0};
-            u32x4 x[3];
-            const uint16_t *from = Xp + (n * 16 + col) * X::kPitchT + grp * 8;
-            get_planes<3>(from, X::kPlaneT, x);
-            multiply<3, 3, 2>(fi[0], x, z[n]);
-            if (wave >= 2) {
+            for (int n = 0; n < NT; ++n) {
+                Sums<2> sum;
+                u32x4 x[3];
+                const uint16_t *from = Xp + (n * 16 + col) * X::kPitchT + grp * 8;
+                get_planes<3>(from, X::kPlaneT, x);
+                sum.add(i0, x);
                 get_planes<3>(from + 32, X::kPlaneT, x);
-                multiply<3, 3, 2>(fi[1], x, z[n]);
+                sum.add(i1, x);
+                z[n] = sum.total();
             }
         }
-        if (more) load_inverse(c + 1);
+        load_inverse(next);
+        if constexpr (kLate) load_kt(c, FULL);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float u[4], uf[4];
@@ -195,52 +238,65 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
             for (int n = 0; n < NT; ++n) S[i][n] *= last;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+        for (int i = 0; i < X::kMT; ++i) {
+            u32x4 k0[TI], k1[TI];
+            const bool in = (wave * X::kMT + i) * 16 + col < a.d.P;
+            planes_of<DT>(only<DT>(ft[i][0], in), k0);
+            planes_of<DT>(only<DT>(ft[i][1], in), k1);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                Sums<2> sum;
                 u32x4 u[3];
-                get_planes<3>(Uf + (n * 16 + col) * X::kPitchT + ks * 32 + grp * 8, X::kPlaneT, u);
-#pragma unroll
-                for (int i = 0; i < X::kMT; ++i) multiply<TI, 3, 2>(ft[i][ks], u, S[i][n]);
+                const uint16_t *from = Uf + (n * 16 + col) * X::kPitchT + grp * 8;
+                get_planes<3>(from, X::kPlaneT, u);
+                sum.add(k0, u);
+                get_planes<3>(from + 32, X::kPlaneT, u);
+                sum.add(k1, u);
+                S[i][n] += sum.total();
             }
-        if (more) load_kt(c + 1);
+        }
+        if constexpr (!kLate && FULL) load_kt(next_full, true);
         put_state();
         // y
+        u32x4 a0[OP], a1[OP];
+        planes_of<OP>(fa[0], a0);
+        planes_of<OP>(fa[1], a1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            f32x4 o = {0, 0, 0, 0};
+            Sums<OO> o;
             u32x4 u[OP];
             const uint16_t *from = Up + (n * 16 + col) * X::kPitchT + grp * 8;
             get_planes<OP>(from, X::kPlaneT, u);
-            multiply<OP, OP, OO>(fa[0], u, o);
-            if (wave >= 2) {
-                get_planes<OP>(from + 32, X::kPlaneT, u);
-                multiply<OP, OP, OO>(fa[1], u, o);
-            }
+            o.add(a0, u);
+            get_planes<OP>(from + 32, X::kPlaneT, u);
+            o.add(a1, u);
+                const f32x4 p = o.total();
             float y[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(veq[r], qs[n][r], o[r]);
+            for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(veq[r], qS[n][r], p[r]);
             if (v0 + n * 16 + col < a.d.V) {
                 const int t = steps_first + c * kDeltaChunk + mine;
                 // past the sequence's end: zeros, up to the end of the rows
+                if constexpr (!FULL) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
-                store4_until<DT>(yrow[n], t, a.d.L, y);
+                    for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
+                }
+                store4_until<DT>(yrow[n], FULL, t, a.d.L, y);
             }
         }
-        if (more) {
-            load_attn(c + 1);
-            load_steps(c + 1);
-        }
+        load_attn(next);
         if constexpr (SAVE) saved += delta_saved(a.d.P, a.d.V);
-    }
+    };
+    for (int c = 0; c < full; ++c) chunk(c, Whole<true>());
+    if (full < chunks) chunk(full, Whole<false>());
     // chunks past the sequence's end
     for (int c = chunks; c < a.s.nc; ++c) {
         const float zeros[4] = {};
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             if (v0 + n * 16 + col < a.d.V)
-                store4_until<DT>(yrow[n], steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+                store4_until<DT>(yrow[n], steps_first + (c + 1) * kDeltaChunk <= a.d.L, steps_first + c * kDeltaChunk + mine,
+                                 a.d.L, zeros);
     }
     {
         float *out = a.last ? a.d.final_state : state_out;

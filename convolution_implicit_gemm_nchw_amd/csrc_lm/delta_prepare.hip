@@ -17,7 +17,6 @@ struct Prepare {
     static constexpr int kCols = DK < 128 ? DK : 128;      // channels at a time
     static constexpr int kSteps = kCols / 32;
     static constexpr int kPlane = 64 * kCols * 2;          // bytes of one plane in LDS
-    static constexpr int kOut = BWD ? 3 : (TI == 1 ? 2 : 3);   // planes of attn: y's are to order 1 for bf16
     static constexpr int kFrags = 2 * TI * kPlane;
     static constexpr int kSolve = 64 * kRow * 4 + 4 * 16 * 20 * 4;
     static constexpr int kShared = kFrags > kSolve ? kFrags : kSolve;
@@ -28,8 +27,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     constexpr int TI = in_planes(DT);
     typedef Prepare<TI, DK, BWD> X;
     __shared__ __attribute__((aligned(16))) char shared[X::kShared];
-    __shared__ __attribute__((aligned(16))) float A[64 * kRow], M[64 * kRow];
-    __shared__ float part[2][X::kCols / 8][64];
+    __shared__ __attribute__((aligned(16))) float A[64 * kRow];
+    float (*const part)[X::kCols / 8][64] = (float (*)[X::kCols / 8][64])A;     // before A: sums of squares
     __shared__ __attribute__((aligned(16))) DeltaSteps steps;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int id = a.more + blockIdx.x;
@@ -53,23 +52,22 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
             const int tb = (in & 7) * 8, db = (in >> 3) * 8;
             const miconv_rows_t &rows = operand ? a.d.q : a.d.k;
             float x[8][8];
+            Raw8<DT> raw[8];
+            const bool whole = end >= kDeltaChunk;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int d = d0 + db + i;
-                if (d < a.d.P) {
-                    load8<DT>(row_of<DT>(rows, B, hk * a.d.P + d) + t0, tb, end, x[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
-                }
+                raw[i] = steps8<DT>(row_of<DT>(rows, B, hk * a.d.P + (d < a.d.P ? d : 0)) + t0, whole, tb, end);
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) widen8<DT>(only<DT>(raw[i], d0 + db + i < a.d.P), x[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) squares[j] = __builtin_fmaf(x[i][j], x[i][j], squares[j]);
-            // [t][p]: to LDS, and k (forward: q too) to memory; [p][t]: k^T (backward: q^T too) to memory
-            const bool rows_out = leads && (!operand || !BWD), cols_out = leads && (!operand || BWD);
-            char *const flat = a.ws + (operand ? a.w.q : a.w.k) + of_k, *const turned = a.ws + (operand ? a.w.q : a.w.kt) + of_k;
+            // [t][p]: to LDS, and k (forward: q too) to memory
+            const bool rows_out = leads && (!operand || !BWD);
+            char *const flat = a.ws + (operand ? a.w.q : a.w.k) + of_k;
 #pragma unroll
             for (int p = 0; p < TI; ++p) {
 #pragma unroll
@@ -82,15 +80,6 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
                     if (rows_out)
                         *(u32x4 *)(flat + (size_t)p * 64 * DK * 2 + ((t >> 4) * (DK / 32) + ((d0 + db) >> 5)) * 1024 +
                                    lane_at * 16) = v;
-                }
-                if (cols_out) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const u32x4 v = {upper_pair(x[i][0], x[i][1]), upper_pair(x[i][2], x[i][3]),
-                                         upper_pair(x[i][4], x[i][5]), upper_pair(x[i][6], x[i][7])};
-                        const int d = d0 + db + i, lane_at = (d & 15) + (tb >> 3 & 3) * 16;
-                        *(u32x4 *)(turned + (size_t)p * 64 * DK * 2 + ((d >> 4) * 2 + (tb >> 5)) * 1024 + lane_at * 16) = v;
-                    }
                 }
                 if (p + 1 < TI) {
 #pragma unroll
@@ -113,10 +102,15 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
                 u32x4 col[TI];
                 fragment<TI>(shared, n * X::kSteps + ks, X::kPlane, col);
                 multiply<TI, TI, 2>(rk, col, kk[n]);
-                multiply<TI, TI, 2>(rq, col, qk[n]);
+                // q k^T with four neighbouring keys to a lane (backward: queries), as attn is stored
+                if constexpr (BWD)
+                    multiply<TI, TI, 2>(rq, col, qk[n]);
+                else
+                    multiply<TI, TI, 2>(col, rq, qk[n]);
             }
         }
     }
+    settle();
     {
         const int operand = tid / kBlocks, in = tid % kBlocks;
         if (operand < 2) {
@@ -158,28 +152,37 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
         steps.ek[lane] *= steps.rk[lane];
         steps.fk[lane] *= steps.rk[lane];
     }
-    // the system's matrix (its diagonal of ones left out) and the products of queries with keys
+    // The system's matrix (its diagonal of ones left out), and the products of queries with keys, which go to memory
+    // from here.  A block of 32 columns past the diagonal is never read.
     const int col = lane & 15, row4 = (lane >> 4) * 4;
+    char *const inv = a.ws + a.w.inv + of_v * 16384, *const attn = a.ws + a.w.attn + of_v * 16384;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
+        if (n > (wave | 1)) break;
         const int j = n * 16 + col;
         const double Gj = steps.G[j];
         const float rkj = steps.rk[j], bj = steps.beta[j];
-        float m[4];
+        f32x4 m;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = wave * 16 + row4 + r;
-            const float D = i >= j ? exp_any((float)(steps.G[i] - Gj)) : 0.0f;
-            const float v = kk[n][r] * (steps.rk[i] * rkj) * D * (BWD ? steps.beta[i] : bj);
-            A[i * kRow + j] = i > j ? v : 0.0f;
-            m[r] = i >= j ? qk[n][r] * (steps.rq[i] * a.d.scale * rkj) * D : 0.0f;
+            const float D = i > j ? exp_any((float)(steps.G[i] - Gj)) : 0.0f;
+            A[i * kRow + j] = i > j ? kk[n][r] * (steps.rk[i] * rkj) * D * (BWD ? steps.beta[i] : bj) : 0.0f;
+            if constexpr (BWD) m[r] = i >= j ? qk[n][r] * (steps.rq[i] * a.d.scale * rkj) * (i == j ? 1.0f : D) : 0.0f;
         }
-        if constexpr (BWD) {
-            *(f32x4 *)(M + j * kRow + wave * 16 + row4) = f32x4{m[0], m[1], m[2], m[3]};
-        } else {
+        if constexpr (!BWD) {
+            const int i = wave * 16 + col;
+            const double Gi = steps.G[i];
+            const float ri = steps.rq[i] * a.d.scale;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) M[(wave * 16 + row4 + r) * kRow + j] = m[r];
+            for (int r = 0; r < 4; ++r) {
+                const int key = n * 16 + row4 + r;
+                m[r] = i >= key ? qk[n][r] * (ri * steps.rk[key]) * exp_any((float)(Gi - steps.G[key])) : 0.0f;
+            }
         }
+        // row tile, block of 32 columns, and the half of it, of the four values
+        const int tile = BWD ? n : wave, block = (BWD ? wave : n) >> 1, eight = ((BWD ? wave : n) & 1) * 2 + (lane >> 5);
+        *(f32x4 *)(attn + (tile * 2 + block) * 2048 + (col + eight * 16) * 32 + (lane >> 4 & 1) * 16) = m;
     }
     __syncthreads();
 
@@ -229,6 +232,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     Tc[di] = __builtin_amdgcn_mfma_f32_16x16x4f32(-left[r], y[r], Tc[di], 0, 0, 0);
+                settle();
             }
         }
         // block column `wave` of the inverse, zeros above the diagonal; transposed for the backward pass
@@ -247,31 +251,16 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
         }
     }
     __syncthreads();
-    // Both out as planes in operand order, without the quarter that is zero: columns 32.. of rows 0..31 (forward),
-    // columns 0..31 of rows 32.. (backward).
-    char *const inv = a.ws + a.w.inv + of_v * 3 * 8192, *const attn = a.ws + a.w.attn + of_v * X::kOut * 8192;
+    // Out in operand order, without the quarter that is zero: columns 32.. of rows 0..31 (forward), columns 0..31 of
+    // rows 32.. (backward).
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int f = half * 4 + wave, tile = f >> 1, ks = f & 1;
         if (BWD ? (tile >= 2 && ks == 0) : (tile < 2 && ks == 1)) continue;
-        const int at = (tile * 16 + col) * kRow + ks * 32 + (lane >> 4) * 8;
-        float v[8], m[8];
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const f32x4 tv = *(const f32x4 *)(Tm + at + e), mv = *(const f32x4 *)(M + at + e);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[e + i] = tv[i];
-                m[e + i] = mv[i];
-            }
-        }
-        u32x4 planes[3];
-        split8<3>(v, planes);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *(u32x4 *)(inv + p * 8192 + f * 1024 + lane * 16) = planes[p];
-        split8<3>(m, planes);
-#pragma unroll
-        for (int p = 0; p < X::kOut; ++p) *(u32x4 *)(attn + p * 8192 + f * 1024 + lane * 16) = planes[p];
+        const float *from = Tm + (tile * 16 + col) * kRow + ks * 32 + (lane >> 4) * 8;
+        f32x4 *const to = (f32x4 *)(inv + f * 2048 + lane * 32);
+        to[0] = *(const f32x4 *)from;
+        to[1] = *(const f32x4 *)(from + 4);
     }
     if (tid < (int)(sizeof(DeltaSteps) / 16))
         ((u32x4 *)(a.ws + a.w.steps + of_v * sizeof(DeltaSteps)))[tid] = ((const u32x4 *)&steps)[tid];

@@ -315,6 +315,15 @@ DEVI int again(int v) {
     return v;
 }
 
+// Between MFMAs and the first read of their sums.  The compiler adds the wait states that a read needs, but where a
+// branch lies between the two it was found (hipcc 7.2) to count them along the longer way only, and the last elements
+// of a sum were read before they were written.  24 states cover the longest MFMA; the read would wait for its own anyway.
+DEVI void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 7");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Orders this wave's LDS accesses: what a lane wrote before is read by the others after.
 DEVI void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
