@@ -25,6 +25,10 @@ constexpr int delta_chunks(int L) { return (L + kDeltaChunk - 1) / kDeltaChunk; 
 constexpr int delta_key_pad(int P) { return P <= 64 ? 64 : (P <= 128 ? 128 : 256); }
 constexpr int delta_value_pad(int V) { return (V + 31) / 32 * 32; }
 
+// Planes of attn: y of bf16 type rests on sums to order 1.
+constexpr int delta_attn_planes(int dtype, bool backward) { return !backward && dtype == MICONV_BF16 ? 2 : 3; }
+constexpr int kDeltaSquare = kDeltaChunk * kDeltaChunk * 2;    // bytes of a plane of 64 x 64
+
 // What the pass over chunks finds about each step of a chunk and value head.
 struct DeltaSteps {
     double G[kDeltaChunk];                 // sums of log decays
@@ -45,7 +49,7 @@ struct DeltaSlice {
 // the row operand of 16x16x32 MFMAs: [row tile of 16][32 columns][lane][8].
 struct DeltaWork {
     size_t k, q;                           // k and (forward) q, [t][p], a plane of bf16 after the other
-    size_t inv, attn;                      // the inverse and (D * q k^T), fp32, transposed in the backward pass
+    size_t inv, attn;                      // planes of the inverse and of (D * q k^T), transposed in the backward pass
     size_t steps;                          // DeltaSteps
     size_t state;                          // [nb][Hv][Pp][Vp] fp32: carried between slices of time
     size_t F, after;                       // backward: [chunk][Vp][64], [chunk][Pp][Vp] fp32

@@ -17,11 +17,10 @@ DeltaWork delta_work(const miconv_gated_delta_t &d, int dtype, const DeltaSlice 
     };
     const size_t chunks = (size_t)s.nb * s.nc, heads = chunks * d.Hv, DK = delta_key_pad(d.P), Vp = delta_value_pad(d.V);
     const size_t operand = chunks * d.Hk * (dtype == MICONV_BF16 ? 1 : 3) * kDeltaChunk * DK * 2;
-    const size_t square = kDeltaChunk * kDeltaChunk * 4;
     take(&w.k, operand);
     if (!backward) take(&w.q, operand);
-    take(&w.inv, heads * square);
-    take(&w.attn, heads * square);
+    take(&w.inv, heads * 3 * kDeltaSquare);
+    take(&w.attn, heads * delta_attn_planes(dtype, backward) * kDeltaSquare);
     take(&w.steps, heads * sizeof(DeltaSteps));
     if (backward) {
         take(&w.F, heads * Vp * kDeltaChunk * 4);
@@ -39,7 +38,7 @@ DeltaWork delta_work(const miconv_gated_delta_t &d, int dtype, const DeltaSlice 
 DeltaSlice delta_slice(const miconv_gated_delta_t &d, int dtype, size_t budget, bool backward) {
     const int chunks = delta_chunks(d.L);
     // a launch of the scans counts its work-groups in 32 bits of work-items
-    const long long most = ((1ll << 32) / 256 - 1) / ((long long)d.Hv * (delta_value_pad(d.V) / kDeltaSlice));
+    const long long most = ((1ll << 32) / 512 - 1) / ((long long)d.Hv * (delta_value_pad(d.V) / kDeltaSlice));
     const int nb = d.B < most ? d.B : (int)(most > 1 ? most : 1);
     const auto fits = [&](int b, int c) {
         return delta_work(d, dtype, {0, b, 0, c}, backward).bytes <= budget && (long long)b * c * d.Hv < (1ll << 30);

@@ -17,15 +17,21 @@ namespace miconv {
 
 namespace {
 
-// Laid out and split as the forward scan; the state here is dS.
+// Laid out and split as the forward scan; the state here is dS.  Four waves go along the chain k dS, the transposed inverse
+// times du, dS - (e k)^T (beta F); the others compute attn^T dy, for the chunk that comes next, and meanwhile
+// (e q)^T dy for all key channels, half of which they hand over through LDS.
 template <int DT, int DK, int NT>
-__global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
-    constexpr int TI = in_planes(DT), kKS = DK / 32, kMT = DK / 64, kN = NT * 16;
+__global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
+    constexpr int TI = in_planes(DT), kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = NT * 16;
     constexpr int kPitchS = DK + 8, kPitchT = kDeltaChunk + 8, kPlaneS = kN * kPitchS, kPlaneT = kN * kPitchT;
+    constexpr int kPitchF = kDeltaChunk + 4, kHalf = kTiles < 8 ? kTiles : kTiles / 2;   // tiles of the chain's waves
     typedef typename Elem<DT>::T T;
     __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * kPlaneS], Up[3 * kPlaneT], Wp[3 * kPlaneT];
+    __shared__ __attribute__((aligned(16))) float Bs[2][kN * kPitchF];   // attn^T dy of this chunk and the next
+    __shared__ __attribute__((aligned(16))) float Qs[kHalf * NT * 64 * 4];   // (e q)^T dy as accumulators
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
-    const int row4 = grp * 4, mine = wave * 16 + row4;
+    const bool queries = wave >= 4, owner = wave * kMT < kTiles;
+    const int part = wave & 3, row4 = grp * 4, mine = part * 16 + row4;
     const int total = a.s.nb * a.d.Hv * a.slices;
     const int id = xcd_remap(blockIdx.x, total);
     const int slice = id % a.slices, bh = id / a.slices, h = bh % a.d.Hv, b = bh / a.d.Hv, B = a.s.b0 + b;
@@ -51,6 +57,7 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
                 }
     }
     const auto put_state = [&] {
+        if (!owner) return;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -60,107 +67,42 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
             }
     };
     put_state();
+    for (int i = threadIdx.x; i < 3 * kN * 8; i += 512)        // the zeros behind du's steps
+        Up[i / (kN * 8) * kPlaneT + i / 8 % kN * kPitchT + kDeltaChunk + i % 8] = 0;
 
     const size_t of_k = ((size_t)b * a.s.nc * a.d.Hk + hk) * TI * 64 * DK * 2, step_k = (size_t)a.d.Hk * TI * 64 * DK * 2;
     const size_t of_v = (size_t)b * a.s.nc * a.d.Hv + h;
     constexpr int kPlaneK = 64 * DK * 2;
     // three planes of 256 key channels are more than the registers hold ahead of their use
     constexpr bool kLate = TI == 3 && DK == 256;
-    u32x4 fk[kKS][TI];
-    Raw8<DT> ft[kMT][2], fq[kMT][2], fg[NT][2];   // k^T, q^T and, as column operand, dy
-    Eight fi[2], fa[2], feq[2];                // feq: the queries' factors of the steps that fg holds
-    f32x4 vek, vfk, vbeta;
-    float last = 0.0f;
-    const T *grow[NT];
-    T *out[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int v = v0 + n * 16 + col, at = h * a.d.V + (v < a.d.V ? v : 0);
-        grow[n] = row_of<DT>(a.d.dy, B, at);
-        out[n] = row_of<DT>(a.d.dv, B, at);
-    }
-    const auto load_k = [&](int c) {
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
-            fragment<TI>(a.ws + a.w.k + of_k + c * step_k, wave * kKS + ks, kPlaneK, fk[ks]);
-    };
-    const T *krow[kMT], *qrow[kMT];
+    const T *krow[kMT];
 #pragma unroll
     for (int i = 0; i < kMT; ++i) {
-        const int p = (wave * kMT + i) * 16 + col, at = hk * a.d.P + (p < a.d.P ? p : 0);
-        krow[i] = row_of<DT>(a.d.k, B, at);
-        qrow[i] = row_of<DT>(a.d.q, B, at);
+        const int p = (wave * kMT + i) * 16 + col;
+        krow[i] = row_of<DT>(a.d.k, B, hk * a.d.P + (p < a.d.P ? p : 0));
     }
-    const auto turned = [&](const T *row, int c, int ks, bool whole) {
-        return steps8<DT>(row, whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+    Raw8<DT> ft[kMT][2];
+    float last = 0.0f;
+    const auto steps_of = [&](int c) {
+        return (const DeltaSteps *)(a.ws + a.w.steps + (of_v + (size_t)c * a.d.Hv) * sizeof(DeltaSteps));
     };
     const auto load_turned = [&](int c, bool whole) {
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                ft[i][ks] = turned(krow[i], c, ks, whole);
-                fq[i][ks] = turned(qrow[i], c, ks, whole);
-            }
-    };
-    // both are upper triangular: the first 32 columns of rows from 32 on are zero and not stored
-    const Eight nothing = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    fi[0] = fa[0] = nothing;
-    const auto load_inverse = [&](int c) {
-        const char *i = a.ws + a.w.inv + (of_v + (size_t)c * a.d.Hv) * 16384;
-        if (wave < 2) fi[0] = fragment32(i, wave * 2);
-        fi[1] = fragment32(i, wave * 2 + 1);
-    };
-    const auto load_attn = [&](int c) {
-        const char *at = a.ws + a.w.attn + (of_v + (size_t)c * a.d.Hv) * 16384;
-        if (wave < 2) fa[0] = fragment32(at, wave * 2);
-        fa[1] = fragment32(at, wave * 2 + 1);
-    };
-    const auto load_dy = [&](int c, bool whole) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
             for (int ks = 0; ks < 2; ++ks)
-                fg[n][ks] = steps8<DT>(grow[n], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+                ft[i][ks] = steps8<DT>(krow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
     };
-    const auto load_steps = [&](int c) {
-        const DeltaSteps *s = (const DeltaSteps *)(a.ws + a.w.steps + (of_v + (size_t)c * a.d.Hv) * sizeof(DeltaSteps));
-        vek = *(const f32x4 *)(s->ek + mine);
-        vfk = *(const f32x4 *)(s->fk + mine);
-        vbeta = *(const f32x4 *)(s->beta + mine);
-        last = s->last;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const f32x4 *eq = (const f32x4 *)(s->eq + ks * 32 + grp * 8);
-            feq[ks] = {eq[0], eq[1]};
-        }
+    // The transposed inverse and attn are upper triangular: the first 32 columns of rows 32.. are zero and not stored.
+    const bool lower = part < 2;
+    const auto load_m = [&](size_t place, int c, u32x4 (&fm)[2][3]) {
+        const char *at = a.ws + place + (of_v + (size_t)c * a.d.Hv) * 3 * kDeltaSquare;
+        fragment<3>(at, part * 2 + (lower ? 0 : 1), kDeltaSquare, fm[0]);
+        fragment<3>(at, part * 2 + 1, kDeltaSquare, fm[1]);
     };
-    // as in the forward scan; here the chunk that ends inside comes first
-    int full = (valid - steps_first) / kDeltaChunk;
-    full = valid <= steps_first ? 0 : (full < chunks ? full : chunks);
-    if (chunks) {
-        load_k(chunks - 1);
-        load_attn(chunks - 1);
-        load_inverse(chunks - 1);
-        load_dy(chunks - 1, full == chunks);
-        if constexpr (!kLate) load_turned(chunks - 1, full == chunks);
-    }
-    // chunks past the sequence's end
-    for (int c = chunks; c < a.s.nc; ++c) {
-        const float zeros[4] = {};
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (v0 + n * 16 + col < a.d.V)
-                store4_until<DT>(out[n], steps_first + (c + 1) * kDeltaChunk <= a.d.L, steps_first + c * kDeltaChunk + mine,
-                                 a.d.L, zeros);
-    }
-    const auto chunk = [&](const int c, auto is_full) {
-        constexpr bool FULL = decltype(is_full)::value;
-        const int next = c ? c - 1 : 0;
-        const bool whole = FULL || c;          // of the next chunk's loads, or again the same
-        const size_t at = of_v + (size_t)c * a.d.Hv;
-        float *after = (float *)(a.ws + a.w.after) + at * DK * a.Vp, *Fout = (float *)(a.ws + a.w.F) + at * a.Vp * kDeltaChunk;
-        load_steps(c);                         // ahead of the stores: loads come back in their order, stores among them
+    const auto save_state = [&](int c) {
+        if (!owner) return;
+        float *after = (float *)(a.ws + a.w.after) + (of_v + (size_t)c * a.d.Hv) * DK * a.Vp;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -168,140 +110,273 @@ __global__ __launch_bounds__(256) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     after[(size_t)((wave * kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
-        f32x4 back[NT];
-        {
-            u32x4 a0[3], a1[3];
-            planes_of<3>(fa[0], a0);
-            planes_of<3>(fa[1], a1);
+    };
+    // dS from `given`, (e q)^T dy of the wave's own tiles
+    const auto update = [&](int c, bool whole, f32x4 (&given)[kMT][NT]) {
+        if (!owner) return;
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+            if constexpr (kLate) {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    ft[i][ks] = steps8<DT>(krow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+            }
+            u32x4 k0[TI], k1[TI];
+            const int tile = wave * kMT + i;
+            planes_of<DT>(only<DT>(ft[i][0], tile * 16 + col < a.d.P), k0);
+            planes_of<DT>(only<DT>(ft[i][1], tile * 16 + col < a.d.P), k1);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 Sums<2> sum;
-                u32x4 g[TI];
-                planes_of<DT>(only<DT>(fg[n][0], v0 + n * 16 + col < a.d.V), g);
-                sum.add(a0, g);
-                planes_of<DT>(only<DT>(fg[n][1], v0 + n * 16 + col < a.d.V), g);
-                sum.add(a1, g);
-                back[n] = sum.total();
+                u32x4 w[3];
+                const uint16_t *from = Wp + (n * 16 + col) * kPitchT + grp * 8;
+                get_planes<3>(from, kPlaneT, w);
+                sum.add(k0, w);
+                get_planes<3>(from + 32, kPlaneT, w);
+                sum.add(k1, w);
+                S[i][n] = S[i][n] * last + (given[i][n] + sum.total());
             }
         }
-        load_attn(next);
-        __syncthreads();
+        put_state();
+    };
+    // as in the forward scan; here the chunk that ends inside comes first
+    int full = (valid - steps_first) / kDeltaChunk;
+    full = valid <= steps_first ? 0 : (full < chunks ? full : chunks);
+    const int begin = chunks - 1;
+    if (chunks) {
+        if constexpr (!kLate) load_turned(begin, full == chunks);
+        last = steps_of(begin)->last;
+    }
+    if (!chunks) {
+    } else if (!queries) {
+        u32x4 fk[kLate ? 1 : kKS][TI], fi[2][3];
+        T *out[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            Sums<2> kd;
+            const int v = v0 + n * 16 + col;
+            out[n] = row_of<DT>(a.d.dv, B, h * a.d.V + (v < a.d.V ? v : 0));
+        }
+        const auto load_k = [&](int c) {
+#pragma unroll
+            for (int ks = 0; ks < kKS && !kLate; ++ks)
+                fragment<TI>(a.ws + a.w.k + of_k + c * step_k, part * kKS + ks, kPlaneK, fk[ks]);
+        };
+        load_k(begin);
+        load_m(a.w.inv, begin, fi);
+        f32x4 vek = *(const f32x4 *)(steps_of(begin)->ek + mine), vfk = *(const f32x4 *)(steps_of(begin)->fk + mine);
+        f32x4 vbeta = *(const f32x4 *)(steps_of(begin)->beta + mine);
+        // rows 32.. meet the first fragment with the zeros behind each channel's 64 steps
+        const int first_half = lower ? 0 : kDeltaChunk - grp * 8;
+        const auto chunk = [&](const int c, auto is_full) {
+            constexpr bool FULL = decltype(is_full)::value;
+            const int next = c ? c - 1 : 0;
+            save_state(c);
+            __syncthreads();
+            Sums<2> kd[NT];
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks) {
-                u32x4 s[3];
-                get_planes<3>(Sp + (n * 16 + col) * kPitchS + ks * 32 + grp * 8, kPlaneS, s);
-                kd.add(fk[ks], s);
-            }
-            const f32x4 k = kd.total();
-            float du[4];
+                if constexpr (kLate) fragment<TI>(a.ws + a.w.k + of_k + c * step_k, part * kKS + ks, kPlaneK, fk[0]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], k[r], back[n][r]);
-            put_planes<3>(Up + (n * 16 + col) * kPitchT + mine, kPlaneT, du);
-        }
-        load_k(next);
-        __syncthreads();
-        {
-            u32x4 i0[3], i1[3];
-            planes_of<3>(fi[0], i0);
-            planes_of<3>(fi[1], i1);
+                for (int n = 0; n < NT; ++n) {
+                    u32x4 s[3];
+                    get_planes<3>(Sp + (n * 16 + col) * kPitchS + ks * 32 + grp * 8, kPlaneS, s);
+                    kd[n].add(fk[kLate ? 0 : ks], s);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const f32x4 k = kd[n].total(), back = *(const f32x4 *)(Bs[c & 1] + (n * 16 + col) * kPitchF + mine);
+                float du[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], k[r], back[r]);
+                put_planes<3>(Up + (n * 16 + col) * kPitchT + mine, kPlaneT, du);
+            }
+            load_k(next);
+            vfk = *(const f32x4 *)(steps_of(next)->fk + mine);
+            __syncthreads();
+            float *Fout = (float *)(a.ws + a.w.F) + (of_v + (size_t)c * a.d.Hv) * a.Vp * kDeltaChunk;
+            f32x4 F[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 Sums<2> sum;
                 u32x4 u[3];
                 const uint16_t *from = Up + (n * 16 + col) * kPitchT + grp * 8;
-                get_planes<3>(from, kPlaneT, u);
-                sum.add(i0, u);
+                get_planes<3>(from + first_half, kPlaneT, u);
+                sum.add(fi[0], u);
                 get_planes<3>(from + 32, kPlaneT, u);
-                sum.add(i1, u);
-                const f32x4 F = sum.total();
-                *(f32x4 *)(Fout + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = F;
-                float w[4], dv[4];
+                sum.add(fi[1], u);
+                F[n] = sum.total();
+                float w[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    dv[r] = vbeta[r] * F[r];
-                    w[r] = -(vek[r] * dv[r]);
-                }
+                for (int r = 0; r < 4; ++r) w[r] = -(vek[r] * (vbeta[r] * F[n][r]));
                 put_planes<3>(Wp + (n * 16 + col) * kPitchT + mine, kPlaneT, w);
+            }
+            // ahead of the stores: loads come back in their order, stores among them
+            const f32x4 beta = vbeta;
+            load_m(a.w.inv, next, fi);
+            vek = *(const f32x4 *)(steps_of(next)->ek + mine);
+            vbeta = *(const f32x4 *)(steps_of(next)->beta + mine);
+            __syncthreads();
+            f32x4 given[kMT][NT];
+            if (owner) {
+#pragma unroll
+                for (int i = 0; i < kMT; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        given[i][n] = *(const f32x4 *)(Qs + (((wave * kMT + i) * NT + n) * 64 + lane) * 4);
+            }
+            update(c, FULL, given);
+            last = steps_of(next)->last;
+            if constexpr (!kLate) load_turned(next, FULL || c);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                *(f32x4 *)(Fout + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = F[n];
                 if (v0 + n * 16 + col < a.d.V) {
                     const int t = steps_first + c * kDeltaChunk + mine;
-                    if constexpr (!FULL) {
+                    float dv[4];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) dv[r] = t + r < valid ? dv[r] : 0.0f;
-                    }
+                    for (int r = 0; r < 4; ++r) dv[r] = FULL || t + r < valid ? beta[r] * F[n][r] : 0.0f;
                     store4_until<DT>(out[n], FULL, t, a.d.L, dv);
                 }
             }
+        };
+        if (full < chunks) chunk(full, Whole<false>());
+        for (int c = full - 1; c >= 0; --c) chunk(c, Whole<true>());
+    } else {
+        constexpr bool kAhead = TI == 1 && DK <= 128;    // queries likewise, where the registers hold them
+        u32x4 fa[2][3];
+        Raw8<DT> fq[kAhead ? 2 * kMT : 1][2];
+        Raw8<DT> fg[NT][2], fn[NT][2];         // dy as column operand: of this chunk, and of the next
+        f32x4 veq[2][2];                       // of the steps that fg holds
+        const T *grow[NT], *qrow[2 * kMT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int v = v0 + n * 16 + col;
+            grow[n] = row_of<DT>(a.d.dy, B, h * a.d.V + (v < a.d.V ? v : 0));
         }
-        load_inverse(next);
-        // dS: what the queries give needs none of the above
-        u32x4 g[NT][2][3];
+        // tiles of queries that this wave multiplies: its own and those of the wave that it hands over to
+        const auto tile_of = [&](int i) { return (i < kMT ? wave : part) * kMT + i % kMT; };
+#pragma unroll
+        for (int i = 0; i < 2 * kMT; ++i) {
+            const int p = tile_of(i) * 16 + col;
+            qrow[i] = row_of<DT>(a.d.q, B, hk * a.d.P + (p < a.d.P ? p : 0));
+        }
+        const auto load_dy = [&](int c, bool whole) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    fn[n][ks] = steps8<DT>(grow[n], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+        };
+        const auto turned_q = [&](int i, int c, int ks, bool whole) {
+            return steps8<DT>(qrow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+        };
+        const auto load_q = [&](int c, bool whole) {
+#pragma unroll
+            for (int i = 0; i < 2 * kMT && kAhead; ++i)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) fq[i][ks] = turned_q(i, c, ks, whole);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) veq[ks][e] = *(const f32x4 *)(steps_of(c)->eq + ks * 32 + grp * 8 + e * 4);
+        };
+        // attn^T dy of chunk c, whose attn is in fa and dy in fn, to Bs[c & 1]; then the next one's are loaded
+        const auto put_back = [&](int c, int next, bool whole) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                Sums<2> sum;
+                u32x4 g[TI];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    planes_of<DT>(only<DT>(fn[n][ks], v0 + n * 16 + col < a.d.V && (ks || lower)), g);
+                    sum.add(fa[ks], g);
+                }
+                *(f32x4 *)(Bs[c & 1] + (n * 16 + col) * kPitchF + mine) = sum.total();
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) fg[n][ks] = fn[n][ks];
+            load_m(a.w.attn, next, fa);
+            load_dy(next, whole);
+        };
+        load_m(a.w.attn, begin, fa);
+        load_dy(begin, full == chunks);
+        load_q(begin, full == chunks);
+        put_back(begin, begin ? begin - 1 : 0, begin || full == chunks);
+        const auto chunk = [&](const int c, auto is_full) {
+            constexpr bool FULL = decltype(is_full)::value;
+            const int next = c ? c - 1 : 0;
+            save_state(c);
+            __syncthreads();
+            f32x4 given[kMT][NT];
+            u32x4 g[NT][2][3];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    float x[8];
+                    widen8<DT>(only<DT>(fg[n][ks], v0 + n * 16 + col < a.d.V), x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= veq[ks][e >> 2][e & 3];
+                    split8<3>(x, g[n][ks]);
+                }
+#pragma unroll
+            for (int i = 0; i < 2 * kMT; ++i) {
+                const int tile = tile_of(i);
+                if (kTiles < 8 && i < kMT) continue;     // with 64 key channels these waves own no tile
+                Sums<2> sum[NT];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    u32x4 q[TI];
+                    if constexpr (!kAhead) fq[0][ks] = turned_q(i, c, ks, FULL);
+                    planes_of<DT>(only<DT>(fq[kAhead ? i : 0][ks], tile * 16 + col < a.d.P), q);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) sum[n].add(q, g[n][ks]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const f32x4 t = sum[n].total();
+                    if (i < kMT)
+                        given[i % kMT][n] = t;
+                    else
+                        *(f32x4 *)(Qs + ((tile * NT + n) * 64 + lane) * 4) = t;
+                }
+            }
+            load_q(next, FULL || c);
+            __syncthreads();
+            put_back(next, c > 1 ? c - 2 : 0, FULL || c);      // after the first chunk of time, for nothing
+            __syncthreads();
+            update(c, FULL, given);
+            last = steps_of(next)->last;
+            if constexpr (!kLate) load_turned(next, FULL || c);
+        };
+        if (full < chunks) chunk(full, Whole<false>());
+        for (int c = full - 1; c >= 0; --c) chunk(c, Whole<true>());
+    }
+    // chunks past the sequence's end
+    for (int c = chunks; queries && c < a.s.nc; ++c) {
+        const float zeros[4] = {};
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                float x[8];
-                widen8<DT>(only<DT>(fg[n][ks], v0 + n * 16 + col < a.d.V), x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] *= feq[ks].lo[e];
-                    x[4 + e] *= feq[ks].hi[e];
-                }
-                split8<3>(x, g[n][ks]);
-            }
-        load_dy(next, FULL || whole);
-        Sums<2> sum[kMT][NT];
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                if constexpr (kLate) fq[i][ks] = turned(qrow[i], c, ks, FULL);
-                u32x4 q[TI];
-                planes_of<DT>(only<DT>(fq[i][ks], (wave * kMT + i) * 16 + col < a.d.P), q);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) sum[i][n].add(q, g[n][ks]);
-            }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                u32x4 w[3];
-                get_planes<3>(Wp + (n * 16 + col) * kPitchT + ks * 32 + grp * 8, kPlaneT, w);
-#pragma unroll
-                for (int i = 0; i < kMT; ++i) {
-                    if constexpr (kLate) ft[i][ks] = turned(krow[i], c, ks, FULL);
-                    u32x4 k[TI];
-                    planes_of<DT>(only<DT>(ft[i][ks], (wave * kMT + i) * 16 + col < a.d.P), k);
-                    sum[i][n].add(k, w);
-                }
-            }
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * last + sum[i][n].total();
-        if constexpr (!kLate) load_turned(next, FULL || whole);
-        put_state();
-    };
-    if (full < chunks) chunk(full, Whole<false>());
-    for (int c = full - 1; c >= 0; --c) chunk(c, Whole<true>());
-    {
-        float *to = a.first ? a.d.d_initial_state : state_out;
+            if (v0 + n * 16 + col < a.d.V)
+                store4_until<DT>(row_of<DT>(a.d.dv, B, h * a.d.V + v0 + n * 16 + col), steps_first + (c + 1) * kDeltaChunk <= a.d.L,
+                                 steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+    }
+    float *to = a.first ? a.d.d_initial_state : state_out;
+    if (to && owner) {
         const int P = a.first ? a.d.P : DK, V = a.first ? a.d.V : a.Vp;
         const long long at = a.first ? (long long)B * a.d.Hv + h : bh;
-        if (to) {
 #pragma unroll
-            for (int i = 0; i < kMT; ++i)
+        for (int i = 0; i < kMT; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
-                        if (p < P && v < V) to[(at * P + p) * V + v] = S[i][n][r];
-                    }
-        }
+                for (int r = 0; r < 4; ++r) {
+                    const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
+                    if (p < P && v < V) to[(at * P + p) * V + v] = S[i][n][r];
+                }
     }
 }
 
@@ -711,7 +786,7 @@ template <int DT, int DK>
 int backward(DeltaArgs a, hipStream_t st) {
     float *carry = (float *)(a.ws + a.w.state);
     a.slices = a.Vp / 16;
-    hipLaunchKernelGGL((delta_bwd_kernel<DT, DK, 1>), dim3((unsigned)(a.s.nb * a.d.Hv * a.slices)), dim3(256), 0, st, a,
+    hipLaunchKernelGGL((delta_bwd_kernel<DT, DK, 1>), dim3((unsigned)(a.s.nb * a.d.Hv * a.slices)), dim3(512), 0, st, a,
                        carry, carry);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }

@@ -109,20 +109,6 @@ struct Sums {
     }
 };
 
-// Eight fp32 values of a fragment stored as [lane][8] fp32.
-struct Eight {
-    f32x4 lo, hi;
-};
-DEVI Eight fragment32(const char *at, int frag) {
-    const f32x4 *p = (const f32x4 *)(at + frag * 2048 + (threadIdx.x & 63) * 32);
-    return {p[0], p[1]};
-}
-template <int N>
-DEVI void planes_of(const Eight &e, u32x4 (&v)[N]) {
-    const float f[8] = {e.lo[0], e.lo[1], e.lo[2], e.lo[3], e.hi[0], e.hi[1], e.hi[2], e.hi[3]};
-    split8<N>(f, v);
-}
-
 template <bool W>
 struct Whole {
     static constexpr bool value = W;

@@ -5,27 +5,30 @@ namespace miconv {
 
 namespace {
 
-// One work-group of four waves carries a value slice of NT * 16 channels of one head through time; the
-// state [DK][NT * 16] stays in accumulators.  A wave owns 16 of a chunk's 64 steps in the products with the state
-// and with the inverse, and DK / 4 key channels of the state.  Row operands come from memory in operand
-// order, the next chunk's as soon as this one's are used; what waves exchange (the state's planes, X, u) are column
-// operands in LDS, [channel][step or key channel], rows padded by 8 against bank conflicts.
+// One work-group carries a value slice of NT * 16 channels of one head through time; the state [DK][NT * 16] stays in
+// accumulators, key channels of it in each of the eight waves.  A chunk is a chain that no step of can wait:
+// k S, the inverse times X = v - e (k S), the state's update.  Four waves (16 steps each) go along it; the four others meanwhile compute y,
+// of the chunk before while the first ones multiply k S, and q S while those multiply by the inverse.  Row operands come from memory in
+// operand order, the next chunk's as soon as this one's are used; what waves exchange (planes of the state, X and u f, and u) are column
+// operands in LDS, [channel][step or key channel], rows padded by 16 bytes against bank conflicts.
 template <int DK, int NT>
 struct Scan {
-    static constexpr int kKS = DK / 32, kMT = DK / 64, kN = NT * 16;
+    static constexpr int kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = NT * 16;
     static constexpr int kPitchS = DK + 8, kPitchT = kDeltaChunk + 8;   // bf16 elements
     static constexpr int kPlaneS = kN * kPitchS, kPlaneT = kN * kPitchT;
 };
 
 template <int DT, int DK, int NT, bool SAVE>
-__global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
+__global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
     constexpr int TI = in_planes(DT), OO = out_order(DT), OP = OO + 1;
     typedef Scan<DK, NT> X;
     typedef typename Elem<DT>::T T;
-    __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * X::kPlaneS], Xp[3 * X::kPlaneT], Up[OP * X::kPlaneT],
-        Uf[3 * X::kPlaneT];
+    constexpr int kPitchU = kDeltaChunk + 4;   // floats
+    __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * X::kPlaneS], Xp[3 * X::kPlaneT], Uf[3 * X::kPlaneT];
+    __shared__ __attribute__((aligned(16))) float Us[2][X::kN * kPitchU];      // u of this chunk and the one before
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
-    const int row4 = grp * 4, mine = wave * 16 + row4;             // a lane's four steps
+    const bool queries = wave >= 4, owner = wave * X::kMT < X::kTiles;
+    const int part = wave & 3, row4 = grp * 4, mine = part * 16 + row4;     // a lane's four steps
     // the slices of a head side by side on one XCD: they share its operands in the L2
     const int total = a.s.nb * a.d.Hv * a.slices;
     const int id = xcd_remap(blockIdx.x, total);
@@ -53,6 +56,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
                 }
     }
     const auto put_state = [&] {
+        if (!owner) return;
 #pragma unroll
         for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
@@ -62,67 +66,30 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
             }
     };
     put_state();
+    for (int i = threadIdx.x; i < 3 * X::kN * 8; i += 512)      // the zeros behind X's steps
+        Xp[i / (X::kN * 8) * X::kPlaneT + i / 8 % X::kN * X::kPitchT + kDeltaChunk + i % 8] = 0;
 
     const size_t of_k = ((size_t)b * a.s.nc * a.d.Hk + hk) * TI * 64 * DK * 2, step_k = (size_t)a.d.Hk * TI * 64 * DK * 2;
     const size_t of_v = (size_t)b * a.s.nc * a.d.Hv + h;
     constexpr int kPlaneK = 64 * DK * 2;
-    // three planes of 256 key channels are more than the registers hold ahead of their use
-    constexpr bool kLate = TI == 3 && DK == 256;
-    u32x4 fk[X::kKS][TI], fq[X::kKS][TI];
-    Raw8<DT> ft[X::kMT][2];
-    Eight fi[2], fa[2];
-    Raw4<DT> vin[NT];
-    f32x4 vek, veq, vfk, vbeta, nek, neq, nfk, nbeta;              // of this chunk, and of the next
-    float last = 0.0f, nlast = 0.0f;
-    const char *pk = a.ws + a.w.k + of_k, *pq = a.ws + a.w.q + of_k;
-    const char *pi = a.ws + a.w.inv + of_v * 16384, *pa = a.ws + a.w.attn + of_v * 16384;
-    const char *ps = a.ws + a.w.steps + of_v * sizeof(DeltaSteps);
-    const T *vrow[NT];
-    T *yrow[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int v = v0 + n * 16 + col, at = h * a.d.V + (v < a.d.V ? v : 0);
-        vrow[n] = row_of<DT>(a.d.v, B, at);
-        yrow[n] = row_of<DT>(a.d.y, B, at);
-    }
-    const auto load_kq = [&](int c) {
-#pragma unroll
-        for (int ks = 0; ks < X::kKS; ++ks) {
-            fragment<TI>(pk + c * step_k, wave * X::kKS + ks, kPlaneK, fk[ks]);
-            if constexpr (!kLate) fragment<TI>(pq + c * step_k, wave * X::kKS + ks, kPlaneK, fq[ks]);
-        }
-    };
-    const auto load_steps = [&](int c) {
-        const DeltaSteps *s = (const DeltaSteps *)(ps + (size_t)c * a.d.Hv * sizeof(DeltaSteps));
-        nek = *(const f32x4 *)(s->ek + mine);
-        neq = *(const f32x4 *)(s->eq + mine);
-        nfk = *(const f32x4 *)(s->fk + mine);
-        nbeta = *(const f32x4 *)(s->beta + mine);
-        nlast = s->last;
-    };
-    const auto load_v = [&](int c, bool whole) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) vin[n] = steps4<DT>(vrow[n], whole, steps_first + c * kDeltaChunk + mine, valid);
-    };
-    // the second 32 columns of rows 0..31 are zero and not stored
-    const Eight nothing = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    fi[1] = fa[1] = nothing;
-    const auto load_inverse = [&](int c) {
-        const char *i = pi + (size_t)c * a.d.Hv * 16384;
-        fi[0] = fragment32(i, wave * 2);
-        if (wave >= 2) fi[1] = fragment32(i, wave * 2 + 1);
-    };
-    const auto load_attn = [&](int c) {
-        const char *at = pa + (size_t)c * a.d.Hv * 16384;
-        fa[0] = fragment32(at, wave * 2);
-        if (wave >= 2) fa[1] = fragment32(at, wave * 2 + 1);
-    };
+    // three planes of 128 key channels are more than the registers hold ahead of their use
+    constexpr bool kLate = TI == 3 && DK >= 128;
+    u32x4 fx[kLate ? 1 : X::kKS][TI];          // keys or queries
+    const char *px = a.ws + (queries ? a.w.q : a.w.k) + of_k, *pi = a.ws + a.w.inv + of_v * 3 * kDeltaSquare;
+    const char *pa = a.ws + a.w.attn + of_v * OP * kDeltaSquare, *ps = a.ws + a.w.steps + of_v * sizeof(DeltaSteps);
     const T *krow[X::kMT];
 #pragma unroll
     for (int i = 0; i < X::kMT; ++i) {
         const int p = (wave * X::kMT + i) * 16 + col;
         krow[i] = row_of<DT>(a.d.k, B, hk * a.d.P + (p < a.d.P ? p : 0));
     }
+    Raw8<DT> ft[X::kMT][2];
+    float last = 0.0f;
+    const auto steps_of = [&](int c) { return (const DeltaSteps *)(ps + (size_t)c * a.d.Hv * sizeof(DeltaSteps)); };
+    const auto load_x = [&](int c) {
+#pragma unroll
+        for (int ks = 0; ks < X::kKS && !kLate; ++ks) fragment<TI>(px + c * step_k, part * X::kKS + ks, kPlaneK, fx[ks]);
+    };
     const auto load_kt = [&](int c, bool whole) {
 #pragma unroll
         for (int i = 0; i < X::kMT; ++i)
@@ -130,36 +97,24 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
             for (int ks = 0; ks < 2; ++ks)
                 ft[i][ks] = steps8<DT>(krow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
     };
+    const auto times_state = [&](int c, f32x4 (&xS)[NT]) {
+        Sums<2> sum[NT];
+#pragma unroll
+        for (int ks = 0; ks < X::kKS; ++ks) {
+            if constexpr (kLate) fragment<TI>(px + c * step_k, part * X::kKS + ks, kPlaneK, fx[0]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                u32x4 s[3];
+                get_planes<3>(Sp + (n * 16 + col) * X::kPitchS + ks * 32 + grp * 8, X::kPlaneS, s);
+                sum[n].add(fx[kLate ? 0 : ks], s);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xS[n] = sum[n].total();
+    };
     float *saved = SAVE ? (float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0) * delta_saved(a.d.P, a.d.V) : nullptr;
-
-    // Chunks of 64 valid steps, and the one that ends inside, if any, whose loads look at each step.  A chunk's loads
-    // for the next one stand without a branch (after the last they load it again), so that a chunk is one block
-    // of code: no wait is counted along a way that was not taken.
-    int full = (valid - steps_first) / kDeltaChunk;
-    full = valid <= steps_first ? 0 : (full < chunks ? full : chunks);
-    if (chunks) {
-        load_steps(0);
-        load_kq(0);
-        load_inverse(0);
-        load_attn(0);
-        if (full) {
-            load_v(0, true);
-            if constexpr (!kLate) load_kt(0, true);
-        }
-    }
-    const auto chunk = [&](const int c, auto is_full) {
-        constexpr bool FULL = decltype(is_full)::value;
-        const int next = c + 1 < chunks ? c + 1 : c, next_full = c + 1 < full ? c + 1 : c;
-        vek = nek;
-        veq = neq;
-        vfk = nfk;
-        vbeta = nbeta;
-        last = nlast;
-        if constexpr (!FULL) {
-            load_v(c, false);
-            if constexpr (!kLate) load_kt(c, false);
-        }
-        if constexpr (SAVE) {
+    const auto save_state = [&] {
+        if (SAVE && owner) {
 #pragma unroll
             for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
@@ -168,75 +123,9 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
                     for (int r = 0; r < 4; ++r)
                         saved[(size_t)((wave * X::kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
         }
-        __syncthreads();
-        Sums<2> ks_[NT];
-        Sums<OO> qs[NT];
-#pragma unroll
-        for (int ks = 0; ks < X::kKS; ++ks)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                u32x4 s[3];
-                get_planes<3>(Sp + (n * 16 + col) * X::kPitchS + ks * 32 + grp * 8, X::kPlaneS, s);
-                if constexpr (kLate) fragment<TI>(pq + c * step_k, wave * X::kKS + ks, kPlaneK, fq[ks]);
-                ks_[n].add(fk[ks], s);
-                qs[n].add(fq[ks], s);
-            }
-        f32x4 kS[NT], qS[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            kS[n] = ks_[n].total();
-            qS[n] = qs[n].total();
-        }
-        // loads come back in their order, stores among them: the next chunk's factors, first of all needed, go first
-        load_steps(next);
-        load_kq(next);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float x[4];
-            widen4<DT>(vin[n], v0 + n * 16 + col < a.d.V, x);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], kS[n][r], x[r]);
-            put_planes<3>(Xp + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, x);
-        }
-        if constexpr (FULL) load_v(next_full, true);
-        __syncthreads();
-        f32x4 z[NT];
-        {
-            u32x4 i0[3], i1[3];
-            planes_of<3>(fi[0], i0);
-            planes_of<3>(fi[1], i1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> sum;
-                u32x4 x[3];
-                const uint16_t *from = Xp + (n * 16 + col) * X::kPitchT + grp * 8;
-                get_planes<3>(from, X::kPlaneT, x);
-                sum.add(i0, x);
-                get_planes<3>(from + 32, X::kPlaneT, x);
-                sum.add(i1, x);
-                z[n] = sum.total();
-            }
-        }
-        load_inverse(next);
-        if constexpr (kLate) load_kt(c, FULL);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float u[4], uf[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                u[r] = vbeta[r] * z[n][r];
-                uf[r] = u[r] * vfk[r];
-            }
-            put_planes<3>(Uf + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, uf);
-            put_planes<OP>(Up + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, u);
-            if constexpr (SAVE)
-                *(f32x4 *)(saved + (size_t)DK * a.Vp + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = z[n];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < X::kMT; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) S[i][n] *= last;
+    };
+    const auto update = [&] {
+        if (!owner) return;
 #pragma unroll
         for (int i = 0; i < X::kMT; ++i) {
             u32x4 k0[TI], k1[TI];
@@ -252,67 +141,201 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a, float *stat
                 sum.add(k0, u);
                 get_planes<3>(from + 32, X::kPlaneT, u);
                 sum.add(k1, u);
-                S[i][n] += sum.total();
+                S[i][n] = S[i][n] * last + sum.total();
             }
         }
-        if constexpr (!kLate && FULL) load_kt(next_full, true);
         put_state();
-        // y
-        u32x4 a0[OP], a1[OP];
-        planes_of<OP>(fa[0], a0);
-        planes_of<OP>(fa[1], a1);
+    };
+
+    // Chunks of 64 valid steps, and the one that ends inside, if any, whose loads look at each step.  Both kinds of waves have a loop of
+    // their own, and a chunk's loads for the next one (after the last, for itself again) depend on no branch: where two
+    // ways meet, what they loaded is moved, and waited for.
+    int full = (valid - steps_first) / kDeltaChunk;
+    full = valid <= steps_first ? 0 : (full < chunks ? full : chunks);
+    const bool upper = part >= 2;              // the second 32 columns of rows 0..31 of the inverse and of attn are not stored
+    if (chunks) {
+        load_x(0);
+        if (full) load_kt(0, true);
+        last = steps_of(0)->last;
+    }
+    if (!chunks) {
+    } else if (!queries) {
+        u32x4 fi[2][3];
+        Raw4<DT> vin[NT];
+        const T *vrow[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            Sums<OO> o;
-            u32x4 u[OP];
-            const uint16_t *from = Up + (n * 16 + col) * X::kPitchT + grp * 8;
-            get_planes<OP>(from, X::kPlaneT, u);
-            o.add(a0, u);
-            get_planes<OP>(from + 32, X::kPlaneT, u);
-            o.add(a1, u);
-                const f32x4 p = o.total();
-            float y[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(veq[r], qS[n][r], p[r]);
-            if (v0 + n * 16 + col < a.d.V) {
-                const int t = steps_first + c * kDeltaChunk + mine;
-                // past the sequence's end: zeros, up to the end of the rows
-                if constexpr (!FULL) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
-                }
-                store4_until<DT>(yrow[n], FULL, t, a.d.L, y);
-            }
+            const int v = v0 + n * 16 + col;
+            vrow[n] = row_of<DT>(a.d.v, B, h * a.d.V + (v < a.d.V ? v : 0));
         }
-        load_attn(next);
-        if constexpr (SAVE) saved += delta_saved(a.d.P, a.d.V);
-    };
-    for (int c = 0; c < full; ++c) chunk(c, Whole<true>());
-    if (full < chunks) chunk(full, Whole<false>());
+        const auto load_inverse = [&](int c) {
+            const char *at = pi + (size_t)c * a.d.Hv * 3 * kDeltaSquare;
+            fragment<3>(at, part * 2, kDeltaSquare, fi[0]);
+            fragment<3>(at, part * 2 + upper, kDeltaSquare, fi[1]);
+        };
+        const auto load_v = [&](int c, bool whole) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) vin[n] = steps4<DT>(vrow[n], whole, steps_first + c * kDeltaChunk + mine, valid);
+        };
+        load_inverse(0);
+        f32x4 vek = *(const f32x4 *)(steps_of(0)->ek + mine), vfk = *(const f32x4 *)(steps_of(0)->fk + mine);
+        f32x4 vbeta = *(const f32x4 *)(steps_of(0)->beta + mine);
+        if (full) load_v(0, true);
+        // rows 0..31 meet the second fragment with the zeros behind each channel's 64 steps
+        const int second = upper ? 32 : kDeltaChunk - grp * 8;
+        const auto chunk = [&](const int c, auto is_full) {
+            constexpr bool FULL = decltype(is_full)::value;
+            const int next = c + 1 < chunks ? c + 1 : c, next_full = c + 1 < full ? c + 1 : c;
+            if constexpr (!FULL) {
+                load_v(c, false);
+                load_kt(c, false);
+            }
+            save_state();
+            __syncthreads();
+            f32x4 kS[NT];
+            times_state(c, kS);
+            load_x(next);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[4];
+                widen4<DT>(vin[n], v0 + n * 16 + col < a.d.V, x);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], kS[n][r], x[r]);
+                put_planes<3>(Xp + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, x);
+            }
+            vek = *(const f32x4 *)(steps_of(next)->ek + mine);
+            if constexpr (FULL) load_v(next_full, true);
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                Sums<2> sum;
+                u32x4 x[3];
+                const uint16_t *from = Xp + (n * 16 + col) * X::kPitchT + grp * 8;
+                get_planes<3>(from, X::kPlaneT, x);
+                sum.add(fi[0], x);
+                get_planes<3>(from + second, X::kPlaneT, x);
+                sum.add(fi[1], x);
+                const f32x4 z = sum.total(), u = z * vbeta;
+                float uf[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) uf[r] = u[r] * vfk[r];
+                put_planes<3>(Uf + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, uf);
+                *(f32x4 *)(Us[c & 1] + (n * 16 + col) * kPitchU + mine) = u;
+                if constexpr (SAVE)
+                    *(f32x4 *)(saved + (size_t)DK * a.Vp + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = z;
+            }
+            load_inverse(next);
+            vfk = *(const f32x4 *)(steps_of(next)->fk + mine);
+            vbeta = *(const f32x4 *)(steps_of(next)->beta + mine);
+            __syncthreads();
+            update();
+            last = steps_of(next)->last;
+            if constexpr (FULL) load_kt(next_full, true);
+            if constexpr (SAVE) saved += delta_saved(a.d.P, a.d.V);
+        };
+        for (int c = 0; c < full; ++c) chunk(c, Whole<true>());
+        if (full < chunks) chunk(full, Whole<false>());
+    } else {
+        u32x4 fa[2][OP];
+        f32x4 veq = {0, 0, 0, 0}, qS[NT];
+        T *yrow[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int v = v0 + n * 16 + col;
+            yrow[n] = row_of<DT>(a.d.y, B, h * a.d.V + (v < a.d.V ? v : 0));
+            qS[n] = f32x4{0, 0, 0, 0};
+        }
+        const auto load_attn = [&](int c) {
+            const char *at = pa + (size_t)c * a.d.Hv * OP * kDeltaSquare;
+            fragment<OP>(at, part * 2, kDeltaSquare, fa[0]);
+            fragment<OP>(at, part * 2 + upper, kDeltaSquare, fa[1]);
+            veq = *(const f32x4 *)(steps_of(c)->eq + mine);
+        };
+        // y of chunk c, whose u is in Us[c & 1]
+        const auto put_y = [&](const int c, auto is_full) {
+            constexpr bool FULL = decltype(is_full)::value;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                Sums<OO> o;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const f32x4 *from = (const f32x4 *)(Us[c & 1] + (n * 16 + col) * kPitchU + ks * 32 + grp * 8);
+                    const f32x4 lo = from[0], hi = from[1];
+                    float u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = ks == 0 || upper ? u[e] : 0.0f;
+                    u32x4 planes[OP];
+                    split8<OP>(u, planes);
+                    o.add(fa[ks], planes);
+                }
+                const f32x4 p = o.total();
+                float y[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(veq[r], qS[n][r], p[r]);
+                if (v0 + n * 16 + col < a.d.V) {
+                    const int t = steps_first + c * kDeltaChunk + mine;
+                    // past the sequence's end: zeros, up to the end of the rows
+                    if constexpr (!FULL) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
+                    }
+                    store4_until<DT>(yrow[n], FULL, t, a.d.L, y);
+                }
+            }
+        };
+        const auto chunk = [&](const int c, auto is_full, auto is_first) {
+            constexpr bool FULL = decltype(is_full)::value, FIRST = decltype(is_first)::value;
+            const int next = c + 1 < chunks ? c + 1 : c, next_full = c + 1 < full ? c + 1 : c;
+            if constexpr (!FULL) load_kt(c, false);
+            save_state();
+            __syncthreads();
+            if constexpr (!FIRST) put_y(c - 1, Whole<true>());
+            load_attn(c);
+            __syncthreads();
+            times_state(c, qS);
+            load_x(next);
+            __syncthreads();
+            update();
+            last = steps_of(next)->last;
+            if constexpr (FULL) load_kt(next_full, true);
+            if constexpr (SAVE) saved += delta_saved(a.d.P, a.d.V);
+        };
+        if (full) {
+            chunk(0, Whole<true>(), Whole<true>());
+            for (int c = 1; c < full; ++c) chunk(c, Whole<true>(), Whole<false>());
+            if (full < chunks) {
+                chunk(full, Whole<false>(), Whole<false>());
+                put_y(full, Whole<false>());
+            } else {
+                put_y(full - 1, Whole<true>());
+            }
+        } else {
+            chunk(0, Whole<false>(), Whole<true>());
+            put_y(0, Whole<false>());
+        }
+    }
     // chunks past the sequence's end
-    for (int c = chunks; c < a.s.nc; ++c) {
+    for (int c = chunks; queries && c < a.s.nc; ++c) {
         const float zeros[4] = {};
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             if (v0 + n * 16 + col < a.d.V)
-                store4_until<DT>(yrow[n], steps_first + (c + 1) * kDeltaChunk <= a.d.L, steps_first + c * kDeltaChunk + mine,
-                                 a.d.L, zeros);
+                store4_until<DT>(row_of<DT>(a.d.y, B, h * a.d.V + v0 + n * 16 + col), steps_first + (c + 1) * kDeltaChunk <= a.d.L,
+                                 steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
     }
-    {
-        float *out = a.last ? a.d.final_state : state_out;
+    float *out = a.last ? a.d.final_state : state_out;
+    if (out && owner) {
         const int P = a.last ? a.d.P : DK, V = a.last ? a.d.V : a.Vp;
         const long long at = a.last ? (long long)B * a.d.Hv + h : bh;
-        if (out) {
 #pragma unroll
-            for (int i = 0; i < X::kMT; ++i)
+        for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
-                        if (p < P && v < V) out[(at * P + p) * V + v] = S[i][n][r];
-                    }
-        }
+                for (int r = 0; r < 4; ++r) {
+                    const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
+                    if (p < P && v < V) out[(at * P + p) * V + v] = S[i][n][r];
+                }
     }
 }
 
@@ -321,9 +344,9 @@ int forward(const DeltaArgs &a, hipStream_t st) {
     float *carry = (float *)(a.ws + a.w.state);
     const unsigned groups = (unsigned)(a.s.nb * a.d.Hv * a.slices);
     if (a.d.states)
-        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, true>), dim3(groups), dim3(256), 0, st, a, carry, carry);
+        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, true>), dim3(groups), dim3(512), 0, st, a, carry, carry);
     else
-        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, false>), dim3(groups), dim3(256), 0, st, a, carry, carry);
+        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, false>), dim3(groups), dim3(512), 0, st, a, carry, carry);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }
 

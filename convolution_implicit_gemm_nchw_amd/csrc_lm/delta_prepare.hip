@@ -155,14 +155,15 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     // The system's matrix (its diagonal of ones left out), and the products of queries with keys, which go to memory
     // from here.  A block of 32 columns past the diagonal is never read.
     const int col = lane & 15, row4 = (lane >> 4) * 4;
-    char *const inv = a.ws + a.w.inv + of_v * 16384, *const attn = a.ws + a.w.attn + of_v * 16384;
+    constexpr int kPlanes = delta_attn_planes(DT, BWD);
+    char *const inv = a.ws + a.w.inv + of_v * 3 * kDeltaSquare, *const attn = a.ws + a.w.attn + of_v * kPlanes * kDeltaSquare;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         if (n > (wave | 1)) break;
         const int j = n * 16 + col;
         const double Gj = steps.G[j];
         const float rkj = steps.rk[j], bj = steps.beta[j];
-        f32x4 m;
+        float m[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = wave * 16 + row4 + r;
@@ -182,7 +183,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
         }
         // row tile, block of 32 columns, and the half of it, of the four values
         const int tile = BWD ? n : wave, block = (BWD ? wave : n) >> 1, eight = ((BWD ? wave : n) & 1) * 2 + (lane >> 5);
-        *(f32x4 *)(attn + (tile * 2 + block) * 2048 + (col + eight * 16) * 32 + (lane >> 4 & 1) * 16) = m;
+        put_planes<kPlanes>((uint16_t *)(attn + (tile * 2 + block) * 1024 + (col + eight * 16) * 16 + (lane >> 4 & 1) * 8),
+                            kDeltaSquare / 2, m);
     }
     __syncthreads();
 
@@ -258,9 +260,12 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
         const int f = half * 4 + wave, tile = f >> 1, ks = f & 1;
         if (BWD ? (tile >= 2 && ks == 0) : (tile < 2 && ks == 1)) continue;
         const float *from = Tm + (tile * 16 + col) * kRow + ks * 32 + (lane >> 4) * 8;
-        f32x4 *const to = (f32x4 *)(inv + f * 2048 + lane * 32);
-        to[0] = *(const f32x4 *)from;
-        to[1] = *(const f32x4 *)(from + 4);
+        const f32x4 lo = *(const f32x4 *)from, hi = *(const f32x4 *)(from + 4);
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        u32x4 planes[3];
+        split8<3>(v, planes);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *(u32x4 *)(inv + p * kDeltaSquare + f * 1024 + lane * 16) = planes[p];
     }
     if (tid < (int)(sizeof(DeltaSteps) / 16))
         ((u32x4 *)(a.ws + a.w.steps + of_v * sizeof(DeltaSteps)))[tid] = ((const u32x4 *)&steps)[tid];
