@@ -308,10 +308,7 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
         const auto chunk = [&](const int c, auto is_full) {
             constexpr bool FULL = decltype(is_full)::value;
             const int next = c ? c - 1 : 0;
-            save_state(c);
-            __syncthreads();
-            f32x4 given[kMT][NT];
-            u32x4 g[NT][2][3];
+            u32x4 g[NT][2][3];                     // e dy, split while the other waves finish the chunk before
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -321,7 +318,12 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] *= veq[ks][e >> 2][e & 3];
                     split8<3>(x, g[n][ks]);
+#pragma unroll
+                    for (int o = 0; o < 3; ++o) asm volatile("" : "+v"(g[n][ks][o]));
                 }
+            save_state(c);
+            __syncthreads();
+            f32x4 given[kMT][NT];
 #pragma unroll
             for (int i = 0; i < 2 * kMT; ++i) {
                 const int tile = tile_of(i);

@@ -252,8 +252,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             veq = *(const f32x4 *)(steps_of(c)->eq + mine);
         };
         // y of chunk c, whose u is in Us[c & 1]
-        const auto put_y = [&](const int c, auto is_full) {
-            constexpr bool FULL = decltype(is_full)::value;
+        const auto make_y = [&](const int c, float (&y)[NT][4]) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 Sums<OO> o;
@@ -269,19 +268,31 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
                     o.add(fa[ks], planes);
                 }
                 const f32x4 p = o.total();
-                float y[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(veq[r], qS[n][r], p[r]);
+                for (int r = 0; r < 4; ++r) {
+                    y[n][r] = __builtin_fmaf(veq[r], qS[n][r], p[r]);
+                    asm volatile("" : "+v"(y[n][r]));
+                }
+            }
+        };
+        const auto put_y = [&](const int c, auto is_full, float (&y)[NT][4]) {
+            constexpr bool FULL = decltype(is_full)::value;
+            const int t = steps_first + c * kDeltaChunk + mine;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
                 if (v0 + n * 16 + col < a.d.V) {
-                    const int t = steps_first + c * kDeltaChunk + mine;
                     // past the sequence's end: zeros, up to the end of the rows
                     if constexpr (!FULL) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
+                        for (int r = 0; r < 4; ++r) y[n][r] = t + r < valid ? y[n][r] : 0.0f;
                     }
-                    store4_until<DT>(yrow[n], FULL, t, a.d.L, y);
+                    store4_until<DT>(yrow[n], FULL, t, a.d.L, y[n]);
                 }
-            }
+        };
+        const auto finish = [&](const int c, auto is_full) {
+            float y[NT][4];
+            make_y(c, y);
+            put_y(c, is_full, y);
         };
         const auto chunk = [&](const int c, auto is_full, auto is_first) {
             constexpr bool FULL = decltype(is_full)::value, FIRST = decltype(is_first)::value;
@@ -289,9 +300,12 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             if constexpr (!FULL) load_kt(c, false);
             save_state();
             __syncthreads();
-            if constexpr (!FIRST) put_y(c - 1, Whole<true>());
-            load_attn(c);
+            // the waves of the state are ahead till their x stands, and behind after it: y is stored then
+            float y[NT][4];
+            if constexpr (!FIRST) make_y(c - 1, y);
             __syncthreads();
+            load_attn(c);
+            if constexpr (!FIRST) put_y(c - 1, Whole<true>(), y);
             times_state(c, qS);
             load_x(next);
             __syncthreads();
@@ -305,13 +319,13 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             for (int c = 1; c < full; ++c) chunk(c, Whole<true>(), Whole<false>());
             if (full < chunks) {
                 chunk(full, Whole<false>(), Whole<false>());
-                put_y(full, Whole<false>());
+                finish(full, Whole<false>());
             } else {
-                put_y(full - 1, Whole<true>());
+                finish(full - 1, Whole<true>());
             }
         } else {
             chunk(0, Whole<false>(), Whole<true>());
-            put_y(0, Whole<false>());
+            finish(0, Whole<false>());
         }
     }
     // chunks past the sequence's end
