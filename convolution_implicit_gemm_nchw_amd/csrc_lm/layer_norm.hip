@@ -111,18 +111,18 @@ __global__ __launch_bounds__(Row<ROW>::kThreads) void norm_fwd_kernel(miconv_lay
     }
 }
 
-// Every work-group (ROW 64: every wave) takes every `parts`-th token, its channels' sums of dw and db in registers.
+// Work-group p takes tokens p, p + parts, ... (ROW 64: four at a time, one a wave), its channels' sums of dw and db
+// in registers; the four waves' sums are joined in LDS, which leaves a quarter of the rows to write and read again.
 template <int DT, int ROW, int VPT>
 __global__ __launch_bounds__(Row<ROW>::kThreads) void norm_bwd_kernel(miconv_layer_norm_t a, FDiv by_length, int parts,
                                                                       float *part) {
     typedef Row<ROW> X;
     typedef typename Elem<DT>::T T;
     __shared__ float red[X::kWaves][2];
-    const int in = threadIdx.x % ROW, p = blockIdx.x * X::kTokens + threadIdx.x / ROW;
-    if (p >= parts) return;
+    const int in = threadIdx.x % ROW, p = blockIdx.x * X::kTokens + threadIdx.x / ROW, step = parts * X::kTokens;
     float dw[VPT][8] = {}, db[VPT][8] = {};
     const uint32_t tokens = (uint32_t)a.B * a.L;
-    for (uint32_t token = p; token < tokens; token += parts) {
+    for (uint32_t token = p; token < tokens; token += step) {
         const int b = (int)fdiv(token, by_length), l = (int)token - b * a.L;
         T *const dx = token_of<DT>(a.dx, b, l);
         const bool valid = l < valid_steps(a.lengths, b, a.L);
@@ -162,7 +162,27 @@ __global__ __launch_bounds__(Row<ROW>::kThreads) void norm_bwd_kernel(miconv_lay
             store8<DT>(dx, (i * ROW + in) * 8, a.C, h[i]);
         }
     }
-    float *const mine = part + (size_t)p * 2 * a.C;
+    float *const mine = part + (size_t)blockIdx.x * 2 * a.C;
+    if constexpr (X::kTokens > 1) {
+        __shared__ float joined[X::kTokens][2][VPT * 64][8];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            *(f32x4 *)&joined[threadIdx.x / ROW][0][i * ROW + in][0] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+            *(f32x4 *)&joined[threadIdx.x / ROW][0][i * ROW + in][4] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+            *(f32x4 *)&joined[threadIdx.x / ROW][1][i * ROW + in][0] = f32x4{db[i][0], db[i][1], db[i][2], db[i][3]};
+            *(f32x4 *)&joined[threadIdx.x / ROW][1][i * ROW + in][4] = f32x4{db[i][4], db[i][5], db[i][6], db[i][7]};
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.C; c += X::kThreads)
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                float t = 0.0f;
+#pragma unroll
+                for (int w = 0; w < X::kTokens; ++w) t += joined[w][which][c / 8][c % 8];
+                mine[which * a.C + c] = t;
+            }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         store8<0>(mine, (i * ROW + in) * 8, a.C, dw[i]);
@@ -506,8 +526,17 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float *part, int 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const long long column = (long long)blockIdx.x * 64 + lane, columns = 2ll * C;
     float s = 0.0f;
-    if (column < columns)
-        for (int p = wave; p < parts; p += 16) s += part[p * columns + column];
+    if (column < columns) {
+        int p = wave;
+        for (; p + 112 < parts; p += 128) {      // eight loads in flight: their latency bounds this kernel
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = part[(p + i * 16) * columns + column];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
+        for (; p < parts; p += 16) s += part[p * columns + column];
+    }
     red[wave][lane] = s;
     __syncthreads();
     if (wave || column >= columns) return;
@@ -566,8 +595,7 @@ template <int DT>
 int tokens_bwd(const miconv_layer_norm_t &n, int parts, float *part, hipStream_t st) {
     const FDiv f = make_fdiv((uint32_t)n.L);
 #define MICONV_NORM(ROW, VPT)                                                                                       \
-    hipLaunchKernelGGL((norm_bwd_kernel<DT, ROW, VPT>), dim3((parts + Row<ROW>::kTokens - 1) / Row<ROW>::kTokens),   \
-                       dim3(Row<ROW>::kThreads), 0, st, n, f, parts, part)
+    hipLaunchKernelGGL((norm_bwd_kernel<DT, ROW, VPT>), dim3(parts), dim3(Row<ROW>::kThreads), 0, st, n, f, parts, part)
     if (n.C <= 512)
         MICONV_NORM(64, 1);
     else if (n.C <= 1024)
@@ -631,9 +659,9 @@ bool norm_tokens_first(const miconv_layer_norm_t &n, bool backward) {
 int norm_parts(const miconv_layer_norm_t &n, int dtype, size_t budget) {
     long long most;
     if (norm_tokens_first(n, true)) {
-        most = (long long)n.B * n.L;
-        const long long fill = n.C <= 1024 ? 2048 : 512;         // waves, or work-groups
-        if (most > fill) most = fill;
+        const int at_once = n.C <= 1024 ? Row<64>::kTokens : 1;
+        most = ((long long)n.B * n.L + at_once - 1) / at_once;
+        if (most > 512) most = 512;
     } else {
         const RowsForm f = rows_form(n, dtype, true);
         const int steps = (f.lanes ? f.lanes : 8) * 8;
