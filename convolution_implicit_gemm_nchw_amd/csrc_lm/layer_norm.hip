@@ -400,15 +400,32 @@ __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(miconv_layer_norm_t
         store8<0>(a.stats + (size_t)b * a.L, t, a.L, mean);
         store8<0>(a.stats + ((size_t)a.B + b) * a.L, t, a.L, r);
     }
-#pragma unroll U
-    for (int i = 0; i < rows; ++i) {
-        const int c = i * groups + g;
-        if (c >= a.C) break;
-        row(i, c);
-        const float w = a.weight ? a.weight[c] : 1.0f, o = a.bias ? a.bias[c] : 0.0f;
+    // Four rows' parameters are loaded ahead of the stores before them: loads behind stores would wait for those.
+    constexpr int kAhead = LOOP ? 1 : 4;
+    float w[2][kAhead], o[2][kAhead];
+    const auto params = [&](int i, int set) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = t + e < end ? __builtin_fmaf((v[e] - mean[e]) * r[e], w, o) : 0.0f;
-        store8<DT>(y + (long long)c * a.y.stride_c, t, a.L, v);
+        for (int k = 0; k < kAhead; ++k) {
+            const int c = (i + k) * groups + g, at = c < a.C ? c : a.C - 1;
+            w[set][k] = a.weight ? a.weight[at] : 1.0f;
+            o[set][k] = a.bias ? a.bias[at] : 0.0f;
+        }
+    };
+    params(0, 0);
+    constexpr int UA = LOOP ? 2 : R / kAhead;
+#pragma unroll UA
+    for (int j = 0; j < (LOOP ? rows : R / kAhead); ++j) {
+        if (LOOP || j + 1 < R / kAhead) params((j + 1) * kAhead, (j + 1) % 2);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = j * kAhead + k, c = i * groups + g;
+            if (c >= a.C) return;
+            row(i, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = t + e < end ? __builtin_fmaf((v[e] - mean[e]) * r[e], w[j % 2][k], o[j % 2][k]) : 0.0f;
+            store8<DT>(y + (long long)c * a.y.stride_c, t, a.L, v);
+        }
     }
 }
 
@@ -422,7 +439,20 @@ __global__ __launch_bounds__(512) void norm_rows_bwd_kernel(miconv_layer_norm_t 
     const int p = xcd_remap(blockIdx.x, gridDim.x), tl = threadIdx.x % TL, groups = blockDim.x / TL;
     const int rows = LOOP ? (a.C + groups - 1) / groups : R;
     float *const mine = part + (size_t)p * 2 * a.C;
-    float dw[LOOP ? 1 : R] = {}, db[LOOP ? 1 : R] = {};
+    float dw[LOOP ? 1 : R] = {}, db[LOOP ? 1 : R] = {}, held_w[LOOP ? 1 : R];
+    if constexpr (!LOOP) {                     // held: loads behind the stores of dx would wait for those
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = i * groups + threadIdx.x / TL;
+            held_w[i] = a.weight ? a.weight[c < a.C ? c : a.C - 1] : 1.0f;
+        }
+    }
+    const auto weight = [&](int i, int c) {
+        if constexpr (LOOP)
+            return a.weight ? a.weight[c] : 1.0f;
+        else
+            return held_w[i];
+    };
     bool begun = false;
     for (long long id = p; id < (long long)a.B * tiles; id += parts) {
         const int g = again(threadIdx.x / TL);  // the rows' addresses are not held from tile to tile
@@ -455,7 +485,7 @@ __global__ __launch_bounds__(512) void norm_rows_bwd_kernel(miconv_layer_norm_t 
             const int c = i * groups + g;
             if (c >= a.C) break;
             row(i, c);
-            const float w = a.weight ? a.weight[c] : 1.0f;
+            const float w = weight(i, c);
             float sw = 0.0f, sb = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -496,7 +526,7 @@ __global__ __launch_bounds__(512) void norm_rows_bwd_kernel(miconv_layer_norm_t 
             const int c = i * groups + g;
             if (c >= a.C) break;
             row(i, c);
-            const float w = a.weight ? a.weight[c] : 1.0f;
+            const float w = weight(i, c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[e] = t + e < end ? r[e] * (h[e] * w - s[e] - n[e] * q[e]) : 0.0f;
             store8<DT>(dx + (long long)c * a.dx.stride_c, t, a.L, h);
@@ -565,7 +595,7 @@ struct RowsForm {
 RowsForm rows_form(const miconv_layer_norm_t &n, int dtype, bool backward) {
     const int held = dtype == MICONV_BF16 ? 16 : 8, most = backward ? 512 : 1024;
     int lanes = 8;
-    while (lanes > 1 && (most / lanes * held < n.C || (long long)n.B * ((n.L + lanes * 8 - 1) / (lanes * 8)) < 200)) lanes /= 2;
+    while (lanes > 1 && (most / lanes * held < n.C || (long long)n.B * ((n.L + lanes * 8 - 1) / (lanes * 8)) < (backward ? 200 : 400))) lanes /= 2;
     if (most / lanes * held < n.C) return {0, most};
     int threads = 256;
     while (threads < most && threads / lanes * held < n.C) threads *= 2;
