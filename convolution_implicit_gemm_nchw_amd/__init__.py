@@ -952,8 +952,8 @@ def quantize_f8(x, channel_major=False, q=None, scale=None, stream=None):
     2^e, e >= -127, with max|x| <= 448 * 2^e, and q = x / 2^e rounded to nearest, ties to even.  x as for
     quantize_tokens.  Returns q [tokens, C_pad] float8_e4m3fn (C_pad = C rounded up to 128, zeros past C) and scale
     [C_pad / 128, tokens] float8_e8m0fnu.  A block with an infinity or a NaN becomes NaN.  A weight [O, C] is
-    quantised in the same way; w.t()[None] or dy.t()[None] is channel_major, with blocks along the other axis,
-    as the products of a backward pass take them."""
+    quantised in the same way; w[None] or dy[None] as channel_major has its blocks along the first axis, as the
+    products of a backward pass take them: dx = dy w from (dy, w[None]), dw = dy^T x from (dy[None], x[None])."""
     return _call(_bind.quantize_f8, stream, x, channel_major, q, scale)
 
 

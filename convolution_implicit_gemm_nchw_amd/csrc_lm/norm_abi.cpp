@@ -1,5 +1,6 @@
 // norm_abi.cpp -- the C entry points of layer norm: validation (before anything is enqueued),
 // workspace, launches.
+#include <float.h>
 #include <hip/hip_runtime_api.h>
 
 #include "lm_check.h"
@@ -33,6 +34,7 @@ int layer_norm_fwd(const miconv_layer_norm_t *n, int dtype, void *stream) {
     if (!n) return MICONV_ERR_NULL;
     const int bad_sizes = check_sizes(*n, dtype);
     if (bad_sizes != MICONV_OK) return bad_sizes;
+    if (!(n->eps >= 0.0f && n->eps <= FLT_MAX)) return MICONV_ERR_BAD_DIM;
     const bool first = norm_tokens_first(*n, false);
     if (!first && !(rows_of_steps(*n, n->x) && rows_of_steps(*n, n->y))) return MICONV_ERR_BAD_DIM;
     const size_t es = elem_size(dtype);

@@ -706,7 +706,8 @@ int gated_delta_step(const miconv_gated_delta_t *d, int dtype, const float *stat
  * (mean, then rstd; tokens run over [B, L] in that order), when given, is written by the forward pass and read
  * by the backward pass.  lengths as above: padding is 0 in y and dx, and no part of dw or db.
  * Backward: dy and stats in; dx, and in fp32 dw = sum over tokens of dy * (x - mean) * rstd and
- * db = sum over tokens of dy out, dw and db optional.  C is at most 2^20, B*L at most 2^30.
+ * db = sum over tokens of dy out, dw and db optional.  C is at most 2^20, B*L at most 2^30, eps finite and not
+ * negative (MICONV_ERR_BAD_DIM).
  * Workspace: partial sums of dw and db; the fastest split that fits, 8*C bytes at least
  * (else MICONV_ERR_WORKSPACE).
  */
