@@ -385,16 +385,22 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
 // ------------------------------------------------------------------ the rest of each chunk
 //
 // A work-group takes one chunk of one key head, its value heads in turn, whose gradients of q and k add up in
-// registers.  A wave owns NC tiles of 16 key channels for all 64 steps; the state and dS are its column operands,
-// read from memory once and split in registers.  Z, F and dy stand in LDS as planes [step][value channel],
-// 64 channels at a time; after them, in the same place, dP and dA in both orders.
+// registers.  A wave owns a quarter of the key channels, NC tiles of 16, for half of the 64 steps; the state and dS
+// are its column operands, read from memory and split in registers.  Z, F and dy stand in LDS as planes
+// [step][value channel], 64 channels at a time; after them, in the same place, dP and dA in both orders.
+// One work-group fits a CU (122 KB of LDS, 248 registers), and no phase hides another's waits: of some 60000 cycles
+// 14000 go to Z, F and dy, 15000 to the products with the states (9000 of matrix instructions), 8000 to those with dP
+// and dA.  An eighth of the channels for all steps would split the states once instead of twice: 64 key channels then
+// have 4 waves, and 13 heads of 6599 steps take 230 us instead of 172; at 128 channels both take as long.
+// 2 x 2048 steps of 16 heads, 128 and 128 channels, bf16: 134 us, 2 TB/s of states, Z, F and operands.
 template <int DT, int DK>
 struct Grads {
-    static constexpr int kWaves = DK == 64 ? 4 : 8, kThreads = kWaves * 64, kNC = DK / 16 / kWaves;
-    static constexpr int kTiles = 16 / kWaves;             // column tiles of the 64 x 64 products per wave
+    static constexpr int kWaves = 8, kThreads = kWaves * 64, kNC = DK / 64;
+    static constexpr int kPair = kNC > 1 ? 2 : 1;          // tiles that share what is read of Z, F, dy, dP and dA
+    static constexpr int kTiles = 2;                       // column tiles of the 64 x 64 products per wave
     static constexpr int kPitch = 72, kPlane = 64 * kPitch;   // bf16 elements
     static constexpr int TI = in_planes(DT);
-    static constexpr bool kKeep = DK < 256;
+    static constexpr bool kKeep = DK < 256, kHold = DK < 256, kAhead = DK == 64;
     static constexpr int kValues = 6 + TI, kPlanes = kValues > 12 ? kValues : 12;
 };
 
@@ -410,7 +416,7 @@ DEVI float sum16(float v) {
 template <int DT, int DK>
 __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(DeltaArgs a) {
     typedef Grads<DT, DK> X;
-    constexpr int TI = X::TI, NC = X::kNC, W = X::kWaves, TILES = X::kTiles;
+    constexpr int TI = X::TI, NC = X::kNC, NP = X::kPair, W = X::kWaves, TILES = X::kTiles;
     typedef typename Elem<DT>::T T;
     __shared__ __attribute__((aligned(16))) uint16_t shared[X::kPlanes * X::kPlane];
     __shared__ float rows[W][4][64];           // a wave's part of q.dq, k.(read - write), and q.dq, k.dk in full
@@ -418,11 +424,10 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
     __shared__ float norm_q[64], norm_k[64];   // q.dq and k.dk of all heads, for the normalisation
     __shared__ float diag[64], diag_p[64], e[64], f[64];
     __shared__ __attribute__((aligned(16))) DeltaSteps steps;
-    const int tid = threadIdx.x, wave = uniform(tid >> 6);
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), m0 = (wave >> 2) * 2;   // tiles m0, m0 + 1 of 16 steps
     const int id = a.more + blockIdx.x;
     const int hk = id % a.d.Hk, bc = id / a.d.Hk, c = bc % a.s.nc, b = bc / a.s.nc, B = a.s.b0 + b;
     const int t0 = (a.s.c0 + c) * kDeltaChunk, valid = valid_steps(a.d.lengths, B, a.d.L), end = valid - t0;
-    const bool whole = end >= kDeltaChunk;
     const int stop = a.d.L - t0 < kDeltaChunk ? a.d.L - t0 : kDeltaChunk;     // steps of this chunk in the tensors
     if (end <= 0) {                            // a chunk past the sequence's end
         for (int i = tid; i < a.d.P * kDeltaChunk; i += X::kThreads) {
@@ -439,349 +444,403 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
         }
         return;
     }
-    // The sums over heads stay in registers where these hold them, else in the workspace, each lane's own.
-    f32x4 dq[X::kKeep ? 4 : 1][NC], dk[X::kKeep ? 4 : 1][NC];
-    if constexpr (X::kKeep) {
+    const auto chunk = [&](auto is_whole) {
+        constexpr bool whole = decltype(is_whole)::value;
+        // The sums over heads stay in registers where these hold them, else in the workspace, each lane's own.
+        f32x4 dq[X::kKeep ? 2 : 1][NC], dk[X::kKeep ? 2 : 1][NC];
+        if constexpr (X::kKeep) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int n = 0; n < NC; ++n) dq[m][n] = dk[m][n] = f32x4{0, 0, 0, 0};
-    }
-    if (tid < 64) norm_q[tid] = norm_k[tid] = 0.0f;
-
-    for (int hr = 0; hr < a.rep; ++hr) {
-        const int h = hk * a.rep + hr;
-        // a lane's place, of which the compiler does not know that it is the same for all heads: what is made from
-        // it is then not held in registers from one to the next
-        const int lane = again(tid & 63), col = lane & 15, grp = lane >> 4, row4 = grp * 4;
-        const int d0 = wave * NC * 16 + col;   // key channels d0 + 16 n
-        const size_t of_v = (size_t)bc * a.d.Hv + h;
-        const float *S0 = (const float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0 + c) * delta_saved(a.d.P, a.d.V);
-        const float *Zs = S0 + (size_t)DK * a.Vp;
-        const float *S1 = (const float *)(a.ws + a.w.after) + of_v * DK * a.Vp;
-        const float *Fs = (const float *)(a.ws + a.w.F) + of_v * a.Vp * kDeltaChunk;
-        __syncthreads();                       // the head before has read steps, shared and rows
-        if (tid < (int)(sizeof(DeltaSteps) / 16))
-            ((u32x4 *)&steps)[tid] = ((const u32x4 *)(a.ws + a.w.steps + of_v * sizeof(DeltaSteps)))[tid];
-        f32x4 q_[4][NC], read[4][NC], write[4][NC], FZ[TILES], OZ[TILES];
+                for (int n = 0; n < NC; ++n) dq[m][n] = dk[m][n] = f32x4{0, 0, 0, 0};
+        }
+        if (tid < 64) norm_q[tid] = norm_k[tid] = 0.0f;
+        // four steps of this lane's channels of key and query, where the registers hold them: they are used three times
+        Raw4<DT> held_k[X::kHold ? NC : 1][2], held_q[X::kHold ? NC : 1][2];
+        if constexpr (X::kHold) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+            for (int n = 0; n < NC; ++n) {
+                const int d = (wave & 3) * NC * 16 + n * 16 + (tid & 15), row = hk * a.d.P + (d < a.d.P ? d : 0);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) q_[m][n] = read[m][n] = write[m][n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < TILES; ++j) FZ[j] = OZ[j] = f32x4{0, 0, 0, 0};
-        float ends = 0.0f;
-        const int mi = wave * 4 / W, j0 = wave % (W / 4);         // the wave's tiles: row mi, columns j0 + j W / 4
-
-        for (int v0 = 0; v0 < a.Vp; v0 += 64) {
-            if (v0) __syncthreads();           // the channels before are used up
-            // blocks of 4 steps x 8 channels: Z, F, dy
-            for (int i = again(tid); i < 3 * 128; i += X::kThreads) {
-                const int which = uniform(i >> 7), t = (i & 15) * 4, v = v0 + (i >> 4 & 7) * 8;
-                float x[8][4];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const bool in = v + k < (which == 2 ? a.d.V : a.Vp);
-                    if (which == 2) {
-                        const T *row = row_of<DT>(a.d.dy, B, h * a.d.V + (in ? v + k : 0)) + t0;
-                        widen4<DT>(steps4<DT>(row, whole, t, end), in, x[k]);
-                    } else {
-                        const f32x4 s = *(const f32x4 *)((which ? Fs : Zs) + (size_t)(in ? v + k : 0) * kDeltaChunk + t);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) x[k][r] = in ? s[r] : 0.0f;
-                    }
-                }
-                uint16_t *to = shared + which * 3 * X::kPlane + t * X::kPitch + (v - v0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float eight[8] = {x[0][r], x[1][r], x[2][r], x[3][r], x[4][r], x[5][r], x[6][r], x[7][r]};
-                    u32x4 s[3];
-                    split8<3>(eight, s);
-                    *(u32x4 *)(to + r * X::kPitch) = s[0];
-                    if (which < 2 || TI == 3) {
-                        *(u32x4 *)(to + r * X::kPitch + X::kPlane) = s[1];
-                        *(u32x4 *)(to + r * X::kPitch + 2 * X::kPlane) = s[2];
-                    }
+                for (int m = 0; m < 2; ++m) {
+                    const int t = (m0 + m) * 16 + (tid >> 4 & 3) * 4;
+                    held_k[n][m] = steps4<DT>(row_of<DT>(a.d.k, B, row) + t0, whole, t, end);
+                    held_q[n][m] = steps4<DT>(row_of<DT>(a.d.q, B, row) + t0, whole, t, end);
                 }
             }
-            __syncthreads();
-            const uint16_t *Zp = shared, *Fp = shared + 3 * X::kPlane, *Op = shared + 6 * X::kPlane;
-#pragma unroll 1
-            for (int ks = 0; ks < 2; ++ks) {
-                if (v0 + ks * 32 >= a.Vp) break;
-                const int at = again(ks * 32 + grp * 8);
-                // F Z^T and dy Z^T up to the diagonal
-                {
-                    u32x4 fr[3], og[TI];
-                    get_planes<3>(Fp + (mi * 16 + col) * X::kPitch + at, X::kPlane, fr);
-                    get_planes<TI>(Op + (mi * 16 + col) * X::kPitch + at, X::kPlane, og);
+        }
+
+        for (int hr = 0; hr < a.rep; ++hr) {
+            const int h = hk * a.rep + hr;
+            // a lane's place, of which the compiler does not know that it is the same for all heads: what is made from
+            // it is then not held in registers from one to the next
+            const int lane = again(tid & 63), col = lane & 15, grp = lane >> 4, row4 = grp * 4;
+            const int d0 = (wave & 3) * NC * 16 + col;   // key channels d0 + 16 n
+            const size_t of_v = (size_t)bc * a.d.Hv + h;
+            const float *S0 = (const float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0 + c) * delta_saved(a.d.P, a.d.V);
+            const float *Zs = S0 + (size_t)DK * a.Vp;
+            const float *S1 = (const float *)(a.ws + a.w.after) + of_v * DK * a.Vp;
+            const float *Fs = (const float *)(a.ws + a.w.F) + of_v * a.Vp * kDeltaChunk;
+            if (hr) __syncthreads();               // the head before has read steps, shared and rows
+            if (tid < (int)(sizeof(DeltaSteps) / 16))
+                ((u32x4 *)&steps)[tid] = ((const u32x4 *)(a.ws + a.w.steps + of_v * sizeof(DeltaSteps)))[tid];
+            f32x4 q_[2][NC], read[2][NC], write[2][NC], FZ[TILES], OZ[TILES];
 #pragma unroll
-                    for (int j = 0; j < TILES; ++j) {
-                        const int jt = j0 + j * (W / 4);
-                        if (jt > mi) break;
-                        u32x4 z[3];
-                        get_planes<3>(Zp + (jt * 16 + col) * X::kPitch + at, X::kPlane, z);
-                        multiply<3, 3, 2>(fr, z, FZ[j]);
-                        multiply<TI, 3, 2>(og, z, OZ[j]);
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NC; ++n) q_[m][n] = read[m][n] = write[m][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) FZ[j] = OZ[j] = f32x4{0, 0, 0, 0};
+            float ends = 0.0f;
+            const int mi = wave * 4 / W, j0 = wave % (W / 4);         // the wave's tiles: row mi, columns j0 + j W / 4
+
+            // eight value channels of this lane's rows of the state and of dS: the next 32 columns' while these are multiplied
+            f32x4 states0[NP][2], states1[NP][2];
+            const auto load_states = [&](int n, int v) {
+                const unsigned from = again(d0 + n * 16) * a.Vp + (v < a.Vp ? v : 0) + grp * 8;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    states0[n % NP][k] = *(const f32x4 *)(S0 + from + k * 4);
+                    states1[n % NP][k] = *(const f32x4 *)(S1 + from + k * 4);
+                }
+            };
+            if constexpr (X::kAhead) {
+#pragma unroll
+                for (int n = 0; n < NC; ++n) load_states(n, 0);
+            }
+            for (int v0 = 0; v0 < a.Vp; v0 += 64) {
+                if (v0) __syncthreads();           // the channels before are used up
+                // blocks of 4 steps x 8 channels: Z, F, dy; each of them loads and stores in a branch of its own
+                const auto put = [&](int which, int t, int vl, const float (&x)[8][4]) {
+                    uint16_t *to = shared + which * 3 * X::kPlane + t * X::kPitch + vl;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float eight[8] = {x[0][r], x[1][r], x[2][r], x[3][r], x[4][r], x[5][r], x[6][r], x[7][r]};
+                        u32x4 s[3];
+                        split8<3>(eight, s);
+                        *(u32x4 *)(to + r * X::kPitch) = s[0];
+                        if (which < 2 || TI == 3) {
+                            *(u32x4 *)(to + r * X::kPitch + X::kPlane) = s[1];
+                            *(u32x4 *)(to + r * X::kPitch + 2 * X::kPlane) = s[2];
+                        }
+                    }
+                };
+                for (int i = again(tid); i < 3 * 128; i += X::kThreads) {
+                    const int which = uniform(i >> 7), t = (i & 15) * 4, vl = (i >> 4 & 7) * 8, v = v0 + vl;
+                    float x[8][4];
+                    if (which == 2) {
+                        Raw4<DT> held[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            held[c] = steps4<DT>(row_of<DT>(a.d.dy, B, h * a.d.V + (v + c < a.d.V ? v + c : 0)) + t0, whole, t, end);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) widen4<DT>(held[c], v + c < a.d.V, x[c]);
+                        put(2, t, vl, x);
+                    } else {
+                        const float *from = which ? Fs : Zs;
+                        f32x4 held[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) held[c] = *(const f32x4 *)(from + (size_t)(v + c < a.Vp ? v + c : 0) * kDeltaChunk + t);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) x[c][r] = v + c < a.Vp ? held[c][r] : 0.0f;
+                        put(which, t, vl, x);
                     }
                 }
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    u32x4 s0[3], s1[3];
+                __syncthreads();
+                const uint16_t *Zp = shared, *Fp = shared + 3 * X::kPlane, *Op = shared + 6 * X::kPlane;
+#pragma unroll 1
+                for (int ks = 0; ks < 2; ++ks) {
+                    if (v0 + ks * 32 >= a.Vp) break;
+                    const int at = again(ks * 32 + grp * 8);
+                    // F Z^T and dy Z^T up to the diagonal
                     {
-                        const unsigned from = again(d0 + n * 16) * a.Vp + v0 + at;
-                        float x[8], y[8];
+                        u32x4 fr[3], og[TI];
+                        get_planes<3>(Fp + (mi * 16 + col) * X::kPitch + at, X::kPlane, fr);
+                        get_planes<TI>(Op + (mi * 16 + col) * X::kPitch + at, X::kPlane, og);
 #pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const f32x4 lo = *(const f32x4 *)(S0 + from + k), hi = *(const f32x4 *)(S1 + from + k);
+                        for (int j = 0; j < TILES; ++j) {
+                            const int jt = j0 + j * (W / 4);
+                            if (jt > mi) break;
+                            u32x4 z[3];
+                            get_planes<3>(Zp + (jt * 16 + col) * X::kPitch + at, X::kPlane, z);
+                            multiply<3, 3, 2>(fr, z, FZ[j]);
+                            multiply<TI, 3, 2>(og, z, OZ[j]);
+                        }
+                    }
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                x[k + r] = lo[r];
-                                y[k + r] = hi[r];
+                    for (int n = 0; n < NC; n += NP) {
+                        u32x4 s0[NP][3], s1[NP][3];
+#pragma unroll
+                        for (int w = 0; w < NP; ++w) {
+                            if constexpr (!X::kAhead) load_states(n + w, v0 + ks * 32);
+                            float x[8], y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                x[k] = states0[w][k >> 2][k & 3];
+                                y[k] = states1[w][k >> 2][k & 3];
+                                ends = __builtin_fmaf(x[k], y[k], ends);
                             }
+                            split8<3>(x, s0[w]);
+                            split8<3>(y, s1[w]);
+                            if constexpr (X::kAhead) load_states(n + w, v0 + ks * 32 + 32);
                         }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) ends = __builtin_fmaf(x[k], y[k], ends);
-                        split8<3>(x, s0);
-                        split8<3>(y, s1);
-                    }
+                        for (int m = 0; m < 2; ++m) {
+                            const int from = again(((m0 + m) * 16 + col) * X::kPitch) + at;
+                            u32x4 og[TI], r3[3];
+                            get_planes<TI>(Op + from, X::kPlane, og);
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        u32x4 og[TI], r3[3];
-                        get_planes<TI>(Op + (m * 16 + col) * X::kPitch + at, X::kPlane, og);
-                        multiply<TI, 3, 2>(og, s0, q_[m][n]);
-                        get_planes<3>(Fp + (m * 16 + col) * X::kPitch + at, X::kPlane, r3);
-                        multiply<3, 3, 2>(r3, s0, read[m][n]);
-                        get_planes<3>(Zp + (m * 16 + col) * X::kPitch + at, X::kPlane, r3);
-                        multiply<3, 3, 2>(r3, s1, write[m][n]);
-                        __builtin_amdgcn_sched_barrier(0);   // loads further ahead would not fit the registers
+                            for (int w = 0; w < NP; ++w) multiply<TI, 3, 2>(og, s0[w], q_[m][n + w]);
+                            get_planes<3>(Fp + from, X::kPlane, r3);
+#pragma unroll
+                            for (int w = 0; w < NP; ++w) multiply<3, 3, 2>(r3, s0[w], read[m][n + w]);
+                            get_planes<3>(Zp + from, X::kPlane, r3);
+#pragma unroll
+                            for (int w = 0; w < NP; ++w) multiply<3, 3, 2>(r3, s1[w], write[m][n + w]);
+                            __builtin_amdgcn_sched_barrier(0);   // loads further ahead would not fit the registers
+                        }
                     }
                 }
             }
-        }
-        if (tid < 64) {
-            e[tid] = exp_any((float)steps.G[tid]);
-            f[tid] = exp_any((float)(steps.G[63] - steps.G[tid]));
-        }
-        __syncthreads();                       // and the products have left the planes
-        settle();
-        ends *= steps.last;
-        // the rows' factors; the chunk's end reaches its decays through the last of them
-        // four steps of a channel of key or query
-        const auto four = [&](const miconv_rows_t &rows, int d, int t, float (&v)[4]) {
-            const int at = again(d);
-            widen4<DT>(steps4<DT>(row_of<DT>(rows, B, hk * a.d.P + (at < a.d.P ? at : 0)) + t0, whole, t, end), at < a.d.P, v);
-        };
+            if (tid < 64) {
+                e[tid] = exp_any((float)steps.G[tid]);
+                f[tid] = exp_any((float)(steps.G[63] - steps.G[tid]));
+            }
+            __syncthreads();                       // and the products have left the planes
+            settle();
+            ends = m0 ? 0.0f : ends * steps.last;   // both halves of the steps have read the states
+            // the rows' factors; the chunk's end reaches its decays through the last of them
+            const auto four = [&](const miconv_rows_t &rows, const auto &held, int n, int m, float (&v)[4]) {
+                const int at = again(d0 + n * 16);
+                if constexpr (X::kHold)
+                    widen4<DT>(held[n][m], at < a.d.P, v);
+                else
+                    widen4<DT>(steps4<DT>(row_of<DT>(rows, B, hk * a.d.P + (at < a.d.P ? at : 0)) + t0, whole, (m0 + m) * 16 + row4, end),
+                               at < a.d.P, v);
+            };
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+            for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int t = again(m * 16 + row4);
-                float k[4];
-                four(a.d.k, d0 + n * 16, t, k);
+                for (int m = 0; m < 2; ++m) {
+                    const int t = again((m0 + m) * 16 + row4);
+                    float k[4];
+                    four(a.d.k, held_k, n, m, k);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float beta = steps.beta[t + r];
+                        q_[m][n][r] *= e[t + r];
+                        read[m][n][r] *= -(e[t + r] * beta);
+                        write[m][n][r] *= f[t + r] * beta;
+                        ends = __builtin_fmaf(k[r] * steps.rk[t + r], write[m][n][r], ends);
+                    }
+                    // here, not where the sum is used, with all its terms in registers till then
+                    asm volatile("" : "+v"(ends), "+v"(q_[m][n]), "+v"(read[m][n]), "+v"(write[m][n]));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            // dP and dA as row operands: [i][j] times the key's factor of j, for q and read, and [j][i] times the query's
+            // or key's factor of i, for write
+            uint16_t *Mq = shared, *Mr = shared + 3 * X::kPlane, *Mp = shared + 6 * X::kPlane, *Ma = shared + 9 * X::kPlane;
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) {
+                const int jt = j0 + j * (W / 4);
+                if (jt > (mi | 1)) break;          // a block of 32 columns past the diagonal is never read
+                const int cj = again(jt * 16 + col);
+                const double Gj = steps.G[cj];
+                const float bj = steps.beta[cj], rkj = steps.rk[cj];
+                float pq[4], ar[4], pw[4], aw[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float beta = steps.beta[t + r];
-                    q_[m][n][r] *= e[t + r];
-                    read[m][n][r] *= -(e[t + r] * beta);
-                    write[m][n][r] *= f[t + r] * beta;
-                    ends = __builtin_fmaf(k[r] * steps.rk[t + r], write[m][n][r], ends);
+                    const int i = mi * 16 + row4 + r;
+                    const float D = i >= cj ? exp_any((float)(steps.G[i] - Gj)) * bj : 0.0f;
+                    const float dP = i > cj ? D * OZ[j][r] : 0.0f, dA = i > cj ? -(D * steps.beta[i]) * FZ[j][r] : 0.0f;
+                    pq[r] = dP * rkj;
+                    ar[r] = dA * rkj;
+                    pw[r] = dP * (steps.rq[i] * a.d.scale);
+                    aw[r] = dA * steps.rk[i];
+                    if (i == cj) {
+                        diag[i] = FZ[j][r];
+                        diag_p[i] = D * OZ[j][r];
+                    }
                 }
-                // here, not where the sum is used, with all its terms in registers till then
-                asm volatile("" : "+v"(ends), "+v"(q_[m][n]), "+v"(read[m][n]), "+v"(write[m][n]));
+                u32x2 s[3];
+                const auto across = [&](uint16_t *to) {
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            to[p * X::kPlane + (mi * 16 + row4 + r) * X::kPitch + cj] =
+                                (uint16_t)(r & 1 ? s[p][r >> 1] >> 16 : s[p][r >> 1]);
+                };
+                split4<3>(pq, s);
+                across(Mq);
+                split4<3>(ar, s);
+                across(Mr);
+                put_planes<3>(Mp + cj * X::kPitch + mi * 16 + row4, X::kPlane, pw);
+                put_planes<3>(Ma + cj * X::kPitch + mi * 16 + row4, X::kPlane, aw);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NC; n += NP)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    u32x4 fk[NP][TI], fq[NP][TI];
+#pragma unroll
+                    for (int w = 0; w < NP; ++w) {
+                        const int d = again(d0 + (n + w) * 16), row = hk * a.d.P + (d < a.d.P ? d : 0), t = ks * 32 + grp * 8;
+                        planes_of<DT>(only<DT>(steps8<DT>(row_of<DT>(a.d.k, B, row) + t0, whole, t, end), d < a.d.P), fk[w]);
+                        planes_of<DT>(only<DT>(steps8<DT>(row_of<DT>(a.d.q, B, row) + t0, whole, t, end), d < a.d.P), fq[w]);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const int at = again(((m0 + m) * 16 + col) * X::kPitch + ks * 32 + grp * 8);
+                        u32x4 s[3];
+                        if (m0 >= 2 * ks) {        // columns up to the diagonal
+                            get_planes<3>(Mq + at, X::kPlane, s);
+#pragma unroll
+                            for (int w = 0; w < NP; ++w) multiply<3, TI, 2>(s, fk[w], q_[m][n + w]);
+                            get_planes<3>(Mr + at, X::kPlane, s);
+#pragma unroll
+                            for (int w = 0; w < NP; ++w) multiply<3, TI, 2>(s, fk[w], read[m][n + w]);
+                        }
+                        if (m0 < 2 * ks + 2) {     // columns from the diagonal on
+                            get_planes<3>(Mp + at, X::kPlane, s);
+#pragma unroll
+                            for (int w = 0; w < NP; ++w) multiply<3, TI, 2>(s, fq[w], write[m][n + w]);
+                            get_planes<3>(Ma + at, X::kPlane, s);
+#pragma unroll
+                            for (int w = 0; w < NP; ++w) multiply<3, TI, 2>(s, fk[w], write[m][n + w]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            settle();
+            // The rows' products with normalised query and key.  A step's own dP_ii k_i and dP_ii q_i add the same to
+            // q_i.dq_i and k_i.write_i, so they enter after the decays' part: its terms then cancel no further than its
+            // definition's do, and the first step from a zero state gets a zero.
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float x[4] = {}, y[4] = {}, z[4] = {}, w[4] = {};
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    float k[4], q[4];
+                    four(a.d.k, held_k, n, m, k);
+                    four(a.d.q, held_q, n, m, q);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int t = (m0 + m) * 16 + row4 + r;
+                        x[r] = __builtin_fmaf(q[r], q_[m][n][r], x[r]);
+                        y[r] = __builtin_fmaf(k[r], read[m][n][r] - write[m][n][r], y[r]);
+                        q_[m][n][r] = __builtin_fmaf(diag_p[t] * steps.rk[t], k[r], q_[m][n][r]);
+                        write[m][n][r] = __builtin_fmaf(diag_p[t] * (steps.rq[t] * a.d.scale), q[r], write[m][n][r]);
+                        z[r] = __builtin_fmaf(q[r], q_[m][n][r], z[r]);
+                        w[r] = __builtin_fmaf(k[r], read[m][n][r] + write[m][n][r], w[r]);
+                        if constexpr (X::kKeep) {
+                            dq[m][n][r] += q_[m][n][r];
+                            dk[m][n][r] += read[m][n][r] + write[m][n][r];
+                        }
+                    }
+                    if constexpr (!X::kKeep) {
+                        f32x4 *const sums = (f32x4 *)(a.ws + a.w.sums) + (((size_t)bc * a.d.Hk + hk) * 2 * 2 * NC + (m * NC + n) * 2) * X::kThreads + again(tid);
+                        read[m][n] += write[m][n];
+                        if (hr) {
+                            q_[m][n] += sums[0];
+                            read[m][n] += sums[X::kThreads];
+                        }
+                        if (hr + 1 < a.rep) {
+                            sums[0] = q_[m][n];
+                            sums[X::kThreads] = read[m][n];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = (m0 + m) * 16 + row4 + r;
+                    x[r] = sum16(x[r]);
+                    y[r] = sum16(y[r]);
+                    z[r] = sum16(z[r]);
+                    w[r] = sum16(w[r]);
+                    if (col == 0) {
+                        rows[wave][0][t] = x[r] * steps.rq[t];
+                        rows[wave][1][t] = y[r] * steps.rk[t];
+                        rows[wave][2][t] = z[r] * steps.rq[t];
+                        rows[wave][3][t] = w[r] * steps.rk[t];
+                    }
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
-        // dP and dA as row operands: [i][j] times the key's factor of j, for q and read, and [j][i] times the query's
-        // or key's factor of i, for write
-        uint16_t *Mq = shared, *Mr = shared + 3 * X::kPlane, *Mp = shared + 6 * X::kPlane, *Ma = shared + 9 * X::kPlane;
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-            const int jt = j0 + j * (W / 4);
-            if (jt > (mi | 1)) break;          // a block of 32 columns past the diagonal is never read
-            const int cj = again(jt * 16 + col);
-            const double Gj = steps.G[cj];
-            const float bj = steps.beta[cj], rkj = steps.rk[cj];
-            float pq[4], ar[4], pw[4], aw[4];
+            for (int o = 32; o; o /= 2) ends += __shfl_xor(ends, o);
+            if (lane == 0) part[wave] = ends;
+            __syncthreads();
+            if (wave == 0) {
+                float x = 0.0f, y = 0.0f, z = 0.0f, u = 0.0f, w = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = mi * 16 + row4 + r;
-                const float D = i >= cj ? exp_any((float)(steps.G[i] - Gj)) * bj : 0.0f;
-                const float dP = i > cj ? D * OZ[j][r] : 0.0f, dA = i > cj ? -(D * steps.beta[i]) * FZ[j][r] : 0.0f;
-                pq[r] = dP * rkj;
-                ar[r] = dA * rkj;
-                pw[r] = dP * (steps.rq[i] * a.d.scale);
-                aw[r] = dA * steps.rk[i];
-                if (i == cj) {
-                    diag[i] = FZ[j][r];
-                    diag_p[i] = D * OZ[j][r];
+                for (int i = 0; i < 4; ++i) {
+                    const int from = (lane >> 5) * 4 + i;
+                    x += rows[from][0][lane];
+                    y += rows[from][1][lane];
+                    z += rows[from][2][lane];
+                    u += rows[from][3][lane];
+                    w += part[i] + part[4 + i];
+                }
+                norm_q[lane] += z;
+                norm_k[lane] += u;
+                // sums of the decays' gradients from each step on, in 64 bits like the decays' own
+                double s = (double)x * a.d.scale + y;
+#pragma unroll
+                for (int o = 1; o < 64; o *= 2) {
+                    const double other = __shfl_down(s, o);
+                    if (lane + o < 64) s += other;
+                }
+                if (lane < stop) {
+                    const size_t at = ((size_t)B * a.d.Hv + h) * a.d.L + t0 + lane;
+                    a.d.dg[at] = lane < end ? (float)(s + w) : 0.0f;
+                    a.d.dbeta[at] = lane < end ? diag[lane] : 0.0f;
                 }
             }
-            u32x2 s[3];
-            const auto across = [&](uint16_t *to) {
+            if (hr + 1 < a.rep) continue;
+            __syncthreads();
+            // through the normalisation n = r x: dx = r (dn - n (n . dn))
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
+            for (int n = 0; n < NC; ++n) {
+                const int d = again(d0 + n * 16);
+                if (d >= a.d.P) continue;
+                T *const qrow = row_of<DT>(a.d.dq, B, hk * a.d.P + d) + t0, *const krow = row_of<DT>(a.d.dk, B, hk * a.d.P + d) + t0;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        to[p * X::kPlane + (mi * 16 + row4 + r) * X::kPitch + cj] =
-                            (uint16_t)(r & 1 ? s[p][r >> 1] >> 16 : s[p][r >> 1]);
-            };
-            split4<3>(pq, s);
-            across(Mq);
-            split4<3>(ar, s);
-            across(Mr);
-            put_planes<3>(Mp + cj * X::kPitch + mi * 16 + row4, X::kPlane, pw);
-            put_planes<3>(Ma + cj * X::kPitch + mi * 16 + row4, X::kPlane, aw);
-        }
-        __syncthreads();
+                for (int m = 0; m < 2; ++m) {
+                    const int t = (m0 + m) * 16 + row4;
+                    float k[4], q[4], x[4], y[4];
+                    four(a.d.k, held_k, n, m, k);
+                    four(a.d.q, held_q, n, m, q);
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int d = again(d0 + n * 16), row = hk * a.d.P + (d < a.d.P ? d : 0);
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const int t = ks * 32 + grp * 8;
-                u32x4 fk[TI], fq[TI];
-                planes_of<DT>(only<DT>(steps8<DT>(row_of<DT>(a.d.k, B, row) + t0, whole, t, end), d < a.d.P), fk);
-                planes_of<DT>(only<DT>(steps8<DT>(row_of<DT>(a.d.q, B, row) + t0, whole, t, end), d < a.d.P), fq);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int at = again((m * 16 + col) * X::kPitch + ks * 32 + grp * 8);
-                    u32x4 s[3];
-                    if (m >= 2 * ks) {         // columns up to the diagonal
-                        get_planes<3>(Mq + at, X::kPlane, s);
-                        multiply<3, TI, 2>(s, fk, q_[m][n]);
-                        get_planes<3>(Mr + at, X::kPlane, s);
-                        multiply<3, TI, 2>(s, fk, read[m][n]);
+                    for (int r = 0; r < 4; ++r) {
+                        const float rq = steps.rq[t + r], rk = steps.rk[t + r];
+                        float g, u;
+                        if constexpr (X::kKeep) {
+                            g = dq[m][n][r], u = dk[m][n][r];
+                        } else {
+                            g = q_[m][n][r], u = read[m][n][r];
+                        }
+                        if (a.d.l2norm) {
+                            g -= q[r] * rq * norm_q[t + r];
+                            u -= k[r] * rk * norm_k[t + r];
+                        }
+                        x[r] = t + r < end ? g * (rq * a.d.scale) : 0.0f;
+                        y[r] = t + r < end ? u * rk : 0.0f;
                     }
-                    if (m < 2 * ks + 2) {      // columns from the diagonal on
-                        get_planes<3>(Mp + at, X::kPlane, s);
-                        multiply<3, TI, 2>(s, fq, write[m][n]);
-                        get_planes<3>(Ma + at, X::kPlane, s);
-                        multiply<3, TI, 2>(s, fk, write[m][n]);
-                    }
+                    store4_until<DT>(qrow, stop == kDeltaChunk, t, stop, x);
+                    store4_until<DT>(krow, stop == kDeltaChunk, t, stop, y);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
-        settle();
-        // The rows' products with normalised query and key.  A step's own dP_ii k_i and dP_ii q_i add the same to
-        // q_i.dq_i and k_i.write_i, so they enter after the decays' part: its terms then cancel no further than its
-        // definition's do, and the first step from a zero state gets a zero.
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            float x[4] = {}, y[4] = {}, z[4] = {}, w[4] = {};
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                float k[4], q[4];
-                four(a.d.k, d0 + n * 16, m * 16 + row4, k);
-                four(a.d.q, d0 + n * 16, m * 16 + row4, q);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = m * 16 + row4 + r;
-                    x[r] = __builtin_fmaf(q[r], q_[m][n][r], x[r]);
-                    y[r] = __builtin_fmaf(k[r], read[m][n][r] - write[m][n][r], y[r]);
-                    q_[m][n][r] = __builtin_fmaf(diag_p[t] * steps.rk[t], k[r], q_[m][n][r]);
-                    write[m][n][r] = __builtin_fmaf(diag_p[t] * (steps.rq[t] * a.d.scale), q[r], write[m][n][r]);
-                    z[r] = __builtin_fmaf(q[r], q_[m][n][r], z[r]);
-                    w[r] = __builtin_fmaf(k[r], read[m][n][r] + write[m][n][r], w[r]);
-                    if constexpr (X::kKeep) {
-                        dq[m][n][r] += q_[m][n][r];
-                        dk[m][n][r] += read[m][n][r] + write[m][n][r];
-                    }
-                }
-                if constexpr (!X::kKeep) {
-                    f32x4 *const sums = (f32x4 *)(a.ws + a.w.sums) + (((size_t)bc * a.d.Hk + hk) * 2 * 4 * NC + (m * NC + n) * 2) * X::kThreads + again(tid);
-                    read[m][n] += write[m][n];
-                    if (hr) {
-                        q_[m][n] += sums[0];
-                        read[m][n] += sums[X::kThreads];
-                    }
-                    if (hr + 1 < a.rep) {
-                        sums[0] = q_[m][n];
-                        sums[X::kThreads] = read[m][n];
-                    }
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = m * 16 + row4 + r;
-                x[r] = sum16(x[r]);
-                y[r] = sum16(y[r]);
-                z[r] = sum16(z[r]);
-                w[r] = sum16(w[r]);
-                if (col == 0) {
-                    rows[wave][0][t] = x[r] * steps.rq[t];
-                    rows[wave][1][t] = y[r] * steps.rk[t];
-                    rows[wave][2][t] = z[r] * steps.rq[t];
-                    rows[wave][3][t] = w[r] * steps.rk[t];
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int o = 32; o; o /= 2) ends += __shfl_xor(ends, o);
-        if (lane == 0) part[wave] = ends;
-        __syncthreads();
-        if (wave == 0) {
-            float x = 0.0f, y = 0.0f, z = 0.0f, u = 0.0f, w = 0.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                x += rows[i][0][lane];
-                y += rows[i][1][lane];
-                z += rows[i][2][lane];
-                u += rows[i][3][lane];
-                w += part[i];
-            }
-            norm_q[lane] += z;
-            norm_k[lane] += u;
-            // sums of the decays' gradients from each step on, in 64 bits like the decays' own
-            double s = (double)x * a.d.scale + y;
-#pragma unroll
-            for (int o = 1; o < 64; o *= 2) {
-                const double other = __shfl_down(s, o);
-                if (lane + o < 64) s += other;
-            }
-            if (lane < stop) {
-                const size_t at = ((size_t)B * a.d.Hv + h) * a.d.L + t0 + lane;
-                a.d.dg[at] = lane < end ? (float)(s + w) : 0.0f;
-                a.d.dbeta[at] = lane < end ? diag[lane] : 0.0f;
-            }
-        }
-        if (hr + 1 < a.rep) continue;
-        __syncthreads();
-        // through the normalisation n = r x: dx = r (dn - n (n . dn))
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int d = again(d0 + n * 16);
-            if (d >= a.d.P) continue;
-            T *const qrow = row_of<DT>(a.d.dq, B, hk * a.d.P + d) + t0, *const krow = row_of<DT>(a.d.dk, B, hk * a.d.P + d) + t0;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int t = m * 16 + row4;
-                float k[4], q[4], x[4], y[4];
-                four(a.d.k, d, t, k);
-                four(a.d.q, d, t, q);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float rq = steps.rq[t + r], rk = steps.rk[t + r];
-                    float g, u;
-                    if constexpr (X::kKeep) {
-                        g = dq[m][n][r], u = dk[m][n][r];
-                    } else {
-                        g = q_[m][n][r], u = read[m][n][r];
-                    }
-                    if (a.d.l2norm) {
-                        g -= q[r] * rq * norm_q[t + r];
-                        u -= k[r] * rk * norm_k[t + r];
-                    }
-                    x[r] = t + r < end ? g * (rq * a.d.scale) : 0.0f;
-                    y[r] = t + r < end ? u * rk : 0.0f;
-                }
-                store4_until<DT>(qrow, stop == kDeltaChunk, t, stop, x);
-                store4_until<DT>(krow, stop == kDeltaChunk, t, stop, y);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-    }
+    };
+    if (end >= kDeltaChunk)
+        chunk(Whole<true>());
+    else
+        chunk(Whole<false>());
 }
 
 template <int DT, int DK>
