@@ -39,6 +39,29 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     const bool leads = h == hk * a.rep;                           // writes the operands that heads share
     const size_t of_k = ((size_t)bc * a.d.Hk + hk) * TI * 64 * DK * 2, of_v = (size_t)bc * a.d.Hv + h;
 
+    // the decays' loads and those of the first operands are in flight together
+    const int own = lane < end ? lane : 0;
+    const float decay = ((const float *)a.d.g.data + (long long)B * a.d.g.stride_b + (long long)h * a.d.g.stride_d + t0)[own];
+    const float size = ((const float *)a.d.beta.data + (long long)B * a.d.beta.stride_b +
+                        (long long)h * a.d.beta.stride_d + t0)[own];
+    const auto decays = [&] {
+        // sums of log decays in 64 bits: their differences are the exponents between near steps, however far
+        // the sums have gone.  A decay of exp(-200) is 0 in fp32, so that also stands for less, minus infinity included.
+        if (wave == 0) {
+            double G = lane >= end ? 0.0 : decay < -200.0f ? -200.0 : (double)decay;
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) {
+                const double other = __shfl_up(G, o);
+                if (lane >= o) G += other;
+            }
+            const double last = __shfl(G, 63);
+            steps.G[lane] = G;
+            steps.ek[lane] = exp_any((float)G);                      // the keys' factors are applied below
+            steps.fk[lane] = exp_any((float)(last - G));
+            steps.beta[lane] = lane < end ? size : 0.0f;
+            if (lane == 0) steps.last = exp_any((float)last);
+        }
+    };
     // operands, in blocks of 8 steps x 8 channels per thread: keys first, then queries
     constexpr int kBlocks = X::kCols;                             // per operand: 8 x kCols / 8
     f32x4 kk[4], qk[4];
@@ -48,17 +71,18 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     for (int d0 = 0; d0 < DK; d0 += X::kCols) {
         if (d0) __syncthreads();                                  // the products of the columns before are done
         const int operand = tid / kBlocks, in = tid % kBlocks;
-        if (operand < 2) {
+        const auto block = [&](auto is_whole) {
+            constexpr bool whole = decltype(is_whole)::value;
             const int tb = (in & 7) * 8, db = (in >> 3) * 8;
             const miconv_rows_t &rows = operand ? a.d.q : a.d.k;
             float x[8][8];
             Raw8<DT> raw[8];
-            const bool whole = end >= kDeltaChunk;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int d = d0 + db + i;
                 raw[i] = steps8<DT>(row_of<DT>(rows, B, hk * a.d.P + (d < a.d.P ? d : 0)) + t0, whole, tb, end);
             }
+            if (d0 == 0) decays();                                // while they are in flight
 #pragma unroll
             for (int i = 0; i < 8; ++i) widen8<DT>(only<DT>(raw[i], d0 + db + i < a.d.P), x[i]);
 #pragma unroll
@@ -88,6 +112,12 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
                         for (int j = 0; j < 8; ++j) x[i][j] -= upper(x[i][j]);
                 }
             }
+        };
+        if (operand < 2) {
+            if (end >= kDeltaChunk)
+                block(Whole<true>());
+            else
+                block(Whole<false>());
         }
         __syncthreads();
         // k k^T and q k^T: the wave's 16 rows, column tiles up to the diagonal
@@ -117,26 +147,6 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) part[operand][in >> 3][(in & 7) * 8 + j] = squares[j];
         }
-    }
-    // sums of log decays in 64 bits: their differences are the exponents between near steps, however far
-    // the sums have gone.  A decay of exp(-200) is 0 in fp32, so that also stands for less, minus infinity included.
-    if (wave == 0) {
-        const float *g = (const float *)a.d.g.data + (long long)B * a.d.g.stride_b + (long long)h * a.d.g.stride_d + t0;
-        const float *beta = (const float *)a.d.beta.data + (long long)B * a.d.beta.stride_b +
-                            (long long)h * a.d.beta.stride_d + t0;
-        const float one = lane < end ? g[lane] : 0.0f;
-        double G = one < -200.0f ? -200.0 : (double)one;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const double other = __shfl_up(G, o);
-            if (lane >= o) G += other;
-        }
-        const double last = __shfl(G, 63);
-        steps.G[lane] = G;
-        steps.ek[lane] = exp_any((float)G);                      // the keys' factors are applied below
-        steps.fk[lane] = exp_any((float)(last - G));
-        steps.beta[lane] = lane < end ? beta[lane] : 0.0f;
-        if (lane == 0) steps.last = exp_any((float)last);
     }
     __syncthreads();
     if (wave < 2) {
