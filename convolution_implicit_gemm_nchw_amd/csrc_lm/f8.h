@@ -16,7 +16,7 @@ int f8_splits(int T, int O, int K, size_t budget);
 struct F8Form {
     int few, side, stages;
 };
-F8Form f8_form(int T, int O, int K, int splits);
+F8Form f8_form(int T, int O);
 int launch_matmul_f8(int B, int L, int O, int K, const unsigned char *q, const unsigned char *qs, const unsigned char *wq,
                      const unsigned char *ws, const float *bias, int channel_major, int out_dtype, void *y, int splits,
                      float *part, hipStream_t st);

@@ -62,7 +62,7 @@ int matmul_f8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, c
     if (st != MICONV_OK) return st;
     const size_t cap = MICONV_MAX_WORKSPACE_BYTES;
     const int splits = f8_splits(B * L, O, C_pad, workspace_bytes < cap ? workspace_bytes : cap);
-    const F8Form f = f8_form(B * L, O, C_pad, splits);
+    const F8Form f = f8_form(B * L, O);
     if (f.few)
         snprintf(buf, buflen, "algo=f8_few tokens=%d", f.few * 16);
     else

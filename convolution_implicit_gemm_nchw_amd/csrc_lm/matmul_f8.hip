@@ -507,13 +507,18 @@ int tiled(F8Args a, int splits, hipStream_t st) {
     return MICONV_OK;
 }
 
+// Up to here the kernel of few tokens is the faster one, or as fast: 64 tokens of 4096 and 8192 channels out take 15.1 us
+// with it and 20.4 with tiles of 64, 32 tokens 10.5 and 20.1, 64 of 1024 out 13.6 and 13.5 (bf16; fp32: 15.5 and
+// 20.9, 10.3 and 20.2, 13.7 and 18.0).
 constexpr int kFewTokens = 64;
 
 long long tile_count(long long T, long long O, int side) {
     return ((T + side - 1) / side) * ((O + side - 1) / side);
 }
 
-// Side of the square tile: the largest that gives most of the 256 CUs a tile.
+// Side of the square tile: the largest that gives most of the 256 CUs a tile.  Sides 256 / 128 / 64 take, in us, for
+// 4096 x 4096 outputs of 4096 (256 tiles of 256): 63 / 69 / 151; 2048 x 4096 (128 of them, 512 of 128): 59 / 37 / 79;
+// 512 x 4096 (128 of 128): 56 / 26 / 21 (bf16; fp32: 110 / 126 / 184, 93 / 67 / 98, 85 / 35 / 28).
 int tile_side(int T, int O) {
     if (tile_count(T, O, 256) >= 140) return 256;
     if (tile_count(T, O, 128) >= 140) return 128;
@@ -522,11 +527,13 @@ int tile_side(int T, int O) {
 
 }  // namespace
 
-// Splits of k, for deep products of few tiles, each at least 2048 deep.
+// Splits of k, for deep products of few tiles, each at least 2048 deep: two work-groups a CU in all.  512 x 1024 outputs
+// of 8192 (128 tiles) take 37 us whole, 27.6 in 2, 24.5 in 4 and 34.7 in 8 splits; 1024 x 1024 of 16384 (256 tiles) 67
+// whole, 51 in 2, 59 in 4; 128 x 1024 of 4096, which stays whole, 13.5, and 14.3 in 2 (bf16).
 int f8_splits(int T, int O, int K, size_t budget) {
     if (T <= kFewTokens || K < 8192) return 1;
     const long long tiles = tile_count(T, O, tile_side(T, O));
-    long long s = 160 / tiles;
+    long long s = 512 / tiles;
     if (s > K / 2048) s = K / 2048;
     if (s > 16) s = 16;
     const size_t one = (size_t)T * O * 4;
@@ -536,11 +543,12 @@ int f8_splits(int T, int O, int K, size_t budget) {
     return (steps + per - 1) / per;            // no empty split
 }
 
-F8Form f8_form(int T, int O, int K, int splits) {
+F8Form f8_form(int T, int O) {
     if (T <= kFewTokens) return {T <= 16 ? 1 : (T <= 32 ? 2 : 4), 0, 0};
+    // stages in LDS: four where the tile is small; at 128 two leave room for a second work-group on the CU, which hides more
+    // (2048 x 2048 outputs of 4096: 26.6 us, 28.7 with four; 2048 x 4096: 37 and 55)
     const int side = tile_side(T, O);
-    const bool four = side == 64 || (side == 128 && tile_count(T, O, 128) * splits <= 256 && K >= 4096);
-    return {0, side, four ? 4 : 2};
+    return {0, side, side == 64 ? 4 : 2};
 }
 
 template <int OD>
@@ -549,9 +557,7 @@ static int f8_by_form(const F8Args &a, const F8Form &f, bool stream, int splits,
         case 256:
             if (stream) return tiled<OD, 2, 4, 4, 2, 2, OD == 1>(a, splits, st);
             return tiled<OD, 2, 4, 4, 2, 2>(a, splits, st);
-        case 128:
-            if (f.stages == 4) return tiled<OD, 4, 2, 1, 2, 4>(a, splits, st);
-            return tiled<OD, 4, 2, 1, 2, 2>(a, splits, st);
+        case 128: return tiled<OD, 4, 2, 1, 2, 2>(a, splits, st);
         default: return tiled<OD, 2, 2, 1, 1, 4>(a, splits, st);
     }
 }
@@ -560,7 +566,7 @@ int launch_matmul_f8(int B, int L, int O, int K, const unsigned char *q, const u
                      const unsigned char *ws, const float *bias, int channel_major, int out_dtype, void *y, int splits,
                      float *part, hipStream_t st) {
     const int T = B * L;
-    const F8Form f = f8_form(T, O, K, splits);
+    const F8Form f = f8_form(T, O);
     if (f.few) {
 #define MICONV_FEW(FT)                                                                            \
     (out_dtype ? few<1, FT>(T, O, K, L, q, qs, wq, ws, bias, channel_major, y, st)                \
