@@ -19,7 +19,8 @@ namespace {
 
 // Laid out and split as the forward scan; the state here is dS.  Four waves go along the chain k dS, the transposed inverse
 // times du, dS - (e k)^T (beta F); the others compute attn^T dy, for the chunk that comes next, and meanwhile
-// (e q)^T dy for all key channels, half of which they hand over through LDS.
+// (e q)^T dy for all key channels, half of which they hand over through LDS.  Bound like that one by the chain's
+// latency: 2 x 2048 steps of 16 heads of 128 and 128 channels in bf16, 32 chunks, take 100 us.
 template <int DT, int DK, int NT>
 __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
     constexpr int TI = in_planes(DT), kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = NT * 16;

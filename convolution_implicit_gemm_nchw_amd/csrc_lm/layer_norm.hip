@@ -1,7 +1,9 @@
 // layer_norm.hip -- layer normalisation over the channels of each token, y = (x - m) r w + b with
 // r = 1 / sqrt(var + eps), and its gradients: with h = dy w and n = (x - m) r,
 //   dx = r (h - mean(h) - n mean(h n)),   dw = sum over tokens of dy n,   db = sum over tokens of dy.
-// Memory bound: x (and dy) are read once, held in registers between the sums and the result.
+// Memory bound: x (and dy) are read once, held in registers between the sums and the result.  8192 tokens of 4096 channels
+// in bf16, tokens first, forward: 24.5 us, 134 MB at 5.5 TB/s.  8192 tokens of 2048, channel-major: forward 19 us, 67 MB at
+// 3.5 TB/s, backward 30 us, 101 MB at 3.4: one or two work-groups a CU read all of theirs, then write all.
 //
 // The variance is the mean square of the differences from the mean, in a second run over the registers: no
 // cancellation however large the mean.
@@ -582,12 +584,15 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float *part, int 
 
 // ------------------------------------------------------------------ which kernel
 
-// Channels per work-group: up to 512 a wave, up to 8192 a work-group of 256 hold a token in registers.
+// Up to 1024 channels a wave, up to 8192 a work-group of 256 holds a token in registers (at 8192 the backward pass has 256
+// registers of them; another step would not fit).
 constexpr int kLongest = 8192;
 
 bool contiguous(const miconv_tokens_t &v, int C) { return v.stride_c == 1 || C == 1; }
 
-// Time lanes of the channel-major kernels: as many as leave most CUs a tile; 0: a loop over the channels.
+// Time lanes of the channel-major kernels: as many as leave most CUs a tile, forward two tiles; 0: a loop over the
+// channels.  4 x 2048 tokens of 2048 channels in bf16 take, with 256 tiles of 4 lanes and 512 of 2, forward 22.2 and 22.1 us
+// (fp32, a larger one: 43.8 and 37), backward 32 and 46, as its 256 work-groups then take two tiles each.
 struct RowsForm {
     int lanes, threads;
 };

