@@ -691,12 +691,18 @@ bool norm_tokens_first(const miconv_layer_norm_t &n, bool backward) {
     return backward ? contiguous(n.dy, n.C) && contiguous(n.dx, n.C) : contiguous(n.y, n.C);
 }
 
+// Work-groups of the backward pass, a row of partial sums each.  Tokens first, up to four a CU hide each other's loads, but long
+// rows of sums cost more than that gains: 8192 tokens take, with 256 / 512 / 1024 / 2048 work-groups, 54 / 35 / 29 / 35 us at 2048
+// channels and 83 / 55 / 60 / 62 at 4096 (bf16); 2048 tokens of 8192 channels 43 / 49 / 63 / 96 (fp32).  Channel-major a
+// work-group mostly fills a CU: 7 x 1626 tokens of 1382 channels in fp32 take 58 us with 256 and 73 with 512, 8 x 4096 of 256 in
+// bf16 24 and 20, others differ little.
 int norm_parts(const miconv_layer_norm_t &n, int dtype, size_t budget) {
     long long most;
     if (norm_tokens_first(n, true)) {
         const int at_once = n.C <= 1024 ? Row<64>::kTokens : 1;
         most = ((long long)n.B * n.L + at_once - 1) / at_once;
-        if (most > 512) most = 512;
+        const int rows = n.C <= 2048 ? 1024 : n.C <= 4096 ? 512 : 256;
+        if (most > rows) most = rows;
     } else {
         const RowsForm f = rows_form(n, dtype, true);
         const int steps = (f.lanes ? f.lanes : 8) * 8;
