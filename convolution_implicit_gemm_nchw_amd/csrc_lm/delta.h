@@ -25,9 +25,7 @@ constexpr int delta_chunks(int L) { return (L + kDeltaChunk - 1) / kDeltaChunk; 
 constexpr int delta_key_pad(int P) { return P <= 64 ? 64 : (P <= 128 ? 128 : 256); }
 constexpr int delta_value_pad(int V) { return (V + 31) / 32 * 32; }
 
-// Planes of attn: y of bf16 type rests on sums to order 1.
-constexpr int delta_attn_planes(int dtype, bool backward) { return !backward && dtype == MICONV_BF16 ? 2 : 3; }
-constexpr int kDeltaSquare = kDeltaChunk * kDeltaChunk * 2;    // bytes of a plane of 64 x 64
+constexpr int kDeltaSquare = kDeltaChunk * kDeltaChunk * 2;    // bytes of a plane of 64 x 64; inv and attn have three
 
 // What the pass over chunks finds about each step of a chunk and value head.
 struct DeltaSteps {

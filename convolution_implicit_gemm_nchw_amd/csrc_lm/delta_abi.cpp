@@ -20,7 +20,7 @@ DeltaWork delta_work(const miconv_gated_delta_t &d, int dtype, const DeltaSlice 
     take(&w.k, operand);
     if (!backward) take(&w.q, operand);
     take(&w.inv, heads * 3 * kDeltaSquare);
-    take(&w.attn, heads * delta_attn_planes(dtype, backward) * kDeltaSquare);
+    take(&w.attn, heads * 3 * kDeltaSquare);
     take(&w.steps, heads * sizeof(DeltaSteps));
     if (backward) {
         take(&w.F, heads * Vp * kDeltaChunk * 4);

@@ -14,10 +14,6 @@ namespace miconv {
 
 constexpr int in_planes(int DT) { return DT == 1 ? 1 : 3; }
 
-// Outputs of bf16 type (y, and the gradients of q, k and v) rest on sums to order 1: what is left out there, below
-// 2^-16, is far under the half step of their type, 2^-8.
-constexpr int out_order(int DT) { return DT == 1 ? 1 : 2; }
-
 DEVI uint32_t upper_pair(float lo, float hi) {
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }

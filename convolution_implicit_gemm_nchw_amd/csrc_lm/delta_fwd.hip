@@ -25,7 +25,7 @@ struct Scan {
 
 template <int DT, int DK, int NT, bool SAVE>
 __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
-    constexpr int TI = in_planes(DT), OO = out_order(DT), OP = OO + 1;
+    constexpr int TI = in_planes(DT);
     typedef Scan<DK, NT> X;
     typedef typename Elem<DT>::T T;
     constexpr int kPitchU = kDeltaChunk + 4;   // floats
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
     constexpr bool kLate = TI == 3 && DK >= 128;
     u32x4 fx[kLate ? 1 : X::kKS][TI];          // keys or queries
     const char *px = a.ws + (queries ? a.w.q : a.w.k) + of_k, *pi = a.ws + a.w.inv + of_v * 3 * kDeltaSquare;
-    const char *pa = a.ws + a.w.attn + of_v * OP * kDeltaSquare, *ps = a.ws + a.w.steps + of_v * sizeof(DeltaSteps);
+    const char *pa = a.ws + a.w.attn + of_v * 3 * kDeltaSquare, *ps = a.ws + a.w.steps + of_v * sizeof(DeltaSteps);
     const T *krow[X::kMT];
 #pragma unroll
     for (int i = 0; i < X::kMT; ++i) {
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
         for (int c = 0; c < full; ++c) chunk(c, Whole<true>());
         if (full < chunks) chunk(full, Whole<false>());
     } else {
-        u32x4 fa[2][OP];
+        u32x4 fa[2][3];
         f32x4 veq = {0, 0, 0, 0}, qS[NT];
         T *yrow[NT];
 #pragma unroll
@@ -251,16 +251,16 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             qS[n] = f32x4{0, 0, 0, 0};
         }
         const auto load_attn = [&](int c) {
-            const char *at = pa + (size_t)c * a.d.Hv * OP * kDeltaSquare;
-            fragment<OP>(at, part * 2, kDeltaSquare, fa[0]);
-            fragment<OP>(at, part * 2 + upper, kDeltaSquare, fa[1]);
+            const char *at = pa + (size_t)c * a.d.Hv * 3 * kDeltaSquare;
+            fragment<3>(at, part * 2, kDeltaSquare, fa[0]);
+            fragment<3>(at, part * 2 + upper, kDeltaSquare, fa[1]);
             veq = *(const f32x4 *)(steps_of(c)->eq + mine);
         };
         // y of chunk c, whose u is in Us[c & 1]
         const auto make_y = [&](const int c, float (&y)[NT][4]) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                Sums<OO> o;
+                Sums<2> o;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     const f32x4 *from = (const f32x4 *)(Us[c & 1] + (n * 16 + col) * kPitchU + ks * 32 + grp * 8);
@@ -268,8 +268,8 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
                     float u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) u[e] = ks == 0 || upper ? u[e] : 0.0f;
-                    u32x4 planes[OP];
-                    split8<OP>(u, planes);
+                    u32x4 planes[3];
+                    split8<3>(u, planes);
                     o.add(fa[ks], planes);
                 }
                 const f32x4 p = o.total();

@@ -167,8 +167,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     // The system's matrix (its diagonal of ones left out), and the products of queries with keys, which go to memory
     // from here.  A block of 32 columns past the diagonal is never read.
     const int col = lane & 15, row4 = (lane >> 4) * 4;
-    constexpr int kPlanes = delta_attn_planes(DT, BWD);
-    char *const inv = a.ws + a.w.inv + of_v * 3 * kDeltaSquare, *const attn = a.ws + a.w.attn + of_v * kPlanes * kDeltaSquare;
+    char *const inv = a.ws + a.w.inv + of_v * 3 * kDeltaSquare, *const attn = a.ws + a.w.attn + of_v * 3 * kDeltaSquare;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         if (n > (wave | 1)) break;
@@ -195,8 +194,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
         }
         // row tile, block of 32 columns, and the half of it, of the four values
         const int tile = BWD ? n : wave, block = (BWD ? wave : n) >> 1, eight = ((BWD ? wave : n) & 1) * 2 + (lane >> 5);
-        put_planes<kPlanes>((uint16_t *)(attn + (tile * 2 + block) * 1024 + (col + eight * 16) * 16 + (lane >> 4 & 1) * 8),
-                            kDeltaSquare / 2, m);
+        put_planes<3>((uint16_t *)(attn + (tile * 2 + block) * 1024 + (col + eight * 16) * 16 + (lane >> 4 & 1) * 8),
+                      kDeltaSquare / 2, m);
     }
     __syncthreads();
 
