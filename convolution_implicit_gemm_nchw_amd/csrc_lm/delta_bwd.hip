@@ -610,7 +610,7 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
                 f[tid] = exp_any((float)(steps.G[63] - steps.G[tid]));
             }
             __syncthreads();                       // and the products have left the planes
-            settle();
+            settle(q_, read, write, FZ, OZ);
             ends = m0 ? 0.0f : ends * steps.last;   // both halves of the steps have read the states
             // the rows' factors; the chunk's end reaches its decays through the last of them
             const auto four = [&](const miconv_rows_t &rows, const auto &held, int n, int m, float (&v)[4]) {
@@ -716,7 +716,7 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
-            settle();
+            settle(q_, read, write);
             // The rows' products with normalised query and key.  A step's own dP_ii k_i and dP_ii q_i add the same to
             // q_i.dq_i and k_i.write_i, so they enter after the decays' part: its terms then cancel no further than its
             // definition's do, and the first step from a zero state gets a zero.

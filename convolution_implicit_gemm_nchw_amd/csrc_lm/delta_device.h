@@ -95,7 +95,8 @@ struct Sums {
                     s[i + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
                                                                        __builtin_bit_cast(bf16x8, b[j]), s[i + j], 0, 0, 0);
     }
-    // After settle().  Read here, not where the total is used.
+    // Read here, not where the total is used.  In the scans no branch lies between the products and this, and the compiler
+    // counts the states in between right; where one does, settle(s) goes first.
     DEVI f32x4 total() const {
         f32x4 t = s[ORDER];
 #pragma unroll

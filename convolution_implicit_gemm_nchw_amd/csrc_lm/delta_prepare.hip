@@ -142,7 +142,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
             }
         }
     }
-    settle();
+    settle(kk, qk);
     {
         const int operand = tid / kBlocks, in = tid % kBlocks;
         if (operand < 2) {
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     Tc[di] = __builtin_amdgcn_mfma_f32_16x16x4f32(-left[r], y[r], Tc[di], 0, 0, 0);
-                settle();
+                settle(Tc[di]);
             }
         }
         // block column `wave` of the inverse, zeros above the diagonal; transposed for the backward pass

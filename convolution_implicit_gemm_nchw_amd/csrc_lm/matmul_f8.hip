@@ -314,7 +314,7 @@ __global__ __launch_bounds__(64 * WC * WR) void f8_tile_kernel(F8Args a) {
             fill = fill + 1 < ST ? fill + 1 : 0;
         }
     }
-    settle();
+    settle(acc);
     constexpr int kW = FC * 32, kMine = 32 * kW, kMix = kW >= 64 ? 15 : 7;
     constexpr int kLanes = kW / 8;             // lanes per row of the output, eight columns each
     const int thread = again(threadIdx.x);     // nothing made from it takes registers during the products
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(512) void f8_few_kernel(const unsigned char *q, con
             }
         }
     }
-    settle();
+    settle(acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll

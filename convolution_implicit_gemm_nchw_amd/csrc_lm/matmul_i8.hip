@@ -274,6 +274,7 @@ __global__ __launch_bounds__(64 * WC * WR) void i8_tile_kernel(I8Args a) {
             next = next + 1 < ST ? next + 1 : 0;
         }
     }
+    settle(acc);
     __syncthreads();
     // Through LDS, 32 rows of the wave's FC*32 columns at a time, so that y is written
     // in 16-byte pieces of consecutive lanes; a row's pieces are permuted as above.
@@ -391,6 +392,7 @@ __global__ __launch_bounds__(512) void i8_few_kernel(const signed char *q, const
                 for (int j = 0; j < FT; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0[s][i], b0[s][j], acc[i][j], 0, 0, 0);
     }
+    settle(acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll

@@ -315,13 +315,26 @@ DEVI int again(int v) {
     return v;
 }
 
+// A value's place in the order of the asm statements: what computes it stays before, what uses it behind.
+template <typename T>
+DEVI void pin(T &v) {
+    asm volatile("" : "+v"(v));
+}
+template <typename T, int N>
+DEVI void pin(T (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) pin(v[i]);
+}
+
 // Between MFMAs and the first read of their sums.  The compiler adds the wait states that a read needs, but where a
 // branch lies between the two it was found (hipcc 7.2) to count them along the longer way only, and the last elements
 // of a sum were read before they were written.  24 states cover the longest MFMA; the read would wait for its own anyway.
-DEVI void settle() {
-    __builtin_amdgcn_sched_barrier(0);
+// The sums are named, because the compiler moves MFMAs behind these states otherwise, next to the reads.
+template <typename... S>
+DEVI void settle(S &...sums) {
+    (pin(sums), ...);
     asm volatile("s_nop 15\n\ts_nop 7");
-    __builtin_amdgcn_sched_barrier(0);
+    (pin(sums), ...);
 }
 
 // Orders this wave's LDS accesses: what a lane wrote before is read by the others after.
