@@ -82,9 +82,12 @@ void inputs(const miconv_gated_delta_t &d, size_t es, Checker *k) {
     k->input(rows_span(d.beta, d.B, d.Hv, d.L, 4), true);
 }
 
-size_t state_count(const miconv_gated_delta_t &d) { return (size_t)d.B * d.Hv * d.P * d.V; }
+// Counts of values.  Sizes that pass on their own can have products past 64 bits: from kMaxSpan + 1 on a count stands
+// for all larger ones, and no tensor is that large.
+size_t count(__int128 n) { return (size_t)(n > kMaxSpan ? kMaxSpan + 1 : n); }
+size_t state_count(const miconv_gated_delta_t &d, int states) { return count((__int128)states * d.Hv * d.P * d.V); }
 size_t saved_count(const miconv_gated_delta_t &d) {
-    return (size_t)d.B * d.Hv * delta_chunks(d.L) * delta_saved(d.P, d.V);
+    return count((__int128)d.B * d.Hv * delta_chunks(d.L) * delta_saved(d.P, d.V));
 }
 
 size_t capped(size_t bytes) { return bytes < MICONV_MAX_WORKSPACE_BYTES ? bytes : MICONV_MAX_WORKSPACE_BYTES; }
@@ -125,7 +128,9 @@ int gated_delta_states_size(int B, int Hv, int P, int V, int L, size_t *bytes_ou
     d.B = B, d.Hk = 1, d.Hv = Hv, d.P = P, d.V = V, d.L = L;
     const int bad = check_sizes(d, MICONV_F32);
     if (bad != MICONV_OK) return bad;
-    *bytes_out = saved_count(d) * 4;
+    const size_t n = saved_count(d);
+    if (n > kMaxSpan) return MICONV_ERR_TOO_LARGE;
+    *bytes_out = n * 4;
     return MICONV_OK;
 }
 
@@ -162,10 +167,10 @@ int gated_delta_fwd(const miconv_gated_delta_t *d, int dtype, void *workspace, s
     if (need > capped(workspace_bytes)) return MICONV_ERR_WORKSPACE;
     Checker k;
     inputs(*d, es, &k);
-    k.input(flat(d->initial_state, state_count(*d), 4), false);
+    k.input(flat(d->initial_state, state_count(*d, d->B), 4), false);
     k.input(flat(d->lengths, d->B, 4), false);
     k.output(rows_span(d->y, d->B, d->Hv * d->V, d->L, es), true);
-    k.output(flat(d->final_state, state_count(*d), 4), false);
+    k.output(flat(d->final_state, state_count(*d, d->B), 4), false);
     k.output(flat(d->states, saved_count(*d), 4), false);
     k.output(flat(workspace, need / 4, 4), true);
     if ((uintptr_t)workspace % 16 || (uintptr_t)d->states % 16) k.fail(MICONV_ERR_ALIGN);
@@ -186,13 +191,13 @@ int gated_delta_bwd(const miconv_gated_delta_t *d, int dtype, void *workspace, s
     k.input(flat(d->lengths, d->B, 4), false);
     k.input(flat(d->states, saved_count(*d), 4), true);
     k.input(rows_span(d->dy, d->B, d->Hv * d->V, d->L, es), true);
-    k.input(flat(d->d_final_state, state_count(*d), 4), false);
+    k.input(flat(d->d_final_state, state_count(*d, d->B), 4), false);
     k.output(rows_span(d->dq, d->B, d->Hk * d->P, d->L, es), true);
     k.output(rows_span(d->dk, d->B, d->Hk * d->P, d->L, es), true);
     k.output(rows_span(d->dv, d->B, d->Hv * d->V, d->L, es), true);
     k.output(flat(d->dg, steps, 4), true);
     k.output(flat(d->dbeta, steps, 4), true);
-    k.output(flat(d->d_initial_state, state_count(*d), 4), false);
+    k.output(flat(d->d_initial_state, state_count(*d, d->B), 4), false);
     k.output(flat(workspace, need / 4, 4), true);
     if ((uintptr_t)workspace % 16 || (uintptr_t)d->states % 16) k.fail(MICONV_ERR_ALIGN);
     const int bad = k.done();
@@ -205,7 +210,7 @@ int gated_delta_step(const miconv_gated_delta_t *d, int dtype, const float *stat
     const int bad_sizes = check_sizes(*d, dtype);
     if (bad_sizes != MICONV_OK) return bad_sizes;
     if (d->L != 1 || bad_size(slots) || (!slot_of && slots != d->B)) return MICONV_ERR_BAD_DIM;
-    const size_t es = elem_size(dtype), ns = (size_t)slots * d->Hv * d->P * d->V;
+    const size_t es = elem_size(dtype), ns = state_count(*d, slots);
     Checker k;
     inputs(*d, es, &k);
     k.input(flat(slot_of, d->B, 4), false);

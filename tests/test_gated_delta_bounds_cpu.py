@@ -1,0 +1,31 @@
+"""Sizes past what a call can take: refused, with no count that wraps (no GPU needed; addresses are never dereferenced)."""
+import ctypes
+
+import convolution_implicit_gemm_nchw_amd as mc
+import test_delta_layer_cpu as layer
+
+OK, E_BIG, at = layer.OK, layer.E_BIG, layer.at
+
+
+def test_saved_states_do_not_wrap():
+    need = ctypes.c_size_t(1)
+
+    def size(*a):
+        return mc.lib().gated_delta_states_size(*a, ctypes.byref(need))
+    assert size(16384, 65536, 256, 512, 1 << 30) == E_BIG      # 2^30 heads x 2^24 chunks x 163840 x 4 bytes, 0 modulo 2^64
+    assert size(1 << 30, 1, 1, 1, 1 << 30) == E_BIG
+    assert size(4, 32, 128, 128, 8192) == OK and need.value == 4 * 32 * 128 * (128 + 64) * 128 * 4
+
+
+def step(**kw):
+    kw = {**dict(L=1, q=layer.rows(0, 16, 1), k=layer.rows(1, 16, 1), v=layer.rows(2, 24, 1), g=layer.rows(3, 4, 1),
+                 beta=layer.rows(4, 4, 1), y=layer.rows(7, 24, 1)), **kw}
+    slots = kw.pop("slots")
+    return mc.lib().gated_delta_step(ctypes.byref(layer.delta_args(**kw)), 0, at(20), slots, at(22), at(20), None)
+
+
+def test_pools_of_states_do_not_wrap():
+    one = mc._Rows(at(0), 0, 0)
+    rows = dict(B=1, Hk=1, Hv=65536, P=256, V=512, q=one, k=mc._Rows(at(1), 0, 0), v=mc._Rows(at(2), 0, 0),
+                g=mc._Rows(at(3), 0, 0), beta=mc._Rows(at(4), 0, 0), y=mc._Rows(1 << 60, 1 << 25, 1))
+    assert step(slots=1 << 30, **rows) == E_BIG                # 2^63 values
