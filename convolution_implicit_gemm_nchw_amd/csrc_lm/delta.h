@@ -19,6 +19,7 @@ namespace miconv {
 
 constexpr int kDeltaChunk = 64;
 constexpr int kDeltaSlice = 16;            // value channels of one MFMA tile
+constexpr int kDeltaStepValues = 64;       // of one work-group of the single-token step
 
 constexpr int delta_chunks(int L) { return (L + kDeltaChunk - 1) / kDeltaChunk; }
 // Key channels are padded to whole loops of the kernels, value channels to a pair of tiles.

@@ -210,6 +210,8 @@ int gated_delta_step(const miconv_gated_delta_t *d, int dtype, const float *stat
     const int bad_sizes = check_sizes(*d, dtype);
     if (bad_sizes != MICONV_OK) return bad_sizes;
     if (d->L != 1 || bad_size(slots) || (!slot_of && slots != d->B)) return MICONV_ERR_BAD_DIM;
+    // the kernel numbers its work-groups in 31 bits
+    if ((long long)d->B * d->Hv * ((d->V + kDeltaStepValues - 1) / kDeltaStepValues) > 0x7fffffff) return MICONV_ERR_TOO_LARGE;
     const size_t es = elem_size(dtype), ns = state_count(*d, slots);
     Checker k;
     inputs(*d, es, &k);

@@ -390,18 +390,16 @@ int forward_by_width(const DeltaArgs &a, hipStream_t st) {
 // takes 64 value channels of one head; a thread four neighbouring channels of every 16th key channel.  64 sequences of
 // 32 heads of 128 and 128 channels: 49 us, 268 MB at 5.5 TB/s (the rate of a large copy is 4.95); one of 8 heads of 64
 // and 64: 4.6 us, a launch.
-constexpr int kStepValues = 64;
-
 template <int DT, int DK>
 __global__ __launch_bounds__(256) void delta_step_kernel(miconv_gated_delta_t d, const float *state, int slots,
                                                          const int *slot_of, float *state_out, int tiles, int first) {
     constexpr int kRows = DK / 16;
     typedef typename Elem<DT>::T T;
     __shared__ float ks[DK], qs[DK], sums[4][2];
-    __shared__ __attribute__((aligned(16))) float red[4][kStepValues];
+    __shared__ __attribute__((aligned(16))) float red[4][kDeltaStepValues];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int id = first + blockIdx.x, tile = id % tiles, bh = id / tiles, h = bh % d.Hv, b = bh / d.Hv;
-    const int hk = h / (d.Hv / d.Hk), v = tile * kStepValues + (tid & 15) * 4, p0 = tid >> 4;
+    const int hk = h / (d.Hv / d.Hk), v = tile * kDeltaStepValues + (tid & 15) * 4, p0 = tid >> 4;
     const int slot = slot_of ? slot_of[b] : b;
     const bool unused = slot < 0 || slot >= slots;
     T *const y = row_of<DT>(d.y, b, 0) + ((long long)h * d.V) * d.y.stride_d;
@@ -524,7 +522,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(miconv_gated_delta_t d,
 template <int DT>
 int step(const miconv_gated_delta_t &d, const float *state, int slots, const int *slot_of, float *state_out,
          hipStream_t st) {
-    const int tiles = (d.V + kStepValues - 1) / kStepValues;
+    const int tiles = (d.V + kDeltaStepValues - 1) / kDeltaStepValues;
     return launch_groups((long long)d.B * d.Hv * tiles, 256, [&](unsigned n, unsigned first) {
         switch (delta_key_pad(d.P)) {
             case 64:

@@ -694,7 +694,8 @@ int gated_delta_describe(const miconv_gated_delta_t *d, int dtype, int backward,
                          size_t buflen);
 /*
  * One time step for each of B sequences (L = 1): q, k, v, y [B][...] (stride_b, stride_d),
- * state [slots][Hv][P][V]; slots, slot_of and state_out as for causal_conv1d_step.
+ * state [slots][Hv][P][V]; slots, slot_of and state_out as for causal_conv1d_step.  B * Hv * (V / 64 rounded up)
+ * is below 2^31.
  */
 int gated_delta_step(const miconv_gated_delta_t *d, int dtype, const float *state, int slots, const int *slot_of,
                      float *state_out, void *stream);

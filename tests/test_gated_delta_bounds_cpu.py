@@ -29,3 +29,10 @@ def test_pools_of_states_do_not_wrap():
     rows = dict(B=1, Hk=1, Hv=65536, P=256, V=512, q=one, k=mc._Rows(at(1), 0, 0), v=mc._Rows(at(2), 0, 0),
                 g=mc._Rows(at(3), 0, 0), beta=mc._Rows(at(4), 0, 0), y=mc._Rows(1 << 60, 1 << 25, 1))
     assert step(slots=1 << 30, **rows) == E_BIG                # 2^63 values
+
+
+def test_steps_whose_groups_pass_31_bits():
+    """A work-group takes 64 value channels of a head and counts in 32 bits with a sign."""
+    none = dict(q=mc._Rows(at(0), 0, 0), k=mc._Rows(at(1), 0, 0), v=mc._Rows(at(2), 0, 0), g=mc._Rows(at(3), 0, 0),
+                beta=mc._Rows(at(4), 0, 0))
+    assert step(slots=1, B=1 << 25, Hk=1, Hv=32, P=1, V=129, y=mc._Rows(1 << 60, 32 * 129, 1), **none) == E_BIG
