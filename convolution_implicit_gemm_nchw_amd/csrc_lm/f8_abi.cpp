@@ -33,6 +33,7 @@ int quantize_f8(int B, int L, int C, int dtype, const void *x, long long stride_
     if (stride_c != 1 && C > 1 && stride_l != 1 && L > 1) return MICONV_ERR_BAD_DIM;
     if (stride_b < 0 || stride_l < 0 || stride_c < 0) return MICONV_ERR_BAD_DIM;
     const size_t es = elem_size(dtype), blocks = ((size_t)C + MICONV_I8_PAD - 1) / MICONV_I8_PAD, tokens = (size_t)B * L;
+    if (tokens * blocks > 0x7fffffff) return MICONV_ERR_TOO_LARGE;      // the kernels number them in 31 bits
     const __int128 one = (__int128)(L - 1) * stride_l + (__int128)(C - 1) * stride_c + 1;
     if (one > kMaxSpan) return MICONV_ERR_TOO_LARGE;
     Checker k;

@@ -622,7 +622,7 @@ int matmul_i8_describe(int B, int L, int O, int C_pad, size_t workspace_bytes, c
  * q is [B*L][C_pad] (e4m3 bits), C_pad = C rounded up to a multiple of 128, the padding 0;
  * scale is [C_pad / 128][B*L], e + 127 (e8m0 bits).  A block that holds an infinity or a NaN gets the scale's NaN,
  * 255, and NaN for each q.  A weight [O][C] is quantised in the same way; its transpose or a
- * gradient's, for the products of a backward pass, through the strides.
+ * gradient's, for the products of a backward pass, through the strides.  B * L * C_pad / 128 is below 2^31.
  */
 int quantize_f8(int B, int L, int C, int dtype, const void *x, long long stride_b, long long stride_l,
                 long long stride_c, unsigned char *q, unsigned char *scale, void *stream);

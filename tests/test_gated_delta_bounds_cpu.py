@@ -36,3 +36,11 @@ def test_steps_whose_groups_pass_31_bits():
     none = dict(q=mc._Rows(at(0), 0, 0), k=mc._Rows(at(1), 0, 0), v=mc._Rows(at(2), 0, 0), g=mc._Rows(at(3), 0, 0),
                 beta=mc._Rows(at(4), 0, 0))
     assert step(slots=1, B=1 << 25, Hk=1, Hv=32, P=1, V=129, y=mc._Rows(1 << 60, 32 * 129, 1), **none) == E_BIG
+
+
+def test_quantised_blocks_past_31_bits():
+    """The same for blocks of 128 channels of all tokens."""
+    def quantize(B, L, C, sc):
+        return mc.lib().quantize_f8(B, L, C, 1, at(0), 0, 1 if sc != 1 else 0, sc, 1 << 60, 1 << 59, None)
+    assert quantize(1 << 25, 1, 128 * 65, 0) == E_BIG
+    assert quantize(1 << 21, 1, 131072, 1) == E_BIG
