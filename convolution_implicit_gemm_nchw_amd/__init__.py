@@ -718,7 +718,8 @@ for _name, _args in {
         "matmul_f8_describe": [_I, _I, _I, _I, _SZ, ctypes.c_char_p, _SZ],
         "layer_norm_fwd": [_VP, _I, _VP],
         "layer_norm_bwd": [_VP, _I, _VP, _SZ, _VP],
-        "layer_norm_bwd_workspace_size": [_VP, _I, _SZ, _SZP]}.items():
+        "layer_norm_bwd_workspace_size": [_VP, _I, _SZ, _SZP],
+        "layer_norm_describe": [_VP, _I, _I, _SZ, ctypes.c_char_p, _SZ]}.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _I
@@ -916,6 +917,15 @@ def layer_norm_bwd(x, dy, stats, weight=None, bias=None, channel_major=False, le
     a weight, a bias).  `stats` is what the forward pass saved for the same x; dx 0 past the lengths, whose padding is
     no part of dw and db."""
     return _call(_bind.layer_norm_bwd, stream, x, dy, stats, weight, bias, channel_major, lengths, dx, dw, db, workspace)
+
+
+def layer_norm_describe(B, L, C, dtype=F32, channel_major=False, backward=False, workspace_bytes=MAX_WORKSPACE_BYTES):
+    """The kernel that a pass takes for contiguous tensors of these sizes."""
+    t = _Tokens(0, L * C, 1, L) if channel_major else _Tokens(0, L * C, C, 1)
+    n = _LayerNorm(B=B, L=L, C=C, x=t, y=t, dy=t, dx=t)
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.layer_norm_describe(ctypes.byref(n), dtype, int(backward), workspace_bytes, buf, 256), "layer_norm_describe")
+    return buf.value.decode()
 
 
 I8_PAD = 128

@@ -584,28 +584,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float *part, int 
 
 // ------------------------------------------------------------------ which kernel
 
-// Up to 1024 channels a wave, up to 8192 a work-group of 256 holds a token in registers (at 8192 the backward pass has 256
-// registers of them; another step would not fit).
-constexpr int kLongest = 8192;
-
 bool contiguous(const miconv_tokens_t &v, int C) { return v.stride_c == 1 || C == 1; }
-
-// Time lanes of the channel-major kernels: as many as leave most CUs a tile, forward two tiles; 0: a loop over the
-// channels.  4 x 2048 tokens of 2048 channels in bf16 take, with 256 tiles of 4 lanes and 512 of 2, forward 22.2 and 22.1 us
-// (fp32, a larger one: 43.8 and 37), backward 32 and 46, as its 256 work-groups then take two tiles each.
-struct RowsForm {
-    int lanes, threads;
-};
-
-RowsForm rows_form(const miconv_layer_norm_t &n, int dtype, bool backward) {
-    const int held = dtype == MICONV_BF16 ? 16 : 8, most = backward ? 512 : 1024;
-    int lanes = 8;
-    while (lanes > 1 && (most / lanes * held < n.C || (long long)n.B * ((n.L + lanes * 8 - 1) / (lanes * 8)) < (backward ? 200 : 400))) lanes /= 2;
-    if (most / lanes * held < n.C) return {0, most};
-    int threads = 256;
-    while (threads < most && threads / lanes * held < n.C) threads *= 2;
-    return {lanes, threads};
-}
 
 template <int DT>
 int tokens_fwd(const miconv_layer_norm_t &n, hipStream_t st) {
@@ -615,11 +594,13 @@ int tokens_fwd(const miconv_layer_norm_t &n, hipStream_t st) {
     launch_groups((tokens + Row<ROW>::kTokens - 1) / Row<ROW>::kTokens, Row<ROW>::kThreads, [&](unsigned g, unsigned first) { \
         hipLaunchKernelGGL((norm_fwd_kernel<DT, ROW, VPT>), dim3(g), dim3(Row<ROW>::kThreads), 0, st, n, f, first);   \
     })
-    if (n.C <= 512) return MICONV_NORM(64, 1);
-    if (n.C <= 1024) return MICONV_NORM(64, 2);
-    if (n.C <= 2048) return MICONV_NORM(256, 1);
-    if (n.C <= 4096) return MICONV_NORM(256, 2);
-    if (n.C <= kLongest) return MICONV_NORM(256, 4);
+    const TokensForm t = tokens_form(n.C);
+    if (t.threads == 64) return t.times == 1 ? MICONV_NORM(64, 1) : MICONV_NORM(64, 2);
+    switch (t.times) {
+        case 1: return MICONV_NORM(256, 1);
+        case 2: return MICONV_NORM(256, 2);
+        case 4: return MICONV_NORM(256, 4);
+    }
 #undef MICONV_NORM
     return launch_groups(tokens, 1024, [&](unsigned g, unsigned first) {
         hipLaunchKernelGGL(norm_fwd_long_kernel<DT>, dim3(g), dim3(1024), 0, st, n, f, first);
@@ -631,15 +612,16 @@ int tokens_bwd(const miconv_layer_norm_t &n, int parts, float *part, hipStream_t
     const FDiv f = make_fdiv((uint32_t)n.L);
 #define MICONV_NORM(ROW, VPT)                                                                                       \
     hipLaunchKernelGGL((norm_bwd_kernel<DT, ROW, VPT>), dim3(parts), dim3(Row<ROW>::kThreads), 0, st, n, f, parts, part)
-    if (n.C <= 512)
+    const TokensForm t = tokens_form(n.C);
+    if (t.threads == 64 && t.times == 1)
         MICONV_NORM(64, 1);
-    else if (n.C <= 1024)
+    else if (t.threads == 64)
         MICONV_NORM(64, 2);
-    else if (n.C <= 2048)
+    else if (t.times == 1)
         MICONV_NORM(256, 1);
-    else if (n.C <= 4096)
+    else if (t.times == 2)
         MICONV_NORM(256, 2);
-    else if (n.C <= kLongest)
+    else if (t.times == 4)
         MICONV_NORM(256, 4);
     else
         hipLaunchKernelGGL(norm_bwd_long_kernel<DT>, dim3(parts), dim3(1024), 0, st, n, f, parts, part);
@@ -650,12 +632,12 @@ int tokens_bwd(const miconv_layer_norm_t &n, int parts, float *part, hipStream_t
 template <int DT>
 int rows_fwd(const miconv_layer_norm_t &n, hipStream_t st) {
     const RowsForm f = rows_form(n, DT, false);
-    const int lanes = f.lanes ? f.lanes : 8, tiles = (n.L + lanes * 8 - 1) / (lanes * 8);
+    const int tiles = (n.L + f.lanes * 8 - 1) / (f.lanes * 8);
     constexpr int R = DT == 1 ? 16 : 8;
     return launch_groups((long long)n.B * tiles, 1024, [&](unsigned g, unsigned first) {
 #define MICONV_NORM(TL, LOOP) \
     hipLaunchKernelGGL((norm_rows_fwd_kernel<DT, TL, R, LOOP>), dim3(g), dim3(f.threads), 0, st, n, tiles, first)
-        switch (f.lanes) {
+        switch (f.loop ? 0 : f.lanes) {
             case 8: MICONV_NORM(8, false); break;
             case 4: MICONV_NORM(4, false); break;
             case 2: MICONV_NORM(2, false); break;
@@ -669,11 +651,11 @@ int rows_fwd(const miconv_layer_norm_t &n, hipStream_t st) {
 template <int DT>
 int rows_bwd(const miconv_layer_norm_t &n, int parts, float *part, hipStream_t st) {
     const RowsForm f = rows_form(n, DT, true);
-    const int lanes = f.lanes ? f.lanes : 8, tiles = (n.L + lanes * 8 - 1) / (lanes * 8);
+    const int tiles = (n.L + f.lanes * 8 - 1) / (f.lanes * 8);
     constexpr int R = DT == 1 ? 16 : 8;
 #define MICONV_NORM(TL, LOOP) \
     hipLaunchKernelGGL((norm_rows_bwd_kernel<DT, TL, R, LOOP>), dim3(parts), dim3(f.threads), 0, st, n, tiles, parts, part)
-    switch (f.lanes) {
+    switch (f.loop ? 0 : f.lanes) {
         case 8: MICONV_NORM(8, false); break;
         case 4: MICONV_NORM(4, false); break;
         case 2: MICONV_NORM(2, false); break;
@@ -685,6 +667,27 @@ int rows_bwd(const miconv_layer_norm_t &n, int parts, float *part, hipStream_t s
 }
 
 }  // namespace
+
+// Up to 1024 channels a wave, up to 8192 a work-group of 256 holds a token in registers (at 8192 the backward pass has 256
+// registers of them; another step would not fit).
+TokensForm tokens_form(int C) {
+    if (C <= 1024) return {64, C <= 512 ? 1 : 2};
+    if (C <= 8192) return {256, C <= 2048 ? 1 : C <= 4096 ? 2 : 4};
+    return {1024, 0};
+}
+
+// Time lanes of the channel-major kernels: as many as leave most CUs a tile, forward two tiles.
+// 4 x 2048 tokens of 2048 channels in bf16 take, with 256 tiles of 4 lanes and 512 of 2, forward 22.2 and 22.1 us
+// (fp32, a larger one: 43.8 and 37), backward 32 and 46, as its 256 work-groups then take two tiles each.
+RowsForm rows_form(const miconv_layer_norm_t &n, int dtype, bool backward) {
+    const int held = dtype == MICONV_BF16 ? 16 : 8, most = backward ? 512 : 1024;
+    int lanes = 8;
+    while (lanes > 1 && (most / lanes * held < n.C || (long long)n.B * ((n.L + lanes * 8 - 1) / (lanes * 8)) < (backward ? 200 : 400))) lanes /= 2;
+    if (most / lanes * held < n.C) return {8, most, true};
+    int threads = 256;
+    while (threads < most && threads / lanes * held < n.C) threads *= 2;
+    return {lanes, threads, false};
+}
 
 bool norm_tokens_first(const miconv_layer_norm_t &n, bool backward) {
     if (!contiguous(n.x, n.C)) return false;
@@ -704,8 +707,7 @@ int norm_parts(const miconv_layer_norm_t &n, int dtype, size_t budget) {
         const int rows = n.C <= 2048 ? 1024 : n.C <= 4096 ? 512 : 256;
         if (most > rows) most = rows;
     } else {
-        const RowsForm f = rows_form(n, dtype, true);
-        const int steps = (f.lanes ? f.lanes : 8) * 8;
+        const int steps = rows_form(n, dtype, true).lanes * 8;
         most = (long long)n.B * ((n.L + steps - 1) / steps);
         if (most > 256) most = 256;
     }

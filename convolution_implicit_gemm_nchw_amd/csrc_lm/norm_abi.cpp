@@ -2,6 +2,7 @@
 // workspace, launches.
 #include <float.h>
 #include <hip/hip_runtime_api.h>
+#include <stdio.h>
 
 #include "lm_check.h"
 #include "norm.h"
@@ -55,6 +56,31 @@ int layer_norm_bwd_workspace_size(const miconv_layer_norm_t *n, int dtype, size_
     if (bad_sizes != MICONV_OK) return bad_sizes;
     const size_t cap = MICONV_MAX_WORKSPACE_BYTES;
     *bytes_out = parts_bytes(*n, norm_parts(*n, dtype, workspace_limit < cap ? workspace_limit : cap));
+    return MICONV_OK;
+}
+
+int layer_norm_describe(const miconv_layer_norm_t *n, int dtype, int backward, size_t workspace_bytes, char *buf,
+                        size_t buflen) {
+    if (!buf || buflen == 0) return MICONV_ERR_NULL;
+    buf[0] = 0;
+    if (!n) return MICONV_ERR_NULL;
+    const int bad = check_sizes(*n, dtype);
+    if (bad != MICONV_OK) return bad;
+    char parts[32] = "";
+    if (backward) {
+        const size_t cap = MICONV_MAX_WORKSPACE_BYTES;
+        const int p = norm_parts(*n, dtype, workspace_bytes < cap ? workspace_bytes : cap);
+        if (parts_bytes(*n, p) > workspace_bytes) return MICONV_ERR_WORKSPACE;
+        snprintf(parts, sizeof parts, " parts=%d", p);
+    }
+    if (norm_tokens_first(*n, backward != 0)) {
+        const TokensForm f = tokens_form(n->C);
+        snprintf(buf, buflen, "algo=norm_tokens threads=%d times=%d%s", f.threads, f.times, parts);
+    } else {
+        const RowsForm f = rows_form(*n, dtype, backward != 0);
+        snprintf(buf, buflen, "algo=%s lanes=%d threads=%d%s", f.loop ? "norm_rows_loop" : "norm_rows", f.lanes, f.threads,
+                 parts);
+    }
     return MICONV_OK;
 }
 

@@ -737,6 +737,10 @@ typedef struct miconv_layer_norm {
 int layer_norm_fwd(const miconv_layer_norm_t *n, int dtype, void *stream);
 int layer_norm_bwd(const miconv_layer_norm_t *n, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 int layer_norm_bwd_workspace_size(const miconv_layer_norm_t *n, int dtype, size_t workspace_limit, size_t *bytes_out);
+/* One-line description of the kernel that a pass runs for these sizes and strides: its threads, time lanes and, backward
+ * under workspace_bytes, work-groups. */
+int layer_norm_describe(const miconv_layer_norm_t *n, int dtype, int backward, size_t workspace_bytes, char *buf,
+                        size_t buflen);
 
 /* Static text for a status code (never NULL). */
 const char *miconv_status_string(int status);

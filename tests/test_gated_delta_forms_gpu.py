@@ -2,11 +2,13 @@
 import pytest
 import torch
 
+import delta_reference as ref
+import test_norm_f8_gpu as layer
 import test_state_space_gpu as base
 
 pytestmark = pytest.mark.gpu
 mc = base.mc
-DEV = base.DEV
+DEV, TDT = base.DEV, base.TDT
 
 
 def rounded_between(got, lower, upper):
@@ -31,3 +33,39 @@ def test_bf16_outputs_are_fp32_sums_rounded_once(mc, size):
     assert bool((want > 0).all())
     rounded = rounded_between(y, want * (1 - 2.0 ** -20), want * (1 + 2.0 ** -20))
     assert rounded
+
+
+# ------------------------------------------------------------------ channel-major layer norm: 2, 4 and 8 time lanes
+
+#             B  L     C    time lanes forward and backward; ends inside the last tile of each
+LANES = {(4, 1003, 40): (1, 2), (8, 1003, 40): (2, 4), (8, 1701, 70): (4, 8), (16, 1701, 33): (8, 8), (4, 1003, 1100): (1, 2),
+         (8, 1701, 300): (4, 8)}
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("size", LANES, ids=lambda s: "-".join(map(str, s)))
+def test_layer_norm_over_time_lanes(mc, size, ragged, dt):
+    B, L, C = size
+    code = mc.BF16 if dt == "bf16" else mc.F32
+    form = [mc.layer_norm_describe(*size, dtype=code, channel_major=True, backward=b).split() for b in (False, True)]
+    assert [f[:2] for f in form] == [["algo=norm_rows", f"lanes={n}"] for n in LANES[size]]
+    (x, cx), (dy, cdy), w, b, n, want = layer.norm_case(B, L, C, dt, True, ragged, True)
+    (y, cy), (dx, cdx) = base.out_view((B, C, L), dt), base.out_view((B, C, L), dt)
+    stats = mc.layer_norm_stats(x, channel_major=True)
+    stats.fill_(float("nan"))
+    kw = dict(channel_major=True, lengths=n[1])
+    mc.layer_norm_fwd(x, w, b, y=y, stats=stats, **kw)
+    _, dw, db = mc.layer_norm_bwd(x, dy, stats, w, b, dx=dx, **kw)
+    layer.agree("y", y.transpose(1, 2), *want["y"], ref.HALF[dt])
+    layer.agree("dx", dx.transpose(1, 2), *want["dx"], ref.HALF[dt])
+    layer.agree("dw", dw, *want["dw"])
+    layer.agree("db", db, *want["db"])
+    # several tiles to a work-group
+    ws = torch.full((3 * 8 * C + 64,), 0xff, dtype=torch.uint8, device=DEV)
+    dx2, dw, db = mc.layer_norm_bwd(x, dy, stats, w, b, workspace=ws[:3 * 8 * C], **kw)
+    assert torch.equal(dx2, dx) and bool((ws[3 * 8 * C:] == 0xff).all())
+    layer.agree("dw of three work-groups", dw, *want["dw"])
+    layer.agree("db of three work-groups", db, *want["db"])
+    for check in (cx, cdy, cy, cdx):
+        check()
