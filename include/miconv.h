@@ -633,7 +633,8 @@ int quantize_f8(int B, int L, int C, int dtype, const void *x, long long stride_
  * [C_pad / 128][B*L], wscale [C_pad / 128][O]; a scale of 255 makes the token's, or channel's, y NaN.
  * y, out_dtype and the workspace as for matmul_i8.  Sums are fp32; y is rounded once.  For an fp32 y the operands are
  * multiplied as bf16 numbers, which hold q * scale exactly between 2^-126 and 2^128: more than that counts as infinite,
- * less as zero.  For a bf16 y products of 64 neighbouring k that are 2^13 times smaller than the largest of them may be lost.
+ * less as zero.  For a bf16 y products of 64 neighbouring k that are 2^13 times smaller than the largest of them may be lost:
+ * before it is rounded y is off by at most 2^-10 of the sum of its products' magnitudes, a quarter of a bf16 number's half step.
  */
 int matmul_f8(int B, int L, int O, int C_pad, const unsigned char *q, const unsigned char *qscale,
               const unsigned char *wq, const unsigned char *wscale, const float *bias, int channel_major, int out_dtype,

@@ -69,3 +69,93 @@ def test_layer_norm_over_time_lanes(mc, size, ragged, dt):
     layer.agree("db of three work-groups", db, *want["db"])
     for check in (cx, cdy, cy, cdx):
         check()
+
+
+# ------------------------------------------------------------------ 8-bit float products: every tile
+
+#            T     C     O      kernel; ends inside the tiles, one block of k, odd and even numbers of blocks
+PRODUCTS = [((1500, 100, 1601), "tile=128 stages=2 splits=1"),
+            ((1500, 300, 1600), "tile=128 stages=2 splits=1"),
+            ((1500, 8200, 1601), "tile=128 stages=2 splits=3"),
+            ((3003, 100, 3100), "tile=256 stages=2 splits=1"),
+            ((3003, 250, 3101), "tile=256 stages=2 splits=1"),
+            ((3003, 300, 3100), "tile=256 stages=2 splits=1"),
+            ((3100, 1100, 3003), "tile=256 stages=2 splits=1")]
+
+
+# What a bf16 output may be off by before it is rounded, of the sum of its products' magnitudes: the 8-bit matrix instruction
+# adds eight products at a time and drops what lies below 2^-13 of the largest, 7 x 2^-13 of that at most.
+DROPPED = 2.0 ** -10
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("size,kernel", PRODUCTS, ids=lambda s: "-".join(map(str, s)) if isinstance(s, tuple) else "")
+def test_product_tiles(mc, size, kernel, out):
+    """Against the 64-bit product, with either order of y; and the bits of the small tiles, which add each output's products
+    in the same order, for some hundred tokens at a time."""
+    T, C, O = size
+    f = base.Data(2, "f32")
+    x, w = layer.f8_inputs(f, T, C, "f32"), torch.randn(O, C, generator=f.gen) * C ** -0.5
+    b = torch.randn(O, generator=f.gen)
+    q, s, wq, ws = *mc.quantize_f8(x.to(DEV)), *mc.quantize_f8(w.to(DEV))
+    K = q.shape[1]
+    assert kernel in mc.matmul_f8_describe(T, O, K)
+    e, we = s.view(torch.uint8).cpu().t().int() - 127, ws.view(torch.uint8).cpu().t().int() - 127
+    want, size_of = ref.product(q.float().cpu(), e, wq.float().cpu(), we)
+    bound = (K / 16 + 8) * ref.U * size_of + 2 * ref.U * (size_of + b.abs().double())
+    if out == "bf16":
+        bound = bound + DROPPED * size_of
+    kw = dict(out_dtype=TDT[out])
+    y = mc.matmul_f8(q, s, wq, ws, b.to(DEV), **kw)
+    layer.agree("y", y, want + b.double(), bound, ref.HALF[out])
+    for L in {T, max(d for d in range(1, 33) if T % d == 0)}:
+        z = torch.full((T // L, O, L), float("nan"), dtype=TDT[out], device=DEV)
+        mc.matmul_f8(q, s, wq, ws, b.to(DEV), length=L, y=z)
+        assert torch.equal(z.transpose(1, 2).reshape(T, O), y), L
+    whole = mc.matmul_f8(q, s, wq, ws, b.to(DEV), workspace=torch.empty(0, dtype=torch.uint8, device=DEV), **kw)
+    layer.agree("without splits", whole, want + b.double(), bound, ref.HALF[out])
+    for t in range(0, T, 150):
+        n = min(t + 150, T)
+        if n - t <= 64:
+            continue                                   # the kernel of few tokens adds in an order of its own
+        assert "tile=64" in mc.matmul_f8_describe(n - t, O, K)
+        part = mc.matmul_f8(q[t:n].contiguous(), s[:, t:n].contiguous(), wq, ws, b.to(DEV),
+                            workspace=torch.empty(0, dtype=torch.uint8, device=DEV), **kw)
+        assert torch.equal(part, whole[t:n]), t
+
+
+def test_product_past_the_caches(mc):
+    """A bf16 output of 128 MB, which is written past the caches: 50 of its rows, and both orders of all of it."""
+    T, C, O, L = 8200, 250, 8200, 41
+    assert T * O * 2 >= 128 << 20 and "tile=256" in mc.matmul_f8_describe(T, O, 256)
+    f = base.Data(12, "f32")
+    x, w = torch.randn(T, C, generator=f.gen), torch.randn(O, C, generator=f.gen)
+    q, s, wq, ws = *mc.quantize_f8(x.to(DEV)), *mc.quantize_f8(w.to(DEV))
+    y = mc.matmul_f8(q, s, wq, ws, out_dtype=torch.bfloat16)
+    rows = torch.cat([torch.arange(20), torch.randint(T, (10,), generator=f.gen), torch.arange(T - 20, T)])
+    e, we = s.view(torch.uint8).cpu().t().int() - 127, ws.view(torch.uint8).cpu().t().int() - 127
+    want, size_of = ref.product(q.float().cpu()[rows], e[rows], wq.float().cpu(), we)
+    layer.agree("rows", y[rows.to(DEV)], want, (256 / 16 + 8) * ref.U * size_of + DROPPED * size_of, ref.HALF["bf16"])
+    z = torch.full((T // L, O, L), float("nan"), dtype=torch.bfloat16, device=DEV)
+    mc.matmul_f8(q, s, wq, ws, length=L, y=z)
+    assert torch.equal(z.transpose(1, 2).reshape(T, O), y)
+
+
+@pytest.mark.parametrize("T", [5, 40, 100])
+def test_product_of_numbers_of_all_sizes(mc, T):
+    """Products from 2^-18 to 2^17 side by side: what is dropped stays within DROPPED.  All are positive here, so
+    that it adds up."""
+    gen = torch.Generator().manual_seed(13)
+    C, O = 640, 90
+    x, w = (torch.exp2(-9 + 17.5 * torch.rand(n, C, generator=gen)) for n in (T, O))
+    x[0], w[0] = 2.0 ** -6, 1.0                        # one large product among eight, the others just below what it keeps
+    x[0, 3::8] = 256.0
+    x[1], w[1] = 0.0625, 448.0                         # in blocks of k that turn against each other
+    x[1, ::64] = 448.0
+    q, wq = (t.to(DEV).to(torch.float8_e4m3fn) for t in (x, w))
+    one, wone = (torch.full((C // 128, n), 127, dtype=torch.uint8, device=DEV).view(torch.float8_e8m0fnu) for n in (T, O))
+    want, size_of = ref.product(q.float().cpu(), torch.zeros(T, C // 128, dtype=torch.int32), wq.float().cpu(),
+                                torch.zeros(O, C // 128, dtype=torch.int32))
+    sums = (C / 16 + 8) * ref.U * size_of
+    layer.agree("bf16", mc.matmul_f8(q, one, wq, wone, out_dtype=torch.bfloat16), want, sums + DROPPED * size_of, ref.HALF["bf16"])
+    layer.agree("fp32", mc.matmul_f8(q, one, wq, wone), want, sums, ref.HALF["f32"])
