@@ -21,15 +21,15 @@ namespace {
 // times du, dS - (e k)^T (beta F); the others compute attn^T dy, for the chunk that comes next, and meanwhile
 // (e q)^T dy for all key channels, half of which they hand over through LDS.  Bound like that one by the chain's
 // latency: 2 x 2048 steps of 16 heads of 128 and 128 channels in bf16, 32 chunks, take 100 us.
-template <int DT, int DK, int NT>
+template <int DT, int DK>
 __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
-    constexpr int TI = in_planes(DT), kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = NT * 16;
+    constexpr int TI = in_planes(DT), kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = kDeltaSlice;
     constexpr int kPitchS = DK + 8, kPitchT = kDeltaChunk + 8, kPlaneS = kN * kPitchS, kPlaneT = kN * kPitchT;
     constexpr int kPitchF = kDeltaChunk + 4, kHalf = kTiles < 8 ? kTiles : kTiles / 2;   // tiles of the chain's waves
     typedef typename Elem<DT>::T T;
     __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * kPlaneS], Up[3 * kPlaneT], Wp[3 * kPlaneT];
     __shared__ __attribute__((aligned(16))) float Bs[2][kN * kPitchF];   // attn^T dy of this chunk and the next
-    __shared__ __attribute__((aligned(16))) float Qs[kHalf * NT * 64 * 4];   // (e q)^T dy as accumulators
+    __shared__ __attribute__((aligned(16))) float Qs[kHalf * 64 * 4];   // (e q)^T dy as accumulators
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
     const bool queries = wave >= 4, owner = wave * kMT < kTiles;
     const int part = wave & 3, row4 = grp * 4, mine = part * 16 + row4;
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
     int chunks = (valid - steps_first + kDeltaChunk - 1) / kDeltaChunk;
     chunks = chunks < 0 ? 0 : (chunks > a.s.nc ? a.s.nc : chunks);
 
-    f32x4 S[kMT][NT];
+    f32x4 S[kMT];
     {
         const int P = a.last ? a.d.P : DK, V = a.last ? a.d.V : a.Vp;
         const float *in = a.last ? a.d.d_final_state : state_in;
@@ -50,22 +50,18 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
-                    S[i][n][r] = in && p < P && v < V ? in[(at * P + p) * V + v] : 0.0f;
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + col;
+                S[i][r] = in && p < P && v < V ? in[(at * P + p) * V + v] : 0.0f;
+            }
     }
     const auto put_state = [&] {
         if (!owner) return;
 #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float v[4] = {S[i][n][0], S[i][n][1], S[i][n][2], S[i][n][3]};
-                put_planes<3>(Sp + (n * 16 + col) * kPitchS + (wave * kMT + i) * 16 + row4, kPlaneS, v);
-            }
+        for (int i = 0; i < kMT; ++i) {
+            const float v[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
+            put_planes<3>(Sp + col * kPitchS + (wave * kMT + i) * 16 + row4, kPlaneS, v);
+        }
     };
     put_state();
     for (int i = threadIdx.x; i < 3 * kN * 8; i += 512)        // the zeros behind du's steps
@@ -107,13 +103,11 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    after[(size_t)((wave * kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
+            for (int r = 0; r < 4; ++r)
+                after[(size_t)((wave * kMT + i) * 16 + row4 + r) * a.Vp + v0 + col] = S[i][r];
     };
     // dS from `given`, (e q)^T dy of the wave's own tiles
-    const auto update = [&](int c, bool whole, f32x4 (&given)[kMT][NT]) {
+    const auto update = [&](int c, bool whole, f32x4 (&given)[kMT]) {
         if (!owner) return;
 #pragma unroll
         for (int i = 0; i < kMT; ++i) {
@@ -126,17 +120,14 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
             const int tile = wave * kMT + i;
             planes_of<DT>(only<DT>(ft[i][0], tile * 16 + col < a.d.P), k0);
             planes_of<DT>(only<DT>(ft[i][1], tile * 16 + col < a.d.P), k1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> sum;
-                u32x4 w[3];
-                const uint16_t *from = Wp + (n * 16 + col) * kPitchT + grp * 8;
-                get_planes<3>(from, kPlaneT, w);
-                sum.add(k0, w);
-                get_planes<3>(from + 32, kPlaneT, w);
-                sum.add(k1, w);
-                S[i][n] = S[i][n] * last + (given[i][n] + sum.total());
-            }
+            Sums<2> sum;
+            u32x4 w[3];
+            const uint16_t *from = Wp + col * kPitchT + grp * 8;
+            get_planes<3>(from, kPlaneT, w);
+            sum.add(k0, w);
+            get_planes<3>(from + 32, kPlaneT, w);
+            sum.add(k1, w);
+            S[i] = S[i] * last + (given[i] + sum.total());
         }
         put_state();
     };
@@ -151,12 +142,7 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
     if (!chunks) {
     } else if (!queries) {
         u32x4 fk[kLate ? 1 : kKS][TI], fi[2][3];
-        T *out[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int v = v0 + n * 16 + col;
-            out[n] = row_of<DT>(a.d.dv, B, h * a.d.V + (v < a.d.V ? v : 0));
-        }
+        T *const out = row_of<DT>(a.d.dv, B, h * a.d.V + (v0 + col < a.d.V ? v0 + col : 0));
         const auto load_k = [&](int c) {
 #pragma unroll
             for (int ks = 0; ks < kKS && !kLate; ++ks)
@@ -173,72 +159,57 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
             const int next = c ? c - 1 : 0;
             save_state(c);
             __syncthreads();
-            Sums<2> kd[NT];
+            Sums<2> kd;
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks) {
                 if constexpr (kLate) fragment<TI>(a.ws + a.w.k + of_k + c * step_k, part * kKS + ks, kPlaneK, fk[0]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    u32x4 s[3];
-                    get_planes<3>(Sp + (n * 16 + col) * kPitchS + ks * 32 + grp * 8, kPlaneS, s);
-                    kd[n].add(fk[kLate ? 0 : ks], s);
-                }
+                u32x4 s[3];
+                get_planes<3>(Sp + col * kPitchS + ks * 32 + grp * 8, kPlaneS, s);
+                kd.add(fk[kLate ? 0 : ks], s);
             }
+            const f32x4 k = kd.total(), back = *(const f32x4 *)(Bs[c & 1] + col * kPitchF + mine);
+            float du[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const f32x4 k = kd[n].total(), back = *(const f32x4 *)(Bs[c & 1] + (n * 16 + col) * kPitchF + mine);
-                float du[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], k[r], back[r]);
-                put_planes<3>(Up + (n * 16 + col) * kPitchT + mine, kPlaneT, du);
-            }
+            for (int r = 0; r < 4; ++r) du[r] = __builtin_fmaf(vfk[r], k[r], back[r]);
+            put_planes<3>(Up + col * kPitchT + mine, kPlaneT, du);
             load_k(next);
             vfk = *(const f32x4 *)(steps_of(next)->fk + mine);
             __syncthreads();
             float *Fout = (float *)(a.ws + a.w.F) + (of_v + (size_t)c * a.d.Hv) * a.Vp * kDeltaChunk;
-            f32x4 F[NT];
+            Sums<2> sum;
+            u32x4 u[3];
+            const uint16_t *from = Up + col * kPitchT + grp * 8;
+            get_planes<3>(from + first_half, kPlaneT, u);
+            sum.add(fi[0], u);
+            get_planes<3>(from + 32, kPlaneT, u);
+            sum.add(fi[1], u);
+            const f32x4 F = sum.total();
+            float w[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> sum;
-                u32x4 u[3];
-                const uint16_t *from = Up + (n * 16 + col) * kPitchT + grp * 8;
-                get_planes<3>(from + first_half, kPlaneT, u);
-                sum.add(fi[0], u);
-                get_planes<3>(from + 32, kPlaneT, u);
-                sum.add(fi[1], u);
-                F[n] = sum.total();
-                float w[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) w[r] = -(vek[r] * (vbeta[r] * F[n][r]));
-                put_planes<3>(Wp + (n * 16 + col) * kPitchT + mine, kPlaneT, w);
-            }
+            for (int r = 0; r < 4; ++r) w[r] = -(vek[r] * (vbeta[r] * F[r]));
+            put_planes<3>(Wp + col * kPitchT + mine, kPlaneT, w);
             // ahead of the stores: loads come back in their order, stores among them
             const f32x4 beta = vbeta;
             load_m(a.w.inv, next, fi);
             vek = *(const f32x4 *)(steps_of(next)->ek + mine);
             vbeta = *(const f32x4 *)(steps_of(next)->beta + mine);
             __syncthreads();
-            f32x4 given[kMT][NT];
+            f32x4 given[kMT];
             if (owner) {
 #pragma unroll
                 for (int i = 0; i < kMT; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        given[i][n] = *(const f32x4 *)(Qs + (((wave * kMT + i) * NT + n) * 64 + lane) * 4);
+                    given[i] = *(const f32x4 *)(Qs + ((wave * kMT + i) * 64 + lane) * 4);
             }
             update(c, FULL, given);
             last = steps_of(next)->last;
             if constexpr (!kLate) load_turned(next, FULL || c);
+            *(f32x4 *)(Fout + (size_t)(v0 + col) * kDeltaChunk + mine) = F;
+            if (v0 + col < a.d.V) {
+                const int t = steps_first + c * kDeltaChunk + mine;
+                float dv[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                *(f32x4 *)(Fout + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = F[n];
-                if (v0 + n * 16 + col < a.d.V) {
-                    const int t = steps_first + c * kDeltaChunk + mine;
-                    float dv[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) dv[r] = FULL || t + r < valid ? beta[r] * F[n][r] : 0.0f;
-                    store4_until<DT>(out[n], FULL, t, a.d.L, dv);
-                }
+                for (int r = 0; r < 4; ++r) dv[r] = FULL || t + r < valid ? beta[r] * F[r] : 0.0f;
+                store4_until<DT>(out, FULL, t, a.d.L, dv);
             }
         };
         if (full < chunks) chunk(full, Whole<false>());
@@ -247,14 +218,9 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
         constexpr bool kAhead = TI == 1 && DK <= 128;    // queries likewise, where the registers hold them
         u32x4 fa[2][3];
         Raw8<DT> fq[kAhead ? 2 * kMT : 1][2];
-        Raw8<DT> fg[NT][2], fn[NT][2];         // dy as column operand: of this chunk, and of the next
+        Raw8<DT> fg[2], fn[2];                 // dy as column operand: of this chunk, and of the next
         f32x4 veq[2][2];                       // of the steps that fg holds
-        const T *grow[NT], *qrow[2 * kMT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int v = v0 + n * 16 + col;
-            grow[n] = row_of<DT>(a.d.dy, B, h * a.d.V + (v < a.d.V ? v : 0));
-        }
+        const T *const grow = row_of<DT>(a.d.dy, B, h * a.d.V + (v0 + col < a.d.V ? v0 + col : 0)), *qrow[2 * kMT];
         // tiles of queries that this wave multiplies: its own and those of the wave that it hands over to
         const auto tile_of = [&](int i) { return (i < kMT ? wave : part) * kMT + i % kMT; };
 #pragma unroll
@@ -264,10 +230,8 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
         }
         const auto load_dy = [&](int c, bool whole) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    fn[n][ks] = steps8<DT>(grow[n], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
+            for (int ks = 0; ks < 2; ++ks)
+                fn[ks] = steps8<DT>(grow, whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
         };
         const auto turned_q = [&](int i, int c, int ks, bool whole) {
             return steps8<DT>(qrow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
@@ -284,21 +248,16 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
         };
         // attn^T dy of chunk c, whose attn is in fa and dy in fn, to Bs[c & 1]; then the next one's are loaded
         const auto put_back = [&](int c, int next, bool whole) {
+            Sums<2> sum;
+            u32x4 g[TI];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> sum;
-                u32x4 g[TI];
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    planes_of<DT>(only<DT>(fn[n][ks], v0 + n * 16 + col < a.d.V && (ks || lower)), g);
-                    sum.add(fa[ks], g);
-                }
-                *(f32x4 *)(Bs[c & 1] + (n * 16 + col) * kPitchF + mine) = sum.total();
+            for (int ks = 0; ks < 2; ++ks) {
+                planes_of<DT>(only<DT>(fn[ks], v0 + col < a.d.V && (ks || lower)), g);
+                sum.add(fa[ks], g);
             }
+            *(f32x4 *)(Bs[c & 1] + col * kPitchF + mine) = sum.total();
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) fg[n][ks] = fn[n][ks];
+            for (int ks = 0; ks < 2; ++ks) fg[ks] = fn[ks];
             load_m(a.w.attn, next, fa);
             load_dy(next, whole);
         };
@@ -309,43 +268,37 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
         const auto chunk = [&](const int c, auto is_full) {
             constexpr bool FULL = decltype(is_full)::value;
             const int next = c ? c - 1 : 0;
-            u32x4 g[NT][2][3];                     // e dy, split while the other waves finish the chunk before
+            u32x4 g[2][3];                         // e dy, split while the other waves finish the chunk before
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int ks = 0; ks < 2; ++ks) {
+                float x[8];
+                widen8<DT>(only<DT>(fg[ks], v0 + col < a.d.V), x);
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    float x[8];
-                    widen8<DT>(only<DT>(fg[n][ks], v0 + n * 16 + col < a.d.V), x);
+                for (int e = 0; e < 8; ++e) x[e] *= veq[ks][e >> 2][e & 3];
+                split8<3>(x, g[ks]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= veq[ks][e >> 2][e & 3];
-                    split8<3>(x, g[n][ks]);
-#pragma unroll
-                    for (int o = 0; o < 3; ++o) asm volatile("" : "+v"(g[n][ks][o]));
-                }
+                for (int o = 0; o < 3; ++o) asm volatile("" : "+v"(g[ks][o]));
+            }
             save_state(c);
             __syncthreads();
-            f32x4 given[kMT][NT];
+            f32x4 given[kMT];
 #pragma unroll
             for (int i = 0; i < 2 * kMT; ++i) {
                 const int tile = tile_of(i);
                 if (kTiles < 8 && i < kMT) continue;     // with 64 key channels these waves own no tile
-                Sums<2> sum[NT];
+                Sums<2> sum;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     u32x4 q[TI];
                     if constexpr (!kAhead) fq[0][ks] = turned_q(i, c, ks, FULL);
                     planes_of<DT>(only<DT>(fq[kAhead ? i : 0][ks], tile * 16 + col < a.d.P), q);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) sum[n].add(q, g[n][ks]);
+                    sum.add(q, g[ks]);
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const f32x4 t = sum[n].total();
-                    if (i < kMT)
-                        given[i % kMT][n] = t;
-                    else
-                        *(f32x4 *)(Qs + ((tile * NT + n) * 64 + lane) * 4) = t;
-                }
+                const f32x4 t = sum.total();
+                if (i < kMT)
+                    given[i % kMT] = t;
+                else
+                    *(f32x4 *)(Qs + (tile * 64 + lane) * 4) = t;
             }
             load_q(next, FULL || c);
             __syncthreads();
@@ -361,11 +314,9 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
     // chunks past the sequence's end
     for (int c = chunks; queries && c < a.s.nc; ++c) {
         const float zeros[4] = {};
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (v0 + n * 16 + col < a.d.V)
-                store4_until<DT>(row_of<DT>(a.d.dv, B, h * a.d.V + v0 + n * 16 + col), steps_first + (c + 1) * kDeltaChunk <= a.d.L,
-                                 steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+        if (v0 + col < a.d.V)
+            store4_until<DT>(row_of<DT>(a.d.dv, B, h * a.d.V + v0 + col), steps_first + (c + 1) * kDeltaChunk <= a.d.L,
+                             steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
     }
     float *to = a.first ? a.d.d_initial_state : state_out;
     if (to && owner) {
@@ -374,12 +325,10 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
-                    if (p < P && v < V) to[(at * P + p) * V + v] = S[i][n][r];
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int p = (wave * kMT + i) * 16 + row4 + r, v = v0 + col;
+                if (p < P && v < V) to[(at * P + p) * V + v] = S[i][r];
+            }
     }
 }
 
@@ -847,8 +796,8 @@ __global__ __launch_bounds__((Grads<DT, DK>::kThreads)) void delta_grads_kernel(
 template <int DT, int DK>
 int backward(DeltaArgs a, hipStream_t st) {
     float *carry = (float *)(a.ws + a.w.state);
-    a.slices = a.Vp / 16;
-    hipLaunchKernelGGL((delta_bwd_kernel<DT, DK, 1>), dim3((unsigned)(a.s.nb * a.d.Hv * a.slices)), dim3(512), 0, st, a,
+    a.slices = a.Vp / kDeltaSlice;
+    hipLaunchKernelGGL((delta_bwd_kernel<DT, DK>), dim3((unsigned)(a.s.nb * a.d.Hv * a.slices)), dim3(512), 0, st, a,
                        carry, carry);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
 }

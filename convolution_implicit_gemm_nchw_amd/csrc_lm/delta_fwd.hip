@@ -5,7 +5,7 @@ namespace miconv {
 
 namespace {
 
-// One work-group carries a value slice of NT * 16 channels of one head through time; the state [DK][NT * 16] stays in
+// One work-group carries a value slice of 16 channels of one head through time; the state [DK][16] stays in
 // accumulators, key channels of it in each of the eight waves.  A chunk is a chain of which no step can wait:
 // k S, the inverse times X = v - e (k S), the state's update.  Four waves (16 steps each) go along it; the four others meanwhile compute y,
 // of the chunk before while the first ones multiply k S, and q S while those multiply by the inverse.  Row operands come from memory in
@@ -16,17 +16,17 @@ namespace {
 // 700, the state to LDS 450), 112 us for a prompt of 64 chunks, 32 heads of 128 and 128 channels in bf16, 256
 // work-groups.  Wider slices have fewer work-groups and chains as long, so a slice is one MFMA's 16 channels.
 // One role for all waves, in turn, took 152 us.
-template <int DK, int NT>
+template <int DK>
 struct Scan {
-    static constexpr int kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = NT * 16;
+    static constexpr int kKS = DK / 32, kTiles = DK / 16, kMT = kTiles > 8 ? kTiles / 8 : 1, kN = kDeltaSlice;
     static constexpr int kPitchS = DK + 8, kPitchT = kDeltaChunk + 8;   // bf16 elements
     static constexpr int kPlaneS = kN * kPitchS, kPlaneT = kN * kPitchT;
 };
 
-template <int DT, int DK, int NT, bool SAVE>
+template <int DT, int DK, bool SAVE>
 __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *state_in, float *state_out) {
     constexpr int TI = in_planes(DT);
-    typedef Scan<DK, NT> X;
+    typedef Scan<DK> X;
     typedef typename Elem<DT>::T T;
     constexpr int kPitchU = kDeltaChunk + 4;   // floats
     __shared__ __attribute__((aligned(16))) uint16_t Sp[3 * X::kPlaneS], Xp[3 * X::kPlaneT], Uf[3 * X::kPlaneT];
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
     chunks = chunks < 0 ? 0 : (chunks > a.s.nc ? a.s.nc : chunks);
 
     // the state: from the caller, from the slice of time before, or zeros
-    f32x4 S[X::kMT][NT];
+    f32x4 S[X::kMT];
     {
         const int P = a.first ? a.d.P : DK, V = a.first ? a.d.V : a.Vp;
         const float *in = a.first ? a.d.initial_state : state_in;
@@ -53,22 +53,18 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
-                    S[i][n][r] = in && p < P && v < V ? in[(at * P + p) * V + v] : 0.0f;
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + col;
+                S[i][r] = in && p < P && v < V ? in[(at * P + p) * V + v] : 0.0f;
+            }
     }
     const auto put_state = [&] {
         if (!owner) return;
 #pragma unroll
-        for (int i = 0; i < X::kMT; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float v[4] = {S[i][n][0], S[i][n][1], S[i][n][2], S[i][n][3]};
-                put_planes<3>(Sp + (n * 16 + col) * X::kPitchS + (wave * X::kMT + i) * 16 + row4, X::kPlaneS, v);
-            }
+        for (int i = 0; i < X::kMT; ++i) {
+            const float v[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
+            put_planes<3>(Sp + col * X::kPitchS + (wave * X::kMT + i) * 16 + row4, X::kPlaneS, v);
+        }
     };
     put_state();
     for (int i = threadIdx.x; i < 3 * X::kN * 8; i += 512)      // the zeros behind X's steps
@@ -102,20 +98,16 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             for (int ks = 0; ks < 2; ++ks)
                 ft[i][ks] = steps8<DT>(krow[i], whole, steps_first + c * kDeltaChunk + ks * 32 + grp * 8, valid);
     };
-    const auto times_state = [&](int c, f32x4 (&xS)[NT]) {
-        Sums<2> sum[NT];
+    const auto times_state = [&](int c, f32x4 &xS) {
+        Sums<2> sum;
 #pragma unroll
         for (int ks = 0; ks < X::kKS; ++ks) {
             if constexpr (kLate) fragment<TI>(px + c * step_k, part * X::kKS + ks, kPlaneK, fx[0]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                u32x4 s[3];
-                get_planes<3>(Sp + (n * 16 + col) * X::kPitchS + ks * 32 + grp * 8, X::kPlaneS, s);
-                sum[n].add(fx[kLate ? 0 : ks], s);
-            }
+            u32x4 s[3];
+            get_planes<3>(Sp + col * X::kPitchS + ks * 32 + grp * 8, X::kPlaneS, s);
+            sum.add(fx[kLate ? 0 : ks], s);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) xS[n] = sum[n].total();
+        xS = sum.total();
     };
     float *saved = SAVE ? (float *)a.d.states + (((size_t)B * a.d.Hv + h) * a.chunks + a.s.c0) * delta_saved(a.d.P, a.d.V) : nullptr;
     const auto save_state = [&] {
@@ -123,10 +115,8 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
             for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        saved[(size_t)((wave * X::kMT + i) * 16 + row4 + r) * a.Vp + v0 + n * 16 + col] = S[i][n][r];
+                for (int r = 0; r < 4; ++r)
+                    saved[(size_t)((wave * X::kMT + i) * 16 + row4 + r) * a.Vp + v0 + col] = S[i][r];
         }
     };
     const auto update = [&] {
@@ -137,17 +127,14 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             const bool in = (wave * X::kMT + i) * 16 + col < a.d.P;
             planes_of<DT>(only<DT>(ft[i][0], in), k0);
             planes_of<DT>(only<DT>(ft[i][1], in), k1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> sum;
-                u32x4 u[3];
-                const uint16_t *from = Uf + (n * 16 + col) * X::kPitchT + grp * 8;
-                get_planes<3>(from, X::kPlaneT, u);
-                sum.add(k0, u);
-                get_planes<3>(from + 32, X::kPlaneT, u);
-                sum.add(k1, u);
-                S[i][n] = S[i][n] * last + sum.total();
-            }
+            Sums<2> sum;
+            u32x4 u[3];
+            const uint16_t *from = Uf + col * X::kPitchT + grp * 8;
+            get_planes<3>(from, X::kPlaneT, u);
+            sum.add(k0, u);
+            get_planes<3>(from + 32, X::kPlaneT, u);
+            sum.add(k1, u);
+            S[i] = S[i] * last + sum.total();
         }
         put_state();
     };
@@ -166,21 +153,15 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
     if (!chunks) {
     } else if (!queries) {
         u32x4 fi[2][3];
-        Raw4<DT> vin[NT];
-        const T *vrow[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int v = v0 + n * 16 + col;
-            vrow[n] = row_of<DT>(a.d.v, B, h * a.d.V + (v < a.d.V ? v : 0));
-        }
+        Raw4<DT> vin;
+        const T *const vrow = row_of<DT>(a.d.v, B, h * a.d.V + (v0 + col < a.d.V ? v0 + col : 0));
         const auto load_inverse = [&](int c) {
             const char *at = pi + (size_t)c * a.d.Hv * 3 * kDeltaSquare;
             fragment<3>(at, part * 2, kDeltaSquare, fi[0]);
             fragment<3>(at, part * 2 + upper, kDeltaSquare, fi[1]);
         };
         const auto load_v = [&](int c, bool whole) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) vin[n] = steps4<DT>(vrow[n], whole, steps_first + c * kDeltaChunk + mine, valid);
+            vin = steps4<DT>(vrow, whole, steps_first + c * kDeltaChunk + mine, valid);
         };
         load_inverse(0);
         f32x4 vek = *(const f32x4 *)(steps_of(0)->ek + mine), vfk = *(const f32x4 *)(steps_of(0)->fk + mine);
@@ -197,38 +178,32 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             }
             save_state();
             __syncthreads();
-            f32x4 kS[NT];
+            f32x4 kS;
             times_state(c, kS);
             load_x(next);
+            float x[4];
+            widen4<DT>(vin, v0 + col < a.d.V, x);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float x[4];
-                widen4<DT>(vin[n], v0 + n * 16 + col < a.d.V, x);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], kS[n][r], x[r]);
-                put_planes<3>(Xp + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, x);
-            }
+            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(-vek[r], kS[r], x[r]);
+            put_planes<3>(Xp + col * X::kPitchT + mine, X::kPlaneT, x);
             vek = *(const f32x4 *)(steps_of(next)->ek + mine);
             if constexpr (FULL) load_v(next_full, true);
             __syncthreads();
+            Sums<2> sum;
+            u32x4 planes[3];
+            const uint16_t *from = Xp + col * X::kPitchT + grp * 8;
+            get_planes<3>(from, X::kPlaneT, planes);
+            sum.add(fi[0], planes);
+            get_planes<3>(from + second, X::kPlaneT, planes);
+            sum.add(fi[1], planes);
+            const f32x4 z = sum.total(), u = z * vbeta;
+            float uf[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> sum;
-                u32x4 x[3];
-                const uint16_t *from = Xp + (n * 16 + col) * X::kPitchT + grp * 8;
-                get_planes<3>(from, X::kPlaneT, x);
-                sum.add(fi[0], x);
-                get_planes<3>(from + second, X::kPlaneT, x);
-                sum.add(fi[1], x);
-                const f32x4 z = sum.total(), u = z * vbeta;
-                float uf[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) uf[r] = u[r] * vfk[r];
-                put_planes<3>(Uf + (n * 16 + col) * X::kPitchT + mine, X::kPlaneT, uf);
-                *(f32x4 *)(Us[c & 1] + (n * 16 + col) * kPitchU + mine) = u;
-                if constexpr (SAVE)
-                    *(f32x4 *)(saved + (size_t)DK * a.Vp + (size_t)(v0 + n * 16 + col) * kDeltaChunk + mine) = z;
-            }
+            for (int r = 0; r < 4; ++r) uf[r] = u[r] * vfk[r];
+            put_planes<3>(Uf + col * X::kPitchT + mine, X::kPlaneT, uf);
+            *(f32x4 *)(Us[c & 1] + col * kPitchU + mine) = u;
+            if constexpr (SAVE)
+                *(f32x4 *)(saved + (size_t)DK * a.Vp + (size_t)(v0 + col) * kDeltaChunk + mine) = z;
             load_inverse(next);
             vfk = *(const f32x4 *)(steps_of(next)->fk + mine);
             vbeta = *(const f32x4 *)(steps_of(next)->beta + mine);
@@ -242,14 +217,8 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
         if (full < chunks) chunk(full, Whole<false>());
     } else {
         u32x4 fa[2][3];
-        f32x4 veq = {0, 0, 0, 0}, qS[NT];
-        T *yrow[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int v = v0 + n * 16 + col;
-            yrow[n] = row_of<DT>(a.d.y, B, h * a.d.V + (v < a.d.V ? v : 0));
-            qS[n] = f32x4{0, 0, 0, 0};
-        }
+        f32x4 veq = {0, 0, 0, 0}, qS = {0, 0, 0, 0};
+        T *const yrow = row_of<DT>(a.d.y, B, h * a.d.V + (v0 + col < a.d.V ? v0 + col : 0));
         const auto load_attn = [&](int c) {
             const char *at = pa + (size_t)c * a.d.Hv * 3 * kDeltaSquare;
             fragment<3>(at, part * 2, kDeltaSquare, fa[0]);
@@ -257,45 +226,40 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             veq = *(const f32x4 *)(steps_of(c)->eq + mine);
         };
         // y of chunk c, whose u is in Us[c & 1]
-        const auto make_y = [&](const int c, float (&y)[NT][4]) {
+        const auto make_y = [&](const int c, float (&y)[4]) {
+            Sums<2> o;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Sums<2> o;
+            for (int ks = 0; ks < 2; ++ks) {
+                const f32x4 *from = (const f32x4 *)(Us[c & 1] + col * kPitchU + ks * 32 + grp * 8);
+                const f32x4 lo = from[0], hi = from[1];
+                float u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const f32x4 *from = (const f32x4 *)(Us[c & 1] + (n * 16 + col) * kPitchU + ks * 32 + grp * 8);
-                    const f32x4 lo = from[0], hi = from[1];
-                    float u[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                for (int e = 0; e < 8; ++e) u[e] = ks == 0 || upper ? u[e] : 0.0f;
+                u32x4 planes[3];
+                split8<3>(u, planes);
+                o.add(fa[ks], planes);
+            }
+            const f32x4 p = o.total();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = ks == 0 || upper ? u[e] : 0.0f;
-                    u32x4 planes[3];
-                    split8<3>(u, planes);
-                    o.add(fa[ks], planes);
-                }
-                const f32x4 p = o.total();
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    y[n][r] = __builtin_fmaf(veq[r], qS[n][r], p[r]);
-                    asm volatile("" : "+v"(y[n][r]));
-                }
+            for (int r = 0; r < 4; ++r) {
+                y[r] = __builtin_fmaf(veq[r], qS[r], p[r]);
+                asm volatile("" : "+v"(y[r]));
             }
         };
-        const auto put_y = [&](const int c, auto is_full, float (&y)[NT][4]) {
+        const auto put_y = [&](const int c, auto is_full, float (&y)[4]) {
             constexpr bool FULL = decltype(is_full)::value;
             const int t = steps_first + c * kDeltaChunk + mine;
+            if (v0 + col < a.d.V) {
+                // past the sequence's end: zeros, up to the end of the rows
+                if constexpr (!FULL) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (v0 + n * 16 + col < a.d.V) {
-                    // past the sequence's end: zeros, up to the end of the rows
-                    if constexpr (!FULL) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) y[n][r] = t + r < valid ? y[n][r] : 0.0f;
-                    }
-                    store4_until<DT>(yrow[n], FULL, t, a.d.L, y[n]);
+                    for (int r = 0; r < 4; ++r) y[r] = t + r < valid ? y[r] : 0.0f;
                 }
+                store4_until<DT>(yrow, FULL, t, a.d.L, y);
+            }
         };
         const auto finish = [&](const int c, auto is_full) {
-            float y[NT][4];
+            float y[4];
             make_y(c, y);
             put_y(c, is_full, y);
         };
@@ -306,7 +270,7 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
             save_state();
             __syncthreads();
             // the waves of the state are ahead till their x stands, and behind after it: y is stored then
-            float y[NT][4];
+            float y[4];
             if constexpr (!FIRST) make_y(c - 1, y);
             __syncthreads();
             load_attn(c);
@@ -336,11 +300,9 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
     // chunks past the sequence's end
     for (int c = chunks; queries && c < a.s.nc; ++c) {
         const float zeros[4] = {};
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (v0 + n * 16 + col < a.d.V)
-                store4_until<DT>(row_of<DT>(a.d.y, B, h * a.d.V + v0 + n * 16 + col), steps_first + (c + 1) * kDeltaChunk <= a.d.L,
-                                 steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
+        if (v0 + col < a.d.V)
+            store4_until<DT>(row_of<DT>(a.d.y, B, h * a.d.V + v0 + col), steps_first + (c + 1) * kDeltaChunk <= a.d.L,
+                             steps_first + c * kDeltaChunk + mine, a.d.L, zeros);
     }
     float *out = a.last ? a.d.final_state : state_out;
     if (out && owner) {
@@ -349,38 +311,31 @@ __global__ __launch_bounds__(512) void delta_fwd_kernel(DeltaArgs a, float *stat
 #pragma unroll
         for (int i = 0; i < X::kMT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + n * 16 + col;
-                    if (p < P && v < V) out[(at * P + p) * V + v] = S[i][n][r];
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int p = (wave * X::kMT + i) * 16 + row4 + r, v = v0 + col;
+                if (p < P && v < V) out[(at * P + p) * V + v] = S[i][r];
+            }
     }
 }
 
-template <int DT, int DK, int NT>
-int forward(const DeltaArgs &a, hipStream_t st) {
+template <int DT, int DK>
+int forward(DeltaArgs a, hipStream_t st) {
     float *carry = (float *)(a.ws + a.w.state);
+    a.slices = a.Vp / kDeltaSlice;
     const unsigned groups = (unsigned)(a.s.nb * a.d.Hv * a.slices);
     if (a.d.states)
-        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, true>), dim3(groups), dim3(512), 0, st, a, carry, carry);
+        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, true>), dim3(groups), dim3(512), 0, st, a, carry, carry);
     else
-        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, NT, false>), dim3(groups), dim3(512), 0, st, a, carry, carry);
+        hipLaunchKernelGGL((delta_fwd_kernel<DT, DK, false>), dim3(groups), dim3(512), 0, st, a, carry, carry);
     return hipGetLastError() == hipSuccess ? MICONV_OK : MICONV_ERR_HIP;
-}
-
-template <int DT, int DK>
-int forward_by_slices(DeltaArgs a, hipStream_t st) {
-    a.slices = a.Vp / 16;
-    return forward<DT, DK, 1>(a, st);
 }
 
 template <int DT>
 int forward_by_width(const DeltaArgs &a, hipStream_t st) {
     switch (delta_key_pad(a.d.P)) {
-        case 64: return forward_by_slices<DT, 64>(a, st);
-        case 128: return forward_by_slices<DT, 128>(a, st);
-        default: return forward_by_slices<DT, 256>(a, st);
+        case 64: return forward<DT, 64>(a, st);
+        case 128: return forward<DT, 128>(a, st);
+        default: return forward<DT, 256>(a, st);
     }
 }
 
