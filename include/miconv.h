@@ -631,9 +631,10 @@ int quantize_f8(int B, int L, int C, int dtype, const void *x, long long stride_
  *   y = sum over blocks j of 2^(qscale[j][m] - 127 + wscale[j][n] - 127) sum_{k in j} q[m][k] * wq[n][k]  (+ bias[n])
  * q [B*L][C_pad], wq [O][C_pad], 16-byte aligned, C_pad a multiple of 128 and at most 131072; qscale
  * [C_pad / 128][B*L], wscale [C_pad / 128][O]; a scale of 255 makes the token's, or channel's, y NaN.
- * y, out_dtype and the workspace as for matmul_i8.  Sums are fp32; y is rounded once.  For an fp32 y the operands are
+ * y, out_dtype and the workspace as for matmul_i8.  Sums are fp32; y is rounded once.  The operands are
  * multiplied as bf16 numbers, which hold q * scale exactly between 2^-126 and 2^128: more than that counts as infinite,
- * less as zero.  For a bf16 y products of 64 neighbouring k that are 2^13 times smaller than the largest of them may be lost:
+ * less as zero.  A bf16 y of more than 64 tokens is multiplied by 8-bit matrix instructions instead:
+ * products of 64 neighbouring k that are 2^13 times smaller than the largest of them may be lost, and
  * before it is rounded y is off by at most 2^-10 of the sum of its products' magnitudes, a quarter of a bf16 number's half step.
  */
 int matmul_f8(int B, int L, int O, int C_pad, const unsigned char *q, const unsigned char *qscale,

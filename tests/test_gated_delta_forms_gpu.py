@@ -124,6 +124,19 @@ def test_product_tiles(mc, size, kernel, out):
         assert torch.equal(part, whole[t:n]), t
 
 
+@pytest.mark.parametrize("size", [(1, 64, 64), (3, 130, 70), (16, 1000, 333), (17, 700, 1500), (33, 2000, 90), (64, 4096, 200)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_bf16_products_of_few_tokens_are_fp32_sums_rounded_once(mc, size):
+    """Few tokens wait for their loads, not for their products: the same sums for both types."""
+    T, C, O = size
+    f = base.Data(14, "f32")
+    x, w, b = layer.f8_inputs(f, T, C, "f32"), torch.randn(O, C, generator=f.gen), torch.randn(O, generator=f.gen)
+    args = (*mc.quantize_f8(x.to(DEV)), *mc.quantize_f8(w.to(DEV)), b.to(DEV))
+    assert "algo=f8_few" in mc.matmul_f8_describe(T, O, args[0].shape[1])
+    y = mc.matmul_f8(*args)
+    assert torch.equal(mc.matmul_f8(*args, out_dtype=torch.bfloat16), y.to(torch.bfloat16))
+
+
 def test_product_past_the_caches(mc):
     """A bf16 output of 128 MB, which is written past the caches: 50 of its rows, and both orders of all of it."""
     T, C, O, L = 8200, 250, 8200, 41
