@@ -4,7 +4,7 @@
 //
 // One work-group of four waves per (sequence, chunk, value head), three on a CU in bf16.  Latency bounds it: barriers between
 // the products, the substitution of 16 dependent rows and the inverse's blocks down each column, 12 us for a single
-// chunk.  2048 of them (a prompt of 4096 steps, 32 value heads on 16 key heads of 128 channels, bf16): 48 us.
+// chunk.  2048 of them (a prompt of 4096 steps, 32 value heads on 16 key heads of 128 channels, bf16): 50 us.
 #include "delta_device.h"
 
 namespace miconv {

@@ -2,8 +2,8 @@
 // r = 1 / sqrt(var + eps), and its gradients: with h = dy w and n = (x - m) r,
 //   dx = r (h - mean(h) - n mean(h n)),   dw = sum over tokens of dy n,   db = sum over tokens of dy.
 // Memory bound: x (and dy) are read once, held in registers between the sums and the result.  8192 tokens of 4096 channels
-// in bf16, tokens first, forward: 24.5 us, 134 MB at 5.5 TB/s.  8192 tokens of 2048, channel-major: forward 19 us, 67 MB at
-// 3.5 TB/s, backward 30 us, 101 MB at 3.4: one or two work-groups a CU read all of theirs, then write all.
+// in bf16, tokens first, forward: 24.5 us, 134 MB at 5.5 TB/s.  8192 tokens of 2048, channel-major: forward 19.5 us, 67 MB at
+// 3.4 TB/s, backward 31 us, 101 MB at 3.3: one or two work-groups a CU read all of theirs, then write all.
 //
 // The variance is the mean square of the differences from the mean, in a second run over the registers: no
 // cancellation however large the mean.

@@ -14,7 +14,7 @@
 // lane's accumulators run along the rows; the other is axis R.  Tiles arrive in LDS and leave it as in the 8-bit
 // integer product (matmul_i8.hip).
 //
-// 8192 tokens, 4096 -> 8192, bf16: 258 to 295 us by the card's clock at the time, 2.1 to 1.9 PFLOP/s, the MFMAs' rate under the
+// 8192 tokens, 4096 -> 8192, bf16: 258 to 299 us by the card's clock at the time, 2.1 to 1.8 PFLOP/s, the MFMAs' rate under the
 // power limit (as for the integer product).
 #include "device.h"
 #include "f8.h"

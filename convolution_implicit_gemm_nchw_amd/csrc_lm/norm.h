@@ -10,7 +10,7 @@ namespace miconv {
 
 // Whether channels are contiguous in every operand (tokens first), else time steps are.
 bool norm_tokens_first(const miconv_layer_norm_t &n, bool backward);
-// Work-groups of the backward pass, each with a row of partial sums of dw and db in the workspace; 1 needs none.
+// Work-groups of the backward pass, each with a row of partial sums of dw and db in the workspace.
 int norm_parts(const miconv_layer_norm_t &n, int dtype, size_t budget);
 
 // Tokens first: threads of a token, and how often each takes eight channels (0: a loop over them).

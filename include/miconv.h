@@ -691,7 +691,7 @@ int gated_delta_bwd(const miconv_gated_delta_t *d, int dtype, void *workspace, s
 int gated_delta_states_size(int B, int Hv, int P, int V, int L, size_t *bytes_out);
 int gated_delta_workspace_size(const miconv_gated_delta_t *d, int dtype, int backward, size_t workspace_limit,
                                size_t *bytes_out);
-/* The slices (sequences x chunks) and value tiles a call with these sizes and workspace takes. */
+/* The slices (sequences x chunks) that a call with these sizes and workspace takes, and the bytes of it that it uses. */
 int gated_delta_describe(const miconv_gated_delta_t *d, int dtype, int backward, size_t workspace_bytes, char *buf,
                          size_t buflen);
 /*
