@@ -44,3 +44,19 @@ def test_quantised_blocks_past_31_bits():
         return mc.lib().quantize_f8(B, L, C, 1, at(0), 0, 1 if sc != 1 else 0, sc, 1 << 60, 1 << 59, None)
     assert quantize(1 << 25, 1, 128 * 65, 0) == E_BIG
     assert quantize(1 << 21, 1, 131072, 1) == E_BIG
+
+
+def test_norm_describes_what_it_takes():
+    buf, lib = ctypes.create_string_buffer(64), mc.lib()
+
+    def describe(n, dtype=0, backward=1, ws=1 << 20, size=64):
+        return lib.layer_norm_describe(None if n is None else ctypes.byref(n), dtype, backward, ws, buf, size)
+    n = layer.norm_args()
+    assert describe(n) == OK and buf.value == b"algo=norm_tokens threads=64 times=1 parts=20"
+    assert describe(n, ws=2 * 8 * 24) == OK and buf.value.endswith(b"parts=2")
+    assert describe(n, backward=0) == OK and buf.value == b"algo=norm_tokens threads=64 times=1"
+    assert describe(layer.norm_args(major=True), backward=0) == OK and buf.value == b"algo=norm_rows lanes=1 threads=256"
+    assert describe(None) == layer.E_NULL and lib.layer_norm_describe(ctypes.byref(n), 0, 0, 0, None, 64) == layer.E_NULL
+    assert describe(layer.norm_args(C=0)) == layer.E_DIM and describe(n, dtype=2) == layer.E_DT
+    assert describe(n, ws=8 * 24 - 1) == layer.E_WS and buf.value == b""
+    assert describe(n, backward=0, size=5) == OK and buf.value == b"algo"
