@@ -14,7 +14,7 @@ namespace {
 // LDS matrices of 64 x 64 fp32 have rows of 68: 16-byte aligned, and 16 rows of a column block on different banks.
 constexpr int kRow = 68;
 
-template <int TI, int DK, bool BWD>
+template <int TI, int DK>
 struct Prepare {
     static constexpr int kCols = DK < 128 ? DK : 128;      // channels at a time
     static constexpr int kSteps = kCols / 32;
@@ -27,7 +27,7 @@ struct Prepare {
 template <int DT, int DK, bool BWD>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     constexpr int TI = in_planes(DT);
-    typedef Prepare<TI, DK, BWD> X;
+    typedef Prepare<TI, DK> X;
     __shared__ __attribute__((aligned(16))) char shared[X::kShared];
     __shared__ __attribute__((aligned(16))) float A[64 * kRow];
     float (*const part)[X::kCols / 8][64] = (float (*)[X::kCols / 8][64])A;     // before A: sums of squares
