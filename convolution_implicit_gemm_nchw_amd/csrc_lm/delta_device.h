@@ -6,9 +6,9 @@
 
 namespace miconv {
 
-// Splits into planes are exact: a plane takes the eight leading bits of what the planes before it left (by
-// truncation, so that nothing rounds up to infinity), and three hold all 24 bits of an fp32 value.  bf16
-// operands are one plane.  The products of planes i and j with i + j <= ORDER are summed: for ORDER 2 what is left
+// Splits into planes are exact: a plane takes eight bits of what the planes before it left, and three hold all 24 of
+// an fp32 value.  The first is cut, so that nothing rounds up to infinity, the second rounded to nearest, so that what
+// the products leave out has either sign (cut, it is of one, 2^-25 of every product on average).  bf16 operands are one plane.  The products of planes i and j with i + j <= ORDER are summed: for ORDER 2 what is left
 // out is below 2^-24 of the product, so three bf16 planes stand for fp32 at 3 (one operand bf16) or 6 MFMAs, where
 // the fp32 MFMA takes the time of 16.
 
@@ -20,18 +20,29 @@ DEVI uint32_t upper_pair(float lo, float hi) {
 
 DEVI float upper(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
+// Plane p of N of two values, which keep what is left of them.
+template <int N>
+DEVI uint32_t take_plane(int p, float &lo, float &hi) {
+    if (p == 0 || p + 1 == N) {
+        const uint32_t o = upper_pair(lo, hi);
+        lo -= upper(lo);
+        hi -= upper(hi);
+        return o;
+    }
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 near = {(__bf16)lo, (__bf16)hi};
+    const uint32_t o = __builtin_bit_cast(uint32_t, near);
+    lo -= __uint_as_float(o << 16);
+    hi -= __uint_as_float(o & 0xffff0000u);
+    return o;
+}
+
 // v[0..4) as planes; plane p's four values are out[p].
 template <int N>
 DEVI void split4(const float (&v)[4], u32x2 (&out)[N]) {
     float r[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-        out[p] = u32x2{upper_pair(r[0], r[1]), upper_pair(r[2], r[3])};
-        if (p + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] -= upper(r[i]);
-        }
-    }
+    for (int p = 0; p < N; ++p) out[p] = u32x2{take_plane<N>(p, r[0], r[1]), take_plane<N>(p, r[2], r[3])};
 }
 
 template <int N>
@@ -40,13 +51,9 @@ DEVI void split8(const float (&v)[8], u32x4 (&out)[N]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = v[i];
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-        out[p] = u32x4{upper_pair(r[0], r[1]), upper_pair(r[2], r[3]), upper_pair(r[4], r[5]), upper_pair(r[6], r[7])};
-        if (p + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] -= upper(r[i]);
-        }
-    }
+    for (int p = 0; p < N; ++p)
+        out[p] = u32x4{take_plane<N>(p, r[0], r[1]), take_plane<N>(p, r[2], r[3]), take_plane<N>(p, r[4], r[5]),
+                       take_plane<N>(p, r[6], r[7])};
 }
 
 // Planes of four values of a lane, and a lane's eight of a column or row operand, in LDS.

@@ -98,20 +98,14 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
             for (int p = 0; p < TI; ++p) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const u32x4 v = {upper_pair(x[0][j], x[1][j]), upper_pair(x[2][j], x[3][j]),
-                                     upper_pair(x[4][j], x[5][j]), upper_pair(x[6][j], x[7][j])};
+                    const u32x4 v = {take_plane<TI>(p, x[0][j], x[1][j]), take_plane<TI>(p, x[2][j], x[3][j]),
+                                     take_plane<TI>(p, x[4][j], x[5][j]), take_plane<TI>(p, x[6][j], x[7][j])};
                     const int t = tb + j, lane_at = (t & 15) + (db >> 3 & 3) * 16;
                     *(u32x4 *)(shared + (operand * TI + p) * X::kPlane + ((t >> 4) * X::kSteps + (db >> 5)) * 1024 +
                                lane_at * 16) = v;
                     if (rows_out)
                         *(u32x4 *)(flat + (size_t)p * 64 * DK * 2 + ((t >> 4) * (DK / 32) + ((d0 + db) >> 5)) * 1024 +
                                    lane_at * 16) = v;
-                }
-                if (p + 1 < TI) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[i][j] -= upper(x[i][j]);
                 }
             }
         };

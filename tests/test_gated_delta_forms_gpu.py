@@ -35,6 +35,25 @@ def test_bf16_outputs_are_fp32_sums_rounded_once(mc, size):
     assert rounded
 
 
+@pytest.mark.parametrize("size", [(64, 32, 64), (128, 64, 128), (200, 32, 64)], ids=lambda s: "-".join(map(str, s)))
+def test_errors_have_either_sign(mc, size):
+    """fp32 operands are three planes of eight bits, and of their products those below 2^-24 are left out.  With planes cut
+    towards zero that is 2 x 2^-9 x 2^-17 = 2^-25 of every product on average, always of its sign, and a state's value is a
+    sum of products of what came from two more: all positive here, so the errors' average would be 2^-25 more than once.
+    Rounded to nearest, what is left out averages 0."""
+    P, V, L = size
+    gen = torch.Generator().manual_seed(31)
+    one = lambda *s: 0.5 + torch.rand(s, generator=gen) / 2  # noqa: E731
+    q, k, v = one(2, 2 * P, L), one(2, 2 * P, L) / (64 * P) ** 0.5, one(2, 4 * V, L)
+    g, beta = -0.1 * torch.rand(2, 4, L, generator=gen), 0.25 * one(2, 4, L)
+    s = torch.empty(2, 4, P, V, device=DEV)
+    mc.gated_delta_fwd(*(t.to(DEV) for t in (q, k, v, g, beta)), key_heads=2, final_state=s)
+    want = ref.rule(*(t.double() for t in (q, k, v, g, beta)), 2)[1]
+    mean = float(((s.double().cpu() - want) / want).mean())
+    print(f"  mean error {mean:.2e}", flush=True)
+    assert abs(mean) <= 2.0 ** -25
+
+
 # ------------------------------------------------------------------ channel-major layer norm: 2, 4 and 8 time lanes
 
 #             B  L     C    time lanes forward and backward; ends inside the last tile of each
