@@ -342,7 +342,7 @@ __global__ __launch_bounds__(512) void delta_bwd_kernel(DeltaArgs a, float *stat
 // 14000 go to Z, F and dy, 15000 to the products with the states (9000 of matrix instructions), 8000 to those with dP
 // and dA.  An eighth of the channels for all steps would split the states once instead of twice: 64 key channels then
 // have 4 waves, and 13 heads of 6599 steps take 230 us instead of 172; at 128 channels both take as long.
-// 2 x 2048 steps of 16 heads, 128 and 128 channels, bf16: 135 us, 2 TB/s of states, Z, F and operands.
+// 2 x 2048 steps of 16 heads, 128 and 128 channels, bf16: 136 us, 2 TB/s of states, Z, F and operands.
 template <int DT, int DK>
 struct Grads {
     static constexpr int kWaves = 8, kThreads = kWaves * 64, kNC = DK / 64;

@@ -13,7 +13,7 @@ namespace {
 // operands in LDS, [channel][step or key channel], rows padded by 16 bytes against bank conflicts.
 //
 // The chain's latency bounds it: some 3900 cycles a chunk (of 3700 with a plane less of the scores, k S took 650, x to LDS 400,
-// the inverse 850, u f to LDS 500, the update 700, the state to LDS 450), 118 us at best and 130 in the median for a prompt
+// the inverse 850, u f to LDS 500, the update 700, the state to LDS 450), 119 us at best and 135 in the median for a prompt
 // of 64 chunks, 32 heads of 128 and 128 channels in bf16, 256 work-groups.  Wider slices have fewer work-groups and
 // chains as long, so a slice is one MFMA's 16 channels.
 // One role for all waves, in turn, took 152 us.
